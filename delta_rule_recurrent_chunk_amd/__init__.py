@@ -11,6 +11,9 @@ missing, every entry point raises; there is no CPU fallback.
     o, S_T = fwd_varlen(q, k, v, f, beta, c, cu_seqlens, S0=None)   (packed sequences)
     y, S_T = mixer_fwd(raw, params, g, S0=None)      (projections -> gated, normalised read-out)
 
+The layers beside the mixer (``layers.py``: the gated linear recurrence glr_*, rotary positions rope*, attention
+over a sliding window with sinks swa_*) are reached here under the same names.
+
 Shapes: q, k, f [B, T, H, d]; v [B, T, H, d]; beta, c [B, T, H] fp32;
 S0 / S_T [B, H, d, d] fp32 (S[i][j], i over values, j over keys).
 Dtypes: q, k, v, f (and o, dO, dq, ...) all bfloat16 or all float32.
@@ -19,6 +22,10 @@ from __future__ import annotations
 
 import ctypes
 import os
+
+from . import layers as _layers
+from .layers import (glr_bwd, glr_fwd, glr_step, glr_workspace_bytes, rope, rope_bwd, rope_frequencies,  # noqa: F401
+                     swa_bwd, swa_cache_store, swa_decode, swa_decode_workspace, swa_fwd)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkrondelta.so")
@@ -30,7 +37,7 @@ EXPORTED = ("kron_delta_abi_version", "kron_delta_status_string",
             "kron_delta_decode", "kron_delta_fwd_varlen", "kron_delta_gdn2_fwd",
             "kron_delta_fwd_train", "kron_delta_bwd_saved", "kron_delta_mixer_pre",
             "kron_delta_mixer_post", "kron_delta_mixer_fwd", "kron_delta_bwd_noalloc",
-            "kron_delta_bwd_status", "kron_delta_bwd_set_wait_limit")
+            "kron_delta_bwd_status", "kron_delta_bwd_set_wait_limit") + _layers.EXPORTED
 KD_WS_FWD, KD_WS_BWD, KD_WS_MIXER = 0, 1, 2
 KD_ERR_SCRATCH = -8     # kron_delta_bwd_noalloc: the problem needs more than its fixed scratch
 KD_ERR_TIMEOUT = -9     # kron_delta_bwd_status: a bounded wait of the backward ran out
@@ -119,6 +126,7 @@ def lib():
         L.kron_delta_mixer_post.argtypes = [dp, mp] + [vp] * 3 + [vp]
         L.kron_delta_mixer_fwd.restype = i32
         L.kron_delta_mixer_fwd.argtypes = [dp, mp] + [vp] * 10 + [vp, sz, vp]
+        _layers.declare(L)
         if L.kron_delta_abi_version() != ABI_VERSION:
             raise ImportError("libkrondelta.so ABI version mismatch")
         _lib = L

@@ -7,6 +7,7 @@
 
 #include <atomic>
 
+#include "kd_check.h"
 #include "kron_delta.h"
 
 namespace kd {
@@ -56,23 +57,11 @@ hipError_t launch_fwd16_split(const void* q, const void* k, const void* v, const
 
 namespace {
 
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes) {
-    Range r;
-    r.lo = (uintptr_t)p;
-    r.hi = r.lo + bytes;
-    return r;
-}
-
-bool overlap(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool misaligned(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) != 0; }
+using kd::Range;
+using kd::misaligned;
+using kd::overlap;
+using kd::range_of;
+using kd::up256;
 
 // fp32_d128: whether the entry point supports fp32 at d = 128 (decode only)
 kd_status check_desc(const kd_desc* d, bool fp32_d128 = false) {
@@ -90,8 +79,6 @@ kd_status check_desc(const kd_desc* d, bool fp32_d128 = false) {
 }
 
 size_t esize(const kd_desc* d) { return d->dtype == KD_BF16 ? 2 : 4; }
-
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The mixer forward's workspace: q, k, v, f (desc dtype), beta, c (fp32), the
 // read-out o, and the hand-off words of the one-launch form (8 bytes per

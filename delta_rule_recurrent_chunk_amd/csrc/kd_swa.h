@@ -1,0 +1,215 @@
+// kd_swa.h -- building blocks of the sliding-window attention kernels, gfx950.
+//
+// A query at position p sees the keys s <= p with p - s < W (the window) or
+// s < S (the sinks).  All products run on 32x32 MFMA tiles (wave64):
+//   * A operand: lane l holds row l % 32, B operand: lane l holds column
+//     l % 32; lane group g = l / 32 holds its share of K, one 16-byte fragment
+//     (8 bf16 or 4 fp32 values) per step;
+//   * C/D: lane l holds column l % 32, rows 8 (r / 4) + 4 g + r % 4, r < 16.
+// The order of K in a product is free as long as A and B agree.  So a tile of
+// weights that a product left as an accumulator (rows = the next product's K)
+// is that product's B operand after packing, with no trip through LDS; its A
+// operand is read with the same K order (ld_col).
+#pragma once
+
+#include "kd_device.h"
+
+namespace kd {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+constexpr int SWA_MAX_SINKS = 64;   // KRON_DELTA_SWA_MAX_SINKS
+
+struct SwaArgs {
+    const void *q, *k, *v;
+    int64_t qs[3], ks[3], vs[3];       // strides over batch, token, head (elements)
+    void* o;                           // [B, Tq, Hq, d]
+    float* lse;                        // [B, Hq, Tq] or null
+    const void* dO;                    // [B, Tq, Hq, d]
+    float* delta;                      // [B, Hq, Tq]: sum_i dO_i o_i
+    void *dq, *dk, *dv;                // contiguous
+    const int* cu;                     // packed: N + 1 offsets into the Tq == Tk rows
+    int B, N, Tq, Tk, Hq, Hkv;
+    int W, S;
+    float scale, c;                    // c = scale log2(e)
+};
+
+// Row-major LDS tile of D columns, 16-byte chunks permuted within each row so
+// that both a read of one chunk of 16 consecutive rows (ld_row) and the
+// transpose read of 4 + 4 rows (ld_col) spread over all 64 banks.
+template <class E, int D>
+struct SwaTile {
+    static constexpr int EPC = 16 / sizeof(E);    // elements per chunk
+    static constexpr int CPR = D / EPC;           // chunks per row
+    static __device__ __forceinline__ int swz(int r) {
+        if constexpr (CPR == 4) return (r >> 2) & 3;
+        if constexpr (CPR == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+        if constexpr (CPR == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+        return ((r & 7) << 1) | ((r >> 3) & 1);
+    }
+    static __device__ __forceinline__ int off(int r, int chunk) { return r * D + ((chunk ^ swz(r)) * EPC); }
+};
+
+template <class E>
+struct SwaT;
+
+template <>
+struct SwaT<__bf16> {
+    typedef __bf16 E;
+    typedef bf16x8 Frag;
+    static constexpr int KC = 16;    // K per step: one MFMA
+    static constexpr int PR = 8;     // accumulator rows (registers) per packed fragment
+    static __device__ __forceinline__ floatx16 mma(Frag a, Frag b, floatx16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // registers 8j .. 8j + 7 of an accumulator: K = 16j + {4g .. 4g + 3, 8 + 4g .. 8 + 4g + 3}
+    static __device__ __forceinline__ Frag pack(const floatx16& p, int j) {
+        Frag r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = (__bf16)p[8 * j + e];
+        return r;
+    }
+    // A operand of rows d = c0 + l % 32 with that K order, from the tile's
+    // columns: two transpose reads of four rows each (ds_read_b64_tr_b16: in
+    // each 16-lane block lane j names four elements of row j / 4 and receives
+    // column j of the four rows)
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col(const E* tile, int row0, int c0, int lane) {
+        typedef SwaTile<E, D> TL;
+        typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+        const int j = lane & 15, col = c0 + 16 * ((lane >> 4) & 1) + 4 * (j & 3);
+        const int r = row0 + 4 * (lane >> 5) + (j >> 2);
+        const E* lo = tile + TL::off(r, col / TL::EPC) + (col % TL::EPC);
+        const E* hi = tile + TL::off(r + 8, col / TL::EPC) + (col % TL::EPC);
+        const s16x4 a = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (__attribute__((address_space(3))) v4s*)(lo)));
+        const s16x4 b = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (__attribute__((address_space(3))) v4s*)(hi)));
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    static __device__ __forceinline__ float dot(Frag a, Frag b) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf((float)a[e], (float)b[e], s);
+        return s;
+    }
+};
+
+template <>
+struct SwaT<float> {
+    typedef float E;
+    typedef floatx4 Frag;
+    static constexpr int KC = 8;     // K per step: four MFMAs, K = 4g + i in the i-th
+    static constexpr int PR = 4;
+    static __device__ __forceinline__ floatx16 mma(Frag a, Frag b, floatx16 c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag pack(const floatx16& p, int j) {
+        return Frag{p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]};
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col(const E* tile, int row0, int c0, int lane) {
+        typedef SwaTile<E, D> TL;
+        const int d = c0 + (lane & 31), r = row0 + 4 * (lane >> 5);
+        Frag x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = tile[TL::off(r + i, d / TL::EPC) + d % TL::EPC];
+        return x;
+    }
+    static __device__ __forceinline__ float dot(Frag a, Frag b) {
+        return fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
+    }
+};
+
+// fragment ks of row r: its chunk 2 ks + g
+template <class E, int D>
+__device__ __forceinline__ typename SwaT<E>::Frag swa_ld_row(const E* tile, int r, int ks, int g) {
+    return *reinterpret_cast<const typename SwaT<E>::Frag*>(tile + SwaTile<E, D>::off(r, 2 * ks + g));
+}
+// the same from a row in memory
+template <class E>
+__device__ __forceinline__ typename SwaT<E>::Frag swa_ld_mem(const E* row, int ks, int g) {
+    return *reinterpret_cast<const typename SwaT<E>::Frag*>(row + (2 * ks + g) * (16 / (int)sizeof(E)));
+}
+template <class E>
+__device__ __forceinline__ typename SwaT<E>::Frag swa_zero() {
+    typename SwaT<E>::Frag z;
+#pragma unroll
+    for (int e = 0; e < (int)(16 / sizeof(E)); ++e) z[e] = (E)0.f;
+    return z;
+}
+
+// the other lane group's value of the same column
+__device__ __forceinline__ float swa_swap(float x) { return __shfl_xor(x, 32); }
+
+// Sequence and block of a workgroup.  Batched: row block `slot` of batch
+// element b.  Packed: sequence s owns the slots cu[s] / R + s onwards (at
+// least as many as its blocks of R rows, and no two sequences share one), so
+// the grid needs T / R + N slots and no table.  Offsets are clamped into
+// [0, T].  Returns false when the slot holds no rows.
+struct SwaSeq {
+    int q0, nq, nk, past, blk;   // first row, rows, keys, position of row 0, block of R rows
+};
+__device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bool keys, SwaSeq& s) {
+    if (!a.cu) {
+        s.q0 = 0;
+        s.nq = a.Tq;
+        s.nk = a.Tk;
+        s.past = a.Tk - a.Tq;
+        s.blk = slot;
+        return (int64_t)slot * R < (keys ? s.nk : s.nq);
+    }
+    const int lane = threadIdx.x & 63;
+    int n = 0;   // sequences that start at or before the slot
+    for (int i = 0; i < a.N; i += 64) {
+        const int at = i + lane;
+        const bool in = at < a.N && min(max(a.cu[min(at, a.N)], 0), a.Tq) / R + at <= slot;
+        n += __popcll(__ballot(in));
+    }
+    if (n == 0) return false;
+    const int q = n - 1;
+    const int lo = min(max(a.cu[q], 0), a.Tq), hi = min(max(a.cu[q + 1], lo), a.Tq);
+    s.q0 = lo;
+    s.nq = s.nk = hi - lo;
+    s.past = 0;
+    s.blk = slot - (lo / R + q);
+    return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
+}
+
+__device__ __forceinline__ bool swa_visible(int key, int pos, int W, int S) {
+    return key <= pos && (pos - key < W || key < S);
+}
+
+// rows row0 .. row0 + R - 1 of a matrix (row stride rs elements) into a tile,
+// zeros past `rows`
+template <class E, int D, int R, int NT>
+__device__ __forceinline__ void swa_stage(E* tile, const E* base, int64_t rs, int row0, int rows, int tid) {
+    typedef SwaTile<E, D> TL;
+    typedef typename SwaT<E>::Frag Frag;
+#pragma unroll 4
+    for (int i = tid; i < R * TL::CPR; i += NT) {
+        const int r = i / TL::CPR, ch = i % TL::CPR;
+        const Frag x = row0 + r < rows ? *reinterpret_cast<const Frag*>(base + (int64_t)(row0 + r) * rs + ch * TL::EPC)
+                                       : swa_zero<E>();
+        *reinterpret_cast<Frag*>(tile + TL::off(r, ch)) = x;
+    }
+}
+
+// column q of an accumulator stack (rows = the D head elements) to a row in memory
+template <class E, int D>
+__device__ __forceinline__ void swa_store_row(E* row, const floatx16* acc, float f, int g) {
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            typedef E E4 __attribute__((ext_vector_type(4)));
+            E4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = (E)(acc[dt][4 * j + e] * f);
+            *reinterpret_cast<E4*>(row + 32 * dt + 8 * j + 4 * g) = x;
+        }
+}
+
+}  // namespace kd

@@ -1,0 +1,126 @@
+// kd_swa_fwd.hip -- sliding-window attention with sinks, forward, gfx950.
+//
+// One workgroup of four waves takes 128 query rows of one head, one wave 32 of
+// them; tiles of BN keys and values pass through LDS.  Per tile a wave forms
+//     St = K Qt   (rows = keys, columns = the lane's query)
+// so a query's scores lie in one lane (and its partner 32 lanes away): the
+// running maximum m and sum l of its softmax are per-lane scalars.  The
+// weights exp2(c s - m) are packed to the input type (bf16: off by at most
+// 2^-9 of each weight, whose sum is kept in fp32) and go straight back in as
+// the B operand of Ot += Vt Pt.
+#include "kd_swa.h"
+
+namespace kd {
+
+template <class E, int D, int BN>
+__global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
+{
+    typedef SwaT<E> T;
+    typedef typename T::Frag Frag;
+    constexpr int NK = D / T::KC, NS = BN / 32, ND = D / 32, NP = 16 / T::PR;
+    __shared__ __align__(16) E kt[BN * D];
+    __shared__ __align__(16) E vt[BN * D];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 5;
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hkv);
+    SwaSeq s;
+    if (!swa_locate(a, blockIdx.x, 128, false, s)) return;
+    const int r0 = s.blk * 128, row = r0 + 32 * w + (lane & 31), pos = s.past + row;
+
+    const E* qrow = (const E*)a.q + b * a.qs[0] + (int64_t)(s.q0 + min(row, s.nq - 1)) * a.qs[1] + h * a.qs[2];
+    Frag q[NK];
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) q[ks] = row < s.nq ? swa_ld_mem<E>(qrow, ks, g) : swa_zero<E>();
+    const E* kb = (const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2];
+    const E* vb = (const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2];
+
+    floatx16 o[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    // tiles: the sinks' tiles in front of the window, then lo .. hi - 1
+    const int pmax = min(s.past + r0 + 127, s.nk - 1);
+    const int lo = max(0, s.past + r0 - a.W + 1) / BN, hi = pmax < 0 ? 0 : pmax / BN + 1;
+    const int sk = min((a.S + BN - 1) / BN, lo);
+    const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;      // this wave's positions
+    for (int i = 0; i < sk + max(hi - lo, 0); ++i) {
+        const int k0 = (i < sk ? i : lo + (i - sk)) * BN;
+        __syncthreads();
+        swa_stage<E, D, BN, 256>(kt, kb, a.ks[1], k0, s.nk, tid);
+        swa_stage<E, D, BN, 256>(vt, vb, a.vs[1], k0, s.nk, tid);
+        __syncthreads();
+        if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) continue;   // nothing visible to the wave
+        floatx16 sc[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sc[n][r] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < NK; ++ks)
+                sc[n] = T::mma(swa_ld_row<E, D>(kt, 32 * n + (lane & 31), ks, g), q[ks], sc[n]);
+        }
+        // every pair of the tile visible: no mask
+        const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
+        if (!full) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) sc[n][r] = -INFINITY;
+        }
+        float mx = sc[0][0];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[n][r]);
+        mx = fmaxf(mx, swa_swap(mx));
+        const float mn = fmaxf(m, mx * a.c), mu = mn == -INFINITY ? 0.f : mn;
+        const float alpha = __builtin_amdgcn_exp2f(m - mu);
+        m = mn;
+        float ls = 0.f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                sc[n][r] = __builtin_amdgcn_exp2f(fmaf(sc[n][r], a.c, -mu));
+                ls += sc[n][r];
+            }
+        l = fmaf(l, alpha, ls);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) o[dt] *= alpha;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const Frag p = T::pack(sc[n], j);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+                    o[dt] = T::mma(T::template ld_col<D>(vt, 32 * n + (32 / NP) * j, 32 * dt, lane), p, o[dt]);
+            }
+    }
+    l += swa_swap(l);
+    if (row >= s.nq) return;
+    // a row that sees nothing: o = 0, lse = -infinity
+    const bool none = m == -INFINITY && l == 0.f;
+    swa_store_row<E, D>((E*)a.o + (((int64_t)b * a.Tq + s.q0 + row) * a.Hq + h) * D, o, none ? 0.f : 1.f / l, g);
+    if (a.lse && g == 0)
+        a.lse[((int64_t)b * a.Hq + h) * a.Tq + s.q0 + row] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
+}
+
+template <class E, int D>
+static hipError_t swa_fwd(const SwaArgs& a, hipStream_t st)
+{
+    const unsigned nx = a.cu ? (unsigned)(a.Tq / 128 + a.N) : (unsigned)(((int64_t)a.Tq + 127) / 128);
+    kd_swa_fwd_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<dim3(nx, a.Hq, a.B), 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_swa_fwd(int bf16, int d, const SwaArgs& a, hipStream_t st)
+{
+    if (bf16) return d == 32 ? swa_fwd<__bf16, 32>(a, st) : d == 64 ? swa_fwd<__bf16, 64>(a, st) : swa_fwd<__bf16, 128>(a, st);
+    return d == 32 ? swa_fwd<float, 32>(a, st) : d == 64 ? swa_fwd<float, 64>(a, st) : swa_fwd<float, 128>(a, st);
+}
+
+}  // namespace kd

@@ -396,6 +396,186 @@ KD_API kd_status kron_delta_mixer_fwd(const kd_desc *desc, const kd_mixer_params
                          const void *g, const float *S0, void *y, float *ST,
                          void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Layers beside the mixer.  The hybrid form of the KronLSTM summary (section
+ * "전제와 한계") alternates the mixer with attention over a sliding window;
+ * the entry points below are that attention, the rotary positions of its
+ * queries and keys, and the element-wise member of the recurrence family.
+ * Ownership, streams, checks and status codes are those of the calls above;
+ * sizes and strides are the ones each descriptor names.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Gated linear recurrence, element-wise over D channels: with the state h in
+ * fp32,
+ *     h_t = f_t h_{t-1} + i_t x_t          (i NULL: i_t = 1)
+ *  * x, f, i, h (and their gradients): [B, T, D] in desc->dtype; h0, hT, dhT,
+ *    dh0: [B, D] fp32.  f is the forget gate, in [0, 1].
+ *  * Any D >= 1 and T >= 0; B <= 65535, D, T <= 2^30.
+ *  * hs, when not NULL, receives the states entering every
+ *    KRON_DELTA_GLR_CHUNK tokens ([B, ceil(T / KRON_DELTA_GLR_CHUNK), D]
+ *    fp32, the first one h0): what the backward pass starts from.
+ *  * ws: kron_delta_glr_workspace_bytes(desc) bytes, contents on entry
+ *    ignored (may be NULL when that is 0); not shared by calls that overlap
+ *    on the device.
+ * Results do not depend on how the work is scheduled: repeated calls agree
+ * bit for bit.
+ */
+#define KRON_DELTA_GLR_CHUNK 128
+typedef struct {
+    int32_t B, T, D;
+    int32_t dtype;     /* kd_dtype */
+} kd_glr_desc;
+
+KD_API size_t kron_delta_glr_workspace_bytes(const kd_glr_desc *desc);
+
+/* Forward: h, and when not NULL the last state hT (h0 when T = 0) and hs. */
+KD_API kd_status kron_delta_glr_fwd(const kd_glr_desc *desc, const void *x, const void *f, const void *i,
+                         const float *h0, void *h, float *hT, float *hs,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Backward: gradients of L = <dh, h> + <dhT, h_T> (dhT NULL = 0) with respect
+ * to x, f, i and h0 (dh0 NULL: not returned; di only with i), from the inputs
+ * and the hs of the forward call.
+ */
+KD_API kd_status kron_delta_glr_bwd(const kd_glr_desc *desc, const void *x, const void *f, const void *i,
+                         const float *hs, const void *dh, const float *dhT,
+                         void *dx, void *df, void *di, float *dh0,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * One token (desc->T = 1): x, f, i, y are [B, D]; h_in, h_out [B, D] fp32 and
+ * may be the same buffer; y = h_out in desc->dtype.
+ */
+KD_API kd_status kron_delta_glr_step(const kd_glr_desc *desc, const void *x, const void *f, const void *i,
+                         const float *h_in, void *y, float *h_out, void *stream);
+
+/*
+ * Rotary positions: pair j < rot/2 of every head of q and k at position p is
+ * turned by the angle p * freqs[j] and multiplied by `scale`,
+ *     (a, b) -> scale (a cos - b sin, b cos + a sin),
+ * a and b being elements j and j + rot/2 (KD_ROPE_HALF) or 2j and 2j + 1
+ * (KD_ROPE_INTERLEAVED) of the head; elements from rot on are copied.
+ * inverse != 0 turns the other way: with the same scale this is the backward
+ * pass (gradients of the outputs in, of the inputs out).
+ *  * q, q_out: [B, T, Hq, d]; k, k_out: [B, T, Hk, d] (Hk = 0: no k) in
+ *    desc->dtype, with strides over batch, token and head in elements and a
+ *    contiguous last dimension.  An output may be its input (same strides);
+ *    q and k may be the heads of one fused tensor.  d <= 256, rot even.
+ *  * pos: [T] or, with pos_batched, [B, T]; int32 or, with pos64, int64.
+ *  * freqs: [rot/2] fp64, radians per position.  The angle is formed in fp64
+ *    and reduced before its sine and cosine in fp32, so far positions keep
+ *    the precision of near ones.
+ */
+#define KD_ROPE_HALF 0
+#define KD_ROPE_INTERLEAVED 1
+typedef struct {
+    int32_t B, T, Hq, Hk, d, rot;
+    int32_t layout;            /* KD_ROPE_HALF or KD_ROPE_INTERLEAVED */
+    int32_t dtype;             /* kd_dtype */
+    int32_t pos64, pos_batched, inverse;
+    float scale;
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} kd_rope_desc;
+
+KD_API kd_status kron_delta_rope(const kd_rope_desc *desc, const void *q, const void *k, const void *pos,
+                         const double *freqs, void *q_out, void *k_out, void *stream);
+
+/*
+ * Attention over a sliding window with sinks: the query at position p sees
+ * the keys s <= p with p - s < window or s < sinks,
+ *     o = sum_s softmax_s(scale q . k_s) v_s,   lse = log sum_s exp(scale q . k_s).
+ * Query head h reads key head h / (Hq / Hkv).  A query that sees no key gets
+ * o = 0 and lse = -infinity.
+ *  * q: [B, Tq, Hq, d], k, v: [B, Tk, Hkv, d] in desc->dtype, strides over
+ *    batch, token and head in elements (multiples of 16 bytes), contiguous
+ *    last dimension; o, dO, dq: contiguous [B, Tq, Hq, d]; dk, dv: contiguous
+ *    [B, Tk, Hkv, d]; lse: [B, Hq, Tq] fp32.  d in {32, 64, 128}; bf16, or
+ *    fp32 (a diagnostic precision).  sinks <= KRON_DELTA_SWA_MAX_SINKS.
+ *  * The queries stand at the end of the keys: query t has position
+ *    Tk - Tq + t (a later piece of a prompt has Tk > Tq; with Tk < Tq the
+ *    first queries see nothing).
+ *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of
+ *    Tq = Tk rows, offsets int32 [B + 1] on the device, non-decreasing from 0
+ *    to Tq (clamped into that range where they are read); q is [Tq, Hq, d],
+ *    lse [Hq, Tq], the batch strides are ignored.  Rows that no sequence
+ *    covers are left unwritten.
+ */
+#define KRON_DELTA_SWA_MAX_SINKS 64
+typedef struct {
+    int32_t B, Tq, Tk, Hq, Hkv, d;
+    int32_t dtype;             /* kd_dtype */
+    int32_t window, sinks;     /* window >= 1 */
+    float scale;               /* > 0 */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+} kd_swa_desc;
+
+/* Workspace of kron_delta_swa_bwd; packed != 0 when it is called with cu_seqlens. */
+KD_API size_t kron_delta_swa_workspace_bytes(const kd_swa_desc *desc, int packed);
+
+/* Forward; lse may be NULL. */
+KD_API kd_status kron_delta_swa_fwd(const kd_swa_desc *desc, const int32_t *cu_seqlens,
+                         const void *q, const void *k, const void *v,
+                         void *o, float *lse, void *stream);
+
+/*
+ * Backward: gradients of <dO, o> with respect to q, k, v, from the forward's
+ * o and lse.  ws as kron_delta_swa_workspace_bytes says, contents on entry
+ * ignored.  Every gradient is summed in a fixed order.
+ */
+KD_API kd_status kron_delta_swa_bwd(const kd_swa_desc *desc, const int32_t *cu_seqlens,
+                         const void *q, const void *k, const void *v, const void *o, const float *lse,
+                         const void *dO, void *dq, void *dk, void *dv,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * One decoding step per sequence over a rolling cache.  k_cache and v_cache
+ * are [B, cap, Hkv, d] (strides over batch, slot and head in elements,
+ * multiples of 16 bytes) with cap >= sinks + window; position s lives in slot
+ * s for s < sinks and in sinks + (s - sinks) mod (cap - sinks) otherwise, so a
+ * cache as long as the sequence is a plain one and a shorter one never runs
+ * full.  lens[b] is the number of tokens before this one (its position); a
+ * negative lens[b] marks an unused row: its o is set to 0, its cache is left
+ * as it is.  For the others:
+ *   1. with rot > 0, q and k are turned to position lens[b] (as
+ *      kron_delta_rope: layout, rope_scale, freqs);
+ *   2. k, rounded to the cache's type, and v are stored in the position's slot;
+ *   3. o = attention of q over the visible positions, the new one included.
+ *  * q [B, Hq, d], k, v [B, Hkv, d]: heads contiguous, batch strides (elements)
+ *    in in_stride (q, k, v); o [B, Hq, d] contiguous.  lens is read on the
+ *    device and not changed.
+ *  * ws: kron_delta_swa_decode_workspace_bytes(desc) bytes whose contents are
+ *    zero before the first call; every call leaves it ready for the next one
+ *    of the same descriptor or any other that it is large enough for.  Calls
+ *    that overlap on the device must not share it.
+ */
+typedef struct {
+    int32_t B, Hq, Hkv, d, cap;
+    int32_t dtype;             /* kd_dtype */
+    int32_t window, sinks;
+    float scale;               /* > 0 */
+    int32_t rot, layout;       /* rot 0: q and k are taken as they are */
+    float rope_scale;
+    int64_t k_stride[3], v_stride[3];
+} kd_swa_cache_desc;
+
+KD_API size_t kron_delta_swa_decode_workspace_bytes(const kd_swa_cache_desc *desc);
+KD_API kd_status kron_delta_swa_decode(const kd_swa_cache_desc *desc, const void *q, const void *k, const void *v,
+                         const int64_t in_stride[3], void *k_cache, void *v_cache, const int32_t *lens,
+                         const double *freqs, void *o, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Stores a prompt's keys and values (already turned) in the cache: token t of
+ * k, v [B, T, Hkv, d] goes to position t, for t < lens[b] (NULL: T; clamped
+ * to [0, T]).  Of positions that share a slot only the last is stored.  Uses
+ * the cache part of the descriptor (scale and rot are not read, Hq only as a
+ * multiple of Hkv).
+ */
+KD_API kd_status kron_delta_swa_cache_store(const kd_swa_cache_desc *desc, int32_t T, const void *k, const void *v,
+                         const int64_t k_stride[3], const int64_t v_stride[3], const int32_t *lens,
+                         void *k_cache, void *v_cache, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
