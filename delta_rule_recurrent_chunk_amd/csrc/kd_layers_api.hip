@@ -115,6 +115,8 @@ kd_status check_glr(const kd_glr_desc* d) {
     if (!d) return KD_ERR_NULL;
     if (!known(d->dtype)) return KD_ERR_DTYPE;
     if (d->B < 1 || d->B > 65535 || d->D < 1 || d->T < 0 || d->T > (1 << 30) || d->D > (1 << 30)) return KD_ERR_SHAPE;
+    // one workgroup per 128 tokens of 64 channels or more, and 16 bytes of workspace per 128 tokens and channel
+    if (((int64_t)d->D + 63) / 64 * d->B > INT32_MAX / 2 / ((int64_t)d->T / 128 + 1)) return KD_ERR_SHAPE;
     return KD_OK;
 }
 
