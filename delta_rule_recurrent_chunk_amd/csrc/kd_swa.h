@@ -197,6 +197,51 @@ __device__ __forceinline__ void swa_stage(E* tile, const E* base, int64_t rs, in
     }
 }
 
+// The same by loads that go straight to LDS (a wave's lane i fills the 16 bytes
+// at its base + 16 i, so the chunk order within a row is set by which chunk
+// each lane reads).  Rows past the end repeat the last one: their keys are
+// masked for every query.  The loads are in flight until swa_landed().
+template <class E, int D, int R, int NT>
+__device__ __forceinline__ void swa_fetch(E* tile, const E* base, int64_t rs, int row0, int rows, int tid) {
+    typedef SwaTile<E, D> TL;
+    static_assert(R * TL::CPR % NT == 0, "whole instructions");
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+    for (int i = 0; i < R * TL::CPR / NT; ++i) {
+        const int at = i * NT + tid, r = at / TL::CPR, ch = (at % TL::CPR) ^ TL::swz(r);
+        const E* src = base + (int64_t)min(row0 + r, rows - 1) * rs + ch * TL::EPC;
+        E* dst = tile + (i * NT + 64 * w) * TL::EPC;
+        // (written out, because the compiler would let every LDS read wait for the
+        // builtin's loads, those of the other buffer too)
+        const uint32_t at_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at_lds), "v"(src)
+                     : "memory", "m0");
+    }
+}
+// all loads of this wave have landed, then all waves of the workgroup are here
+__device__ __forceinline__ void swa_landed() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Work item of a workgroup: runs of 16 items go to one XCD (workgroups go
+// round the 8 XCDs one by one), so that the heads of a group and neighbouring
+// blocks, which read the same keys, share an L2.  False past the end.
+__device__ __forceinline__ bool swa_item(int64_t n, int64_t& item) {
+    const int64_t id = blockIdx.x, run = id >> 3;
+    item = (run >> 4) * 128 + (id & 7) * 16 + (run & 15);
+    return item < n;
+}
+__host__ __device__ inline int64_t swa_grid(int64_t n) { return (n + 127) / 128 * 128; }
+
+// Waits for a loaded fragment here rather than at its first use inside a loop
+// (where the wait would cover the loop's own loads).
+template <class F>
+__device__ __forceinline__ void swa_arrive(F& f) {
+    floatx4 r = __builtin_bit_cast(floatx4, f);
+    asm volatile("" : "+v"(r));
+    f = __builtin_bit_cast(F, r);
+}
+
 // column q of an accumulator stack (rows = the D head elements) to a row in memory
 template <class E, int D>
 __device__ __forceinline__ void swa_store_row(E* row, const floatx16* acc, float f, int g) {

@@ -13,23 +13,32 @@
 namespace kd {
 
 template <class E, int D, int BN>
-__global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
+__global__ __launch_bounds__(256, 2) void kd_swa_fwd_kernel(SwaArgs a, int nslots)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = D / T::KC, NS = BN / 32, ND = D / 32, NP = 16 / T::PR;
-    __shared__ __align__(16) E kt[BN * D];
-    __shared__ __align__(16) E vt[BN * D];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 5;
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hkv);
+    __shared__ __align__(16) E kt[2][BN * D];
+    __shared__ __align__(16) E vt[2][BN * D];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
+    const int G = a.Hq / a.Hkv;
+    int64_t item;
+    if (!swa_item((int64_t)nslots * a.Hq * a.B, item)) return;
+    const int hg = item % G;
+    item /= G;
+    const int slot = nslots - 1 - item % nslots;    // the rows that see most first
+    item /= nslots;
+    const int hk = item % a.Hkv, b = item / a.Hkv, h = hk * G + hg;
     SwaSeq s;
-    if (!swa_locate(a, blockIdx.x, 128, false, s)) return;
+    if (!swa_locate(a, slot, 128, false, s)) return;
     const int r0 = s.blk * 128, row = r0 + 32 * w + (lane & 31), pos = s.past + row;
 
     const E* qrow = (const E*)a.q + b * a.qs[0] + (int64_t)(s.q0 + min(row, s.nq - 1)) * a.qs[1] + h * a.qs[2];
     Frag q[NK];
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) q[ks] = row < s.nq ? swa_ld_mem<E>(qrow, ks, g) : swa_zero<E>();
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
     const E* kb = (const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2];
     const E* vb = (const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2];
 
@@ -43,15 +52,22 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
     // tiles: the sinks' tiles in front of the window, then lo .. hi - 1
     const int pmax = min(s.past + r0 + 127, s.nk - 1);
     const int lo = max(0, s.past + r0 - a.W + 1) / BN, hi = pmax < 0 ? 0 : pmax / BN + 1;
-    const int sk = min((a.S + BN - 1) / BN, lo);
+    const int sk = min((a.S + BN - 1) / BN, lo), nt = sk + max(hi - lo, 0);
     const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;      // this wave's positions
-    for (int i = 0; i < sk + max(hi - lo, 0); ++i) {
-        const int k0 = (i < sk ? i : lo + (i - sk)) * BN;
-        __syncthreads();
-        swa_stage<E, D, BN, 256>(kt, kb, a.ks[1], k0, s.nk, tid);
-        swa_stage<E, D, BN, 256>(vt, vb, a.vs[1], k0, s.nk, tid);
-        __syncthreads();
+    auto key0 = [&](int i) { return (i < sk ? i : lo + (i - sk)) * BN; };
+    auto fetch = [&](int i) {
+        swa_fetch<E, D, BN, 256>(kt[i & 1], kb, a.ks[1], key0(i), s.nk, tid);
+        swa_fetch<E, D, BN, 256>(vt[i & 1], vb, a.vs[1], key0(i), s.nk, tid);
+    };
+    if (nt > 0) fetch(0);
+    for (int i = 0; i < nt; ++i) {
+        // tile i is here; the buffer of tile i - 1 is free
+        swa_landed();
+        if (i + 1 < nt) fetch(i + 1);
+        const int k0 = key0(i);
         if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) continue;   // nothing visible to the wave
+        const E* kl = kt[i & 1];
+        const E* vl = vt[i & 1];
         floatx16 sc[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -59,7 +75,7 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
             for (int r = 0; r < 16; ++r) sc[n][r] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < NK; ++ks)
-                sc[n] = T::mma(swa_ld_row<E, D>(kt, 32 * n + (lane & 31), ks, g), q[ks], sc[n]);
+                sc[n] = T::mma(swa_ld_row<E, D>(kl, 32 * n + (lane & 31), ks, g), q[ks], sc[n]);
         }
         // every pair of the tile visible: no mask
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
@@ -75,10 +91,18 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[n][r]);
-        mx = fmaxf(mx, swa_swap(mx));
-        const float mn = fmaxf(m, mx * a.c), mu = mn == -INFINITY ? 0.f : mn;
-        const float alpha = __builtin_amdgcn_exp2f(m - mu);
-        m = mn;
+        mx = fmaxf(mx, swa_swap(mx)) * a.c;
+        // The reference of the exponents follows the maximum only when some row
+        // of the wave outgrows it by 2^8: weights up to 2^8 lose nothing in
+        // fp32 sums or in the type's relative rounding, and o is rescaled rarely.
+        if (__any(mx > m + 8.f)) {
+            const float mn = fmaxf(m, mx), alpha = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) o[dt] *= alpha;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
         float ls = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -87,9 +111,7 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
                 sc[n][r] = __builtin_amdgcn_exp2f(fmaf(sc[n][r], a.c, -mu));
                 ls += sc[n][r];
             }
-        l = fmaf(l, alpha, ls);
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) o[dt] *= alpha;
+        l += ls;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -97,7 +119,7 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
                 const Frag p = T::pack(sc[n], j);
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt)
-                    o[dt] = T::mma(T::template ld_col<D>(vt, 32 * n + (32 / NP) * j, 32 * dt, lane), p, o[dt]);
+                    o[dt] = T::mma(T::template ld_col<D>(vl, 32 * n + (32 / NP) * j, 32 * dt, lane), p, o[dt]);
             }
     }
     l += swa_swap(l);
@@ -112,8 +134,10 @@ __global__ __launch_bounds__(256) void kd_swa_fwd_kernel(SwaArgs a)
 template <class E, int D>
 static hipError_t swa_fwd(const SwaArgs& a, hipStream_t st)
 {
-    const unsigned nx = a.cu ? (unsigned)(a.Tq / 128 + a.N) : (unsigned)(((int64_t)a.Tq + 127) / 128);
-    kd_swa_fwd_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<dim3(nx, a.Hq, a.B), 256, 0, st>>>(a);
+    const int nslots = a.cu ? a.Tq / 128 + a.N : (int)(((int64_t)a.Tq + 127) / 128);
+    const int64_t grid = swa_grid((int64_t)nslots * a.Hq * a.B);
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    kd_swa_fwd_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<(unsigned)grid, 256, 0, st>>>(a, nslots);
     return hipGetLastError();
 }
 
