@@ -23,8 +23,8 @@ hipError_t launch_glr_step(int bf16, const void* x, const void* f, const void* g
                            float* h_out, int64_t n, hipStream_t st);
 hipError_t launch_rope(int bf16, const RopeArgs& a, hipStream_t st);
 hipError_t launch_swa_fwd(int bf16, int d, const SwaArgs& a, hipStream_t st);
-hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, hipStream_t st);
-size_t swa_bwd_workspace_bytes(int B, int Tq, int Hq);
+hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, void* ws, hipStream_t st);
+size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S);
 hipError_t launch_swa_decode(int bf16, int d, const SwaDecodeArgs& a, hipStream_t st);
 hipError_t launch_swa_store(const SwaStoreArgs& a, int B, hipStream_t st);
 int swa_decode_items(int B, int Hq, int Hkv);
@@ -325,7 +325,7 @@ kd::SwaArgs swa_args(const kd_swa_desc* d, const int32_t* cu, const void* q, con
 size_t kron_delta_swa_workspace_bytes(const kd_swa_desc* d, int packed) {
     SwaSpans s;
     if (check_swa(d, packed != 0, &s) != KD_OK) return 0;
-    return kd::swa_bwd_workspace_bytes(packed ? 1 : d->B, d->Tq, d->Hq);
+    return kd::swa_bwd_workspace_bytes(packed != 0, d->B, d->Tq, d->Tk, d->Hq, d->Hkv, d->d, d->window, d->sinks);
 }
 
 kd_status kron_delta_swa_fwd(const kd_swa_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
@@ -364,7 +364,7 @@ kd_status kron_delta_swa_bwd(const kd_swa_desc* d, const int32_t* cu, const void
         if (misaligned(p)) return KD_ERR_ALIGN;
     if (((uintptr_t)lse & 3u) != 0 || ((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
     const size_t lb = s.o / es_of(d->dtype) / d->d * 4;
-    const size_t need = kd::swa_bwd_workspace_bytes(cu ? 1 : d->B, d->Tq, d->Hq);
+    const size_t need = kron_delta_swa_workspace_bytes(d, cu != nullptr);
     const Range ins[] = {range_of(q, s.q),   range_of(k, s.k),  range_of(v, s.v), range_of(o, s.o),
                          range_of(lse, lb), range_of(dO, s.o), range_of(cu, cu ? ((size_t)d->B + 1) * 4 : 0)};
     const Range outs[] = {range_of(dq, s.o), range_of(dk, s.kg), range_of(dv, s.kg), range_of(ws, ws ? need : 0)};
@@ -374,11 +374,10 @@ kd_status kron_delta_swa_bwd(const kd_swa_desc* d, const int32_t* cu, const void
     a.o = const_cast<void*>(o);
     a.lse = const_cast<float*>(lse);
     a.dO = dO;
-    a.delta = (float*)ws;
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;
-    return done(kd::launch_swa_bwd(d->dtype == KD_BF16, d->d, a, (hipStream_t)stream));
+    return done(kd::launch_swa_bwd(d->dtype == KD_BF16, d->d, a, ws, (hipStream_t)stream));
 }
 
 namespace {

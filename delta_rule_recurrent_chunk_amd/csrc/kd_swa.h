@@ -26,7 +26,9 @@ struct SwaArgs {
     void* o;                           // [B, Tq, Hq, d]
     float* lse;                        // [B, Hq, Tq] or null
     const void* dO;                    // [B, Tq, Hq, d]
-    float* delta;                      // [B, Hq, Tq]: sum_i dO_i o_i
+    float2* rows;                      // [B, Hq, Tq]: lse log2(e) and delta of every query
+    float* part;                       // partial dK, dV of the sinks
+    int pslots;                        // query chunks of the sinks' pass (0: none)
     void *dq, *dk, *dv;                // contiguous
     const int* cu;                     // packed: N + 1 offsets into the Tq == Tk rows
     int B, N, Tq, Tk, Hq, Hkv;
@@ -69,6 +71,13 @@ struct SwaT<__bf16> {
         for (int e = 0; e < 8; ++e) r[e] = (__bf16)p[8 * j + e];
         return r;
     }
+    // what the packing of fragment j rounded away
+    static __device__ __forceinline__ Frag rest(const floatx16& p, int j, Frag x) {
+        Frag r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = (__bf16)(p[8 * j + e] - (float)x[e]);
+        return r;
+    }
     // A operand of rows d = c0 + l % 32 with that K order, from the tile's
     // columns: two transpose reads of four rows each (ds_read_b64_tr_b16: in
     // each 16-lane block lane j names four elements of row j / 4 and receives
@@ -109,6 +118,7 @@ struct SwaT<float> {
     static __device__ __forceinline__ Frag pack(const floatx16& p, int j) {
         return Frag{p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]};
     }
+    static __device__ __forceinline__ Frag rest(const floatx16&, int, Frag) { return Frag{0.f, 0.f, 0.f, 0.f}; }
     template <int D>
     static __device__ __forceinline__ Frag ld_col(const E* tile, int row0, int c0, int lane) {
         typedef SwaTile<E, D> TL;
@@ -151,6 +161,7 @@ __device__ __forceinline__ float swa_swap(float x) { return __shfl_xor(x, 32); }
 // [0, T].  Returns false when the slot holds no rows.
 struct SwaSeq {
     int q0, nq, nk, past, blk;   // first row, rows, keys, position of row 0, block of R rows
+    int slot0;                   // the sequence's first slot in chunks of 1024 rows
 };
 __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bool keys, SwaSeq& s) {
     if (!a.cu) {
@@ -159,6 +170,7 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
         s.nk = a.Tk;
         s.past = a.Tk - a.Tq;
         s.blk = slot;
+        s.slot0 = 0;
         return (int64_t)slot * R < (keys ? s.nk : s.nq);
     }
     const int lane = threadIdx.x & 63;
@@ -175,6 +187,7 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     s.nq = s.nk = hi - lo;
     s.past = 0;
     s.blk = slot - (lo / R + q);
+    s.slot0 = lo / 1024 + q;
     return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
 }
 
@@ -182,22 +195,8 @@ __device__ __forceinline__ bool swa_visible(int key, int pos, int W, int S) {
     return key <= pos && (pos - key < W || key < S);
 }
 
-// rows row0 .. row0 + R - 1 of a matrix (row stride rs elements) into a tile,
-// zeros past `rows`
-template <class E, int D, int R, int NT>
-__device__ __forceinline__ void swa_stage(E* tile, const E* base, int64_t rs, int row0, int rows, int tid) {
-    typedef SwaTile<E, D> TL;
-    typedef typename SwaT<E>::Frag Frag;
-#pragma unroll 4
-    for (int i = tid; i < R * TL::CPR; i += NT) {
-        const int r = i / TL::CPR, ch = i % TL::CPR;
-        const Frag x = row0 + r < rows ? *reinterpret_cast<const Frag*>(base + (int64_t)(row0 + r) * rs + ch * TL::EPC)
-                                       : swa_zero<E>();
-        *reinterpret_cast<Frag*>(tile + TL::off(r, ch)) = x;
-    }
-}
-
-// The same by loads that go straight to LDS (a wave's lane i fills the 16 bytes
+// Rows row0 .. row0 + R - 1 of a matrix (row stride rs elements) into a tile, by
+// loads that go straight to LDS (a wave's lane i fills the 16 bytes
 // at its base + 16 i, so the chunk order within a row is set by which chunk
 // each lane reads).  Rows past the end repeat the last one: their keys are
 // masked for every query.  The loads are in flight until swa_landed().

@@ -1,29 +1,52 @@
 // kd_swa_bwd.hip -- sliding-window attention with sinks, backward, gfx950.
 //
 // With P = exp(scale s - lse) recomputed from the saved lse and
-// delta_t = sum_i dO_ti o_ti:
+// delta_t = sum_s P_ts dP_ts (= sum_i dO_ti o_ti):
 //     dV = Pt dO;  dP = dO Vt;  dS = P (dP - delta);  dQ = scale dS K;  dK = scale dSt Q
-// Two kernels, so that every gradient is summed in registers in a fixed order
-// (no atomics): one over query blocks for dQ (and delta), one over key blocks
-// for dK and dV, which also sums over the query heads that share a key head.
+// Every gradient is summed in registers in a fixed order, no atomics:
+//   1. over query blocks: dQ, and delta for the other two;
+//   2. where queries lie beyond the window of the first 128 keys: the sinks'
+//      dK and dV from those queries, in partial sums over chunks of 1024;
+//   3. over key blocks: dK and dV from the queries whose window holds them,
+//      also summed over the query heads of a group; the first block adds the
+//      partial sums of 2.
 #include "kd_swa.h"
 
 namespace kd {
 
+constexpr int SWA_CHUNK = 1024;        // queries per partial sum of the sinks
+constexpr float LOG2E = 1.4426950408889634f;
+
+// first query beyond the window of keys 0 .. 127
+__device__ __forceinline__ int swa_far(const SwaArgs& a, int past) { return max(0, 127 + a.W - past); }
+
 // dQ and delta of 128 query rows of one head: the forward's layout, with the
 // scores' gradient in the weights' place and K in V's.
+//
+// dS is rounded to the type before its product with K.  Its delta comes from
+// the rounded o there (the sum of P dP is only known at the end, when it goes
+// to the other kernels): for queries that see few keys the two roundings
+// together would double the error of dQ, so waves whose queries see fewer than
+// 512 keys take the rounding's remainder of dS through a second product.
 template <class E, int D, int BN>
-__global__ __launch_bounds__(256) void kd_swa_dq_kernel(SwaArgs a)
+__global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_kernel(SwaArgs a, int nslots)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = D / T::KC, NS = BN / 32, ND = D / 32, NP = 16 / T::PR;
-    __shared__ __align__(16) E kt[BN * D];
-    __shared__ __align__(16) E vt[BN * D];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 5;
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hkv);
+    __shared__ __align__(16) E kt[2][BN * D];
+    __shared__ __align__(16) E vt[2][BN * D];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
+    const int G = a.Hq / a.Hkv;
+    int64_t item;
+    if (!swa_item((int64_t)nslots * a.Hq * a.B, item)) return;
+    const int hg = item % G;
+    item /= G;
+    const int slot = nslots - 1 - item % nslots;
+    item /= nslots;
+    const int hk = item % a.Hkv, b = item / a.Hkv, h = hk * G + hg;
     SwaSeq s;
-    if (!swa_locate(a, blockIdx.x, 128, false, s)) return;
+    if (!swa_locate(a, slot, 128, false, s)) return;
     const int r0 = s.blk * 128, row = r0 + 32 * w + (lane & 31), pos = s.past + row, rc = min(row, s.nq - 1);
 
     const E* qrow = (const E*)a.q + b * a.qs[0] + (int64_t)(s.q0 + rc) * a.qs[1] + h * a.qs[2];
@@ -38,9 +61,14 @@ __global__ __launch_bounds__(256) void kd_swa_dq_kernel(SwaArgs a)
         delta += T::dot(dO[ks], ov);
     }
     delta += swa_swap(delta);
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+        swa_arrive(q[ks]);
+        swa_arrive(dO[ks]);
+    }
     const int64_t li = ((int64_t)b * a.Hq + h) * a.Tq + s.q0 + rc;
-    const float lse2 = a.lse[li] * 1.4426950408889634f;
-    if (row < s.nq && g == 0) a.delta[li] = delta;
+    float lse2 = a.lse[li] * LOG2E, dsum = 0.f;
+    asm volatile("" : "+v"(lse2));
     const E* kb = (const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2];
     const E* vb = (const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2];
 
@@ -52,61 +80,147 @@ __global__ __launch_bounds__(256) void kd_swa_dq_kernel(SwaArgs a)
 
     const int pmax = min(s.past + r0 + 127, s.nk - 1);
     const int lo = max(0, s.past + r0 - a.W + 1) / BN, hi = pmax < 0 ? 0 : pmax / BN + 1;
-    const int sk = min((a.S + BN - 1) / BN, lo);
+    const int sk = min((a.S + BN - 1) / BN, lo), nt = sk + max(hi - lo, 0);
     const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;
-    for (int i = 0; i < sk + max(hi - lo, 0); ++i) {
-        const int k0 = (i < sk ? i : lo + (i - sk)) * BN;
-        __syncthreads();
-        swa_stage<E, D, BN, 256>(kt, kb, a.ks[1], k0, s.nk, tid);
-        swa_stage<E, D, BN, 256>(vt, vb, a.vs[1], k0, s.nk, tid);
-        __syncthreads();
+    const bool few = sizeof(E) == 2 && (wp0 < 511 || a.W + a.S < 512);
+    auto key0 = [&](int i) { return (i < sk ? i : lo + (i - sk)) * BN; };
+    auto fetch = [&](int i) {
+        swa_fetch<E, D, BN, 256>(kt[i & 1], kb, a.ks[1], key0(i), s.nk, tid);
+        swa_fetch<E, D, BN, 256>(vt[i & 1], vb, a.vs[1], key0(i), s.nk, tid);
+    };
+    if (nt > 0) fetch(0);
+    for (int i = 0; i < nt; ++i) {
+        swa_landed();
+        if (i + 1 < nt) fetch(i + 1);
+        const int k0 = key0(i);
         if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) continue;
+        const E* kl = kt[i & 1];
+        const E* vl = vt[i & 1];
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
-#pragma unroll
+#pragma unroll 1      // (unrolled, the two halves spill)
         for (int n = 0; n < NS; ++n) {
             floatx16 sc, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < NK; ++ks) {
-                sc = T::mma(swa_ld_row<E, D>(kt, 32 * n + (lane & 31), ks, g), q[ks], sc);
-                dp = T::mma(swa_ld_row<E, D>(vt, 32 * n + (lane & 31), ks, g), dO[ks], dp);
+                sc = T::mma(swa_ld_row<E, D>(kl, 32 * n + (lane & 31), ks, g), q[ks], sc);
+                dp = T::mma(swa_ld_row<E, D>(vl, 32 * n + (lane & 31), ks, g), dO[ks], dp);
+            }
+            if (!full) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) {
+                        sc[r] = -INFINITY;     // a weight of 0, whatever dP holds there
+                        dp[r] = 0.f;
+                    }
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(sc[r], a.c, -lse2)) * (dp[r] - delta);
-                const bool vis = full || swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S);
-                sc[r] = vis ? p : 0.f;
+                const float p = __builtin_amdgcn_exp2f(fmaf(sc[r], a.c, -lse2));
+                dsum = fmaf(p, dp[r], dsum);
+                sc[r] = p * (dp[r] - delta);
+            }
+            if (!full) {      // a row that sees nothing has lse = -infinity and no weights
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) sc[r] = 0.f;
             }
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
                 const Frag p = T::pack(sc, j);
+                Frag c[ND];
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt)
-                    acc[dt] = T::mma(T::template ld_col<D>(kt, 32 * n + (32 / NP) * j, 32 * dt, lane), p, acc[dt]);
+                for (int dt = 0; dt < ND; ++dt) {
+                    c[dt] = T::template ld_col<D>(kl, 32 * n + (32 / NP) * j, 32 * dt, lane);
+                    acc[dt] = T::mma(c[dt], p, acc[dt]);
+                }
+                if (few) {
+                    const Frag rest = T::rest(sc, j, p);
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) acc[dt] = T::mma(c[dt], rest, acc[dt]);
+                }
             }
         }
     }
-    if (row < s.nq) swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
+    dsum += swa_swap(dsum);
+    if (row >= s.nq) return;
+    swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
+    if (g == 0) a.rows[li] = make_float2(lse2, pos < 0 ? 0.f : dsum);
 }
 
-// dK and dV of 128 keys of one key head, 32 per wave: tiles of BQ query rows
-// of every head of the group pass through LDS.  S = Q Kt has the queries as
-// rows, so the weights and their gradients are again the B operands of the
-// next products (dVt += dOt P, dKt += Qt dS).
-template <class E, int D, int BQ>
-__global__ __launch_bounds__(256) void kd_swa_dkv_kernel(SwaArgs a)
+// One 32-row piece of a query tile against 32 keys held as B operands: S and
+// dP have the queries as rows, so the weights and their gradients are again
+// the B operands of the next products (dVt += dOt P, dKt += Qt dS).
+template <class E, int D>
+__device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const float2* rl, int r0,
+                                             const typename SwaT<E>::Frag* k, const typename SwaT<E>::Frag* v,
+                                             floatx16* dk, floatx16* dv, float c, bool full, int lane, int key, int p0,
+                                             int left, int W, int S)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
-    constexpr int NK = D / T::KC, NS = BQ / 32, ND = D / 32, NP = 16 / T::PR;
-    __shared__ __align__(16) E qt[BQ * D];
-    __shared__ __align__(16) E dt_[BQ * D];
-    __shared__ __align__(16) float ls[BQ], ds[BQ];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 5;
-    const int hk = blockIdx.y, b = blockIdx.z, G = a.Hq / a.Hkv;
+    constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    const int g = lane >> 5;
+    floatx16 sc, dp;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+        sc = T::mma(swa_ld_row<E, D>(qt, r0 + (lane & 31), ks, g), k[ks], sc);
+        dp = T::mma(swa_ld_row<E, D>(dt, r0 + (lane & 31), ks, g), v[ks], dp);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int rr = 8 * (j / 2) + 4 * g + 2 * (j % 2);      // two rows
+        const floatx4 ld = *reinterpret_cast<const floatx4*>(rl + r0 + rr);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 2 * j + e;
+            float p = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ld[2 * e]));
+            float d = p * (dp[r] - ld[2 * e + 1]);
+            if (!full) {
+                const bool vis = rr + e < left && swa_visible(key, p0 + rr + e, W, S);
+                p = vis ? p : 0.f;
+                d = vis ? d : 0.f;
+            }
+            sc[r] = p;
+            dp[r] = d;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        const Frag pv = T::pack(sc, j), pk = T::pack(dp, j);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+            dv[i] = T::mma(T::template ld_col<D>(dt, r0 + (32 / NP) * j, 32 * i, lane), pv, dv[i]);
+            dk[i] = T::mma(T::template ld_col<D>(qt, r0 + (32 / NP) * j, 32 * i, lane), pk, dk[i]);
+        }
+    }
+}
+
+// dK and dV of 128 keys of one key head, 32 per wave: tiles of BQ query rows
+// of every head of the group pass through LDS, one tile ahead.
+template <class E, int D, int BQ>
+__global__ __launch_bounds__(256, 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
+{
+    typedef SwaT<E> T;
+    typedef typename T::Frag Frag;
+    constexpr int NK = D / T::KC, NS = BQ / 32, ND = D / 32;
+    // the tiles first: loads to LDS take destinations in its first 64 KB
+    __shared__ __align__(16) struct {
+        E q[2][BQ * D], dO[2][BQ * D];
+        float2 rows[2][BQ];
+    } sm;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
+    const int G = a.Hq / a.Hkv;
+    int64_t item;
+    if (!swa_item((int64_t)nslots * a.Hkv * a.B, item)) return;
+    const int slot = item % nslots;
+    item /= nslots;
+    const int hk = item % a.Hkv, b = item / a.Hkv;
     SwaSeq s;
-    if (!swa_locate(a, blockIdx.x, 128, true, s)) return;
+    if (!swa_locate(a, slot, 128, true, s)) return;
     const int k0 = s.blk * 128, key = k0 + 32 * w + (lane & 31), kc = min(key, s.nk - 1);
     const E* krow = (const E*)a.k + b * a.ks[0] + (int64_t)(s.q0 + kc) * a.ks[1] + hk * a.ks[2];
     const E* vrow = (const E*)a.v + b * a.vs[0] + (int64_t)(s.q0 + kc) * a.vs[1] + hk * a.vs[2];
@@ -116,97 +230,211 @@ __global__ __launch_bounds__(256) void kd_swa_dkv_kernel(SwaArgs a)
         k[ks] = key < s.nk ? swa_ld_mem<E>(krow, ks, g) : swa_zero<E>();
         v[ks] = key < s.nk ? swa_ld_mem<E>(vrow, ks, g) : swa_zero<E>();
     }
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+        swa_arrive(k[ks]);
+        swa_arrive(v[ks]);
+    }
     floatx16 dk[ND], dv[ND];
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
 
-    // rows that see a key of the block
-    const int t0 = max(0, k0 - s.past) / BQ * BQ;
-    const int t1 = k0 < a.S ? s.nq : min(s.nq, k0 + 127 + a.W - s.past);
+    // rows whose window holds a key of the block, for every head of the group
+    const int t0 = max(0, k0 - s.past) / BQ, t1 = min(s.nq, k0 + 127 + a.W - s.past);
+    const int per = max(0, (t1 + BQ - 1) / BQ - t0), nt = per * G;
     const int wk0 = k0 + 32 * w, wk1 = wk0 + 31;
-    for (int hg = 0; hg < G; ++hg) {
-        const int h = hk * G + hg;
-        const E* qb = (const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + h * a.qs[2];
-        const E* ob = (const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + h) * D;
-        const int64_t li = ((int64_t)b * a.Hq + h) * a.Tq + s.q0;
-        for (int t = t0; t < t1; t += BQ) {
-            __syncthreads();
-            swa_stage<E, D, BQ, 256>(qt, qb, a.qs[1], t, s.nq, tid);
-            swa_stage<E, D, BQ, 256>(dt_, ob, (int64_t)a.Hq * D, t, s.nq, tid);
-            if (tid < BQ) {
-                ls[tid] = t + tid < s.nq ? a.lse[li + t + tid] * 1.4426950408889634f : 0.f;
-                ds[tid] = t + tid < s.nq ? a.delta[li + t + tid] : 0.f;
-            }
-            __syncthreads();
-            const int p0 = s.past + t, p1 = p0 + BQ - 1;
-            if (p1 < wk0 || (p0 - wk1 >= a.W && wk0 >= a.S)) continue;
-            const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= s.nq;
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                floatx16 sc, dp;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < NK; ++ks) {
-                    sc = T::mma(swa_ld_row<E, D>(qt, 32 * n + (lane & 31), ks, g), k[ks], sc);
-                    dp = T::mma(swa_ld_row<E, D>(dt_, 32 * n + (lane & 31), ks, g), v[ks], dp);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int rr = 32 * n + 8 * j + 4 * g;
-                    const floatx4 le = *reinterpret_cast<const floatx4*>(ls + rr);
-                    const floatx4 de = *reinterpret_cast<const floatx4*>(ds + rr);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 4 * j + e;
-                        const bool vis = full || (t + rr + e < s.nq && swa_visible(key, p0 + rr + e, a.W, a.S));
-                        const float p = __builtin_amdgcn_exp2f(fmaf(sc[r], a.c, -le[e]));
-                        sc[r] = vis ? p : 0.f;
-                        dp[r] = vis ? p * (dp[r] - de[e]) : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const Frag pv = T::pack(sc, j), pk = T::pack(dp, j);
-#pragma unroll
-                    for (int i = 0; i < ND; ++i) {
-                        dv[i] = T::mma(T::template ld_col<D>(dt_, 32 * n + (32 / NP) * j, 32 * i, lane), pv, dv[i]);
-                        dk[i] = T::mma(T::template ld_col<D>(qt, 32 * n + (32 / NP) * j, 32 * i, lane), pk, dk[i]);
-                    }
-                }
-            }
+    const E* qb = (const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + hk * G * a.qs[2];
+    const E* ob = (const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G) * D;
+    const float2* rb = a.rows + ((int64_t)b * a.Hq + hk * G) * a.Tq + s.q0;
+    int fh = 0, ft = 0;      // head and tile of the next fetch
+    float2 next;             // lse and delta of a row of it
+    auto fetch = [&](int i) {
+        const int t = (t0 + ft) * BQ;
+        swa_fetch<E, D, BQ, 256>(sm.q[i & 1], qb + fh * a.qs[2], a.qs[1], t, s.nq, tid);
+        swa_fetch<E, D, BQ, 256>(sm.dO[i & 1], ob + fh * D, (int64_t)a.Hq * D, t, s.nq, tid);
+        if (tid < BQ) next = rb[(int64_t)fh * a.Tq + min(t + tid, s.nq - 1)];
+        if (++ft == per) {
+            ft = 0;
+            ++fh;
         }
+    };
+    if (nt > 0) {
+        fetch(0);
+        if (tid < BQ) sm.rows[0][tid] = next;
+    }
+    int ct = 0;
+    for (int i = 0; i < nt; ++i) {
+        swa_landed();
+        if (i + 1 < nt) fetch(i + 1);
+        const int t = (t0 + ct) * BQ;
+        if (++ct == per) ct = 0;
+        const int p0 = s.past + t, p1 = p0 + BQ - 1;
+        if (!(p1 < wk0 || (p0 - wk1 >= a.W && wk0 >= a.S))) {
+            const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= t1;   // (rows from t1 on: the sinks' pass)
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                swa_dkv_tile<E, D>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1], 32 * n, k, v, dk, dv, a.c, full, lane,
+                                   key, p0 + 32 * n, t1 - t - 32 * n, a.W, a.S);
+        }
+        if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][tid] = next;
     }
     if (key >= s.nk) return;
+    // the sinks' part from the queries beyond the window
+    if (a.pslots > 0 && key < a.S && swa_far(a, s.past) < s.nq) {
+        const int first = s.slot0 + swa_far(a, s.past) / SWA_CHUNK, last = s.slot0 + (s.nq - 1) / SWA_CHUNK;
+        for (int x = first; x <= last; ++x) {
+            const float* pk = a.part + ((((int64_t)b * a.pslots + x) * a.Hkv + hk) * 2 * SWA_MAX_SINKS + key) * D;
+            const float* pv = pk + SWA_MAX_SINKS * D;
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const floatx4 x0 = *reinterpret_cast<const floatx4*>(pk + 32 * i + 8 * j + 4 * g);
+                    const floatx4 x1 = *reinterpret_cast<const floatx4*>(pv + 32 * i + 8 * j + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dk[i][4 * j + e] += x0[e];
+                        dv[i][4 * j + e] += x1[e];
+                    }
+                }
+        }
+    }
     const int64_t at = (((int64_t)b * a.Tk + s.q0 + key) * a.Hkv + hk) * D;
     swa_store_row<E, D>((E*)a.dk + at, dk, a.scale, g);
     swa_store_row<E, D>((E*)a.dv + at, dv, 1.f, g);
 }
 
+// Partial dK and dV of 32 sinks from one chunk of queries beyond the window:
+// the waves share the rows (32 each of a tile), their sums are joined in LDS
+// one wave after the other.
+template <class E, int D, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
+{
+    typedef SwaT<E> T;
+    typedef typename T::Frag Frag;
+    constexpr int NK = D / T::KC, ND = D / 32, BQ = 32 * NW;
+    __shared__ __align__(16) struct {
+        E q[BQ * D], dO[BQ * D];
+        float2 rows[BQ];
+    } sm;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
+    const int G = a.Hq / a.Hkv, ng = (a.S + 31) / 32;
+    const int slot = blockIdx.x / ng, k0 = blockIdx.x % ng * 32, hk = blockIdx.y, b = blockIdx.z;
+    SwaSeq s;
+    if (!swa_locate(a, slot, SWA_CHUNK, false, s)) return;
+    const int ta = max(s.blk * SWA_CHUNK, swa_far(a, s.past)), tb = min(s.blk * SWA_CHUNK + SWA_CHUNK, s.nq);
+    if (ta >= tb) return;
+    const int key = k0 + (lane & 31), kc = min(key, s.nk - 1);
+    const E* krow = (const E*)a.k + b * a.ks[0] + (int64_t)(s.q0 + kc) * a.ks[1] + hk * a.ks[2];
+    const E* vrow = (const E*)a.v + b * a.vs[0] + (int64_t)(s.q0 + kc) * a.vs[1] + hk * a.vs[2];
+    Frag k[NK], v[NK];
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+        k[ks] = swa_ld_mem<E>(krow, ks, g);
+        v[ks] = swa_ld_mem<E>(vrow, ks, g);
+    }
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+        swa_arrive(k[ks]);
+        swa_arrive(v[ks]);
+    }
+    floatx16 dk[ND], dv[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
+    const bool all = k0 + 32 <= a.S;
+    for (int hg = 0; hg < G; ++hg) {
+        const int h = hk * G + hg;
+        const E* qb = (const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + h * a.qs[2];
+        const E* ob = (const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + h) * D;
+        const float2* rb = a.rows + ((int64_t)b * a.Hq + h) * a.Tq + s.q0;
+        for (int t = ta; t < tb; t += BQ) {
+            __syncthreads();
+            swa_fetch<E, D, BQ, 64 * NW>(sm.q, qb, a.qs[1], t, s.nq, tid);
+            swa_fetch<E, D, BQ, 64 * NW>(sm.dO, ob, (int64_t)a.Hq * D, t, s.nq, tid);
+            if (tid < BQ) sm.rows[tid] = rb[min(t + tid, s.nq - 1)];
+            swa_landed();
+            // beyond the window a row sees the sinks alone: window 1 leaves their mask
+            swa_dkv_tile<E, D>(sm.q, sm.dO, sm.rows, 32 * w, k, v, dk, dv, a.c, all && t + BQ <= tb, lane, key,
+                               s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
+        }
+    }
+    __syncthreads();
+    float* sum = reinterpret_cast<float*>(sm.q);     // 32 keys by D, dK then dV
+    float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hkv + hk) * 2 * SWA_MAX_SINKS + k0) * D;
+    for (int x = 0; x < 2; ++x) {
+        for (int y = 0; y < NW; ++y) {
+            if (w == y) {
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        floatx4* p = reinterpret_cast<floatx4*>(sum + (lane & 31) * D + 32 * i + 8 * j + 4 * g);
+                        floatx4 z;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[e] = x == 0 ? dk[i][4 * j + e] : dv[i][4 * j + e];
+                        *p = y == 0 ? z : *p + z;
+                    }
+            }
+            __syncthreads();
+        }
+        for (int i = tid; i < 32 * D / 4; i += 64 * NW)
+            if (k0 + i / (D / 4) < a.S)
+                reinterpret_cast<floatx4*>(out + x * SWA_MAX_SINKS * D)[i] = reinterpret_cast<const floatx4*>(sum)[i];
+        __syncthreads();
+    }
+}
+
+static int64_t swa_slots(bool packed, int N, int T, int R) { return packed ? (int64_t)T / R + N : ((int64_t)T + R - 1) / R; }
+
+// Chunks of the sinks' partial sums; none where every query lies within the
+// window of the first 128 keys.
+static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S) {
+    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, SWA_CHUNK) : 0;
+}
+
+static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * Hq * 8 + 255) & ~(size_t)255; }
+
+size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {
+    const int nb = packed ? 1 : B;
+    return swa_rows_bytes(nb, Tq, Hq) +
+           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S) * nb * Hkv * 2 * SWA_MAX_SINKS * d * 4;
+}
+
 template <class E, int D>
-static hipError_t swa_bwd(const SwaArgs& a, hipStream_t st)
+static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
 {
     constexpr int BN = sizeof(E) == 2 ? 64 : 32;
-    const unsigned nq = a.cu ? (unsigned)(a.Tq / 128 + a.N) : (unsigned)(((int64_t)a.Tq + 127) / 128);
-    const unsigned nk = a.cu ? nq : (unsigned)(((int64_t)a.Tk + 127) / 128);
+    const int64_t nq = swa_slots(a.cu, a.N, a.Tq, 128), nk = swa_slots(a.cu, a.N, a.Tk, 128);
+    const int64_t gq = swa_grid(nq * a.Hq * a.B), gk = swa_grid(nk * a.Hkv * a.B);
+    const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S);
+    if (gq > INT32_MAX || gk > INT32_MAX || np > INT32_MAX / 2) return hipErrorInvalidValue;
+    a.rows = (float2*)ws;
+    a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));
+    a.pslots = (int)np;
     if (a.Tq > 0) {
-        kd_swa_dq_kernel<E, D, BN><<<dim3(nq, a.Hq, a.B), 256, 0, st>>>(a);
+        kd_swa_dq_kernel<E, D, BN><<<(unsigned)gq, 256, 0, st>>>(a, (int)nq);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (np > 0) {
+        constexpr int NW = sizeof(E) == 2 ? 4 : 2;
+        kd_swa_sink_kernel<E, D, NW><<<dim3((unsigned)(np * ((a.S + 31) / 32)), a.Hkv, a.B), 64 * NW, 0, st>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (nk == 0) return hipSuccess;
-    kd_swa_dkv_kernel<E, D, 32><<<dim3(nk, a.Hkv, a.B), 256, 0, st>>>(a);
+    kd_swa_dkv_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
     return hipGetLastError();
 }
 
-size_t swa_bwd_workspace_bytes(int B, int Tq, int Hq) { return (((size_t)B * Tq * Hq * 4) + 255) & ~(size_t)255; }
-
-hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, hipStream_t st)
+hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, void* ws, hipStream_t st)
 {
-    if (bf16) return d == 32 ? swa_bwd<__bf16, 32>(a, st) : d == 64 ? swa_bwd<__bf16, 64>(a, st) : swa_bwd<__bf16, 128>(a, st);
-    return d == 32 ? swa_bwd<float, 32>(a, st) : d == 64 ? swa_bwd<float, 64>(a, st) : swa_bwd<float, 128>(a, st);
+    if (bf16) return d == 32 ? swa_bwd<__bf16, 32>(a, ws, st) : d == 64 ? swa_bwd<__bf16, 64>(a, ws, st) : swa_bwd<__bf16, 128>(a, ws, st);
+    return d == 32 ? swa_bwd<float, 32>(a, ws, st) : d == 64 ? swa_bwd<float, 64>(a, ws, st) : swa_bwd<float, 128>(a, ws, st);
 }
 
 }  // namespace kd

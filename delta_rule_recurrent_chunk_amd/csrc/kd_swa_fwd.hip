@@ -13,7 +13,7 @@
 namespace kd {
 
 template <class E, int D, int BN>
-__global__ __launch_bounds__(256, 2) void kd_swa_fwd_kernel(SwaArgs a, int nslots)
+__global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_kernel(SwaArgs a, int nslots)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;

@@ -222,7 +222,8 @@ def swa_inputs(B, Tq, Tk, Hq, Hkv, d, dtype, seed):
 SWA = [  # Tq, Tk, Hq, Hkv, window, sinks
     (1, 1, 1, 1, 1, 0), (1, 300, 4, 1, 64, 4), (5, 5, 2, 2, 2, 1), (64, 64, 2, 1, 64, 0), (130, 130, 3, 1, 33, 4),
     (200, 200, 4, 2, 1, 0), (200, 200, 2, 2, 1, 64), (257, 257, 2, 1, 1000, 3), (129, 320, 2, 1, 100, 7),
-    (300, 170, 2, 1, 50, 2), (7, 0, 2, 1, 4, 1), (0, 9, 2, 1, 4, 1), (333, 333, 8, 1, 65, 64), (600, 600, 1, 1, 129, 4)]
+    (300, 170, 2, 1, 50, 2), (7, 0, 2, 1, 4, 1), (0, 9, 2, 1, 4, 1), (333, 333, 8, 1, 65, 64), (600, 600, 1, 1, 129, 4),
+    (2300, 2300, 2, 1, 100, 40), (1500, 1700, 2, 2, 700, 5)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -249,7 +250,7 @@ def test_swa_forward_and_backward(Tq, Tk, Hq, Hkv, window, sinks, d, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens", [[1], [0, 5, 0], [128, 128, 1, 127], [300, 1, 1, 0, 77, 129, 256],
-                                  [3] * 70 + [200]])
+                                  [3] * 70 + [200], [1500, 1, 2100, 90]])
 def test_swa_packed_equals_each_sequence_alone(lens, dtype):
     import delta_rule_recurrent_chunk_amd as kd
     torch = _torch()
