@@ -28,7 +28,7 @@ struct SwaArgs {
     const void* dO;                    // [B, Tq, Hq, d]
     float2* rows;                      // [B, Hq, Tq]: lse log2(e) and delta of every query
     float* part;                       // partial dK, dV of the sinks
-    int pslots;                        // query chunks of the sinks' pass (0: none)
+    int pslots, chunk;                 // query chunks of the sinks' pass (0: none), their rows
     void *dq, *dk, *dv;                // contiguous
     const int* cu;                     // packed: N + 1 offsets into the Tq == Tk rows
     int B, N, Tq, Tk, Hq, Hkv;
@@ -161,7 +161,7 @@ __device__ __forceinline__ float swa_swap(float x) { return __shfl_xor(x, 32); }
 // [0, T].  Returns false when the slot holds no rows.
 struct SwaSeq {
     int q0, nq, nk, past, blk;   // first row, rows, keys, position of row 0, block of R rows
-    int slot0;                   // the sequence's first slot in chunks of 1024 rows
+    int slot0;                   // the sequence's first chunk of the sinks' pass
 };
 __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bool keys, SwaSeq& s) {
     if (!a.cu) {
@@ -187,36 +187,73 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     s.nq = s.nk = hi - lo;
     s.past = 0;
     s.blk = slot - (lo / R + q);
-    s.slot0 = lo / 1024 + q;
+    s.slot0 = a.chunk > 0 ? lo / a.chunk + q : 0;
     return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
 }
 
 __device__ __forceinline__ bool swa_visible(int key, int pos, int W, int S) {
-    return key <= pos && (pos - key < W || key < S);
+    return (key <= pos) & ((pos - key < W) | (key < S));      // (no branches)
 }
 
-// Rows row0 .. row0 + R - 1 of a matrix (row stride rs elements) into a tile, by
-// loads that go straight to LDS (a wave's lane i fills the 16 bytes
-// at its base + 16 i, so the chunk order within a row is set by which chunk
-// each lane reads).  Rows past the end repeat the last one: their keys are
-// masked for every query.  The loads are in flight until swa_landed().
-template <class E, int D, int R, int NT>
-__device__ __forceinline__ void swa_fetch(E* tile, const E* base, int64_t rs, int row0, int rows, int tid) {
-    typedef SwaTile<E, D> TL;
-    static_assert(R * TL::CPR % NT == 0, "whole instructions");
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-#pragma unroll
-    for (int i = 0; i < R * TL::CPR / NT; ++i) {
-        const int at = i * NT + tid, r = at / TL::CPR, ch = (at % TL::CPR) ^ TL::swz(r);
-        const E* src = base + (int64_t)min(row0 + r, rows - 1) * rs + ch * TL::EPC;
-        E* dst = tile + (i * NT + 64 * w) * TL::EPC;
-        // (written out, because the compiler would let every LDS read wait for the
-        // builtin's loads, those of the other buffer too)
-        const uint32_t at_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at_lds), "v"(src)
-                     : "memory", "m0");
-    }
+// Tiles of R rows of a matrix (row stride rs elements, `rows` rows) by loads
+// that go straight to LDS: a wave's lane i fills the 16 bytes at its base + 16 i,
+// so the chunk order within a row is set by which chunk each lane reads.  The
+// addresses are a scalar base and one 32-bit offset per lane that all tiles
+// share; a last tile with rows past the end repeats the last row (its keys are
+// masked for every query).  The loads are in flight until swa_landed(); they
+// are written out because the compiler would make every LDS read wait for a
+// builtin's loads, those of the other buffer too.  Destinations lie in the
+// first 64 KB of LDS.
+__device__ __forceinline__ int64_t swa_uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
 }
+template <class E, int D, int R, int NT>
+struct SwaFetch {
+    typedef SwaTile<E, D> TL;
+    static constexpr int STEP = NT / TL::CPR;              // rows per round of the workgroup
+    static constexpr int NV = STEP >= 16 ? 1 : 16 / STEP;  // rounds until the chunk order (of 16 rows) repeats
+    static_assert(R % STEP == 0, "whole instructions");
+    const E* base;
+    int64_t rs;
+    int rows, r, ch;
+    uint32_t lane[NV];
+    bool far;
+
+    __device__ __forceinline__ SwaFetch(const E* base_, int64_t rs_, int rows_, int tid)
+        : base((const E*)swa_uniform((int64_t)base_)), rs(swa_uniform(rs_)), rows(__builtin_amdgcn_readfirstlane(rows_)) {
+        r = tid / TL::CPR;
+        ch = tid % TL::CPR;
+        far = rs > (1 << 22);      // rows too far apart for 32-bit offsets
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            lane[i] = (uint32_t)((r * (int)rs + (ch ^ TL::swz(r + i * STEP)) * TL::EPC) * (int)sizeof(E));
+    }
+    // into `tile` of a buffer at byte `at` of LDS, from head offset `ho` (elements)
+    __device__ __forceinline__ void operator()(E* tile, int64_t ho, int row, int w) const {
+        const int row0 = __builtin_amdgcn_readfirstlane(row);
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile + 1024 * w;
+        const E* b = base + swa_uniform(ho) + (int64_t)row0 * rs;
+        if (row0 + R <= rows && !far) {
+#pragma unroll
+            for (int i = 0; i < R / STEP; ++i)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at + i * NT * 16),
+                             "v"(lane[i % NV]), "s"(swa_uniform((int64_t)(b + (int64_t)(i * STEP) * rs)))
+                             : "memory", "m0");
+        } else {
+            // the last tile's rows; each lane's address in full
+            const int last = rows - 1 - row0;
+#pragma unroll
+            for (int i = 0; i < R / STEP; ++i) {
+                const int rr = r + i * STEP;
+                const E* src = b + (int64_t)min(rr, last) * rs + (ch ^ TL::swz(rr)) * TL::EPC;
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at + i * NT * 16),
+                             "v"(src)
+                             : "memory", "m0");
+            }
+        }
+    }
+};
 // all loads of this wave have landed, then all waves of the workgroup are here
 __device__ __forceinline__ void swa_landed() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");

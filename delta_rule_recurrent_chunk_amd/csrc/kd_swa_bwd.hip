@@ -6,7 +6,7 @@
 // Every gradient is summed in registers in a fixed order, no atomics:
 //   1. over query blocks: dQ, and delta for the other two;
 //   2. where queries lie beyond the window of the first 128 keys: the sinks'
-//      dK and dV from those queries, in partial sums over chunks of 1024;
+//      dK and dV from those queries, in partial sums over chunks of queries;
 //   3. over key blocks: dK and dV from the queries whose window holds them,
 //      also summed over the query heads of a group; the first block adds the
 //      partial sums of 2.
@@ -14,7 +14,6 @@
 
 namespace kd {
 
-constexpr int SWA_CHUNK = 1024;        // queries per partial sum of the sinks
 constexpr float LOG2E = 1.4426950408889634f;
 
 // first query beyond the window of keys 0 .. 127
@@ -69,8 +68,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     const int64_t li = ((int64_t)b * a.Hq + h) * a.Tq + s.q0 + rc;
     float lse2 = a.lse[li] * LOG2E, dsum = 0.f;
     asm volatile("" : "+v"(lse2));
-    const E* kb = (const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2];
-    const E* vb = (const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2];
+    const SwaFetch<E, D, BN, 256> kf((const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2], a.ks[1], s.nk, tid);
+    const SwaFetch<E, D, BN, 256> vf((const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2], a.vs[1], s.nk, tid);
 
     floatx16 acc[ND];
 #pragma unroll
@@ -85,8 +84,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     const bool few = sizeof(E) == 2 && (wp0 < 511 || a.W + a.S < 512);
     auto key0 = [&](int i) { return (i < sk ? i : lo + (i - sk)) * BN; };
     auto fetch = [&](int i) {
-        swa_fetch<E, D, BN, 256>(kt[i & 1], kb, a.ks[1], key0(i), s.nk, tid);
-        swa_fetch<E, D, BN, 256>(vt[i & 1], vb, a.vs[1], key0(i), s.nk, tid);
+        kf(kt[i & 1], 0, key0(i), w);
+        vf(vt[i & 1], 0, key0(i), w);
     };
     if (nt > 0) fetch(0);
     for (int i = 0; i < nt; ++i) {
@@ -146,29 +145,38 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     dsum += swa_swap(dsum);
     if (row >= s.nq) return;
     swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
-    if (g == 0) a.rows[li] = make_float2(lse2, pos < 0 ? 0.f : dsum);
+    // (a row that sees nothing: no weight comes of a masked score whatever its lse)
+    if (g == 0) a.rows[li] = lse2 == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse2, dsum);
 }
 
-// One 32-row piece of a query tile against 32 keys held as B operands: S and
-// dP have the queries as rows, so the weights and their gradients are again
-// the B operands of the next products (dVt += dOt P, dKt += Qt dS).
-template <class E, int D>
+// One 32-row piece of a query tile against 32 keys held as B operands (the
+// values' either in registers or as rows of an LDS tile): S and dP have the
+// queries as rows, so the weights and their gradients are again the B operands
+// of the next products (dVt += dOt P, dKt += Qt dS).
+template <class E, int D, class VF>
 __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const float2* rl, int r0,
-                                             const typename SwaT<E>::Frag* k, const typename SwaT<E>::Frag* v,
+                                             const typename SwaT<E>::Frag* k, const VF& v,
                                              floatx16* dk, floatx16* dv, float c, bool full, int lane, int key, int p0,
                                              int left, int W, int S)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    lane += opaque_zero();      // (the tile's LDS addresses are formed anew, not kept across the loop)
     const int g = lane >> 5;
     floatx16 sc, dp;
 #pragma unroll
     for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-        sc = T::mma(swa_ld_row<E, D>(qt, r0 + (lane & 31), ks, g), k[ks], sc);
-        dp = T::mma(swa_ld_row<E, D>(dt, r0 + (lane & 31), ks, g), v[ks], dp);
+    for (int ks = 0; ks < NK; ++ks) sc = T::mma(swa_ld_row<E, D>(qt, r0 + (lane & 31), ks, g), k[ks], sc);
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) dp = T::mma(swa_ld_row<E, D>(dt, r0 + (lane & 31), ks, g), v(ks, lane), dp);
+    if (!full) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int rr = 8 * (r / 4) + 4 * g + r % 4;
+            if (!((rr < left) & swa_visible(key, p0 + rr, W, S))) sc[r] = -INFINITY;
+        }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -177,15 +185,9 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * j + e;
-            float p = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ld[2 * e]));
-            float d = p * (dp[r] - ld[2 * e + 1]);
-            if (!full) {
-                const bool vis = rr + e < left && swa_visible(key, p0 + rr + e, W, S);
-                p = vis ? p : 0.f;
-                d = vis ? d : 0.f;
-            }
-            sc[r] = p;
-            dp[r] = d;
+            // (rows past the end and rows that see nothing have lse2 = 0 here: a masked score has weight 0)
+            sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ld[2 * e]));
+            dp[r] = sc[r] * (dp[r] - ld[2 * e + 1]);
         }
     }
 #pragma unroll
@@ -200,16 +202,21 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
 }
 
 // dK and dV of 128 keys of one key head, 32 per wave: tiles of BQ query rows
-// of every head of the group pass through LDS, one tile ahead.
+// of every head of the group pass through LDS, one tile ahead.  In bf16 the
+// values' fragments are read from LDS too: with those of the keys, dK and dV
+// in registers (160 of 256) two waves fit a SIMD, and one's products overlap
+// the other's exponentials.
 template <class E, int D, int BQ>
-__global__ __launch_bounds__(256, 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = D / T::KC, NS = BQ / 32, ND = D / 32;
+    constexpr bool VL = sizeof(E) == 2;
     // the tiles first: loads to LDS take destinations in its first 64 KB
     __shared__ __align__(16) struct {
         E q[2][BQ * D], dO[2][BQ * D];
+        E v[VL ? 128 * D : 8];
         float2 rows[2][BQ];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
@@ -224,17 +231,25 @@ __global__ __launch_bounds__(256, 1) void kd_swa_dkv_kernel(SwaArgs a, int nslot
     const int k0 = s.blk * 128, key = k0 + 32 * w + (lane & 31), kc = min(key, s.nk - 1);
     const E* krow = (const E*)a.k + b * a.ks[0] + (int64_t)(s.q0 + kc) * a.ks[1] + hk * a.ks[2];
     const E* vrow = (const E*)a.v + b * a.vs[0] + (int64_t)(s.q0 + kc) * a.vs[1] + hk * a.vs[2];
-    Frag k[NK], v[NK];
+    Frag k[NK], vr[VL ? 1 : NK];
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) {
-        k[ks] = key < s.nk ? swa_ld_mem<E>(krow, ks, g) : swa_zero<E>();
-        v[ks] = key < s.nk ? swa_ld_mem<E>(vrow, ks, g) : swa_zero<E>();
+        k[ks] = swa_ld_mem<E>(krow, ks, g);
+        if (!VL) vr[VL ? 0 : ks] = swa_ld_mem<E>(vrow, ks, g);
     }
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) {
         swa_arrive(k[ks]);
-        swa_arrive(v[ks]);
+        if (!VL) swa_arrive(vr[VL ? 0 : ks]);
     }
+    if (VL) {
+        const SwaFetch<E, D, 128, 256> vf((const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2], a.vs[1], s.nk, tid);
+        vf(sm.v, 0, k0, w);
+    }
+    auto v = [&](int ks, int ln) -> Frag {
+        if constexpr (VL) return swa_ld_row<E, D>(sm.v, 32 * w + (ln & 31), ks, ln >> 5);
+        else return vr[ks];
+    };
     floatx16 dk[ND], dv[ND];
 #pragma unroll
     for (int i = 0; i < ND; ++i)
@@ -245,15 +260,15 @@ __global__ __launch_bounds__(256, 1) void kd_swa_dkv_kernel(SwaArgs a, int nslot
     const int t0 = max(0, k0 - s.past) / BQ, t1 = min(s.nq, k0 + 127 + a.W - s.past);
     const int per = max(0, (t1 + BQ - 1) / BQ - t0), nt = per * G;
     const int wk0 = k0 + 32 * w, wk1 = wk0 + 31;
-    const E* qb = (const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + hk * G * a.qs[2];
-    const E* ob = (const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G) * D;
+    const SwaFetch<E, D, BQ, 256> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + hk * G * a.qs[2], a.qs[1], s.nq, tid);
+    const SwaFetch<E, D, BQ, 256> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G) * D, (int64_t)a.Hq * D, s.nq, tid);
     const float2* rb = a.rows + ((int64_t)b * a.Hq + hk * G) * a.Tq + s.q0;
     int fh = 0, ft = 0;      // head and tile of the next fetch
     float2 next;             // lse and delta of a row of it
     auto fetch = [&](int i) {
         const int t = (t0 + ft) * BQ;
-        swa_fetch<E, D, BQ, 256>(sm.q[i & 1], qb + fh * a.qs[2], a.qs[1], t, s.nq, tid);
-        swa_fetch<E, D, BQ, 256>(sm.dO[i & 1], ob + fh * D, (int64_t)a.Hq * D, t, s.nq, tid);
+        qf(sm.q[i & 1], fh * a.qs[2], t, w);
+        of(sm.dO[i & 1], fh * D, t, w);
         if (tid < BQ) next = rb[(int64_t)fh * a.Tq + min(t + tid, s.nq - 1)];
         if (++ft == per) {
             ft = 0;
@@ -280,34 +295,47 @@ __global__ __launch_bounds__(256, 1) void kd_swa_dkv_kernel(SwaArgs a, int nslot
         }
         if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][tid] = next;
     }
-    if (key >= s.nk) return;
-    // the sinks' part from the queries beyond the window
-    if (a.pslots > 0 && key < a.S && swa_far(a, s.past) < s.nq) {
-        const int first = s.slot0 + swa_far(a, s.past) / SWA_CHUNK, last = s.slot0 + (s.nq - 1) / SWA_CHUNK;
-        for (int x = first; x <= last; ++x) {
-            const float* pk = a.part + ((((int64_t)b * a.pslots + x) * a.Hkv + hk) * 2 * SWA_MAX_SINKS + key) * D;
-            const float* pv = pk + SWA_MAX_SINKS * D;
+    // the sinks' part from the queries beyond the window: all threads add the
+    // chunks' partial sums, the lanes that hold the keys take them from LDS
+    if (s.blk == 0 && a.pslots > 0 && swa_far(a, s.past) < s.nq) {
+        const int first = s.slot0 + swa_far(a, s.past) / a.chunk, last = s.slot0 + (s.nq - 1) / a.chunk;
+        float* sum = reinterpret_cast<float*>(&sm);
+        const int64_t step = (int64_t)a.Hq * 2 * SWA_MAX_SINKS * D;      // floats of one chunk
+        for (int x = 0; x < 2; ++x) {
+            const float* pb = a.part + ((int64_t)b * a.pslots + first) * step + ((int64_t)hk * G * 2 + x) * SWA_MAX_SINKS * D;
+            __syncthreads();
+            for (int i = tid; i < a.S * D / 4; i += 256) {
+                floatx4 z = {0.f, 0.f, 0.f, 0.f};
+                for (int y = 0; y <= last - first; ++y)
+#pragma unroll 4
+                    for (int hg = 0; hg < G; ++hg)
+                        z += reinterpret_cast<const floatx4*>(pb + y * step + (int64_t)hg * 2 * SWA_MAX_SINKS * D)[i];
+                reinterpret_cast<floatx4*>(sum)[i] = z;
+            }
+            __syncthreads();
+            if (key < a.S) {
 #pragma unroll
-            for (int i = 0; i < ND; ++i)
+                for (int i = 0; i < ND; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const floatx4 x0 = *reinterpret_cast<const floatx4*>(pk + 32 * i + 8 * j + 4 * g);
-                    const floatx4 x1 = *reinterpret_cast<const floatx4*>(pv + 32 * i + 8 * j + 4 * g);
+                    for (int j = 0; j < 4; ++j) {
+                        const floatx4 z = *reinterpret_cast<const floatx4*>(sum + key * D + 32 * i + 8 * j + 4 * g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        dk[i][4 * j + e] += x0[e];
-                        dv[i][4 * j + e] += x1[e];
+                        for (int e = 0; e < 4; ++e) {
+                            if (x == 0) dk[i][4 * j + e] += z[e];
+                            else dv[i][4 * j + e] += z[e];
+                        }
                     }
-                }
+            }
         }
     }
+    if (key >= s.nk) return;
     const int64_t at = (((int64_t)b * a.Tk + s.q0 + key) * a.Hkv + hk) * D;
     swa_store_row<E, D>((E*)a.dk + at, dk, a.scale, g);
     swa_store_row<E, D>((E*)a.dv + at, dv, 1.f, g);
 }
 
-// Partial dK and dV of 32 sinks from one chunk of queries beyond the window:
-// the waves share the rows (32 each of a tile), their sums are joined in LDS
+// Partial dK and dV of 32 sinks from one chunk of one head's queries beyond the
+// window: the waves share the rows (32 each of a tile), their sums are joined in LDS
 // one wave after the other.
 template <class E, int D, int NW>
 __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
@@ -320,11 +348,11 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
         float2 rows[BQ];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
-    const int G = a.Hq / a.Hkv, ng = (a.S + 31) / 32;
-    const int slot = blockIdx.x / ng, k0 = blockIdx.x % ng * 32, hk = blockIdx.y, b = blockIdx.z;
+    const int ng = (a.S + 31) / 32;
+    const int slot = blockIdx.x / ng, k0 = blockIdx.x % ng * 32, h = blockIdx.y, hk = h / (a.Hq / a.Hkv), b = blockIdx.z;
     SwaSeq s;
-    if (!swa_locate(a, slot, SWA_CHUNK, false, s)) return;
-    const int ta = max(s.blk * SWA_CHUNK, swa_far(a, s.past)), tb = min(s.blk * SWA_CHUNK + SWA_CHUNK, s.nq);
+    if (!swa_locate(a, slot, a.chunk, false, s)) return;
+    const int ta = max(s.blk * a.chunk, swa_far(a, s.past)), tb = min(s.blk * a.chunk + a.chunk, s.nq);
     if (ta >= tb) return;
     const int key = k0 + (lane & 31), kc = min(key, s.nk - 1);
     const E* krow = (const E*)a.k + b * a.ks[0] + (int64_t)(s.q0 + kc) * a.ks[1] + hk * a.ks[2];
@@ -346,25 +374,23 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
     const bool all = k0 + 32 <= a.S;
-    for (int hg = 0; hg < G; ++hg) {
-        const int h = hk * G + hg;
-        const E* qb = (const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + h * a.qs[2];
-        const E* ob = (const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + h) * D;
-        const float2* rb = a.rows + ((int64_t)b * a.Hq + h) * a.Tq + s.q0;
-        for (int t = ta; t < tb; t += BQ) {
-            __syncthreads();
-            swa_fetch<E, D, BQ, 64 * NW>(sm.q, qb, a.qs[1], t, s.nq, tid);
-            swa_fetch<E, D, BQ, 64 * NW>(sm.dO, ob, (int64_t)a.Hq * D, t, s.nq, tid);
-            if (tid < BQ) sm.rows[tid] = rb[min(t + tid, s.nq - 1)];
-            swa_landed();
-            // beyond the window a row sees the sinks alone: window 1 leaves their mask
-            swa_dkv_tile<E, D>(sm.q, sm.dO, sm.rows, 32 * w, k, v, dk, dv, a.c, all && t + BQ <= tb, lane, key,
-                               s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
-        }
+    auto vf = [&](int ks, int) -> Frag { return v[ks]; };
+    const SwaFetch<E, D, BQ, 64 * NW> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + h * a.qs[2], a.qs[1], s.nq, tid);
+    const SwaFetch<E, D, BQ, 64 * NW> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + h) * D, (int64_t)a.Hq * D, s.nq, tid);
+    const float2* rb = a.rows + ((int64_t)b * a.Hq + h) * a.Tq + s.q0;
+    for (int t = ta; t < tb; t += BQ) {
+        __syncthreads();
+        qf(sm.q, 0, t, w);
+        of(sm.dO, 0, t, w);
+        if (tid < BQ) sm.rows[tid] = rb[min(t + tid, s.nq - 1)];
+        swa_landed();
+        // beyond the window a row sees the sinks alone: window 1 leaves their mask
+        swa_dkv_tile<E, D>(sm.q, sm.dO, sm.rows, 32 * w, k, vf, dk, dv, a.c, all && t + BQ <= tb, lane, key,
+                           s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
     }
     __syncthreads();
     float* sum = reinterpret_cast<float*>(sm.q);     // 32 keys by D, dK then dV
-    float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hkv + hk) * 2 * SWA_MAX_SINKS + k0) * D;
+    float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hq + h) * 2 * SWA_MAX_SINKS + k0) * D;
     for (int x = 0; x < 2; ++x) {
         for (int y = 0; y < NW; ++y) {
             if (w == y) {
@@ -390,18 +416,22 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
 
 static int64_t swa_slots(bool packed, int N, int T, int R) { return packed ? (int64_t)T / R + N : ((int64_t)T + R - 1) / R; }
 
+// Rows of a chunk of the sinks' pass: sixteen chunks of a sequence as long as
+// all queries together, none below 256 rows.
+static int swa_chunk(int Tq) { return max(256, (Tq / 16 + 127) / 128 * 128); }
+
 // Chunks of the sinks' partial sums; none where every query lies within the
 // window of the first 128 keys.
 static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S) {
-    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, SWA_CHUNK) : 0;
+    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, swa_chunk(Tq)) : 0;
 }
 
 static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * Hq * 8 + 255) & ~(size_t)255; }
 
-size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {
+size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int d, int W, int S) {
     const int nb = packed ? 1 : B;
     return swa_rows_bytes(nb, Tq, Hq) +
-           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S) * nb * Hkv * 2 * SWA_MAX_SINKS * d * 4;
+           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S) * nb * Hq * 2 * SWA_MAX_SINKS * d * 4;
 }
 
 template <class E, int D>
@@ -415,6 +445,7 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     a.rows = (float2*)ws;
     a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));
     a.pslots = (int)np;
+    a.chunk = swa_chunk(a.Tq);
     if (a.Tq > 0) {
         kd_swa_dq_kernel<E, D, BN><<<(unsigned)gq, 256, 0, st>>>(a, (int)nq);
         const hipError_t e = hipGetLastError();
@@ -422,12 +453,12 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     }
     if (np > 0) {
         constexpr int NW = sizeof(E) == 2 ? 4 : 2;
-        kd_swa_sink_kernel<E, D, NW><<<dim3((unsigned)(np * ((a.S + 31) / 32)), a.Hkv, a.B), 64 * NW, 0, st>>>(a);
+        kd_swa_sink_kernel<E, D, NW><<<dim3((unsigned)(np * ((a.S + 31) / 32)), a.Hq, a.B), 64 * NW, 0, st>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (nk == 0) return hipSuccess;
-    kd_swa_dkv_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
+    kd_swa_dkv_kernel<E, D, sizeof(E) * D == 64 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
     return hipGetLastError();
 }
 

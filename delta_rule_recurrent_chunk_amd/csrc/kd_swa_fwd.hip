@@ -39,8 +39,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
     for (int ks = 0; ks < NK; ++ks) q[ks] = row < s.nq ? swa_ld_mem<E>(qrow, ks, g) : swa_zero<E>();
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
-    const E* kb = (const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2];
-    const E* vb = (const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2];
+    const SwaFetch<E, D, BN, 256> kf((const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2], a.ks[1], s.nk, tid);
+    const SwaFetch<E, D, BN, 256> vf((const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2], a.vs[1], s.nk, tid);
 
     floatx16 o[ND];
 #pragma unroll
@@ -56,8 +56,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
     const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;      // this wave's positions
     auto key0 = [&](int i) { return (i < sk ? i : lo + (i - sk)) * BN; };
     auto fetch = [&](int i) {
-        swa_fetch<E, D, BN, 256>(kt[i & 1], kb, a.ks[1], key0(i), s.nk, tid);
-        swa_fetch<E, D, BN, 256>(vt[i & 1], vb, a.vs[1], key0(i), s.nk, tid);
+        kf(kt[i & 1], 0, key0(i), w);
+        vf(vt[i & 1], 0, key0(i), w);
     };
     if (nt > 0) fetch(0);
     for (int i = 0; i < nt; ++i) {
