@@ -54,9 +54,9 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     float delta = 0.f;
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) {
-        q[ks] = row < s.nq ? swa_ld_mem<E>(qrow, ks, g) : swa_zero<E>();
-        dO[ks] = row < s.nq ? swa_ld_mem<E>((const E*)a.dO + orow, ks, g) : swa_zero<E>();
-        const Frag ov = row < s.nq ? swa_ld_mem<E>((const E*)a.o + orow, ks, g) : swa_zero<E>();
+        q[ks] = swa_ld_mem<E>(qrow, ks, g);
+        dO[ks] = swa_ld_mem<E>((const E*)a.dO + orow, ks, g);
+        const Frag ov = swa_ld_mem<E>((const E*)a.o + orow, ks, g);
         delta += T::dot(dO[ks], ov);
     }
     delta += swa_swap(delta);

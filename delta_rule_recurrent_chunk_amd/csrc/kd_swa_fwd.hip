@@ -36,7 +36,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
     const E* qrow = (const E*)a.q + b * a.qs[0] + (int64_t)(s.q0 + min(row, s.nq - 1)) * a.qs[1] + h * a.qs[2];
     Frag q[NK];
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) q[ks] = row < s.nq ? swa_ld_mem<E>(qrow, ks, g) : swa_zero<E>();
+    for (int ks = 0; ks < NK; ++ks) q[ks] = swa_ld_mem<E>(qrow, ks, g);
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
     const SwaFetch<E, D, BN, 256> kf((const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2], a.ks[1], s.nk, tid);
@@ -69,6 +69,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
         const E* kl = kt[i & 1];
         const E* vl = vt[i & 1];
         floatx16 sc[NS];
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
 #pragma unroll
@@ -77,6 +78,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
             for (int ks = 0; ks < NK; ++ks)
                 sc[n] = T::mma(swa_ld_row<E, D>(kl, 32 * n + (lane & 31), ks, g), q[ks], sc[n]);
         }
+        __builtin_amdgcn_s_setprio(0);
         // every pair of the tile visible: no mask
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
         if (!full) {
@@ -112,6 +114,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
                 ls += sc[n][r];
             }
         l += ls;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -121,6 +124,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
                 for (int dt = 0; dt < ND; ++dt)
                     o[dt] = T::mma(T::template ld_col<D>(vl, 32 * n + (32 / NP) * j, 32 * dt, lane), p, o[dt]);
             }
+        __builtin_amdgcn_s_setprio(0);
     }
     l += swa_swap(l);
     if (row >= s.nq) return;
