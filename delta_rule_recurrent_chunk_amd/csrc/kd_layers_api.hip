@@ -210,9 +210,7 @@ kd_status kron_delta_rope(const kd_rope_desc* d, const void* q, const void* k, c
     if (d->B < 1 || d->T < 0 || d->Hq < 1 || d->Hk < 0 || d->d < 1 || d->d > kd::ROPE_MAX_D || d->rot < 2 ||
         d->rot > d->d || d->rot % 2 != 0 || d->layout < 0 || d->layout > 1 || !isfinite(d->scale))
         return KD_ERR_SHAPE;
-    if ((int64_t)d->Hq * d->d > INT32_MAX || (int64_t)d->Hk * d->d > INT32_MAX ||
-        (int64_t)d->B * d->T > (int64_t)4 * INT32_MAX)
-        return KD_ERR_SHAPE;
+    if (d->Hq > kd::ROPE_MAX_H || d->Hk > kd::ROPE_MAX_H || (int64_t)d->B * d->T > INT32_MAX) return KD_ERR_SHAPE;
     const size_t es = es_of(d->dtype);
     size_t qi, ki, qo, ko;
     if (!span(d->q_stride, d->B, d->T, d->Hq, d->d, es, false, &qi) ||

@@ -7,6 +7,8 @@
 namespace kd {
 
 constexpr int ROPE_MAX_D = 256;
+constexpr int ROPE_TOKENS = 8;     // most tokens of a workgroup
+constexpr int ROPE_MAX_H = 32767;  // most heads of q and of k (item numbers are divided by multiplication)
 
 // one of the two tensors a launch rotates; strides over batch, token and head
 // in elements (the last dimension is contiguous)
@@ -23,6 +25,9 @@ struct RopeArgs {
     const double* freqs;    // [rot / 2], radians per position
     int B, T, d, rot, pos64, pos_batched, interleaved, inverse;
     float scale;
+    // the launch's own
+    int per, tokens;                // work items per head, tokens per workgroup
+    unsigned div_row, div_per;      // 2^32 / items per token, / items per head, rounded up
 };
 
 // scale (cos, sin) of the angle pos * freq (its negative for the inverse):

@@ -143,7 +143,7 @@ def test_glr_split_sequence_continues_from_its_state():
 # ---------------------------------------------------------- rotary positions
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-@pytest.mark.parametrize("d,rot", [(128, 128), (128, 64), (64, 36), (32, 2), (256, 256), (80, 80), (7, 6), (64, 48)])
+@pytest.mark.parametrize("d,rot", [(128, 128), (128, 64), (64, 36), (32, 2), (256, 256), (80, 80), (7, 6), (64, 48), (16, 16), (24, 10)])
 def test_rope(d, rot, layout, dtype):
     import delta_rule_recurrent_chunk_amd as kd
     torch = _torch()
@@ -171,6 +171,26 @@ def test_rope(d, rot, layout, dtype):
     assert none is None and torch.equal(a, b)
     c, _ = kd.rope(q[1], None, torch.tensor(pos[1], device="cuda"), freqs, layout=layout)
     assert torch.equal(c, b[1])
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk,d,rot", [(1, 1, 1, 0, 16, 16), (3, 77, 5, 1, 64, 36), (2, 1000, 1, 0, 16, 16),
+                                             (1, 3, 700, 300, 128, 128), (5, 130, 16, 4, 128, 64), (1, 9, 1, 1, 2, 2)])
+def test_rope_sizes(B, T, Hq, Hk, d, rot):
+    """Sizes that fill a workgroup's tokens in different ways, against the reference."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    r = np.random.default_rng(B * T)
+    freqs, _ = kd.rope_frequencies(rot, device="cuda")
+    pos = torch.arange(7, 7 + T, dtype=torch.int32, device="cuda")
+    for layout in ("half", "interleaved"):
+        for dtype in ("bf16", "fp32"):
+            q, qv = dev(r.standard_normal((B, T, Hq, d)), dtype)
+            k, kv = dev(r.standard_normal((B, T, Hk, d)), dtype) if Hk else (None, None)
+            qo, ko = kd.rope(q, k, pos, freqs, layout=layout)
+            for got, x in ((qo, qv), (ko, kv)):
+                if x is not None:
+                    ref, e = R.rope(x, np.broadcast_to(np.arange(7, 7 + T), (B, T)), freqs.cpu().numpy(), layout, 1.0)
+                    check("rope", got, ref, 1.01 * (e + R.unit(dtype) * np.abs(ref)))
 
 
 def test_rope_far_positions_and_gradient_by_differences():
