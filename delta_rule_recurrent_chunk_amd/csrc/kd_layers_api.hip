@@ -27,7 +27,6 @@ hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, void* ws, hipStream
 size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int d, int W, int S);
 hipError_t launch_swa_decode(int bf16, int d, const SwaDecodeArgs& a, hipStream_t st);
 hipError_t launch_swa_store(const SwaStoreArgs& a, int B, hipStream_t st);
-int swa_decode_items(int B, int Hq, int Hkv);
 int swa_decode_splits(int B, int Hq, int Hkv, int seen);
 size_t swa_decode_part_bytes(int B, int Hq, int Hkv, int d, int seen);
 }  // namespace kd

@@ -7,7 +7,8 @@
 
 namespace kd {
 
-constexpr int SWA_DECODE_COUNTERS = 1024;   // arrival counters at the start of the workspace
+constexpr int SWA_DECODE_COUNTERS = 512;    // arrival counters at the start of the workspace
+constexpr int SWA_DECODE_SPLITS = 32;       // most splits of a row's keys
 
 struct SwaDecodeArgs {
     const void *q, *k, *v;          // [B, H, d], batch strides qb, kb, vb (elements)

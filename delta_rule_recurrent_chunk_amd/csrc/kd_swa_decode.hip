@@ -15,219 +15,312 @@
 #include "kd_rope.h"
 #include "kd_swa_decode.h"
 
-#include <type_traits>
 
 namespace kd {
 
 // slot of position s
 __device__ __forceinline__ int64_t cache_slot(int s, int S, int cap) { return s < S ? s : S + (s - S) % (cap - S); }
 
-// sum over the LPR adjacent lanes that share a key, on every one of them
-template <int LPR>
-__device__ __forceinline__ float lanes_sum(float x) {
-#define KD_DPP_ADD(c) x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), c, 0xf, 0xf, false))
-    KD_DPP_ADD(0xB1);                               // quad_perm [1,0,3,2]
-    KD_DPP_ADD(0x4E);                               // quad_perm [2,3,0,1]
-    if constexpr (LPR >= 8) KD_DPP_ADD(0x141);      // row_half_mirror
-    if constexpr (LPR >= 16) KD_DPP_ADD(0x140);     // row_mirror
-    if constexpr (LPR >= 32) x += __shfl_xor(x, 16);
-#undef KD_DPP_ADD
-    return x;
+// a pair of floats to and from the memory that every compute unit sees
+__device__ __forceinline__ void swa_put(float* p, float x, float y) {
+    __hip_atomic_store((unsigned long long*)p, ((unsigned long long)__float_as_uint(y) << 32) | __float_as_uint(x),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 swa_get(const float* p) {
+    const unsigned long long v = __hip_atomic_load((const unsigned long long*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__uint_as_float((unsigned)v), __uint_as_float((unsigned)(v >> 32)));
 }
 
-// Workgroup (split, key head, group of GB query heads; b): four waves share the
-// split's keys.  LPR lanes hold one key's row, 16 bytes each, so a wave reads
-// 64 / LPR keys per instruction; every such row group keeps its own running
-// maximum, sum and output, joined at the end over groups, waves and splits.
-template <class E, int D, int GB>
-__global__ __launch_bounds__(256) void kd_swa_decode_kernel(SwaDecodeArgs a)
+// What a query head of one position still needs: keys seen before the new one
+// are numbered 0 .. nv - 1, the sinks 0 .. ns - 1 first, then the window's.
+struct Seen {
+    int ns, nv, first;     // first: slot of the window's first key
+};
+__device__ __forceinline__ Seen swa_seen(int pos, int W, int S, int cap) {
+    const int p0 = max(0, pos - W + 1);
+    Seen s;
+    s.ns = min(S, p0);
+    s.nv = s.ns + pos - p0;
+    s.first = (int)cache_slot(p0, S, cap);
+    return s;
+}
+__device__ __forceinline__ int swa_slot(const Seen& s, int j, int S, int cap) {
+    if (j < s.ns) return j;
+    const int x = s.first + (j - s.ns);
+    // positions below S are slots themselves, the others wrap within cap - S (once: W <= cap - S)
+    return x < cap ? x : x - (cap - S);
+}
+
+// Workgroup (split, key head and block of up to 32 query heads, b): two waves
+// share the split's keys, 32 at a time.  The heads are the columns of the same
+// products that the forward pass makes with queries, St = K Qt and Ot += Vt Pt,
+// so the cache is read once for all heads of a group; each wave streams its
+// own tiles straight to LDS, one tile ahead, with no barrier between.  The
+// matrix units have room to spare here (the step is bound by reading the
+// cache), so in bf16 the queries (turned and scaled in fp32) and the weights
+// go through as a rounded part and its remainder: nothing is lost to bf16 but
+// the output's rounding.
+template <class E, int D>
+__global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
 {
-    constexpr int EPC = 16 / sizeof(E), LPR = D / EPC, KPI = 64 / LPR, U = 4;
-    typedef E Vec __attribute__((ext_vector_type(EPC)));
-    __shared__ float2 cs[D / 2];
-    __shared__ __align__(16) float qs[GB * D];
-    __shared__ __align__(16) float accs[4][GB][D];
-    __shared__ float ms[4][GB], lsum[4][GB];
-    __shared__ int last;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane % LPR, kg = lane / LPR;
-    const int G = a.Hq / a.Hkv, nhb = (G + GB - 1) / GB;
+    typedef SwaT<E> T;
+    typedef typename T::Frag Frag;
+    typedef SwaTile<E, D> TL;
+    constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    constexpr int ST = D * sizeof(E) > 256 ? 1 : 2;              // tiles of a wave in LDS
+    constexpr int NI = 32 * TL::CPR / 64;                        // loads of one K or V tile
+    constexpr bool TWO = sizeof(E) == 2;
+    // K and V tiles of both waves (loads to LDS take destinations in the first 64 KB);
+    // the queries pass through the second tiles' room before those are fetched
+    __shared__ __align__(16) struct {
+        E kv[ST][2][2][32 * D];
+        float qx[ST == 2 ? 4 : 32 * D];
+        float kn[D], vn[D];
+        float2 cs[D / 2];
+        float ms[3][32], ls[3][32], mw[32][SWA_DECODE_SPLITS + 1], wl[32];
+        int last;
+    } sm;
+    auto& kv = sm.kv;
+    auto& cs = sm.cs;
+    float(*const ms)[32] = sm.ms;
+    float(*const ls)[32] = sm.ls;
+    float(*const mw)[SWA_DECODE_SPLITS + 1] = sm.mw;
+    float *const kn = sm.kn, *const vn = sm.vn, *const wl = sm.wl;
+    int& last = sm.last;
+    float* const qs = ST == 2 ? reinterpret_cast<float*>(kv[ST - 1]) : sm.qx;      // [32][D]
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
+    const int G = a.Hq / a.Hkv, nhb = (G + 31) / 32;
     const int sp = blockIdx.x, hk = blockIdx.y / nhb, hb = blockIdx.y % nhb, b = blockIdx.z;
-    const int h0 = hk * G + hb * GB, nh = min(GB, G - hb * GB);
+    const int h0 = hk * G + hb * 32, nh = min(32, G - hb * 32);
     const int pos = a.lens[b];
     E* o = (E*)a.o + ((int64_t)b * a.Hq + h0) * D;
     if (pos < 0) {     // an unused row: nothing is stored, its output is zero
         if (sp == 0)
-            for (int i = tid; i < nh * D; i += 256) o[i] = (E)0.f;
+            for (int i = tid; i < nh * D; i += 128) o[i] = (E)0.f;
         return;
     }
-    // queries (turned, times scale log2 e) and, for the workgroup that stores it, the new key
+    const Seen se = swa_seen(pos, a.W, a.S, a.cap);
+    E* kc = (E*)a.kc + b * a.kcs[0] + hk * a.kcs[2];
+    E* vc = (E*)a.vc + b * a.vcs[0] + hk * a.vcs[2];
+    // this split's tiles of 32 keys; the wave takes every second one
+    const int tiles = (se.nv + 31) / 32, per = (tiles + a.nsplit - 1) / a.nsplit;
+    const int ta = min(sp * per, tiles), tb = min(ta + per, tiles);
+    auto fetch = [&](int t, int st) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int at = i * 64 + lane, r = at / TL::CPR, ch = (at % TL::CPR) ^ TL::swz(r);
+            // (numbers past the last key read it again; they are masked)
+            const int64_t slot = swa_slot(se, min(t * 32 + r, se.nv - 1), a.S, a.cap);
+            const E* ks = kc + slot * a.kcs[1] + ch * TL::EPC;
+            const E* vs = vc + slot * a.vcs[1] + ch * TL::EPC;
+            const uint32_t kd = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)kv[st][w][0] + 1024 * i;
+            const uint32_t vd = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)kv[st][w][1] + 1024 * i;
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\t"
+                         "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, off" ::"s"(kd),
+                         "v"(ks), "s"(vd), "v"(vs)
+                         : "memory", "m0");
+        }
+    };
+    int t = ta + w;
+    if (t < tb) fetch(t, 0);
+
+    // queries (turned, times scale log2 e), and where they are needed the new key and value
     const int n = a.rot / 2;
-    for (int j = tid; j < n; j += 256) cs[j] = rope_cs((double)pos, a.freqs[j], a.rope_scale, 0);
+    for (int j = tid; j < n; j += 128) cs[j] = rope_cs((double)pos, a.freqs[j], a.rope_scale, 0);
     __syncthreads();
-    const E* qrow = (const E*)a.q + b * a.qb + (int64_t)h0 * D;
     auto turned = [&](const E* row, int i) -> float {
         const float x = (float)row[i];
         if (i >= a.rot) return x;
-        const int j = a.interleaved ? i / 2 : i % n;
+        const int j = a.interleaved ? i / 2 : i < n ? i : i - n;
         const bool second = a.interleaved ? (i & 1) : i >= n;
         const float y = (float)row[a.interleaved ? i ^ 1 : second ? i - n : i + n];
         return second ? fmaf(x, cs[j].x, y * cs[j].y) : fmaf(x, cs[j].x, -y * cs[j].y);
     };
-    for (int i = tid; i < GB * D; i += 256) qs[i] = i < nh * D ? turned(qrow + i / D * D, i % D) * a.c : 0.f;
-    const E* krow = (const E*)a.k + b * a.kb + (int64_t)hk * D;
-    const E* vrow = (const E*)a.v + b * a.vb + (int64_t)hk * D;
-    E* kc = (E*)a.kc + b * a.kcs[0] + hk * a.kcs[2];
-    E* vc = (E*)a.vc + b * a.vcs[0] + hk * a.vcs[2];
-    if (sp == 0 && hb == 0 && tid < D) {
+    const E* qrow = (const E*)a.q + b * a.qb + (int64_t)h0 * D;
+    for (int i = tid; i < nh * D; i += 128) qs[i] = turned(qrow + i / D * D, i % D) * a.c;
+    if (sp == 0) {
+        const E* krow = (const E*)a.k + b * a.kb + (int64_t)hk * D;
+        const E* vrow = (const E*)a.v + b * a.vb + (int64_t)hk * D;
         const int64_t slot = cache_slot(pos, a.S, a.cap);
-        kc[slot * a.kcs[1] + tid] = (E)turned(krow, tid);
-        vc[slot * a.vcs[1] + tid] = vrow[tid];
-    }
-    __syncthreads();
-    float q[GB][EPC], acc[GB][EPC], m[GB], l[GB];
-#pragma unroll
-    for (int h = 0; h < GB; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) {
-            q[h][e] = qs[h * D + c * EPC + e];
-            acc[h][e] = 0.f;
-        }
-    }
-    // keys seen before the new one: the sinks 0 .. ns - 1, then p0 .. pos - 1
-    const int p0 = max(0, pos - a.W + 1), ns = min(a.S, p0), nv = ns + pos - p0;
-    const int per = (((nv + a.nsplit - 1) / a.nsplit) + 4 * KPI - 1) / (4 * KPI) * (4 * KPI);
-    const int jlo = min((int64_t)sp * per, (int64_t)nv), jhi = min(jlo + per, nv);
-    auto step = [&](const Vec* kv, const Vec* vv, const bool* ok, auto un) {
-        constexpr int N = decltype(un)::value;
-#pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            float s[N], mx = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                float d = 0.f;
-#pragma unroll
-                for (int e = 0; e < EPC; ++e) d = fmaf((float)kv[u][e], q[h][e], d);
-                d = lanes_sum<LPR>(d);
-                s[u] = ok[u] ? d : -INFINITY;
-                mx = fmaxf(mx, s[u]);
-            }
-            const float mn = fmaxf(m[h], mx), mu = mn == -INFINITY ? 0.f : mn;
-            const float al = __builtin_amdgcn_exp2f(m[h] - mu);
-            m[h] = mn;
-            l[h] *= al;
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) acc[h][e] *= al;
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const float p = __builtin_amdgcn_exp2f(s[u] - mu);
-                l[h] += p;
-#pragma unroll
-                for (int e = 0; e < EPC; ++e) acc[h][e] = fmaf(p, (float)vv[u][e], acc[h][e]);
-            }
-        }
-    };
-    for (int j0 = jlo + w * KPI; j0 < jhi; j0 += 4 * KPI * U) {
-        Vec kv[U], vv[U];
-        bool ok[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u * 4 * KPI + kg;
-            ok[u] = j < jhi;
-            if (ok[u]) {
-                const int64_t slot = cache_slot(j < ns ? j : p0 + (j - ns), a.S, a.cap);
-                kv[u] = *reinterpret_cast<const Vec*>(kc + slot * a.kcs[1] + c * EPC);
-                vv[u] = *reinterpret_cast<const Vec*>(vc + slot * a.vcs[1] + c * EPC);
-            } else {
-#pragma unroll
-                for (int e = 0; e < EPC; ++e) kv[u][e] = vv[u][e] = (E)0.f;
-            }
-        }
-        step(kv, vv, ok, std::integral_constant<int, U>());
-    }
-    if (sp == 0 && w == 0) {     // the new token, on the wave's first row group
-        Vec kv, vv;
-        const bool ok = kg == 0;
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) {
-            kv[e] = (E)turned(krow, c * EPC + e);
-            vv[e] = ok ? vrow[c * EPC + e] : (E)0.f;
-        }
-        step(&kv, &vv, &ok, std::integral_constant<int, 1>());
-    }
-    // row groups of the wave
-#pragma unroll
-    for (int h = 0; h < GB; ++h) {
-#pragma unroll
-        for (int x = LPR; x < 64; x *= 2) {
-            const float mo = __shfl_xor(m[h], x), mn = fmaxf(m[h], mo), mu = mn == -INFINITY ? 0.f : mn;
-            const float f = __builtin_amdgcn_exp2f(m[h] - mu), fo = __builtin_amdgcn_exp2f(mo - mu);
-            l[h] = l[h] * f + __shfl_xor(l[h], x) * fo;
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) acc[h][e] = acc[h][e] * f + __shfl_xor(acc[h][e], x) * fo;
-            m[h] = mn;
-        }
-        if (kg == 0) {
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) accs[w][h][c * EPC + e] = acc[h][e];
-            if (c == 0) {
-                ms[w][h] = m[h];
-                lsum[w][h] = l[h];
+        for (int i = tid; i < D; i += 128) {
+            const E kx = (E)turned(krow, i), vx = vrow[i];
+            kn[i] = (float)kx;
+            vn[i] = (float)vx;
+            if (hb == 0) {
+                kc[slot * a.kcs[1] + i] = kx;
+                vc[slot * a.vcs[1] + i] = vx;
             }
         }
     }
     __syncthreads();
-    // waves, then splits: the last workgroup of (b, heads) to arrive joins them
-    const int item = (b * (int)gridDim.y + blockIdx.y);
-    float* part = a.part + ((int64_t)item * a.nsplit + sp) * GB * (D + 2);
-    for (int i = tid; i < nh * D; i += 256) {
-        const int h = i / D, e = i % D;
-        const float mn = fmaxf(fmaxf(ms[0][h], ms[1][h]), fmaxf(ms[2][h], ms[3][h]));
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        float A = 0.f, L = 0.f;
+    Frag q[NK], ql[TWO ? NK : 1];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float f = __builtin_amdgcn_exp2f(ms[x][h] - mu);
-            A = fmaf(accs[x][h][e], f, A);
-            L = fmaf(lsum[x][h], f, L);
+    for (int ks = 0; ks < NK; ++ks) {
+        const float* src = qs + (lane & 31) * D + (2 * ks + g) * TL::EPC;
+#pragma unroll
+        for (int e = 0; e < TL::EPC; ++e) {
+            const float x = (lane & 31) < nh ? src[e] : 0.f;
+            q[ks][e] = (E)x;
+            if (TWO) ql[TWO ? ks : 0][e] = (E)(x - (float)q[ks][e]);
         }
+    }
+    // the new token's score (four lanes a head)
+    if (sp == 0) {
+        const int h = tid / 4;
+        float s = 0.f;
+        if (h < nh)
+            for (int i = tid % 4; i < D; i += 4) s = fmaf(qs[h * D + i], kn[i], s);
+        s += __shfl_xor(s, 1);
+        s += __shfl_xor(s, 2);
+        if (tid % 4 == 0) {
+            ms[2][h] = h < nh ? s : -INFINITY;
+            ls[2][h] = 1.f;
+        }
+    }
+    __syncthreads();
+
+    floatx16 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    if (ST == 2 && t + 2 < tb) fetch(t + 2, 1);
+    for (int st = 0; t < tb; t += 2, st ^= ST - 1) {
+        if (ST == 2 && t + 2 < tb) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NI) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const E* kl = kv[st][w][0];
+        const E* vl = kv[st][w][1];
+        floatx16 sc;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sc[r] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+            const Frag kf = swa_ld_row<E, D>(kl, lane & 31, ks, g);
+            sc = T::mma(kf, q[ks], sc);
+            if (TWO) sc = T::mma(kf, ql[TWO ? ks : 0], sc);
+        }
+        if (t * 32 + 32 > se.nv) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (t * 32 + 8 * (r / 4) + 4 * g + r % 4 >= se.nv) sc[r] = -INFINITY;
+        }
+        float mx = sc[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[r]);
+        mx = fmaxf(mx, swa_swap(mx));
+        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+        const float al = __builtin_amdgcn_exp2f(m - mu);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) acc[i] *= al;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            sc[r] = __builtin_amdgcn_exp2f(sc[r] - mu);
+            l += sc[r];
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const Frag p = T::pack(sc, j), pr = T::rest(sc, j, p);
+#pragma unroll
+            for (int i = 0; i < ND; ++i) {
+                const Frag vf = T::template ld_col<D>(vl, (32 / NP) * j, 32 * i, lane);
+                acc[i] = T::mma(vf, p, acc[i]);
+                if (TWO) acc[i] = T::mma(vf, pr, acc[i]);
+            }
+        }
+        if (t + 2 * ST < tb) fetch(t + 2 * ST, st);
+    }
+    l += swa_swap(l);
+
+    // the two waves' and the new token's results; head h of wave x at part[x][h]
+    __syncthreads();
+    float* const accs = reinterpret_cast<float*>(kv);      // [2][32][D]
+    if ((lane & 31) < nh) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<floatx4*>(accs + (w * 32 + (lane & 31)) * D + 32 * i + 8 * j + 4 * g) =
+                    floatx4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+        if (g == 0) {
+            ms[w][lane & 31] = m;
+            ls[w][lane & 31] = l;
+        }
+    }
+    __syncthreads();
+    const int item = b * (int)gridDim.y + blockIdx.y;
+    const int64_t pstep = (int64_t)32 * (D + 2);
+    float* part = a.part + ((int64_t)item * a.nsplit + sp) * pstep;
+    for (int i = tid; i < nh * D / 2; i += 128) {
+        const int h = 2 * i / D, e = 2 * i % D;
+        const float m2 = sp == 0 ? ms[2][h] : -INFINITY;
+        const float mn = fmaxf(fmaxf(ms[0][h], ms[1][h]), m2), mu = mn == -INFINITY ? 0.f : mn;
+        const float f0 = __builtin_amdgcn_exp2f(ms[0][h] - mu), f1 = __builtin_amdgcn_exp2f(ms[1][h] - mu);
+        const float f2 = __builtin_amdgcn_exp2f(m2 - mu);
+        float x[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            x[y] = accs[h * D + e + y] * f0 + accs[(32 + h) * D + e + y] * f1;
+            if (sp == 0) x[y] = fmaf(vn[e + y], f2, x[y]);
+        }
+        const float L = ls[0][h] * f0 + ls[1][h] * f1 + f2;
         if (a.nsplit == 1) {
-            o[i] = (E)(A / L);
+            o[2 * i] = (E)(x[0] / L);
+            o[2 * i + 1] = (E)(x[1] / L);
             continue;
         }
         // stores that reach the memory every compute unit sees
-        __hip_atomic_store(part + i, A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (e == 0) {
-            __hip_atomic_store(part + GB * D + 2 * h, mn, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(part + GB * D + 2 * h + 1, L, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
+        swa_put(part + 2 * i, x[0], x[1]);
+        if (e == 0) swa_put(part + 32 * D + 2 * h, mn, L);
     }
     if (a.nsplit == 1) return;
+    // the last workgroup of (b, heads) to arrive joins the splits
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __builtin_amdgcn_s_waitcnt(0);       // the stores are done before the arrival is counted
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the stores are done before the arrival is counted
     __syncthreads();
     if (tid == 0)
         last = __hip_atomic_fetch_add(a.count + item, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.nsplit - 1;
     __syncthreads();
     if (!last) return;
     if (tid == 0) __hip_atomic_store(a.count + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
-    const float* pb = a.part + (int64_t)item * a.nsplit * GB * (D + 2);
-    for (int i = tid; i < nh * D; i += 256) {
-        const int h = i / D;
-        float mn = -INFINITY, A = 0.f, L = 0.f;
-        for (int x = 0; x < a.nsplit; ++x)
-            mn = fmaxf(mn, __hip_atomic_load(pb + (int64_t)x * GB * (D + 2) + GB * D + 2 * h, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT));
+    const float* pb = a.part + (int64_t)item * a.nsplit * pstep;
+    for (int i = tid; i < nh * a.nsplit; i += 128) {
+        const int h = i % nh, x = i / nh;
+        const float2 v = swa_get(pb + x * pstep + 32 * D + 2 * h);
+        mw[h][x] = v.x;
+        accs[h * SWA_DECODE_SPLITS + x] = v.y;
+    }
+    __syncthreads();
+    if (tid < nh) {      // weight of every split
+        float mn = -INFINITY, L = 0.f;
+        for (int x = 0; x < a.nsplit; ++x) mn = fmaxf(mn, mw[tid][x]);
         const float mu = mn == -INFINITY ? 0.f : mn;
         for (int x = 0; x < a.nsplit; ++x) {
-            const float* px = pb + (int64_t)x * GB * (D + 2);
-            const float f = __builtin_amdgcn_exp2f(
-                __hip_atomic_load(px + GB * D + 2 * h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - mu);
-            A = fmaf(__hip_atomic_load(px + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), f, A);
-            L = fmaf(__hip_atomic_load(px + GB * D + 2 * h + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), f, L);
+            const float f = __builtin_amdgcn_exp2f(mw[tid][x] - mu);
+            mw[tid][x] = f;
+            L = fmaf(accs[tid * SWA_DECODE_SPLITS + x], f, L);
         }
-        o[i] = (E)(A / L);
+        wl[tid] = 1.f / L;
+    }
+    __syncthreads();
+    for (int i = tid; i < nh * D / 2; i += 128) {
+        const int h = 2 * i / D;
+        float x0 = 0.f, x1 = 0.f;
+        for (int x = 0; x < a.nsplit; x += 8) {
+            float2 v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) v[y] = swa_get(pb + min(x + y, a.nsplit - 1) * pstep + 2 * i);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float f = x + y < a.nsplit ? mw[h][x + y] : 0.f;
+                x0 = fmaf(v[y].x, f, x0);
+                x1 = fmaf(v[y].y, f, x1);
+            }
+        }
+        o[2 * i] = (E)(x0 * wl[h]);
+        o[2 * i + 1] = (E)(x1 * wl[h]);
     }
 }
 
@@ -252,41 +345,34 @@ __global__ __launch_bounds__(256) void kd_swa_store_kernel(SwaStoreArgs a)
     *reinterpret_cast<V*>(vd) = *reinterpret_cast<const V*>(vs);
 }
 
-// heads of a group that one workgroup takes
-static int heads_per_block(int G) { return G >= 4 ? 4 : G == 3 ? 4 : G; }
+// Work items before splitting: one per sequence, key head and block of 32 of
+// its query heads.
+static int swa_decode_items(int B, int Hq, int Hkv) { return B * Hkv * ((Hq / Hkv + 31) / 32); }
 
-int swa_decode_items(int B, int Hq, int Hkv) {
-    const int G = Hq / Hkv, gb = heads_per_block(G);
-    return B * Hkv * ((G + gb - 1) / gb);
-}
-
-// Splits of a row's keys: enough workgroups to fill the chip's 256 compute
-// units about four times over, none below 64 keys.  Rows are split only where
-// there are fewer than SWA_DECODE_COUNTERS items, so that many counters serve
-// every call.
+// Splits of a row's keys: two workgroups for each of the chip's 256 compute
+// units (all of them resident: 64 KB of LDS each), none below 64 keys.  Rows
+// are split only where there are fewer than SWA_DECODE_COUNTERS items, so that
+// many counters serve every call.
 int swa_decode_splits(int B, int Hq, int Hkv, int seen) {
     const int items = swa_decode_items(B, Hq, Hkv);
-    int n = (SWA_DECODE_COUNTERS + items - 1) / items;
+    int n = SWA_DECODE_COUNTERS / items;
     const int most = (seen + 63) / 64;
     n = n < most ? n : most;
-    n = n < 32 ? n : 32;
+    n = n < SWA_DECODE_SPLITS ? n : SWA_DECODE_SPLITS;
     return n < 1 ? 1 : n;
 }
 
 // The splits' partial results (none where a row's keys are not split).
 size_t swa_decode_part_bytes(int B, int Hq, int Hkv, int d, int seen) {
-    const int gb = heads_per_block(Hq / Hkv), n = swa_decode_splits(B, Hq, Hkv, seen);
-    return n == 1 ? 0 : (size_t)swa_decode_items(B, Hq, Hkv) * n * gb * (d + 2) * 4;
+    const int n = swa_decode_splits(B, Hq, Hkv, seen);
+    return n == 1 ? 0 : (size_t)swa_decode_items(B, Hq, Hkv) * n * 32 * (d + 2) * 4;
 }
 
 template <class E, int D>
 static hipError_t swa_decode(const SwaDecodeArgs& a, hipStream_t st)
 {
-    const int G = a.Hq / a.Hkv, gb = heads_per_block(G);
-    const dim3 grid(a.nsplit, a.Hkv * ((G + gb - 1) / gb), a.B);
-    if (gb == 1) kd_swa_decode_kernel<E, D, 1><<<grid, 256, 0, st>>>(a);
-    else if (gb == 2) kd_swa_decode_kernel<E, D, 2><<<grid, 256, 0, st>>>(a);
-    else kd_swa_decode_kernel<E, D, 4><<<grid, 256, 0, st>>>(a);
+    const dim3 grid(a.nsplit, a.Hkv * ((a.Hq / a.Hkv + 31) / 32), a.B);
+    kd_swa_decode_kernel<E, D><<<grid, 128, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -366,7 +366,8 @@ class Cache:
 
 DEC = [  # Hq, Hkv, d, window, sinks, cap
     (1, 1, 32, 1, 0, 1), (4, 4, 64, 5, 2, 7), (8, 2, 128, 64, 4, 68), (6, 2, 64, 100, 0, 131), (16, 1, 128, 33, 64, 97),
-    (10, 2, 32, 300, 1, 400), (4, 1, 128, 2048, 4, 2052)]
+    (10, 2, 32, 300, 1, 400), (4, 1, 128, 2048, 4, 2052), (40, 1, 64, 70, 3, 90), (66, 2, 128, 40, 4, 44),
+    (2, 2, 128, 500, 30, 700)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
