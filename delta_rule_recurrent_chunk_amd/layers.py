@@ -78,9 +78,23 @@ def declare(L):
     L.kron_delta_swa_cache_store.argtypes = [P(KdSwaCacheDesc), _i32, vp, vp, P(_i64), P(_i64), vp, vp, vp, vp]
 
 
-def _pkg():
+_torch = None
+_lib = None
+_done = None
+
+
+def _load():
+    """torch and the library, imported on the first call."""
+    global _torch, _lib, _done
+    import torch
+
     import delta_rule_recurrent_chunk_amd as kd
-    return kd
+    _lib, _done, _torch = kd.lib(), kd._done, torch
+    return torch, _lib
+
+
+def _ready():
+    return (_torch, _lib) if _torch is not None else _load()
 
 
 def _ptr(t):
@@ -89,14 +103,19 @@ def _ptr(t):
 
 def _call(what, dev, fn, *args):
     """Runs a library call on the current stream of the tensors' device."""
-    import torch
-    st = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        r = fn(*args, st)
+    cuda = _torch.cuda
+    i = dev.index
+    if cuda.current_device() == i:
+        r = fn(*args, _stream(i))
     else:
-        with torch.cuda.device(dev):
-            r = fn(*args, st)
-    _pkg()._done(r, what, dev)
+        with cuda.device(i):
+            r = fn(*args, _stream(i))
+    _done(r, what, dev)
+
+
+def _stream(i):
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)      # (a tenth of the public call's time)
+    return raw(i) if raw is not None else _torch.cuda.current_stream(i).cuda_stream
 
 
 def _same_device(dev, **tensors):
@@ -112,17 +131,16 @@ def _need_cuda(t, name):
 
 
 def _check(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
 def _code(dt):
-    import torch
-    if dt == torch.bfloat16:
+    if dt == _torch.bfloat16:
         return 1
-    if dt == torch.float32:
+    if dt == _torch.float32:
         return 0
     raise TypeError("tensors must be bfloat16 or float32, got %s" % dt)
 
@@ -137,37 +155,35 @@ def _flat(t):
 
 def _workspace(workspace, need, dev):
     """The caller's workspace, or a new one when there is none."""
-    import torch
     if need == 0 and workspace is None:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous and on %s" % dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
 # ------------------------------------------------- gated linear recurrence
 def _glr(x, f, i):
     dev = _need_cuda(x, "x")
-    _code(x.dtype)
-    _check("f", f, x.shape, x.dtype)
-    if i is not None:
-        _check("i", i, x.shape, x.dtype)
-    _same_device(dev, f=f, i=i)
+    for name, t in (("f", f), ("i", i)):
+        if t is not None:
+            _check(name, t, x.shape, x.dtype)
+            if t.device != dev:
+                raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
     return dev, _flat(x), _flat(f), _flat(i)
 
 
 def glr_workspace_bytes(B, T, D, dtype_code) -> int:
-    return int(_pkg().lib().kron_delta_glr_workspace_bytes(ctypes.byref(KdGlrDesc(B, T, D, dtype_code))))
+    return int(_ready()[1].kron_delta_glr_workspace_bytes(ctypes.byref(KdGlrDesc(B, T, D, dtype_code))))
 
 
 def glr_fwd(x, f, i=None, h0=None, *, save_states=False, workspace=None):
     """h_t = f_t h_{t-1} + i_t x_t over x, f, i [B, T, D] (i None: 1) from h0
     [B, D] float32 (None: 0).  Returns (h, hT), with save_states also the
     states that glr_bwd starts from."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
     dev, x, f, i = _glr(x, f, i)
@@ -189,8 +205,7 @@ def glr_fwd(x, f, i=None, h0=None, *, save_states=False, workspace=None):
 def glr_bwd(x, f, i, hs, dh, dhT=None, *, workspace=None):
     """Gradients of <dh, h> + <dhT, hT>: a dict with dx, df, di (None without
     i) and dh0 [B, D] float32."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
     dev, x, f, i = _glr(x, f, i)
@@ -214,21 +229,19 @@ def glr_bwd(x, f, i, hs, dh, dhT=None, *, workspace=None):
 def glr_step(x, f, i, h, *, h_out=None):
     """One token: x, f, i [B, D], the state h [B, D] float32.  Returns y in
     x's dtype; the new state goes to h_out, or into h itself when it is None."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
     dev, x, f, i = _glr(x, f, i)
     out = h if h_out is None else h_out
     for name, t in (("h", h), ("h_out", out)):
         _check(name, t, x.shape, torch.float32)
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    _same_device(dev, h=h, h_out=out)
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError("%s must be contiguous and on %s" % (name, dev))
     y = torch.empty_like(x)
     desc = KdGlrDesc(x.shape[0], 1, x.shape[1], _code(x.dtype))
-    _call("kron_delta_glr_step", dev, L.kron_delta_glr_step, ctypes.byref(desc), _ptr(x), _ptr(f), _ptr(i), _ptr(h),
-          _ptr(y), _ptr(out))
+    _call("kron_delta_glr_step", dev, L.kron_delta_glr_step, ctypes.byref(desc), x.data_ptr(), f.data_ptr(), _ptr(i),
+          h.data_ptr(), y.data_ptr(), out.data_ptr())
     return y
 
 
@@ -277,10 +290,10 @@ def _layout(layout):
 
 
 def _freqs(freqs, dev):
-    import torch
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.numel() < 1:
+    if freqs.dtype != _torch.float64 or freqs.dim() != 1 or freqs.numel() < 1:
         raise TypeError("freqs must be a float64 vector (rope_frequencies)")
-    _same_device(dev, freqs=freqs)
+    if freqs.device != dev:
+        raise ValueError("freqs is on %s, not on %s" % (freqs.device, dev))
     return freqs.contiguous()
 
 
@@ -289,50 +302,61 @@ def rope(q, k, positions, freqs, *, layout="half", scale=1.0, inverse=False, out
     [T, H, d]; k may be None) at positions [T] or [B, T] (int32 or int64).
     Pairs past len(freqs) stay as they are.  Returns (q, k) rotated: new
     tensors, or those of `out` (which may be the inputs themselves)."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     dev = _need_cuda(q, "q")
-    packed = q.dim() == 3
-    if q.dim() not in (3, 4):
+    nd = q.dim()
+    if nd not in (3, 4):
         raise ValueError("q must be [B, T, H, d] or [T, H, d]")
+    qs = q.shape
+    if nd == 4:
+        B, T, Hq, d = qs
+    else:
+        B, (T, Hq, d) = 1, qs
+    Hk = 0
     if k is not None:
+        ks = k.shape
         if k.dtype != q.dtype:
             raise TypeError("k has dtype %s, q has %s" % (k.dtype, q.dtype))
-        if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+        if len(ks) != nd or ks[:-2] != qs[:-2] or ks[-1] != d:
             raise ValueError("k must be shaped like q but for its heads")
-    oq, ok = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=dev),
-                                          None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev))
-    if (ok is None) != (k is None):
-        raise ValueError("out must hold a tensor for each of q and k")
-    _check("out[0]", oq, q.shape, q.dtype)
-    if k is not None:
-        _check("out[1]", ok, k.shape, k.dtype)
-    _same_device(dev, k=k, positions=positions, out_q=oq, out_k=ok)
-
-    def four(t):
-        return None if t is None else t[None] if packed else t
-
-    def inner(t):      # a contiguous last dimension
-        return t if t is None or t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous()
-
-    q4, k4, oq4, ok4 = four(inner(q)), four(inner(k)), four(oq), four(ok)
-    for t in (oq4, ok4):
-        if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("out must have a contiguous last dimension")
-    B, T, Hq, d = q4.shape
-    if positions.dtype not in (torch.int32, torch.int64):
+        if k.device != dev:
+            raise ValueError("k is on %s, not on %s" % (k.device, dev))
+        Hk = ks[-2]
+        if k.stride(-1) != 1 and d > 1:
+            k = k.contiguous()
+    if q.stride(-1) != 1 and d > 1:
+        q = q.contiguous()
+    if out is None:
+        oq = torch.empty(qs, dtype=q.dtype, device=dev)
+        ok = None if k is None else torch.empty(ks, dtype=q.dtype, device=dev)
+    else:
+        oq, ok = out
+        if (ok is None) != (k is None):
+            raise ValueError("out must hold a tensor for each of q and k")
+        for name, o, x in (("out[0]", oq, q), ("out[1]", ok, k)):
+            if x is None:
+                continue
+            _check(name, o, x.shape, x.dtype)
+            if o.device != dev:
+                raise ValueError("%s is on %s, not on %s" % (name, o.device, dev))
+            if o.stride(-1) != 1 and d > 1:
+                raise ValueError("out must have a contiguous last dimension")
+    pdt, pdim = positions.dtype, positions.dim()
+    if pdt != torch.int64 and pdt != torch.int32:
         raise TypeError("positions must be int32 or int64")
-    if tuple(positions.shape) not in ((T,), (B, T)) or (packed and positions.dim() != 1):
+    if not (positions.shape == (T,) or (nd == 4 and positions.shape == (B, T))):
         raise ValueError("positions must be [T] or [B, T]")
-    positions = positions.contiguous()
-    freqs = _freqs(freqs, dev)
-    z = (0, 0, 0)
-    desc = KdRopeDesc(B, T, Hq, 0 if k is None else k4.shape[2], d, 2 * freqs.numel(), _layout(layout), _code(q.dtype),
-                      int(positions.dtype == torch.int64), int(positions.dim() == 2), int(bool(inverse)), float(scale),
-                      _s3(*q4.stride()[:3]), _s3(*(z if k is None else k4.stride()[:3])), _s3(*oq4.stride()[:3]),
-                      _s3(*(z if k is None else ok4.stride()[:3])))
-    _call("kron_delta_rope", dev, L.kron_delta_rope, ctypes.byref(desc), _ptr(q4), _ptr(k4), _ptr(positions),
-          _ptr(freqs), _ptr(oq4), _ptr(ok4))
+    if positions.device != dev:
+        raise ValueError("positions is on %s, not on %s" % (positions.device, dev))
+    positions, freqs = positions.contiguous(), _freqs(freqs, dev)
+
+    def strides(t):
+        return (0, 0, 0) if t is None else t.stride()[:3] if nd == 4 else (0,) + t.stride()[:2]
+
+    desc = KdRopeDesc(B, T, Hq, Hk, d, 2 * freqs.numel(), _layout(layout), _code(q.dtype), pdt == torch.int64,
+                      pdim == 2, bool(inverse), scale, strides(q), strides(k), strides(oq), strides(ok))
+    _call("kron_delta_rope", dev, L.kron_delta_rope, ctypes.byref(desc), q.data_ptr(), _ptr(k), positions.data_ptr(),
+          freqs.data_ptr(), oq.data_ptr(), _ptr(ok))
     return oq, ok
 
 
@@ -352,7 +376,7 @@ def _rows(t):
 
 
 def _swa(q, k, v, window, sinks, scale, cu):
-    import torch
+    torch = _torch
     dev = _need_cuda(q, "q")
     dims = 3 if cu is not None else 4
     if q.dim() != dims or k.dim() != dims or v.dim() != dims:
@@ -383,8 +407,7 @@ def swa_fwd(q, k, v, window, sinks=0, *, scale=None, cu_seqlens=None, return_lse
     [B, Tq, Hq, d], k, v [B, Tk, Hkv, d], the queries at the end of the keys; or
     packed [T, H, d] with cu_seqlens int32 [N + 1].  scale None: 1 / sqrt(d).
     Returns o, with return_lse (o, lse [B, Hq, Tq] or [Hq, T] float32)."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     dev, desc, q, k, v, cu = _swa(q, k, v, window, sinks, scale, cu_seqlens)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
@@ -404,8 +427,7 @@ def swa_fwd(q, k, v, window, sinks=0, *, scale=None, cu_seqlens=None, return_lse
 
 def swa_bwd(q, k, v, o, lse, dO, window, sinks=0, *, scale=None, cu_seqlens=None, workspace=None):
     """Gradients of <dO, o> from swa_fwd's o and lse: a dict with dq, dk, dv."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     dev, desc, q, k, v, cu = _swa(q, k, v, window, sinks, scale, cu_seqlens)
     _check("o", o, q.shape, q.dtype)
     _check("dO", dO, q.shape, q.dtype)
@@ -428,19 +450,18 @@ def _cache_desc(q_heads, k_cache, v_cache, window, sinks, scale=1.0, rot=0, layo
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("%s must have a contiguous last dimension" % name)
     B, cap, Hkv, d = k_cache.shape
-    return KdSwaCacheDesc(B, q_heads, Hkv, d, cap, _code(k_cache.dtype), int(window), int(sinks), float(scale), rot,
-                          layout, float(rope_scale), _s3(*k_cache.stride()[:3]), _s3(*v_cache.stride()[:3]))
+    return KdSwaCacheDesc(B, q_heads, Hkv, d, cap, _code(k_cache.dtype), int(window), int(sinks), scale,
+                          rot, layout, rope_scale, k_cache.stride()[:3], v_cache.stride()[:3])
 
 
 def swa_decode_workspace(q, k_cache):
     """A workspace for swa_decode calls with these shapes and any window (zero
     filled; every call leaves it ready for the next).  One per stream."""
-    import torch
-    need = 0
+    torch, L = _ready()
     cap = k_cache.shape[1]
     # the splits grow with the number of visible keys: the widest window needs most
     desc = _cache_desc(q.shape[1], k_cache, k_cache, cap, 0)
-    need = int(_pkg().lib().kron_delta_swa_decode_workspace_bytes(ctypes.byref(desc)))
+    need = int(L.kron_delta_swa_decode_workspace_bytes(ctypes.byref(desc)))
     if need == 0:
         raise ValueError("unsupported cache for q [B, Hq, d]: %s, %s" % (list(q.shape), list(k_cache.shape)))
     return torch.zeros(need, dtype=torch.uint8, device=k_cache.device)
@@ -453,46 +474,49 @@ def swa_decode(q, k, v, k_cache, v_cache, lens, window, sinks=0, *, scale=None, 
     and receive the new one; lens is not changed.  freqs: turn q and k to their
     position first.  Rows with a negative length are skipped (their o is 0).
     Returns o [B, Hq, d]."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     dev = _need_cuda(q, "q")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [B, Hq, d], k and v [B, Hkv, d]")
-    B, Hkv, d = k_cache.shape[0], k_cache.shape[2], k_cache.shape[3]
-    _check("q", q, (B, q.shape[1], d), k_cache.dtype)
-    _check("k", k, (B, Hkv, d), k_cache.dtype)
-    _check("v", v, (B, Hkv, d), k_cache.dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [B, cap, Hkv, d] of one dtype")
+    (B, _, Hkv, d), dt, Hq = k_cache.shape, k_cache.dtype, q.shape[1]
+    _check("q", q, (B, Hq, d), dt)
+    _check("k", k, (B, Hkv, d), dt)
+    _check("v", v, (B, Hkv, d), dt)
     _check("lens", lens, (B,), torch.int32)
-    _same_device(dev, k=k, v=v, k_cache=k_cache, v_cache=v_cache, lens=lens, workspace=workspace)
+    for name, t in (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("lens", lens)):
+        if t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
 
     def heads(t):      # heads and elements contiguous, any batch stride
-        return t if t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]) and t.stride(0) >= 0 \
-            else t.contiguous()
+        b, h, e = t.stride()
+        return t if e == 1 and (h == d or t.shape[1] == 1) else t.contiguous()
 
     q, k, v, lens = heads(q), heads(k), heads(v), lens.contiguous()
     rot = 0
     if freqs is not None:
         freqs = _freqs(freqs, dev)
         rot = 2 * freqs.numel()
-    desc = _cache_desc(q.shape[1], k_cache, v_cache, window, sinks, 1.0 / math.sqrt(d) if scale is None else scale,
-                       rot, _layout(layout), rope_scale)
+    desc = _cache_desc(Hq, k_cache, v_cache, window, sinks, 1.0 / math.sqrt(d) if scale is None else scale, rot,
+                       _layout(layout), rope_scale)
     if workspace is None:
         need = int(L.kron_delta_swa_decode_workspace_bytes(ctypes.byref(desc)))
         workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    o = torch.empty((B, q.shape[1], d), dtype=q.dtype, device=dev)
-    _call("kron_delta_swa_decode", dev, L.kron_delta_swa_decode, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
-          _s3(q.stride(0), k.stride(0), v.stride(0)), _ptr(k_cache), _ptr(v_cache), _ptr(lens), _ptr(freqs), _ptr(o),
-          _ptr(workspace), workspace.numel() * workspace.element_size())
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    o = torch.empty((B, Hq, d), dtype=dt, device=dev)
+    _call("kron_delta_swa_decode", dev, L.kron_delta_swa_decode, ctypes.byref(desc), q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), _s3(q.stride(0), k.stride(0), v.stride(0)), k_cache.data_ptr(), v_cache.data_ptr(),
+          lens.data_ptr(), _ptr(freqs), o.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return o
 
 
 def swa_cache_store(k, v, k_cache, v_cache, window, sinks=0, *, lens=None):
     """A prompt's (turned) keys and values [B, T, Hkv, d] into the caches of
     swa_decode: token t at position t for t < lens[b] (int32 [B]; None: all)."""
-    import torch
-    L = _pkg().lib()
+    torch, L = _ready()
     dev = _need_cuda(k, "k")
     B, _, Hkv, d = k_cache.shape
     if k.dim() != 4:
