@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
         const int p0 = s.past + t, p1 = p0 + BQ - 1;
         if (!(p1 < wk0 || (p0 - wk1 >= a.W && wk0 >= a.S))) {
             const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= t1;   // (rows from t1 on: the sinks' pass)
-#pragma unroll
+#pragma unroll 1
             for (int n = 0; n < NS; ++n)
                 swa_dkv_tile<E, D>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1], 32 * n, k, v, dk, dv, a.c, full, lane,
                                    key, p0 + 32 * n, t1 - t - 32 * n, a.W, a.S);
@@ -389,16 +389,17 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
                            s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
     }
     __syncthreads();
-    float* sum = reinterpret_cast<float*>(sm.q);     // 32 keys by D, dK then dV
+    constexpr int DP = D + 4;                        // (a row's stride: the lanes' rows start in different banks)
+    float* sum = reinterpret_cast<float*>(&sm);      // 32 keys by D, dK then dV
     float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hq + h) * 2 * SWA_MAX_SINKS + k0) * D;
     for (int x = 0; x < 2; ++x) {
         for (int y = 0; y < NW; ++y) {
-            if (w == y) {
+            if (w == y && key < a.S) {
 #pragma unroll
                 for (int i = 0; i < ND; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        floatx4* p = reinterpret_cast<floatx4*>(sum + (lane & 31) * D + 32 * i + 8 * j + 4 * g);
+                        floatx4* p = reinterpret_cast<floatx4*>(sum + (lane & 31) * DP + 32 * i + 8 * j + 4 * g);
                         floatx4 z;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z[e] = x == 0 ? dk[i][4 * j + e] : dv[i][4 * j + e];
@@ -407,23 +408,26 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
             }
             __syncthreads();
         }
-        for (int i = tid; i < 32 * D / 4; i += 64 * NW)
-            if (k0 + i / (D / 4) < a.S)
-                reinterpret_cast<floatx4*>(out + x * SWA_MAX_SINKS * D)[i] = reinterpret_cast<const floatx4*>(sum)[i];
+        for (int i = tid; i < min(32, a.S - k0) * D / 4; i += 64 * NW)
+            reinterpret_cast<floatx4*>(out + x * SWA_MAX_SINKS * D)[i] =
+                *reinterpret_cast<const floatx4*>(sum + i / (D / 4) * DP + i % (D / 4) * 4);
         __syncthreads();
     }
 }
 
 static int64_t swa_slots(bool packed, int N, int T, int R) { return packed ? (int64_t)T / R + N : ((int64_t)T + R - 1) / R; }
 
-// Rows of a chunk of the sinks' pass: sixteen chunks of a sequence as long as
-// all queries together, none below 256 rows.
-static int swa_chunk(int Tq) { return max(256, (Tq / 16 + 127) / 128 * 128); }
+// Rows of a chunk of the sinks' pass: about 256 workgroups over all heads, so
+// that the start of each is paid for, and chunks of 256 to 4096 rows.
+static int swa_chunk(int64_t rows, int Hq, int S) {
+    const int64_t n = rows * Hq * ((S + 31) / 32) / 256;
+    return (int)min((int64_t)4096, max((int64_t)256, (n + 127) / 128 * 128));
+}
 
 // Chunks of the sinks' partial sums; none where every query lies within the
 // window of the first 128 keys.
-static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S) {
-    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, swa_chunk(Tq)) : 0;
+static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S, int chunk) {
+    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, chunk) : 0;
 }
 
 static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * Hq * 8 + 255) & ~(size_t)255; }
@@ -431,7 +435,7 @@ static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * H
 size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int d, int W, int S) {
     const int nb = packed ? 1 : B;
     return swa_rows_bytes(nb, Tq, Hq) +
-           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S) * nb * Hq * 2 * SWA_MAX_SINKS * d * 4;
+           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S, swa_chunk((int64_t)nb * Tq, Hq, S)) * nb * Hq * 2 * SWA_MAX_SINKS * d * 4;
 }
 
 template <class E, int D>
@@ -440,12 +444,12 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     constexpr int BN = sizeof(E) == 2 ? 64 : 32;
     const int64_t nq = swa_slots(a.cu, a.N, a.Tq, 128), nk = swa_slots(a.cu, a.N, a.Tk, 128);
     const int64_t gq = swa_grid(nq * a.Hq * a.B), gk = swa_grid(nk * a.Hkv * a.B);
-    const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S);
+    a.chunk = swa_chunk((int64_t)a.B * a.Tq, a.Hq, a.S);
+    const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S, a.chunk);
     if (gq > INT32_MAX || gk > INT32_MAX || np > INT32_MAX / 2) return hipErrorInvalidValue;
     a.rows = (float2*)ws;
     a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));
     a.pslots = (int)np;
-    a.chunk = swa_chunk(a.Tq);
     if (a.Tq > 0) {
         kd_swa_dq_kernel<E, D, BN><<<(unsigned)gq, 256, 0, st>>>(a, (int)nq);
         const hipError_t e = hipGetLastError();
@@ -458,7 +462,7 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
         if (e != hipSuccess) return e;
     }
     if (nk == 0) return hipSuccess;
-    kd_swa_dkv_kernel<E, D, sizeof(E) * D == 64 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
+    kd_swa_dkv_kernel<E, D, sizeof(E) * D <= 128 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
     return hipGetLastError();
 }
 
