@@ -272,7 +272,7 @@ struct SwaSpans {
 kd_status check_swa(const kd_swa_desc* d, bool packed, SwaSpans* s) {
     if (!d) return KD_ERR_NULL;
     if (!known(d->dtype)) return KD_ERR_DTYPE;
-    if (d->B < 1 || d->Tq < 0 || d->Tk < 0 || d->Tq > (1 << 30) || d->Tk > (1 << 30) || d->Hq < 1 || d->Hkv < 1 ||
+    if (d->B < 1 || d->Tq < 0 || d->Tk < 0 || d->Tq > (1 << 29) || d->Tk > (1 << 29) || d->Hq < 1 || d->Hkv < 1 ||
         d->Hq > 65535 || d->Hq % d->Hkv != 0 || (d->d != 32 && d->d != 64 && d->d != 128) || d->window < 1 ||
         d->sinks < 0 || d->sinks > kd::SWA_MAX_SINKS || !(d->scale > 0.f) || !isfinite(d->scale))
         return KD_ERR_SHAPE;

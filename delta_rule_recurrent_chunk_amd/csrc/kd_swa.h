@@ -191,8 +191,34 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
 }
 
-__device__ __forceinline__ bool swa_visible(int key, int pos, int W, int S) {
-    return (key <= pos) & ((pos - key < W) | (key < S));      // (no branches)
+// Masks of a 32x32 tile whose lane holds one query at position pos and 16 of
+// the keys from k0 on (key0 = k0 + 4 g; register r is key0 + 8 (r / 4) + r % 4):
+// compares of constants with three numbers per lane.
+__device__ __forceinline__ void swa_mask_keys(floatx16& x, int key0, int pos, int W, int S) {
+    const int hi = pos - key0, lo = hi - W;
+    if (key0 - (key0 & 4) >= S) {      // no sinks among the keys (one answer for the wave)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int i = 8 * (r / 4) + r % 4;
+            if (!((i <= hi) & (i > lo))) x[r] = -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int i = 8 * (r / 4) + r % 4;
+            if (!((i <= hi) & ((i > lo) | (i < S - key0)))) x[r] = -INFINITY;
+        }
+    }
+}
+// The same where the lane holds one key and 16 of the queries at positions p0
+// on (p0 with 4 g added), of which the first `left` (less 4 g) count.
+__device__ __forceinline__ void swa_mask_rows(floatx16& x, int key, int p0, int left, int W, int S) {
+    const int lo = key - p0, hi = min(left, key < S ? left : lo + W);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int i = 8 * (r / 4) + r % 4;
+        if (!((i >= lo) & (i < hi))) x[r] = -INFINITY;
+    }
 }
 
 // Tiles of R rows of a matrix (row stride rs elements, `rows` rows) by loads
@@ -234,11 +260,12 @@ struct SwaFetch {
         const int row0 = __builtin_amdgcn_readfirstlane(row);
         const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile + 1024 * w;
         const E* b = base + swa_uniform(ho) + (int64_t)row0 * rs;
+        const int64_t step = (int64_t)STEP * rs;
         if (row0 + R <= rows && !far) {
 #pragma unroll
             for (int i = 0; i < R / STEP; ++i)
                 asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at + i * NT * 16),
-                             "v"(lane[i % NV]), "s"(swa_uniform((int64_t)(b + (int64_t)(i * STEP) * rs)))
+                             "v"(lane[i % NV]), "s"(swa_uniform((int64_t)(b + i * step)))
                              : "memory", "m0");
         } else {
             // the last tile's rows; each lane's address in full

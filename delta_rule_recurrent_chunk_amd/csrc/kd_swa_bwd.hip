@@ -67,6 +67,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     }
     const int64_t li = ((int64_t)b * a.Hq + h) * a.Tq + s.q0 + rc;
     float lse2 = a.lse[li] * LOG2E, dsum = 0.f;
+    if (lse2 == -INFINITY) lse2 = 0.f;      // a row that sees nothing: a masked score has no weight whatever its lse
     asm volatile("" : "+v"(lse2));
     const SwaFetch<E, D, BN, 256> kf((const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2], a.ks[1], s.nk, tid);
     const SwaFetch<E, D, BN, 256> vf((const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2], a.vs[1], s.nk, tid);
@@ -98,32 +99,20 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
 #pragma unroll 1      // (unrolled, the two halves spill)
         for (int n = 0; n < NS; ++n) {
+            // the products of dP start from -delta
             floatx16 sc, dp;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
+            for (int r = 0; r < 16; ++r) sc[r] = 0.f, dp[r] = -delta;
 #pragma unroll
             for (int ks = 0; ks < NK; ++ks) {
                 sc = T::mma(swa_ld_row<E, D>(kl, 32 * n + (lane & 31), ks, g), q[ks], sc);
                 dp = T::mma(swa_ld_row<E, D>(vl, 32 * n + (lane & 31), ks, g), dO[ks], dp);
             }
-            if (!full) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) {
-                        sc[r] = -INFINITY;     // a weight of 0, whatever dP holds there
-                        dp[r] = 0.f;
-                    }
-            }
+            if (!full) swa_mask_keys(sc, k0 + 32 * n + 4 * g, pos, a.W, a.S);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(sc[r], a.c, -lse2));
-                dsum = fmaf(p, dp[r], dsum);
-                sc[r] = p * (dp[r] - delta);
-            }
-            if (!full) {      // a row that sees nothing has lse = -infinity and no weights
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) sc[r] = 0.f;
+                sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], a.c, -lse2)) * dp[r];
+                dsum += sc[r];
             }
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -145,16 +134,17 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     dsum += swa_swap(dsum);
     if (row >= s.nq) return;
     swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
-    // (a row that sees nothing: no weight comes of a masked score whatever its lse)
-    if (g == 0) a.rows[li] = lse2 == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse2, dsum);
+    // the sum of P dP: that of P (dP - delta) and delta (P sums to 1)
+    if (g == 0) a.rows[li] = make_float2(lse2, pos < 0 ? 0.f : delta + dsum);
 }
 
 // One 32-row piece of a query tile against 32 keys held as B operands (the
 // values' either in registers or as rows of an LDS tile): S and dP have the
 // queries as rows, so the weights and their gradients are again the B operands
-// of the next products (dVt += dOt P, dKt += Qt dS).
-template <class E, int D, class VF>
-__device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const float2* rl, int r0,
+// of the next products (dVt += dOt P, dKt += Qt dS).  rl: lse2 of the tile's
+// queries, and RS floats on their -delta.
+template <class E, int D, int RS, class VF>
+__device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const float* rl, int r0,
                                              const typename SwaT<E>::Frag* k, const VF& v,
                                              floatx16* dk, floatx16* dv, float c, bool full, int lane, int key, int p0,
                                              int left, int W, int S)
@@ -162,33 +152,28 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
-    lane += opaque_zero();      // (the tile's LDS addresses are formed anew, not kept across the loop)
+    // (where registers are short the tile's LDS addresses are formed anew, not kept across the loop)
+    if (sizeof(E) * D >= 256) lane += opaque_zero();
     const int g = lane >> 5;
-    floatx16 sc, dp;
+    // lse and -delta of the queries; the products of dP start from -delta
+    floatx16 sc, dp, ls;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) sc[r] = dp[r] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+        const floatx4 le = *reinterpret_cast<const floatx4*>(rl + r0 + 8 * j + 4 * g);
+        const floatx4 de = *reinterpret_cast<const floatx4*>(rl + RS + r0 + 8 * j + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[4 * j + e] = 0.f, ls[4 * j + e] = le[e], dp[4 * j + e] = de[e];
+    }
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) sc = T::mma(swa_ld_row<E, D>(qt, r0 + (lane & 31), ks, g), k[ks], sc);
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) dp = T::mma(swa_ld_row<E, D>(dt, r0 + (lane & 31), ks, g), v(ks, lane), dp);
-    if (!full) {
+    // (rows that see nothing have lse 0 here: a masked score has no weight)
+    if (!full) swa_mask_rows(sc, key, p0 + 4 * g, left - 4 * g, W, S);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int rr = 8 * (r / 4) + 4 * g + r % 4;
-            if (!((rr < left) & swa_visible(key, p0 + rr, W, S))) sc[r] = -INFINITY;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int rr = 8 * (j / 2) + 4 * g + 2 * (j % 2);      // two rows
-        const floatx4 ld = *reinterpret_cast<const floatx4*>(rl + r0 + rr);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 2 * j + e;
-            // (rows past the end and rows that see nothing have lse2 = 0 here: a masked score has weight 0)
-            sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ld[2 * e]));
-            dp[r] = sc[r] * (dp[r] - ld[2 * e + 1]);
-        }
+    for (int r = 0; r < 16; ++r) {
+        sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ls[r]));
+        dp[r] *= sc[r];
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -217,7 +202,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
     __shared__ __align__(16) struct {
         E q[2][BQ * D], dO[2][BQ * D];
         E v[VL ? 128 * D : 8];
-        float2 rows[2][BQ];
+        float rows[2][2][BQ];      // lse2, -delta
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
     const int G = a.Hq / a.Hkv;
@@ -277,7 +262,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
     };
     if (nt > 0) {
         fetch(0);
-        if (tid < BQ) sm.rows[0][tid] = next;
+        if (tid < BQ) sm.rows[0][0][tid] = next.x, sm.rows[0][1][tid] = -next.y;
     }
     int ct = 0;
     for (int i = 0; i < nt; ++i) {
@@ -290,10 +275,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
             const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= t1;   // (rows from t1 on: the sinks' pass)
 #pragma unroll 1
             for (int n = 0; n < NS; ++n)
-                swa_dkv_tile<E, D>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1], 32 * n, k, v, dk, dv, a.c, full, lane,
+                swa_dkv_tile<E, D, BQ>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1][0], 32 * n, k, v, dk, dv, a.c, full, lane,
                                    key, p0 + 32 * n, t1 - t - 32 * n, a.W, a.S);
         }
-        if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][tid] = next;
+        if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][0][tid] = next.x, sm.rows[(i + 1) & 1][1][tid] = -next.y;
     }
     // the sinks' part from the queries beyond the window: all threads add the
     // chunks' partial sums, the lanes that hold the keys take them from LDS
@@ -345,7 +330,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
     constexpr int NK = D / T::KC, ND = D / 32, BQ = 32 * NW;
     __shared__ __align__(16) struct {
         E q[BQ * D], dO[BQ * D];
-        float2 rows[BQ];
+        float rows[2][BQ];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
     const int ng = (a.S + 31) / 32;
@@ -382,10 +367,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
         __syncthreads();
         qf(sm.q, 0, t, w);
         of(sm.dO, 0, t, w);
-        if (tid < BQ) sm.rows[tid] = rb[min(t + tid, s.nq - 1)];
+        if (tid < BQ) {
+            const float2 x = rb[min(t + tid, s.nq - 1)];
+            sm.rows[0][tid] = x.x;
+            sm.rows[1][tid] = -x.y;
+        }
         swa_landed();
         // beyond the window a row sees the sinks alone: window 1 leaves their mask
-        swa_dkv_tile<E, D>(sm.q, sm.dO, sm.rows, 32 * w, k, vf, dk, dv, a.c, all && t + BQ <= tb, lane, key,
+        swa_dkv_tile<E, D, BQ>(sm.q, sm.dO, sm.rows[0], 32 * w, k, vf, dk, dv, a.c, all && t + BQ <= tb, lane, key,
                            s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
     }
     __syncthreads();

@@ -83,10 +83,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
         if (!full) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!swa_visible(k0 + 32 * n + 8 * (r / 4) + 4 * g + r % 4, pos, a.W, a.S)) sc[n][r] = -INFINITY;
+            for (int n = 0; n < NS; ++n) swa_mask_keys(sc[n], k0 + 32 * n + 4 * g, pos, a.W, a.S);
         }
         float mx = sc[0][0];
 #pragma unroll

@@ -493,7 +493,8 @@ KD_API kd_status kron_delta_rope(const kd_rope_desc *desc, const void *q, const 
  *    batch, token and head in elements (multiples of 16 bytes), contiguous
  *    last dimension; o, dO, dq: contiguous [B, Tq, Hq, d]; dk, dv: contiguous
  *    [B, Tk, Hkv, d]; lse: [B, Hq, Tq] fp32.  d in {32, 64, 128}; bf16, or
- *    fp32 (a diagnostic precision).  sinks <= KRON_DELTA_SWA_MAX_SINKS.
+ *    fp32 (a diagnostic precision).  sinks <= KRON_DELTA_SWA_MAX_SINKS; Tq, Tk
+ *    <= 2^29.
  *  * The queries stand at the end of the keys: query t has position
  *    Tk - Tq + t (a later piece of a prompt has Tk > Tq; with Tk < Tq the
  *    first queries see nothing).
