@@ -238,12 +238,12 @@ template <class E, int D, int R, int NT>
 struct SwaFetch {
     typedef SwaTile<E, D> TL;
     static constexpr int STEP = NT / TL::CPR;              // rows per round of the workgroup
-    static constexpr int NV = STEP >= 16 ? 1 : 16 / STEP;  // rounds until the chunk order (of 16 rows) repeats
+    static constexpr int NL = R / STEP;                    // loads of a tile per lane
     static_assert(R % STEP == 0, "whole instructions");
     const E* base;
     int64_t rs;
     int rows, r, ch;
-    uint32_t lane[NV];
+    uint32_t lane[NL];
     bool far;
 
     __device__ __forceinline__ SwaFetch(const E* base_, int64_t rs_, int rows_, int tid)
@@ -252,31 +252,30 @@ struct SwaFetch {
         ch = tid % TL::CPR;
         far = rs > (1 << 22);      // rows too far apart for 32-bit offsets
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            lane[i] = (uint32_t)((r * (int)rs + (ch ^ TL::swz(r + i * STEP)) * TL::EPC) * (int)sizeof(E));
+        for (int i = 0; i < NL; ++i)
+            lane[i] = (uint32_t)(((r + i * STEP) * (int)rs + (ch ^ TL::swz(r + i * STEP)) * TL::EPC) * (int)sizeof(E));
     }
-    // into `tile` of a buffer at byte `at` of LDS, from head offset `ho` (elements)
+    // rows row0 .. into `tile`, from `ho` elements on (a head), as wave w of the workgroup
     __device__ __forceinline__ void operator()(E* tile, int64_t ho, int row, int w) const {
         const int row0 = __builtin_amdgcn_readfirstlane(row);
         const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile + 1024 * w;
         const E* b = base + swa_uniform(ho) + (int64_t)row0 * rs;
-        const int64_t step = (int64_t)STEP * rs;
         if (row0 + R <= rows && !far) {
 #pragma unroll
-            for (int i = 0; i < R / STEP; ++i)
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at + i * NT * 16),
-                             "v"(lane[i % NV]), "s"(swa_uniform((int64_t)(b + i * step)))
-                             : "memory", "m0");
+            for (int i = 0; i < NL; ++i)
+                asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(lane[i]),
+                             "s"(swa_uniform((int64_t)b)), "i"(i * NT * 16)
+                             : "memory", "m0", "scc");
         } else {
             // the last tile's rows; each lane's address in full
             const int last = rows - 1 - row0;
 #pragma unroll
-            for (int i = 0; i < R / STEP; ++i) {
+            for (int i = 0; i < NL; ++i) {
                 const int rr = r + i * STEP;
                 const E* src = b + (int64_t)min(rr, last) * rs + (ch ^ TL::swz(rr)) * TL::EPC;
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at + i * NT * 16),
-                             "v"(src)
-                             : "memory", "m0");
+                asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src),
+                             "i"(i * NT * 16)
+                             : "memory", "m0", "scc");
             }
         }
     }

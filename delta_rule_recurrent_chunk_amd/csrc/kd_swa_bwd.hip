@@ -89,13 +89,11 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
         vf(vt[i & 1], 0, key0(i), w);
     };
     if (nt > 0) fetch(0);
-    for (int i = 0; i < nt; ++i) {
+    auto tile = [&](int i, const E* kl, const E* vl) {
         swa_landed();
         if (i + 1 < nt) fetch(i + 1);
         const int k0 = key0(i);
-        if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) continue;
-        const E* kl = kt[i & 1];
-        const E* vl = vt[i & 1];
+        if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) return;
         const bool full = k0 + BN - 1 <= wp0 && (wp1 - k0 < a.W || k0 + BN <= a.S);
 #pragma unroll 1      // (unrolled, the two halves spill)
         for (int n = 0; n < NS; ++n) {
@@ -130,6 +128,10 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
                 }
             }
         }
+    };
+    for (int i = 0; i < nt; i += 2) {
+        tile(i, kt[0], vt[0]);
+        if (i + 1 < nt) tile(i + 1, kt[1], vt[1]);
     }
     dsum += swa_swap(dsum);
     if (row >= s.nq) return;

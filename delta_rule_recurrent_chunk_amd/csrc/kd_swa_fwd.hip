@@ -60,14 +60,13 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
         vf(vt[i & 1], 0, key0(i), w);
     };
     if (nt > 0) fetch(0);
-    for (int i = 0; i < nt; ++i) {
+    // (one copy of the loop's body per buffer, whose LDS addresses are then constants)
+    auto tile = [&](int i, const E* kl, const E* vl) {
         // tile i is here; the buffer of tile i - 1 is free
         swa_landed();
         if (i + 1 < nt) fetch(i + 1);
         const int k0 = key0(i);
-        if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) continue;   // nothing visible to the wave
-        const E* kl = kt[i & 1];
-        const E* vl = vt[i & 1];
+        if (k0 > wp1 || (k0 + BN - 1 <= wp0 - a.W && k0 >= a.S)) return;   // nothing visible to the wave
         floatx16 sc[NS];
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -122,6 +121,10 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
                     o[dt] = T::mma(T::template ld_col<D>(vl, 32 * n + (32 / NP) * j, 32 * dt, lane), p, o[dt]);
             }
         __builtin_amdgcn_s_setprio(0);
+    };
+    for (int i = 0; i < nt; i += 2) {
+        tile(i, kt[0], vt[0]);
+        if (i + 1 < nt) tile(i + 1, kt[1], vt[1]);
     }
     l += swa_swap(l);
     if (row >= s.nq) return;
