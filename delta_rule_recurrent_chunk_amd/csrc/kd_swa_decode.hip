@@ -51,6 +51,27 @@ __device__ __forceinline__ int swa_slot(const Seen& s, int j, int S, int cap) {
     return x < cap ? x : x - (cap - S);
 }
 
+template <class E, int D, int N>
+__device__ __forceinline__ void swa_join(const float* pb, int64_t pstep, int nsplit, int nh,
+                                         const float (*mw)[SWA_DECODE_SPLITS + 1], const float* wl, E* o, int tid) {
+    for (int i = tid; i < nh * D / 2; i += 128) {
+        const int h = 2 * i / D;
+        float2 v[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) v[x] = swa_get(pb + min(x, nsplit - 1) * pstep + 2 * i);
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            if (x >= nsplit) continue;
+            const float f = mw[h][x];
+            x0 = fmaf(v[x].x, f, x0);
+            x1 = fmaf(v[x].y, f, x1);
+        }
+        o[2 * i] = (E)(x0 * wl[h]);
+        o[2 * i + 1] = (E)(x1 * wl[h]);
+    }
+}
+
 // Workgroup (split, key head and block of up to 32 query heads, b): two waves
 // share the split's keys, 32 at a time.  The heads are the columns of the same
 // products that the forward pass makes with queries, St = K Qt and Ot += Vt Pt,
@@ -74,8 +95,8 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     // the queries pass through the second tiles' room before those are fetched
     __shared__ __align__(16) struct {
         E kv[ST][2][2][32 * D];
-        float qx[ST == 2 ? 4 : 32 * D];
-        float kn[D], vn[D];
+        float qx[ST == 2 ? 4 : 64 * D];
+        float kr[D], kn[D], vn[D];      // the new key as given and as the cache holds it, the new value
         float2 cs[D / 2];
         float ms[3][32], ls[3][32], mw[32][SWA_DECODE_SPLITS + 1], wl[32];
         int last;
@@ -85,14 +106,27 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     float(*const ms)[32] = sm.ms;
     float(*const ls)[32] = sm.ls;
     float(*const mw)[SWA_DECODE_SPLITS + 1] = sm.mw;
-    float *const kn = sm.kn, *const vn = sm.vn, *const wl = sm.wl;
+    float *const kr = sm.kr, *const kn = sm.kn, *const vn = sm.vn, *const wl = sm.wl;
     int& last = sm.last;
     float* const qs = ST == 2 ? reinterpret_cast<float*>(kv[ST - 1]) : sm.qx;      // [32][D]
+    float* const raw = qs + 32 * D;                                                // the queries as given
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
     const int G = a.Hq / a.Hkv, nhb = (G + 31) / 32;
     const int sp = blockIdx.x, hk = blockIdx.y / nhb, hb = blockIdx.y % nhb, b = blockIdx.z;
     const int h0 = hk * G + hb * 32, nh = min(32, G - hb * 32);
+    // everything that does not depend on the position loads while it does
+    const E* qrow = (const E*)a.q + b * a.qb + (int64_t)h0 * D;
+    const E* krow = (const E*)a.k + b * a.kb + (int64_t)hk * D;
+    const E* vrow = (const E*)a.v + b * a.vb + (int64_t)hk * D;
+    const int n = a.rot / 2;
+    const double fr = tid < n ? a.freqs[tid] : 0.0;      // (n <= 64)
     const int pos = a.lens[b];
+    for (int i = tid; i < nh * D; i += 128) raw[i] = (float)qrow[i];
+    if (sp == 0)
+        for (int i = tid; i < D; i += 128) {
+            kr[i] = (float)krow[i];
+            vn[i] = (float)vrow[i];
+        }
     E* o = (E*)a.o + ((int64_t)b * a.Hq + h0) * D;
     if (pos < 0) {     // an unused row: nothing is stored, its output is zero
         if (sp == 0)
@@ -125,31 +159,24 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     if (t < tb) fetch(t, 0);
 
     // queries (turned, times scale log2 e), and where they are needed the new key and value
-    const int n = a.rot / 2;
-    for (int j = tid; j < n; j += 128) cs[j] = rope_cs((double)pos, a.freqs[j], a.rope_scale, 0);
+    if (tid < n) cs[tid] = rope_cs((double)pos, fr, a.rope_scale, 0);
     __syncthreads();
-    auto turned = [&](const E* row, int i) -> float {
-        const float x = (float)row[i];
+    auto turned = [&](const float* row, int i) -> float {
+        const float x = row[i];
         if (i >= a.rot) return x;
         const int j = a.interleaved ? i / 2 : i < n ? i : i - n;
         const bool second = a.interleaved ? (i & 1) : i >= n;
-        const float y = (float)row[a.interleaved ? i ^ 1 : second ? i - n : i + n];
+        const float y = row[a.interleaved ? i ^ 1 : second ? i - n : i + n];
         return second ? fmaf(x, cs[j].x, y * cs[j].y) : fmaf(x, cs[j].x, -y * cs[j].y);
     };
-    const E* qrow = (const E*)a.q + b * a.qb + (int64_t)h0 * D;
-    for (int i = tid; i < nh * D; i += 128) qs[i] = turned(qrow + i / D * D, i % D) * a.c;
-    if (sp == 0) {
-        const E* krow = (const E*)a.k + b * a.kb + (int64_t)hk * D;
-        const E* vrow = (const E*)a.v + b * a.vb + (int64_t)hk * D;
-        const int64_t slot = cache_slot(pos, a.S, a.cap);
-        for (int i = tid; i < D; i += 128) {
-            const E kx = (E)turned(krow, i), vx = vrow[i];
-            kn[i] = (float)kx;
-            vn[i] = (float)vx;
-            if (hb == 0) {
-                kc[slot * a.kcs[1] + i] = kx;
-                vc[slot * a.vcs[1] + i] = vx;
-            }
+    for (int i = tid; i < nh * D; i += 128) qs[i] = turned(raw + i / D * D, i % D) * a.c;
+    if (sp == 0 && tid < D) {
+        const E kx = (E)turned(kr, tid);
+        kn[tid] = (float)kx;
+        if (hb == 0) {
+            const int64_t slot = cache_slot(pos, a.S, a.cap);
+            kc[slot * a.kcs[1] + tid] = kx;
+            vc[slot * a.vcs[1] + tid] = (E)vn[tid];
         }
     }
     __syncthreads();
@@ -286,42 +313,26 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     if (!last) return;
     if (tid == 0) __hip_atomic_store(a.count + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
     const float* pb = a.part + (int64_t)item * a.nsplit * pstep;
-    for (int i = tid; i < nh * a.nsplit; i += 128) {
-        const int h = i % nh, x = i / nh;
-        const float2 v = swa_get(pb + x * pstep + 32 * D + 2 * h);
-        mw[h][x] = v.x;
-        accs[h * SWA_DECODE_SPLITS + x] = v.y;
+    // weight of every split, 32 lanes a head
+    static_assert(SWA_DECODE_SPLITS == 32, "one lane per split");
+    for (int h = tid / 32; h < nh; h += 4) {
+        const int x = tid % 32;
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (x < a.nsplit) v = swa_get(pb + x * pstep + 32 * D + 2 * h);
+        float mn = v.x;
+#pragma unroll
+        for (int y = 16; y > 0; y /= 2) mn = fmaxf(mn, __shfl_xor(mn, y));
+        const float f = __builtin_amdgcn_exp2f(v.x - (mn == -INFINITY ? 0.f : mn));
+        float L = f * v.y;
+#pragma unroll
+        for (int y = 16; y > 0; y /= 2) L += __shfl_xor(L, y);
+        mw[h][x] = f;
+        if (x == 0) wl[h] = 1.f / L;
     }
     __syncthreads();
-    if (tid < nh) {      // weight of every split
-        float mn = -INFINITY, L = 0.f;
-        for (int x = 0; x < a.nsplit; ++x) mn = fmaxf(mn, mw[tid][x]);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        for (int x = 0; x < a.nsplit; ++x) {
-            const float f = __builtin_amdgcn_exp2f(mw[tid][x] - mu);
-            mw[tid][x] = f;
-            L = fmaf(accs[tid * SWA_DECODE_SPLITS + x], f, L);
-        }
-        wl[tid] = 1.f / L;
-    }
-    __syncthreads();
-    for (int i = tid; i < nh * D / 2; i += 128) {
-        const int h = 2 * i / D;
-        float x0 = 0.f, x1 = 0.f;
-        for (int x = 0; x < a.nsplit; x += 8) {
-            float2 v[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = swa_get(pb + min(x + y, a.nsplit - 1) * pstep + 2 * i);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const float f = x + y < a.nsplit ? mw[h][x + y] : 0.f;
-                x0 = fmaf(v[y].x, f, x0);
-                x1 = fmaf(v[y].y, f, x1);
-            }
-        }
-        o[2 * i] = (E)(x0 * wl[h]);
-        o[2 * i + 1] = (E)(x1 * wl[h]);
-    }
+    // all splits' values in flight at once
+    if (a.nsplit <= 8) swa_join<E, D, 8>(pb, pstep, a.nsplit, nh, mw, wl, o, tid);
+    else swa_join<E, D, SWA_DECODE_SPLITS>(pb, pstep, a.nsplit, nh, mw, wl, o, tid);
 }
 
 // Tokens of a prompt into the cache: token t of sequence b, t < lens[b], at
