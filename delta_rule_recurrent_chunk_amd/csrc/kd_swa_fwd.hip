@@ -12,6 +12,40 @@
 
 namespace kd {
 
+// o of a wave's queries, one key after the other (rare, see its call): keys
+// 0 .. S - 1 and first .. last, each for the queries that see it.
+template <class E, int D>
+__device__ __forceinline__ void swa_fwd_single(floatx16* o, const typename SwaT<E>::Frag* q, const E* k, int64_t krs,
+                                               const E* v, int64_t vrs, int last, int first, int pos, int W, int S,
+                                               float c, float mu, int g)
+{
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+#pragma unroll 1
+    for (int key = S > 0 ? 0 : first; key <= last; ++key) {
+        if (key >= S && key < first) key = first;
+        if (key > last) break;
+        float s = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) s += SwaT<E>::dot(q[ks], swa_ld_mem<E>(k + key * krs, ks, g));
+        s += swa_swap(s);
+        const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
+        const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -mu)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const E4 x = *reinterpret_cast<const E4*>(v + key * vrs + 32 * i + 8 * j + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][4 * j + e] = fmaf(p, sees ? (float)x[e] : 0.f, o[i][4 * j + e]);
+            }
+    }
+}
+
 template <class E, int D, int BN>
 __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_kernel(SwaArgs a, int nslots)
 {
@@ -127,6 +161,18 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
         if (i + 1 < nt) tile(i + 1, kt[1], vt[1]);
     }
     l += swa_swap(l);
+    // A hidden key has weight 0, and 0 times an infinity or a NaN in its values
+    // would still reach the queries of its tile.  A wave with an output that is
+    // not finite makes its outputs again from the maxima and sums it has, key by
+    // key over the keys that each query sees.
+    float sum = 0.f;      // (0 times what is not finite is a NaN)
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum = fmaf(o[i][r], 0.f, sum);
+    if (__any(!(sum == 0.f)))
+        swa_fwd_single<E, D>(o, q, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1), pos, a.W,
+                             a.S, a.c, m == -INFINITY ? 0.f : m, g);
     if (row >= s.nq) return;
     // a row that sees nothing: o = 0, lse = -infinity
     const bool none = m == -INFINITY && l == 0.f;

@@ -306,6 +306,40 @@ def test_swa_packed_with_bad_offsets_stays_inside():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_swa_hidden_infinities_and_nans_stay_hidden(d, dtype):
+    """Keys and values that are not finite reach the queries that see them and no others (a padded batch's tail, a
+    bad token outside the window)."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    T, W, S = 300, 70, 3
+    (q, qv), (k, kv), (v, vv), _ = swa_inputs(1, T, T, 2, 1, d, dtype, d)
+    val, err = R.attention_heads(qv[0], kv[0], vv[0], W, S, 1 / np.sqrt(d), None, R.unit(dtype))
+    pos = np.arange(T)
+    inf, nan = float("inf"), float("nan")
+    for at, value in ((1, nan), (100, inf), (129, nan), (130, -inf), (250, nan), (T - 1, inf)):
+        sees = (pos >= at) & ((pos - at < W) | (at < S))
+        bad = v.clone()
+        bad[0, at, 0, ::5] = value
+        o, l = kd.swa_fwd(q, k, bad, W, S, return_lse=True)
+        o = host(o[0])
+        check("hidden from", o[~sees], val["o"][~sees], err["o"][~sees])
+        check("lse", l[0], val["lse"], err["lse"])
+        # (a weight can be zero in fp32; none is here: scores are a few units apart)
+        got = o[sees][..., ::5]
+        assert np.isnan(got).all() if value != value else (got == value).all(), at
+        rest = [i for i in range(d) if i % 5]
+        check("other elements", o[sees][..., rest], val["o"][sees][..., rest], err["o"][sees][..., rest])
+        bad = k.clone()
+        bad[0, at] = value
+        check("key", host(kd.swa_fwd(q, bad, v, W, S)[0])[~sees], val["o"][~sees], err["o"][~sees])
+    # everything behind token 200 is garbage: the first 200 rows do not see it
+    kk, vv2, qq = k.clone(), v.clone(), q.clone()
+    kk[:, 200:], vv2[:, 200:], qq[:, 200:] = nan, nan, nan
+    check("padded", host(kd.swa_fwd(qq, kk, vv2, W, S)[0, :200]), val["o"][:200], err["o"][:200])
+
+
 def test_swa_on_views_and_pieces():
     """Views of a fused projection, [B, H, T, d] memory, a broadcast batch; a prompt in pieces."""
     import delta_rule_recurrent_chunk_amd as kd
