@@ -156,7 +156,7 @@ const char* kron_delta_status_string(int s) {
     switch (s) {
     case KD_OK: return "ok";
     case KD_ERR_NULL: return "a required pointer is NULL";
-    case KD_ERR_SHAPE: return "unsupported shape (need B,H>=1, T>=0, dk==dv in {32,64,128})";
+    case KD_ERR_SHAPE: return "unsupported shape (delta rule: B,H>=1, T>=0, dk==dv in {32,64,128}; other calls: the sizes kron_delta.h names)";
     case KD_ERR_DTYPE: return "unsupported dtype for this call (bf16: d in {32,64,128}; fp32: d in {32,64}, and 128 in the forward, decode, backward and training pair)";
     case KD_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case KD_ERR_WORKSPACE: return "workspace missing or too small";

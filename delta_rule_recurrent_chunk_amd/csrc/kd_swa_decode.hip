@@ -277,9 +277,9 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
         }
     }
     __syncthreads();
-    const int item = b * (int)gridDim.y + blockIdx.y;
+    const int64_t item = (int64_t)b * gridDim.y + blockIdx.y;
     const int64_t pstep = (int64_t)32 * (D + 2);
-    float* part = a.part + ((int64_t)item * a.nsplit + sp) * pstep;
+    float* part = a.part + (item * a.nsplit + sp) * pstep;
     for (int i = tid; i < nh * D / 2; i += 128) {
         const int h = 2 * i / D, e = 2 * i % D;
         const float m2 = sp == 0 ? ms[2][h] : -INFINITY;
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     __syncthreads();
     if (!last) return;
     if (tid == 0) __hip_atomic_store(a.count + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
-    const float* pb = a.part + (int64_t)item * a.nsplit * pstep;
+    const float* pb = a.part + item * a.nsplit * pstep;
     // weight of every split, 32 lanes a head
     static_assert(SWA_DECODE_SPLITS == 32, "one lane per split");
     for (int h = tid / 32; h < nh; h += 4) {
@@ -358,15 +358,14 @@ __global__ __launch_bounds__(256) void kd_swa_store_kernel(SwaStoreArgs a)
 
 // Work items before splitting: one per sequence, key head and block of 32 of
 // its query heads.
-static int swa_decode_items(int B, int Hq, int Hkv) { return B * Hkv * ((Hq / Hkv + 31) / 32); }
+static int64_t swa_decode_items(int B, int Hq, int Hkv) { return (int64_t)B * Hkv * ((Hq / Hkv + 31) / 32); }
 
 // Splits of a row's keys: two workgroups for each of the chip's 256 compute
 // units (all of them resident: 64 KB of LDS each), none below 64 keys.  Rows
 // are split only where there are fewer than SWA_DECODE_COUNTERS items, so that
 // many counters serve every call.
 int swa_decode_splits(int B, int Hq, int Hkv, int seen) {
-    const int items = swa_decode_items(B, Hq, Hkv);
-    int n = SWA_DECODE_COUNTERS / items;
+    int n = (int)(SWA_DECODE_COUNTERS / swa_decode_items(B, Hq, Hkv));
     const int most = (seen + 63) / 64;
     n = n < most ? n : most;
     n = n < SWA_DECODE_SPLITS ? n : SWA_DECODE_SPLITS;

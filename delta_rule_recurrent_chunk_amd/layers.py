@@ -145,6 +145,11 @@ def _code(dt):
     raise TypeError("tensors must be bfloat16 or float32, got %s" % dt)
 
 
+def _int32(x):
+    """An integer for an int32 field: a value outside its range becomes the nearest one in it."""
+    return min(max(int(x), -(1 << 31)), (1 << 31) - 1)
+
+
 def _flat(t):
     """The tensor, contiguous and at a 16-byte address (a copy where it is not)."""
     if t is None:
@@ -396,7 +401,7 @@ def _swa(q, k, v, window, sinks, scale, cu):
     else:
         B, q4, k4, v4 = q.shape[0], q, k, v
     d = q.shape[-1]
-    desc = KdSwaDesc(B, q4.shape[1], k4.shape[1], q4.shape[2], k4.shape[2], d, _code(q.dtype), int(window), int(sinks),
+    desc = KdSwaDesc(B, q4.shape[1], k4.shape[1], q4.shape[2], k4.shape[2], d, _code(q.dtype), _int32(window), _int32(sinks),
                      float(1.0 / math.sqrt(d) if scale is None else scale), _s3(*q4.stride()[:3]),
                      _s3(*k4.stride()[:3]), _s3(*v4.stride()[:3]))
     return dev, desc, q, k, v, cu
@@ -450,7 +455,7 @@ def _cache_desc(q_heads, k_cache, v_cache, window, sinks, scale=1.0, rot=0, layo
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("%s must have a contiguous last dimension" % name)
     B, cap, Hkv, d = k_cache.shape
-    return KdSwaCacheDesc(B, q_heads, Hkv, d, cap, _code(k_cache.dtype), int(window), int(sinks), scale,
+    return KdSwaCacheDesc(B, q_heads, Hkv, d, cap, _code(k_cache.dtype), _int32(window), _int32(sinks), scale,
                           rot, layout, rope_scale, k_cache.stride()[:3], v_cache.stride()[:3])
 
 

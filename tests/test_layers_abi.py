@@ -198,6 +198,7 @@ def test_binding_refuses_host_tensors_and_bad_arguments():
                dict(rot=4, factor=0.5)):
         with pytest.raises(ValueError):
             kd.rope_frequencies(**kw)
+    assert la._int32(10 ** 12) == 2 ** 31 - 1 and la._int32(-10 ** 12) == -2 ** 31 and la._int32(5) == 5   # (no wrap)
     w, m = kd.rope_frequencies(8, scaling="linear", factor=4.0)
     assert m == 1.0 and torch.allclose(w * 4, kd.rope_frequencies(8)[0])
     w, m = kd.rope_frequencies(64, scaling="byparts", factor=8.0, original_length=4096)
