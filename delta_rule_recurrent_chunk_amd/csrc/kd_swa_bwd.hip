@@ -29,7 +29,40 @@ __device__ __forceinline__ int swa_far(const SwaArgs& a, int past) { return max(
 // the rounded o there (the sum of P dP is only known at the end, when it goes
 // to the other kernels): for queries that see few keys the two roundings
 // together would double the error of dQ, so waves whose queries see fewer than
-// 512 keys take the rounding's remainder of dS through a second product.
+// 512 keys take the rounding's remainder of dS through a second product.  The
+// error that o's rounding leaves in delta falls with the root of the number of
+// keys against that of dQ; waves whose queries see at most 32 first take the
+// sum of P dP from memory, in a pass of its own.
+//
+// That pass: delta plus the sum of P (dP - delta) over the keys k0 .. k1 - 1
+// that the wave's queries see, 32 at a time.
+template <class E, int D>
+__device__ __forceinline__ float swa_dq_near(float delta, const typename SwaT<E>::Frag* q, const typename SwaT<E>::Frag* dO,
+                                             const E* k, int64_t krs, const E* v, int64_t vrs, int k0, int k1, int nk,
+                                             int pos, int W, int S, float c, float lse2, int lane)
+{
+    typedef SwaT<E> T;
+    constexpr int NK = D / T::KC;
+    const int g = lane >> 5;
+    float sum = 0.f;
+#pragma unroll 1
+    for (; k0 < k1; k0 += 32) {
+        const int64_t key = min(k0 + (lane & 31), nk - 1);
+        floatx16 sc, dp;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sc[r] = 0.f, dp[r] = -delta;
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+            sc = T::mma(swa_ld_mem<E>(k + key * krs, ks, g), q[ks], sc);
+            dp = T::mma(swa_ld_mem<E>(v + key * vrs, ks, g), dO[ks], dp);
+        }
+        swa_mask_keys(sc, k0 + 4 * g, pos, W, S);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum = fmaf(__builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse2)), dp[r], sum);
+    }
+    return sum;
+}
+
 template <class E, int D, int BN>
 __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_kernel(SwaArgs a, int nslots)
 {
@@ -75,6 +108,18 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     const SwaFetch<E, D, BN, 256> kf((const E*)a.k + b * a.ks[0] + (int64_t)s.q0 * a.ks[1] + hk * a.ks[2], a.ks[1], s.nk, tid);
     const SwaFetch<E, D, BN, 256> vf((const E*)a.v + b * a.vs[0] + (int64_t)s.q0 * a.vs[1] + hk * a.vs[2], a.vs[1], s.nk, tid);
 
+    const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;
+    if (sizeof(E) == 2 && (wp0 < 32 || a.W <= 32 - a.S)) {
+        const int first = max(0, wp0 - a.W + 1) & ~31;
+        auto near = [&](int k0, int k1) {
+            return swa_dq_near<E, D>(delta, q, dO, kf.base, a.ks[1], vf.base, a.vs[1], k0, min(k1, s.nk), s.nk, pos, a.W, a.S,
+                                     a.c, lse2, lane);
+        };
+        float more = near(first, wp1 + 1);
+        if (first > 0 && a.S > 0) more += near(0, a.S);
+        delta += more + swa_swap(more);
+    }
+
     floatx16 acc[ND];
 #pragma unroll
     for (int i = 0; i < ND; ++i)
@@ -84,7 +129,6 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     const int pmax = min(s.past + r0 + 127, s.nk - 1);
     const int lo = max(0, s.past + r0 - a.W + 1) / BN, hi = pmax < 0 ? 0 : pmax / BN + 1;
     const int sk = min((a.S + BN - 1) / BN, lo), nt = sk + max(hi - lo, 0);
-    const int wp0 = s.past + r0 + 32 * w, wp1 = wp0 + 31;
     const bool few = sizeof(E) == 2 && (wp0 < 511 || a.W + a.S < 512);
     auto key0 = [&](int i) { return (i < sk ? i : lo + (i - sk)) * BN; };
     auto fetch = [&](int i) {
@@ -146,12 +190,14 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
 // One 32-row piece of a query tile against 32 keys held as B operands (the
 // values' either in registers or as rows of an LDS tile): S and dP have the
 // queries as rows, so the weights and their gradients are again the B operands
-// of the next products (dVt += dOt P, dKt += Qt dS).  rl: lse2 of the tile's
+// of the next products (dVt += dOt P, dKt += Qt dS).  few: the keys are seen by
+// fewer than 64 queries; P and dS then carry what their rounding left, which
+// averages out in longer sums.  rl: lse2 of the tile's
 // queries, and RS floats on their -delta.
 template <class E, int D, int RS, class VF>
 __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const float* rl, int r0,
                                              const typename SwaT<E>::Frag* k, const VF& v,
-                                             floatx16* dk, floatx16* dv, float c, bool full, int lane, int key, int p0,
+                                             floatx16* dk, floatx16* dv, float c, bool full, bool few, int lane, int key, int p0,
                                              int left, int W, int S)
 {
     typedef SwaT<E> T;
@@ -187,6 +233,15 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
         for (int i = 0; i < ND; ++i) {
             dv[i] = T::mma(T::template ld_col<D>(dt, r0 + (32 / NP) * j, 32 * i, lane), pv, dv[i]);
             dk[i] = T::mma(T::template ld_col<D>(qt, r0 + (32 / NP) * j, 32 * i, lane), pk, dk[i]);
+        }
+        if (sizeof(E) == 2 && few) {
+            const Frag rv = T::rest(sc, j, pv), rk = T::rest(dp, j, pk);
+            const int ln = lane + opaque_zero();
+#pragma unroll
+            for (int i = 0; i < ND; ++i) {
+                dv[i] = T::mma(T::template ld_col<D>(dt, r0 + (32 / NP) * j, 32 * i, ln), rv, dv[i]);
+                dk[i] = T::mma(T::template ld_col<D>(qt, r0 + (32 / NP) * j, 32 * i, ln), rk, dk[i]);
+            }
         }
     }
 }
@@ -252,6 +307,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
     const int t0 = max(0, k0 - s.past) / BQ, t1 = min(s.nq, k0 + 127 + a.W - s.past);
     const int per = max(0, (t1 + BQ - 1) / BQ - t0), nt = per * G;
     const int wk0 = k0 + 32 * w, wk1 = wk0 + 31;
+    const bool few = (int64_t)(min(t1, wk1 + a.W - s.past) - max(0, wk0 - s.past)) * G < 64;
     const SwaFetch<E, D, BQ, 256> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + hk * G * a.qs[2], a.qs[1], s.nq, tid);
     const SwaFetch<E, D, BQ, 256> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G) * D, (int64_t)a.Hq * D, s.nq, tid);
     const float2* rb = a.rows + ((int64_t)b * a.Hq + hk * G) * a.Tq + s.q0;
@@ -282,7 +338,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
             const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= t1;   // (rows from t1 on: the sinks' pass)
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                swa_dkv_tile<E, D, BQ>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1][0], 32 * n, k, v, dk, dv, a.c, full, lane,
+                swa_dkv_tile<E, D, BQ>(sm.q[i & 1], sm.dO[i & 1], sm.rows[i & 1][0], 32 * n, k, v, dk, dv, a.c, full, few, lane,
                                    key, p0 + 32 * n, t1 - t - 32 * n, a.W, a.S);
         }
         if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][0][tid] = next.x, sm.rows[(i + 1) & 1][1][tid] = -next.y;
@@ -366,7 +422,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
     for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
-    const bool all = k0 + 32 <= a.S;
+    const bool all = k0 + 32 <= a.S, few = (int64_t)(s.nq - swa_far(a, s.past)) * (a.Hq / a.Hkv) < 64;
     auto vf = [&](int ks, int) -> Frag { return v[ks]; };
     const SwaFetch<E, D, BQ, 64 * NW> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + h * a.qs[2], a.qs[1], s.nq, tid);
     const SwaFetch<E, D, BQ, 64 * NW> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + h) * D, (int64_t)a.Hq * D, s.nq, tid);
@@ -382,7 +438,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
         }
         swa_landed();
         // beyond the window a row sees the sinks alone: window 1 leaves their mask
-        swa_dkv_tile<E, D, BQ>(sm.q, sm.dO, sm.rows[0], 32 * w, k, vf, dk, dv, a.c, all && t + BQ <= tb, lane, key,
+        swa_dkv_tile<E, D, BQ>(sm.q, sm.dO, sm.rows[0], 32 * w, k, vf, dk, dv, a.c, all && t + BQ <= tb, few, lane, key,
                            s.past + t + 32 * w, tb - t - 32 * w, 1, a.S);
     }
     __syncthreads();

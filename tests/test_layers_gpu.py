@@ -268,6 +268,27 @@ def test_swa_forward_and_backward(Tq, Tk, Hq, Hkv, window, sinks, d, dtype):
     assert all(torch.equal(g[n], g2[n]) for n in g)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,window,sinks", [
+    (2, 2, 1, 1, 7, 0), (6, 6, 1, 1, 17, 9), (5, 5, 4, 2, 551, 4), (9, 9, 2, 1, 1121, 9), (20, 20, 3, 1, 3, 2),
+    (31, 50, 2, 1, 4, 0), (30, 100, 2, 2, 20, 5), (10, 300, 1, 1, 30, 2)])
+def test_swa_gradients_that_few_keys_make_up_lose_the_rounding_of_the_result_alone(Tq, Tk, Hq, Hkv, window, sinks, d):
+    """Where a sum has few terms its weights' roundings to bf16 do not average out, nor does the one in delta: there
+    the weights carry their remainders (two bf16 numbers: 2^-16 of each term; 2^-14 is allowed) and delta is summed
+    in fp32, which leaves the rounding of the result, 2^-8 of it."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    print("case", (Tq, Tk, Hq, Hkv, window, sinks, d), flush=True)
+    (q, qv), (k, kv), (v, vv), (dO, ov) = swa_inputs(2, Tq, Tk, Hq, Hkv, d, "bf16", 7 * Tq + Tk + d)
+    o, lse = kd.swa_fwd(q, k, v, window, sinks, return_lse=True)
+    g = kd.swa_bwd(q, k, v, o, lse, dO, window, sinks)
+    torch.cuda.synchronize()
+    for b in range(2):
+        val, err = R.attention_heads(qv[b], kv[b], vv[b], window, sinks, 1 / np.sqrt(d), ov[b], 2.0 ** -14)
+        for n in ("dq", "dk", "dv"):
+            check(n, g[n][b], val[n], err[n] + 2.0 ** -8 * np.abs(val[n]))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens", [[1], [0, 5, 0], [128, 128, 1, 127], [300, 1, 1, 0, 77, 129, 256],
                                   [3] * 70 + [200], [1500, 1, 2100, 90]])
