@@ -58,8 +58,64 @@ __device__ __forceinline__ float swa_dq_near(float delta, const typename SwaT<E>
         }
         swa_mask_keys(sc, k0 + 4 * g, pos, W, S);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sum = fmaf(__builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse2)), dp[r], sum);
+        for (int r = 0; r < 16; ++r) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse2)) * dp[r];
+            sum += sc[r] == -INFINITY ? 0.f : x;      // (a hidden key's dP may be anything)
+        }
     }
+    return sum;
+}
+
+// dQ (before its scale) of a wave's queries and the sum of P (dP - delta), one
+// key after the other (rare, see its call): keys 0 .. S - 1 and first .. last,
+// each for the queries that see it.
+template <class E, int D>
+__device__ __forceinline__ float swa_dq_single(floatx16* acc, const typename SwaT<E>::Frag* q, const typename SwaT<E>::Frag* dO,
+                                               const E* k, int64_t krs, const E* v, int64_t vrs, int last, int first,
+                                               int pos, int W, int S, float c, float lse2, float delta, int g)
+{
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    float dsum = 0.f;
+#pragma unroll 1
+    for (int key = S > 0 ? 0 : first; key <= last; ++key) {
+        if (key >= S && key < first) key = first;
+        if (key > last) break;
+        float s = 0.f, dp = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+            s += SwaT<E>::dot(q[ks], swa_ld_mem<E>(k + key * krs, ks, g));
+            dp += SwaT<E>::dot(dO[ks], swa_ld_mem<E>(v + key * vrs, ks, g));
+        }
+        s += swa_swap(s);
+        dp += swa_swap(dp);
+        const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
+        const float ds = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)) * (dp - delta) : 0.f;
+        dsum += ds;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const E4 x = *reinterpret_cast<const E4*>(k + key * krs + 32 * i + 8 * j + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][4 * j + e] = fmaf(ds, sees ? (float)x[e] : 0.f, acc[i][4 * j + e]);
+            }
+    }
+    return dsum;
+}
+
+template <int ND>
+__device__ __forceinline__ float swa_zero_if_finite(const floatx16* x)
+{
+    float sum = 0.f;      // (0 times what is not finite is a NaN)
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum = fmaf(x[i][r], 0.f, sum);
     return sum;
 }
 
@@ -181,6 +237,12 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
         if (i + 1 < nt) tile(i + 1, kt[1], vt[1]);
     }
     dsum += swa_swap(dsum);
+    // A hidden key's gradient is 0, and 0 times an infinity or a NaN in its key
+    // or value would still reach the queries of its tile: a wave with a result
+    // that is not finite makes it again key by key.
+    if (__any(!(swa_zero_if_finite<ND>(acc) == 0.f)))
+        dsum = swa_dq_single<E, D>(acc, q, dO, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1),
+                                   pos, a.W, a.S, a.c, lse2, delta, g);
     if (row >= s.nq) return;
     swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
     // the sum of P dP: that of P (dP - delta) and delta (P sums to 1)
@@ -246,6 +308,60 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
     }
 }
 
+// dK (before its scale) and dV of a wave's keys, one query of the group after
+// the other (rare, see its call): rows t0 .. t1 - 1 of G heads.
+template <class E, int D, class VF>
+__device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const typename SwaT<E>::Frag* k, const VF& v,
+                                               const E* q, int64_t qrs, int64_t qhs, const E* dO, int64_t ors,
+                                               const float2* rows, int64_t rhs, int G, int t0, int t1, int past, int key,
+                                               int W, int S, float c, int lane)
+{
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
+    const int g = lane >> 5;
+    // 32 elements at a time, the scores anew for each: few registers beside k
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+        floatx16 x, y;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < G; ++h)
+#pragma unroll 1
+            for (int t = t0; t < t1; ++t) {
+                const E* qr = q + h * qhs + t * qrs;
+                const E* gr = dO + h * D + t * ors;
+                const float2 row = rows[h * rhs + t];
+                float s = 0.f, dp = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < NK; ++ks) {
+                    s += SwaT<E>::dot(k[ks], swa_ld_mem<E>(qr, ks, g));
+                    dp += SwaT<E>::dot(v(ks, lane), swa_ld_mem<E>(gr, ks, g));
+                    asm volatile("" : "+v"(s), "+v"(dp) : : "memory");      // (a few loads at a time)
+                }
+                s += swa_swap(s);
+                dp += swa_swap(dp);
+                const int pos = past + t;
+                const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
+                const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -row.x)) : 0.f;
+                const float ds = sees ? p * (dp - row.y) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const E4 qe = *reinterpret_cast<const E4*>(qr + 32 * i + 8 * j + 4 * g);
+                    const E4 ge = *reinterpret_cast<const E4*>(gr + 32 * i + 8 * j + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[4 * j + e] = fmaf(ds, sees ? (float)qe[e] : 0.f, x[4 * j + e]);
+                        y[4 * j + e] = fmaf(p, sees ? (float)ge[e] : 0.f, y[4 * j + e]);
+                    }
+                    asm volatile("" : : : "memory");
+                }
+            }
+        dk[i] = x;
+        dv[i] = y;
+    }
+}
+
 // dK and dV of 128 keys of one key head, 32 per wave: tiles of BQ query rows
 // of every head of the group pass through LDS, one tile ahead.  In bf16 the
 // values' fragments are read from LDS too: with those of the keys, dK and dV
@@ -254,7 +370,7 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
 // for four products (241 GFLOP of visible pairs, 690 TFLOP/s; with V in registers
 // and one wave per SIMD 623 us).
 template <class E, int D, int BQ>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
+__global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
@@ -343,6 +459,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void kd_swa_dkv_kernel
         }
         if (i + 1 < nt && tid < BQ) sm.rows[(i + 1) & 1][0][tid] = next.x, sm.rows[(i + 1) & 1][1][tid] = -next.y;
     }
+    // queries that do not see a key, as in dQ
+    if (__any(!(swa_zero_if_finite<ND>(dk) + swa_zero_if_finite<ND>(dv) == 0.f)))
+        swa_dkv_single<E, D>(dk, dv, k, v, qf.base, a.qs[1], a.qs[2], of.base, (int64_t)a.Hq * D, rb, a.Tq, G,
+                             max(0, wk0 - s.past), t1, s.past, key, a.W, a.S, a.c, lane);
     // the sinks' part from the queries beyond the window: all threads add the
     // chunks' partial sums, the lanes that hold the keys take them from LDS
     if (s.blk == 0 && a.pslots > 0 && swa_far(a, s.past) < s.nq) {

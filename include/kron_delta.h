@@ -489,6 +489,8 @@ KD_API kd_status kron_delta_rope(const kd_rope_desc *desc, const void *q, const 
  *     o = sum_s softmax_s(scale q . k_s) v_s,   lse = log sum_s exp(scale q . k_s).
  * Query head h reads key head h / (Hq / Hkv).  A query that sees no key gets
  * o = 0 and lse = -infinity.
+ * What a query does not see (a key, a value; for the gradients of a key, a
+ * query that does not see it) may hold infinities and NaNs.
  *  * q: [B, Tq, Hq, d], k, v: [B, Tk, Hkv, d] in desc->dtype, strides over
  *    batch, token and head in elements (multiples of 16 bytes), contiguous
  *    last dimension; o, dO, dq: contiguous [B, Tq, Hq, d]; dk, dv: contiguous

@@ -361,6 +361,37 @@ def test_swa_hidden_infinities_and_nans_stay_hidden(d, dtype):
     check("padded", host(kd.swa_fwd(qq, kk, vv2, W, S)[0, :200]), val["o"][:200], err["o"][:200])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("W,S", [(37, 0), (50, 3), (400, 5)])
+@pytest.mark.parametrize("what,at", [("k", 131), ("v", 131), ("kv", slice(200, None)), ("kvqg", slice(200, None)),
+                                     ("kvqg", slice(0, 70)), ("q", 140), ("g", 140), ("v", 299)])
+def test_swa_gradients_of_what_does_not_see_infinities_and_nans(what, at, W, S, d, dtype):
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    T = 300
+    print("case", what, at, W, S, d, dtype, flush=True)
+    (q, qv), (k, kv), (v, vv), (dO, ov) = swa_inputs(1, T, T, 2, 1, d, dtype, 11 + d)
+    val, err = R.attention_heads(qv[0], kv[0], vv[0], W, S, 1 / np.sqrt(d), ov[0], R.unit(dtype))
+    vis = R.visible(T, T, W, S)
+    row = np.zeros(T, bool)
+    row[at] = True
+    queries = row & (("q" in what) or ("g" in what))
+    if "k" in what or "v" in what:
+        queries = queries | vis[:, row].any(1)
+    keys = vis[queries].any(0) | (row & (("k" in what) or ("v" in what)))
+    for value in (float("nan"), float("inf")):
+        kk, v2, qq, gg = k.clone(), v.clone(), q.clone(), dO.clone()
+        for n, t in (("k", kk), ("v", v2), ("q", qq), ("g", gg)):
+            if n in what:
+                t[:, at] = value
+        o, lse = kd.swa_fwd(qq, kk, v2, W, S, return_lse=True)
+        g = kd.swa_bwd(qq, kk, v2, o, lse, gg, W, S)
+        check("dq", host(g["dq"][0])[~queries], val["dq"][~queries], err["dq"][~queries])
+        for n in ("dk", "dv"):
+            check(n, host(g[n][0])[~keys], val[n][~keys], err[n][~keys])
+
+
 def test_swa_on_views_and_pieces():
     """Views of a fused projection, [B, H, T, d] memory, a broadcast batch; a prompt in pieces."""
     import delta_rule_recurrent_chunk_amd as kd
