@@ -151,6 +151,12 @@ def _int32(x):
     return min(max(int(x), -(1 << 31)), (1 << 31) - 1)
 
 
+def _fits(name, shape):
+    """Refuses a dimension that an int32 field of a descriptor would wrap."""
+    if max(shape) > 0x7fffffff:
+        raise ValueError("%s has a dimension past 32 bits: %s" % (name, list(shape)))
+
+
 def _flat(t):
     """The tensor, contiguous and at a 16-byte address (a copy where it is not)."""
     if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
@@ -173,6 +179,7 @@ def _workspace(workspace, need, dev):
 def _glr(x, f, i):
     dev = _need_cuda(x, "x")
     shape, dt = x.shape, x.dtype
+    _fits("x", shape)
     for name, t in (("f", f), ("i", i)):
         if t is not None and (t.shape != shape or t.dtype != dt or t.device != dev):
             _check(name, t, shape, dt)
@@ -181,6 +188,7 @@ def _glr(x, f, i):
 
 
 def glr_workspace_bytes(B, T, D, dtype_code) -> int:
+    _fits("the layer", (B, T, D))
     return int(_ready()[1].kron_delta_glr_workspace_bytes(ctypes.byref(KdGlrDesc(B, T, D, dtype_code))))
 
 
@@ -314,6 +322,7 @@ def rope(q, k, positions, freqs, *, layout="half", scale=1.0, inverse=False, out
     if nd not in (3, 4):
         raise ValueError("q must be [B, T, H, d] or [T, H, d]")
     qs = q.shape
+    _fits("q", qs)
     if nd == 4:
         B, T, Hq, d = qs
     else:
@@ -327,6 +336,7 @@ def rope(q, k, positions, freqs, *, layout="half", scale=1.0, inverse=False, out
             raise ValueError("k must be shaped like q but for its heads")
         if k.device != dev:
             raise ValueError("k is on %s, not on %s" % (k.device, dev))
+        _fits("k", ks)
         Hk = ks[-2]
         if k.stride(-1) != 1 and d > 1:
             k = k.contiguous()
@@ -392,11 +402,14 @@ def _swa(q, k, v, window, sinks, scale, cu):
             raise TypeError("%s has dtype %s, q has %s" % (name, t.dtype, q.dtype))
     if k.shape != v.shape or k.shape[-1] != q.shape[-1] or (dims == 4 and k.shape[0] != q.shape[0]):
         raise ValueError("k and v must be one shape and match q's batch and head size")
+    _fits("q", q.shape)
+    _fits("k", k.shape)
     _same_device(dev, k=k, v=v, cu_seqlens=cu)
     q, k, v = _rows(q), _rows(k), _rows(v)
     if cu is not None:
         if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:
             raise ValueError("cu_seqlens must be an int32 device vector [N + 1]")
+        _fits("cu_seqlens", cu.shape)
         cu = cu.contiguous()
         B, q4, k4, v4 = cu.numel() - 1, q[None], k[None], v[None]
     else:
@@ -452,10 +465,11 @@ def swa_bwd(q, k, v, o, lse, dO, window, sinks=0, *, scale=None, cu_seqlens=None
 def _cache_desc(q_heads, k_cache, v_cache, window, sinks, scale=1.0, rot=0, layout=0, rope_scale=1.0):
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
         raise ValueError("k_cache and v_cache must be [B, cap, Hkv, d] of one dtype")
+    B, cap, Hkv, d = k_cache.shape
+    _fits("k_cache", (B, cap, Hkv, d, q_heads))
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("%s must have a contiguous last dimension" % name)
-    B, cap, Hkv, d = k_cache.shape
     return KdSwaCacheDesc(B, q_heads, Hkv, d, cap, _code(k_cache.dtype), _int32(window), _int32(sinks), scale,
                           rot, layout, rope_scale, k_cache.stride()[:3], v_cache.stride()[:3])
 
@@ -529,6 +543,7 @@ def swa_cache_store(k, v, k_cache, v_cache, window, sinks=0, *, lens=None):
     if k.dim() != 4:
         raise ValueError("k and v must be [B, T, Hkv, d]")
     T = k.shape[1]
+    _fits("k", k.shape)
     _check("k", k, (B, T, Hkv, d), k_cache.dtype)
     _check("v", v, (B, T, Hkv, d), k_cache.dtype)
     if lens is not None:

@@ -620,6 +620,24 @@ def test_a_layer_trains_through_rope_and_attention():
         assert abs(num - (host(got) * step).sum()) < 1e-4 * np.abs(host(got) * step).sum() + 1e-6
 
 
+def test_dimensions_past_32_bits_are_refused():
+    """Views of one element: a count that wrapped would leave 128 tokens, a call that succeeds."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    n = (1 << 32) + 128
+    one = torch.zeros(1, dtype=torch.bfloat16, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    freqs, _ = kd.rope_frequencies(16, device="cuda")
+    row, x = one.expand(1, n), one.expand(1, n, 1)
+    heads = one.expand(1, n, 1, 32)
+    for call in (lambda: kd.glr_fwd(x, x), lambda: kd.glr_step(row, row, None, torch.zeros(1, 1, device="cuda").expand(1, n)),
+                 lambda: kd.rope(heads, None, lens.expand(n), freqs), lambda: kd.swa_fwd(heads, heads, heads, 8, 0),
+                 lambda: kd.swa_decode(heads[:, 0], heads[:, 0], heads[:, 0], heads, heads, lens, 8, 0),
+                 lambda: kd.swa_cache_store(heads, heads, heads[:, :128], heads[:, :128], 8, 0)):
+        with pytest.raises(ValueError, match="past 32 bits"):
+            call()
+
+
 def test_streams_and_graphs():
     """Another stream than the current one of the allocation, and captured calls replayed between eager ones."""
     import delta_rule_recurrent_chunk_amd as kd
