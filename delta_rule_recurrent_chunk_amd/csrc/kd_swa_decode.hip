@@ -263,7 +263,10 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
                 if (TWO) acc[i] = T::mma(vf, pr, acc[i]);
             }
         }
-        if (t + 2 * ST < tb) fetch(t + 2 * ST, st);
+        if (t + 2 * ST < tb) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the reads of the tile that is replaced are done
+            fetch(t + 2 * ST, st);
+        }
     }
     l += swa_swap(l);
 
