@@ -24,7 +24,7 @@ hipError_t launch_glr_step(int bf16, const void* x, const void* f, const void* g
 hipError_t launch_rope(int bf16, const RopeArgs& a, hipStream_t st);
 hipError_t launch_swa_fwd(int bf16, int d, const SwaArgs& a, hipStream_t st);
 hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, void* ws, hipStream_t st);
-size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int d, int W, int S);
+size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S);
 hipError_t launch_swa_decode(int bf16, int d, const SwaDecodeArgs& a, hipStream_t st);
 hipError_t launch_swa_store(const SwaStoreArgs& a, int B, hipStream_t st);
 int swa_decode_splits(int B, int Hq, int Hkv, int seen);
@@ -322,7 +322,7 @@ kd::SwaArgs swa_args(const kd_swa_desc* d, const int32_t* cu, const void* q, con
 size_t kron_delta_swa_workspace_bytes(const kd_swa_desc* d, int packed) {
     SwaSpans s;
     if (check_swa(d, packed != 0, &s) != KD_OK) return 0;
-    return kd::swa_bwd_workspace_bytes(packed != 0, d->B, d->Tq, d->Tk, d->Hq, d->d, d->window, d->sinks);
+    return kd::swa_bwd_workspace_bytes(packed != 0, d->B, d->Tq, d->Tk, d->Hq, d->Hkv, d->d, d->window, d->sinks);
 }
 
 kd_status kron_delta_swa_fwd(const kd_swa_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,

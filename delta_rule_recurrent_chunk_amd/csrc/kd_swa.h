@@ -29,6 +29,8 @@ struct SwaArgs {
     float2* rows;                      // [B, Hq, Tq]: lse log2(e) and delta of every query
     float* part;                       // partial dK, dV of the sinks
     int pslots, chunk;                 // query chunks of the sinks' pass (0: none), their rows
+    float* shared;                     // parts of dK, dV of the workgroups that share a group's heads
+    int nsp;                           // how many do
     void *dq, *dk, *dv;                // contiguous
     const int* cu;                     // packed: N + 1 offsets into the Tq == Tk rows
     int B, N, Tq, Tk, Hq, Hkv;

@@ -9,7 +9,8 @@
 //      dK and dV from those queries, in partial sums over chunks of queries;
 //   3. over key blocks: dK and dV from the queries whose window holds them,
 //      also summed over the query heads of a group; the first block adds the
-//      partial sums of 2.
+//      partial sums of 2.  Where key blocks are few, workgroups share the heads
+//      of a group and a last pass adds their fp32 sums.
 #include "kd_swa.h"
 
 namespace kd {
@@ -385,9 +386,11 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
     const int G = a.Hq / a.Hkv;
     int64_t item;
-    if (!swa_item((int64_t)nslots * a.Hkv * a.B, item)) return;
+    if (!swa_item((int64_t)nslots * a.nsp * a.Hkv * a.B, item)) return;
     const int slot = item % nslots;
     item /= nslots;
+    const int sp = item % a.nsp, g0 = sp * G / a.nsp, GS = (sp + 1) * G / a.nsp - g0;      // its heads of the group
+    item /= a.nsp;
     const int hk = item % a.Hkv, b = item / a.Hkv;
     SwaSeq s;
     if (!swa_locate(a, slot, 128, true, s)) return;
@@ -421,12 +424,12 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
 
     // rows whose window holds a key of the block, for every head of the group
     const int t0 = max(0, k0 - s.past) / BQ, t1 = min(s.nq, k0 + 127 + a.W - s.past);
-    const int per = max(0, (t1 + BQ - 1) / BQ - t0), nt = per * G;
+    const int per = max(0, (t1 + BQ - 1) / BQ - t0), nt = per * GS;
     const int wk0 = k0 + 32 * w, wk1 = wk0 + 31;
     const bool few = (int64_t)(min(t1, wk1 + a.W - s.past) - max(0, wk0 - s.past)) * G < 64;
-    const SwaFetch<E, D, BQ, 256> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + hk * G * a.qs[2], a.qs[1], s.nq, tid);
-    const SwaFetch<E, D, BQ, 256> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G) * D, (int64_t)a.Hq * D, s.nq, tid);
-    const float2* rb = a.rows + ((int64_t)b * a.Hq + hk * G) * a.Tq + s.q0;
+    const SwaFetch<E, D, BQ, 256> qf((const E*)a.q + b * a.qs[0] + (int64_t)s.q0 * a.qs[1] + (hk * G + g0) * a.qs[2], a.qs[1], s.nq, tid);
+    const SwaFetch<E, D, BQ, 256> of((const E*)a.dO + (((int64_t)b * a.Tq + s.q0) * a.Hq + hk * G + g0) * D, (int64_t)a.Hq * D, s.nq, tid);
+    const float2* rb = a.rows + ((int64_t)b * a.Hq + hk * G + g0) * a.Tq + s.q0;
     int fh = 0, ft = 0;      // head and tile of the next fetch
     float2 next;             // lse and delta of a row of it
     auto fetch = [&](int i) {
@@ -461,7 +464,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
     }
     // queries that do not see a key, as in dQ
     if (__any(!(swa_zero_if_finite<ND>(dk) + swa_zero_if_finite<ND>(dv) == 0.f)))
-        swa_dkv_single<E, D>(dk, dv, k, v, qf.base, a.qs[1], a.qs[2], of.base, (int64_t)a.Hq * D, rb, a.Tq, G,
+        swa_dkv_single<E, D>(dk, dv, k, v, qf.base, a.qs[1], a.qs[2], of.base, (int64_t)a.Hq * D, rb, a.Tq, GS,
                              max(0, wk0 - s.past), t1, s.past, key, a.W, a.S, a.c, lane);
     // the sinks' part from the queries beyond the window: all threads add the
     // chunks' partial sums, the lanes that hold the keys take them from LDS
@@ -470,13 +473,13 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
         float* sum = reinterpret_cast<float*>(&sm);
         const int64_t step = (int64_t)a.Hq * 2 * SWA_MAX_SINKS * D;      // floats of one chunk
         for (int x = 0; x < 2; ++x) {
-            const float* pb = a.part + ((int64_t)b * a.pslots + first) * step + ((int64_t)hk * G * 2 + x) * SWA_MAX_SINKS * D;
+            const float* pb = a.part + ((int64_t)b * a.pslots + first) * step + ((int64_t)(hk * G + g0) * 2 + x) * SWA_MAX_SINKS * D;
             __syncthreads();
             for (int i = tid; i < a.S * D / 4; i += 256) {
                 floatx4 z = {0.f, 0.f, 0.f, 0.f};
                 for (int y = 0; y <= last - first; ++y)
 #pragma unroll 4
-                    for (int hg = 0; hg < G; ++hg)
+                    for (int hg = 0; hg < GS; ++hg)
                         z += reinterpret_cast<const floatx4*>(pb + y * step + (int64_t)hg * 2 * SWA_MAX_SINKS * D)[i];
                 reinterpret_cast<floatx4*>(sum)[i] = z;
             }
@@ -498,8 +501,31 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
     }
     if (key >= s.nk) return;
     const int64_t at = (((int64_t)b * a.Tk + s.q0 + key) * a.Hkv + hk) * D;
+    if (a.nsp > 1) {
+        const int64_t n = (int64_t)a.B * a.Tk * a.Hkv * D;
+        swa_store_row<float, D>(a.shared + 2 * sp * n + at, dk, a.scale, g);
+        swa_store_row<float, D>(a.shared + (2 * sp + 1) * n + at, dv, 1.f, g);
+        return;
+    }
     swa_store_row<E, D>((E*)a.dk + at, dk, a.scale, g);
     swa_store_row<E, D>((E*)a.dv + at, dv, 1.f, g);
+}
+
+// The sum of the workgroups' parts of dK (y = 0) and dV, in their order: n / 4
+// pieces of four elements, still in the caches.
+template <class E>
+__global__ __launch_bounds__(256) void kd_swa_sum_kernel(SwaArgs a, int64_t n)
+{
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const float* p = a.shared + blockIdx.y * n + i;
+    floatx4 z = *reinterpret_cast<const floatx4*>(p);
+    for (int sp = 1; sp < a.nsp; ++sp) z += *reinterpret_cast<const floatx4*>(p + 2 * sp * n);
+    E4 x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (E)z[e];
+    *reinterpret_cast<E4*>((E*)(blockIdx.y ? a.dv : a.dk) + i) = x;
 }
 
 // Partial dK and dV of 32 sinks from one chunk of one head's queries beyond the
@@ -605,10 +631,25 @@ static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S, 
 
 static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * Hq * 8 + 255) & ~(size_t)255; }
 
-size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int d, int W, int S) {
-    const int nb = packed ? 1 : B;
+static size_t swa_part_bytes(int64_t slots, int B, int Hq, int d) { return (size_t)slots * B * Hq * 2 * SWA_MAX_SINKS * d * 4; }
+
+// Workgroups that share the heads of a group in the dK/dV pass: where its blocks
+// fill less than half of the chip's 256 compute units and each would pass
+// over 512 rows or more (16 tiles; the pass that adds the parts costs about
+// four).  Packed calls bring their own blocks.  The whole backward, bf16, heads
+// of 128, one workgroup per block and shared: 1 x 820, 32/8 heads: 199 and 94 us;
+// 1 x 4096, 16/1 heads, window 1024: 970 and 232 us; 1 x 200, 8/2: 45 and 31 us.
+static int swa_head_splits(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int W) {
+    const int64_t blocks = swa_slots(false, B, Tk, 128) * Hkv * B, rows = min((int64_t)Tq, (int64_t)min(W, Tk) + 127);
+    if (packed || blocks == 0 || blocks > 128 || rows * (Hq / Hkv) < 512) return 1;
+    return (int)min((int64_t)(Hq / Hkv), 256 / blocks);
+}
+
+size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {
+    const int nb = packed ? 1 : B, nsp = swa_head_splits(packed, B, Tq, Tk, Hq, Hkv, W);
     return swa_rows_bytes(nb, Tq, Hq) +
-           (size_t)swa_part_slots(packed, B, Tq, Tk, W, S, swa_chunk((int64_t)nb * Tq, Hq, S)) * nb * Hq * 2 * SWA_MAX_SINKS * d * 4;
+           swa_part_bytes(swa_part_slots(packed, B, Tq, Tk, W, S, swa_chunk((int64_t)nb * Tq, Hq, S)), nb, Hq, d) +
+           (nsp > 1 ? (size_t)nsp * 2 * B * Tk * Hkv * d * 4 : 0);
 }
 
 template <class E, int D>
@@ -616,13 +657,16 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
 {
     constexpr int BN = sizeof(E) == 2 ? 64 : 32;
     const int64_t nq = swa_slots(a.cu, a.N, a.Tq, 128), nk = swa_slots(a.cu, a.N, a.Tk, 128);
-    const int64_t gq = swa_grid(nq * a.Hq * a.B), gk = swa_grid(nk * a.Hkv * a.B);
+    const int64_t gq = swa_grid(nq * a.Hq * a.B);
+    a.nsp = swa_head_splits(a.cu, a.B, a.Tq, a.Tk, a.Hq, a.Hkv, a.W);
+    const int64_t gk = swa_grid(nk * a.nsp * a.Hkv * a.B);
     a.chunk = swa_chunk((int64_t)a.B * a.Tq, a.Hq, a.S);
     const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S, a.chunk);
     if (gq > INT32_MAX || gk > INT32_MAX || np > INT32_MAX / 2) return hipErrorInvalidValue;
     a.rows = (float2*)ws;
     a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));
     a.pslots = (int)np;
+    a.shared = (float*)((char*)a.part + swa_part_bytes(np, a.B, a.Hq, D));
     if (a.Tq > 0) {
         kd_swa_dq_kernel<E, D, BN><<<(unsigned)gq, 256, 0, st>>>(a, (int)nq);
         const hipError_t e = hipGetLastError();
@@ -636,6 +680,10 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     }
     if (nk == 0) return hipSuccess;
     kd_swa_dkv_kernel<E, D, sizeof(E) * D <= 128 ? 64 : 32><<<(unsigned)gk, 256, 0, st>>>(a, (int)nk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.nsp == 1) return e;
+    const int64_t n = (int64_t)a.B * a.Tk * a.Hkv * D;
+    kd_swa_sum_kernel<E><<<dim3((unsigned)((n / 4 + 255) / 256), 2), 256, 0, st>>>(a, n);
     return hipGetLastError();
 }
 

@@ -268,6 +268,28 @@ def test_swa_forward_and_backward(Tq, Tk, Hq, Hkv, window, sinks, d, dtype):
     assert all(torch.equal(g[n], g2[n]) for n in g)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,window,sinks", [(300, 300, 8, 1, 1000, 3), (800, 800, 24, 8, 100, 5),
+                                                       (260, 700, 16, 2, 300, 64), (600, 200, 8, 2, 300, 0), (513, 513, 5, 1, 1, 1)])
+def test_swa_gradients_with_few_blocks_of_keys(Tq, Tk, Hq, Hkv, window, sinks, d, dtype):
+    """Few key blocks and long groups: workgroups share the heads of a group (evenly or not)."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    print("case", (Tq, Tk, Hq, Hkv, window, sinks, d), dtype, flush=True)
+    (q, qv), (k, kv), (v, vv), (dO, ov) = swa_inputs(2, Tq, Tk, Hq, Hkv, d, dtype, Tq + 3 * Tk + d)
+    o, lse = kd.swa_fwd(q, k, v, window, sinks, return_lse=True)
+    ws = torch.full((1 << 27,), 255, dtype=torch.uint8, device="cuda")      # (NaNs: nothing is read that was not written)
+    g = kd.swa_bwd(q, k, v, o, lse, dO, window, sinks, workspace=ws)
+    g2 = kd.swa_bwd(q, k, v, o, lse, dO, window, sinks)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[n], g2[n]) for n in g)
+    for b in range(2):
+        val, err = R.attention_heads(qv[b], kv[b], vv[b], window, sinks, 1 / np.sqrt(d), ov[b], R.unit(dtype))
+        for n in ("dq", "dk", "dv"):
+            check(n, g[n][b], val[n], err[n])
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("Tq,Tk,Hq,Hkv,window,sinks", [
     (2, 2, 1, 1, 7, 0), (6, 6, 1, 1, 17, 9), (5, 5, 4, 2, 551, 4), (9, 9, 2, 1, 1121, 9), (20, 20, 3, 1, 3, 2),
