@@ -633,16 +633,20 @@ static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * H
 
 static size_t swa_part_bytes(int64_t slots, int B, int Hq, int d) { return (size_t)slots * B * Hq * 2 * SWA_MAX_SINKS * d * 4; }
 
-// Workgroups that share the heads of a group in the dK/dV pass: where its blocks
-// fill less than half of the chip's 256 compute units and each would pass
-// over 512 rows or more (16 tiles; the pass that adds the parts costs about
-// four).  Packed calls bring their own blocks.  The whole backward, bf16, heads
-// of 128, one workgroup per block and shared: 1 x 820, 32/8 heads: 199 and 94 us;
-// 1 x 4096, 16/1 heads, window 1024: 970 and 232 us; 1 x 200, 8/2: 45 and 31 us.
+// Workgroups that share the heads of a group in the dK/dV pass: so that there
+// is one for each of the chip's 256 compute units, or two where a group's rows
+// are many (1536: 48 tiles; the parts, 128 KB of each workgroup's, are written
+// and read once more); none share below 512 rows (16 tiles).  Packed calls bring
+// their own blocks.  The heads' sums are added in another order then, so the last
+// bits differ from an unshared call's.  The whole backward, bf16, heads of 128, one workgroup per block and
+// shared: 1 x 820, 32/8 heads: 199 and 94 us; 1 x 4096, 16/1 heads, window 1024:
+// 970 and 190 us; 1 x 4096, 16/8 heads (256 blocks), window 1024: 191 and 174 us,
+// window 256: 90 and, shared against the rule, 98 us; 1 x 200, 8/2: 45 and 31 us.
 static int swa_head_splits(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int W) {
-    const int64_t blocks = swa_slots(false, B, Tk, 128) * Hkv * B, rows = min((int64_t)Tq, (int64_t)min(W, Tk) + 127);
-    if (packed || blocks == 0 || blocks > 128 || rows * (Hq / Hkv) < 512) return 1;
-    return (int)min((int64_t)(Hq / Hkv), 256 / blocks);
+    const int64_t blocks = swa_slots(false, B, Tk, 128) * Hkv * B;
+    const int64_t rows = min((int64_t)Tq, (int64_t)min(W, Tk) + 127) * (Hq / Hkv);
+    if (packed || blocks == 0 || rows < 512) return 1;
+    return (int)max((int64_t)1, min((int64_t)(Hq / Hkv), (rows < 1536 ? 256 : 512) / blocks));
 }
 
 size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {

@@ -526,7 +526,9 @@ KD_API kd_status kron_delta_swa_fwd(const kd_swa_desc *desc, const int32_t *cu_s
 /*
  * Backward: gradients of <dO, o> with respect to q, k, v, from the forward's
  * o and lse.  ws as kron_delta_swa_workspace_bytes says, contents on entry
- * ignored.  Every gradient is summed in a fixed order.
+ * ignored.  Every gradient is summed in a fixed order, which the desc
+ * determines (a packed call may add the heads of a group in another one than
+ * calls for each sequence).
  */
 KD_API kd_status kron_delta_swa_bwd(const kd_swa_desc *desc, const int32_t *cu_seqlens,
                          const void *q, const void *k, const void *v, const void *o, const float *lse,
