@@ -193,6 +193,11 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
 }
 
+// Whether a query at position pos sees one key or none.  The softmax of one
+// score is 1 whatever the score, so nothing behind it has a gradient there:
+// P (dP - delta) would be what the roundings of P and delta leave.
+__device__ __forceinline__ bool swa_alone(int pos, int W, int S) { return pos <= 0 || W + S == 1; }
+
 // Masks of a 32x32 tile whose lane holds one query at position pos and 16 of
 // the keys from k0 on (key0 = k0 + 4 g; register r is key0 + 8 (r / 4) + r % 4):
 // compares of constants with three numbers per lane.

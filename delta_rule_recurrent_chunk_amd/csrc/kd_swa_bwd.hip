@@ -95,7 +95,7 @@ __device__ __forceinline__ float swa_dq_single(floatx16* acc, const typename Swa
         s += swa_swap(s);
         dp += swa_swap(dp);
         const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
-        const float ds = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)) * (dp - delta) : 0.f;
+        const float ds = sees && !swa_alone(pos, W, S) ? __builtin_amdgcn_exp2f(fmaf(s, c, -lse2)) * (dp - delta) : 0.f;
         dsum += ds;
 #pragma unroll
         for (int i = 0; i < ND; ++i)
@@ -103,7 +103,8 @@ __device__ __forceinline__ float swa_dq_single(floatx16* acc, const typename Swa
             for (int j = 0; j < 4; ++j) {
                 const E4 x = *reinterpret_cast<const E4*>(k + key * krs + 32 * i + 8 * j + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][4 * j + e] = fmaf(ds, sees ? (float)x[e] : 0.f, acc[i][4 * j + e]);
+                for (int e = 0; e < 4; ++e)
+                    acc[i][4 * j + e] = fmaf(ds, sees && !swa_alone(pos, W, S) ? (float)x[e] : 0.f, acc[i][4 * j + e]);
             }
     }
     return dsum;
@@ -238,6 +239,12 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
         if (i + 1 < nt) tile(i + 1, kt[1], vt[1]);
     }
     dsum += swa_swap(dsum);
+    if (swa_alone(pos, a.W, a.S)) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    }
     // A hidden key's gradient is 0, and 0 times an infinity or a NaN in its key
     // or value would still reach the queries of its tile: a wave with a result
     // that is not finite makes it again key by key.
@@ -288,6 +295,12 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
     for (int r = 0; r < 16; ++r) {
         sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ls[r]));
         dp[r] *= sc[r];
+    }
+    // queries of one key lie in masked tiles; most masked tiles have none
+    if (!full && (p0 <= 0 || W + S == 1)) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (swa_alone(p0 + 4 * g + 8 * (r / 4) + r % 4, W, S)) dp[r] = 0.f;
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -345,14 +358,15 @@ __device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const
                 const int pos = past + t;
                 const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
                 const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -row.x)) : 0.f;
-                const float ds = sees ? p * (dp - row.y) : 0.f;
+                const bool moves = sees && !swa_alone(pos, W, S);
+                const float ds = moves ? p * (dp - row.y) : 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const E4 qe = *reinterpret_cast<const E4*>(qr + 32 * i + 8 * j + 4 * g);
                     const E4 ge = *reinterpret_cast<const E4*>(gr + 32 * i + 8 * j + 4 * g);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[4 * j + e] = fmaf(ds, sees ? (float)qe[e] : 0.f, x[4 * j + e]);
+                        x[4 * j + e] = fmaf(ds, moves ? (float)qe[e] : 0.f, x[4 * j + e]);
                         y[4 * j + e] = fmaf(p, sees ? (float)ge[e] : 0.f, y[4 * j + e]);
                     }
                     asm volatile("" : : : "memory");
