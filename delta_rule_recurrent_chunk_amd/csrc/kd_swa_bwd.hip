@@ -253,8 +253,10 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
                                    pos, a.W, a.S, a.c, lse2, delta, g);
     if (row >= s.nq) return;
     swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
-    // the sum of P dP: that of P (dP - delta) and delta (P sums to 1)
-    if (g == 0) a.rows[li] = make_float2(lse2, pos < 0 ? 0.f : delta + dsum);
+    // the sum of P dP: that of P (dP - delta) and delta (P sums to 1).  Queries
+    // that see one key are zeros to the dK/dV pass, with lse 0.
+    const bool alone = swa_alone(pos, a.W, a.S);
+    if (g == 0) a.rows[li] = make_float2(alone ? 0.f : lse2, alone ? 0.f : delta + dsum);
 }
 
 // One 32-row piece of a query tile against 32 keys held as B operands (the
@@ -295,12 +297,6 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
     for (int r = 0; r < 16; ++r) {
         sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -ls[r]));
         dp[r] *= sc[r];
-    }
-    // queries of one key lie in masked tiles; most masked tiles have none
-    if (!full && (p0 <= 0 || W + S == 1)) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (swa_alone(p0 + 4 * g + 8 * (r / 4) + r % 4, W, S)) dp[r] = 0.f;
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -357,8 +353,8 @@ __device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const
                 dp += swa_swap(dp);
                 const int pos = past + t;
                 const bool sees = (key <= pos) & ((pos - key < W) | (key < S));
-                const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -row.x)) : 0.f;
-                const bool moves = sees && !swa_alone(pos, W, S);
+                const bool alone = swa_alone(pos, W, S), moves = sees && !alone;
+                const float p = !sees ? 0.f : alone ? 1.f : __builtin_amdgcn_exp2f(fmaf(s, c, -row.x));
                 const float ds = moves ? p * (dp - row.y) : 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -467,6 +463,15 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
         const int t = (t0 + ct) * BQ;
         if (++ct == per) ct = 0;
         const int p0 = s.past + t, p1 = p0 + BQ - 1;
+        // Queries that see one key become zeros: their score is 0, their weight
+        // exp2(0 - 0) = 1, and dK takes nothing from them, with no test per pair.
+        if (p0 <= 0 || a.W + a.S == 1) {
+            typedef SwaTile<E, D> TL;
+            for (int x = tid; x < BQ * TL::CPR; x += 256)
+                if (swa_alone(p0 + x / TL::CPR, a.W, a.S))
+                    *reinterpret_cast<Frag*>(sm.q[i & 1] + x * TL::EPC) = swa_zero<E>();
+            __syncthreads();
+        }
         if (!(p1 < wk0 || (p0 - wk1 >= a.W && wk0 >= a.S))) {
             const bool full = p0 >= wk1 && (p1 - wk0 < a.W || wk1 < a.S) && t + BQ <= t1;   // (rows from t1 on: the sinks' pass)
 #pragma unroll
