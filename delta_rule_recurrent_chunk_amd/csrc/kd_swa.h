@@ -27,8 +27,9 @@ struct SwaArgs {
     float* lse;                        // [B, Hq, Tq] or null
     const void* dO;                    // [B, Tq, Hq, d]
     float2* rows;                      // [B, Hq, Tq]: lse log2(e) and delta of every query
-    float* part;                       // partial dK, dV of the sinks
+    float* part;                       // partial dK, dV of the sinks: [B, pslots, Hq, 2, S, d]
     int pslots, chunk;                 // query chunks of the sinks' pass (0: none), their rows
+    int apart;                         // packed: rows by which that pass numbers its sequences (0: one by one)
     float* shared;                     // parts of dK, dV of the workgroups that share a group's heads
     int nsp;                           // how many do
     void *dq, *dk, *dv;                // contiguous
@@ -159,13 +160,19 @@ __device__ __forceinline__ float swa_swap(float x) { return __shfl_xor(x, 32); }
 // Sequence and block of a workgroup.  Batched: row block `slot` of batch
 // element b.  Packed: sequence s owns the slots cu[s] / R + s onwards (at
 // least as many as its blocks of R rows, and no two sequences share one), so
-// the grid needs T / R + N slots and no table.  Offsets are clamped into
-// [0, T].  Returns false when the slot holds no rows.
+// the grid needs T / R + N slots and no table.  Where only sequences of at
+// least `apart` rows have work, cu[s] / R + cu[s] / apart serves them as well
+// (one that starts after such a sequence starts at least `apart` rows later):
+// T / R + T / apart slots, however many short sequences there are.  Offsets
+// are clamped into [0, T].  Returns false when the slot holds no rows.
 struct SwaSeq {
     int q0, nq, nk, past, blk;   // first row, rows, keys, position of row 0, block of R rows
     int slot0;                   // the sequence's first chunk of the sinks' pass
 };
-__device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bool keys, SwaSeq& s) {
+__device__ __forceinline__ int swa_first_slot(int row, int seq, int R, int apart) {
+    return row / R + (apart > 0 ? row / apart : seq);
+}
+__device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bool keys, SwaSeq& s, int apart = 0) {
     if (!a.cu) {
         s.q0 = 0;
         s.nq = a.Tq;
@@ -179,7 +186,7 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     int n = 0;   // sequences that start at or before the slot
     for (int i = 0; i < a.N; i += 64) {
         const int at = i + lane;
-        const bool in = at < a.N && min(max(a.cu[min(at, a.N)], 0), a.Tq) / R + at <= slot;
+        const bool in = at < a.N && swa_first_slot(min(max(a.cu[min(at, a.N)], 0), a.Tq), at, R, apart) <= slot;
         n += __popcll(__ballot(in));
     }
     if (n == 0) return false;
@@ -188,8 +195,8 @@ __device__ __forceinline__ bool swa_locate(const SwaArgs& a, int slot, int R, bo
     s.q0 = lo;
     s.nq = s.nk = hi - lo;
     s.past = 0;
-    s.blk = slot - (lo / R + q);
-    s.slot0 = a.chunk > 0 ? lo / a.chunk + q : 0;
+    s.blk = slot - swa_first_slot(lo, q, R, apart);
+    s.slot0 = a.chunk > 0 ? swa_first_slot(lo, q, a.chunk, a.apart) : 0;
     return s.blk >= 0 && (int64_t)s.blk * R < s.nq;
 }
 

@@ -490,16 +490,16 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
     if (s.blk == 0 && a.pslots > 0 && swa_far(a, s.past) < s.nq) {
         const int first = s.slot0 + swa_far(a, s.past) / a.chunk, last = s.slot0 + (s.nq - 1) / a.chunk;
         float* sum = reinterpret_cast<float*>(&sm);
-        const int64_t step = (int64_t)a.Hq * 2 * SWA_MAX_SINKS * D;      // floats of one chunk
+        const int64_t step = (int64_t)a.Hq * 2 * a.S * D;      // floats of one chunk
         for (int x = 0; x < 2; ++x) {
-            const float* pb = a.part + ((int64_t)b * a.pslots + first) * step + ((int64_t)(hk * G + g0) * 2 + x) * SWA_MAX_SINKS * D;
+            const float* pb = a.part + ((int64_t)b * a.pslots + first) * step + ((int64_t)(hk * G + g0) * 2 + x) * a.S * D;
             __syncthreads();
             for (int i = tid; i < a.S * D / 4; i += 256) {
                 floatx4 z = {0.f, 0.f, 0.f, 0.f};
                 for (int y = 0; y <= last - first; ++y)
 #pragma unroll 4
                     for (int hg = 0; hg < GS; ++hg)
-                        z += reinterpret_cast<const floatx4*>(pb + y * step + (int64_t)hg * 2 * SWA_MAX_SINKS * D)[i];
+                        z += reinterpret_cast<const floatx4*>(pb + y * step + (int64_t)hg * 2 * a.S * D)[i];
                 reinterpret_cast<floatx4*>(sum)[i] = z;
             }
             __syncthreads();
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
     const int ng = (a.S + 31) / 32;
     const int slot = blockIdx.x / ng, k0 = blockIdx.x % ng * 32, h = blockIdx.y, hk = h / (a.Hq / a.Hkv), b = blockIdx.z;
     SwaSeq s;
-    if (!swa_locate(a, slot, a.chunk, false, s)) return;
+    if (!swa_locate(a, slot, a.chunk, false, s, a.apart)) return;
     const int ta = max(s.blk * a.chunk, swa_far(a, s.past)), tb = min(s.blk * a.chunk + a.chunk, s.nq);
     if (ta >= tb) return;
     const int key = k0 + (lane & 31), kc = min(key, s.nk - 1);
@@ -609,7 +609,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
     __syncthreads();
     constexpr int DP = D + 4;                        // (a row's stride: the lanes' rows start in different banks)
     float* sum = reinterpret_cast<float*>(&sm);      // 32 keys by D, dK then dV
-    float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hq + h) * 2 * SWA_MAX_SINKS + k0) * D;
+    float* out = a.part + ((((int64_t)b * a.pslots + slot) * a.Hq + h) * 2 * a.S + k0) * D;
     for (int x = 0; x < 2; ++x) {
         for (int y = 0; y < NW; ++y) {
             if (w == y && key < a.S) {
@@ -627,7 +627,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
             __syncthreads();
         }
         for (int i = tid; i < min(32, a.S - k0) * D / 4; i += 64 * NW)
-            reinterpret_cast<floatx4*>(out + x * SWA_MAX_SINKS * D)[i] =
+            reinterpret_cast<floatx4*>(out + x * a.S * D)[i] =
                 *reinterpret_cast<const floatx4*>(sum + i / (D / 4) * DP + i % (D / 4) * 4);
         __syncthreads();
     }
@@ -642,15 +642,25 @@ static int swa_chunk(int64_t rows, int Hq, int S) {
     return (int)min((int64_t)4096, max((int64_t)256, (n + 127) / 128 * 128));
 }
 
+// Rows by which the sinks' pass numbers packed sequences: those of 128 + W rows
+// or more have queries beyond the window of their first 128 keys.  0 (one by
+// one) where that needs fewer slots.
+static int swa_apart(bool packed, int N, int T, int W) {
+    const int64_t least = 128 + (int64_t)W;
+    return packed && T / least < N ? (int)min(least, (int64_t)INT32_MAX) : 0;
+}
+
 // Chunks of the sinks' partial sums; none where every query lies within the
 // window of the first 128 keys.
 static int64_t swa_part_slots(bool packed, int N, int Tq, int Tk, int W, int S, int chunk) {
-    return S > 0 && Tk > 127 + (int64_t)W && Tq > 0 ? swa_slots(packed, N, Tq, chunk) : 0;
+    if (S == 0 || Tq == 0 || Tk <= 127 + (int64_t)W) return 0;
+    const int apart = swa_apart(packed, N, Tq, W);
+    return swa_slots(packed, apart > 0 ? Tq / apart : N, Tq, chunk);
 }
 
 static size_t swa_rows_bytes(int B, int Tq, int Hq) { return ((size_t)B * Tq * Hq * 8 + 255) & ~(size_t)255; }
 
-static size_t swa_part_bytes(int64_t slots, int B, int Hq, int d) { return (size_t)slots * B * Hq * 2 * SWA_MAX_SINKS * d * 4; }
+static size_t swa_part_bytes(int64_t slots, int B, int Hq, int S, int d) { return (size_t)slots * B * Hq * 2 * S * d * 4; }
 
 // Workgroups that share the heads of a group in the dK/dV pass: so that there
 // is one for each of the chip's 256 compute units, or two where a group's rows
@@ -671,7 +681,7 @@ static int swa_head_splits(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, 
 size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {
     const int nb = packed ? 1 : B, nsp = swa_head_splits(packed, B, Tq, Tk, Hq, Hkv, W);
     return swa_rows_bytes(nb, Tq, Hq) +
-           swa_part_bytes(swa_part_slots(packed, B, Tq, Tk, W, S, swa_chunk((int64_t)nb * Tq, Hq, S)), nb, Hq, d) +
+           swa_part_bytes(swa_part_slots(packed, B, Tq, Tk, W, S, swa_chunk((int64_t)nb * Tq, Hq, S)), nb, Hq, S, d) +
            (nsp > 1 ? (size_t)nsp * 2 * B * Tk * Hkv * d * 4 : 0);
 }
 
@@ -686,10 +696,11 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     a.chunk = swa_chunk((int64_t)a.B * a.Tq, a.Hq, a.S);
     const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S, a.chunk);
     if (gq > INT32_MAX || gk > INT32_MAX || np > INT32_MAX / 2) return hipErrorInvalidValue;
+    a.apart = swa_apart(a.cu, a.N, a.Tq, a.W);
     a.rows = (float2*)ws;
     a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));
     a.pslots = (int)np;
-    a.shared = (float*)((char*)a.part + swa_part_bytes(np, a.B, a.Hq, D));
+    a.shared = (float*)((char*)a.part + swa_part_bytes(np, a.B, a.Hq, a.S, D));
     if (a.Tq > 0) {
         kd_swa_dq_kernel<E, D, BN><<<(unsigned)gq, 256, 0, st>>>(a, (int)nq);
         const hipError_t e = hipGetLastError();

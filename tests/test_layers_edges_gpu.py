@@ -54,3 +54,37 @@ def test_queries_of_one_key_in_batches(Tq, Tk, Hq, Hkv, window, sinks, d, dtype)
         val, err = R.attention_heads(qv[b], kv[b], vv[b], window, sinks, 1 / np.sqrt(d), ov[b], R.unit(dtype))
         for n in ("dq", "dk", "dv"):
             check(n, g[n][b], val[n], err[n])
+
+
+# ------------------------------------------------------- many packed sequences
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,window,sinks", [([3] * 200 + [900] + [7] * 60 + [400] + [1] * 90 + [300, 128, 700], 60, 5),
+                                               ([300] * 9, 30, 64), ([187, 188, 189, 0, 0, 600, 1, 188] * 3, 60, 33), ([2600, 200, 1], 1, 1)])
+def test_many_packed_sequences_equal_each_alone(lens, window, sinks, dtype):
+    """Sequences with queries beyond the window of the first keys among others without; nothing behind the workspace
+    is written, nothing in it is read that was not written."""
+    import ctypes
+
+    import delta_rule_recurrent_chunk_amd as kd
+    from delta_rule_recurrent_chunk_amd import layers as la
+    torch = _torch()
+    T, Hq, Hkv, d = sum(lens), 4, 2, 64
+    print("case", lens[:8], window, sinks, dtype, flush=True)
+    (q, _), (k, _), (v, _), (dO, _) = swa_inputs(1, T, T, Hq, Hkv, d, dtype, T)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    o, lse = kd.swa_fwd(q[0], k[0], v[0], window, sinks, cu_seqlens=cu, return_lse=True)
+    _, desc, *_ = la._swa(q[0], k[0], v[0], window, sinks, None, cu)
+    need = kd.lib().kron_delta_swa_workspace_bytes(ctypes.byref(desc), 1)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    g = kd.swa_bwd(q[0], k[0], v[0], o, lse, dO[0], window, sinks, cu_seqlens=cu, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 255).all()
+    a = 0
+    for n in lens:
+        s = slice(a, a + n)
+        a += n
+        if n < 100 and a > 200:
+            continue
+        oo, ll = kd.swa_fwd(q[:, s], k[:, s], v[:, s], window, sinks, return_lse=True)
+        gg = kd.swa_bwd(q[:, s], k[:, s], v[:, s], oo, ll, dO[:, s], window, sinks)
+        assert torch.equal(o[s], oo[0]) and all(torch.equal(g[m][s], gg[m][0]) for m in g), n
