@@ -51,6 +51,56 @@ __device__ __forceinline__ int swa_slot(const Seen& s, int j, int S, int cap) {
     return x < cap ? x : x - (cap - S);
 }
 
+// A split's maxima, sums and o in plain fp32 (rare, see its call), head by
+// head, 128 keys j0 .. j1 - 1 at a time: a thread makes the score of one key,
+// then sums one element over all of them.  The results go where the first
+// wave's were, the second's become those of no keys.  Every thread calls it.
+template <class E, int D, class Q>
+__device__ __forceinline__ void swa_decode_plain(const SwaDecodeArgs& a, const Seen& se, int j0, int j1, int nh, const E* kc,
+                                                 const E* vc, Q&& q, float* accs, float (*ms)[32], float (*ls)[32],
+                                                 float* sc, int tid)
+{
+    float* const qh = accs + 32 * D;
+#pragma unroll 1
+    for (int h = 0; h < nh; ++h) {
+        __syncthreads();
+        if (tid < D) qh[tid] = q(h, tid);
+        float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 1
+        for (int j = j0; j < j1; j += 128) {
+            const int n = min(128, j1 - j);
+            __syncthreads();
+            if (tid < n) {
+                const E* k = kc + swa_slot(se, j + tid, a.S, a.cap) * a.kcs[1];
+                float s = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < D; ++i) s = fmaf(qh[i], (float)k[i], s);
+                sc[tid] = s;
+            }
+            __syncthreads();
+            float mx = m;
+#pragma unroll 1
+            for (int x = 0; x < n; ++x) mx = fmaxf(mx, sc[x]);
+            const float mu = mx == -INFINITY ? 0.f : mx, f = __builtin_amdgcn_exp2f(m - mu);
+            m = mx;
+            l *= f;
+            o = o == 0.f ? 0.f : o * f;
+#pragma unroll 8
+            for (int x = 0; x < n; ++x) {
+                const float p = __builtin_amdgcn_exp2f(sc[x] - mu);
+                l += p;
+                if (tid < D) o = fmaf(p, (float)vc[swa_slot(se, j + x, a.S, a.cap) * a.vcs[1] + tid], o);
+            }
+        }
+        if (tid < D) accs[h * D + tid] = o;
+        if (tid == 0) ms[0][h] = m, ls[0][h] = l, ms[1][h] = -INFINITY, ls[1][h] = 0.f;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < 32 * D; i += 128) qh[i] = 0.f;
+    __syncthreads();
+}
+
 template <class E, int D, int N>
 __device__ __forceinline__ void swa_join(const float* pb, int64_t pstep, int nsplit, int nh,
                                          const float (*mw)[SWA_DECODE_SPLITS + 1], const float* wl, E* o, int tid) {
@@ -84,7 +134,7 @@ __device__ __forceinline__ void swa_join(const float* pb, int64_t pstep, int nsp
 //
 // Bound by reading the caches: 32 sequences of up to 2052 keys, 4 key heads of
 // 128, bf16 (119 MB): 34 us, 3.5 TB/s (row by row on vector units: 62 us).  One
-// sequence of 1500: 14 us, a chain of dependent reads (length, keys, partial
+// sequence of 1500: 14.4 us, a chain of dependent reads (length, keys, partial
 // results, join).  32 keys a tile: the matrix tile's edge, and 64 KB of LDS for
 // two waves with a tile ahead.
 template <class E, int D>
@@ -105,7 +155,7 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
         float kr[D], kn[D], vn[D];      // the new key as given and as the cache holds it, the new value
         float2 cs[D / 2];
         float ms[3][32], ls[3][32], mw[32][SWA_DECODE_SPLITS + 1], wl[32];
-        int last;
+        int last, again;
     } sm;
     auto& kv = sm.kv;
     auto& cs = sm.cs;
@@ -166,13 +216,14 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
 
     // queries (turned, times scale log2 e), and where they are needed the new key and value
     if (tid < n) cs[tid] = rope_cs((double)pos, fr, a.rope_scale, 0);
+    if (tid == 0) sm.again = 0;
     __syncthreads();
-    auto turned = [&](const float* row, int i) -> float {
-        const float x = row[i];
+    auto turned = [&](const auto* row, int i) -> float {
+        const float x = (float)row[i];
         if (i >= a.rot) return x;
         const int j = a.interleaved ? i / 2 : i < n ? i : i - n;
         const bool second = a.interleaved ? (i & 1) : i >= n;
-        const float y = row[a.interleaved ? i ^ 1 : second ? i - n : i + n];
+        const float y = (float)row[a.interleaved ? i ^ 1 : second ? i - n : i + n];
         return second ? fmaf(x, cs[j].x, y * cs[j].y) : fmaf(x, cs[j].x, -y * cs[j].y);
     };
     for (int i = tid; i < nh * D; i += 128) qs[i] = turned(raw + i / D * D, i % D) * a.c;
@@ -273,7 +324,13 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
     // the two waves' and the new token's results; head h of wave x at part[x][h]
     __syncthreads();
     float* const accs = reinterpret_cast<float*>(kv);      // [2][32][D]
+    floatx4 zero = {0.f, 0.f, 0.f, 0.f};      // (0 times what is not finite is a NaN)
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) zero[r % 4] = fmaf(acc[i][r], 0.f, zero[r % 4]);
     if ((lane & 31) < nh) {
+        if (!(zero[0] + zero[1] + (zero[2] + zero[3]) == 0.f)) sm.again = 1;
 #pragma unroll
         for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -285,7 +342,13 @@ __global__ __launch_bounds__(128, 1) void kd_swa_decode_kernel(SwaDecodeArgs a)
             ls[w][lane & 31] = l;
         }
     }
+    // An infinity that is seen becomes a NaN above: a remainder's product has
+    // another sign or is 0 times it, and so is a row that fills up the last
+    // tile.  A split with a result that is not finite makes all of it again.
     __syncthreads();
+    if (sm.again)
+        swa_decode_plain<E, D>(a, se, ta * 32, min(tb * 32, se.nv), nh, kc, vc, [&](int h, int i) { return turned(qrow + h * D, i) * a.c; },
+                               accs, ms, ls, reinterpret_cast<float*>(sm.mw), tid);
     const int64_t item = (int64_t)b * gridDim.y + blockIdx.y;
     const int64_t pstep = (int64_t)32 * (D + 2);
     float* part = a.part + (item * a.nsplit + sp) * pstep;

@@ -550,7 +550,8 @@ KD_API kd_status kron_delta_swa_bwd(const kd_swa_desc *desc, const int32_t *cu_s
  *   3. o = attention of q over the visible positions, the new one included.
  *  * q [B, Hq, d], k, v [B, Hkv, d]: heads contiguous, batch strides (elements)
  *    in in_stride (q, k, v); o [B, Hq, d] contiguous.  lens is read on the
- *    device and not changed.
+ *    device and not changed.  Infinities and NaNs in what a query sees show as
+ *    in kron_delta_swa_fwd; what it does not see may hold any.
  *  * ws: kron_delta_swa_decode_workspace_bytes(desc) bytes whose contents are
  *    zero before the first call; every call leaves it ready for the next one
  *    of the same descriptor or any other that it is large enough for.  Calls

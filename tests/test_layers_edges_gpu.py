@@ -88,3 +88,69 @@ def test_many_packed_sequences_equal_each_alone(lens, window, sinks, dtype):
         oo, ll = kd.swa_fwd(q[:, s], k[:, s], v[:, s], window, sinks, return_lse=True)
         gg = kd.swa_bwd(q[:, s], k[:, s], v[:, s], oo, ll, dO[:, s], window, sinks)
         assert torch.equal(o[s], oo[0]) and all(torch.equal(g[m][s], gg[m][0]) for m in g), n
+
+
+# ------------------------------------------------- infinities that are seen
+def softmax_of(s, v):
+    """softmax(s) v over the last axis of s [H, n] with v [n, H, d], infinities and NaNs as IEEE arithmetic has them."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        m = s.max(1, keepdims=True)
+        p = np.exp(s - m)
+        return np.einsum("hn,nhd->hd", p, v) / p.sum(1)[:, None]
+
+
+def same_but_for(name, got, ref, tol):
+    got = host(got)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), (name, np.isnan(got).sum(), np.isnan(ref).sum())
+    inf = np.isinf(ref)
+    assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], ref[inf]), name
+    ok = np.isfinite(ref)
+    check(name, got[ok], ref[ok], np.broadcast_to(tol, ref.shape)[ok])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks,p", [(4, 2, 64, 40, 2, 33), (8, 1, 128, 300, 4, 500), (3, 1, 32, 64, 0, 63), (6, 2, 128, 32, 1, 32),
+                                                     (40, 1, 64, 70, 3, 90), (2, 1, 128, 2048, 4, 5000)])
+def test_decoding_keeps_the_infinities_it_sees(Hq, Hkv, d, window, sinks, p, dtype):
+    """An infinite value is an infinite output, an infinite key a weight of 0 or a NaN, as in the prompt's pass:
+    remainders of roundings and the rows that fill a tile up make nothing else of them."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    r = np.random.default_rng(p)
+    cap, inf = window + sinks, float("inf")
+    seen = R.seen(p, window, sinks)
+    (q, qv), (kn, _), (vn, _) = (dev(r.standard_normal((1, h, d)), dtype) for h in (Hq, Hkv, Hkv))
+    (k, kv), (v, vv) = (dev(r.standard_normal((len(seen), Hkv, d)), dtype) for _ in range(2))
+    lens = torch.tensor([p], dtype=torch.int32, device="cuda")
+    at = torch.tensor([R.slot(s, sinks, cap) for s in seen], device="cuda")
+    scale, G = 1 / np.sqrt(d), Hq // Hkv
+    n = len(seen)
+    for which, where, value in (("v", 0, inf), ("v", n - 2, -inf), ("v", n - 1, inf), ("v", n // 2, float("nan")), ("k", 0, inf),
+                                ("k", n - 2, -inf), ("k", n - 1, inf), ("k", n // 2, inf), ("kv", n - 2, inf)):
+        print("case", (Hq, Hkv, d, window, sinks, p), dtype, which, where, value, flush=True)
+        k2, v2, kv2, vv2 = k.clone(), v.clone(), kv.copy(), vv.copy()
+        if "v" in which:
+            v2[where, 0, 3::7], vv2[where, 0, 3::7] = value, value
+        if "k" in which:
+            k2[where, 0, 5], kv2[where, 0, 5] = value, value
+        kc, vc = (torch.zeros(1, cap, Hkv, d, dtype=q.dtype, device="cuda") for _ in range(2))
+        kc[0, at[:-1]], vc[0, at[:-1]] = k2[:-1], v2[:-1]
+        o = kd.swa_decode(q, k2[-1:], v2[-1:], kc, vc, lens, window, sinks)
+        kk, vs = np.repeat(kv2, G, 1), np.repeat(vv2, G, 1)
+        with np.errstate(invalid="ignore"):
+            s = scale * np.einsum("hd,nhd->hn", qv[0], kk)
+        ref = softmax_of(s, vs)
+        # bounds: the weights of the finite scores, as in attention()
+        fin = np.where(np.isfinite(s), s, -1e30)
+        P = np.exp(fin - fin.max(1, keepdims=True))
+        P /= P.sum(1)[:, None]
+        av = np.where(np.isfinite(vs), np.abs(vs), 0)
+        smax = np.abs(s[np.isfinite(s)]).max()
+        absk = np.where(np.isfinite(kk), np.abs(kk), 0)
+        ds = 2 * R.W * (d * np.einsum("hd,nhd->hn", np.abs(qv[0]), absk).max() * scale + 8 * smax + 8)
+        with np.errstate(invalid="ignore"):
+            tol = (R.unit(dtype) + 2 * ds + n * R.W) * np.einsum("hn,nhd->hd", P, av) + R.unit(dtype) * np.abs(ref)
+        same_but_for("o", o[0], ref, tol)
+        # the prompt's pass over the same keys, the query last
+        w = kd.swa_fwd(q[None], k2[None], v2[None], n, 0)
+        same_but_for("prompt", w[0, 0], ref, tol)
