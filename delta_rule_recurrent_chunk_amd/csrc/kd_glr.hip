@@ -95,6 +95,40 @@ __device__ __forceinline__ void glr_fresh(V& v) {
     }
 }
 
+// A product of gates over a run of tokens.  One that falls below fp32's range
+// becomes the smallest number (a step of rounding there), so that 0 still says
+// that a gate was 0: an infinite carried value survives every gate but that
+// one, where it becomes a NaN, as it does token by token.
+__device__ __forceinline__ float glr_least(float a) {
+    return a == 0.f ? copysignf(1.401298464324817e-45f, a) : a;      // 2^-149
+}
+// the products A of a thread's own tokens
+template <class V, int TOK, int VEC>
+__device__ __forceinline__ void glr_own_gates(float (&A)[VEC], const V (&f)[TOK]) {
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) any |= A[e] == 0.f;
+    if (!any) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        bool zero = false;
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) zero |= glr_at(f[t], e) == 0.f;
+        if (!zero) A[e] = glr_least(A[e]);
+    }
+}
+// pa, the product of GROUPS rows' gates, and those in front of each row, p:
+// the first `rows` of them (in the order of `down`) have no 0 in them
+template <int GROUPS, int CW>
+__device__ __forceinline__ void glr_row_gates(float& pa, float (*p)[CW], int c, int rows, bool down) {
+    if (pa != 0.f) return;
+    for (int r = 0; r <= min(rows, GROUPS - 1); ++r) {
+        float& x = p[down ? GROUPS - 1 - r : r][c];
+        x = glr_least(x);
+    }
+    if (rows == GROUPS) pa = glr_least(pa);
+}
+
 __device__ __forceinline__ u64 glr_pair(float a, float b) {
     unsigned x = __float_as_uint(a);
     if (x == 0xffffffffu) x = 0x7fc00000u;      // a NaN either way; all ones means empty
@@ -195,6 +229,7 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_fwd_kernel(GlrArgs p)
             Bh[e] = fmaf(ff, Bh[e], u);
             A[e] *= ff;
         }
+    glr_own_gates(A, f);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         sA[g][cl + e] = A[e];
@@ -204,6 +239,7 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_fwd_kernel(GlrArgs p)
     if (tid < CW && c0 + tid < p.D) {
         // the rows' entering (A, B), then the tile's
         float pa = 1.f, pb = 0.f;
+        int rows = GROUPS;      // those in front of the first with a gate of 0
 #pragma unroll
         for (int r = 0; r < GROUPS; ++r) {
             const float a = sA[r][tid], bb = sB[r][tid];
@@ -211,7 +247,9 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_fwd_kernel(GlrArgs p)
             sB[r][tid] = pb;
             pb = fmaf(a, pb, bb);
             pa *= a;
+            rows = a == 0.f ? min(rows, r) : rows;
         }
+        glr_row_gates<GROUPS>(pa, sA, tid, rows, false);
         const int64_t ch = (int64_t)b * p.D + c0 + tid, step = (int64_t)p.B * p.D, w = n * step + ch;
         float c;
         if (n == 0) {
@@ -293,6 +331,7 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_bwd_kernel(GlrArgs p)
     for (int t = TOK - 1; t >= 0; --t)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) Bm[e] = glr_at(f[t], e) * (glr_at(d[t], e) + Bm[e]);
+    glr_own_gates(A, f);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
         sA[g][cl + e] = A[e];
@@ -303,6 +342,7 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_bwd_kernel(GlrArgs p)
     const int64_t step = (int64_t)p.B * p.D;
     if (tid < CW && c0 + tid < p.D) {
         float pa = 1.f, pm = 0.f;
+        int rows = GROUPS;      // those behind the last with a gate of 0
 #pragma unroll
         for (int q = GROUPS - 1; q >= 0; --q) {
             const float a = sA[q][tid], m = sM[q][tid];
@@ -310,7 +350,9 @@ __global__ __launch_bounds__(GLR_NT) void kd_glr_bwd_kernel(GlrArgs p)
             sM[q][tid] = pm;
             pm = fmaf(a, pm, m);
             pa *= a;
+            rows = a == 0.f ? min(rows, GROUPS - 1 - q) : rows;
         }
+        glr_row_gates<GROUPS>(pa, sP, tid, rows, true);
         const int64_t ch = (int64_t)b * p.D + c0 + tid, w = n * step + ch;
         float c;
         if (r == 0) {

@@ -154,3 +154,57 @@ def test_decoding_keeps_the_infinities_it_sees(Hq, Hkv, d, window, sinks, p, dty
         # the prompt's pass over the same keys, the query last
         w = kd.swa_fwd(q[None], k2[None], v2[None], n, 0)
         same_but_for("prompt", w[0, 0], ref, tol)
+
+
+def glr_loop(x, f, i, h0):
+    with np.errstate(invalid="ignore"):
+        return R.glr(x, f, i, h0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,D", [(100, 9), (700, 12), (700, 9), (2000, 12)])
+@pytest.mark.parametrize("gate", [True, False])
+def test_glr_infinities_and_nans(gate, T, D, dtype):
+    """As the recurrence has them token by token: an infinite state stays one through any product of gates that is
+    not 0 (over a tile the product is below fp32's range here), and a gate of 0 makes it a NaN."""
+    import delta_rule_recurrent_chunk_amd as kd
+    _torch()
+    print("case", gate, (T, D), dtype, flush=True)
+    r = np.random.default_rng(T + D)
+    inf, nan = float("inf"), float("nan")
+    c = dict(x=r.standard_normal((2, T, D)), f=r.uniform(0.2, 0.5, (2, T, D)), i=r.uniform(0.1, 1, (2, T, D)), dh=r.standard_normal((2, T, D)))
+    s = dict(h0=r.standard_normal((2, D)), dhT=r.standard_normal((2, D)))
+    clean = {n: a.copy() for n, a in {**c, **s}.items()}
+    s["h0"][:, 0], s["h0"][:, 1], s["h0"][:, 4], s["h0"][:, 6] = inf, -inf, inf, -inf
+    c["x"][:, T // 3, 2], c["x"][:, T // 4, 3] = inf, nan
+    for a in (c, clean):
+        a["f"][:, T // 2, 4:6] = 0
+        a["f"][:, 16:20, 6] = a["f"][:, T - 20:T - 16, 8] = 1e-30       # a few tokens' product below fp32's range
+    s["dhT"][:, 0], s["dhT"][:, 3], s["dhT"][:, 5], s["dhT"][:, 8] = inf, -inf, -inf, inf
+    c["dh"][:, 2 * T // 3, 7], c["dh"][:, 2 * T // 3, 1] = -inf, nan
+    t, v, e = {}, {}, {}
+    for n in c:
+        t[n], v[n] = dev(c[n], dtype)
+        e[n] = dev(clean[n], dtype)[1]
+    for n in s:
+        t[n], v[n] = dev(s[n], "fp32")
+        e[n] = dev(clean[n], "fp32")[1]
+    if not gate:
+        t["i"] = v["i"] = e["i"] = None
+    h, hT, hs = kd.glr_fwd(t["x"], t["f"], t["i"], t["h0"], save_states=True)
+    g = kd.glr_bwd(t["x"], t["f"], t["i"], hs, t["dh"], t["dhT"])
+    ref = glr_loop(v["x"], v["f"], v["i"], v["h0"])
+    with np.errstate(invalid="ignore"):
+        _, dx, df, di, dh0 = R.glr_bwd(v["x"], v["f"], v["i"], ref, v["dh"], v["dhT"])
+    eh, eg, H, G = R.glr_bounds(e["x"], e["f"], e["i"], e["h0"], e["dh"], e["dhT"])
+    u, a = R.unit(dtype), np.abs
+    with np.errstate(invalid="ignore"):
+        same_but_for("h", h, ref[:, 1:], eh[:, 1:] + u * a(ref[:, 1:]) * 1.01)
+        same_but_for("hT", hT, ref[:, -1], eh[:, -1])
+        same_but_for("hs", hs, ref[:, :-1][:, ::128], eh[:, :-1][:, ::128])
+        i = 1.0 if v["i"] is None else a(v["i"])
+        same_but_for("dx", g["dx"], dx, 1.01 * (i * eg + (u + R.W) * a(dx)))
+        same_but_for("df", g["df"], df, 1.01 * (G * eh[:, :-1] + (H[:, :-1] + eh[:, :-1]) * eg + (u + R.W) * a(df)))
+        if gate:
+            same_but_for("di", g["di"], di, 1.01 * (a(v["x"]) * eg + (u + R.W) * a(di)))
+        same_but_for("dh0", g["dh0"], dh0, 1.01 * (a(v["f"][:, 0]) * eg[:, 0] + 140 * R.W * a(v["f"][:, 0]) * G[:, 0]))
