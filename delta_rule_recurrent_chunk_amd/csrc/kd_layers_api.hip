@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "kd_check.h"
 #include "kd_rope.h"
 #include "kd_swa.h"
@@ -192,14 +194,31 @@ kd_status kron_delta_glr_step(const kd_glr_desc* d, const void* x, const void* f
 }
 
 // ---------------------------------------------------------- rotary positions
-// Whether the heads of q_out and k_out, which share batch and token strides,
-// lie apart within a token's row: k_out starts `gap` elements after q_out.
-static bool rope_heads_apart(const kd_rope_desc* d, int64_t gap) {
-    if (d->Hk == 0) return true;
-    const int64_t eq = d->q_out_stride[2] * (d->Hq - 1) + d->d, ek = d->k_out_stride[2] * (d->Hk - 1) + d->d;
-    const int64_t st = d->T > 1 ? d->q_out_stride[1] : d->B > 1 ? d->q_out_stride[0] : INT64_MAX;
-    const int64_t bs = d->B > 1 ? d->q_out_stride[0] : INT64_MAX, row = st < bs ? st : bs;
-    return gap >= 0 ? gap >= eq && gap <= row - ek : -gap >= ek && -gap <= row - eq;
+// One of the tensors of a rotation, as its address, strides, heads and span.
+struct RopeHeads {
+    const void* p;
+    const int64_t* st;
+    int heads;
+    size_t bytes;
+};
+
+// Whether two of them share no address: apart in memory, or different heads of
+// one tensor with the batch and token strides of both, in any order.  The
+// heads of both then lie in one block per token, or go on from one to the
+// other in steps of the head stride.
+static bool rope_apart(const kd_rope_desc* d, RopeHeads a, RopeHeads b, int64_t es) {
+    if (a.heads == 0 || b.heads == 0 || !overlap(range_of(a.p, a.bytes), range_of(b.p, b.bytes))) return true;
+    if ((d->B > 1 && a.st[0] != b.st[0]) || (d->T > 1 && a.st[1] != b.st[1])) return false;
+    if ((const char*)a.p > (const char*)b.p) std::swap(a, b);
+    const int64_t bytes = (const char*)b.p - (const char*)a.p, gap = bytes / es;
+    if (bytes % es != 0) return false;
+    const int64_t block[3] = {a.st[0], a.st[1], 0};
+    const __int128 ea = (__int128)a.st[2] * (a.heads - 1) + d->d, eb = (__int128)b.st[2] * (b.heads - 1) + d->d;
+    if (gap >= ea && gap + eb < INT64_MAX && distinct(block, d->B, d->T, 1, (int64_t)(gap + eb))) return true;
+    const int64_t step = a.heads > 1 ? a.st[2] : b.heads > 1 ? b.st[2] : gap;
+    if (step <= 0 || gap % step != 0 || gap / step < a.heads || (a.heads > 1 && b.heads > 1 && a.st[2] != b.st[2])) return false;
+    const int64_t all[3] = {a.st[0], a.st[1], step};
+    return distinct(all, d->B, d->T, gap / step + b.heads, d->d);
 }
 
 kd_status kron_delta_rope(const kd_rope_desc* d, const void* q, const void* k, const void* pos, const double* freqs,
@@ -231,18 +250,16 @@ kd_status kron_delta_rope(const kd_rope_desc* d, const void* q, const void* k, c
                     d->q_stride[2] == d->q_out_stride[2];
     const bool sk = k == k_out && d->k_stride[0] == d->k_out_stride[0] && d->k_stride[1] == d->k_out_stride[1] &&
                     d->k_stride[2] == d->k_out_stride[2];
-    const Range rq = range_of(q, qi), rk = range_of(k, ki), oq = range_of(q_out, qo), ok = range_of(k_out, ko);
     const Range rp = range_of(pos, (size_t)(d->pos_batched ? ntok : d->T) * (d->pos64 ? 8 : 4));
     const Range rf = range_of(freqs, (size_t)(d->rot / 2) * 8);
-    // q and k (in or out) may be the heads of one fused tensor
-    const int64_t gap = ((const char*)k_out - (const char*)q_out) / (int64_t)es;
-    const bool heads_apart = d->q_out_stride[0] == d->k_out_stride[0] && d->q_out_stride[1] == d->k_out_stride[1] &&
-                             rope_heads_apart(d, gap);
-    const bool same_fused = sq && sk && heads_apart;
-    if (!same_fused && ((overlap(oq, ok) && !heads_apart) || overlap(oq, rk) || overlap(ok, rq))) return KD_ERR_ALIAS;
-    if ((!sq && overlap(oq, rq)) || (!sk && overlap(ok, rk)) || overlap(oq, rp) || overlap(oq, rf) || overlap(ok, rp) ||
-        overlap(ok, rf))
+    // q and k (in or out) may be the heads of one tensor
+    const RopeHeads hq = {q, d->q_stride, d->Hq, qi}, hk = {k, d->k_stride, d->Hk, ki};
+    const RopeHeads gq = {q_out, d->q_out_stride, d->Hq, qo}, gk = {k_out, d->k_out_stride, d->Hk, ko};
+    if (!rope_apart(d, gq, gk, es) || !rope_apart(d, gq, hk, es) || !rope_apart(d, gk, hq, es) ||
+        (!sq && !rope_apart(d, gq, hq, es)) || (!sk && !rope_apart(d, gk, hk, es)))
         return KD_ERR_ALIAS;
+    const Range oq = range_of(q_out, qo), ok = range_of(k_out, ko);
+    if (overlap(oq, rp) || overlap(oq, rf) || overlap(ok, rp) || overlap(ok, rf)) return KD_ERR_ALIAS;
     kd::RopeArgs a;
     a.side[0] = {q, q_out, {d->q_stride[0], d->q_stride[1], d->q_stride[2]},
                  {d->q_out_stride[0], d->q_out_stride[1], d->q_out_stride[2]}, d->Hq};

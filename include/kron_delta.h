@@ -462,7 +462,8 @@ KD_API kd_status kron_delta_glr_step(const kd_glr_desc *desc, const void *x, con
  *  * q, q_out: [B, T, Hq, d]; k, k_out: [B, T, Hk, d] (Hk = 0: no k) in
  *    desc->dtype, with strides over batch, token and head in elements and a
  *    contiguous last dimension.  An output may be its input (same strides);
- *    q and k may be the heads of one fused tensor.  d <= 256, rot even,
+ *    all four may be heads of one tensor, in any order of its dimensions, as
+ *    long as no two but an output and its own input hold the same.  d <= 256, rot even,
  *    Hq, Hk <= 32767, B T < 2^31.
  *  * pos: [T] or, with pos_batched, [B, T]; int32 or, with pos64, int64.
  *  * freqs: [rot/2] fp64, radians per position.  The angle is formed in fp64

@@ -208,3 +208,37 @@ def test_glr_infinities_and_nans(gate, T, D, dtype):
         if gate:
             same_but_for("di", g["di"], di, 1.01 * (a(v["x"]) * eg + (u + R.W) * a(di)))
         same_but_for("dh0", g["dh0"], dh0, 1.01 * (a(v["f"][:, 0]) * eg[:, 0] + 140 * R.W * a(v["f"][:, 0]) * G[:, 0]))
+
+
+# ------------------------------------------------------------- fused tensors
+@pytest.mark.parametrize("order", ["bthd", "bhtd", "tbhd"])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (1, 1), (3, 1), (1, 2)])
+def test_rope_in_place_on_heads_of_one_tensor_in_any_order(Hq, Hk, order):
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    B, T, d, H = 3, 6, 64, Hq + Hk + 2
+    perm = dict(bthd=(0, 1, 2, 3), bhtd=(0, 2, 1, 3), tbhd=(1, 0, 2, 3))[order]
+    base = torch.randn(B, T, H, d, device="cuda").to(torch.bfloat16)
+    qkv = base.permute(perm).contiguous().permute(perm)          # [B, T, H, d], in that order in memory
+    assert torch.equal(base, qkv)
+    freqs, _ = kd.rope_frequencies(32, device="cuda")
+    pos = torch.arange(T, device="cuda")
+    for qa, ka in ((0, Hq), (Hk, 0), (1, Hq + 1)):
+        x = torch.empty_strided(qkv.shape, qkv.stride(), dtype=qkv.dtype, device="cuda").copy_(qkv)
+        q, k = x[:, :, qa:qa + Hq], x[:, :, ka:ka + Hk]
+        rq, rk = kd.rope(q.contiguous(), k.contiguous(), pos, freqs)
+        # the queries alone in place; both in place
+        y = torch.empty_like(rk)
+        z = torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device="cuda").copy_(x)
+        kd.rope(z[:, :, qa:qa + Hq], z[:, :, ka:ka + Hk], pos, freqs, out=(z[:, :, qa:qa + Hq], y))
+        assert torch.equal(z[:, :, qa:qa + Hq], rq) and torch.equal(y, rk) and torch.equal(z[:, :, ka:ka + Hk], k)
+        kd.rope(q, k, pos, freqs, out=(q, k))
+        assert torch.equal(q, rq) and torch.equal(k, rk)
+        w = torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device="cuda").copy_(base)
+        kd.rope(w[:, :, :1], None, pos, freqs, out=(w[:, :, H - 1:], None))       # from one head to another
+        assert torch.equal(w[:, :, H - 1:], kd.rope(base[:, :, :1].contiguous(), None, pos, freqs)[0]) and torch.equal(w[:, :, :H - 1], base[:, :, :H - 1])
+        rest = [h for h in range(H) if not (qa <= h < qa + Hq or ka <= h < ka + Hk)]
+        assert torch.equal(x[:, :, rest], base[:, :, rest])
+    # heads that both hold are still refused
+    with pytest.raises(kd.KronDeltaError):
+        kd.rope(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk], pos, freqs, out=(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk]))

@@ -5,7 +5,7 @@ import pytest
 
 import delta_rule_recurrent_chunk_amd as kd
 from delta_rule_recurrent_chunk_amd import layers as la
-from tests.test_layers_abi import L, S3  # noqa: F401  (L is a fixture)
+from tests.test_layers_abi import ALIAS, L, P, S3  # noqa: F401  (L is a fixture)
 
 
 def swa(B, T, Hq, Hkv, d, window, sinks, dtype=1):
@@ -24,3 +24,11 @@ def test_packed_workspace_does_not_grow_with_short_sequences(L, N, T, window, si
     assert 8 * T * Hq <= need <= 8 * T * Hq + 256 + (T // 256 + long) * Hq * 2 * sinks * d * 4
     if sinks == 4:
         assert need < 100 << 20
+
+
+@pytest.mark.parametrize("strides,gap", [((110, 100, 10), 10), ((200, 100, 10), 95), ((100, 200, 10), -95), ((110, 100, 10), -10)])
+def test_rope_outputs_that_meet_in_other_tokens_are_refused(L, strides, gap):
+    """q_out and k_out of one head each in rows that interleave: apart in every token, but not from the next one."""
+    s = S3(*strides)
+    d = la.KdRopeDesc(2, 2, 1, 1, 10, 4, 0, 0, 0, 0, 0, 1.0, s, s, s, s)
+    assert L.kron_delta_rope(ctypes.byref(d), P(0), P(1), P(2), P(3), P(4, 4000), P(4, 4000 + 4 * gap), None) == ALIAS
