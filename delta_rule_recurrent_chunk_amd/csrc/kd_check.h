@@ -24,6 +24,10 @@ inline bool overlap(Range a, Range b) {
 
 inline bool misaligned(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) != 0; }
 
+// Whether a launch of `blocks` workgroups along one dimension is possible: the
+// runtime counts its threads in 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace kd

@@ -26,6 +26,7 @@
 // a tile only ever waits for tiles whose workgroups started earlier and which
 // wait, in turn, only for earlier ones, so every wait ends (a bound of some
 // seconds, after which the results become NaN, is there all the same).
+#include "kd_check.h"
 #include "kd_device.h"
 
 namespace kd {
@@ -433,19 +434,23 @@ __global__ __launch_bounds__(256) void kd_glr_step_kernel(const E* __restrict__ 
                                                           const E* __restrict__ gi, const float* h_in,
                                                           E* __restrict__ y, float* h_out, int64_t n)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= n) return;
-    const float u = GATE ? (float)gi[at] * (float)x[at] : (float)x[at];
-    const float s = fmaf((float)f[at], h_in[at], u);
-    y[at] = (E)s;
-    h_out[at] = s;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
+        const float u = GATE ? (float)gi[at] * (float)x[at] : (float)x[at];
+        const float s = fmaf((float)f[at], h_in[at], u);
+        y[at] = (E)s;
+        h_out[at] = s;
+    }
 }
+
+// Workgroups for n elements, which take more than one each beyond 2^30.
+static unsigned glr_grid(int64_t n) { return (unsigned)min((int64_t)1 << 22, (n + 255) / 256); }
+
 
 template <class E>
 static hipError_t glr_step(const void* x, const void* f, const void* gi, const float* h_in, void* y, float* h_out,
                            int64_t n, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((n + 255) / 256);
+    const unsigned grid = glr_grid(n);
     if (gi)
         kd_glr_step_kernel<E, true><<<grid, 256, 0, st>>>((const E*)x, (const E*)f, (const E*)gi, h_in, (E*)y, h_out, n);
     else
@@ -462,11 +467,19 @@ size_t glr_workspace_bytes(int, int B, int T, int D) {
 
 // Four adjacent channels per thread where a row's length keeps them aligned,
 // one otherwise.
+static int glr_vec(int D) { return D % 4 == 0 ? 4 : 1; }
+static int glr_lanes(int D) { return D % 4 == 0 ? 32 : 64; }
+static int64_t glr_tiles(int B, int T, int D) {
+    const int cw = glr_vec(D) * glr_lanes(D);
+    return ((int64_t)D + cw - 1) / cw * B * max((int64_t)1, ((int64_t)T + GLR_CHUNK - 1) / GLR_CHUNK);
+}
+// (with D, T <= 2^30 and B <= 65535 their number stays below 2^63)
+bool glr_fits(int B, int T, int D) { return T == 0 || grid_fits(glr_tiles(B, T, D), GLR_NT); }
+
 template <class E, bool GATE, int VEC, int LANES>
 static hipError_t glr_run(GlrArgs p, bool bwd, void* ws, hipStream_t st)
 {
-    const int64_t tiles = ((int64_t)p.D + LANES * VEC - 1) / (LANES * VEC) * p.B * max(1, (p.T + GLR_CHUNK - 1) / GLR_CHUNK);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t tiles = glr_tiles(p.B, p.T, p.D);
     if (p.T > GLR_CHUNK) {
         const int64_t n = glr_words(p.B, p.T, p.D);
         p.ticket = (unsigned*)ws;
@@ -484,20 +497,20 @@ static hipError_t glr_run(GlrArgs p, bool bwd, void* ws, hipStream_t st)
 template <class E>
 static hipError_t glr_any(const GlrArgs& p, bool bwd, void* ws, hipStream_t st)
 {
-    if (p.D % 4 == 0) return p.i ? glr_run<E, true, 4, 32>(p, bwd, ws, st) : glr_run<E, false, 4, 32>(p, bwd, ws, st);
+    if (glr_vec(p.D) == 4) return p.i ? glr_run<E, true, 4, 32>(p, bwd, ws, st) : glr_run<E, false, 4, 32>(p, bwd, ws, st);
     return p.i ? glr_run<E, true, 1, 64>(p, bwd, ws, st) : glr_run<E, false, 1, 64>(p, bwd, ws, st);
 }
 
 // T = 0: the state passes through
 __global__ __launch_bounds__(256) void kd_glr_pass_kernel(const float* from, float* to, int64_t n)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at < n) to[at] = from ? from[at] : 0.f;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256)
+        to[at] = from ? from[at] : 0.f;
 }
 static hipError_t glr_pass(const float* from, float* to, int B, int D, hipStream_t st)
 {
     const int64_t n = (int64_t)B * D;
-    kd_glr_pass_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(from, to, n);
+    kd_glr_pass_kernel<<<glr_grid(n), 256, 0, st>>>(from, to, n);
     return hipGetLastError();
 }
 

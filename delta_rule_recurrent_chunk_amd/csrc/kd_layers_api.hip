@@ -16,6 +16,7 @@
 
 namespace kd {
 size_t glr_workspace_bytes(int bf16, int B, int T, int D);
+bool glr_fits(int B, int T, int D);
 hipError_t launch_glr_fwd(int bf16, const void* x, const void* f, const void* gi, const float* h0, void* h, float* hT,
                           float* hs, void* ws, int B, int T, int D, hipStream_t st);
 hipError_t launch_glr_bwd(int bf16, const void* x, const void* f, const void* gi, const float* hs, const void* dh,
@@ -23,8 +24,11 @@ hipError_t launch_glr_bwd(int bf16, const void* x, const void* f, const void* gi
                           hipStream_t st);
 hipError_t launch_glr_step(int bf16, const void* x, const void* f, const void* gi, const float* h_in, void* y,
                            float* h_out, int64_t n, hipStream_t st);
+bool rope_fits(int bf16, RopeArgs a);
 hipError_t launch_rope(int bf16, const RopeArgs& a, hipStream_t st);
+bool swa_fwd_fits(const SwaArgs& a);
 hipError_t launch_swa_fwd(int bf16, int d, const SwaArgs& a, hipStream_t st);
+bool swa_bwd_fits(bool packed, int N, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S);
 hipError_t launch_swa_bwd(int bf16, int d, const SwaArgs& a, void* ws, hipStream_t st);
 size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S);
 hipError_t launch_swa_decode(int bf16, int d, const SwaDecodeArgs& a, hipStream_t st);
@@ -35,6 +39,7 @@ size_t swa_decode_part_bytes(int B, int Hq, int Hkv, int d, int seen);
 
 namespace {
 
+using kd::grid_fits;
 using kd::misaligned;
 using kd::overlap;
 using kd::Range;
@@ -116,8 +121,6 @@ kd_status check_glr(const kd_glr_desc* d) {
     if (!d) return KD_ERR_NULL;
     if (!known(d->dtype)) return KD_ERR_DTYPE;
     if (d->B < 1 || d->B > 65535 || d->D < 1 || d->T < 0 || d->T > (1 << 30) || d->D > (1 << 30)) return KD_ERR_SHAPE;
-    // one workgroup per 128 tokens of 64 channels or more, and 16 bytes of workspace per 128 tokens and channel
-    if (((int64_t)d->D + 63) / 64 * d->B > INT32_MAX / 2 / ((int64_t)d->T / 128 + 1)) return KD_ERR_SHAPE;
     return KD_OK;
 }
 
@@ -130,7 +133,7 @@ size_t glr_chunks(const kd_glr_desc* d) {
 extern "C" {
 
 size_t kron_delta_glr_workspace_bytes(const kd_glr_desc* d) {
-    if (check_glr(d) != KD_OK) return 0;
+    if (check_glr(d) != KD_OK || !kd::glr_fits(d->B, d->T, d->D)) return 0;
     return kd::glr_workspace_bytes(d->dtype == KD_BF16, d->B, d->T, d->D);
 }
 
@@ -138,6 +141,7 @@ kd_status kron_delta_glr_fwd(const kd_glr_desc* d, const void* x, const void* f,
                              void* h, float* hT, float* hs, void* ws, size_t ws_bytes, void* stream) {
     const kd_status st = check_glr(d);
     if (st != KD_OK) return st;
+    if (!kd::glr_fits(d->B, d->T, d->D)) return KD_ERR_SHAPE;
     const size_t n = (size_t)d->B * d->T * d->D, xb = n * es_of(d->dtype), sb = (size_t)d->B * d->D * 4;
     if (n > 0 && (!x || !f || !h)) return KD_ERR_NULL;
     const size_t need = kd::glr_workspace_bytes(d->dtype == KD_BF16, d->B, d->T, d->D);
@@ -159,6 +163,7 @@ kd_status kron_delta_glr_bwd(const kd_glr_desc* d, const void* x, const void* f,
                              size_t ws_bytes, void* stream) {
     const kd_status st = check_glr(d);
     if (st != KD_OK) return st;
+    if (!kd::glr_fits(d->B, d->T, d->D)) return KD_ERR_SHAPE;
     const size_t n = (size_t)d->B * d->T * d->D, xb = n * es_of(d->dtype), sb = (size_t)d->B * d->D * 4;
     if (n > 0 && (!x || !f || !hs || !dh || !dx || !df || (i && !di))) return KD_ERR_NULL;
     const size_t need = kd::glr_workspace_bytes(d->dtype == KD_BF16, d->B, d->T, d->D);
@@ -180,7 +185,7 @@ kd_status kron_delta_glr_step(const kd_glr_desc* d, const void* x, const void* f
                               void* y, float* h_out, void* stream) {
     const kd_status st = check_glr(d);
     if (st != KD_OK) return st;
-    if (d->T != 1 || (int64_t)d->B * d->D > ((int64_t)1 << 37)) return KD_ERR_SHAPE;
+    if (d->T != 1) return KD_ERR_SHAPE;
     const size_t n = (size_t)d->B * d->D, xb = n * es_of(d->dtype), sb = n * 4;
     if (!x || !f || !h_in || !y || !h_out) return KD_ERR_NULL;
     const void* ptrs[] = {x, f, i, h_in, y, h_out};
@@ -276,6 +281,7 @@ kd_status kron_delta_rope(const kd_rope_desc* d, const void* q, const void* k, c
     a.interleaved = d->layout == KD_ROPE_INTERLEAVED;
     a.inverse = d->inverse != 0;
     a.scale = d->scale;
+    if (!kd::rope_fits(d->dtype == KD_BF16, a)) return KD_ERR_SHAPE;
     return done(kd::launch_rope(d->dtype == KD_BF16, a, (hipStream_t)stream));
 }
 
@@ -310,6 +316,10 @@ kd_status check_swa(const kd_swa_desc* d, bool packed, SwaSpans* s) {
     return KD_OK;
 }
 
+bool swa_bwd_fits(const kd_swa_desc* d, bool packed) {
+    return kd::swa_bwd_fits(packed, d->B, packed ? 1 : d->B, d->Tq, d->Tk, d->Hq, d->Hkv, d->d, d->window, d->sinks);
+}
+
 kd::SwaArgs swa_args(const kd_swa_desc* d, const int32_t* cu, const void* q, const void* k, const void* v) {
     kd::SwaArgs a = {};
     a.q = q;
@@ -338,7 +348,7 @@ kd::SwaArgs swa_args(const kd_swa_desc* d, const int32_t* cu, const void* q, con
 
 size_t kron_delta_swa_workspace_bytes(const kd_swa_desc* d, int packed) {
     SwaSpans s;
-    if (check_swa(d, packed != 0, &s) != KD_OK) return 0;
+    if (check_swa(d, packed != 0, &s) != KD_OK || !swa_bwd_fits(d, packed != 0)) return 0;
     return kd::swa_bwd_workspace_bytes(packed != 0, d->B, d->Tq, d->Tk, d->Hq, d->Hkv, d->d, d->window, d->sinks);
 }
 
@@ -361,6 +371,7 @@ kd_status kron_delta_swa_fwd(const kd_swa_desc* d, const int32_t* cu, const void
     kd::SwaArgs a = swa_args(d, cu, q, k, v);
     a.o = o;
     a.lse = lse;
+    if (!kd::swa_fwd_fits(a)) return KD_ERR_SHAPE;
     return done(kd::launch_swa_fwd(d->dtype == KD_BF16, d->d, a, (hipStream_t)stream));
 }
 
@@ -370,6 +381,7 @@ kd_status kron_delta_swa_bwd(const kd_swa_desc* d, const int32_t* cu, const void
     SwaSpans s;
     const kd_status st = check_swa(d, cu != nullptr, &s);
     if (st != KD_OK) return st;
+    if (!swa_bwd_fits(d, cu != nullptr)) return KD_ERR_SHAPE;
     if (d->Tk == 0 && d->Tq == 0) return KD_OK;
     if (d->Tq > 0 && (!q || !o || !lse || !dO || !dq)) return KD_ERR_NULL;
     if (d->Tk > 0 && (!k || !v || !dk || !dv)) return KD_ERR_NULL;
@@ -514,7 +526,7 @@ kd_status kron_delta_swa_cache_store(const kd_swa_cache_desc* d, int32_t T, cons
         return KD_ERR_SHAPE;
     kd::SwaStoreArgs a = {};
     a.row = (int)(d->d * es / 16);
-    if (((int64_t)T * d->Hkv * a.row + 255) / 256 > INT32_MAX) return KD_ERR_SHAPE;
+    if (!grid_fits(((int64_t)T * d->Hkv * a.row + 255) / 256, 256)) return KD_ERR_SHAPE;
     const void* ptrs[] = {k, v, k_cache, v_cache};
     for (const void* p : ptrs)
         if (misaligned(p)) return KD_ERR_ALIGN;

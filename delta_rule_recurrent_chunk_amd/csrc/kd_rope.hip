@@ -17,6 +17,7 @@
 // loading while the angles are made.  8 x 2048 tokens of 16 + 4 heads of 128
 // (bf16, half layout, 168 MB): 37 us, 4.5 TB/s (a large copy: 5.1); one wave per
 // token and pair by pair it took 77 us.
+#include "kd_check.h"
 #include "kd_device.h"
 #include "kd_rope.h"
 
@@ -134,12 +135,11 @@ static bool rope_aligned(const RopeArgs& a, int64_t es)
 }
 
 // Sixteen bytes at a time where addresses, strides and (half layout) the two
-// halves allow it; pair by pair otherwise.
-template <class E>
-static hipError_t rope(RopeArgs a, hipStream_t st)
+// halves allow it (vec); pair by pair otherwise.  Returns the workgroups.
+static int64_t rope_plan(RopeArgs& a, int es, bool& vec)
 {
-    const int epc = 16 / sizeof(E), H = a.side[0].heads + a.side[1].heads;
-    const bool vec = rope_aligned(a, sizeof(E)) && a.d % epc == 0 && (a.interleaved || a.rot / 2 % epc == 0);
+    const int epc = 16 / es, H = a.side[0].heads + a.side[1].heads;
+    vec = rope_aligned(a, es) && a.d % epc == 0 && (a.interleaved || a.rot / 2 % epc == 0);
     a.per = vec ? (a.interleaved ? a.d / epc : a.rot / 2 / epc + (a.d - a.rot) / epc) : a.rot / 2 + (a.d - a.rot);
     const int64_t row = (int64_t)a.per * H;
     // about 1280 items per workgroup, so that small calls spread over the chip
@@ -147,9 +147,14 @@ static hipError_t rope(RopeArgs a, hipStream_t st)
     a.tokens = (int)max((int64_t)1, min((int64_t)ROPE_TOKENS, 1280 / row));
     a.div_row = (unsigned)(((1ull << 32) + row - 1) / row);
     a.div_per = (unsigned)(((1ull << 32) + a.per - 1) / a.per);
-    const int64_t blocks = ((int64_t)a.B * a.T + a.tokens - 1) / a.tokens;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks);
+    return ((int64_t)a.B * a.T + a.tokens - 1) / a.tokens;
+}
+
+template <class E>
+static hipError_t rope(RopeArgs a, hipStream_t st)
+{
+    bool vec;
+    const dim3 grid((unsigned)rope_plan(a, sizeof(E), vec));
     if (a.interleaved) {
         if (vec) kd_rope_kernel<E, true, true><<<grid, 256, 0, st>>>(a);
         else kd_rope_kernel<E, true, false><<<grid, 256, 0, st>>>(a);
@@ -158,6 +163,12 @@ static hipError_t rope(RopeArgs a, hipStream_t st)
         else kd_rope_kernel<E, false, false><<<grid, 256, 0, st>>>(a);
     }
     return hipGetLastError();
+}
+
+bool rope_fits(int bf16, RopeArgs a)
+{
+    bool vec;
+    return grid_fits(rope_plan(a, bf16 ? 2 : 4, vec), 256);
 }
 
 hipError_t launch_rope(int bf16, const RopeArgs& a, hipStream_t st) { return bf16 ? rope<__bf16>(a, st) : rope<float>(a, st); }

@@ -308,6 +308,8 @@ __device__ __forceinline__ bool swa_item(int64_t n, int64_t& item) {
     return item < n;
 }
 __host__ __device__ inline int64_t swa_grid(int64_t n) { return (n + 127) / 128 * 128; }
+// Slots of R rows (see swa_locate).
+inline int64_t swa_slots(bool packed, int N, int T, int R) { return packed ? (int64_t)T / R + N : ((int64_t)T + R - 1) / R; }
 
 // Waits for a loaded fragment here rather than at its first use inside a loop
 // (where the wait would cover the loop's own loads).

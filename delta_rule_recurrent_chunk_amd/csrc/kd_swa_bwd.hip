@@ -11,6 +11,7 @@
 //      also summed over the query heads of a group; the first block adds the
 //      partial sums of 2.  Where key blocks are few, workgroups share the heads
 //      of a group and a last pass adds their fp32 sums.
+#include "kd_check.h"
 #include "kd_swa.h"
 
 namespace kd {
@@ -633,8 +634,6 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
     }
 }
 
-static int64_t swa_slots(bool packed, int N, int T, int R) { return packed ? (int64_t)T / R + N : ((int64_t)T + R - 1) / R; }
-
 // Rows of a chunk of the sinks' pass: about 256 workgroups over all heads, so
 // that the start of each is paid for, and chunks of 256 to 4096 rows.
 static int swa_chunk(int64_t rows, int Hq, int S) {
@@ -685,6 +684,14 @@ size_t swa_bwd_workspace_bytes(bool packed, int B, int Tq, int Tk, int Hq, int H
            (nsp > 1 ? (size_t)nsp * 2 * B * Tk * Hkv * d * 4 : 0);
 }
 
+// Whether the grids of all passes are possible.
+bool swa_bwd_fits(bool packed, int N, int B, int Tq, int Tk, int Hq, int Hkv, int d, int W, int S) {
+    const int64_t ks = swa_slots(packed, N, Tk, 128) * swa_head_splits(packed, B, Tq, Tk, Hq, Hkv, W);
+    const int64_t np = swa_part_slots(packed, N, Tq, Tk, W, S, swa_chunk((int64_t)B * Tq, Hq, S));
+    return grid_fits(swa_grid(swa_slots(packed, N, Tq, 128) * Hq * B), 256) && grid_fits(swa_grid(ks * Hkv * B), 256) &&
+           grid_fits(np * ((S + 31) / 32), 256) && grid_fits(((int64_t)B * Tk * Hkv * d / 4 + 255) / 256, 256);
+}
+
 template <class E, int D>
 static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
 {
@@ -695,7 +702,6 @@ static hipError_t swa_bwd(SwaArgs a, void* ws, hipStream_t st)
     const int64_t gk = swa_grid(nk * a.nsp * a.Hkv * a.B);
     a.chunk = swa_chunk((int64_t)a.B * a.Tq, a.Hq, a.S);
     const int64_t np = swa_part_slots(a.cu, a.N, a.Tq, a.Tk, a.W, a.S, a.chunk);
-    if (gq > INT32_MAX || gk > INT32_MAX || np > INT32_MAX / 2) return hipErrorInvalidValue;
     a.apart = swa_apart(a.cu, a.N, a.Tq, a.W);
     a.rows = (float2*)ws;
     a.part = (float*)((char*)ws + swa_rows_bytes(a.B, a.Tq, a.Hq));

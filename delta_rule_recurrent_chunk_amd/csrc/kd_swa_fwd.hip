@@ -16,6 +16,7 @@
 // SIMD (registers) overlap about half of that; without its tile loads the
 // kernel takes 0.8 of the time.  Tiles of 64 keys, two in LDS: two workgroups
 // per compute unit; eight waves per block of queries were 4% slower.
+#include "kd_check.h"
 #include "kd_swa.h"
 
 namespace kd {
@@ -189,13 +190,13 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
         a.lse[((int64_t)b * a.Hq + h) * a.Tq + s.q0 + row] = none ? -INFINITY : 0.6931471805599453f * (m + __log2f(l));
 }
 
+bool swa_fwd_fits(const SwaArgs& a) { return grid_fits(swa_grid(swa_slots(a.cu, a.N, a.Tq, 128) * a.Hq * a.B), 256); }
+
 template <class E, int D>
 static hipError_t swa_fwd(const SwaArgs& a, hipStream_t st)
 {
-    const int nslots = a.cu ? a.Tq / 128 + a.N : (int)(((int64_t)a.Tq + 127) / 128);
-    const int64_t grid = swa_grid((int64_t)nslots * a.Hq * a.B);
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-    kd_swa_fwd_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<(unsigned)grid, 256, 0, st>>>(a, nslots);
+    const int64_t nslots = swa_slots(a.cu, a.N, a.Tq, 128), grid = swa_grid(nslots * a.Hq * a.B);
+    kd_swa_fwd_kernel<E, D, sizeof(E) == 2 ? 64 : 32><<<(unsigned)grid, 256, 0, st>>>(a, (int)nslots);
     return hipGetLastError();
 }
 

@@ -402,7 +402,10 @@ KD_API kd_status kron_delta_mixer_fwd(const kd_desc *desc, const kd_mixer_params
  * the entry points below are that attention, the rotary positions of its
  * queries and keys, and the element-wise member of the recurrence family.
  * Ownership, streams, checks and status codes are those of the calls above;
- * sizes and strides are the ones each descriptor names.
+ * sizes and strides are the ones each descriptor names.  Of those, sizes whose
+ * work would take 2^32 threads or more in one launch (128 tokens of 64 channels
+ * of the recurrence are 512 of them, a block of 128 query rows of one head 256,
+ * up to 8 tokens of a rotation 256) are refused with KD_ERR_SHAPE.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -210,6 +210,22 @@ def test_glr_infinities_and_nans(gate, T, D, dtype):
         same_but_for("dh0", g["dh0"], dh0, 1.01 * (a(v["f"][:, 0]) * eg[:, 0] + 140 * R.W * a(v["f"][:, 0]) * G[:, 0]))
 
 
+def test_glr_step_past_32_bits_of_elements():
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    B, D = 5, 1 << 30
+    x, f = torch.zeros(B, D, dtype=torch.bfloat16, device="cuda"), torch.full((B, D), 0.5, dtype=torch.bfloat16, device="cuda")
+    h = torch.full((B, D), 2.0, device="cuda")
+    at = [(0, 0), (0, D - 1), (1, 77), (3, 1 << 29), (4, 5), (4, D - 1)]
+    for n, a in enumerate(at):
+        x[a] = n + 1
+    y = kd.glr_step(x, f, None, h)
+    for n, a in enumerate(at):
+        assert y[a] == n + 2 and h[a] == n + 2
+        y[a], h[a] = 1, 1
+    assert all((t[b] == 1).all() for t in (y, h) for b in range(B))
+
+
 # ------------------------------------------------------------- fused tensors
 @pytest.mark.parametrize("order", ["bthd", "bhtd", "tbhd"])
 @pytest.mark.parametrize("Hq,Hk", [(4, 2), (1, 1), (3, 1), (1, 2)])

@@ -5,7 +5,7 @@ import pytest
 
 import delta_rule_recurrent_chunk_amd as kd
 from delta_rule_recurrent_chunk_amd import layers as la
-from tests.test_layers_abi import ALIAS, L, P, S3  # noqa: F401  (L is a fixture)
+from tests.test_layers_abi import ALIAS, SHAPE, L, P, S3  # noqa: F401  (L is a fixture)
 
 
 def swa(B, T, Hq, Hkv, d, window, sinks, dtype=1):
@@ -32,3 +32,22 @@ def test_rope_outputs_that_meet_in_other_tokens_are_refused(L, strides, gap):
     s = S3(*strides)
     d = la.KdRopeDesc(2, 2, 1, 1, 10, 4, 0, 0, 0, 0, 0, 1.0, s, s, s, s)
     assert L.kron_delta_rope(ctypes.byref(d), P(0), P(1), P(2), P(3), P(4, 4000), P(4, 4000 + 4 * gap), None) == ALIAS
+
+
+def test_launches_past_32_bits_of_threads_are_refused(L):
+    """Within the bounds of the single sizes; the launch itself would fail."""
+    g = la.KdGlrDesc(65535, 1 << 20, 1, 1)
+    assert L.kron_delta_glr_workspace_bytes(ctypes.byref(g)) == 0
+    assert L.kron_delta_glr_fwd(ctypes.byref(g), *[P(i) for i in range(8)], 1 << 40, None) == SHAPE
+    assert L.kron_delta_glr_bwd(ctypes.byref(g), *[P(i) for i in range(11)], 1 << 40, None) == SHAPE
+    s = S3(2 << 30, 2, 2)
+    r = la.KdRopeDesc(1, 1 << 30, 1, 0, 2, 2, 0, 1, 0, 0, 0, 1.0, s, s, s, s)
+    assert L.kron_delta_rope(ctypes.byref(r), P(0), None, P(2), P(3), P(4), None, None) == SHAPE
+    a = swa(65535, 1, 512, 1, 32, 8, 0)
+    assert L.kron_delta_swa_fwd(ctypes.byref(a), None, *[P(i) for i in range(5)], None) == SHAPE
+    assert L.kron_delta_swa_workspace_bytes(ctypes.byref(a), 0) == 0
+    assert L.kron_delta_swa_bwd(ctypes.byref(a), None, *[P(i) for i in range(10)], 1 << 40, None) == SHAPE
+    c = S3(16 * 16 * 128, 16 * 128, 128)
+    c = la.KdSwaCacheDesc(1, 16, 16, 128, 16, 1, 8, 0, 1.0, 0, 0, 1.0, c, c)
+    k = S3(1 << 39, 16 * 128, 128)
+    assert L.kron_delta_swa_cache_store(ctypes.byref(c), 1 << 27, P(0), P(1), k, k, None, P(3), P(4), None) == SHAPE
