@@ -258,3 +258,68 @@ def test_rope_in_place_on_heads_of_one_tensor_in_any_order(Hq, Hk, order):
     # heads that both hold are still refused
     with pytest.raises(kd.KronDeltaError):
         kd.rope(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk], pos, freqs, out=(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk]))
+
+
+# --------------------------------------- what the remainders of roundings are worth
+def ulp(x):
+    """The step of bf16 at x (0 at 0)."""
+    return np.where(x == 0, 0.0, 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 1e-300))) - 7))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks,p", [(64, 1, 128, 40, 4, 100), (32, 1, 64, 5, 2, 30), (16, 2, 32, 300, 1, 301), (32, 4, 128, 2048, 4, 3000),
+                                                     (16, 1, 128, 100, 0, 0), (24, 2, 128, 64, 64, 500)])
+def test_decoding_loses_the_rounding_of_its_output_alone(Hq, Hkv, d, window, sinks, p):
+    """bf16 queries and weights pass as a rounded part and its remainder: each is off by 2^-16 of itself (2^-8 of a
+    remainder of at most 2^-8).  A score is then off by 2^-16 of the products in it, and every weight by twice that; two
+    such errors and that of the weight itself stay below 2^-14 of what the scores hold together."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    print("case", (Hq, Hkv, d, window, sinks, p), flush=True)
+    r = np.random.default_rng(d + p)
+    cap, B = window + sinks, 4
+    kc, vc = (torch.tensor(r.standard_normal((B, cap, Hkv, d)), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    (q, qv), (k, _), (v, _) = (dev(r.standard_normal((B, h, d)), "bf16") for h in (Hq, Hkv, Hkv))
+    lens = torch.full((B,), p, dtype=torch.int32, device="cuda")
+    o = kd.swa_decode(q, k, v, kc, vc, lens, window, sinks)
+    at = [R.slot(s, sinks, cap) for s in R.seen(p, window, sinks)]
+    for b in range(B):
+        kv, vv = host(kc[b])[at], host(vc[b])[at]
+        val, err = R.attention_heads(qv[b][None], kv, vv, len(at), 0, 1 / np.sqrt(d), None, 2.0 ** -14)
+        sc = np.einsum("hd,nhd->hn", np.abs(qv[b]), np.abs(np.repeat(kv, Hq // Hkv, 1))).max(1) / np.sqrt(d)
+        big = np.abs(np.repeat(vv, Hq // Hkv, 1)).max(0)
+        more = 2 * 2.0 ** -16 * sc[:, None] * (big + np.abs(val["o"][0]))
+        check("o", o[b][None], val["o"], err["o"] + more[None] + 2.0 ** -8 * np.abs(val["o"]))
+
+
+@pytest.mark.parametrize("T,W,S,d", [(500, 400, 0, 64), (900, 300, 4, 128), (450, 450, 0, 32), (1500, 60, 2, 64)])
+def test_dq_of_few_hundred_keys_has_the_error_of_two_roundings(T, W, S, d):
+    """Queries that see 33 to 511 keys: dS carries its remainder, which leaves the rounding of the result and that of o
+    in delta.  A rounding is off by a step over the root of 12 in the mean square; the sums of both are formed here from
+    the values, with those of dS for comparison.  Norms over some 10^5 elements scatter by a percent, and the norm
+    without the remainder is 25% above the one with it: 10% above is allowed."""
+    import delta_rule_recurrent_chunk_amd as kd
+    _torch()
+    H = 4
+    (q, qv), (k, kv), (v, vv), (dO, ov) = swa_inputs(1, T, T, H, 2, d, "bf16", T + d)
+    o, lse = kd.swa_fwd(q, k, v, W, S, return_lse=True)
+    got = host(kd.swa_bwd(q, k, v, o, lse, dO, W, S)["dq"][0])
+    off, two, three, scale = 0.0, 0.0, 0.0, 1 / np.sqrt(d)
+    rows = R.visible(T, T, W, S).sum(1)
+    use = (np.arange(T) >= 64) & (rows < 512) & (rows > 32)
+    for h in range(H):
+        kk, v1, q1, g1 = kv[0, :, h // 2], vv[0, :, h // 2], qv[0, :, h], ov[0, :, h]
+        vis = R.visible(T, T, W, S)
+        s = np.where(vis, q1 @ kk.T * scale, -np.inf)
+        P = np.exp(s - s.max(1, keepdims=True))
+        P /= P.sum(1, keepdims=True)
+        oo = P @ v1
+        dS = P * (g1 @ v1.T - (g1 * oo).sum(1, keepdims=True))
+        dq = scale * dS @ kk
+        out = (ulp(dq) ** 2 / 12).sum(1)
+        delta = (g1 ** 2 * ulp(oo) ** 2 / 12).sum(1) * ((scale * P @ kk) ** 2).sum(1)
+        rest = scale ** 2 * (ulp(dS) ** 2 / 12) @ (kk ** 2).sum(1)
+        off += ((got[:, h] - dq)[use] ** 2).sum()
+        two += (out + delta)[use].sum()
+        three += (out + delta + rest)[use].sum()
+    assert three > 1.25 ** 2 * two, (three / two) ** 0.5
+    assert off <= 1.1 ** 2 * two, (off / two) ** 0.5
