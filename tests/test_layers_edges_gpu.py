@@ -260,6 +260,45 @@ def test_rope_in_place_on_heads_of_one_tensor_in_any_order(Hq, Hk, order):
         kd.rope(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk], pos, freqs, out=(qkv[:, :, :Hq], qkv[:, :, Hq - 1:Hq - 1 + Hk]))
 
 
+# ------------------------------------------------------------- two streams
+def test_calls_on_two_streams_at_once(monkeypatch):
+    """Each call has its own workspace, and a recurrence's tiles wait for tiles of their own call alone."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    monkeypatch.setenv("KRON_DELTA_SYNC_CHECK", "0")       # (which would wait after every call)
+    freqs, _ = kd.rope_frequencies(64, device="cuda")
+    pos = torch.arange(2000, device="cuda")
+
+    def made(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+        return dict(x=r(2, 9000, 520), f=torch.sigmoid(r(2, 9000, 520)), dh=r(2, 9000, 520), q=r(1, 2000, 8, 64), k=r(1, 2000, 2, 64),
+                    v=r(1, 2000, 2, 64), dO=r(1, 2000, 8, 64), kc=r(2, 700, 2, 64), vc=r(2, 700, 2, 64))
+
+    def run(t):
+        h, hT, hs = kd.glr_fwd(t["x"], t["f"], None, save_states=True)
+        g = kd.glr_bwd(t["x"], t["f"], None, hs, t["dh"])
+        q, k = kd.rope(t["q"], t["k"], pos, freqs)
+        o, lse = kd.swa_fwd(q, k, t["v"], 300, 4, return_lse=True)
+        s = kd.swa_bwd(q, k, t["v"], o, lse, t["dO"], 300, 4)
+        lens = torch.tensor([800, 650], dtype=torch.int32).to("cuda", non_blocking=True)
+        y = kd.swa_decode(t["q"][0, :2], t["k"][0, :2], t["v"][0, :2], t["kc"], t["vc"], lens, 600, 4, freqs=freqs)
+        return [h, hT, hs, g["dx"], g["df"], g["dh0"], o, lse, s["dq"], s["dk"], s["dv"], y]
+
+    ts = [made(n) for n in range(2)]
+    want = [[t.clone() for t in run(t)] for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    for n in range(10):
+        got = []
+        for t, st in zip(ts, streams):
+            with torch.cuda.stream(st):
+                got.append(run(t))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), n
+
+
 # --------------------------------------- what the remainders of roundings are worth
 def ulp(x):
     """The step of bf16 at x (0 at 0)."""
