@@ -434,9 +434,10 @@ __global__ __launch_bounds__(256) void kd_swa_store_kernel(SwaStoreArgs a)
 static int64_t swa_decode_items(int B, int Hq, int Hkv) { return (int64_t)B * Hkv * ((Hq / Hkv + 31) / 32); }
 
 // Splits of a row's keys: two workgroups for each of the chip's 256 compute
-// units (all of them resident: 64 KB of LDS each), none below 64 keys.  Rows
-// are split only where there are fewer than SWA_DECODE_COUNTERS items, so that
-// many counters serve every call.
+// units, none below 64 keys.  Both are resident (71 KB of LDS at most of 160)
+// but in fp32 with heads of 128 (103 KB), where half of them follow the others.
+// Rows are split only where there are fewer than SWA_DECODE_COUNTERS items, so
+// that many counters serve every call.
 int swa_decode_splits(int B, int Hq, int Hkv, int seen) {
     int n = (int)(SWA_DECODE_COUNTERS / swa_decode_items(B, Hq, Hkv));
     const int most = (seen + 63) / 64;

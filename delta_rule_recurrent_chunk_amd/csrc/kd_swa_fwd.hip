@@ -6,7 +6,7 @@
 // so a query's scores lie in one lane (and its partner 32 lanes away): the
 // running maximum m and sum l of its softmax are per-lane scalars.  The
 // weights exp2(c s - m) are packed to the input type (bf16: off by at most
-// 2^-9 of each weight, whose sum is kept in fp32) and go straight back in as
+// 2^-8 of each weight, whose sum is kept in fp32) and go straight back in as
 // the B operand of Ot += Vt Pt.
 //
 // 1 x 32768, 16 query and 4 key heads of 128, window 2048, 4 sinks, bf16: 596 us,

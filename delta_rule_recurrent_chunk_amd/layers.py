@@ -425,7 +425,9 @@ def swa_fwd(q, k, v, window, sinks=0, *, scale=None, cu_seqlens=None, return_lse
     """Attention over the last `window` keys and the first `sinks` ones.  q
     [B, Tq, Hq, d], k, v [B, Tk, Hkv, d], the queries at the end of the keys; or
     packed [T, H, d] with cu_seqlens int32 [N + 1].  scale None: 1 / sqrt(d).
-    Returns o, with return_lse (o, lse [B, Hq, Tq] or [Hq, T] float32)."""
+    Returns o, with return_lse (o, lse [B, Hq, Tq] or [Hq, T] float32).  Packed
+    rows that no sequence holds are not written: those of a new tensor hold
+    anything."""
     torch, L = _ready()
     dev, desc, q, k, v, cu = _swa(q, k, v, window, sinks, scale, cu_seqlens)
     if out is None:
@@ -445,7 +447,8 @@ def swa_fwd(q, k, v, window, sinks=0, *, scale=None, cu_seqlens=None, return_lse
 
 
 def swa_bwd(q, k, v, o, lse, dO, window, sinks=0, *, scale=None, cu_seqlens=None, workspace=None):
-    """Gradients of <dO, o> from swa_fwd's o and lse: a dict with dq, dk, dv."""
+    """Gradients of <dO, o> from swa_fwd's o and lse: a dict with dq, dk, dv
+    (packed rows that no sequence holds are not written, as in swa_fwd)."""
     torch, L = _ready()
     dev, desc, q, k, v, cu = _swa(q, k, v, window, sinks, scale, cu_seqlens)
     _check("o", o, q.shape, q.dtype)
