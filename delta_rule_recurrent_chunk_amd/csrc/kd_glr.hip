@@ -193,7 +193,7 @@ __device__ __forceinline__ void glr_tile(const GlrArgs& p, int& n, int& b, int& 
 }
 
 // Forward.  Bound by memory: 8 x 2048 x 2048 bf16 with an input gate (268 MB)
-// takes 64.7 us, 4.1 TB/s (a large copy: 5.1).  128 x 128 tiles: 8 tokens of 4
+// takes 64.9 us, 4.1 TB/s (a large copy: 5.1).  128 x 128 tiles: 8 tokens of 4
 // channels per thread keep 48 registers of loads in flight, and the words
 // handed over are 3% of the data.
 template <class E, bool GATE, int VEC, int LANES>

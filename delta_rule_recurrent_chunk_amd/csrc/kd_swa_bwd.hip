@@ -24,8 +24,9 @@ __device__ __forceinline__ int swa_far(const SwaArgs& a, int past) { return max(
 // dQ and delta of 128 query rows of one head: the forward's layout, with the
 // scores' gradient in the weights' place and K in V's.
 //
-// 4 x 4096, 16/4 heads of 128, window 1024, bf16: 285 us for three products
-// (181 GFLOP of visible pairs, 640 TFLOP/s), bound like the forward.
+// 4 x 4096, 16/4 heads of 128, window 1024, bf16: 280 us for three products
+// (181 GFLOP of visible pairs, 650 TFLOP/s), bound like the forward (matrix
+// units 41% of the cycles, vector issue 42%).
 //
 // dS is rounded to the type before its product with K.  Its delta comes from
 // the rounded o there (the sum of P dP is only known at the end, when it goes
@@ -378,9 +379,10 @@ __device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const
 // of every head of the group pass through LDS, one tile ahead.  In bf16 the
 // values' fragments are read from LDS too: with those of the keys, dK and dV
 // in registers (160 of 256) two waves fit a SIMD, and one's products overlap
-// the other's exponentials.  4 x 4096, 16/4 heads of 128, window 1024, bf16: 350 us
-// for four products (241 GFLOP of visible pairs, 690 TFLOP/s; with V in registers
-// and one wave per SIMD 623 us).
+// the other's exponentials (matrix units 40% of the cycles, vector issue 41%).
+// 4 x 4096, 16/4 heads of 128, window 1024, bf16: 355 us for four products (241
+// GFLOP of visible pairs, 680 TFLOP/s; with V in registers and one wave per SIMD
+// 623 us).
 template <class E, int D, int BQ>
 __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_kernel(SwaArgs a, int nslots)
 {
@@ -551,7 +553,7 @@ __global__ __launch_bounds__(256) void kd_swa_sum_kernel(SwaArgs a, int64_t n)
 // Partial dK and dV of 32 sinks from one chunk of one head's queries beyond the
 // window: the waves share the rows (32 each of a tile), their sums are joined in LDS
 // one wave after the other.  4 x 4096 queries of 16 heads beyond a window of 1024:
-// 37 us, bound by reading Q and dO tile by tile.
+// 34 us, bound by reading Q and dO tile by tile (matrix units 11% of the cycles).
 template <class E, int D, int NW>
 __global__ __launch_bounds__(64 * NW, 1) void kd_swa_sink_kernel(SwaArgs a)
 {

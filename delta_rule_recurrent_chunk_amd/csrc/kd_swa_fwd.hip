@@ -9,13 +9,13 @@
 // 2^-8 of each weight, whose sum is kept in fp32) and go straight back in as
 // the B operand of Ot += Vt Pt.
 //
-// 1 x 32768, 16 query and 4 key heads of 128, window 2048, 4 sinks, bf16: 596 us,
-// 895 TFLOP/s of visible pairs (a large library product: 1222).  Bound by
+// 1 x 32768, 16 query and 4 key heads of 128, window 2048, 4 sinks, bf16: 600 us,
+// 890 TFLOP/s of visible pairs (a large library product: 1222).  Bound by
 // instructions: per 64 keys a wave issues 32 matrix products and about 160
-// vector instructions, 32 of them exponentials, and the two waves that fit a
-// SIMD (registers) overlap about half of that; without its tile loads the
-// kernel takes 0.8 of the time.  Tiles of 64 keys, two in LDS: two workgroups
-// per compute unit; eight waves per block of queries were 4% slower.
+// vector instructions, 32 of them exponentials; of a SIMD's cycles the matrix
+// units are busy in 47% and vector instructions issue in 44%, LDS is active in
+// 24% without conflicts.  Tiles of 64 keys, two in LDS: two workgroups per
+// compute unit; eight waves per block of queries were 4% slower.
 #include "kd_check.h"
 #include "kd_swa.h"
 
