@@ -146,6 +146,14 @@ template <class E>
 __device__ __forceinline__ typename SwaT<E>::Frag swa_ld_mem(const E* row, int ks, int g) {
     return *reinterpret_cast<const typename SwaT<E>::Frag*>(row + (2 * ks + g) * (16 / (int)sizeof(E)));
 }
+// and ld_col's fragment of rows row0 .. from a column in memory (row stride rs)
+template <class E>
+__device__ __forceinline__ typename SwaT<E>::Frag swa_ld_col_mem(const E* col, int64_t rs, int64_t row0, int g) {
+    typename SwaT<E>::Frag x;
+#pragma unroll
+    for (int e = 0; e < SwaT<E>::PR; ++e) x[e] = col[(row0 + 4 * g + (e & 3) + 2 * (e & 4)) * rs];
+    return x;
+}
 template <class E>
 __device__ __forceinline__ typename SwaT<E>::Frag swa_zero() {
     typename SwaT<E>::Frag z;

@@ -69,30 +69,63 @@ __device__ __forceinline__ float swa_dq_near(float delta, const typename SwaT<E>
     return sum;
 }
 
-// dQ (before its scale) of a wave's queries and the sum of P (dP - delta), one
-// key after the other (rare, see its call): keys 0 .. S - 1 and first .. last,
-// each for the queries that see it.
+// dQ (before its scale) of a wave's queries (positions wp0 .. wp0 + 31) and the
+// sum of P (dP - delta) again (rare, see its call): keys 0 .. S - 1 and first ..
+// last, 32 at a time where all queries see all of them, the others one after
+// the other, each for the queries that see it.
 template <class E, int D>
-__device__ __forceinline__ float swa_dq_single(floatx16* acc, const typename SwaT<E>::Frag* q, const typename SwaT<E>::Frag* dO,
+__device__ __forceinline__ float swa_dq_single(floatx16* acc, const E* q, const E* dO,
                                                const E* k, int64_t krs, const E* v, int64_t vrs, int last, int first,
-                                               int pos, int W, int S, float c, float lse2, float delta, int g)
+                                               int wp0, int W, int S, float c, float lse2, float delta, bool few, int lane)
 {
+    typedef SwaT<E> T;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
+    constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    const int g = lane >> 5, pos = wp0 + (lane & 31);
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-    float dsum = 0.f;
+    float dsum = 0.f, part = 0.f;      // (part: of this lane's keys alone)
 #pragma unroll 1
     for (int key = S > 0 ? 0 : first; key <= last; ++key) {
         if (key >= S && key < first) key = first;
-        if (key > last) break;
+        if (key + 31 <= min(wp0, last) && (wp0 + 31 - key < W || key + 32 <= S)) {
+            const int64_t at = key + (lane & 31);
+            floatx16 sc, dp;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sc[r] = 0.f, dp[r] = -delta;
+#pragma unroll
+            for (int ks = 0; ks < NK; ++ks) {
+                sc = T::mma(swa_ld_mem<E>(k + at * krs, ks, g), swa_ld_mem<E>(q, ks, g), sc);
+                dp = T::mma(swa_ld_mem<E>(v + at * vrs, ks, g), swa_ld_mem<E>(dO, ks, g), dp);
+                asm volatile("" : "+v"(sc), "+v"(dp) : : "memory");      // (a few loads at a time)
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -lse2)) * dp[r];
+                part += sc[r];
+            }
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const typename T::Frag p = T::pack(sc, j), rest = T::rest(sc, j, p);
+#pragma unroll
+                for (int i = 0; i < ND; ++i) {
+                    const typename T::Frag x = swa_ld_col_mem<E>(k + 32 * i + (lane & 31), krs, key + (32 / NP) * j, g);
+                    acc[i] = T::mma(x, p, acc[i]);
+                    if (few) acc[i] = T::mma(x, rest, acc[i]);
+                    asm volatile("" : "+v"(acc[i]) : : "memory");
+                }
+            }
+            key += 31;
+            continue;
+        }
         float s = 0.f, dp = 0.f;
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) {
-            s += SwaT<E>::dot(q[ks], swa_ld_mem<E>(k + key * krs, ks, g));
-            dp += SwaT<E>::dot(dO[ks], swa_ld_mem<E>(v + key * vrs, ks, g));
+            s += T::dot(swa_ld_mem<E>(q, ks, g), swa_ld_mem<E>(k + key * krs, ks, g));
+            dp += T::dot(swa_ld_mem<E>(dO, ks, g), swa_ld_mem<E>(v + key * vrs, ks, g));
+            asm volatile("" : "+v"(s), "+v"(dp) : : "memory");
         }
         s += swa_swap(s);
         dp += swa_swap(dp);
@@ -109,7 +142,7 @@ __device__ __forceinline__ float swa_dq_single(floatx16* acc, const typename Swa
                     acc[i][4 * j + e] = fmaf(ds, sees && !swa_alone(pos, W, S) ? (float)x[e] : 0.f, acc[i][4 * j + e]);
             }
     }
-    return dsum;
+    return dsum + part + swa_swap(part);
 }
 
 template <int ND>
@@ -249,10 +282,10 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_dq_ke
     }
     // A hidden key's gradient is 0, and 0 times an infinity or a NaN in its key
     // or value would still reach the queries of its tile: a wave with a result
-    // that is not finite makes it again key by key.
+    // that is not finite makes it again over the keys that each query sees.
     if (__any(!(swa_zero_if_finite<ND>(acc) == 0.f)))
-        dsum = swa_dq_single<E, D>(acc, q, dO, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1),
-                                   pos, a.W, a.S, a.c, lse2, delta, g);
+        dsum = swa_dq_single<E, D>(acc, qrow, (const E*)a.dO + orow, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1),
+                                   wp0, a.W, a.S, a.c, lse2, delta, few, lane);
     if (row >= s.nq) return;
     swa_store_row<E, D>((E*)a.dq + orow, acc, a.scale, g);
     // the sum of P dP: that of P (dP - delta) and delta (P sums to 1).  Queries
@@ -320,17 +353,19 @@ __device__ __forceinline__ void swa_dkv_tile(const E* qt, const E* dt, const flo
     }
 }
 
-// dK (before its scale) and dV of a wave's keys, one query of the group after
-// the other (rare, see its call): rows t0 .. t1 - 1 of G heads.
+// dK (before its scale) and dV of a wave's keys (wk0 .. wk0 + 31) again (rare,
+// see its call): rows t0 .. t1 - 1 of G heads, 32 at a time where all of them
+// see all of the keys, the others one after the other.
 template <class E, int D, class VF>
-__device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const typename SwaT<E>::Frag* k, const VF& v,
+__device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const E* k, const VF& v,
                                                const E* q, int64_t qrs, int64_t qhs, const E* dO, int64_t ors,
-                                               const float2* rows, int64_t rhs, int G, int t0, int t1, int past, int key,
-                                               int W, int S, float c, int lane)
+                                               const float2* rows, int64_t rhs, int G, int t0, int t1, int past, int wk0,
+                                               int W, int S, float c, bool few, int lane)
 {
+    typedef SwaT<E> T;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
-    const int g = lane >> 5;
+    constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    const int g = lane >> 5, key = wk0 + (lane & 31);
     // 32 elements at a time, the scores anew for each: few registers beside k
 #pragma unroll
     for (int i = 0; i < ND; ++i) {
@@ -341,13 +376,44 @@ __device__ __forceinline__ void swa_dkv_single(floatx16* dk, floatx16* dv, const
         for (int h = 0; h < G; ++h)
 #pragma unroll 1
             for (int t = t0; t < t1; ++t) {
+                if (t + 32 <= t1 && past + t >= wk0 + 31 && (past + t + 31 - wk0 < W || wk0 + 32 <= S)) {
+                    const E* qa = q + h * qhs + (int64_t)(t + (lane & 31)) * qrs;
+                    const E* ga = dO + h * D + (int64_t)(t + (lane & 31)) * ors;
+                    floatx16 sc, dp;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] = 0.f, dp[r] = -rows[h * rhs + t + 8 * (r / 4) + 4 * g + r % 4].y;
+#pragma unroll
+                    for (int ks = 0; ks < NK; ++ks) {
+                        sc = T::mma(swa_ld_mem<E>(qa, ks, g), swa_ld_mem<E>(k, ks, g), sc);
+                        dp = T::mma(swa_ld_mem<E>(ga, ks, g), v(ks, lane), dp);
+                        asm volatile("" : "+v"(sc), "+v"(dp) : : "memory");      // (a few loads at a time)
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -rows[h * rhs + t + 8 * (r / 4) + 4 * g + r % 4].x));
+                        dp[r] *= sc[r];
+                    }
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        const typename T::Frag pv = T::pack(sc, j), pk = T::pack(dp, j);
+                        const typename T::Frag ge = swa_ld_col_mem<E>(dO + h * D + 32 * i + (lane & 31), ors, t + (32 / NP) * j, g);
+                        y = T::mma(ge, pv, y);
+                        if (sizeof(E) == 2 && few) y = T::mma(ge, T::rest(sc, j, pv), y);
+                        const typename T::Frag qe = swa_ld_col_mem<E>(q + h * qhs + 32 * i + (lane & 31), qrs, t + (32 / NP) * j, g);
+                        x = T::mma(qe, pk, x);
+                        if (sizeof(E) == 2 && few) x = T::mma(qe, T::rest(dp, j, pk), x);
+                        asm volatile("" : "+v"(x), "+v"(y) : : "memory");
+                    }
+                    t += 31;
+                    continue;
+                }
                 const E* qr = q + h * qhs + t * qrs;
                 const E* gr = dO + h * D + t * ors;
                 const float2 row = rows[h * rhs + t];
                 float s = 0.f, dp = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < NK; ++ks) {
-                    s += SwaT<E>::dot(k[ks], swa_ld_mem<E>(qr, ks, g));
+                    s += SwaT<E>::dot(swa_ld_mem<E>(k, ks, g), swa_ld_mem<E>(qr, ks, g));
                     dp += SwaT<E>::dot(v(ks, lane), swa_ld_mem<E>(gr, ks, g));
                     asm volatile("" : "+v"(s), "+v"(dp) : : "memory");      // (a few loads at a time)
                 }
@@ -486,8 +552,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D <= 256 ? 2 : 1) void kd_swa_dkv_
     }
     // queries that do not see a key, as in dQ
     if (__any(!(swa_zero_if_finite<ND>(dk) + swa_zero_if_finite<ND>(dv) == 0.f)))
-        swa_dkv_single<E, D>(dk, dv, k, v, qf.base, a.qs[1], a.qs[2], of.base, (int64_t)a.Hq * D, rb, a.Tq, GS,
-                             max(0, wk0 - s.past), t1, s.past, key, a.W, a.S, a.c, lane);
+        swa_dkv_single<E, D>(dk, dv, krow, v, qf.base, a.qs[1], a.qs[2], of.base, (int64_t)a.Hq * D, rb, a.Tq, GS,
+                             max(0, wk0 - s.past), t1, s.past, wk0, a.W, a.S, a.c, few, lane);
     // the sinks' part from the queries beyond the window: all threads add the
     // chunks' partial sums, the lanes that hold the keys take them from LDS
     if (s.blk == 0 && a.pslots > 0 && swa_far(a, s.past) < s.nq) {

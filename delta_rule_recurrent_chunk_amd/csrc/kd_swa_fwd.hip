@@ -21,15 +21,18 @@
 
 namespace kd {
 
-// o of a wave's queries, one key after the other (rare, see its call): keys
-// 0 .. S - 1 and first .. last, each for the queries that see it.
+// o of a wave's queries (positions wp0 .. wp0 + 31) again (rare, see its call):
+// keys 0 .. S - 1 and first .. last, 32 at a time where all queries see all of
+// them, the others one after the other, each for the queries that see it.
 template <class E, int D>
 __device__ __forceinline__ void swa_fwd_single(floatx16* o, const typename SwaT<E>::Frag* q, const E* k, int64_t krs,
-                                               const E* v, int64_t vrs, int last, int first, int pos, int W, int S,
-                                               float c, float mu, int g)
+                                               const E* v, int64_t vrs, int last, int first, int wp0, int W, int S,
+                                               float c, float mu, int lane)
 {
+    typedef SwaT<E> T;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = D / SwaT<E>::KC, ND = D / 32;
+    constexpr int NK = D / T::KC, ND = D / 32, NP = 16 / T::PR;
+    const int g = lane >> 5, pos = wp0 + (lane & 31);
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -37,7 +40,24 @@ __device__ __forceinline__ void swa_fwd_single(floatx16* o, const typename SwaT<
 #pragma unroll 1
     for (int key = S > 0 ? 0 : first; key <= last; ++key) {
         if (key >= S && key < first) key = first;
-        if (key > last) break;
+        if (key + 31 <= min(wp0, last) && (wp0 + 31 - key < W || key + 32 <= S)) {
+            floatx16 sc;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sc[r] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < NK; ++ks) sc = T::mma(swa_ld_mem<E>(k + (int64_t)(key + (lane & 31)) * krs, ks, g), q[ks], sc);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c, -mu));
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const typename T::Frag p = T::pack(sc, j);
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+                    o[i] = T::mma(swa_ld_col_mem<E>(v + 32 * i + (lane & 31), vrs, key + (32 / NP) * j, g), p, o[i]);
+            }
+            key += 31;
+            continue;
+        }
         float s = 0.f;
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks) s += SwaT<E>::dot(q[ks], swa_ld_mem<E>(k + key * krs, ks, g));
@@ -172,16 +192,16 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_swa_fwd_k
     l += swa_swap(l);
     // A hidden key has weight 0, and 0 times an infinity or a NaN in its values
     // would still reach the queries of its tile.  A wave with an output that is
-    // not finite makes its outputs again from the maxima and sums it has, key by
-    // key over the keys that each query sees.
+    // not finite makes its outputs again from the maxima and sums it has, over
+    // the keys that each query sees.
     float sum = 0.f;      // (0 times what is not finite is a NaN)
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) sum = fmaf(o[i][r], 0.f, sum);
     if (__any(!(sum == 0.f)))
-        swa_fwd_single<E, D>(o, q, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1), pos, a.W,
-                             a.S, a.c, m == -INFINITY ? 0.f : m, g);
+        swa_fwd_single<E, D>(o, q, kf.base, a.ks[1], vf.base, a.vs[1], min(wp1, s.nk - 1), max(0, wp0 - a.W + 1), wp0, a.W,
+                             a.S, a.c, m == -INFINITY ? 0.f : m, lane);
     if (row >= s.nq) return;
     // a row that sees nothing: o = 0, lse = -infinity
     const bool none = m == -INFINITY && l == 0.f;

@@ -495,9 +495,8 @@ KD_API kd_status kron_delta_rope(const kd_rope_desc *desc, const void *q, const 
  * o = 0 and lse = -infinity.
  * What a query does not see (a key, a value; for the gradients of a key, a
  * query that does not see it) may hold infinities and NaNs.  Rows whose result
- * is not finite are made again pair by pair, which takes up to about 100 times
- * as long as the call otherwise (220 ms for the backward of 8192 tokens without
- * a window, all of dO NaN).
+ * is not finite are made again with care, which takes 4 to 20 times as long as
+ * the call otherwise where all of them are.
  *  * q: [B, Tq, Hq, d], k, v: [B, Tk, Hkv, d] in desc->dtype, strides over
  *    batch, token and head in elements (multiples of 16 bytes), contiguous
  *    last dimension; o, dO, dq: contiguous [B, Tq, Hq, d]; dk, dv: contiguous

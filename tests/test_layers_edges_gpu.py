@@ -226,6 +226,53 @@ def test_glr_step_past_32_bits_of_elements():
     assert all((t[b] == 1).all() for t in (y, h) for b in range(B))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,d,W,S", [(600, 700, 4, 1, 64, 300, 40), (333, 333, 2, 2, 128, 1000, 0), (500, 460, 2, 1, 32, 150, 64),
+                                                (900, 900, 2, 1, 128, 97, 3)])
+def test_swa_results_made_again_are_right(Tq, Tk, Hq, Hkv, d, W, S, dtype):
+    """Where a wave's result is not finite it is made again, in groups of 32 fully visible keys or queries and single
+    ones: what does not see the bad ones, and what of the output they do not touch, is as without them."""
+    import delta_rule_recurrent_chunk_amd as kd
+    _torch()
+    (q, qv), (k, kv), (v, vv), (dO, ov) = swa_inputs(1, Tq, Tk, Hq, Hkv, d, dtype, Tq + Tk + d)
+    val, err = R.attention_heads(qv[0], kv[0], vv[0], W, S, 1 / np.sqrt(d), ov[0], R.unit(dtype))
+    vis = R.visible(Tq, Tk, W, S)
+    nan, inf = float("nan"), float("inf")
+    for at, value in ((0, nan), (S + 3, inf), (Tk // 2, nan), (Tk - 40, inf), (Tk - 1, nan)):
+        print("case", (Tq, Tk, Hq, Hkv, d, W, S), dtype, at, value, flush=True)
+        sees = vis[:, at]
+        bad = v.clone()
+        bad[0, at, :, 1::3] = value
+        o, lse = kd.swa_fwd(q, k, bad, W, S, return_lse=True)
+        got, ref = host(o[0]), val["o"].copy()
+        rest = [e for e in range(d) if e % 3 != 1]
+        check("hidden from", got[~sees], ref[~sees], err["o"][~sees])
+        check("other elements", got[sees][..., rest], ref[sees][..., rest], err["o"][sees][..., rest])
+        assert not np.isfinite(got[sees][..., 1::3]).any()
+        bad = k.clone()
+        bad[0, at] = value
+        o, lse = kd.swa_fwd(q, bad, v, W, S, return_lse=True)
+        g = kd.swa_bwd(q, bad, v, o, lse, dO, W, S)
+        check("key hidden", host(o[0])[~sees], ref[~sees], err["o"][~sees])
+        check("dq", host(g["dq"][0])[~sees], val["dq"][~sees], err["dq"][~sees])
+        far = ~vis[sees].any(0)          # keys that no query of the bad one sees
+        far[at] = False
+        for n in ("dk", "dv"):
+            check(n, host(g[n][0])[far], val[n][far], err[n][far])
+    o, lse = kd.swa_fwd(q, k, v, W, S, return_lse=True)
+    for t, value in ((0, inf), (Tq // 3, nan), (Tq // 2 + 31, inf), (Tq - 1, nan)):
+        bad = dO.clone()
+        bad[0, t, :, ::5] = value
+        g = kd.swa_bwd(q, k, v, o, lse, bad, W, S)
+        others = np.arange(Tq) != t
+        check("dq", host(g["dq"][0])[others], val["dq"][others], err["dq"][others])
+        far = ~vis[t]
+        for n in ("dk", "dv"):
+            check(n, host(g[n][0])[far], val[n][far], err[n][far])
+        rest = [e for e in range(d) if e % 5]
+        check("dv", host(g["dv"][0])[..., rest], val["dv"][..., rest], err["dv"][..., rest])
+
+
 # ------------------------------------------------------------- fused tensors
 @pytest.mark.parametrize("order", ["bthd", "bhtd", "tbhd"])
 @pytest.mark.parametrize("Hq,Hk", [(4, 2), (1, 1), (3, 1), (1, 2)])
