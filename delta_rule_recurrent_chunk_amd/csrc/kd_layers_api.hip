@@ -39,80 +39,19 @@ size_t swa_decode_part_bytes(int B, int Hq, int Hkv, int d, int seen);
 
 namespace {
 
+using kd::any_overlap;
+using kd::distinct;
 using kd::grid_fits;
+using kd::interleaved_apart;
 using kd::misaligned;
 using kd::overlap;
 using kd::Range;
 using kd::range_of;
+using kd::span;
 using kd::up256;
 
 bool known(int dtype) { return dtype == KD_F32 || dtype == KD_BF16; }
 size_t es_of(int dtype) { return dtype == KD_BF16 ? 2 : 4; }
-
-// Bytes a strided [n0, n1, n2, d] tensor spans from its first element; false
-// for a negative stride or one that does not keep 16-byte pieces aligned
-// (align16), or an extent beyond 2^62.
-bool span(const int64_t st[3], int64_t n0, int64_t n1, int64_t n2, int64_t d, size_t es, bool align16, size_t* bytes) {
-    const int64_t n[3] = {n0, n1, n2};
-    if (n0 == 0 || n1 == 0 || n2 == 0) {
-        *bytes = 0;
-        return true;
-    }
-    __int128 last = d;
-    for (int i = 0; i < 3; ++i) {
-        if (st[i] < 0) return false;
-        if (align16 && n[i] > 1 && (st[i] * (int64_t)es) % 16 != 0) return false;
-        last += (__int128)st[i] * (n[i] - 1);
-    }
-    if (last * es > ((__int128)1 << 62)) return false;
-    *bytes = (size_t)(last * es);
-    return true;
-}
-
-// Whether no two elements of a strided [n0, n1, n2, d] tensor share an address
-// (an output that is written as such): in the order of their strides, every
-// dimension steps over all that the smaller ones span.
-bool distinct(const int64_t st[3], int64_t n0, int64_t n1, int64_t n2, int64_t d) {
-    int64_t n[3] = {n0, n1, n2}, s[3] = {st[0], st[1], st[2]};
-    if (n0 == 0 || n1 == 0 || n2 == 0) return true;
-    __int128 ext = d;
-    for (int k = 0; k < 3; ++k) {
-        int at = -1;
-        for (int i = 0; i < 3; ++i)
-            if (n[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
-        if (at < 0) return true;
-        if (s[at] < ext) return false;
-        ext += (__int128)s[at] * (n[at] - 1);
-        n[at] = 1;
-    }
-    return true;
-}
-
-// Whether two tensors of one shape and the same strides, `delta` elements
-// apart, share no address although their spans interleave: the shift falls in
-// the gap that one dimension's stride leaves behind the smaller dimensions.
-bool interleaved_apart(const int64_t st[3], int64_t n0, int64_t n1, int64_t n2, int64_t d, int64_t delta) {
-    const int64_t n[3] = {n0, n1, n2};
-    if (delta < 0) delta = -delta;
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        __int128 ext = d;      // what the dimensions of smaller stride span
-        for (int j = 0; j < 3; ++j)
-            if (j != i && n[j] > 1 && st[j] < st[i]) ext += (__int128)st[j] * (n[j] - 1);
-        if (delta >= ext && delta + ext <= st[i]) return true;
-    }
-    return false;
-}
-
-bool any_overlap(const Range* outs, int no, const Range* ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        for (int j = 0; j < ni; ++j)
-            if (overlap(outs[i], ins[j])) return true;
-        for (int j = i + 1; j < no; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-    }
-    return false;
-}
 
 kd_status done(hipError_t e) { return e == hipSuccess ? KD_OK : KD_ERR_LAUNCH; }
 

@@ -589,6 +589,85 @@ KD_API kd_status kron_delta_swa_cache_store(const kd_swa_cache_desc *desc, int32
                          const int64_t k_stride[3], const int64_t v_stride[3], const int32_t *lens,
                          void *k_cache, void *v_cache, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A paged cache, and attention of a batch over a prefix that it shares: the
+ * serving side of the hybrid's attention layers where many requests start
+ * with one prompt.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * k_pages and v_pages are [pages, page, Hkv, d] in desc->dtype (strides over
+ * page, slot and head in elements, multiples of 16 bytes; contiguous last
+ * dimension; d a multiple of 16 bytes).  Own token i of sequence b lies in slot
+ * i % page of page table[b * table_stride + i / page], i / page < width.
+ * Sequences have either one row each in a call (T = B, cu_seqlens NULL), or
+ * cu_seqlens[b + 1] - cu_seqlens[b] packed rows (offsets int32 [B + 1] on the
+ * device, non-decreasing, at most T).  lens[b] (int32, on the device, not
+ * changed) is the number of own tokens before the call's: row r of sequence b
+ * is own token lens[b] + r.  A negative lens[b] marks an unused sequence.
+ * Rows that no sequence holds are left unwritten.
+ */
+typedef struct {
+    int32_t B, T, Hq, Hkv, d;
+    int32_t dtype;             /* kd_dtype */
+    int32_t page, pages;       /* slots of a page, pages of the cache */
+    int32_t width;             /* entries of a table row */
+    int32_t rot, layout;       /* paged_append: as kron_delta_rope; rot 0: nothing is turned */
+    float rope_scale;
+    int64_t offset;            /* paged_append: position of own token 0 */
+    int32_t prefix;            /* prefix_attn: keys of the prefix */
+    int32_t prefix_width;      /* prefix_attn: entries of its table */
+    float scale;               /* prefix_attn: > 0 */
+    int64_t k_stride[3], v_stride[3];
+    int64_t table_stride;
+} kd_paged_desc;
+
+/*
+ * New keys and values into the cache: k turned to position offset + lens[b] + r
+ * (as kron_delta_rope) and rounded to the cache's type, v as it is.  With
+ * Hq > 0 the rows' queries are turned with them: q_out.
+ *  * q [T, Hq, d], k, v [T, Hkv, d]: strides over token and head in elements
+ *    (multiples of 16 bytes) in in_stride (q, k, v); q_out [T, Hq, d]
+ *    contiguous.  d <= 256, rot even, |offset| <= 2^40.
+ *  * Tokens without a page (a table entry outside [0, pages), or past the
+ *    table's width) are not stored; their queries are turned.  Nothing of an
+ *    unused sequence is stored; its rows of q_out are 0.
+ *  * Two tokens of one call that the table sends to one slot: either may stay.
+ */
+KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *q, const void *k, const void *v,
+                         const int64_t in_stride[6], void *k_pages, void *v_pages, const int32_t *table,
+                         const int32_t *lens, const int32_t *cu_seqlens, const double *freqs, void *q_out,
+                         void *stream);
+
+/*
+ * Attention over a shared prefix and each sequence's own keys: row r of
+ * sequence b sees the prefix's keys 0 .. prefix - 1 (key i in slot i % page of
+ * page prefix_table[i / page]) and the own keys 0 .. lens[b] + r (those of the
+ * call's rows are in the cache already, see kron_delta_paged_append),
+ *     o = sum_s softmax_s(scale q . k_s) v_s,   lse = log sum_s exp(scale q . k_s).
+ *  * q [T, Hq, d]: strides over token and head in elements (multiples of 16
+ *    bytes); o [T, Hq, d] contiguous; lse [Hq, T] fp32 or NULL.  Query head h
+ *    reads key head h / (Hq / Hkv).  d in {32, 64, 128}; bf16, or fp32 (a
+ *    diagnostic precision).  prefix <= 2^30 and prefix_width * page.
+ *  * A sequence with prefix 0 has its own keys alone.  Own keys past the
+ *    table's width are not seen.  Rows of unused sequences, and rows that see
+ *    nothing, get o = 0 and lse = -infinity.  Page ids outside [0, pages) are
+ *    clamped into that range where they are read.
+ *  * What a row does not see (later rows' keys, slots behind the last key) may
+ *    hold infinities and NaNs; those that are seen show as IEEE arithmetic has
+ *    them.
+ *  * ws: kron_delta_prefix_attn_workspace_bytes(desc, cu_seqlens != NULL)
+ *    bytes, contents on entry ignored.  Calls that overlap on the device must
+ *    not share it.
+ * Results do not depend on how the work is scheduled: repeated calls agree bit
+ * for bit.
+ */
+KD_API size_t kron_delta_prefix_attn_workspace_bytes(const kd_paged_desc *desc, int packed);
+KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q, const int64_t q_stride[2],
+                         const void *k_pages, const void *v_pages, const int32_t *prefix_table,
+                         const int32_t *table, const int32_t *lens, const int32_t *cu_seqlens,
+                         void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
