@@ -12,7 +12,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkrondelta.so")
 SOURCES = ["kd_api.hip", "kd_fwd.hip", "kd_fwd16.hip", "kd_fwd16s.hip", "kd_bwd.hip", "kd_bwd_token.hip", "kd_decode.hip", "kd_gdn2.hip",
            "kd_mixer.hip", "kd_layers_api.hip", "kd_glr.hip", "kd_rope.hip", "kd_swa_fwd.hip", "kd_swa_bwd.hip",
-           "kd_swa_decode.hip", "kd_paged_api.hip", "kd_paged.hip", "kd_prefix.hip"]
+           "kd_swa_decode.hip", "kd_paged_api.hip", "kd_paged.hip", "kd_prefix.hip",
+           "kd_gdr_api.hip", "kd_gdr_fwd.hip", "kd_gdr_bwd.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

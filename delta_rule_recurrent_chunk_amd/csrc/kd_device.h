@@ -43,6 +43,17 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// One 16-byte load per lane straight to LDS at byte address `to` (wave-uniform,
+// in the first 64 KB; lane i fills to + 16 i, lanes that are masked off fill
+// nothing).  In flight until the wave has waited for its vector memory
+// operations: the builtin would make every LDS read wait.
+__device__ __forceinline__ void load_lds16(uint32_t to, const void* src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
 // A zero the compiler cannot see through: adding it to a per-lane index inside
 // a loop keeps the addresses derived from that index from being hoisted out of
 // the loop (where they would hold registers across the whole loop).

@@ -1,0 +1,280 @@
+// kd_gdr.h -- building blocks of the gated delta rule, gfx950.
+//
+// Per value head the state is S [dv x dk] and for every token
+//     Sb = e^g S;  u = beta (v - Sb k);  S = Sb + u k^T;  o = scale S q.
+// Over a chunk of C = 64 tokens, with b the running sum of g inside it and
+// Gam_rs = e^(b_r - b_s) for s <= r (never a quotient of two decays):
+//     T = tril(beta_r Gam_rs k_r.k_s, -1),  A = (I + T)^-1,  P = scale tril(Gam_rs q_r.k_s)
+//     U = A (beta (V - e^b K S0^T)),   O = scale e^b Q S0^T + P U,
+//     S_C = e^bC S0 + U^T (e^(bC - b) K).
+// A and P do not depend on the state: a first kernel makes them for all chunks
+// at once, a second one passes over the chunks with the state in registers.
+// The columns of S^T (values) do not mix, so every wave of the pass owns 16 of
+// them and needs nothing from another one.
+//
+// 16x16x32 products (kd_device.h).  bf16: what is not a rounded input (S, U and
+// A) goes through as a rounded part and its remainder, 16 bits in all, so the
+// states keep nearly fp32's precision (2^-17 per use; P, which only reaches o,
+// is rounded).  fp32: the same fragments through eight fp32 products.
+#pragma once
+
+#include "kd_device.h"
+#include "kd_swa.h"
+
+namespace kd {
+
+constexpr int GDR_C = 64;              // tokens of a chunk
+constexpr int GDR_BLOCKS = 6;          // 16 x 32 blocks of a lower triangular 64 x 64 matrix that hold anything
+constexpr int GDR_VEC = 5 * 64;        // floats of a chunk's gate factors
+
+typedef float floatx8 __attribute__((ext_vector_type(8)));
+
+struct GdrArgs {
+    const void *q, *k, *v, *g, *beta;          // g, beta [B, T, Hv]
+    int64_t qs[3], ks[3], vs[3];               // strides over batch, token, head
+    const float* S0;                           // [B, Hv, dv, dk] or null
+    void* o;                                   // [B, T, Hv, dv]
+    float* ST;                                 // or null
+    void* hs;                                  // states entering every chunk [slots, Hv, dv, dk], or null
+    // backward
+    const void* dO;
+    const float* dST;
+    void *dq, *dk_, *dv_, *dg, *dbeta;
+    float* dS0;
+    void *ds, *x;                              // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv]
+    // workspace of both
+    void* rec;                                 // the chunks' matrices, in blocks
+    float* vec;                                // and gate factors
+    const int* cu;
+    int B, T, Hk, Hv, dk, dv;                  // packed: B sequences in T rows
+    int slots, gates32;
+    float scale;
+};
+
+// Parts of a chunk's record, GDR_BLOCKS blocks each (bf16; fp32 has no second parts).
+enum { GDR_A, GDR_A2, GDR_P, GDR_AT, GDR_AT2, GDR_PT, GDR_PARTS };
+
+// What a chunk slot holds.  Batched: chunk slot % NC of batch element slot / NC.
+// Packed: sequence s owns the slots cu[s] / 64 + s onwards (kd_swa.h).
+struct GdrChunk {
+    int seq, n, first;        // sequence, chunks before this one, first row within batch element / packed rows
+    int rows;                 // 1 .. 64
+    int64_t base;             // batch element
+};
+__device__ __forceinline__ int gdr_chunks(int T) { return (T + GDR_C - 1) / GDR_C; }
+
+// First row, rows and first slot of a sequence.
+struct GdrSeq {
+    int row0, T, slot0;
+    int64_t b;
+};
+__device__ __forceinline__ GdrSeq gdr_seq(const GdrArgs& a, int s) {
+    GdrSeq r;
+    if (a.cu) {
+        r.row0 = min(max(a.cu[s], 0), a.T);
+        r.T = min(max(a.cu[s + 1], r.row0), a.T) - r.row0;
+        r.slot0 = r.row0 / GDR_C + s;
+        r.b = 0;
+    } else {
+        r.row0 = 0;
+        r.T = a.T;
+        r.slot0 = s * gdr_chunks(a.T);
+        r.b = s;
+    }
+    return r;
+}
+// The chunk in a slot, false when it holds none.  The whole wave calls it.
+__device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c) {
+    if (!a.cu) {
+        const int nc = gdr_chunks(a.T);
+        c.seq = slot / nc;
+        c.n = slot - c.seq * nc;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int n = 0;
+        for (int i = 0; i < a.B; i += 64) {
+            const int at = i + lane;
+            n += __popcll(__ballot(at < a.B && min(max(a.cu[min(at, a.B)], 0), a.T) / GDR_C + at <= slot));
+        }
+        if (n == 0) return false;
+        c.seq = n - 1;
+    }
+    const GdrSeq s = gdr_seq(a, c.seq);
+    if (a.cu) c.n = slot - s.slot0;
+    c.first = s.row0 + c.n * GDR_C;
+    c.rows = min(s.T - c.n * GDR_C, GDR_C);
+    c.base = s.b;
+    return c.rows > 0;
+}
+
+template <class E>
+struct GdrT;
+
+template <>
+struct GdrT<__bf16> {
+    typedef bf16x8 Frag;
+    static constexpr bool TWO = true;
+    static __device__ __forceinline__ floatx4 mma(Frag a, Frag b, floatx4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ Frag pack(floatx4 x, floatx4 y) {
+        return Frag{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3], (__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+    }
+    // what the packing rounded away
+    static __device__ __forceinline__ Frag rest(floatx4 x, floatx4 y, Frag p) {
+        Frag r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = (__bf16)(x[e] - (float)p[e]), r[4 + e] = (__bf16)(y[e] - (float)p[4 + e]);
+        return r;
+    }
+    static __device__ __forceinline__ Frag ld(const __bf16* p) { return *reinterpret_cast<const Frag*>(p); }
+    static __device__ __forceinline__ void st(__bf16* p, Frag f) { *reinterpret_cast<Frag*>(p) = f; }
+    // natural fragment of a tile's row r: columns 32 ks + 8 g ..
+    template <int D>
+    static __device__ __forceinline__ Frag ld_row(const __bf16* tile, int r, int ks, int g) {
+        return ld(tile + SwaTile<__bf16, D>::off(r, 4 * ks + g));
+    }
+    // A operand with K = the tile's rows 32 j + {4g .., 16 + 4g ..} and row m =
+    // column c0 + 8 (m / 4) + m % 4 (kd_device.h's transposed reads, the named
+    // pieces 8 columns apart)
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col8(const __bf16* tile, int j, int c0, int lane) {
+        const int l = lane & 15, r = 32 * j + 4 * (lane >> 4) + (l >> 2), c = c0 + 8 * (l & 3);
+        return tr<D>(tile, r, c);
+    }
+    // the same with row m = column c0 + m
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col(const __bf16* tile, int j, int c0, int lane) {
+        const int l = lane & 15, r = 32 * j + 4 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
+        return tr<D>(tile, r, c);
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag tr(const __bf16* tile, int r, int c) {
+        typedef SwaTile<__bf16, D> TL;
+        typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+        const __bf16* lo = tile + TL::off(r, c / 8) + c % 8;
+        const __bf16* hi = tile + TL::off(r + 16, c / 8) + c % 8;
+        const s16x4 x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(lo)));
+        const s16x4 y = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(hi)));
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+template <>
+struct GdrT<float> {
+    typedef floatx8 Frag;
+    static constexpr bool TWO = false;
+    static __device__ __forceinline__ floatx4 mma(Frag a, Frag b, floatx4 c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag pack(floatx4 x, floatx4 y) {
+        return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    }
+    static __device__ __forceinline__ Frag rest(floatx4, floatx4, Frag p) { return p; }
+    static __device__ __forceinline__ Frag ld(const float* p) {
+        const floatx4 x = *reinterpret_cast<const floatx4*>(p), y = *reinterpret_cast<const floatx4*>(p + 4);
+        return pack(x, y);
+    }
+    static __device__ __forceinline__ void st(float* p, Frag f) {
+        *reinterpret_cast<floatx4*>(p) = floatx4{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<floatx4*>(p + 4) = floatx4{f[4], f[5], f[6], f[7]};
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag ld_row(const float* tile, int r, int ks, int g) {
+        typedef SwaTile<float, D> TL;
+        return pack(*reinterpret_cast<const floatx4*>(tile + TL::off(r, 8 * ks + 2 * g)),
+                    *reinterpret_cast<const floatx4*>(tile + TL::off(r, 8 * ks + 2 * g + 1)));
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col8(const float* tile, int j, int c0, int lane) {
+        const int m = lane & 15;
+        return at<D>(tile, j, c0 + 8 * (m >> 2) + (m & 3), lane);
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag ld_col(const float* tile, int j, int c0, int lane) {
+        return at<D>(tile, j, c0 + (lane & 15), lane);
+    }
+    template <int D>
+    static __device__ __forceinline__ Frag at(const float* tile, int j, int c, int lane) {
+        typedef SwaTile<float, D> TL;
+        const int r = 32 * j + 4 * (lane >> 4);
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = tile[TL::off(r + (e & 3) + 4 * (e & 4), c / 4) + c % 4];
+        return f;
+    }
+};
+
+// x y where x is a packed tile with its remainder and y exact in the type
+template <class E>
+__device__ __forceinline__ floatx4 gdr_mma2(typename GdrT<E>::Frag a, typename GdrT<E>::Frag a2, typename GdrT<E>::Frag b, floatx4 c) {
+    c = GdrT<E>::mma(a, b, c);
+    if (GdrT<E>::TWO) c = GdrT<E>::mma(a2, b, c);
+    return c;
+}
+template <class E>
+__device__ __forceinline__ floatx4 gdr_mma2b(typename GdrT<E>::Frag a, typename GdrT<E>::Frag b, typename GdrT<E>::Frag b2, floatx4 c) {
+    c = GdrT<E>::mma(a, b, c);
+    if (GdrT<E>::TWO) c = GdrT<E>::mma(a, b2, c);
+    return c;
+}
+// both with remainders (their product is left out: 2^-18)
+template <class E>
+__device__ __forceinline__ floatx4 gdr_mma3(typename GdrT<E>::Frag a, typename GdrT<E>::Frag a2, typename GdrT<E>::Frag b,
+                                            typename GdrT<E>::Frag b2, floatx4 c) {
+    c = GdrT<E>::mma(a, b, c);
+    if (GdrT<E>::TWO) {
+        c = GdrT<E>::mma(a2, b, c);
+        c = GdrT<E>::mma(a, b2, c);
+    }
+    return c;
+}
+
+// Block (i, j) of a lower triangular matrix: rows 16 i .., columns 32 j ..;
+// blocks (0,0) (1,0) (2,0) (2,1) (3,0) (3,1).  In a block lane l holds row l %
+// 16 and columns 16 h + 4 (l / 16) + r at element 4 h + r: the order in which
+// two accumulator tiles of 16 rows each are packed.  Its transpose has the
+// blocks (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
+__device__ __forceinline__ constexpr int gdr_block(int i, int j) { return i < 2 ? i : 2 * i - 2 + j; }
+__device__ __forceinline__ constexpr int gdr_block_t(int i, int j) { return i < 2 ? 2 * i + j : 2 + i; }
+
+template <class E>
+__host__ __device__ constexpr int gdr_part() { return GDR_BLOCKS * 512; }      // elements of a part
+
+// Stages rows of K or Q (64 of them, clamped to the sequence's last) in an LDS
+// tile; columns past dk keep what the tile holds (zeros).
+template <class E, int DK>
+__device__ __forceinline__ void gdr_fetch(E* tile, const E* rows, int64_t rs, int row, int last, int dk, int tid, int w) {
+    typedef SwaTile<E, DK> TL;
+    constexpr int STEP = 256 / TL::CPR, NL = 64 / STEP;
+    const int r0 = tid / TL::CPR, ch = tid % TL::CPR;
+    const uint32_t to = lds_address(tile) + 1024 * w;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int r = r0 + i * STEP, x = (ch ^ TL::swz(r)) * TL::EPC;
+        if (x < dk) load_lds16(to + i * 4096, rows + (int64_t)min(row + r, last) * rs + x);
+    }
+}
+
+__device__ __forceinline__ float gdr_gate(const void* p, int64_t i, int gates32, const __bf16*) {
+    return gates32 ? ((const float*)p)[i] : (float)((const __bf16*)p)[i];
+}
+__device__ __forceinline__ float gdr_gate(const void* p, int64_t i, int, const float*) { return ((const float*)p)[i]; }
+
+// Running sum of the log decays (base 2) over the wave's 64 lanes, in 64 bits: decays
+// between two tokens are exp of a difference, which far sums would spoil.  Log
+// decays below -120 are e^-120 = 0 in fp32, and -infinity among them would
+// make NaNs of differences.
+__device__ __forceinline__ double gdr_cumsum(float g, int lane) {
+    double b = (double)(g < -120.f ? -120.f : g) * 1.4426950408889634;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+        const double x = __shfl_up(b, s);
+        if (lane >= s) b += x;
+    }
+    return b;
+}
+
+}  // namespace kd

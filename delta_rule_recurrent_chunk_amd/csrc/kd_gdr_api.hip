@@ -1,0 +1,209 @@
+// kd_gdr_api.hip -- the C ABI of the gated delta rule: argument checks,
+// workspace sizing and dispatch on the caller's stream.  No allocation, no
+// synchronisation.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "kd_check.h"
+#include "kd_gdr.h"
+#include "kron_delta.h"
+
+namespace kd {
+size_t gdr_rec_bytes(int bf16, bool bwd);
+int64_t gdr_pass_grid(int64_t items, int& run);
+hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st);
+hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st);
+hipError_t launch_gdr_step(int bf16, const GdrArgs& a, hipStream_t st);
+}  // namespace kd
+
+namespace {
+
+using kd::any_overlap;
+using kd::grid_fits;
+using kd::misaligned;
+using kd::overlap;
+using kd::Range;
+using kd::range_of;
+using kd::span;
+using kd::up256;
+
+bool known(int dtype) { return dtype == KD_F32 || dtype == KD_BF16; }
+size_t es_of(int dtype) { return dtype == KD_BF16 ? 2 : 4; }
+kd_status done(hipError_t e) { return e == hipSuccess ? KD_OK : KD_ERR_LAUNCH; }
+
+struct GdrSizes {
+    size_t q, k, v, o, qg, kg, gate, state, slots;      // bytes (spanned by the inputs, contiguous others), chunk slots
+};
+
+kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
+    if (!d) return KD_ERR_NULL;
+    if (!known(d->dtype)) return KD_ERR_DTYPE;
+    if (d->B < 1 || d->T < 0 || d->T > (1 << 29) || d->Hk < 1 || d->Hv < 1 || d->Hv > 65535 || d->Hv % d->Hk != 0 ||
+        d->dk < 8 || d->dk > KRON_DELTA_GDR_MAX_DK || d->dk % 8 != 0 || d->dv < 8 || d->dv > KRON_DELTA_GDR_MAX_DV ||
+        d->dv % 8 != 0 || !isfinite(d->scale) || d->B > (packed ? 1 << 24 : 65535))
+        return KD_ERR_SHAPE;
+    const size_t es = es_of(d->dtype);
+    const int64_t nb = packed ? 1 : d->B;
+    if (!span(d->q_stride, nb, d->T, d->Hk, d->dk, es, true, &s->q) || !span(d->k_stride, nb, d->T, d->Hk, d->dk, es, true, &s->k) ||
+        !span(d->v_stride, nb, d->T, d->Hv, d->dv, es, true, &s->v))
+        return KD_ERR_SHAPE;
+    const __int128 rows = (__int128)nb * d->T;
+    const __int128 slots = packed ? (__int128)d->T / 64 + d->B : (__int128)d->B * ((d->T + 63) / 64);
+    if (slots > (1 << 30) || rows * d->Hv * d->dv * es > ((__int128)1 << 60) ||
+        slots * d->Hv * d->dv * d->dk * es > ((__int128)1 << 60))
+        return KD_ERR_SHAPE;
+    s->o = (size_t)(rows * d->Hv * d->dv * es);
+    s->qg = s->kg = (size_t)(rows * d->Hk * d->dk * es);
+    s->gate = (size_t)(rows * d->Hv * (d->gates32 ? 4 : es));
+    s->state = (size_t)d->B * d->Hv * d->dv * d->dk * 4;
+    s->slots = (size_t)slots;
+    int run;
+    if (!grid_fits((int64_t)s->slots * d->Hv, 64) || !grid_fits((int64_t)s->slots * d->Hk, 512) ||
+        !grid_fits(kd::gdr_pass_grid((int64_t)d->B * d->Hv * ((d->dv + 63) / 64), run), 256))
+        return KD_ERR_SHAPE;
+    return KD_OK;
+}
+
+// Offsets of the workspace's parts: matrices, gate factors, dS, X.
+struct GdrSpace {
+    size_t vec, ds, x, bytes;
+};
+GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool bwd) {
+    const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
+    GdrSpace w;
+    w.vec = up256(n * kd::gdr_rec_bytes(d->dtype == KD_BF16, bwd));
+    w.ds = w.vec + up256(n * kd::GDR_VEC * 4);
+    w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
+    w.bytes = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    return w;
+}
+
+kd::GdrArgs gdr_args(const kd_gdr_desc* d, const GdrSizes& s, const void* q, const void* k, const void* v, const void* g,
+                     const void* beta, const int32_t* cu) {
+    kd::GdrArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.beta = beta;
+    for (int i = 0; i < 3; ++i) {
+        a.qs[i] = d->q_stride[i];
+        a.ks[i] = d->k_stride[i];
+        a.vs[i] = d->v_stride[i];
+    }
+    a.cu = cu;
+    a.B = d->B;
+    a.T = d->T;
+    a.Hk = d->Hk;
+    a.Hv = d->Hv;
+    a.dk = d->dk;
+    a.dv = d->dv;
+    a.slots = (int)s.slots;
+    a.gates32 = d->gates32 != 0;
+    a.scale = d->scale;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc* d, int packed, int backward) {
+    GdrSizes s;
+    if (check_gdr(d, packed != 0, &s) != KD_OK) return 0;
+    return gdr_space(d, s, backward != 0).bytes;
+}
+
+kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
+                             const void* g, const void* beta, const float* S0, void* o, float* ST, void* hs, void* ws,
+                             size_t ws_bytes, void* stream) {
+    GdrSizes s;
+    const kd_status st = check_gdr(d, cu != nullptr, &s);
+    if (st != KD_OK) return st;
+    if (d->T > 0 && (!q || !k || !v || !g || !beta || !o)) return KD_ERR_NULL;
+    const void* ptrs[] = {q, k, v, g, beta, S0, o, ST, hs, ws};
+    for (const void* p : ptrs)
+        if (misaligned(p)) return KD_ERR_ALIGN;
+    if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
+    const GdrSpace w = gdr_space(d, s, false);
+    const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
+    const Range ins[] = {range_of(q, s.q),         range_of(k, s.k),       range_of(v, s.v),
+                         range_of(g, s.gate),      range_of(beta, s.gate), range_of(S0, S0 ? s.state : 0),
+                         range_of(cu, cu ? (size_t)(d->B + 1) * 4 : 0)};
+    const Range outs[] = {range_of(o, s.o), range_of(ST, ST ? s.state : 0), range_of(hs, hs ? hsb : 0), range_of(ws, ws ? w.bytes : 0)};
+    if (any_overlap(outs, 4, ins, 7)) return KD_ERR_ALIAS;
+    if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return KD_ERR_WORKSPACE;
+    if (d->T == 0 && !ST) return KD_OK;
+    kd::GdrArgs a = gdr_args(d, s, q, k, v, g, beta, cu);
+    a.S0 = S0;
+    a.o = o;
+    a.ST = ST;
+    a.hs = hs;
+    a.rec = ws;
+    a.vec = (float*)((char*)ws + w.vec);
+    return done(kd::launch_gdr_fwd(d->dtype == KD_BF16, a, (hipStream_t)stream));
+}
+
+kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
+                             const void* g, const void* beta, const void* hs, const void* dO, const float* dST, void* dq,
+                             void* dk, void* dv, void* dg, void* dbeta, float* dS0, void* ws, size_t ws_bytes,
+                             void* stream) {
+    GdrSizes s;
+    const kd_status st = check_gdr(d, cu != nullptr, &s);
+    if (st != KD_OK) return st;
+    if (d->T > 0 && (!q || !k || !v || !g || !beta || !hs || !dO || !dq || !dk || !dv || !dg || !dbeta)) return KD_ERR_NULL;
+    const void* ptrs[] = {q, k, v, g, beta, hs, dO, dST, dq, dk, dv, dg, dbeta, dS0, ws};
+    for (const void* p : ptrs)
+        if (misaligned(p)) return KD_ERR_ALIGN;
+    if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
+    const GdrSpace w = gdr_space(d, s, true);
+    const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
+    const Range ins[] = {range_of(q, s.q),    range_of(k, s.k),       range_of(v, s.v),
+                         range_of(g, s.gate), range_of(beta, s.gate), range_of(hs, hs ? hsb : 0),
+                         range_of(dO, s.o),   range_of(dST, dST ? s.state : 0), range_of(cu, cu ? (size_t)(d->B + 1) * 4 : 0)};
+    const Range outs[] = {range_of(dq, s.qg),   range_of(dk, s.kg),      range_of(dv, s.o),
+                          range_of(dg, s.gate), range_of(dbeta, s.gate), range_of(dS0, dS0 ? s.state : 0),
+                          range_of(ws, ws ? w.bytes : 0)};
+    if (any_overlap(outs, 7, ins, 9)) return KD_ERR_ALIAS;
+    if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return KD_ERR_WORKSPACE;
+    if (d->T == 0 && !dS0) return KD_OK;
+    kd::GdrArgs a = gdr_args(d, s, q, k, v, g, beta, cu);
+    a.hs = const_cast<void*>(hs);
+    a.dO = dO;
+    a.dST = dST;
+    a.dq = dq;
+    a.dk_ = dk;
+    a.dv_ = dv;
+    a.dg = dg;
+    a.dbeta = dbeta;
+    a.dS0 = dS0;
+    a.rec = ws;
+    a.vec = (float*)((char*)ws + w.vec);
+    a.ds = (char*)ws + w.ds;
+    a.x = (char*)ws + w.x;
+    return done(kd::launch_gdr_bwd(d->dtype == KD_BF16, a, (hipStream_t)stream));
+}
+
+kd_status kron_delta_gdr_step(const kd_gdr_desc* d, const void* q, const void* k, const void* v, const void* g,
+                              const void* beta, const float* S_in, void* o, float* S_out, void* stream) {
+    GdrSizes s;
+    const kd_status st = check_gdr(d, false, &s);
+    if (st != KD_OK) return st;
+    if (d->T != 1) return KD_ERR_SHAPE;
+    if (!q || !k || !v || !g || !beta || !S_in || !o || !S_out) return KD_ERR_NULL;
+    const void* ptrs[] = {q, k, v, g, beta, S_in, o, S_out};
+    for (const void* p : ptrs)
+        if (misaligned(p)) return KD_ERR_ALIGN;
+    const Range ins[] = {range_of(q, s.q),    range_of(k, s.k),       range_of(v, s.v),
+                         range_of(g, s.gate), range_of(beta, s.gate), range_of(S_in == S_out ? nullptr : S_in, s.state)};
+    const Range outs[] = {range_of(o, s.o), range_of(S_out, s.state)};
+    if (any_overlap(outs, 2, ins, 6)) return KD_ERR_ALIAS;
+    kd::GdrArgs a = gdr_args(d, s, q, k, v, g, beta, nullptr);
+    a.S0 = S_in;
+    a.o = o;
+    a.ST = S_out;
+    return done(kd::launch_gdr_step(d->dtype == KD_BF16, a, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,577 @@
+// kd_gdr_bwd.hip -- gated delta rule, backward, gfx950.
+//
+// With S0 the state entering a chunk (kept by the forward pass), dS_C the
+// gradient of the one leaving it and the notation of kd_gdr.h:
+//     dU  = P^T dO + e^(bC - b) K dS_C^T,   X = A^T dU,   dV = beta X
+//     dS0 = e^bC dS_C + (scale e^b dO)^T Q - (beta e^b X)^T K
+// is the pass over the chunks, backwards, as the forward's (16 value columns a
+// wave, the gradient of the state in registers); and per chunk
+//     W = V - e^b K S0^T,  U = A beta W
+//     E = Gam (scale dO U^T) (s <= r),   F = -beta Gam (X U^T) (s < r)
+//     dQ = E K + scale e^b dO S0
+//     dK = E^T Q + (F + F^T) K + e^(bC - b) U dS_C - beta e^b X S0
+//     dbeta_r = X_r.W_r + sum_s F_rs k_r.k_s / beta_r
+// The gradient of b collects what each e^b multiplies (rows minus columns of E
+// times Q K^T and of F times K K^T, and dot products of the terms above with q
+// and k); dg is its sum from the chunk's end, with that of e^bC.
+#include "kd_check.h"
+#include "kd_gdr.h"
+
+namespace kd {
+
+int64_t gdr_pass_grid(int64_t items, int& run);
+hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st);
+
+template <class E>
+struct GdrBack {
+    typename GdrT<E>::Frag A[6], A2[GdrT<E>::TWO ? 6 : 1], P[6];      // transposed
+    floatx4 bb[4], ec[4], se[4];
+    float be[4], eC;
+    E d[16];
+};
+
+template <class E, int DK>
+__global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
+{
+    typedef GdrT<E> T;
+    typedef typename T::Frag Frag;
+    typedef GdrBack<E> Back;
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr int PAT = T::TWO ? 2 : 1, PPT = T::TWO ? 4 : 2, PARTS = T::TWO ? 5 : 3;
+    __shared__ __align__(16) struct {
+        E k[NBUF][64 * DK], q[NBUF][64 * DK];
+    } sm;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int slices = (a.dv + 63) / 64;
+    const int64_t id = blockIdx.x;
+    int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;
+    if (item >= (int64_t)a.B * a.Hv * slices) return;
+    const int slice = item % slices;
+    item /= slices;
+    const int hv = item % a.Hv, hk = hv / (a.Hv / a.Hk);
+    const GdrSeq s = gdr_seq(a, item / a.Hv);
+    const int64_t seq = item / a.Hv;
+    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, a.dv - 1);
+    const bool work = dv0 < a.dv;
+    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
+    const int64_t out = ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
+    const E* db = (const E*)a.dO + out + col;
+    E* vb = (E*)a.dv_ + out + dv0 + 4 * g;
+    const int NC = gdr_chunks(s.T);
+
+    floatx4 S[2 * NK];      // dS^T, laid out as the forward's state
+    const int64_t state = ((seq * a.Hv + hv) * (int64_t)a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+    for (int x = 0; x < 2 * NK; ++x) {
+        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (a.dST && 32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(a.dST + state + 32 * (x / 2) + 4 * (x & 1));
+    }
+    if (a.dk < DK) {
+        floatx4* z = reinterpret_cast<floatx4*>(&sm);
+        for (int i = tid; i < (int)(sizeof(sm) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        __syncthreads();
+    }
+    auto fetch = [&](int n, int buf) {
+        gdr_fetch<E, DK>(sm.k[buf], kb, a.ks[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+        gdr_fetch<E, DK>(sm.q[buf], qb, a.qs[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+    };
+    auto ahead = [&](Back& x, int n) {
+        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
+        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
+        const float* vec = a.vec + at * GDR_VEC;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            x.A[i] = T::ld(rec + PAT * gdr_part<E>() + i * 512);
+            if (T::TWO) x.A2[T::TWO ? i : 0] = T::ld(rec + (PAT + 1) * gdr_part<E>() + i * 512);
+            x.P[i] = T::ld(rec + PPT * gdr_part<E>() + i * 512);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            x.be[t] = vec[16 * t + l16];
+            x.bb[t] = *reinterpret_cast<const floatx4*>(vec + 64 + 16 * t + 4 * g);
+            x.ec[t] = *reinterpret_cast<const floatx4*>(vec + 128 + 16 * t + 4 * g);
+            x.se[t] = *reinterpret_cast<const floatx4*>(vec + 192 + 16 * t + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = n * GDR_C + 16 * t + 4 * g + r;
+                const E y = db[(int64_t)min(row, s.T - 1) * a.Hv * a.dv];
+                x.d[4 * t + r] = row < s.T ? y : (E)0.f;
+            }
+        }
+        x.eC = vec[256];
+    };
+    auto chunk = [&](int n, int buf, const Back& x, Back& next) {
+        if (NBUF == 1) {
+            __syncthreads();
+            fetch(n, 0);
+        }
+        swa_landed();
+        if (NBUF == 2 && n > 0) fetch(n - 1, buf ^ 1);
+        if (!work) return;
+        if (n > 0) ahead(next, n - 1);
+        const E* kt = sm.k[buf];
+        const E* qt = sm.q[buf];
+        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
+        Frag sh[NK], sl[NK];
+#pragma unroll
+        for (int p = 0; p < NK; ++p) {
+            sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
+            sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
+        }
+        if (dv0 + l16 < a.dv) {
+            E* ds = (E*)a.ds + (at * a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+            for (int p = 0; p < NK; ++p)
+                if (32 * p + 8 * g < a.dk) T::st(ds + 32 * p, sh[p]);
+        }
+        Frag d[2], f[2], f2[2];
+        floatx4 dO[4], U[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dO[t][r] = (float)x.d[4 * t + r];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            floatx4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < NK; ++p) y = gdr_mma2b<E>(T::template ld_row<DK>(kt, 16 * t + l16, p, g), sh[p], sl[p], y);
+            y *= x.ec[t];
+#pragma unroll
+            for (int j = t / 2; j < 2; ++j) y = T::mma(x.P[gdr_block_t(t, j)], d[j], y);
+            U[t] = y;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+            f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+        }
+        // X once with rows = tokens (what the state takes) and once with rows =
+        // values (what is stored)
+        floatx4 X[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            floatx4 y = {0.f, 0.f, 0.f, 0.f};
+            X[t] = y;
+#pragma unroll
+            for (int j = t / 2; j < 2; ++j) {
+                const int i = gdr_block_t(t, j);
+                X[t] = gdr_mma3<E>(x.A[i], x.A2[T::TWO ? i : 0], f[j], f2[j], X[t]);
+                y = gdr_mma3<E>(f[j], f2[j], x.A[i], x.A2[T::TWO ? i : 0], y);
+            }
+            if (dv0 + 4 * g < a.dv) {
+                const int row = 16 * t + l16;
+                *reinterpret_cast<E4*>((E*)a.x + (at * GDR_C + row) * a.dv + dv0 + 4 * g) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                y *= x.be[t];
+                if (n * GDR_C + row < s.T)
+                    *reinterpret_cast<E4*>(vb + (int64_t)(n * GDR_C + row) * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            X[t] *= -x.bb[t];
+            dO[t] *= x.se[t];
+        }
+        Frag d2[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f[j] = T::pack(X[2 * j], X[2 * j + 1]);
+            f2[j] = T::rest(X[2 * j], X[2 * j + 1], f[j]);
+            d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
+            d2[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2 * NK; ++y) {
+            S[y] *= x.eC;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(qt, j, 32 * (y / 2) + 4 * (y & 1), lane), d[j], d2[j], S[y]);
+                S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane), f[j], f2[j], S[y]);
+            }
+        }
+    };
+    Back x0, x1;
+    if (NC > 0) {
+        if (NBUF == 2) fetch(NC - 1, 0);
+        if (work) ahead(x0, NC - 1);
+    }
+    for (int n = NC - 1; n >= 0; n -= 2) {
+        chunk(n, 0, x0, x1);
+        if (n > 0) chunk(n - 1, NBUF - 1, x1, x0);
+    }
+    if (a.dS0 && work && dv0 + l16 < a.dv) {
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x)
+            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(a.dS0 + state + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+    }
+}
+
+// Natural-order fragments of a row-major LDS tile read by columns: K = rows 32
+// j + 8 g + e, row (or column) of the operand = column c0 + l16.
+template <int D>
+__device__ __forceinline__ bf16x8 gdr_coln(const __bf16* tile, int j, int c0, int lane) {
+    typedef SwaTile<__bf16, D> TL;
+    typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+    const int l = lane & 15, r = 32 * j + 8 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
+    const __bf16* lo = tile + TL::off(r, c / 8) + c % 8;
+    const __bf16* hi = tile + TL::off(r + 4, c / 8) + c % 8;
+    const s16x4 x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(lo)));
+    const s16x4 y = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(hi)));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int D>
+__device__ __forceinline__ floatx8 gdr_coln(const float* tile, int j, int c0, int lane) {
+    typedef SwaTile<float, D> TL;
+    const int c = c0 + (lane & 15), r = 32 * j + 8 * (lane >> 4);
+    floatx8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = tile[TL::off(r + e, c / 4) + c % 4];
+    return f;
+}
+
+// Rows of a matrix into an LDS tile by ordinary loads: R rows of D columns, zero
+// past `rows` and `cols`.
+template <class E, int D>
+__device__ __forceinline__ void gdr_stage(E* tile, int R, const E* src, int64_t rs, int rows, int cols, int tid, int nt) {
+    typedef SwaTile<E, D> TL;
+    for (int i = tid; i < R * TL::CPR; i += nt) {
+        const int r = i / TL::CPR, ch = i % TL::CPR;
+        floatx4 x = {0.f, 0.f, 0.f, 0.f};
+        if (r < rows && ch * TL::EPC < cols) x = *reinterpret_cast<const floatx4*>(src + r * rs + ch * TL::EPC);
+        *reinterpret_cast<floatx4*>(tile + TL::off(r, ch)) = x;
+    }
+}
+
+template <class E, int DK, int DV>
+struct GdrGradLds {
+    E k[64 * DK], q[64 * DK], s[DV * DK], d[64 * DV], x[64 * DV], u[64 * DV], e[64 * 64], f[64 * 64];
+    float bh[64], bl[64], vec[GDR_VEC];
+    float rows[4][64], cols[4][64];      // of the two matrices that enter db
+    float brow[4][64];                   // of the one that enters dbeta
+    float xw[8][64], dot[8][64], send[8][64];
+    float ss[8];
+};
+
+// Gradients of one chunk's q, k, g and beta: eight waves per chunk and key
+// head, the value heads of the group one after the other, values in blocks of
+// DV.
+template <class E, int DK, int DV>
+__global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
+{
+    typedef GdrT<E> T;
+    typedef typename T::Frag Frag;
+    typedef SwaTile<E, DK> TK;
+    typedef SwaTile<E, DV> TV;
+    typedef SwaTile<E, 64> TC;
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int NK = DK / 32, NV = DV / 32, CT = DK / 16, RT = CT / 2;      // column tiles of dq, row tiles of a wave
+    constexpr int PARTS = T::TWO ? 5 : 3;
+    __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, G = a.Hv / a.Hk;
+    GdrChunk c;
+    if (!gdr_slot(a, slot, c)) return;
+    const E* kb = (const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2];
+    gdr_stage<E, DK>(sm.k, 64, kb, a.ks[1], c.rows, a.dk, tid, 512);
+    gdr_stage<E, DK>(sm.q, 64, qb, a.qs[1], c.rows, a.dk, tid, 512);
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    // this wave's tiles of dq^T and dk^T: column tile ct, row tiles r0 ..
+    const int ct = w % CT, r0 = w / CT * RT;
+    floatx4 dq[RT], dk[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) dq[t] = dk[t] = zero;
+    // its tiles (i, j), j <= i, of the 64 x 64 matrices: number w and, for the first two waves, 8 + w
+    auto tile_i = [](int n) { return n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3; };
+    auto four = [&](const E* tile_row) { return *reinterpret_cast<const E4*>(tile_row); };
+
+#pragma unroll 1
+    for (int hg = 0; hg < G; ++hg) {
+        const int hv = hk * G + hg;
+        const int64_t at = (int64_t)slot * a.Hv + hv;
+        const float* vec = a.vec + at * GDR_VEC;
+        __syncthreads();
+        if (w == 0) {
+            const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
+            const double b = gdr_cumsum(lane < c.rows ? gdr_gate(a.g, gate, a.gates32, (const E*)nullptr) : 0.f, lane);
+            sm.bh[lane] = (float)b;
+            sm.bl[lane] = (float)(b - (double)(float)b);
+        }
+        if (tid >= 64 && tid < 64 + 257) sm.vec[tid - 64] = vec[tid - 64];
+        for (int i = tid; i < 64 * 64 * (int)sizeof(E) / 16; i += 512) reinterpret_cast<floatx4*>(sm.e)[i] = zero;
+        floatx4 dP[2], dT[2];
+        dP[0] = dP[1] = dT[0] = dT[1] = zero;
+        floatx4 dqi[RT], dks[RT], dke[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) dqi[t] = dks[t] = dke[t] = zero;
+        float ss = 0.f, xw[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) xw[e] = 0.f;
+        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
+#pragma unroll 1
+        for (int v0 = 0; v0 < a.dv; v0 += DV) {
+            const int nv = min(DV, a.dv - v0);
+            const E* Sb = (const E*)a.hs + (at * a.dv + v0) * a.dk;
+            const E* Db = (const E*)a.ds + (at * a.dv + v0) * a.dk;
+            __syncthreads();
+            gdr_stage<E, DK>(sm.s, DV, Sb, a.dk, nv, a.dk, tid, 512);
+            gdr_stage<E, DV>(sm.d, 64, (const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0,
+                             (int64_t)a.Hv * a.dv, c.rows, nv, tid, 512);
+            gdr_stage<E, DV>(sm.x, 64, (const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid, 512);
+            __syncthreads();
+            // W and U: 16 values a wave
+            if (w < DV / 16) {
+                floatx4 W[4];
+                const int col = 16 * w + l16;
+                const E* vb = (const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0 + min(col, nv - 1);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    floatx4 y = zero;
+#pragma unroll
+                    for (int p = 0; p < NK; ++p)
+                        y = T::mma(T::template ld_row<DK>(sm.k, 16 * t + l16, p, g), T::template ld_row<DK>(sm.s, col, p, g), y);
+                    const floatx4 be = *reinterpret_cast<const floatx4*>(sm.vec + 16 * t + 4 * g);
+                    const floatx4 bb = *reinterpret_cast<const floatx4*>(sm.vec + 64 + 16 * t + 4 * g);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * t + 4 * g + r;
+                        const float v = col < nv ? (float)vb[(int64_t)min(row, c.rows - 1) * a.vs[1]] : 0.f;
+                        // W itself for dbeta (beta may be 0), beta W for U
+                        const float eb = __builtin_amdgcn_exp2f(sm.bh[row]);
+                        xw[4 * t + r] = fmaf((float)sm.x[TV::off(row, col / TV::EPC) + col % TV::EPC], v - eb * y[r], xw[4 * t + r]);
+                        W[t][r] = be[r] * v - bb[r] * y[r];
+                    }
+                }
+                Frag f[2], f2[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f[j] = T::pack(W[2 * j], W[2 * j + 1]);
+                    f2[j] = T::rest(W[2 * j], W[2 * j + 1], f[j]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    floatx4 y = zero;
+#pragma unroll
+                    for (int j = 0; j <= t / 2; ++j) {
+                        const Frag A = T::ld(rec + gdr_block(t, j) * 512);
+                        y = gdr_mma2<E>(f[j], f2[j], A, y);
+                        if (T::TWO) y = T::mma(f[j], T::ld(rec + gdr_part<E>() + gdr_block(t, j) * 512), y);
+                    }
+                    // lane: token, four values
+                    const int row = 16 * t + l16, e = 16 * w + 4 * g;
+                    *reinterpret_cast<E4*>(sm.u + TV::off(row, e / TV::EPC) + e % TV::EPC) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                }
+            }
+            // scale e^b dO S0 and X S0
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const Frag s = gdr_coln<DK>(sm.s, j, 16 * ct, lane);
+                    dqi[t] = T::mma(s, T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), dqi[t]);
+                    dke[t] = T::mma(s, T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g), dke[t]);
+                }
+            __syncthreads();
+            // dS in place of S0, their product on the way
+            for (int i = tid; i < DV * TK::CPR; i += 512) {
+                const int r = i / TK::CPR, ch = i % TK::CPR;
+                typedef E EV __attribute__((ext_vector_type(16 / sizeof(E))));
+                EV x;
+#pragma unroll
+                for (int e = 0; e < TK::EPC; ++e) x[e] = (E)0.f;
+                if (r < nv && ch * TK::EPC < a.dk) x = *reinterpret_cast<const EV*>(Db + (int64_t)r * a.dk + ch * TK::EPC);
+                EV* to = reinterpret_cast<EV*>(sm.s + TK::off(r, ch));
+                const EV y = *to;
+#pragma unroll
+                for (int e = 0; e < TK::EPC; ++e) ss = fmaf((float)x[e], (float)y[e], ss);
+                *to = x;
+            }
+            // dO U^T and X U^T
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int n = w + 8 * o, i = tile_i(n), j = n - i * (i + 1) / 2;
+                if (n >= 10) break;
+#pragma unroll
+                for (int p = 0; p < NV; ++p) {
+                    const Frag u = T::template ld_row<DV>(sm.u, 16 * j + l16, p, g);
+                    dP[o] = T::mma(u, T::template ld_row<DV>(sm.d, 16 * i + l16, p, g), dP[o]);
+                    dT[o] = T::mma(u, T::template ld_row<DV>(sm.x, 16 * i + l16, p, g), dT[o]);
+                }
+            }
+            __syncthreads();
+            // U dS
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    dks[t] = T::mma(gdr_coln<DK>(sm.s, j, 16 * ct, lane), T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g), dks[t]);
+        }
+        // E, F and their sums; lane: token r of block i, s = 16 j + 4 g + e
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int n = w + 8 * o, i = tile_i(n), j = n - i * (i + 1) / 2;
+            if (n >= 10) break;
+            floatx4 kk = zero, qk = zero;
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                const Frag s = T::template ld_row<DK>(sm.k, 16 * j + l16, p, g);
+                kk = T::mma(s, T::template ld_row<DK>(sm.k, 16 * i + l16, p, g), kk);
+                qk = T::mma(s, T::template ld_row<DK>(sm.q, 16 * i + l16, p, g), qk);
+            }
+            const int r = 16 * i + l16;
+            const floatx4 sh = *reinterpret_cast<const floatx4*>(sm.bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(sm.bl + 16 * j + 4 * g);
+            const float rh = sm.bh[r], rl = sm.bl[r], br = sm.vec[r];
+            float row = 0.f, brow = 0.f;
+            floatx4 colsum;
+            E4 e4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int s = 16 * j + 4 * g + e;
+                const float gam = s <= r ? __builtin_amdgcn_exp2f((rh - sh[e]) + (rl - sl[e])) : 0.f;
+                const float x = a.scale * gam * dP[o][e], y = s < r ? -gam * dT[o][e] : 0.f;
+                const float m = x * qk[e] + br * y * kk[e];
+                e4[e] = (E)x;
+                row += m;
+                brow = fmaf(y, kk[e], brow);
+                colsum[e] = m;
+                const E f = (E)(br * y);
+                if (s <= r) {      // (the diagonal is 0)
+                    sm.f[TC::off(r, s / TC::EPC) + s % TC::EPC] = f;
+                    sm.f[TC::off(s, r / TC::EPC) + r % TC::EPC] = f;
+                }
+            }
+            *reinterpret_cast<E4*>(sm.e + TC::off(r, (16 * j + 4 * g) / TC::EPC) + (16 * j + 4 * g) % TC::EPC) = e4;
+            row += __shfl_xor(row, 16);
+            row += __shfl_xor(row, 32);
+            brow += __shfl_xor(brow, 16);
+            brow += __shfl_xor(brow, 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int x = 1; x < 16; x *= 2) colsum[e] += __shfl_xor(colsum[e], x);
+            if (g == 0) {
+                sm.rows[j][r] = row;
+                sm.brow[j][r] = brow;
+            }
+            if (l16 == 0)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sm.cols[i][16 * j + 4 * g + e] = colsum[e];
+        }
+        // X.W over the values
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+#pragma unroll
+            for (int x = 1; x < 16; x *= 2) xw[e] += __shfl_xor(xw[e], x);
+            if (l16 == 0) sm.xw[w][16 * (e / 4) + 4 * g + e % 4] = xw[e];
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) ss += __shfl_xor(ss, x);
+        if (lane == 0) sm.ss[w] = ss;
+        // the terms with the states, and their products with q and k
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const int row = 16 * (r0 + t) + l16, e0 = 16 * ct + 4 * g;
+            const float se = sm.vec[192 + row], ec = sm.vec[128 + row], bb = sm.vec[64 + row];
+            const E4 q4 = four(sm.q + TK::off(row, e0 / TK::EPC) + e0 % TK::EPC), k4 = four(sm.k + TK::off(row, e0 / TK::EPC) + e0 % TK::EPC);
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float qi = se * dqi[t][e], ks = ec * dks[t][e], ke = -bb * dke[t][e];
+                dq[t][e] += qi;
+                dk[t][e] += ks + ke;
+                x = fmaf((float)q4[e], qi, fmaf((float)k4[e], ke, x));
+                y = fmaf((float)k4[e], ks, y);
+            }
+            x -= y;
+            x += __shfl_xor(x, 16);
+            x += __shfl_xor(x, 32);
+            y += __shfl_xor(y, 16);
+            y += __shfl_xor(y, 32);
+            if (g == 0) {
+                sm.dot[ct][row] = x;
+                sm.send[ct][row] = y;
+            }
+        }
+        __syncthreads();
+        // E K, E^T Q and (F + F^T) K
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const Frag k = gdr_coln<DK>(sm.k, j, 16 * ct, lane);
+                dq[t] = T::mma(k, T::template ld_row<64>(sm.e, 16 * (r0 + t) + l16, j, g), dq[t]);
+                dk[t] = T::mma(k, T::template ld_row<64>(sm.f, 16 * (r0 + t) + l16, j, g), dk[t]);
+                dk[t] = T::mma(gdr_coln<DK>(sm.q, j, 16 * ct, lane), gdr_coln<64>(sm.e, j, 16 * (r0 + t), lane), dk[t]);
+            }
+        if (w == 0) {
+            // lane: token
+            float db = 0.f, y = 0.f, dbeta = 0.f, send = 0.f;
+            for (int j = 0; j <= lane / 16; ++j) {
+                db += sm.rows[j][lane];
+                dbeta += sm.brow[j][lane];
+            }
+            for (int i = lane / 16; i < 4; ++i) db -= sm.cols[i][lane];
+#pragma unroll
+            for (int x = 0; x < CT; ++x) {
+                db += sm.dot[x][lane];
+                send += sm.send[x][lane];
+            }
+#pragma unroll
+            for (int x = 0; x < (DV / 16 < 8 ? DV / 16 : 8); ++x) dbeta += sm.xw[x][lane];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) y += sm.ss[x];
+            // from the chunk's end, with what e^bC multiplies
+#pragma unroll
+            for (int x = 1; x < 64; x *= 2) send += __shfl_xor(send, x);
+#pragma unroll
+            for (int x = 1; x < 64; x *= 2) {
+                const float z = __shfl_down(db, x);
+                if (lane + x < 64) db += z;
+            }
+            db += send + sm.vec[256] * y;
+            if (lane < c.rows) {
+                const int64_t gate = (c.base * a.T + c.first + lane) * a.Hv + hv;
+                if (a.gates32) {
+                    ((float*)a.dg)[gate] = db;
+                    ((float*)a.dbeta)[gate] = dbeta;
+                } else {
+                    ((E*)a.dg)[gate] = (E)db;
+                    ((E*)a.dbeta)[gate] = (E)dbeta;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int row = 16 * (r0 + t) + l16, e0 = 16 * ct + 4 * g;
+        if (row >= c.rows || e0 >= a.dk) continue;
+        const int64_t to = ((c.base * a.T + c.first + row) * a.Hk + hk) * (int64_t)a.dk + e0;
+        *reinterpret_cast<E4*>((E*)a.dq + to) = E4{(E)dq[t][0], (E)dq[t][1], (E)dq[t][2], (E)dq[t][3]};
+        *reinterpret_cast<E4*>((E*)a.dk_ + to) = E4{(E)dk[t][0], (E)dk[t][1], (E)dk[t][2], (E)dk[t][3]};
+    }
+}
+
+template <class E, int DK, int DV>
+static hipError_t gdr_bwd(const GdrArgs& a, hipStream_t st)
+{
+    int run;
+    const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 63) / 64), run);
+    kd_gdr_back_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.slots == 0) return e;
+    kd_gdr_grad_kernel<E, DK, DV><<<(unsigned)((int64_t)a.slots * a.Hk), 512, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st)
+{
+    const hipError_t e = launch_gdr_prep(bf16, true, a, st);
+    if (e != hipSuccess) return e;
+    if (bf16) return a.dk <= 64 ? gdr_bwd<__bf16, 64, 128>(a, st) : gdr_bwd<__bf16, 128, 128>(a, st);
+    return a.dk <= 64 ? gdr_bwd<float, 64, 32>(a, st) : gdr_bwd<float, 128, 32>(a, st);
+}
+
+}  // namespace kd

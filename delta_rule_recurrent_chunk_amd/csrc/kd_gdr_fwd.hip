@@ -1,0 +1,508 @@
+// kd_gdr_fwd.hip -- gated delta rule: the chunks' matrices (forward and
+// backward) and the forward pass over the chunks, gfx950.  The formulas are in
+// kd_gdr.h.
+#include "kd_check.h"
+#include "kd_gdr.h"
+
+namespace kd {
+
+// One wave per chunk and value head: T, A = (I + T)^-1 and P of 64 tokens.
+// K K^T and Q K^T take 16-row fragments straight from memory.  A by blocks of
+// 16: the four diagonal blocks by substitution, one column a lane; then row by
+// row of blocks A_ij = -A_ii sum_k T_ik A_kj in fp32 products, in place of T.
+// BWD writes A, its transpose and P's transpose, otherwise A and P.
+template <class E, int DK, bool BWD>
+__global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
+{
+    typedef GdrT<E> T;
+    typedef typename T::Frag Frag;
+    constexpr int NK = DK / 32, LD = 68;
+    constexpr int PA2 = 1, PP = T::TWO ? 2 : 1, PAT = T::TWO ? 2 : 1, PAT2 = 3, PPT = T::TWO ? 4 : 2;
+    constexpr int PARTS = BWD ? (T::TWO ? 5 : 3) : (T::TWO ? 3 : 2);
+    __shared__ __align__(16) float M[64 * LD];
+    __shared__ __align__(16) float bh[64], bl[64], be[64];
+    const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
+    const int hv = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv, hk = hv / (a.Hv / a.Hk);
+    GdrChunk c;
+    if (!gdr_slot(a, slot, c)) return;
+    const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
+    const float gl = lane < c.rows ? gdr_gate(a.g, gate, a.gates32, (const E*)nullptr) : 0.f;
+    const float beta = lane < c.rows ? gdr_gate(a.beta, gate, a.gates32, (const E*)nullptr) : 0.f;
+    Frag k[4][NK], q[4][NK];
+    const E* kb = (const E*)a.k + c.base * a.ks[0] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + c.base * a.qs[0] + hk * a.qs[2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t row = c.first + min(16 * t + l16, c.rows - 1);
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) {
+            const int col = 32 * ks + 8 * g;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) k[t][ks][e] = (E)0.f, q[t][ks][e] = (E)0.f;
+            if (col < a.dk) {
+                k[t][ks] = T::ld(kb + row * a.ks[1] + col);
+                q[t][ks] = T::ld(qb + row * a.qs[1] + col);
+            }
+        }
+    }
+    const double b = gdr_cumsum(gl, lane);
+    const double last = __shfl(b, 63);
+    bh[lane] = (float)b;
+    bl[lane] = (float)(b - (double)(float)b);
+    be[lane] = beta;
+    float* vec = a.vec + ((int64_t)slot * a.Hv + hv) * GDR_VEC;
+    const float eb = __builtin_amdgcn_exp2f((float)b);
+    vec[lane] = beta;
+    vec[64 + lane] = beta * eb;
+    vec[128 + lane] = __builtin_amdgcn_exp2f((float)(last - b));
+    vec[192 + lane] = a.scale * eb;
+    if (lane == 0) vec[256] = __builtin_amdgcn_exp2f((float)last);
+    __syncthreads();
+    E* rec = (E*)a.rec + ((int64_t)slot * a.Hv + hv) * PARTS * gdr_part<E>() + lane * 8;
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+
+    // lane: token r of row block i, s = 16 j + 4 g + e
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 16 * i + l16;
+        const float rh = bh[r], rl = bl[r], br = be[r];
+        floatx4 p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            p[j] = zero;
+            if (j > i) continue;
+            floatx4 x = zero;
+#pragma unroll
+            for (int ks = 0; ks < NK; ++ks) x = T::mma(k[j][ks], k[i][ks], x);
+            if (!BWD) {
+#pragma unroll
+                for (int ks = 0; ks < NK; ++ks) p[j] = T::mma(k[j][ks], q[i][ks], p[j]);
+            }
+            const floatx4 sh = *reinterpret_cast<const floatx4*>(bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(bl + 16 * j + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int s = 16 * j + 4 * g + e;
+                const float gam = __builtin_amdgcn_exp2f((rh - sh[e]) + (rl - sl[e]));
+                x[e] = s < r ? br * gam * x[e] : 0.f;
+                p[j][e] = s <= r ? a.scale * gam * p[j][e] : 0.f;
+            }
+            *reinterpret_cast<floatx4*>(M + r * LD + 16 * j + 4 * g) = x;
+        }
+        if (!BWD) {
+            T::st(rec + PP * gdr_part<E>() + gdr_block(i, 0) * 512, T::pack(p[0], p[1]));
+            if (i >= 2) T::st(rec + PP * gdr_part<E>() + gdr_block(i, 1) * 512, T::pack(p[2], p[3]));
+        }
+    }
+    if (BWD) {
+        // P's transpose: lane: token s of block i, r = 16 j + 4 g + e
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = 16 * i + l16;
+            const float sh = bh[s], sl = bl[s];
+            floatx4 p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p[j] = zero;
+                if (j < i) continue;
+#pragma unroll
+                for (int ks = 0; ks < NK; ++ks) p[j] = T::mma(q[j][ks], k[i][ks], p[j]);
+                const floatx4 rh = *reinterpret_cast<const floatx4*>(bh + 16 * j + 4 * g), rl = *reinterpret_cast<const floatx4*>(bl + 16 * j + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 16 * j + 4 * g + e;
+                    p[j][e] = s <= r ? a.scale * __builtin_amdgcn_exp2f((rh[e] - sh) + (rl[e] - sl)) * p[j][e] : 0.f;
+                }
+            }
+            if (i < 2) T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, 0) * 512, T::pack(p[0], p[1]));
+            T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, 1) * 512, T::pack(p[2], p[3]));
+        }
+    }
+    __syncthreads();
+    {
+        // column l16 of diagonal block g
+        const float* t = M + (16 * g) * LD + 16 * g;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float sum = r == l16 ? 1.f : 0.f;
+#pragma unroll
+            for (int s = 0; s < r; s += 4) {
+                const floatx4 y = *reinterpret_cast<const floatx4*>(t + r * LD + s);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (s + e < r) sum = fmaf(-y[e], x[s + e], sum);
+            }
+            x[r] = sum;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) M[(16 * g + r) * LD + 16 * g + l16] = x[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        floatx4 y[3];
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            y[j] = zero;
+#pragma unroll
+            for (int kk = j; kk < i; ++kk) {
+                const floatx4 t = *reinterpret_cast<const floatx4*>(M + (16 * i + l16) * LD + 16 * kk + 4 * g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[e], M[(16 * kk + 4 * g + e) * LD + 16 * j + l16], y[j], 0, 0, 0);
+            }
+        }
+        const floatx4 d = *reinterpret_cast<const floatx4*>(M + (16 * i + l16) * LD + 16 * i + 4 * g);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            floatx4 x = zero;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_16x16x4f32(-y[j][e], d[e], x, 0, 0, 0);
+            *reinterpret_cast<floatx4*>(M + (16 * i + l16) * LD + 16 * j + 4 * g) = x;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i / 2; ++j) {
+            const float* m = M + (16 * i + l16) * LD + 32 * j + 4 * g;
+            const floatx4 x = *reinterpret_cast<const floatx4*>(m);
+            const floatx4 y = 2 * j + 1 <= i ? *reinterpret_cast<const floatx4*>(m + 16) : zero;
+            const Frag f = T::pack(x, y);
+            T::st(rec + gdr_block(i, j) * 512, f);
+            if (T::TWO) T::st(rec + PA2 * gdr_part<E>() + gdr_block(i, j) * 512, T::rest(x, y, f));
+        }
+    if (!BWD) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = i / 2; j < 2; ++j) {
+            floatx4 x = zero, y = zero;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (2 * j >= i) x[e] = M[(32 * j + 4 * g + e) * LD + 16 * i + l16];
+                y[e] = M[(32 * j + 16 + 4 * g + e) * LD + 16 * i + l16];
+            }
+            const Frag f = T::pack(x, y);
+            T::st(rec + PAT * gdr_part<E>() + gdr_block_t(i, j) * 512, f);
+            if (T::TWO) T::st(rec + PAT2 * gdr_part<E>() + gdr_block_t(i, j) * 512, T::rest(x, y, f));
+        }
+}
+
+// What the pass reads of one chunk beside K and Q, in registers a chunk ahead.
+template <class E>
+struct GdrAhead {
+    typename GdrT<E>::Frag A[6], A2[GdrT<E>::TWO ? 6 : 1], P[6];
+    floatx4 be[4], bb[4], ec[4];
+    float se[4], eC;
+    E v[16];
+};
+
+// The pass: four waves of 16 value columns each.
+template <class E, int DK>
+__global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
+{
+    typedef GdrT<E> T;
+    typedef typename T::Frag Frag;
+    typedef GdrAhead<E> Ahead;
+    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr int PP = T::TWO ? 2 : 1, PARTS = T::TWO ? 3 : 2;
+    __shared__ __align__(16) struct {
+        E k[NBUF][64 * DK], q[NBUF][64 * DK];
+    } sm;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int slices = (a.dv + 63) / 64;
+    const int64_t id = blockIdx.x;
+    int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;      // neighbours, which share keys, on one XCD
+    if (item >= (int64_t)a.B * a.Hv * slices) return;
+    const int slice = item % slices;
+    item /= slices;
+    const int hv = item % a.Hv, hk = hv / (a.Hv / a.Hk);
+    const GdrSeq s = gdr_seq(a, item / a.Hv);
+    const int64_t seq = item / a.Hv;
+    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, a.dv - 1);
+    const bool work = dv0 < a.dv;
+    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
+    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + col;
+    E* ob = (E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv + dv0 + 4 * g;
+    const int NC = gdr_chunks(s.T);
+
+    // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
+    // two packed tiles are a fragment in natural order), column: the lane's value
+    floatx4 S[2 * NK];
+    const int64_t state = ((seq * a.Hv + hv) * (int64_t)a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+    for (int x = 0; x < 2 * NK; ++x) {
+        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (a.S0 && 32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(a.S0 + state + 32 * (x / 2) + 4 * (x & 1));
+    }
+    if (a.dk < DK) {
+        floatx4* z = reinterpret_cast<floatx4*>(&sm);
+        for (int i = tid; i < (int)(sizeof(sm) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        __syncthreads();
+    }
+    auto fetch = [&](int n, int buf) {
+        gdr_fetch<E, DK>(sm.k[buf], kb, a.ks[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+        gdr_fetch<E, DK>(sm.q[buf], qb, a.qs[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+    };
+    auto ahead = [&](Ahead& x, int n) {
+        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
+        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
+        const float* vec = a.vec + at * GDR_VEC;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            x.A[i] = T::ld(rec + i * 512);
+            if (T::TWO) x.A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+            x.P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            x.be[t] = *reinterpret_cast<const floatx4*>(vec + 16 * t + 4 * g);
+            x.bb[t] = *reinterpret_cast<const floatx4*>(vec + 64 + 16 * t + 4 * g);
+            x.ec[t] = *reinterpret_cast<const floatx4*>(vec + 128 + 16 * t + 4 * g);
+            x.se[t] = vec[192 + 16 * t + l16];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x.v[4 * t + r] = vb[(int64_t)min(n * GDR_C + 16 * t + 4 * g + r, s.T - 1) * a.vs[1]];
+        }
+        x.eC = vec[256];
+    };
+    auto chunk = [&](int n, int buf, const Ahead& x, Ahead& next) {
+        if (NBUF == 1) {
+            __syncthreads();
+            fetch(n, 0);
+        }
+        swa_landed();
+        if (NBUF == 2 && n + 1 < NC) fetch(n + 1, buf ^ 1);
+        if (!work) return;
+        if (n + 1 < NC) ahead(next, n + 1);
+        const E* kt = sm.k[buf];
+        const E* qt = sm.q[buf];
+        Frag sh[NK], sl[NK];
+#pragma unroll
+        for (int p = 0; p < NK; ++p) {
+            sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
+            sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
+        }
+        if (a.hs && dv0 + l16 < a.dv) {
+            E* hs = (E*)a.hs + (((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+            for (int p = 0; p < NK; ++p)
+                if (32 * p + 8 * g < a.dk) T::st(hs + 32 * p, sh[p]);
+        }
+        floatx4 U[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            floatx4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < NK; ++p) y = gdr_mma2b<E>(T::template ld_row<DK>(kt, 16 * t + l16, p, g), sh[p], sl[p], y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) U[t][r] = x.be[t][r] * (float)x.v[4 * t + r] - x.bb[t][r] * y[r];
+        }
+        {
+            Frag f[2], f2[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j <= t / 2; ++j) {
+                    const int i = gdr_block(t, j);
+                    U[t] = gdr_mma3<E>(x.A[i], x.A2[T::TWO ? i : 0], f[j], f2[j], U[t]);
+                }
+            }
+        }
+        {
+            Frag f[2], f2[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                floatx4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int p = 0; p < NK; ++p) y = gdr_mma2<E>(sh[p], sl[p], T::template ld_row<DK>(qt, 16 * t + l16, p, g), y);
+                y *= x.se[t];
+#pragma unroll
+                for (int j = 0; j <= t / 2; ++j) y = gdr_mma2<E>(f[j], f2[j], x.P[gdr_block(t, j)], y);
+                const int row = n * GDR_C + 16 * t + l16;
+                typedef E E4 __attribute__((ext_vector_type(4)));
+                if (row < s.T && dv0 + 4 * g < a.dv)
+                    *reinterpret_cast<E4*>(ob + (int64_t)row * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+            }
+        }
+        {
+            Frag f[2], f2[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) U[t] *= x.ec[t];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) {
+                S[y] *= x.eC;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane), f[j], f2[j], S[y]);
+            }
+        }
+    };
+    Ahead x0, x1;
+    if (NC > 0) {
+        if (NBUF == 2) fetch(0, 0);
+        if (work) ahead(x0, 0);
+    }
+    for (int n = 0; n < NC; n += 2) {
+        chunk(n, 0, x0, x1);
+        if (n + 1 < NC) chunk(n + 1, NBUF - 1, x1, x0);
+    }
+    if (a.ST && work && dv0 + l16 < a.dv) {
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x)
+            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(a.ST + state + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+    }
+}
+
+// Workgroups of a pass (items of neighbouring slices and heads, in runs of `run`
+// on one XCD, as many as leave none of the 8 XCDs idle), and their grid.
+int64_t gdr_pass_grid(int64_t items, int& run)
+{
+    run = (int)((items + 7) / 8);
+    run = run < 16 ? run : 16;
+    return (items + 8 * run - 1) / (8 * run) * 8 * run;
+}
+
+template <class E, int DK, bool BWD>
+static hipError_t gdr_prep(const GdrArgs& a, hipStream_t st)
+{
+    kd_gdr_prep_kernel<E, DK, BWD><<<(unsigned)((int64_t)a.slots * a.Hv), 64, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st)
+{
+    if (a.slots == 0) return hipSuccess;
+    if (bf16) {
+        if (a.dk <= 64) return bwd ? gdr_prep<__bf16, 64, true>(a, st) : gdr_prep<__bf16, 64, false>(a, st);
+        return bwd ? gdr_prep<__bf16, 128, true>(a, st) : gdr_prep<__bf16, 128, false>(a, st);
+    }
+    if (a.dk <= 64) return bwd ? gdr_prep<float, 64, true>(a, st) : gdr_prep<float, 64, false>(a, st);
+    return bwd ? gdr_prep<float, 128, true>(a, st) : gdr_prep<float, 128, false>(a, st);
+}
+
+// Bytes of a chunk's and value head's matrices.
+size_t gdr_rec_bytes(int bf16, bool bwd)
+{
+    return (size_t)(bf16 ? (bwd ? 5 : 3) * 2 : (bwd ? 3 : 2) * 4) * GDR_BLOCKS * 512;
+}
+
+template <class E, int DK>
+static hipError_t gdr_pass(const GdrArgs& a, hipStream_t st)
+{
+    int run;
+    const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 63) / 64), run);
+    kd_gdr_pass_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    return hipGetLastError();
+}
+
+hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st)
+{
+    const hipError_t e = launch_gdr_prep(bf16, false, a, st);
+    if (e != hipSuccess) return e;
+    if (bf16) return a.dk <= 64 ? gdr_pass<__bf16, 64>(a, st) : gdr_pass<__bf16, 128>(a, st);
+    return a.dk <= 64 ? gdr_pass<float, 64>(a, st) : gdr_pass<float, 128>(a, st);
+}
+
+// One token.  Lanes of a row's key channels, four each; both products with the
+// old state in one pass: with r = S k, s = S q,
+//     u = beta (v - e^g r),  S' = e^g S + u k^T,  o = scale (e^g s + u (k.q)).
+// A workgroup takes `rows` rows of one head's state.  Bound by reading and
+// writing the states.
+template <class E, int L>
+__global__ __launch_bounds__(256) void kd_gdr_step_kernel(const E* q, const E* k, const E* v, const void* gp, const void* bp,
+                                                          const float* Si, float* So, E* o, int64_t qb, int64_t kb, int64_t vb,
+                                                          int64_t qh, int64_t kh, int64_t vh, int Hk, int Hv, int dk, int dv,
+                                                          int rows, int gates32, float scale)
+{
+    constexpr int PER = 256 / L, U = 4;      // rows a pass of the workgroup, passes in flight
+    const int tid = threadIdx.x, c = 4 * (tid % L), part = blockIdx.x, hv = blockIdx.y, hk = hv / (Hv / Hk);
+    const int64_t b = blockIdx.z;
+    const bool in = c < dk;
+    const int64_t head = b * Hv + hv;
+    const float* Sr = Si + head * dv * dk + (in ? c : 0);
+    float* Sw = So + head * dv * dk + c;
+    const int r1 = min((part + 1) * rows, dv);
+    floatx4 S[U];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) S[u] = *reinterpret_cast<const floatx4*>(Sr + (int64_t)min(r0 + u * PER + tid / L, dv - 1) * dk);
+    };
+    load(part * rows);
+    floatx4 kx = {0.f, 0.f, 0.f, 0.f}, qx = {0.f, 0.f, 0.f, 0.f};
+    if (in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            kx[e] = (float)k[b * kb + hk * kh + c + e];
+            qx[e] = (float)q[b * qb + hk * qh + c + e];
+        }
+    }
+    const float decay = expf(gdr_gate(gp, head, gates32, (const E*)nullptr));
+    const float beta = gdr_gate(bp, head, gates32, (const E*)nullptr);
+    auto sum = [&](float x) {
+#pragma unroll
+        for (int y = 1; y < L; y *= 2) x += __shfl_xor(x, y);
+        return x;
+    };
+    auto dot = [](floatx4 x, floatx4 y) { return fmaf(x[0], y[0], fmaf(x[1], y[1], fmaf(x[2], y[2], x[3] * y[3]))); };
+    const float kq = sum(dot(kx, qx));
+    for (int r0 = part * rows; r0 < r1; r0 += U * PER) {
+        if (r0 > part * rows) load(r0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = r0 + u * PER + tid / L;
+            const float rk = sum(dot(S[u], kx)), rq = sum(dot(S[u], qx));
+            if (row >= r1) continue;
+            const float x = beta * ((float)v[b * vb + hv * vh + row] - decay * rk);
+            if (in) *reinterpret_cast<floatx4*>(Sw + (int64_t)row * dk) = S[u] * decay + kx * x;
+            if (tid % L == 0) o[head * dv + row] = (E)(scale * fmaf(decay, rq, x * kq));
+        }
+    }
+}
+
+hipError_t launch_gdr_step(int bf16, const GdrArgs& a, hipStream_t st)
+{
+    const int L = a.dk <= 32 ? 8 : a.dk <= 64 ? 16 : 32, per = 256 / L;
+    // whole passes of four loads; more workgroups per head where heads are few
+    int rows = a.dv;
+    while ((int64_t)a.B * a.Hv * ((a.dv + rows - 1) / rows) < 1024 && rows > 4 * per) rows = (rows / 2 + 4 * per - 1) / (4 * per) * 4 * per;
+    const dim3 grid((a.dv + rows - 1) / rows, a.Hv, a.B);
+#define KD_STEP(E, L)                                                                                                        \
+    kd_gdr_step_kernel<E, L><<<grid, 256, 0, st>>>((const E*)a.q, (const E*)a.k, (const E*)a.v, a.g, a.beta, a.S0, a.ST,     \
+                                                   (E*)a.o, a.qs[0], a.ks[0], a.vs[0], a.qs[2], a.ks[2], a.vs[2], a.Hk, a.Hv, \
+                                                   a.dk, a.dv, rows, a.gates32, a.scale)
+    if (bf16) {
+        if (L == 8) KD_STEP(__bf16, 8);
+        else if (L == 16) KD_STEP(__bf16, 16);
+        else KD_STEP(__bf16, 32);
+    } else {
+        if (L == 8) KD_STEP(float, 8);
+        else if (L == 16) KD_STEP(float, 16);
+        else KD_STEP(float, 32);
+    }
+#undef KD_STEP
+    return hipGetLastError();
+}
+
+}  // namespace kd

@@ -76,13 +76,6 @@ __device__ __forceinline__ void prefix_single(floatx16* o, const typename SwaT<E
     }
 }
 
-// One 16-byte load straight to LDS at byte address `to` (wave-uniform; lane i
-// fills to + 16 i).  In flight until waited for (swa_landed, or a count of
-// vector memory operations): the builtin would make every LDS read wait.
-__device__ __forceinline__ void prefix_load(uint32_t to, const void* src) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(src) : "memory", "m0");
-}
-
 template <class E, int D>
 __device__ __forceinline__ void prefix_part(const PrefixArgs& a, int64_t at, const floatx16* o, float m, float l, int g)
 {
@@ -192,8 +185,8 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int ch = (fc ^ TL::swz(fr + i * STEP)) * TL::EPC;
-            prefix_load(kd + i * 4096, K.k + id[i] * K.kp + sl[i] * K.ks + ch);
-            prefix_load(vd + i * 4096, K.v + id[i] * K.vp + sl[i] * K.vs + ch);
+            load_lds16(kd + i * 4096, K.k + id[i] * K.kp + sl[i] * K.ks + ch);
+            load_lds16(vd + i * 4096, K.v + id[i] * K.vp + sl[i] * K.vs + ch);
         }
     };
     auto tile = [&](int i, const E* kl, const E* vl, E* kn, E* vn) {
@@ -320,11 +313,11 @@ __device__ __forceinline__ void prefix_own(const PrefixArgs& a, E* kl, E* vl, co
     auto chunk = [&](int i) { return ((lane % TL::CPR) ^ TL::swz(i * (64 / TL::CPR) + lane / TL::CPR)) * TL::EPC; };
     auto keys = [&]() {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) prefix_load(kd + 1024 * i, K.k + id[i] * K.kp + sl[i] * K.ks + chunk(i));
+        for (int i = 0; i < NI; ++i) load_lds16(kd + 1024 * i, K.k + id[i] * K.kp + sl[i] * K.ks + chunk(i));
     };
     auto values = [&]() {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) prefix_load(vd + 1024 * i, K.v + id[i] * K.vp + sl[i] * K.vs + chunk(i));
+        for (int i = 0; i < NI; ++i) load_lds16(vd + 1024 * i, K.v + id[i] * K.vp + sl[i] * K.vs + chunk(i));
     };
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);

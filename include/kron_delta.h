@@ -668,6 +668,79 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
                          const int32_t *table, const int32_t *lens, const int32_t *cu_seqlens,
                          void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Gated delta rule: one decay and one write strength per head and token, the
+ * scalar-gated relative of kron_delta_gdn2_fwd, with its backward pass and its
+ * step.  Per value head the state S is dv x dk (as in kron_delta_fwd) and, for
+ * every token t,
+ *     Sb = e^(g_t) S;  u = beta_t (v_t - Sb k_t);  S = Sb + u k_t^T;
+ *     o_t = scale S q_t.
+ *  * q, k: [B, T, Hk, dk], v: [B, T, Hv, dv] in desc->dtype, strides over
+ *    batch, token and head in elements (multiples of 16 bytes), contiguous last
+ *    dimension; o, dO, dv: contiguous [B, T, Hv, dv]; dq, dk: contiguous
+ *    [B, T, Hk, dk].  Value head h reads key head h / (Hv / Hk); dq and dk are
+ *    summed over the value heads that share one.
+ *  * g (log decay, at most 0; -infinity clears the state), beta and their
+ *    gradients: contiguous [B, T, Hv] in desc->dtype, or fp32 with gates32.
+ *  * S0, ST, dST, dS0: [B, Hv, dv, dk] fp32.
+ *  * dk and dv multiples of 8, dk <= KRON_DELTA_GDR_MAX_DK, dv <=
+ *    KRON_DELTA_GDR_MAX_DV; bf16, or fp32 (a diagnostic precision).  Keys of
+ *    length at most 1 (and beta in [0, 1]) keep the rule stable; longer ones
+ *    are computed as they are.
+ *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of T
+ *    rows, offsets int32 [B + 1] on the device, non-decreasing from 0 to T
+ *    (clamped into that range where they are read); the batch strides are
+ *    ignored, the states are [B, Hv, dv, dk].  Rows that no sequence covers are
+ *    left unwritten.
+ *  * Tokens are taken 64 at a time: a token with an infinity or a NaN in it
+ *    shows in all rows of its 64.
+ *  * ws: kron_delta_gdr_workspace_bytes(desc, cu_seqlens != NULL, backward)
+ *    bytes, contents on entry ignored.  Calls that overlap on the device must
+ *    not share it.
+ * Results do not depend on how the work is scheduled: repeated calls agree bit
+ * for bit.
+ */
+#define KRON_DELTA_GDR_MAX_DK 128
+#define KRON_DELTA_GDR_MAX_DV 256
+typedef struct {
+    int32_t B, T, Hk, Hv, dk, dv;
+    int32_t dtype;             /* kd_dtype */
+    int32_t gates32;           /* g, beta, dg, dbeta in fp32 whatever dtype is */
+    float scale;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+} kd_gdr_desc;
+
+KD_API size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc *desc, int packed, int backward);
+
+/*
+ * Forward: o, and when not NULL the last state ST (S0 for an empty sequence)
+ * and hs, the states entering every 64 tokens in desc->dtype, which the backward
+ * pass starts from: [slots, Hv, dv, dk] with slots = B ceil(T / 64), or
+ * T / 64 + B for packed sequences.
+ */
+KD_API kd_status kron_delta_gdr_fwd(const kd_gdr_desc *desc, const int32_t *cu_seqlens,
+                         const void *q, const void *k, const void *v, const void *g, const void *beta,
+                         const float *S0, void *o, float *ST, void *hs,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Backward: gradients of <dO, o> + <dST, ST> (dST NULL = 0) with respect to q,
+ * k, v, g, beta and S0 (dS0 NULL: not returned), from the inputs and the hs of
+ * the forward call.
+ */
+KD_API kd_status kron_delta_gdr_bwd(const kd_gdr_desc *desc, const int32_t *cu_seqlens,
+                         const void *q, const void *k, const void *v, const void *g, const void *beta,
+                         const void *hs, const void *dO, const float *dST,
+                         void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dS0,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * One token of every sequence (desc->T = 1): S_in, S_out [B, Hv, dv, dk] fp32
+ * may be the same buffer.
+ */
+KD_API kd_status kron_delta_gdr_step(const kd_gdr_desc *desc, const void *q, const void *k, const void *v,
+                         const void *g, const void *beta, const float *S_in, void *o, float *S_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
