@@ -43,16 +43,12 @@ struct GdrArgs {
     float* dS0;
     void *ds, *x;                              // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv]
     // workspace of both
-    void* rec;                                 // the chunks' matrices, in blocks
-    float* vec;                                // and gate factors
+    void* rec;                                 // the chunks' records: matrices in blocks, then gate factors
     const int* cu;
     int B, T, Hk, Hv, dk, dv;                  // packed: B sequences in T rows
     int slots, gates32;
     float scale;
 };
-
-// Parts of a chunk's record, GDR_BLOCKS blocks each (bf16; fp32 has no second parts).
-enum { GDR_A, GDR_A2, GDR_P, GDR_AT, GDR_AT2, GDR_PT, GDR_PARTS };
 
 // What a chunk slot holds.  Batched: chunk slot % NC of batch element slot / NC.
 // Packed: sequence s owns the slots cu[s] / 64 + s onwards (kd_swa.h).
@@ -148,6 +144,16 @@ struct GdrT<__bf16> {
         const int l = lane & 15, r = 32 * j + 4 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
         return tr<D>(tile, r, c);
     }
+    // rows 16 t + 4 g .. + 3 of column c0 + l16, as an accumulator holds them
+    template <int D>
+    static __device__ __forceinline__ floatx4 ld_acc(const __bf16* tile, int t, int c0, int lane) {
+        typedef SwaTile<__bf16, D> TL;
+        typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+        const int l = lane & 15, r = 16 * t + 4 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
+        const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                        (__attribute__((address_space(3))) v4s*)(tile + TL::off(r, c / 8) + c % 8)));
+        return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+    }
     template <int D>
     static __device__ __forceinline__ Frag tr(const __bf16* tile, int r, int c) {
         typedef SwaTile<__bf16, D> TL;
@@ -197,6 +203,15 @@ struct GdrT<float> {
         return at<D>(tile, j, c0 + (lane & 15), lane);
     }
     template <int D>
+    static __device__ __forceinline__ floatx4 ld_acc(const float* tile, int t, int c0, int lane) {
+        typedef SwaTile<float, D> TL;
+        const int c = c0 + (lane & 15), r = 16 * t + 4 * (lane >> 4);
+        floatx4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = tile[TL::off(r + e, c / 4) + c % 4];
+        return x;
+    }
+    template <int D>
     static __device__ __forceinline__ Frag at(const float* tile, int j, int c, int lane) {
         typedef SwaTile<float, D> TL;
         const int r = 32 * j + 4 * (lane >> 4);
@@ -242,21 +257,117 @@ __device__ __forceinline__ constexpr int gdr_block_t(int i, int j) { return i < 
 
 template <class E>
 __host__ __device__ constexpr int gdr_part() { return GDR_BLOCKS * 512; }      // elements of a part
-
-// Stages rows of K or Q (64 of them, clamped to the sequence's last) in an LDS
-// tile; columns past dk keep what the tile holds (zeros).
-template <class E, int DK>
-__device__ __forceinline__ void gdr_fetch(E* tile, const E* rows, int64_t rs, int row, int last, int dk, int tid, int w) {
-    typedef SwaTile<E, DK> TL;
-    constexpr int STEP = 256 / TL::CPR, NL = 64 / STEP;
-    const int r0 = tid / TL::CPR, ch = tid % TL::CPR;
-    const uint32_t to = lds_address(tile) + 1024 * w;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int r = r0 + i * STEP, x = (ch ^ TL::swz(r)) * TL::EPC;
-        if (x < dk) load_lds16(to + i * 4096, rows + (int64_t)min(row + r, last) * rs + x);
-    }
+// Parts of a record (bf16: A and A^T each with a remainder), and its bytes.
+//   forward:  A [A2] P                backward: A [A2] A^T [A^T2] P^T
+// The last parts and the factors behind them are what a pass reads.
+template <class E>
+__host__ __device__ constexpr int gdr_parts(bool bwd) { return sizeof(E) == 2 ? (bwd ? 5 : 3) : (bwd ? 3 : 2); }
+template <class E>
+__host__ __device__ constexpr int64_t gdr_rec_bytes(bool bwd) {
+    return (int64_t)gdr_parts<E>(bwd) * gdr_part<E>() * (int)sizeof(E) + GDR_VEC * 4;
 }
+
+// Stages 64 rows of K or Q in an LDS tile, from `row` on (past the sequence's
+// last they repeat it); columns past dk keep what the tile holds (zeros).  The
+// addresses are a scalar base and one 32-bit offset per lane that all chunks
+// share.
+template <class E, int DK>
+struct GdrFetch {
+    typedef SwaTile<E, DK> TL;
+    static constexpr int STEP = 256 / TL::CPR, NL = 64 / STEP;
+    const E* base;
+    int64_t rs;
+    int rows, dk, r, ch;
+    uint32_t lane[NL];
+    bool plain;      // rows near enough for 32-bit offsets, all columns there
+    __device__ __forceinline__ GdrFetch(const E* base_, int64_t rs_, int rows_, int dk_, int tid)
+        : base((const E*)swa_uniform((int64_t)base_)), rs(swa_uniform(rs_)), rows(__builtin_amdgcn_readfirstlane(rows_)), dk(dk_) {
+        r = tid / TL::CPR;
+        ch = tid % TL::CPR;
+        plain = rs <= (1 << 22) && dk == DK;
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            lane[i] = (uint32_t)(((r + i * STEP) * (int)rs + (ch ^ TL::swz(r + i * STEP)) * TL::EPC) * (int)sizeof(E));
+    }
+    __device__ __forceinline__ void operator()(E* tile, int row, int w) const {
+        const int row0 = __builtin_amdgcn_readfirstlane(row);
+        const uint32_t to = lds_address(tile) + 1024 * w;
+        const E* b = base + (int64_t)row0 * rs;
+        if (row0 + 64 <= rows && plain) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(lane[i]),
+                             "s"(swa_uniform((int64_t)b)), "i"(i * 4096)
+                             : "memory", "m0", "scc");
+        } else {
+            const int last = rows - 1 - row0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int rr = r + i * STEP, x = (ch ^ TL::swz(rr)) * TL::EPC;
+                if (x < dk) load_lds16(to + i * 4096, b + (int64_t)min(rr, last) * rs + x);
+            }
+        }
+    }
+};
+
+// What a pass reads of a chunk beside K and Q: the end of its record (three
+// parts, fp32 two, and the gate factors) and 64 columns of V (or dO).  The
+// workgroup's 256 threads load it to registers a chunk ahead and put it in LDS
+// when the chunk before is done.
+template <class E>
+struct GdrSide {
+    static constexpr int REC = (GdrT<E>::TWO ? 3 : 2) * GDR_BLOCKS * 512;      // elements
+    static constexpr int PIECES = (REC * (int)sizeof(E) + GDR_VEC * 4) / 16;
+    E rec[REC];
+    float vec[GDR_VEC];
+    E v[64 * 64];
+};
+template <class E>
+struct GdrSideAhead {
+    typedef SwaTile<E, 64> TV;
+    static constexpr int N = (GdrSide<E>::PIECES + 255) / 256, M = 64 * TV::CPR / 256, STEP = 256 / TV::CPR;
+    floatx4 x[N], v[M];
+    const E* vp;      // this thread's first piece of v in row 0
+    int64_t vs;
+    int r, T;
+    bool in;
+    // rows of v: 64 columns from vb on, of which `cols` are there
+    __device__ __forceinline__ GdrSideAhead(const E* vb, int64_t vs_, int cols, int T_, int tid) : vs(vs_), T(T_) {
+        r = tid / TV::CPR;
+        const int c = tid % TV::CPR * TV::EPC;
+        in = c < cols;
+        vp = vb + r * vs + c;
+    }
+    // a chunk's record from `rec` on, rows `row` .. of v (zero past the last, and past the columns)
+    __device__ __forceinline__ void load(const char* rec, int row, int tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E>::PIECES) x[i] = *reinterpret_cast<const floatx4*>(rec + (i * 256 + tid) * 16);
+        const E* p = vp + row * vs;
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (in) {
+            if (row + 64 <= T) {
+#pragma unroll
+                for (int i = 0; i < M; ++i) v[i] = *reinterpret_cast<const floatx4*>(p + i * STEP * vs);
+            } else {
+#pragma unroll
+                for (int i = 0; i < M; ++i)
+                    if (row + r + i * STEP < T) v[i] = *reinterpret_cast<const floatx4*>(p + i * STEP * vs);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(GdrSide<E>& s, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)      // (vec follows rec)
+            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E>::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * 256 + tid] = x[i];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int at = i * 256 + tid;
+            *reinterpret_cast<floatx4*>(s.v + TV::off(at / TV::CPR, at % TV::CPR)) = v[i];
+        }
+    }
+};
 
 __device__ __forceinline__ float gdr_gate(const void* p, int64_t i, int gates32, const __bf16*) {
     return gates32 ? ((const float*)p)[i] : (float)((const __bf16*)p)[i];

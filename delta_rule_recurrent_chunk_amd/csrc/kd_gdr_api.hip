@@ -10,7 +10,6 @@
 #include "kron_delta.h"
 
 namespace kd {
-size_t gdr_rec_bytes(int bf16, bool bwd);
 int64_t gdr_pass_grid(int64_t items, int& run);
 hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st);
 hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st);
@@ -65,15 +64,14 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     return KD_OK;
 }
 
-// Offsets of the workspace's parts: matrices, gate factors, dS, X.
+// Offsets of the workspace's parts: records, dS, X.
 struct GdrSpace {
-    size_t vec, ds, x, bytes;
+    size_t ds, x, bytes;
 };
 GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool bwd) {
     const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
     GdrSpace w;
-    w.vec = up256(n * kd::gdr_rec_bytes(d->dtype == KD_BF16, bwd));
-    w.ds = w.vec + up256(n * kd::GDR_VEC * 4);
+    w.ds = up256(n * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>(bwd) : kd::gdr_rec_bytes<float>(bwd)));
     w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
     w.bytes = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
     return w;
@@ -141,7 +139,6 @@ kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.ST = ST;
     a.hs = hs;
     a.rec = ws;
-    a.vec = (float*)((char*)ws + w.vec);
     return done(kd::launch_gdr_fwd(d->dtype == KD_BF16, a, (hipStream_t)stream));
 }
 
@@ -179,7 +176,6 @@ kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.dbeta = dbeta;
     a.dS0 = dS0;
     a.rec = ws;
-    a.vec = (float*)((char*)ws + w.vec);
     a.ds = (char*)ws + w.ds;
     a.x = (char*)ws + w.x;
     return done(kd::launch_gdr_bwd(d->dtype == KD_BF16, a, (hipStream_t)stream));

@@ -22,25 +22,17 @@ namespace kd {
 int64_t gdr_pass_grid(int64_t items, int& run);
 hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st);
 
-template <class E>
-struct GdrBack {
-    typename GdrT<E>::Frag A[6], A2[GdrT<E>::TWO ? 6 : 1], P[6];      // transposed
-    floatx4 bb[4], ec[4], se[4];
-    float be[4], eC;
-    E d[16];
-};
-
 template <class E, int DK>
 __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    typedef GdrBack<E> Back;
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
-    constexpr int PAT = T::TWO ? 2 : 1, PPT = T::TWO ? 4 : 2, PARTS = T::TWO ? 5 : 3;
+    constexpr int PPT = T::TWO ? 2 : 1;      // P^T's part of what is staged, behind A^T
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
+        GdrSide<E> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -57,7 +49,6 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
     const int64_t out = ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
-    const E* db = (const E*)a.dO + out + col;
     E* vb = (E*)a.dv_ + out + dv0 + 4 * g;
     const int NC = gdr_chunks(s.T);
 
@@ -70,137 +61,169 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     }
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(sizeof(sm) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
+    const GdrFetch<E, DK> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
     auto fetch = [&](int n, int buf) {
-        gdr_fetch<E, DK>(sm.k[buf], kb, a.ks[1], n * GDR_C, s.T - 1, a.dk, tid, w);
-        gdr_fetch<E, DK>(sm.q[buf], qb, a.qs[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+        kf(sm.k[buf], n * GDR_C, w);
+        qf(sm.q[buf], n * GDR_C, w);
     };
-    auto ahead = [&](Back& x, int n) {
-        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
-        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
-        const float* vec = a.vec + at * GDR_VEC;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            x.A[i] = T::ld(rec + PAT * gdr_part<E>() + i * 512);
-            if (T::TWO) x.A2[T::TWO ? i : 0] = T::ld(rec + (PAT + 1) * gdr_part<E>() + i * 512);
-            x.P[i] = T::ld(rec + PPT * gdr_part<E>() + i * 512);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            x.be[t] = vec[16 * t + l16];
-            x.bb[t] = *reinterpret_cast<const floatx4*>(vec + 64 + 16 * t + 4 * g);
-            x.ec[t] = *reinterpret_cast<const floatx4*>(vec + 128 + 16 * t + 4 * g);
-            x.se[t] = *reinterpret_cast<const floatx4*>(vec + 192 + 16 * t + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = n * GDR_C + 16 * t + 4 * g + r;
-                const E y = db[(int64_t)min(row, s.T - 1) * a.Hv * a.dv];
-                x.d[4 * t + r] = row < s.T ? y : (E)0.f;
-            }
-        }
-        x.eC = vec[256];
-    };
-    auto chunk = [&](int n, int buf, const Back& x, Back& next) {
+    GdrSideAhead<E> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(true) +
+                       (gdr_rec_bytes<E>(true) - GdrSide<E>::PIECES * 16);
+    auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), n * GDR_C, tid); };
+    auto chunk = [&](int n, int buf) {
         if (NBUF == 1) {
             __syncthreads();
+            ahead.store(sm.side[0], tid);
             fetch(n, 0);
         }
         swa_landed();
-        if (NBUF == 2 && n > 0) fetch(n - 1, buf ^ 1);
-        if (!work) return;
-        if (n > 0) ahead(next, n - 1);
-        const E* kt = sm.k[buf];
-        const E* qt = sm.q[buf];
-        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
-        Frag sh[NK], sl[NK];
-#pragma unroll
-        for (int p = 0; p < NK; ++p) {
-            sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
-            sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
+        if (n > 0) {
+            if (NBUF == 2) fetch(n - 1, buf ^ 1);
+            load(n - 1);
         }
-        if (dv0 + l16 < a.dv) {
-            E* ds = (E*)a.ds + (at * a.dv + col) * a.dk + 8 * g;
+        if (work) {
+            const E* kt = sm.k[buf];
+            const E* qt = sm.q[buf];
+            const GdrSide<E>& sd = sm.side[buf];
+            const E* rec = sd.rec + lane * 8;
+            auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
+            const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
+            Frag A[6], A2[T::TWO ? 6 : 1];
 #pragma unroll
-            for (int p = 0; p < NK; ++p)
-                if (32 * p + 8 * g < a.dk) T::st(ds + 32 * p, sh[p]);
-        }
-        Frag d[2], f[2], f2[2];
-        floatx4 dO[4], U[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dO[t][r] = (float)x.d[4 * t + r];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            floatx4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int p = 0; p < NK; ++p) y = gdr_mma2b<E>(T::template ld_row<DK>(kt, 16 * t + l16, p, g), sh[p], sl[p], y);
-            y *= x.ec[t];
-#pragma unroll
-            for (int j = t / 2; j < 2; ++j) y = T::mma(x.P[gdr_block_t(t, j)], d[j], y);
-            U[t] = y;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            f[j] = T::pack(U[2 * j], U[2 * j + 1]);
-            f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
-        }
-        // X once with rows = tokens (what the state takes) and once with rows =
-        // values (what is stored)
-        floatx4 X[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            floatx4 y = {0.f, 0.f, 0.f, 0.f};
-            X[t] = y;
-#pragma unroll
-            for (int j = t / 2; j < 2; ++j) {
-                const int i = gdr_block_t(t, j);
-                X[t] = gdr_mma3<E>(x.A[i], x.A2[T::TWO ? i : 0], f[j], f2[j], X[t]);
-                y = gdr_mma3<E>(f[j], f2[j], x.A[i], x.A2[T::TWO ? i : 0], y);
+            for (int i = 0; i < 6; ++i) {
+                A[i] = T::ld(rec + i * 512);
+                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
             }
-            if (dv0 + 4 * g < a.dv) {
-                const int row = 16 * t + l16;
-                *reinterpret_cast<E4*>((E*)a.x + (at * GDR_C + row) * a.dv + dv0 + 4 * g) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
-                y *= x.be[t];
-                if (n * GDR_C + row < s.T)
-                    *reinterpret_cast<E4*>(vb + (int64_t)(n * GDR_C + row) * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+            Frag sh[NK], sl[NK];
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
+                sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
             }
-        }
+            floatx4 dO[4], U[4], X[4], Y[4];
+            Frag d[2], f[2], f2[2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            X[t] *= -x.bb[t];
-            dO[t] *= x.se[t];
-        }
-        Frag d2[2];
+            for (int t = 0; t < 4; ++t) {
+                dO[t] = T::template ld_acc<64>(sd.v, t, 16 * w, lane);
+                U[t] = X[t] = Y[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+            }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            f[j] = T::pack(X[2 * j], X[2 * j + 1]);
-            f2[j] = T::rest(X[2 * j], X[2 * j + 1], f[j]);
-            d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
-            d2[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j]);
-        }
+            for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
 #pragma unroll
-        for (int y = 0; y < 2 * NK; ++y) {
-            S[y] *= x.eC;
+            for (int p = 0; p < NK; ++p) {
+                Frag x[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(kt, 16 * t + l16, p, g);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sh[p], U[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sl[p], U[t]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) U[t] *= factor(2, t);
+#pragma unroll
+            for (int j = 1; j >= 0; --j)
+#pragma unroll
+                for (int t = 0; t < 2 + 2 * j; ++t) U[t] = T::mma(T::ld(rec + PPT * gdr_part<E>() + gdr_block_t(t, j) * 512), d[j], U[t]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(qt, j, 32 * (y / 2) + 4 * (y & 1), lane), d[j], d2[j], S[y]);
-                S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane), f[j], f2[j], S[y]);
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+            // X once with rows = tokens (what the state takes) and once with rows =
+            // values (what is stored)
+#pragma unroll
+            for (int j = 1; j >= 0; --j) {
+#pragma unroll
+                for (int t = 0; t < 2 + 2 * j; ++t) {
+                    X[t] = T::mma(A[gdr_block_t(t, j)], f[j], X[t]);
+                    Y[t] = T::mma(f[j], A[gdr_block_t(t, j)], Y[t]);
+                }
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 2 + 2 * j; ++t) {
+                        X[t] = T::mma(A[gdr_block_t(t, j)], f2[j], X[t]);
+                        Y[t] = T::mma(f2[j], A[gdr_block_t(t, j)], Y[t]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2 + 2 * j; ++t) {
+                        X[t] = T::mma(A2[T::TWO ? gdr_block_t(t, j) : 0], f[j], X[t]);
+                        Y[t] = T::mma(f[j], A2[T::TWO ? gdr_block_t(t, j) : 0], Y[t]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                X[t] *= -factor(1, t);
+                dO[t] *= factor(3, t);
+            }
+            Frag d2[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(X[2 * j], X[2 * j + 1]);
+                f2[j] = T::rest(X[2 * j], X[2 * j + 1], f[j]);
+                d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
+                d2[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j]);
+            }
+            const float eC = sd.vec[256];
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int y0 = 0; y0 < 2 * NK; y0 += 4) {
+                    Frag x[4], z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        z[i] = T::template ld_col8<DK>(qt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
+                        x[i] = T::template ld_col8<DK>(kt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(z[i], d[j], S[y0 + i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f[j], S[y0 + i]);
+                    if (T::TWO) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(z[i], d2[j], S[y0 + i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f2[j], S[y0 + i]);
+                    }
+                }
+            if (dv0 + l16 < a.dv) {
+                E* ds = (E*)a.ds + (at * a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+                for (int p = 0; p < NK; ++p)
+                    if (32 * p + 8 * g < a.dk) T::st(ds + 32 * p, sh[p]);
+            }
+            if (dv0 + 4 * g < a.dv) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int row = 16 * t + l16;
+                    floatx4 y = Y[t];
+                    *reinterpret_cast<E4*>((E*)a.x + (at * GDR_C + row) * a.dv + dv0 + 4 * g) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                    y *= sd.vec[row];
+                    if (n * GDR_C + row < s.T)
+                        *reinterpret_cast<E4*>(vb + (int64_t)(n * GDR_C + row) * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                }
             }
         }
+        if (NBUF == 2 && n > 0) ahead.store(sm.side[buf ^ 1], tid);
     };
-    Back x0, x1;
     if (NC > 0) {
-        if (NBUF == 2) fetch(NC - 1, 0);
-        if (work) ahead(x0, NC - 1);
+        load(NC - 1);
+        if (NBUF == 2) {
+            fetch(NC - 1, 0);
+            ahead.store(sm.side[0], tid);
+        }
     }
     for (int n = NC - 1; n >= 0; n -= 2) {
-        chunk(n, 0, x0, x1);
-        if (n > 0) chunk(n - 1, NBUF - 1, x1, x0);
+        chunk(n, 0);
+        if (n > 0) chunk(n - 1, NBUF - 1);
     }
     if (a.dS0 && work && dv0 + l16 < a.dv) {
 #pragma unroll
@@ -268,7 +291,6 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     typedef SwaTile<E, 64> TC;
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NV = DV / 32, CT = DK / 16, RT = CT / 2;      // column tiles of dq, row tiles of a wave
-    constexpr int PARTS = T::TWO ? 5 : 3;
     __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, G = a.Hv / a.Hk;
@@ -292,7 +314,8 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     for (int hg = 0; hg < G; ++hg) {
         const int hv = hk * G + hg;
         const int64_t at = (int64_t)slot * a.Hv + hv;
-        const float* vec = a.vec + at * GDR_VEC;
+        const char* record = (const char*)a.rec + at * gdr_rec_bytes<E>(true);
+        const float* vec = (const float*)(record + gdr_rec_bytes<E>(true) - GDR_VEC * 4);
         __syncthreads();
         if (w == 0) {
             const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
@@ -310,7 +333,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         float ss = 0.f, xw[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) xw[e] = 0.f;
-        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
+        const E* rec = (const E*)record + lane * 8;
 #pragma unroll 1
         for (int v0 = 0; v0 < a.dv; v0 += DV) {
             const int nv = min(DV, a.dv - v0);

@@ -18,7 +18,6 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
     typedef typename T::Frag Frag;
     constexpr int NK = DK / 32, LD = 68;
     constexpr int PA2 = 1, PP = T::TWO ? 2 : 1, PAT = T::TWO ? 2 : 1, PAT2 = 3, PPT = T::TWO ? 4 : 2;
-    constexpr int PARTS = BWD ? (T::TWO ? 5 : 3) : (T::TWO ? 3 : 2);
     __shared__ __align__(16) float M[64 * LD];
     __shared__ __align__(16) float bh[64], bl[64], be[64];
     const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
@@ -50,7 +49,8 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
     bh[lane] = (float)b;
     bl[lane] = (float)(b - (double)(float)b);
     be[lane] = beta;
-    float* vec = a.vec + ((int64_t)slot * a.Hv + hv) * GDR_VEC;
+    char* const record = (char*)a.rec + ((int64_t)slot * a.Hv + hv) * gdr_rec_bytes<E>(BWD);
+    float* vec = (float*)(record + gdr_parts<E>(BWD) * gdr_part<E>() * (int)sizeof(E));
     const float eb = __builtin_amdgcn_exp2f((float)b);
     vec[lane] = beta;
     vec[64 + lane] = beta * eb;
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
     vec[192 + lane] = a.scale * eb;
     if (lane == 0) vec[256] = __builtin_amdgcn_exp2f((float)last);
     __syncthreads();
-    E* rec = (E*)a.rec + ((int64_t)slot * a.Hv + hv) * PARTS * gdr_part<E>() + lane * 8;
+    E* rec = (E*)record + lane * 8;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
 
     // lane: token r of row block i, s = 16 j + 4 g + e
@@ -192,26 +192,20 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
         }
 }
 
-// What the pass reads of one chunk beside K and Q, in registers a chunk ahead.
-template <class E>
-struct GdrAhead {
-    typename GdrT<E>::Frag A[6], A2[GdrT<E>::TWO ? 6 : 1], P[6];
-    floatx4 be[4], bb[4], ec[4];
-    float se[4], eC;
-    E v[16];
-};
-
-// The pass: four waves of 16 value columns each.
+// The pass: four waves of 16 value columns each.  K and Q of a chunk come by
+// loads straight to LDS, two chunks' worth; what else it needs through
+// registers.
 template <class E, int DK>
 __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    typedef GdrAhead<E> Ahead;
+    typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
-    constexpr int PP = T::TWO ? 2 : 1, PARTS = T::TWO ? 3 : 2;
+    constexpr int PP = T::TWO ? 2 : 1;
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
+        GdrSide<E> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -227,7 +221,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     const bool work = dv0 < a.dv;
     const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
-    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + col;
+    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * 64;
     E* ob = (E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv + dv0 + 4 * g;
     const int NC = gdr_chunks(s.T);
 
@@ -242,68 +236,81 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     }
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(sizeof(sm) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
+    const GdrFetch<E, DK> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
     auto fetch = [&](int n, int buf) {
-        gdr_fetch<E, DK>(sm.k[buf], kb, a.ks[1], n * GDR_C, s.T - 1, a.dk, tid, w);
-        gdr_fetch<E, DK>(sm.q[buf], qb, a.qs[1], n * GDR_C, s.T - 1, a.dk, tid, w);
+        kf(sm.k[buf], n * GDR_C, w);
+        qf(sm.q[buf], n * GDR_C, w);
     };
-    auto ahead = [&](Ahead& x, int n) {
-        const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
-        const E* rec = (const E*)a.rec + at * PARTS * gdr_part<E>() + lane * 8;
-        const float* vec = a.vec + at * GDR_VEC;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            x.A[i] = T::ld(rec + i * 512);
-            if (T::TWO) x.A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
-            x.P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            x.be[t] = *reinterpret_cast<const floatx4*>(vec + 16 * t + 4 * g);
-            x.bb[t] = *reinterpret_cast<const floatx4*>(vec + 64 + 16 * t + 4 * g);
-            x.ec[t] = *reinterpret_cast<const floatx4*>(vec + 128 + 16 * t + 4 * g);
-            x.se[t] = vec[192 + 16 * t + l16];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                x.v[4 * t + r] = vb[(int64_t)min(n * GDR_C + 16 * t + 4 * g + r, s.T - 1) * a.vs[1]];
-        }
-        x.eC = vec[256];
-    };
-    auto chunk = [&](int n, int buf, const Ahead& x, Ahead& next) {
+    GdrSideAhead<E> ahead(vb, a.vs[1], a.dv - slice * 64, s.T, tid);
+    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
+    auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), n * GDR_C, tid); };
+    auto chunk = [&](int n, int buf) {
+        // chunk n is here; the other buffers are free
         if (NBUF == 1) {
             __syncthreads();
+            ahead.store(sm.side[0], tid);
             fetch(n, 0);
         }
         swa_landed();
-        if (NBUF == 2 && n + 1 < NC) fetch(n + 1, buf ^ 1);
-        if (!work) return;
-        if (n + 1 < NC) ahead(next, n + 1);
-        const E* kt = sm.k[buf];
-        const E* qt = sm.q[buf];
-        Frag sh[NK], sl[NK];
-#pragma unroll
-        for (int p = 0; p < NK; ++p) {
-            sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
-            sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
+        if (n + 1 < NC) {
+            if (NBUF == 2) fetch(n + 1, buf ^ 1);
+            load(n + 1);
         }
-        if (a.hs && dv0 + l16 < a.dv) {
-            E* hs = (E*)a.hs + (((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv + col) * a.dk + 8 * g;
+        if (work) {
+            const E* kt = sm.k[buf];
+            const E* qt = sm.q[buf];
+            const GdrSide<E>& sd = sm.side[buf];
+            const E* rec = sd.rec + lane * 8;
+            auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
+            Frag A[6], A2[T::TWO ? 6 : 1];
 #pragma unroll
-            for (int p = 0; p < NK; ++p)
-                if (32 * p + 8 * g < a.dk) T::st(hs + 32 * p, sh[p]);
-        }
-        floatx4 U[4];
+            for (int i = 0; i < 6; ++i) {
+                A[i] = T::ld(rec + i * 512);
+                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+            }
+            Frag sh[NK], sl[NK];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            floatx4 y = {0.f, 0.f, 0.f, 0.f};
+            for (int p = 0; p < NK; ++p) {
+                sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
+                sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
+            }
+            floatx4 U[4], O[4];
 #pragma unroll
-            for (int p = 0; p < NK; ++p) y = gdr_mma2b<E>(T::template ld_row<DK>(kt, 16 * t + l16, p, g), sh[p], sl[p], y);
+            for (int t = 0; t < 4; ++t) U[t] = O[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) U[t][r] = x.be[t][r] * (float)x.v[4 * t + r] - x.bb[t][r] * y[r];
-        }
-        {
+            for (int p = 0; p < NK; ++p) {
+                Frag f[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) f[t] = T::template ld_row<DK>(kt, 16 * t + l16, p, g);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) U[t] = T::mma(f[t], sh[p], U[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) U[t] = T::mma(f[t], sl[p], U[t]);
+                }
+            }
+            // Q S beside what follows from K S
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                Frag x[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p, g);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], x[t], O[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], x[t], O[t]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const floatx4 v = T::template ld_acc<64>(sd.v, t, 16 * w, lane), be = factor(0, t), bb = factor(1, t);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[t][r] = be[r] * v[r] - bb[r] * U[t][r];
+            }
             Frag f[2], f2[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -311,62 +318,89 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+            // (every round over the four tiles: products that do not wait for each other)
 #pragma unroll
-                for (int j = 0; j <= t / 2; ++j) {
-                    const int i = gdr_block(t, j);
-                    U[t] = gdr_mma3<E>(x.A[i], x.A2[T::TWO ? i : 0], f[j], f2[j], U[t]);
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A[gdr_block(t, j)], f[j], U[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A[gdr_block(t, j)], f2[j], U[t]);
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[T::TWO ? gdr_block(t, j) : 0], f[j], U[t]);
+                }
+            }
+            Frag P[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) O[t] *= sd.vec[192 + 16 * t + l16];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f[j], P[gdr_block(t, j)], O[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f2[j], P[gdr_block(t, j)], O[t]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) U[t] *= factor(2, t);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+            }
+            const float eC = sd.vec[256];
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int y0 = 0; y0 < 2 * NK; y0 += 4) {
+                    Frag x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = T::template ld_col8<DK>(kt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f[j], S[y0 + i]);
+                    if (T::TWO) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f2[j], S[y0 + i]);
+                    }
+                }
+            if (a.hs && dv0 + l16 < a.dv) {
+                E* hs = (E*)a.hs + (((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv + col) * a.dk + 8 * g;
+#pragma unroll
+                for (int p = 0; p < NK; ++p)
+                    if (32 * p + 8 * g < a.dk) T::st(hs + 32 * p, sh[p]);
+            }
+            if (dv0 + 4 * g < a.dv) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int row = n * GDR_C + 16 * t + l16;
+                    if (row < s.T)
+                        *reinterpret_cast<E4*>(ob + (int64_t)row * a.Hv * a.dv) = E4{(E)O[t][0], (E)O[t][1], (E)O[t][2], (E)O[t][3]};
                 }
             }
         }
-        {
-            Frag f[2], f2[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
-                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                floatx4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < NK; ++p) y = gdr_mma2<E>(sh[p], sl[p], T::template ld_row<DK>(qt, 16 * t + l16, p, g), y);
-                y *= x.se[t];
-#pragma unroll
-                for (int j = 0; j <= t / 2; ++j) y = gdr_mma2<E>(f[j], f2[j], x.P[gdr_block(t, j)], y);
-                const int row = n * GDR_C + 16 * t + l16;
-                typedef E E4 __attribute__((ext_vector_type(4)));
-                if (row < s.T && dv0 + 4 * g < a.dv)
-                    *reinterpret_cast<E4*>(ob + (int64_t)row * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
-            }
-        }
-        {
-            Frag f[2], f2[2];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] *= x.ec[t];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
-                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
-            }
-#pragma unroll
-            for (int y = 0; y < 2 * NK; ++y) {
-                S[y] *= x.eC;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    S[y] = gdr_mma2b<E>(T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane), f[j], f2[j], S[y]);
-            }
-        }
+        if (NBUF == 2 && n + 1 < NC) ahead.store(sm.side[buf ^ 1], tid);
     };
-    Ahead x0, x1;
     if (NC > 0) {
-        if (NBUF == 2) fetch(0, 0);
-        if (work) ahead(x0, 0);
+        load(0);
+        if (NBUF == 2) {
+            fetch(0, 0);
+            ahead.store(sm.side[0], tid);
+        }
     }
     for (int n = 0; n < NC; n += 2) {
-        chunk(n, 0, x0, x1);
-        if (n + 1 < NC) chunk(n + 1, NBUF - 1, x1, x0);
+        chunk(n, 0);
+        if (n + 1 < NC) chunk(n + 1, NBUF - 1);
     }
     if (a.ST && work && dv0 + l16 < a.dv) {
 #pragma unroll
@@ -400,12 +434,6 @@ hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st)
     }
     if (a.dk <= 64) return bwd ? gdr_prep<float, 64, true>(a, st) : gdr_prep<float, 64, false>(a, st);
     return bwd ? gdr_prep<float, 128, true>(a, st) : gdr_prep<float, 128, false>(a, st);
-}
-
-// Bytes of a chunk's and value head's matrices.
-size_t gdr_rec_bytes(int bf16, bool bwd)
-{
-    return (size_t)(bf16 ? (bwd ? 5 : 3) * 2 : (bwd ? 3 : 2) * 4) * GDR_BLOCKS * 512;
 }
 
 template <class E, int DK>
