@@ -41,7 +41,7 @@ struct GdrArgs {
     const float* dST;
     void *dq, *dk_, *dv_, *dg, *dbeta;
     float* dS0;
-    void *ds, *x;                              // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv]
+    void *ds, *x, *x2;                         // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv] (x2: its remainder)
     // workspace of both
     void* rec;                                 // the chunks' records: matrices in blocks, then gate factors
     const int* cu;
@@ -257,11 +257,11 @@ __device__ __forceinline__ constexpr int gdr_block_t(int i, int j) { return i < 
 
 template <class E>
 __host__ __device__ constexpr int gdr_part() { return GDR_BLOCKS * 512; }      // elements of a part
-// Parts of a record (bf16: A and A^T each with a remainder), and its bytes.
-//   forward:  A [A2] P                backward: A [A2] A^T [A^T2] P^T
+// Parts of a record (bf16: A, A^T and P^T each with a remainder), and its bytes.
+//   forward:  A [A2] P                backward: A [A2] A^T [A^T2] P^T [P^T2]
 // The last parts and the factors behind them are what a pass reads.
 template <class E>
-__host__ __device__ constexpr int gdr_parts(bool bwd) { return sizeof(E) == 2 ? (bwd ? 5 : 3) : (bwd ? 3 : 2); }
+__host__ __device__ constexpr int gdr_parts(bool bwd) { return sizeof(E) == 2 ? (bwd ? 6 : 3) : (bwd ? 3 : 2); }
 template <class E>
 __host__ __device__ constexpr int64_t gdr_rec_bytes(bool bwd) {
     return (int64_t)gdr_parts<E>(bwd) * gdr_part<E>() * (int)sizeof(E) + GDR_VEC * 4;
@@ -310,22 +310,22 @@ struct GdrFetch {
     }
 };
 
-// What a pass reads of a chunk beside K and Q: the end of its record (three
-// parts, fp32 two, and the gate factors) and 64 columns of V (or dO).  The
+// What a pass reads of a chunk beside K and Q: the end of its record (A or A^T,
+// P or P^T, and the gate factors) and 64 columns of V (or dO).  The
 // workgroup's 256 threads load it to registers a chunk ahead and put it in LDS
 // when the chunk before is done.
-template <class E>
+template <class E, bool BWD>
 struct GdrSide {
-    static constexpr int REC = (GdrT<E>::TWO ? 3 : 2) * GDR_BLOCKS * 512;      // elements
+    static constexpr int REC = (GdrT<E>::TWO ? (BWD ? 4 : 3) : 2) * GDR_BLOCKS * 512;      // elements
     static constexpr int PIECES = (REC * (int)sizeof(E) + GDR_VEC * 4) / 16;
     E rec[REC];
     float vec[GDR_VEC];
     E v[64 * 64];
 };
-template <class E>
+template <class E, bool BWD>
 struct GdrSideAhead {
     typedef SwaTile<E, 64> TV;
-    static constexpr int N = (GdrSide<E>::PIECES + 255) / 256, M = 64 * TV::CPR / 256, STEP = 256 / TV::CPR;
+    static constexpr int N = (GdrSide<E, BWD>::PIECES + 255) / 256, M = 64 * TV::CPR / 256, STEP = 256 / TV::CPR;
     floatx4 x[N], v[M];
     const E* vp;      // this thread's first piece of v in row 0
     int64_t vs;
@@ -342,7 +342,7 @@ struct GdrSideAhead {
     __device__ __forceinline__ void load(const char* rec, int row, int tid) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E>::PIECES) x[i] = *reinterpret_cast<const floatx4*>(rec + (i * 256 + tid) * 16);
+            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E, BWD>::PIECES) x[i] = *reinterpret_cast<const floatx4*>(rec + (i * 256 + tid) * 16);
         const E* p = vp + row * vs;
 #pragma unroll
         for (int i = 0; i < M; ++i) v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -357,10 +357,10 @@ struct GdrSideAhead {
             }
         }
     }
-    __device__ __forceinline__ void store(GdrSide<E>& s, int tid) const {
+    __device__ __forceinline__ void store(GdrSide<E, BWD>& s, int tid) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)      // (vec follows rec)
-            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E>::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * 256 + tid] = x[i];
+            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E, BWD>::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * 256 + tid] = x[i];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const int at = i * 256 + tid;

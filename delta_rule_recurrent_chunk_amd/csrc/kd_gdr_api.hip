@@ -64,16 +64,17 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     return KD_OK;
 }
 
-// Offsets of the workspace's parts: records, dS, X.
+// Offsets of the workspace's parts: records, dS, X and (bf16) its remainder.
 struct GdrSpace {
-    size_t ds, x, bytes;
+    size_t ds, x, x2, bytes;
 };
 GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool bwd) {
     const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
     GdrSpace w;
     w.ds = up256(n * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>(bwd) : kd::gdr_rec_bytes<float>(bwd)));
     w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
-    w.bytes = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    w.x2 = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    w.bytes = w.x2 + (bwd && es == 2 ? up256(n * kd::GDR_C * d->dv * es) : 0);
     return w;
 }
 
@@ -178,6 +179,7 @@ kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.rec = ws;
     a.ds = (char*)ws + w.ds;
     a.x = (char*)ws + w.x;
+    a.x2 = (char*)ws + w.x2;
     return done(kd::launch_gdr_bwd(d->dtype == KD_BF16, a, (hipStream_t)stream));
 }
 

@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     constexpr int PPT = T::TWO ? 2 : 1;      // P^T's part of what is staged, behind A^T
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E> side[NBUF];
+        GdrSide<E, true> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -69,9 +69,9 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         kf(sm.k[buf], n * GDR_C, w);
         qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, true> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(true) +
-                       (gdr_rec_bytes<E>(true) - GdrSide<E>::PIECES * 16);
+                       (gdr_rec_bytes<E>(true) - GdrSide<E, true>::PIECES * 16);
     auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), n * GDR_C, tid); };
     auto chunk = [&](int n, int buf) {
         if (NBUF == 1) {
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         if (work) {
             const E* kt = sm.k[buf];
             const E* qt = sm.q[buf];
-            const GdrSide<E>& sd = sm.side[buf];
+            const GdrSide<E, true>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
@@ -129,7 +129,9 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
 #pragma unroll
             for (int j = 1; j >= 0; --j)
 #pragma unroll
-                for (int t = 0; t < 2 + 2 * j; ++t) U[t] = T::mma(T::ld(rec + PPT * gdr_part<E>() + gdr_block_t(t, j) * 512), d[j], U[t]);
+                for (int t = 0; t < 2 + 2 * j; ++t)
+                    for (int p = PPT; p < (T::TWO ? PPT + 2 : PPT + 1); ++p)
+                        U[t] = T::mma(T::ld(rec + p * gdr_part<E>() + gdr_block_t(t, j) * 512), d[j], U[t]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
@@ -205,7 +207,12 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
                 for (int t = 0; t < 4; ++t) {
                     const int row = 16 * t + l16;
                     floatx4 y = Y[t];
-                    *reinterpret_cast<E4*>((E*)a.x + (at * GDR_C + row) * a.dv + dv0 + 4 * g) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                    const E4 hi = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                    const int64_t to = (at * GDR_C + row) * a.dv + dv0 + 4 * g;
+                    *reinterpret_cast<E4*>((E*)a.x + to) = hi;
+                    if (T::TWO)
+                        *reinterpret_cast<E4*>((E*)a.x2 + to) = E4{(E)(y[0] - (float)hi[0]), (E)(y[1] - (float)hi[1]),
+                                                                   (E)(y[2] - (float)hi[2]), (E)(y[3] - (float)hi[3])};
                     y *= sd.vec[row];
                     if (n * GDR_C + row < s.T)
                         *reinterpret_cast<E4*>(vb + (int64_t)(n * GDR_C + row) * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
@@ -255,22 +262,56 @@ __device__ __forceinline__ floatx8 gdr_coln(const float* tile, int j, int c0, in
     return f;
 }
 
-// Rows of a matrix into an LDS tile by ordinary loads: R rows of D columns, zero
-// past `rows` and `cols`.
-template <class E, int D>
-__device__ __forceinline__ void gdr_stage(E* tile, int R, const E* src, int64_t rs, int rows, int cols, int tid, int nt) {
+// R rows of D columns on their way to an LDS tile through registers, zero past
+// `rows` and `cols`.
+template <class E, int D, int R>
+struct GdrStage {
     typedef SwaTile<E, D> TL;
-    for (int i = tid; i < R * TL::CPR; i += nt) {
-        const int r = i / TL::CPR, ch = i % TL::CPR;
-        floatx4 x = {0.f, 0.f, 0.f, 0.f};
-        if (r < rows && ch * TL::EPC < cols) x = *reinterpret_cast<const floatx4*>(src + r * rs + ch * TL::EPC);
-        *reinterpret_cast<floatx4*>(tile + TL::off(r, ch)) = x;
+    static constexpr int N = R * TL::CPR / 512;
+    static_assert(R * TL::CPR % 512 == 0, "whole rounds");
+    floatx4 v[N];
+    __device__ __forceinline__ void load(const E* src, int64_t rs, int rows, int cols, int tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * 512 + tid, r = at / TL::CPR, c = at % TL::CPR * TL::EPC;
+            v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (r < rows && c < cols) v[i] = *reinterpret_cast<const floatx4*>(src + r * rs + c);
+        }
     }
-}
+    __device__ __forceinline__ void store(E* tile, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * 512 + tid;
+            *reinterpret_cast<floatx4*>(tile + TL::off(at / TL::CPR, at % TL::CPR)) = v[i];
+        }
+    }
+    // in place of what the tile holds; the sum of both products
+    __device__ __forceinline__ float replace(E* tile, int tid) const {
+        typedef E EV __attribute__((ext_vector_type(TL::EPC)));
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = i * 512 + tid;
+            EV* to = reinterpret_cast<EV*>(tile + TL::off(at / TL::CPR, at % TL::CPR));
+            const EV x = __builtin_bit_cast(EV, v[i]), y = *to;
+#pragma unroll
+            for (int e = 0; e < TL::EPC; ++e) s = fmaf((float)x[e], (float)y[e], s);
+            *to = x;
+        }
+        return s;
+    }
+};
 
 template <class E, int DK, int DV>
 struct GdrGradLds {
-    E k[64 * DK], q[64 * DK], s[DV * DK], d[64 * DV], x[64 * DV], u[64 * DV], e[64 * 64], f[64 * 64];
+    static constexpr bool TWO = GdrT<E>::TWO;
+    E k[64 * DK], q[64 * DK], s[DV * DK], x[64 * DV], x2[TWO ? 64 * DV : 8], u[64 * DV], u2[TWO ? 64 * DV : 8];
+    union {      // dO is done with when E and F are made
+        E d[64 * DV];
+        struct {
+            E e[64 * 64], f[64 * 64];
+        };
+    };
     float bh[64], bl[64], vec[GDR_VEC];
     float rows[4][64], cols[4][64];      // of the two matrices that enter db
     float brow[4][64];                   // of the one that enters dbeta
@@ -280,7 +321,7 @@ struct GdrGradLds {
 
 // Gradients of one chunk's q, k, g and beta: eight waves per chunk and key
 // head, the value heads of the group one after the other, values in blocks of
-// DV.
+// DV.  bf16: X and U with their remainders, S0, dS, E and F rounded.
 template <class E, int DK, int DV>
 __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 {
@@ -292,14 +333,17 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NV = DV / 32, CT = DK / 16, RT = CT / 2;      // column tiles of dq, row tiles of a wave
     __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane0 = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, G = a.Hv / a.Hk;
     GdrChunk c;
     if (!gdr_slot(a, slot, c)) return;
-    const E* kb = (const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2];
-    const E* qb = (const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2];
-    gdr_stage<E, DK>(sm.k, 64, kb, a.ks[1], c.rows, a.dk, tid, 512);
-    gdr_stage<E, DK>(sm.q, 64, qb, a.qs[1], c.rows, a.dk, tid, 512);
+    {
+        GdrStage<E, DK, 64> k, q;
+        k.load((const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2], a.ks[1], c.rows, a.dk, tid);
+        q.load((const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2], a.qs[1], c.rows, a.dk, tid);
+        k.store(sm.k, tid);
+        q.store(sm.q, tid);
+    }
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     // this wave's tiles of dq^T and dk^T: column tile ct, row tiles r0 ..
     const int ct = w % CT, r0 = w / CT * RT;
@@ -308,7 +352,8 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     for (int t = 0; t < RT; ++t) dq[t] = dk[t] = zero;
     // its tiles (i, j), j <= i, of the 64 x 64 matrices: number w and, for the first two waves, 8 + w
     auto tile_i = [](int n) { return n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3; };
-    auto four = [&](const E* tile_row) { return *reinterpret_cast<const E4*>(tile_row); };
+    // (lane numbers made afresh in every phase: addresses that depend on them would otherwise be kept across all)
+#define KD_LANE const int lane = lane0 + opaque_zero(), l16 = lane & 15, g = lane >> 4
 
 #pragma unroll 1
     for (int hg = 0; hg < G; ++hg) {
@@ -316,56 +361,87 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         const int64_t at = (int64_t)slot * a.Hv + hv;
         const char* record = (const char*)a.rec + at * gdr_rec_bytes<E>(true);
         const float* vec = (const float*)(record + gdr_rec_bytes<E>(true) - GDR_VEC * 4);
-        __syncthreads();
-        if (w == 0) {
-            const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
-            const double b = gdr_cumsum(lane < c.rows ? gdr_gate(a.g, gate, a.gates32, (const E*)nullptr) : 0.f, lane);
-            sm.bh[lane] = (float)b;
-            sm.bl[lane] = (float)(b - (double)(float)b);
-        }
-        if (tid >= 64 && tid < 64 + 257) sm.vec[tid - 64] = vec[tid - 64];
-        for (int i = tid; i < 64 * 64 * (int)sizeof(E) / 16; i += 512) reinterpret_cast<floatx4*>(sm.e)[i] = zero;
         floatx4 dP[2], dT[2];
         dP[0] = dP[1] = dT[0] = dT[1] = zero;
-        floatx4 dqi[RT], dks[RT], dke[RT];
+        float ss = 0.f, xs[RT], ys[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) dqi[t] = dks[t] = dke[t] = zero;
-        float ss = 0.f, xw[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) xw[e] = 0.f;
-        const E* rec = (const E*)record + lane * 8;
+        for (int t = 0; t < RT; ++t) xs[t] = ys[t] = 0.f;
 #pragma unroll 1
         for (int v0 = 0; v0 < a.dv; v0 += DV) {
             const int nv = min(DV, a.dv - v0);
-            const E* Sb = (const E*)a.hs + (at * a.dv + v0) * a.dk;
-            const E* Db = (const E*)a.ds + (at * a.dv + v0) * a.dk;
+            GdrStage<E, DK, DV> st;
+            Frag A[6], A2[T::TWO ? 6 : 1];
+            E v[16];
+            {
+                KD_LANE;
+                GdrStage<E, DV, 64> d, x, x2;
+                st.load((const E*)a.hs + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
+                d.load((const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0, (int64_t)a.Hv * a.dv, c.rows, nv, tid);
+                x.load((const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+                if (T::TWO) x2.load((const E*)a.x2 + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+                if (w < DV / 16) {
+                    const int col = min(16 * w + l16, nv - 1);
+                    const E* vb = (const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0 + col;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = vb[min(16 * (i / 4) + 4 * g + i % 4, c.rows - 1) * a.vs[1]];
+                    const E* rec = (const E*)record + lane * 8;
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        A[i] = T::ld(rec + i * 512);
+                        if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+                    }
+                }
+                __syncthreads();      // the head (or the values) before is done
+                if (v0 == 0) {
+                    if (w == 0) {
+                        const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
+                        const double b = gdr_cumsum(lane < c.rows ? gdr_gate(a.g, gate, a.gates32, (const E*)nullptr) : 0.f, lane);
+                        sm.bh[lane] = (float)b;
+                        sm.bl[lane] = (float)(b - (double)(float)b);
+                    }
+                    if (tid >= 64 && tid < 64 + 257) sm.vec[tid - 64] = vec[tid - 64];
+                }
+                st.store(sm.s, tid);
+                d.store(sm.d, tid);
+                x.store(sm.x, tid);
+                if (T::TWO) x2.store(sm.x2, tid);
+            }
             __syncthreads();
-            gdr_stage<E, DK>(sm.s, DV, Sb, a.dk, nv, a.dk, tid, 512);
-            gdr_stage<E, DV>(sm.d, 64, (const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0,
-                             (int64_t)a.Hv * a.dv, c.rows, nv, tid, 512);
-            gdr_stage<E, DV>(sm.x, 64, (const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid, 512);
-            __syncthreads();
+            st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
             // W and U: 16 values a wave
             if (w < DV / 16) {
-                floatx4 W[4];
+                KD_LANE;
                 const int col = 16 * w + l16;
-                const E* vb = (const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0 + min(col, nv - 1);
+                floatx4 W[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) W[t] = zero;
+#pragma unroll
+                for (int p = 0; p < NK; ++p) {
+                    const Frag s = T::template ld_row<DK>(sm.s, col, p, g);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) W[t] = T::mma(T::template ld_row<DK>(sm.k, 16 * t + l16, p, g), s, W[t]);
+                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    floatx4 y = zero;
-#pragma unroll
-                    for (int p = 0; p < NK; ++p)
-                        y = T::mma(T::template ld_row<DK>(sm.k, 16 * t + l16, p, g), T::template ld_row<DK>(sm.s, col, p, g), y);
                     const floatx4 be = *reinterpret_cast<const floatx4*>(sm.vec + 16 * t + 4 * g);
                     const floatx4 bb = *reinterpret_cast<const floatx4*>(sm.vec + 64 + 16 * t + 4 * g);
+                    const floatx4 b = *reinterpret_cast<const floatx4*>(sm.bh + 16 * t + 4 * g);
+                    floatx4 x = T::template ld_acc<DV>(sm.x, t, 16 * w, lane);
+                    if (T::TWO) x += T::template ld_acc<DV>(sm.x2, t, 16 * w, lane);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int row = 16 * t + 4 * g + r;
-                        const float v = col < nv ? (float)vb[(int64_t)min(row, c.rows - 1) * a.vs[1]] : 0.f;
-                        // W itself for dbeta (beta may be 0), beta W for U
-                        const float eb = __builtin_amdgcn_exp2f(sm.bh[row]);
-                        xw[4 * t + r] = fmaf((float)sm.x[TV::off(row, col / TV::EPC) + col % TV::EPC], v - eb * y[r], xw[4 * t + r]);
-                        W[t][r] = be[r] * v - bb[r] * y[r];
+                        const float vv = col < nv ? (float)v[4 * t + r] : 0.f;
+                        // X.W for dbeta takes W itself (beta may be 0), U takes beta W
+                        x[r] *= vv - __builtin_amdgcn_exp2f(b[r]) * W[t][r];
+                        W[t][r] = be[r] * vv - bb[r] * W[t][r];
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int y = 1; y < 16; y *= 2) x[r] += __shfl_xor(x[r], y);
+                    if (l16 == 0) {
+                        floatx4* to = reinterpret_cast<floatx4*>(sm.xw[w] + 16 * t + 4 * g);
+                        *to = v0 == 0 ? x : *to + x;
                     }
                 }
                 Frag f[2], f2[2];
@@ -378,195 +454,227 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 for (int t = 0; t < 4; ++t) {
                     floatx4 y = zero;
 #pragma unroll
-                    for (int j = 0; j <= t / 2; ++j) {
-                        const Frag A = T::ld(rec + gdr_block(t, j) * 512);
-                        y = gdr_mma2<E>(f[j], f2[j], A, y);
-                        if (T::TWO) y = T::mma(f[j], T::ld(rec + gdr_part<E>() + gdr_block(t, j) * 512), y);
-                    }
+                    for (int j = 0; j <= t / 2; ++j) y = gdr_mma3<E>(f[j], f2[j], A[gdr_block(t, j)], A2[T::TWO ? gdr_block(t, j) : 0], y);
                     // lane: token, four values
-                    const int row = 16 * t + l16, e = 16 * w + 4 * g;
-                    *reinterpret_cast<E4*>(sm.u + TV::off(row, e / TV::EPC) + e % TV::EPC) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                    const int to = TV::off(16 * t + l16, (16 * w + 4 * g) / TV::EPC) + 4 * g % TV::EPC;
+                    const E4 hi = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+                    *reinterpret_cast<E4*>(sm.u + to) = hi;
+                    if (T::TWO)
+                        *reinterpret_cast<E4*>(sm.u2 + (T::TWO ? to : 0)) = E4{(E)(y[0] - (float)hi[0]), (E)(y[1] - (float)hi[1]),
+                                                                              (E)(y[2] - (float)hi[2]), (E)(y[3] - (float)hi[3])};
                 }
             }
-            // scale e^b dO S0 and X S0
+            // scale e^b dO S0 and -beta e^b X S0, and their products with q and k
+            {
+                KD_LANE;
+                floatx4 dqi[RT], dke[RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t) dqi[t] = dke[t] = zero;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const Frag s = gdr_coln<DK>(sm.s, j, 16 * ct, lane);
-                    dqi[t] = T::mma(s, T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), dqi[t]);
-                    dke[t] = T::mma(s, T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g), dke[t]);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        dqi[t] = T::mma(s, T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), dqi[t]);
+                        dke[t] = T::mma(s, T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g), dke[t]);
+                        if (T::TWO) dke[t] = T::mma(s, T::template ld_row<DV>(sm.x2, 16 * (r0 + t) + l16, j, g), dke[t]);
+                    }
                 }
-            __syncthreads();
-            // dS in place of S0, their product on the way
-            for (int i = tid; i < DV * TK::CPR; i += 512) {
-                const int r = i / TK::CPR, ch = i % TK::CPR;
-                typedef E EV __attribute__((ext_vector_type(16 / sizeof(E))));
-                EV x;
 #pragma unroll
-                for (int e = 0; e < TK::EPC; ++e) x[e] = (E)0.f;
-                if (r < nv && ch * TK::EPC < a.dk) x = *reinterpret_cast<const EV*>(Db + (int64_t)r * a.dk + ch * TK::EPC);
-                EV* to = reinterpret_cast<EV*>(sm.s + TK::off(r, ch));
-                const EV y = *to;
+                for (int t = 0; t < RT; ++t) {
+                    const int row = 16 * (r0 + t) + l16, to = TK::off(row, (16 * ct + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                    const float se = sm.vec[192 + row], bb = sm.vec[64 + row];
+                    const E4 q4 = *reinterpret_cast<const E4*>(sm.q + to), k4 = *reinterpret_cast<const E4*>(sm.k + to);
 #pragma unroll
-                for (int e = 0; e < TK::EPC; ++e) ss = fmaf((float)x[e], (float)y[e], ss);
-                *to = x;
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = se * dqi[t][e], y = -bb * dke[t][e];
+                        dq[t][e] += x;
+                        dk[t][e] += y;
+                        xs[t] = fmaf((float)q4[e], x, fmaf((float)k4[e], y, xs[t]));
+                    }
+                }
             }
+            __syncthreads();
+            ss += st.replace(sm.s, tid);      // dS in place of S0
             // dO U^T and X U^T
+            {
+                KD_LANE;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int n = w + 8 * o, i = tile_i(n), j = n - i * (i + 1) / 2;
+                    if (n >= 10) break;
+#pragma unroll
+                    for (int p = 0; p < NV; ++p) {
+                        const Frag u = T::template ld_row<DV>(sm.u, 16 * j + l16, p, g);
+                        const Frag d = T::template ld_row<DV>(sm.d, 16 * i + l16, p, g), x = T::template ld_row<DV>(sm.x, 16 * i + l16, p, g);
+                        dP[o] = T::mma(u, d, dP[o]);
+                        dT[o] = T::mma(u, x, dT[o]);
+                        if (T::TWO) {
+                            const Frag u2 = T::template ld_row<DV>(sm.u2, 16 * j + l16, p, g);
+                            dP[o] = T::mma(u2, d, dP[o]);
+                            dT[o] = T::mma(u2, x, dT[o]);
+                            dT[o] = T::mma(u, T::template ld_row<DV>(sm.x2, 16 * i + l16, p, g), dT[o]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            // e^(bC - b) U dS
+            {
+                KD_LANE;
+                floatx4 dks[RT];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) dks[t] = zero;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const Frag s = gdr_coln<DK>(sm.s, j, 16 * ct, lane);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        dks[t] = T::mma(s, T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g), dks[t]);
+                        if (T::TWO) dks[t] = T::mma(s, T::template ld_row<DV>(sm.u2, 16 * (r0 + t) + l16, j, g), dks[t]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int row = 16 * (r0 + t) + l16, to = TK::off(row, (16 * ct + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                    const float ec = sm.vec[128 + row];
+                    const E4 k4 = *reinterpret_cast<const E4*>(sm.k + to);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = ec * dks[t][e];
+                        dk[t][e] += x;
+                        ys[t] = fmaf((float)k4[e], x, ys[t]);
+                    }
+                }
+            }
+        }
+        {
+            KD_LANE;
+            // E, F and their sums; lane: token r of block i, s = 16 j + 4 g + e
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
                 const int n = w + 8 * o, i = tile_i(n), j = n - i * (i + 1) / 2;
                 if (n >= 10) break;
+                floatx4 kk = zero, qk = zero;
 #pragma unroll
-                for (int p = 0; p < NV; ++p) {
-                    const Frag u = T::template ld_row<DV>(sm.u, 16 * j + l16, p, g);
-                    dP[o] = T::mma(u, T::template ld_row<DV>(sm.d, 16 * i + l16, p, g), dP[o]);
-                    dT[o] = T::mma(u, T::template ld_row<DV>(sm.x, 16 * i + l16, p, g), dT[o]);
+                for (int p = 0; p < NK; ++p) {
+                    const Frag s = T::template ld_row<DK>(sm.k, 16 * j + l16, p, g);
+                    kk = T::mma(s, T::template ld_row<DK>(sm.k, 16 * i + l16, p, g), kk);
+                    qk = T::mma(s, T::template ld_row<DK>(sm.q, 16 * i + l16, p, g), qk);
                 }
-            }
-            __syncthreads();
-            // U dS
+                const int r = 16 * i + l16;
+                const floatx4 sh = *reinterpret_cast<const floatx4*>(sm.bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(sm.bl + 16 * j + 4 * g);
+                const float rh = sm.bh[r], rl = sm.bl[r], br = sm.vec[r];
+                float row = 0.f, brow = 0.f;
+                floatx4 colsum;
+                E4 e4, f4;
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    dks[t] = T::mma(gdr_coln<DK>(sm.s, j, 16 * ct, lane), T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g), dks[t]);
-        }
-        // E, F and their sums; lane: token r of block i, s = 16 j + 4 g + e
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            const int n = w + 8 * o, i = tile_i(n), j = n - i * (i + 1) / 2;
-            if (n >= 10) break;
-            floatx4 kk = zero, qk = zero;
-#pragma unroll
-            for (int p = 0; p < NK; ++p) {
-                const Frag s = T::template ld_row<DK>(sm.k, 16 * j + l16, p, g);
-                kk = T::mma(s, T::template ld_row<DK>(sm.k, 16 * i + l16, p, g), kk);
-                qk = T::mma(s, T::template ld_row<DK>(sm.q, 16 * i + l16, p, g), qk);
-            }
-            const int r = 16 * i + l16;
-            const floatx4 sh = *reinterpret_cast<const floatx4*>(sm.bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(sm.bl + 16 * j + 4 * g);
-            const float rh = sm.bh[r], rl = sm.bl[r], br = sm.vec[r];
-            float row = 0.f, brow = 0.f;
-            floatx4 colsum;
-            E4 e4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int s = 16 * j + 4 * g + e;
-                const float gam = s <= r ? __builtin_amdgcn_exp2f((rh - sh[e]) + (rl - sl[e])) : 0.f;
-                const float x = a.scale * gam * dP[o][e], y = s < r ? -gam * dT[o][e] : 0.f;
-                const float m = x * qk[e] + br * y * kk[e];
-                e4[e] = (E)x;
-                row += m;
-                brow = fmaf(y, kk[e], brow);
-                colsum[e] = m;
-                const E f = (E)(br * y);
-                if (s <= r) {      // (the diagonal is 0)
-                    sm.f[TC::off(r, s / TC::EPC) + s % TC::EPC] = f;
-                    sm.f[TC::off(s, r / TC::EPC) + r % TC::EPC] = f;
+                for (int e = 0; e < 4; ++e) {
+                    const int s = 16 * j + 4 * g + e;
+                    const float gam = s <= r ? __builtin_amdgcn_exp2f((rh - sh[e]) + (rl - sl[e])) : 0.f;
+                    const float x = a.scale * gam * dP[o][e], y = s < r ? -gam * dT[o][e] : 0.f;
+                    const float m = x * qk[e] + br * y * kk[e];
+                    e4[e] = (E)x;
+                    f4[e] = (E)(br * y);
+                    row += m;
+                    brow = fmaf(y, kk[e], brow);
+                    colsum[e] = m;
+                    // F + F^T (the diagonal is 0)
+                    if (s <= r) sm.f[TC::off(s, r / TC::EPC) + r % TC::EPC] = f4[e];
                 }
+                const int to = (16 * j + 4 * g) / TC::EPC, rest = 4 * g % TC::EPC;
+                *reinterpret_cast<E4*>(sm.e + TC::off(r, to) + rest) = e4;
+                if (i > j) {
+                    *reinterpret_cast<E4*>(sm.f + TC::off(r, to) + rest) = f4;
+                    *reinterpret_cast<E4*>(sm.e + TC::off(16 * j + l16, (16 * i + 4 * g) / TC::EPC) + rest) = E4{(E)0.f, (E)0.f, (E)0.f, (E)0.f};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (16 * j + 4 * g + e < r) sm.f[TC::off(r, to) + rest + e] = f4[e];
+                }
+                row += __shfl_xor(row, 16);
+                row += __shfl_xor(row, 32);
+                brow += __shfl_xor(brow, 16);
+                brow += __shfl_xor(brow, 32);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int x = 1; x < 16; x *= 2) colsum[e] += __shfl_xor(colsum[e], x);
+                if (g == 0) {
+                    sm.rows[j][r] = row;
+                    sm.brow[j][r] = brow;
+                }
+                if (l16 == 0) *reinterpret_cast<floatx4*>(sm.cols[i] + 16 * j + 4 * g) = colsum;
             }
-            *reinterpret_cast<E4*>(sm.e + TC::off(r, (16 * j + 4 * g) / TC::EPC) + (16 * j + 4 * g) % TC::EPC) = e4;
-            row += __shfl_xor(row, 16);
-            row += __shfl_xor(row, 32);
-            brow += __shfl_xor(brow, 16);
-            brow += __shfl_xor(brow, 32);
+            ss = wave_sum(ss);
+            if (lane == 0) sm.ss[w] = ss;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int x = 1; x < 16; x *= 2) colsum[e] += __shfl_xor(colsum[e], x);
-            if (g == 0) {
-                sm.rows[j][r] = row;
-                sm.brow[j][r] = brow;
-            }
-            if (l16 == 0)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sm.cols[i][16 * j + 4 * g + e] = colsum[e];
-        }
-        // X.W over the values
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-#pragma unroll
-            for (int x = 1; x < 16; x *= 2) xw[e] += __shfl_xor(xw[e], x);
-            if (l16 == 0) sm.xw[w][16 * (e / 4) + 4 * g + e % 4] = xw[e];
-        }
-#pragma unroll
-        for (int x = 1; x < 64; x *= 2) ss += __shfl_xor(ss, x);
-        if (lane == 0) sm.ss[w] = ss;
-        // the terms with the states, and their products with q and k
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int row = 16 * (r0 + t) + l16, e0 = 16 * ct + 4 * g;
-            const float se = sm.vec[192 + row], ec = sm.vec[128 + row], bb = sm.vec[64 + row];
-            const E4 q4 = four(sm.q + TK::off(row, e0 / TK::EPC) + e0 % TK::EPC), k4 = four(sm.k + TK::off(row, e0 / TK::EPC) + e0 % TK::EPC);
-            float x = 0.f, y = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float qi = se * dqi[t][e], ks = ec * dks[t][e], ke = -bb * dke[t][e];
-                dq[t][e] += qi;
-                dk[t][e] += ks + ke;
-                x = fmaf((float)q4[e], qi, fmaf((float)k4[e], ke, x));
-                y = fmaf((float)k4[e], ks, y);
-            }
-            x -= y;
-            x += __shfl_xor(x, 16);
-            x += __shfl_xor(x, 32);
-            y += __shfl_xor(y, 16);
-            y += __shfl_xor(y, 32);
-            if (g == 0) {
-                sm.dot[ct][row] = x;
-                sm.send[ct][row] = y;
+            for (int t = 0; t < RT; ++t) {
+                float x = xs[t] - ys[t], y = ys[t];
+                x += __shfl_xor(x, 16);
+                x += __shfl_xor(x, 32);
+                y += __shfl_xor(y, 16);
+                y += __shfl_xor(y, 32);
+                if (g == 0) {
+                    sm.dot[ct][16 * (r0 + t) + l16] = x;
+                    sm.send[ct][16 * (r0 + t) + l16] = y;
+                }
             }
         }
         __syncthreads();
-        // E K, E^T Q and (F + F^T) K
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
+        {
+            KD_LANE;
+            // E K, E^T Q and (F + F^T) K
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const Frag k = gdr_coln<DK>(sm.k, j, 16 * ct, lane);
-                dq[t] = T::mma(k, T::template ld_row<64>(sm.e, 16 * (r0 + t) + l16, j, g), dq[t]);
-                dk[t] = T::mma(k, T::template ld_row<64>(sm.f, 16 * (r0 + t) + l16, j, g), dk[t]);
-                dk[t] = T::mma(gdr_coln<DK>(sm.q, j, 16 * ct, lane), gdr_coln<64>(sm.e, j, 16 * (r0 + t), lane), dk[t]);
+                const Frag k = gdr_coln<DK>(sm.k, j, 16 * ct, lane), q = gdr_coln<DK>(sm.q, j, 16 * ct, lane);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    dq[t] = T::mma(k, T::template ld_row<64>(sm.e, 16 * (r0 + t) + l16, j, g), dq[t]);
+                    dk[t] = T::mma(k, T::template ld_row<64>(sm.f, 16 * (r0 + t) + l16, j, g), dk[t]);
+                    dk[t] = T::mma(q, gdr_coln<64>(sm.e, j, 16 * (r0 + t), lane), dk[t]);
+                }
             }
-        if (w == 0) {
-            // lane: token
-            float db = 0.f, y = 0.f, dbeta = 0.f, send = 0.f;
-            for (int j = 0; j <= lane / 16; ++j) {
-                db += sm.rows[j][lane];
-                dbeta += sm.brow[j][lane];
-            }
-            for (int i = lane / 16; i < 4; ++i) db -= sm.cols[i][lane];
+            if (w == 7) {
+                // lane: token
+                float db = 0.f, y = 0.f, dbeta = 0.f, send = 0.f;
+                for (int j = 0; j <= lane / 16; ++j) {
+                    db += sm.rows[j][lane];
+                    dbeta += sm.brow[j][lane];
+                }
+                for (int i = lane / 16; i < 4; ++i) db -= sm.cols[i][lane];
 #pragma unroll
-            for (int x = 0; x < CT; ++x) {
-                db += sm.dot[x][lane];
-                send += sm.send[x][lane];
-            }
+                for (int x = 0; x < CT; ++x) {
+                    db += sm.dot[x][lane];
+                    send += sm.send[x][lane];
+                }
 #pragma unroll
-            for (int x = 0; x < (DV / 16 < 8 ? DV / 16 : 8); ++x) dbeta += sm.xw[x][lane];
+                for (int x = 0; x < DV / 16; ++x) dbeta += sm.xw[x][lane];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) y += sm.ss[x];
-            // from the chunk's end, with what e^bC multiplies
+                for (int x = 0; x < 8; ++x) y += sm.ss[x];
+                // from the chunk's end, with what e^bC multiplies
+                send = wave_sum(send);
 #pragma unroll
-            for (int x = 1; x < 64; x *= 2) send += __shfl_xor(send, x);
-#pragma unroll
-            for (int x = 1; x < 64; x *= 2) {
-                const float z = __shfl_down(db, x);
-                if (lane + x < 64) db += z;
-            }
-            db += send + sm.vec[256] * y;
-            if (lane < c.rows) {
-                const int64_t gate = (c.base * a.T + c.first + lane) * a.Hv + hv;
-                if (a.gates32) {
-                    ((float*)a.dg)[gate] = db;
-                    ((float*)a.dbeta)[gate] = dbeta;
-                } else {
-                    ((E*)a.dg)[gate] = (E)db;
-                    ((E*)a.dbeta)[gate] = (E)dbeta;
+                for (int x = 1; x < 64; x *= 2) {
+                    const float z = __shfl_down(db, x);
+                    if (lane + x < 64) db += z;
+                }
+                db += send + sm.vec[256] * y;
+                if (lane < c.rows) {
+                    const int64_t gate = (c.base * a.T + c.first + lane) * a.Hv + hv;
+                    if (a.gates32) {
+                        ((float*)a.dg)[gate] = db;
+                        ((float*)a.dbeta)[gate] = dbeta;
+                    } else {
+                        ((E*)a.dg)[gate] = (E)db;
+                        ((E*)a.dbeta)[gate] = (E)dbeta;
+                    }
                 }
             }
         }
     }
+    KD_LANE;
+#undef KD_LANE
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int row = 16 * (r0 + t) + l16, e0 = 16 * ct + 4 * g;

@@ -113,8 +113,12 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
                     p[j][e] = s <= r ? a.scale * __builtin_amdgcn_exp2f((rh[e] - sh) + (rl[e] - sl)) * p[j][e] : 0.f;
                 }
             }
-            if (i < 2) T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, 0) * 512, T::pack(p[0], p[1]));
-            T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, 1) * 512, T::pack(p[2], p[3]));
+#pragma unroll
+            for (int j = i / 2; j < 2; ++j) {
+                const Frag f = T::pack(p[2 * j], p[2 * j + 1]);
+                T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, j) * 512, f);
+                if (T::TWO) T::st(rec + (PPT + 1) * gdr_part<E>() + gdr_block_t(i, j) * 512, T::rest(p[2 * j], p[2 * j + 1], f));
+            }
         }
     }
     __syncthreads();
@@ -205,7 +209,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     constexpr int PP = T::TWO ? 2 : 1;
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E> side[NBUF];
+        GdrSide<E, false> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
         kf(sm.k[buf], n * GDR_C, w);
         qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E> ahead(vb, a.vs[1], a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, false> ahead(vb, a.vs[1], a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
     auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), n * GDR_C, tid); };
     auto chunk = [&](int n, int buf) {
@@ -262,7 +266,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
         if (work) {
             const E* kt = sm.k[buf];
             const E* qt = sm.q[buf];
-            const GdrSide<E>& sd = sm.side[buf];
+            const GdrSide<E, false>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             Frag A[6], A2[T::TWO ? 6 : 1];
