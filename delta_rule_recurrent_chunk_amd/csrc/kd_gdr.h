@@ -26,6 +26,7 @@ namespace kd {
 constexpr int GDR_C = 64;              // tokens of a chunk
 constexpr int GDR_BLOCKS = 6;          // 16 x 32 blocks of a lower triangular 64 x 64 matrix that hold anything
 constexpr int GDR_VEC = 5 * 64;        // floats of a chunk's gate factors
+constexpr int GDR_MAX_STEP = 1 << 22;  // elements from one token to the next (64 of them in 32-bit offsets)
 
 typedef float floatx8 __attribute__((ext_vector_type(8)));
 
@@ -279,12 +280,12 @@ struct GdrFetch {
     int64_t rs;
     int rows, dk, r, ch;
     uint32_t lane[NL];
-    bool plain;      // rows near enough for 32-bit offsets, all columns there
+    bool plain;      // all columns there
     __device__ __forceinline__ GdrFetch(const E* base_, int64_t rs_, int rows_, int dk_, int tid)
         : base((const E*)swa_uniform((int64_t)base_)), rs(swa_uniform(rs_)), rows(__builtin_amdgcn_readfirstlane(rows_)), dk(dk_) {
         r = tid / TL::CPR;
         ch = tid % TL::CPR;
-        plain = rs <= (1 << 22) && dk == DK;
+        plain = dk == DK;
 #pragma unroll
         for (int i = 0; i < NL; ++i)
             lane[i] = (uint32_t)(((r + i * STEP) * (int)rs + (ch ^ TL::swz(r + i * STEP)) * TL::EPC) * (int)sizeof(E));
@@ -322,40 +323,60 @@ struct GdrSide {
     float vec[GDR_VEC];
     E v[64 * 64];
 };
+// Rows of a matrix at a wave-uniform address as a buffer: what lies past its
+// bytes reads as zero and is not written, so the ends of a sequence and of a
+// head's columns need no branch.  GDR_NONE: an offset past any of them.
+constexpr int GDR_NONE = 0x7ffffff0;
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gdr_buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)swa_uniform((int64_t)p), 0,
+                                             __builtin_amdgcn_readfirstlane((int)(bytes < 0 ? 0 : bytes)), 0x00027000);
+}
+__device__ __forceinline__ floatx4 gdr_load(__amdgpu_buffer_rsrc_t r, int at) {
+    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+// four elements
+__device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floatx4 x, const __bf16*) {
+    const bf16x4 y = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, y), r, at, 0, 0);
+}
+__device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floatx4 x, const float*) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, x), r, at, 0, 0);
+}
+// eight elements
+__device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, bf16x8 x) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, x), r, at, 0, 0);
+}
+__device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floatx8 x) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{x[0], x[1], x[2], x[3]}), r, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{x[4], x[5], x[6], x[7]}), r, at + 16, 0, 0);
+}
+
 template <class E, bool BWD>
 struct GdrSideAhead {
     typedef SwaTile<E, 64> TV;
     static constexpr int N = (GdrSide<E, BWD>::PIECES + 255) / 256, M = 64 * TV::CPR / 256, STEP = 256 / TV::CPR;
     floatx4 x[N], v[M];
-    const E* vp;      // this thread's first piece of v in row 0
+    const E* vb;
     int64_t vs;
-    int r, T;
-    bool in;
+    int T, cols, at;
     // rows of v: 64 columns from vb on, of which `cols` are there
-    __device__ __forceinline__ GdrSideAhead(const E* vb, int64_t vs_, int cols, int T_, int tid) : vs(vs_), T(T_) {
-        r = tid / TV::CPR;
+    __device__ __forceinline__ GdrSideAhead(const E* vb_, int64_t vs_, int cols_, int T_, int tid) : vb(vb_), vs(vs_), T(T_), cols(cols_) {
         const int c = tid % TV::CPR * TV::EPC;
-        in = c < cols;
-        vp = vb + r * vs + c;
+        at = c < cols ? (int)((tid / TV::CPR * vs + c) * (int)sizeof(E)) : GDR_NONE;
     }
-    // a chunk's record from `rec` on, rows `row` .. of v (zero past the last, and past the columns)
-    __device__ __forceinline__ void load(const char* rec, int row, int tid) {
+    // a chunk's record from `rec` on
+    __device__ __forceinline__ void load(const char* rec, int tid) {
+        const auto r = gdr_buffer(rec, GdrSide<E, BWD>::PIECES * 16);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E, BWD>::PIECES) x[i] = *reinterpret_cast<const floatx4*>(rec + (i * 256 + tid) * 16);
-        const E* p = vp + row * vs;
+        for (int i = 0; i < N; ++i) x[i] = gdr_load(r, (i * 256 + tid) * 16);
+    }
+    // rows `row` .. of v
+    __device__ __forceinline__ void load_v(int row) {
+        const auto r = gdr_buffer(vb + row * vs, ((min(T - row, 64) - 1) * vs + min(cols, 64)) * (int)sizeof(E));
 #pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (in) {
-            if (row + 64 <= T) {
-#pragma unroll
-                for (int i = 0; i < M; ++i) v[i] = *reinterpret_cast<const floatx4*>(p + i * STEP * vs);
-            } else {
-#pragma unroll
-                for (int i = 0; i < M; ++i)
-                    if (row + r + i * STEP < T) v[i] = *reinterpret_cast<const floatx4*>(p + i * STEP * vs);
-            }
-        }
+        for (int i = 0; i < M; ++i) v[i] = gdr_load(r, at + (at == GDR_NONE ? 0 : (int)(i * STEP * vs * (int)sizeof(E))));
     }
     __device__ __forceinline__ void store(GdrSide<E, BWD>& s, int tid) const {
 #pragma unroll
@@ -363,8 +384,8 @@ struct GdrSideAhead {
             if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E, BWD>::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * 256 + tid] = x[i];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            const int at = i * 256 + tid;
-            *reinterpret_cast<floatx4*>(s.v + TV::off(at / TV::CPR, at % TV::CPR)) = v[i];
+            const int to = i * 256 + tid;
+            *reinterpret_cast<floatx4*>(s.v + TV::off(to / TV::CPR, to % TV::CPR)) = v[i];
         }
     }
 };

@@ -40,7 +40,9 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     if (!known(d->dtype)) return KD_ERR_DTYPE;
     if (d->B < 1 || d->T < 0 || d->T > (1 << 29) || d->Hk < 1 || d->Hv < 1 || d->Hv > 65535 || d->Hv % d->Hk != 0 ||
         d->dk < 8 || d->dk > KRON_DELTA_GDR_MAX_DK || d->dk % 8 != 0 || d->dv < 8 || d->dv > KRON_DELTA_GDR_MAX_DV ||
-        d->dv % 8 != 0 || !isfinite(d->scale) || d->B > (packed ? 1 << 24 : 65535))
+        d->dv % 8 != 0 || !isfinite(d->scale) || d->B > (packed ? 1 << 24 : 65535) || (int64_t)d->Hv * d->dv > kd::GDR_MAX_STEP)
+        return KD_ERR_SHAPE;
+    if (d->T > 1 && (d->q_stride[1] > kd::GDR_MAX_STEP || d->k_stride[1] > kd::GDR_MAX_STEP || d->v_stride[1] > kd::GDR_MAX_STEP))
         return KD_ERR_SHAPE;
     const size_t es = es_of(d->dtype);
     const int64_t nb = packed ? 1 : d->B;

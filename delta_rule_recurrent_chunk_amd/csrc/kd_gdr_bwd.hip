@@ -72,7 +72,10 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     GdrSideAhead<E, true> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(true) +
                        (gdr_rec_bytes<E>(true) - GdrSide<E, true>::PIECES * 16);
-    auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), n * GDR_C, tid); };
+    auto load = [&](int n) {
+        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), tid);
+        ahead.load_v(n * GDR_C);
+    };
     auto chunk = [&](int n, int buf) {
         if (NBUF == 1) {
             __syncthreads();

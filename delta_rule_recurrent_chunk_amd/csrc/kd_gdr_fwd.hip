@@ -199,12 +199,11 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // The pass: four waves of 16 value columns each.  K and Q of a chunk come by
 // loads straight to LDS, two chunks' worth; what else it needs through
 // registers.
-template <class E, int DK>
+template <class E, int DK, bool SAVE>
 __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
     constexpr int PP = T::TWO ? 2 : 1;
     __shared__ __align__(16) struct {
@@ -226,8 +225,15 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
     const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * 64;
-    E* ob = (E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv + dv0 + 4 * g;
-    const int NC = gdr_chunks(s.T);
+    const E* ob = (const E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
+    const int NC = gdr_chunks(s.T), os = a.Hv * a.dv;
+    // where the lane's four values of row 16 t + l16, and its eight of a kept state, go
+    int oat[4], hat[NK];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) oat[t] = dv0 + 4 * g < a.dv ? ((16 * t + l16) * os + dv0 + 4 * g) * (int)sizeof(E) : GDR_NONE;
+#pragma unroll
+    for (int p = 0; p < NK; ++p)
+        hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
 
     // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
     // two packed tiles are a fragment in natural order), column: the lane's value
@@ -250,7 +256,13 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     };
     GdrSideAhead<E, false> ahead(vb, a.vs[1], a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
-    auto load = [&](int n) { ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), n * GDR_C, tid); };
+    auto load = [&](int n) {
+        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), tid);
+        ahead.load_v(n * GDR_C);
+    };
+    // The order is for one wave a SIMD, which has nothing else to run while it
+    // waits: fragments are read a stage before their products, loads for the
+    // next chunk are spread over the stages.
     auto chunk = [&](int n, int buf) {
         // chunk n is here; the other buffers are free
         if (NBUF == 1) {
@@ -259,68 +271,86 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
             fetch(n, 0);
         }
         swa_landed();
-        if (n + 1 < NC) {
-            if (NBUF == 2) fetch(n + 1, buf ^ 1);
-            load(n + 1);
-        }
+        const bool more = n + 1 < NC, early = NBUF == 2 && more;
         if (work) {
             const E* kt = sm.k[buf];
             const E* qt = sm.q[buf];
             const GdrSide<E, false>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
-            Frag A[6], A2[T::TWO ? 6 : 1];
+            Frag sh[NK], sl[NK], x[4], A[6], A2[T::TWO ? 6 : 1], f[2], f2[2];
+            floatx4 U[4], O[4], be[4], bb[4], v[4];
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
-                A[i] = T::ld(rec + i * 512);
-                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+            for (int t = 0; t < 4; ++t) {
+                x[t] = T::template ld_row<DK>(kt, 16 * t + l16, 0, g);
+                U[t] = O[t] = floatx4{0.f, 0.f, 0.f, 0.f};
             }
-            Frag sh[NK], sl[NK];
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
                 sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
                 sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
             }
-            floatx4 U[4], O[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] = O[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
-                Frag f[4];
+                Frag y[4];      // the next ones: keys, then queries
 #pragma unroll
-                for (int t = 0; t < 4; ++t) f[t] = T::template ld_row<DK>(kt, 16 * t + l16, p, g);
+                for (int t = 0; t < 4; ++t)
+                    y[t] = p + 1 < NK ? T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g) : T::template ld_row<DK>(qt, 16 * t + l16, 0, g);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) U[t] = T::mma(f[t], sh[p], U[t]);
+                for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sh[p], U[t]);
                 if (T::TWO) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) U[t] = T::mma(f[t], sl[p], U[t]);
+                    for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sl[p], U[t]);
                 }
-            }
-            // Q S beside what follows from K S
 #pragma unroll
-            for (int p = 0; p < NK; ++p) {
-                Frag x[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p, g);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], x[t], O[t]);
-                if (T::TWO) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], x[t], O[t]);
-                }
+                for (int t = 0; t < 4; ++t) x[t] = y[t];
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const floatx4 v = T::template ld_acc<64>(sd.v, t, 16 * w, lane), be = factor(0, t), bb = factor(1, t);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) U[t][r] = be[r] * v[r] - bb[r] * U[t][r];
+                v[t] = T::template ld_acc<64>(sd.v, t, 16 * w, lane);
+                be[t] = factor(0, t);
+                bb[t] = factor(1, t);
             }
-            Frag f[2], f2[2];
+            if (early) kf(sm.k[buf ^ 1], (n + 1) * GDR_C, w);
+            // Q S beside what follows from K S
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                Frag y[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] = x[t];
+                if (p + 1 < NK) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p + 1, g);
+                }
+                if (p == 1 || NK == 1) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) U[t][r] = be[t][r] * v[t][r] - bb[t][r] * U[t][r];
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], y[t], O[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], y[t], O[t]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                A[i] = T::ld(rec + i * 512);
+                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
+            if (early) qf(sm.q[buf ^ 1], (n + 1) * GDR_C, w);
+            Frag P[6], kc[2 * NK];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
             // (every round over the four tiles: products that do not wait for each other)
@@ -335,11 +365,12 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[T::TWO ? gdr_block(t, j) : 0], f[j], U[t]);
                 }
             }
-            Frag P[6];
-#pragma unroll
-            for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+            if (more) ahead.load(rec0 + (n + 1) * a.Hv * gdr_rec_bytes<E>(false), tid);
+            const float eC = sd.vec[256];
 #pragma unroll
             for (int t = 0; t < 4; ++t) O[t] *= sd.vec[192 + 16 * t + l16];
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
@@ -361,39 +392,33 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
-            const float eC = sd.vec[256];
+            if (more) ahead.load_v((n + 1) * GDR_C);
+            const auto ob0 = gdr_buffer(ob + (int64_t)n * GDR_C * os, ((int64_t)(min(s.T - n * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
 #pragma unroll
-            for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f[j], S[y]);
+                if (T::TWO) {
 #pragma unroll
-                for (int y0 = 0; y0 < 2 * NK; y0 += 4) {
-                    Frag x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = T::template ld_col8<DK>(kt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f[j], S[y0 + i]);
-                    if (T::TWO) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f2[j], S[y0 + i]);
-                    }
+                    for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
                 }
-            if (a.hs && dv0 + l16 < a.dv) {
-                E* hs = (E*)a.hs + (((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv + col) * a.dk + 8 * g;
+                if (j == 0) {
 #pragma unroll
-                for (int p = 0; p < NK; ++p)
-                    if (32 * p + 8 * g < a.dk) T::st(hs + 32 * p, sh[p]);
-            }
-            if (dv0 + 4 * g < a.dv) {
+                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int row = n * GDR_C + 16 * t + l16;
-                    if (row < s.T)
-                        *reinterpret_cast<E4*>(ob + (int64_t)row * a.Hv * a.dv) = E4{(E)O[t][0], (E)O[t][1], (E)O[t][2], (E)O[t][3]};
+                    for (int t = 0; t < 4; ++t) gdr_store(ob0, oat[t], O[t], (const E*)nullptr);
                 }
             }
+            if (SAVE) {
+                const auto hs = gdr_buffer((const E*)a.hs + ((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
+#pragma unroll
+                for (int p = 0; p < NK; ++p) gdr_store(hs, hat[p], sh[p]);
+            }
+        } else if (more) {
+            if (early) fetch(n + 1, buf ^ 1);
+            load(n + 1);
         }
-        if (NBUF == 2 && n + 1 < NC) ahead.store(sm.side[buf ^ 1], tid);
+        if (early) ahead.store(sm.side[buf ^ 1], tid);
     };
     if (NC > 0) {
         load(0);
@@ -445,7 +470,8 @@ static hipError_t gdr_pass(const GdrArgs& a, hipStream_t st)
 {
     int run;
     const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 63) / 64), run);
-    kd_gdr_pass_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    if (a.hs) kd_gdr_pass_kernel<E, DK, true><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    else kd_gdr_pass_kernel<E, DK, false><<<(unsigned)grid, 256, 0, st>>>(a, run);
     return hipGetLastError();
 }
 

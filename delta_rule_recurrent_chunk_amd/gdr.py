@@ -16,6 +16,7 @@ from . import layers as _la
 from .layers import _call, _check, _code, _fits, _flat, _need_cuda, _ptr, _ready, _rows, _same_device, _workspace
 
 GDR_MAX_DK, GDR_MAX_DV = 128, 256
+GDR_MAX_STEP = 1 << 22
 
 EXPORTED = ("kron_delta_gdr_workspace_bytes", "kron_delta_gdr_fwd", "kron_delta_gdr_bwd", "kron_delta_gdr_step")
 
@@ -61,7 +62,9 @@ def _gdr(q, k, v, g, beta, scale, cu):
     _check("g", g, v.shape[:-1], g.dtype)
     _check("beta", beta, v.shape[:-1], g.dtype)
     _same_device(dev, k=k, v=v, g=g, beta=beta, cu_seqlens=cu)
-    q, k, v, g, beta = _rows(q), _rows(k), _rows(v), _flat(g), _flat(beta)
+    # (tokens too far apart for the kernels' offsets are copied as well)
+    q, k, v = (t.contiguous() if t.stride(-3) > GDR_MAX_STEP and t.shape[-3] > 1 else t for t in map(_rows, (q, k, v)))
+    g, beta = _flat(g), _flat(beta)
     (T, Hk, dk), (Hv, dv) = q.shape[-3:], v.shape[-2:]
     if cu is not None:
         if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:

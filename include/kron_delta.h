@@ -684,7 +684,8 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *    gradients: contiguous [B, T, Hv] in desc->dtype, or fp32 with gates32.
  *  * S0, ST, dST, dS0: [B, Hv, dv, dk] fp32.
  *  * dk and dv multiples of 8, dk <= KRON_DELTA_GDR_MAX_DK, dv <=
- *    KRON_DELTA_GDR_MAX_DV; bf16, or fp32 (a diagnostic precision).  Keys of
+ *    KRON_DELTA_GDR_MAX_DV; Hv dv and the token strides at most 2^22 elements;
+ *    bf16, or fp32 (a diagnostic precision).  Keys of
  *    length at most 1 (and beta in [0, 1]) keep the rule stable; longer ones
  *    are computed as they are.
  *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of T
