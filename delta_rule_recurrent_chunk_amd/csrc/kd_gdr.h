@@ -29,6 +29,8 @@ constexpr int GDR_VEC = 5 * 64;        // floats of a chunk's gate factors
 constexpr int GDR_MAX_STEP = 1 << 22;  // elements from one token to the next (64 of them in 32-bit offsets)
 
 typedef float floatx8 __attribute__((ext_vector_type(8)));
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
 
 struct GdrArgs {
     const void *q, *k, *v, *g, *beta;          // g, beta [B, T, Hv]
@@ -49,6 +51,9 @@ struct GdrArgs {
     int B, T, Hk, Hv, dk, dv;                  // packed: B sequences in T rows
     int slots, gates32;
     float scale;
+    // long sequences in segments of `seg` chunks, `nseg` a sequence (packed: kd_gdr_fwd.hip), `segs` in all
+    int seg, nseg, segs;
+    float *SI, *M;                             // states entering segments [segs, Hv, dv, dk], their maps [segs, Hv, dk, dk]
 };
 
 // What a chunk slot holds.  Batched: chunk slot % NC of batch element slot / NC.
@@ -79,6 +84,39 @@ __device__ __forceinline__ GdrSeq gdr_seq(const GdrArgs& a, int s) {
         r.b = s;
     }
     return r;
+}
+// Segment `slot` as a sequence of its own, with its number and whether it is the
+// last of its sequence.  Packed: sequence s owns the slots cu[s] / 64 / seg + s
+// onwards.  False when the slot holds none.  The whole wave calls it.
+struct GdrSegment {
+    GdrSeq s;
+    int seq, j;
+    bool last;
+};
+__device__ __forceinline__ bool gdr_segment(const GdrArgs& a, int slot, GdrSegment& r) {
+    if (!a.cu) {
+        r.seq = slot / a.nseg;
+        r.j = slot - r.seq * a.nseg;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int n = 0;
+        for (int i = 0; i < a.B; i += 64) {
+            const int at = i + lane;
+            n += __popcll(__ballot(at < a.B && min(max(a.cu[min(at, a.B)], 0), a.T) / GDR_C / a.seg + at <= slot));
+        }
+        if (n == 0) return false;
+        r.seq = n - 1;
+    }
+    r.s = gdr_seq(a, r.seq);
+    const int NC = gdr_chunks(r.s.T);
+    if (a.cu) r.j = slot - (r.s.row0 / GDR_C / a.seg + r.seq);
+    const int c0 = r.j * a.seg;
+    if (c0 > 0 && c0 >= NC) return false;
+    r.last = NC - c0 <= a.seg;
+    r.s.row0 += c0 * GDR_C;
+    r.s.T = r.last ? r.s.T - c0 * GDR_C : a.seg * GDR_C;
+    r.s.slot0 += c0;
+    return true;
 }
 // The chunk in a slot, false when it holds none.  The whole wave calls it.
 __device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c) {
@@ -114,15 +152,27 @@ struct GdrT<__bf16> {
     static __device__ __forceinline__ floatx4 mma(Frag a, Frag b, floatx4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
+    // two values in one word, and both again
+    static __device__ __forceinline__ unsigned two(float x, float y) {
+        return __builtin_bit_cast(unsigned, bf16x2{(__bf16)x, (__bf16)y});
+    }
     static __device__ __forceinline__ Frag pack(floatx4 x, floatx4 y) {
-        return Frag{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3], (__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+        uintx4 u = {two(x[0], x[1]), two(x[2], x[3]), two(y[0], y[1]), two(y[2], y[3])};
+        // (for rest(): the compiler would round every value once more instead of shifting it out)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("" : "+v"(u[i]));
+        return __builtin_bit_cast(Frag, u);
     }
     // what the packing rounded away
     static __device__ __forceinline__ Frag rest(floatx4 x, floatx4 y, Frag p) {
-        Frag r;
+        const uintx4 u = __builtin_bit_cast(uintx4, p);
+        uintx4 r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = (__bf16)(x[e] - (float)p[e]), r[4 + e] = (__bf16)(y[e] - (float)p[4 + e]);
-        return r;
+        for (int i = 0; i < 4; ++i) {
+            const float a = i < 2 ? x[2 * i] : y[2 * i - 4], b = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+            r[i] = two(a - __uint_as_float(u[i] << 16), b - __uint_as_float(u[i] & 0xffff0000u));
+        }
+        return __builtin_bit_cast(Frag, r);
     }
     static __device__ __forceinline__ Frag ld(const __bf16* p) { return *reinterpret_cast<const Frag*>(p); }
     static __device__ __forceinline__ void st(__bf16* p, Frag f) { *reinterpret_cast<Frag*>(p) = f; }
@@ -327,8 +377,6 @@ struct GdrSide {
 // bytes reads as zero and is not written, so the ends of a sequence and of a
 // head's columns need no branch.  GDR_NONE: an offset past any of them.
 constexpr int GDR_NONE = 0x7ffffff0;
-typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
-typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t gdr_buffer(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)swa_uniform((int64_t)p), 0,
                                              __builtin_amdgcn_readfirstlane((int)(bytes < 0 ? 0 : bytes)), 0x00027000);

@@ -11,6 +11,7 @@
 
 namespace kd {
 int64_t gdr_pass_grid(int64_t items, int& run);
+void gdr_plan(GdrArgs& a, bool packed);
 hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st);
 hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st);
 hipError_t launch_gdr_step(int bf16, const GdrArgs& a, hipStream_t st);
@@ -66,20 +67,6 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     return KD_OK;
 }
 
-// Offsets of the workspace's parts: records, dS, X and (bf16) its remainder.
-struct GdrSpace {
-    size_t ds, x, x2, bytes;
-};
-GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool bwd) {
-    const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
-    GdrSpace w;
-    w.ds = up256(n * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>(bwd) : kd::gdr_rec_bytes<float>(bwd)));
-    w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
-    w.x2 = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
-    w.bytes = w.x2 + (bwd && es == 2 ? up256(n * kd::GDR_C * d->dv * es) : 0);
-    return w;
-}
-
 kd::GdrArgs gdr_args(const kd_gdr_desc* d, const GdrSizes& s, const void* q, const void* k, const void* v, const void* g,
                      const void* beta, const int32_t* cu) {
     kd::GdrArgs a = {};
@@ -106,6 +93,27 @@ kd::GdrArgs gdr_args(const kd_gdr_desc* d, const GdrSizes& s, const void* q, con
     return a;
 }
 
+// Offsets of the workspace's parts: records; backward: dS, X and (bf16) its
+// remainder; forward in segments: their states and maps (si and m are equal
+// where a sequence is not cut).
+struct GdrSpace {
+    size_t ds, x, x2, si, m, bytes;
+};
+GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool packed, bool bwd) {
+    const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
+    GdrSpace w;
+    w.ds = up256(n * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>(bwd) : kd::gdr_rec_bytes<float>(bwd)));
+    w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
+    w.x2 = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    w.si = w.x2 + (bwd && es == 2 ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    kd::GdrArgs a = gdr_args(d, s, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+    kd::gdr_plan(a, packed);
+    const bool cut = !bwd && a.nseg > 1;
+    w.m = w.si + (cut ? up256((size_t)a.segs * d->Hv * d->dv * d->dk * 4) : 0);
+    w.bytes = w.m + (cut ? up256((size_t)a.segs * d->Hv * d->dk * d->dk * 4) : 0);
+    return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,7 +121,7 @@ extern "C" {
 size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc* d, int packed, int backward) {
     GdrSizes s;
     if (check_gdr(d, packed != 0, &s) != KD_OK) return 0;
-    return gdr_space(d, s, backward != 0).bytes;
+    return gdr_space(d, s, packed != 0, backward != 0).bytes;
 }
 
 kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
@@ -127,7 +135,7 @@ kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void
     for (const void* p : ptrs)
         if (misaligned(p)) return KD_ERR_ALIGN;
     if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
-    const GdrSpace w = gdr_space(d, s, false);
+    const GdrSpace w = gdr_space(d, s, cu != nullptr, false);
     const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
     const Range ins[] = {range_of(q, s.q),         range_of(k, s.k),       range_of(v, s.v),
                          range_of(g, s.gate),      range_of(beta, s.gate), range_of(S0, S0 ? s.state : 0),
@@ -142,6 +150,11 @@ kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.ST = ST;
     a.hs = hs;
     a.rec = ws;
+    kd::gdr_plan(a, cu != nullptr);
+    if (w.m > w.si) {
+        a.SI = (float*)((char*)ws + w.si);
+        a.M = (float*)((char*)ws + w.m);
+    }
     return done(kd::launch_gdr_fwd(d->dtype == KD_BF16, a, (hipStream_t)stream));
 }
 
@@ -157,7 +170,7 @@ kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void
     for (const void* p : ptrs)
         if (misaligned(p)) return KD_ERR_ALIGN;
     if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
-    const GdrSpace w = gdr_space(d, s, true);
+    const GdrSpace w = gdr_space(d, s, cu != nullptr, true);
     const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
     const Range ins[] = {range_of(q, s.q),    range_of(k, s.k),       range_of(v, s.v),
                          range_of(g, s.gate), range_of(beta, s.gate), range_of(hs, hs ? hsb : 0),

@@ -199,7 +199,14 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // The pass: four waves of 16 value columns each.  K and Q of a chunk come by
 // loads straight to LDS, two chunks' worth; what else it needs through
 // registers.
-template <class E, int DK, bool SAVE>
+//
+// Few heads and long sequences (gdr_plan): a sequence is cut into segments, all
+// of which pass at once.  A segment maps the state that enters it to S M + N.
+// GDR_MAPS passes over segments without their outputs, for N (from a zero
+// state) and for M (dk columns, from the identity and without values); a small
+// kernel chains them; then the pass runs from the states it found.
+enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
+template <class E, int DK, int MODE>
 __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
@@ -211,17 +218,23 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
         GdrSide<E, false> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int slices = (a.dv + 63) / 64;
+    const int vslices = (a.dv + 63) / 64, slices = MODE == GDR_MAPS ? vslices + (a.dk + 63) / 64 : vslices;
     const int64_t id = blockIdx.x;
     int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;      // neighbours, which share keys, on one XCD
-    if (item >= (int64_t)a.B * a.Hv * slices) return;
-    const int slice = item % slices;
+    if (item >= (int64_t)a.segs * a.Hv * slices) return;
+    int slice = item % slices;
     item /= slices;
-    const int hv = item % a.Hv, hk = hv / (a.Hv / a.Hk);
-    const GdrSeq s = gdr_seq(a, item / a.Hv);
-    const int64_t seq = item / a.Hv;
-    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, a.dv - 1);
-    const bool work = dv0 < a.dv;
+    const int hv = item % a.Hv, hk = hv / (a.Hv / a.Hk), slot = item / a.Hv;
+    GdrSegment sg;
+    if (!gdr_segment(a, slot, sg)) return;
+    const GdrSeq s = sg.s;
+    const int64_t seq = sg.seq;
+    const bool map = MODE == GDR_MAPS && slice >= vslices;
+    if (MODE == GDR_MAPS && (sg.last || (map && sg.j == 0))) return;
+    if (map) slice -= vslices;
+    const int width = map ? a.dk : a.dv;
+    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, width - 1);
+    const bool work = dv0 < width;
     const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
     const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * 64;
@@ -238,11 +251,18 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
     // two packed tiles are a fragment in natural order), column: the lane's value
     floatx4 S[2 * NK];
-    const int64_t state = ((seq * a.Hv + hv) * (int64_t)a.dv + col) * a.dk + 8 * g;
+    const int64_t at = (int64_t)col * a.dk + 8 * g, size = (int64_t)a.dv * a.dk;
+    const float* from = sg.j == 0 ? (a.S0 ? a.S0 + (seq * a.Hv + hv) * size : nullptr)
+                                  : MODE == GDR_MAPS ? nullptr : a.SI + ((int64_t)slot * a.Hv + hv) * size;
 #pragma unroll
     for (int x = 0; x < 2 * NK; ++x) {
         S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (a.S0 && 32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(a.S0 + state + 32 * (x / 2) + 4 * (x & 1));
+        if (map) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[x][r] = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r == dv0 + l16 ? 1.f : 0.f;
+        } else if (from && 32 * (x / 2) + 8 * g < a.dk) {
+            S[x] = *reinterpret_cast<const floatx4*>(from + at + 32 * (x / 2) + 4 * (x & 1));
+        }
     }
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
@@ -252,9 +272,9 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     const GdrFetch<E, DK> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
     auto fetch = [&](int n, int buf) {
         kf(sm.k[buf], n * GDR_C, w);
-        qf(sm.q[buf], n * GDR_C, w);
+        if (MODE != GDR_MAPS) qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, false> ahead(vb, a.vs[1], a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, false> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
     auto load = [&](int n) {
         ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), tid);
@@ -295,7 +315,8 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 Frag y[4];      // the next ones: keys, then queries
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    y[t] = p + 1 < NK ? T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g) : T::template ld_row<DK>(qt, 16 * t + l16, 0, g);
+                    y[t] = p + 1 < NK ? T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g)
+                           : MODE == GDR_MAPS ? x[t] : T::template ld_row<DK>(qt, 16 * t + l16, 0, g);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sh[p], U[t]);
                 if (T::TWO) {
@@ -318,16 +339,17 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 Frag y[4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) y[t] = x[t];
-                if (p + 1 < NK) {
+                if (p + 1 < NK && MODE != GDR_MAPS) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p + 1, g);
                 }
-                if (p == 1 || NK == 1) {
+                if (p == 1) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) U[t][r] = be[t][r] * v[t][r] - bb[t][r] * U[t][r];
                 }
+                if (MODE == GDR_MAPS) continue;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], y[t], O[t]);
                 if (T::TWO) {
@@ -345,10 +367,11 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
-            if (early) qf(sm.q[buf ^ 1], (n + 1) * GDR_C, w);
+            if (early && MODE != GDR_MAPS) qf(sm.q[buf ^ 1], (n + 1) * GDR_C, w);
             Frag P[6], kc[2 * NK];
+            if (MODE != GDR_MAPS)
 #pragma unroll
-            for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+                for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
 #pragma unroll
             for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
 #pragma unroll
@@ -368,21 +391,23 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
             if (more) ahead.load(rec0 + (n + 1) * a.Hv * gdr_rec_bytes<E>(false), tid);
             const float eC = sd.vec[256];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) O[t] *= sd.vec[192 + 16 * t + l16];
-#pragma unroll
             for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
+            if (MODE != GDR_MAPS) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f[j] = T::pack(U[2 * j], U[2 * j + 1]);
-                f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
-            }
+                for (int t = 0; t < 4; ++t) O[t] *= sd.vec[192 + 16 * t + l16];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < 2; ++j) {
+                    f[j] = T::pack(U[2 * j], U[2 * j + 1]);
+                    f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+                }
 #pragma unroll
-                for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f[j], P[gdr_block(t, j)], O[t]);
-                if (T::TWO) {
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                    for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f2[j], P[gdr_block(t, j)], O[t]);
+                    for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f[j], P[gdr_block(t, j)], O[t]);
+                    if (T::TWO) {
+#pragma unroll
+                        for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f2[j], P[gdr_block(t, j)], O[t]);
+                    }
                 }
             }
 #pragma unroll
@@ -405,11 +430,12 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                 if (j == 0) {
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
+                    if (MODE != GDR_MAPS)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) gdr_store(ob0, oat[t], O[t], (const E*)nullptr);
+                        for (int t = 0; t < 4; ++t) gdr_store(ob0, oat[t], O[t], (const E*)nullptr);
                 }
             }
-            if (SAVE) {
+            if (MODE == GDR_SAVE) {
                 const auto hs = gdr_buffer((const E*)a.hs + ((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
 #pragma unroll
                 for (int p = 0; p < NK; ++p) gdr_store(hs, hat[p], sh[p]);
@@ -431,10 +457,65 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
         chunk(n, 0);
         if (n + 1 < NC) chunk(n + 1, NBUF - 1);
     }
-    if (a.ST && work && dv0 + l16 < a.dv) {
+    float* to = MODE != GDR_MAPS ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
+                : map            ? a.M + ((int64_t)slot * a.Hv + hv) * a.dk * a.dk
+                                 : a.SI + ((int64_t)(slot + 1) * a.Hv + hv) * size;
+    if (to && work && dv0 + l16 < width) {
 #pragma unroll
         for (int x = 0; x < 2 * NK; ++x)
-            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(a.ST + state + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(to + at + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+    }
+}
+
+// The states entering a sequence's segments, one after the other: SI_(j+1) =
+// SI_j M_j + N_j, where SI_(j+1) holds N_j (the first one is the state itself).
+// One wave per 16 values of a head, in fp32 products: the state's accumulators
+// are the next product's B operand.
+template <int DK>
+__global__ __launch_bounds__(64, 1) void kd_gdr_chain_kernel(GdrArgs a)
+{
+    constexpr int NT = DK / 16;
+    const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
+    const int hv = blockIdx.y, seq = blockIdx.z, v = min((int)blockIdx.x * 16 + l16, a.dv - 1);
+    const GdrSeq s = gdr_seq(a, seq);
+    const int n = (gdr_chunks(s.T) + a.seg - 1) / a.seg, slot = a.cu ? s.row0 / GDR_C / a.seg + seq : seq * a.nseg;
+    const int64_t size = (int64_t)a.dv * a.dk;
+    if (n < 3) return;
+    // (tile x, register r: key channel 32 (x / 2) + 8 g + 4 (x % 2) + r, as in the pass)
+    auto row = [&](int j) { return a.SI + ((int64_t)(slot + j) * a.Hv + hv) * size + (int64_t)v * a.dk + 8 * g; };
+    floatx4 S[NT], N[NT];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(row(1) + 32 * (x / 2) + 4 * (x & 1));
+    }
+    for (int j = 1; j + 1 < n; ++j) {
+        const float* M = a.M + ((int64_t)(slot + j) * a.Hv + hv) * a.dk * a.dk;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            N[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (32 * (x / 2) + 8 * g < a.dk) N[x] = *reinterpret_cast<const floatx4*>(row(j + 1) + 32 * (x / 2) + 4 * (x & 1));
+        }
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int k = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r;
+                float m[NT];
+#pragma unroll
+                for (int y = 0; y < NT; ++y) {      // the operand's row l16 of tile y, as the state's rows are laid out
+                    const int c = 32 * (y / 2) + 8 * (l16 >> 2) + 4 * (y & 1) + (l16 & 3);
+                    m[y] = k < a.dk && c < a.dk ? M[k * a.dk + c] : 0.f;
+                }
+#pragma unroll
+                for (int y = 0; y < NT; ++y) N[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[y], S[x][r], N[y], 0, 0, 0);
+            }
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            S[x] = N[x];
+            if (32 * (x / 2) + 8 * g < a.dk && blockIdx.x * 16 + l16 < a.dv)
+                *reinterpret_cast<floatx4*>(row(j + 1) + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+        }
     }
 }
 
@@ -469,10 +550,33 @@ template <class E, int DK>
 static hipError_t gdr_pass(const GdrArgs& a, hipStream_t st)
 {
     int run;
-    const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 63) / 64), run);
-    if (a.hs) kd_gdr_pass_kernel<E, DK, true><<<(unsigned)grid, 256, 0, st>>>(a, run);
-    else kd_gdr_pass_kernel<E, DK, false><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    const int64_t heads = (int64_t)a.segs * a.Hv, vs = (a.dv + 63) / 64;
+    if (a.SI) {
+        const int64_t grid = gdr_pass_grid(heads * (vs + (a.dk + 63) / 64), run);
+        kd_gdr_pass_kernel<E, DK, GDR_MAPS><<<(unsigned)grid, 256, 0, st>>>(a, run);
+        kd_gdr_chain_kernel<DK><<<dim3((a.dv + 15) / 16, a.Hv, a.B), 64, 0, st>>>(a);
+    }
+    const int64_t grid = gdr_pass_grid(heads * vs, run);
+    if (a.hs) kd_gdr_pass_kernel<E, DK, GDR_SAVE><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    else kd_gdr_pass_kernel<E, DK, GDR_OUT><<<(unsigned)grid, 256, 0, st>>>(a, run);
     return hipGetLastError();
+}
+
+// Segments.  A pass takes as long as its longest sequence, one workgroup a
+// compute unit; the maps cost about as much work again as the pass itself.  So
+// sequences are cut where they leave three quarters of the 256 compute units
+// idle, into as many segments as fill them, of at least 8 chunks.  Packed
+// sequences are cut by what their average length would be.
+void gdr_plan(GdrArgs& a, bool packed)
+{
+    const int64_t wgs = (int64_t)a.B * a.Hv * ((a.dv + 63) / 64);
+    const int NC = packed ? (a.T / a.B + GDR_C - 1) / GDR_C : (a.T + GDR_C - 1) / GDR_C;
+    int n = wgs * 4 <= 256 ? (int)(256 / wgs) : 1;
+    n = n < NC / 8 ? n : NC / 8;
+    if (n < 3) n = 1;
+    a.seg = n > 1 ? (NC + n - 1) / n : 1 << 24;
+    a.nseg = n > 1 ? (NC + a.seg - 1) / a.seg : 1;
+    a.segs = packed ? (int)((int64_t)a.T / GDR_C / a.seg + a.B) : a.B * a.nseg;
 }
 
 hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st)

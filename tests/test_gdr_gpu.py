@@ -153,6 +153,27 @@ def test_packed_sequences(lens, dtype):
         assert torch.equal(o[0], got["o"][a:b]) and torch.equal(ST[0], got["ST"][i])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv,state", [([1700], 1, 1, 64, 64, True), ([2051], 1, 2, 128, 72, False),
+                                                    ([1600, 1600], 1, 1, 40, 16, True)])
+def test_long_sequences_of_few_heads(lens, Hk, Hv, dk, dv, state, dtype):
+    """Cut into segments that pass at once."""
+    torch = _torch()
+    t = inputs((len(lens), lens[0]), Hk, Hv, dk, dv, dtype, lens[0], state=state)
+    got = run(t, 0.2)
+    compare(t, got, 0.2, dtype)
+    assert all(torch.equal(x, run(t, 0.2)[n]) for n, x in got.items())
+
+
+def test_long_packed_sequences_of_few_heads():
+    torch = _torch()
+    lens = [2000, 1, 0, 700, 5000]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    t = inputs((int(cu[-1]),), 1, 1, 64, 64, "fp32", 77, n=len(lens))
+    got = run(t, 0.2, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    compare(t, got, 0.2, "fp32", [(0, int(a), int(b)) for a, b in zip(cu[:-1], cu[1:])])
+
+
 def test_rows_behind_the_last_sequence_are_left_and_bad_offsets_stay_inside():
     import ctypes
 
