@@ -322,10 +322,11 @@ __host__ __device__ constexpr int64_t gdr_rec_bytes(bool bwd) {
 // last they repeat it); columns past dk keep what the tile holds (zeros).  The
 // addresses are a scalar base and one 32-bit offset per lane that all chunks
 // share.
-template <class E, int DK>
+template <class E, int DK, int NT>
 struct GdrFetch {
     typedef SwaTile<E, DK> TL;
-    static constexpr int STEP = 256 / TL::CPR, NL = 64 / STEP;
+    static constexpr int STEP = NT / TL::CPR, NL = 64 / STEP;
+    static_assert(64 % STEP == 0, "whole rounds");
     const E* base;
     int64_t rs;
     int rows, dk, r, ch;
@@ -348,30 +349,30 @@ struct GdrFetch {
 #pragma unroll
             for (int i = 0; i < NL; ++i)
                 asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(lane[i]),
-                             "s"(swa_uniform((int64_t)b)), "i"(i * 4096)
+                             "s"(swa_uniform((int64_t)b)), "i"(i * NT * 16)
                              : "memory", "m0", "scc");
         } else {
             const int last = rows - 1 - row0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 const int rr = r + i * STEP, x = (ch ^ TL::swz(rr)) * TL::EPC;
-                if (x < dk) load_lds16(to + i * 4096, b + (int64_t)min(rr, last) * rs + x);
+                if (x < dk) load_lds16(to + i * NT * 16, b + (int64_t)min(rr, last) * rs + x);
             }
         }
     }
 };
 
 // What a pass reads of a chunk beside K and Q: the end of its record (A or A^T,
-// P or P^T, and the gate factors) and 64 columns of V (or dO).  The
-// workgroup's 256 threads load it to registers a chunk ahead and put it in LDS
-// when the chunk before is done.
-template <class E, bool BWD>
+// P or P^T, and the gate factors) and 16 columns of V (or dO) a wave.  The
+// workgroup's threads load it to registers a chunk ahead and put it in LDS when
+// the chunk before is done.
+template <class E, bool BWD, int NW>
 struct GdrSide {
     static constexpr int REC = (GdrT<E>::TWO ? (BWD ? 4 : 3) : 2) * GDR_BLOCKS * 512;      // elements
     static constexpr int PIECES = (REC * (int)sizeof(E) + GDR_VEC * 4) / 16;
     E rec[REC];
     float vec[GDR_VEC];
-    E v[64 * 64];
+    E v[64 * 16 * NW];
 };
 // Rows of a matrix at a wave-uniform address as a buffer: what lies past its
 // bytes reads as zero and is not written, so the ends of a sequence and of a
@@ -401,38 +402,39 @@ __device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floa
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{x[4], x[5], x[6], x[7]}), r, at + 16, 0, 0);
 }
 
-template <class E, bool BWD>
+template <class E, bool BWD, int NW>
 struct GdrSideAhead {
-    typedef SwaTile<E, 64> TV;
-    static constexpr int N = (GdrSide<E, BWD>::PIECES + 255) / 256, M = 64 * TV::CPR / 256, STEP = 256 / TV::CPR;
+    typedef SwaTile<E, 16 * NW> TV;
+    typedef GdrSide<E, BWD, NW> Side;
+    static constexpr int NT = 64 * NW, N = (Side::PIECES + NT - 1) / NT, M = 64 * TV::CPR / NT, STEP = NT / TV::CPR;
     floatx4 x[N], v[M];
     const E* vb;
     int64_t vs;
     int T, cols, at;
-    // rows of v: 64 columns from vb on, of which `cols` are there
+    // rows of v: 16 NW columns from vb on, of which `cols` are there
     __device__ __forceinline__ GdrSideAhead(const E* vb_, int64_t vs_, int cols_, int T_, int tid) : vb(vb_), vs(vs_), T(T_), cols(cols_) {
         const int c = tid % TV::CPR * TV::EPC;
         at = c < cols ? (int)((tid / TV::CPR * vs + c) * (int)sizeof(E)) : GDR_NONE;
     }
     // a chunk's record from `rec` on
     __device__ __forceinline__ void load(const char* rec, int tid) {
-        const auto r = gdr_buffer(rec, GdrSide<E, BWD>::PIECES * 16);
+        const auto r = gdr_buffer(rec, Side::PIECES * 16);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = gdr_load(r, (i * 256 + tid) * 16);
+        for (int i = 0; i < N; ++i) x[i] = gdr_load(r, (i * NT + tid) * 16);
     }
     // rows `row` .. of v
     __device__ __forceinline__ void load_v(int row) {
-        const auto r = gdr_buffer(vb + row * vs, ((min(T - row, 64) - 1) * vs + min(cols, 64)) * (int)sizeof(E));
+        const auto r = gdr_buffer(vb + row * vs, ((min(T - row, 64) - 1) * vs + min(cols, 16 * NW)) * (int)sizeof(E));
 #pragma unroll
         for (int i = 0; i < M; ++i) v[i] = gdr_load(r, at + (at == GDR_NONE ? 0 : (int)(i * STEP * vs * (int)sizeof(E))));
     }
-    __device__ __forceinline__ void store(GdrSide<E, BWD>& s, int tid) const {
+    __device__ __forceinline__ void store(Side& s, int tid) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)      // (vec follows rec)
-            if (i < N - 1 || (N - 1) * 256 + tid < GdrSide<E, BWD>::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * 256 + tid] = x[i];
+            if (i < N - 1 || (N - 1) * NT + tid < Side::PIECES) reinterpret_cast<floatx4*>(s.rec)[i * NT + tid] = x[i];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            const int to = i * 256 + tid;
+            const int to = i * NT + tid;
             *reinterpret_cast<floatx4*>(s.v + TV::off(to / TV::CPR, to % TV::CPR)) = v[i];
         }
     }

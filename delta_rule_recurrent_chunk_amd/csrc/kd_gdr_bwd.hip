@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     constexpr int PPT = T::TWO ? 2 : 1;      // P^T's part of what is staged, behind A^T
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, true> side[NBUF];
+        GdrSide<E, true, 4> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -64,14 +64,14 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
-    const GdrFetch<E, DK> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
+    const GdrFetch<E, DK, 256> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
     auto fetch = [&](int n, int buf) {
         kf(sm.k[buf], n * GDR_C, w);
         qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, true> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, true, 4> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(true) +
-                       (gdr_rec_bytes<E>(true) - GdrSide<E, true>::PIECES * 16);
+                       (gdr_rec_bytes<E>(true) - GdrSide<E, true, 4>::PIECES * 16);
     auto load = [&](int n) {
         ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), tid);
         ahead.load_v(n * GDR_C);
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         if (work) {
             const E* kt = sm.k[buf];
             const E* qt = sm.q[buf];
-            const GdrSide<E, true>& sd = sm.side[buf];
+            const GdrSide<E, true, 4>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;

@@ -196,9 +196,11 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
         }
 }
 
-// The pass: four waves of 16 value columns each.  K and Q of a chunk come by
+// The pass: NW waves of 16 value columns each.  K and Q of a chunk come by
 // loads straight to LDS, two chunks' worth; what else it needs through
-// registers.
+// registers.  Four waves (one a SIMD) where there are workgroups of them for
+// every compute unit at most, eight otherwise (bf16): two waves of a SIMD fill
+// each other's waits.
 //
 // Few heads and long sequences (gdr_plan): a sequence is cut into segments, all
 // of which pass at once.  A segment maps the state that enters it to S M + N.
@@ -206,19 +208,19 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // state) and for M (dk columns, from the identity and without values); a small
 // kernel chains them; then the pass runs from the states it found.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
-template <class E, int DK, int MODE>
-__global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
+template <class E, int DK, int MODE, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, NC0 = 16 * NW;      // (columns of a workgroup)
     constexpr int PP = T::TWO ? 2 : 1;
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, false> side[NBUF];
+        GdrSide<E, false, NW> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int vslices = (a.dv + 63) / 64, slices = MODE == GDR_MAPS ? vslices + (a.dk + 63) / 64 : vslices;
+    const int vslices = (a.dv + NC0 - 1) / NC0, slices = MODE == GDR_MAPS ? vslices + (a.dk + NC0 - 1) / NC0 : vslices;
     const int64_t id = blockIdx.x;
     int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;      // neighbours, which share keys, on one XCD
     if (item >= (int64_t)a.segs * a.Hv * slices) return;
@@ -233,11 +235,11 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     if (MODE == GDR_MAPS && (sg.last || (map && sg.j == 0))) return;
     if (map) slice -= vslices;
     const int width = map ? a.dk : a.dv;
-    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, width - 1);
+    const int dv0 = slice * NC0 + 16 * w, col = min(dv0 + l16, width - 1);
     const bool work = dv0 < width;
     const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
-    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * 64;
+    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * NC0;
     const E* ob = (const E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
     const int NC = gdr_chunks(s.T), os = a.Hv * a.dv;
     // where the lane's four values of row 16 t + l16, and its eight of a kept state, go
@@ -266,15 +268,15 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     }
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 64 * NW) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
-    const GdrFetch<E, DK> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
+    const GdrFetch<E, DK, 64 * NW> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
     auto fetch = [&](int n, int buf) {
         kf(sm.k[buf], n * GDR_C, w);
         if (MODE != GDR_MAPS) qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, false> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, false, NW> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
     auto load = [&](int n) {
         ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), tid);
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
         if (work) {
             const E* kt = sm.k[buf];
             const E* qt = sm.q[buf];
-            const GdrSide<E, false>& sd = sm.side[buf];
+            const GdrSide<E, false, NW>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             Frag sh[NK], sl[NK], x[4], A[6], A2[T::TWO ? 6 : 1], f[2], f2[2];
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                v[t] = T::template ld_acc<64>(sd.v, t, 16 * w, lane);
+                v[t] = T::template ld_acc<NC0>(sd.v, t, 16 * w, lane);
                 be[t] = factor(0, t);
                 bb[t] = factor(1, t);
             }
@@ -372,8 +374,10 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
             if (MODE != GDR_MAPS)
 #pragma unroll
                 for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+            if (NW == 4) {
 #pragma unroll
-            for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
+                for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
             // (every round over the four tiles: products that do not wait for each other)
@@ -421,6 +425,10 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
             const auto ob0 = gdr_buffer(ob + (int64_t)n * GDR_C * os, ((int64_t)(min(s.T - n * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                if (NW != 4) {
+#pragma unroll
+                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane);
+                }
 #pragma unroll
                 for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f[j], S[y]);
                 if (T::TWO) {
@@ -428,8 +436,9 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
                     for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
                 }
                 if (j == 0) {
+                    if (NW == 4)
 #pragma unroll
-                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
+                        for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
                     if (MODE != GDR_MAPS)
 #pragma unroll
                         for (int t = 0; t < 4; ++t) gdr_store(ob0, oat[t], O[t], (const E*)nullptr);
@@ -460,7 +469,15 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
     float* to = MODE != GDR_MAPS ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
                 : map            ? a.M + ((int64_t)slot * a.Hv + hv) * a.dk * a.dk
                                  : a.SI + ((int64_t)(slot + 1) * a.Hv + hv) * size;
-    if (to && work && dv0 + l16 < width) {
+    if (map) {      // transposed, for the chain
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r;
+                if (work && dv0 + l16 < width && c < a.dk) to[(int64_t)c * a.dk + dv0 + l16] = S[x][r];
+            }
+    } else if (to && work && dv0 + l16 < width) {
 #pragma unroll
         for (int x = 0; x < 2 * NK; ++x)
             if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(to + at + 32 * (x / 2) + 4 * (x & 1)) = S[x];
@@ -469,53 +486,61 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 
 // The states entering a sequence's segments, one after the other: SI_(j+1) =
 // SI_j M_j + N_j, where SI_(j+1) holds N_j (the first one is the state itself).
-// One wave per 16 values of a head, in fp32 products: the state's accumulators
-// are the next product's B operand.
+// A workgroup per 16 values of a head, in fp32 products: the state's
+// accumulators are the next product's B operand.  Its four waves make NT / 4
+// tiles of rows each and hand them to each other through LDS; maps load a
+// segment ahead.
 template <int DK>
-__global__ __launch_bounds__(64, 1) void kd_gdr_chain_kernel(GdrArgs a)
+__global__ __launch_bounds__(256, 1) void kd_gdr_chain_kernel(GdrArgs a)
 {
-    constexpr int NT = DK / 16;
-    const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
+    constexpr int NT = DK / 16, NY = NT / 4;
+    __shared__ __align__(16) floatx4 tile[2][NT][64];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int hv = blockIdx.y, seq = blockIdx.z, v = min((int)blockIdx.x * 16 + l16, a.dv - 1);
     const GdrSeq s = gdr_seq(a, seq);
     const int n = (gdr_chunks(s.T) + a.seg - 1) / a.seg, slot = a.cu ? s.row0 / GDR_C / a.seg + seq : seq * a.nseg;
     const int64_t size = (int64_t)a.dv * a.dk;
     if (n < 3) return;
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     // (tile x, register r: key channel 32 (x / 2) + 8 g + 4 (x % 2) + r, as in the pass)
-    auto row = [&](int j) { return a.SI + ((int64_t)(slot + j) * a.Hv + hv) * size + (int64_t)v * a.dk + 8 * g; };
-    floatx4 S[NT], N[NT];
-#pragma unroll
-    for (int x = 0; x < NT; ++x) {
-        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(row(1) + 32 * (x / 2) + 4 * (x & 1));
-    }
-    for (int j = 1; j + 1 < n; ++j) {
+    auto channel = [&](int x, int i) { return 32 * (x / 2) + 8 * i + 4 * (x & 1); };
+    auto state = [&](int j, int x) {
+        return a.SI + ((int64_t)(slot + j) * a.Hv + hv) * size + (int64_t)v * a.dk + channel(x, g);
+    };
+    floatx4 S[NT], N[NY], m[NY][NT];
+    auto load = [&](int j) {
         const float* M = a.M + ((int64_t)(slot + j) * a.Hv + hv) * a.dk * a.dk;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            N[x] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (32 * (x / 2) + 8 * g < a.dk) N[x] = *reinterpret_cast<const floatx4*>(row(j + 1) + 32 * (x / 2) + 4 * (x & 1));
+        for (int y = 0; y < NY; ++y) {
+            const int own = NY * w + y, c = channel(own, l16 >> 2) + (l16 & 3);      // the operand's row, as the state's are laid out
+            N[y] = channel(own, g) < a.dk ? *reinterpret_cast<const floatx4*>(state(j + 1, own)) : zero;
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+                m[y][x] = c < a.dk && channel(x, g) < a.dk ? *reinterpret_cast<const floatx4*>(M + (int64_t)c * a.dk + channel(x, g)) : zero;
         }
+    };
+#pragma unroll
+    for (int x = 0; x < NT; ++x) S[x] = channel(x, g) < a.dk ? *reinterpret_cast<const floatx4*>(state(1, x)) : zero;
+    load(1);
+    for (int j = 1; j + 1 < n; ++j) {
+        floatx4 R[NY];
+#pragma unroll
+        for (int y = 0; y < NY; ++y) R[y] = N[y];
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int k = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r;
-                float m[NT];
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int y = 0; y < NT; ++y) {      // the operand's row l16 of tile y, as the state's rows are laid out
-                    const int c = 32 * (y / 2) + 8 * (l16 >> 2) + 4 * (y & 1) + (l16 & 3);
-                    m[y] = k < a.dk && c < a.dk ? M[k * a.dk + c] : 0.f;
-                }
+                for (int y = 0; y < NY; ++y) R[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[y][x][r], S[x][r], R[y], 0, 0, 0);
+        if (j + 2 < n) load(j + 1);
 #pragma unroll
-                for (int y = 0; y < NT; ++y) N[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[y], S[x][r], N[y], 0, 0, 0);
-            }
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            S[x] = N[x];
-            if (32 * (x / 2) + 8 * g < a.dk && blockIdx.x * 16 + l16 < a.dv)
-                *reinterpret_cast<floatx4*>(row(j + 1) + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+        for (int y = 0; y < NY; ++y) {
+            tile[j & 1][NY * w + y][lane] = R[y];
+            if (channel(NY * w + y, g) < a.dk && blockIdx.x * 16 + l16 < a.dv) *reinterpret_cast<floatx4*>(state(j + 1, NY * w + y)) = R[y];
         }
+        lds_barrier();
+#pragma unroll
+        for (int x = 0; x < NT; ++x) S[x] = tile[j & 1][x][lane];
     }
 }
 
@@ -546,32 +571,52 @@ hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st)
     return bwd ? gdr_prep<float, 128, true>(a, st) : gdr_prep<float, 128, false>(a, st);
 }
 
-template <class E, int DK>
-static hipError_t gdr_pass(const GdrArgs& a, hipStream_t st)
+// Columns of a pass's workgroup: see the kernel.
+template <class E>
+static int gdr_waves(int64_t heads, int columns) { return sizeof(E) == 2 && heads * ((columns + 63) / 64) > 256 && columns > 64 ? 8 : 4; }
+
+template <class E, int DK, int MODE, int NW>
+static void gdr_pass(const GdrArgs& a, hipStream_t st)
 {
+    constexpr int C = 16 * NW;
+    const int64_t heads = (int64_t)a.segs * a.Hv;
     int run;
-    const int64_t heads = (int64_t)a.segs * a.Hv, vs = (a.dv + 63) / 64;
-    if (a.SI) {
-        const int64_t grid = gdr_pass_grid(heads * (vs + (a.dk + 63) / 64), run);
-        kd_gdr_pass_kernel<E, DK, GDR_MAPS><<<(unsigned)grid, 256, 0, st>>>(a, run);
-        kd_gdr_chain_kernel<DK><<<dim3((a.dv + 15) / 16, a.Hv, a.B), 64, 0, st>>>(a);
+    const int64_t grid = gdr_pass_grid(heads * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
+    kd_gdr_pass_kernel<E, DK, MODE, NW><<<(unsigned)grid, 64 * NW, 0, st>>>(a, run);
+}
+template <class E, int DK, int MODE>
+static void gdr_pass(const GdrArgs& a, hipStream_t st)
+{
+    const int64_t heads = (int64_t)a.segs * a.Hv;
+    if constexpr (sizeof(E) == 2) {
+        if (MODE == GDR_MAPS ? gdr_waves<E>(2 * heads, min(a.dv, a.dk)) == 8 : gdr_waves<E>(heads, a.dv) == 8)
+            return gdr_pass<E, DK, MODE, 8>(a, st);
     }
-    const int64_t grid = gdr_pass_grid(heads * vs, run);
-    if (a.hs) kd_gdr_pass_kernel<E, DK, GDR_SAVE><<<(unsigned)grid, 256, 0, st>>>(a, run);
-    else kd_gdr_pass_kernel<E, DK, GDR_OUT><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    gdr_pass<E, DK, MODE, 4>(a, st);
+}
+template <class E, int DK>
+static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
+{
+    if (a.SI) {
+        gdr_pass<E, DK, GDR_MAPS>(a, st);
+        kd_gdr_chain_kernel<DK><<<dim3((a.dv + 15) / 16, a.Hv, a.B), 256, 0, st>>>(a);
+    }
+    if (a.hs) gdr_pass<E, DK, GDR_SAVE>(a, st);
+    else gdr_pass<E, DK, GDR_OUT>(a, st);
     return hipGetLastError();
 }
 
-// Segments.  A pass takes as long as its longest sequence, one workgroup a
-// compute unit; the maps cost about as much work again as the pass itself.  So
-// sequences are cut where they leave three quarters of the 256 compute units
-// idle, into as many segments as fill them, of at least 8 chunks.  Packed
-// sequences are cut by what their average length would be.
+// Segments.  A pass takes as long as its longest sequence, a few microseconds a
+// chunk, however few workgroups there are; the maps cost about as much work
+// again as the pass itself.  So sequences are cut where they leave three
+// quarters of the 256 compute units idle, into segments of at least 8 chunks,
+// as many as make 512 workgroups of four waves.  Packed sequences are cut by
+// what their average length would be.
 void gdr_plan(GdrArgs& a, bool packed)
 {
     const int64_t wgs = (int64_t)a.B * a.Hv * ((a.dv + 63) / 64);
     const int NC = packed ? (a.T / a.B + GDR_C - 1) / GDR_C : (a.T + GDR_C - 1) / GDR_C;
-    int n = wgs * 4 <= 256 ? (int)(256 / wgs) : 1;
+    int n = wgs * 4 <= 256 ? (int)(512 / wgs) : 1;
     n = n < NC / 8 ? n : NC / 8;
     if (n < 3) n = 1;
     a.seg = n > 1 ? (NC + n - 1) / n : 1 << 24;
@@ -583,8 +628,8 @@ hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st)
 {
     const hipError_t e = launch_gdr_prep(bf16, false, a, st);
     if (e != hipSuccess) return e;
-    if (bf16) return a.dk <= 64 ? gdr_pass<__bf16, 64>(a, st) : gdr_pass<__bf16, 128>(a, st);
-    return a.dk <= 64 ? gdr_pass<float, 64>(a, st) : gdr_pass<float, 128>(a, st);
+    if (bf16) return a.dk <= 64 ? gdr_passes<__bf16, 64>(a, st) : gdr_passes<__bf16, 128>(a, st);
+    return a.dk <= 64 ? gdr_passes<float, 64>(a, st) : gdr_passes<float, 128>(a, st);
 }
 
 // One token.  Lanes of a row's key channels, four each; both products with the

@@ -165,6 +165,24 @@ def test_long_sequences_of_few_heads(lens, Hk, Hv, dk, dv, state, dtype):
     assert all(torch.equal(x, run(t, 0.2)[n]) for n, x in got.items())
 
 
+@pytest.mark.parametrize("B,T,H,d", [(3, 70, 48, 128), (1, 1600, 32, 128), (9, 65, 16, 72)])
+def test_forward_of_many_heads(B, T, H, d):
+    """Eight waves a workgroup, in the maps of segments too."""
+    import delta_rule_recurrent_chunk_amd as kd
+    t = inputs((B, T), H // 4, H, d, d, "bf16", T)
+    o, ST = kd.gdr_fwd(*(t[n] for n in NAMES), t["S0"])
+    o2, ST2, _ = kd.gdr_fwd(*(t[n] for n in NAMES), t["S0"], save_states=True)
+    assert _torch().equal(o, o2) and _torch().equal(ST, ST2)
+    a = {n: f64(x) for n, x in t.items()}
+    for b in range(B):
+        for h in range(b, H, 5 if T < 100 else 16):
+            x = [a[n][b, :, h // 4 if n in ("q", "k") else h] for n in NAMES]
+            ro, st = R.tokens(*x, a["S0"][b, h], d ** -0.5)
+            e, es, _ = R.bounds(*x, st, d ** -0.5, 2.0 ** -8)
+            check("o", o[b, :, h], ro, 1.01 * (e["o"] + 2.0 ** -8 * np.abs(ro)))
+            check("ST", ST[b, h], st[-1], es)
+
+
 def test_long_packed_sequences_of_few_heads():
     torch = _torch()
     lens = [2000, 1, 0, 700, 5000]
