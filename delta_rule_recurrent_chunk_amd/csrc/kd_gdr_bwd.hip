@@ -274,12 +274,11 @@ struct GdrStage {
     static_assert(R * TL::CPR % 512 == 0, "whole rounds");
     floatx4 v[N];
     __device__ __forceinline__ void load(const E* src, int64_t rs, int rows, int cols, int tid) {
+        const int c = tid % TL::CPR * TL::EPC, step = 512 / TL::CPR * (int)rs * (int)sizeof(E);
+        const int at = c < cols ? (tid / TL::CPR * (int)rs + c) * (int)sizeof(E) : GDR_NONE;
+        const auto buf = gdr_buffer(src, ((rows - 1) * rs + cols) * (int)sizeof(E));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = i * 512 + tid, r = at / TL::CPR, c = at % TL::CPR * TL::EPC;
-            v[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (r < rows && c < cols) v[i] = *reinterpret_cast<const floatx4*>(src + r * rs + c);
-        }
+        for (int i = 0; i < N; ++i) v[i] = gdr_load(buf, at == GDR_NONE ? at : at + i * step);
     }
     __device__ __forceinline__ void store(E* tile, int tid) const {
 #pragma unroll
@@ -374,19 +373,15 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
             const int nv = min(DV, a.dv - v0);
             GdrStage<E, DK, DV> st;
             Frag A[6], A2[T::TWO ? 6 : 1];
-            E v[16];
             {
                 KD_LANE;
-                GdrStage<E, DV, 64> d, x, x2;
+                GdrStage<E, DV, 64> d, x, x2, v;
                 st.load((const E*)a.hs + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
                 d.load((const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0, (int64_t)a.Hv * a.dv, c.rows, nv, tid);
                 x.load((const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
                 if (T::TWO) x2.load((const E*)a.x2 + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+                v.load((const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0, a.vs[1], c.rows, nv, tid);
                 if (w < DV / 16) {
-                    const int col = min(16 * w + l16, nv - 1);
-                    const E* vb = (const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0 + col;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = vb[min(16 * (i / 4) + 4 * g + i % 4, c.rows - 1) * a.vs[1]];
                     const E* rec = (const E*)record + lane * 8;
 #pragma unroll
                     for (int i = 0; i < 6; ++i) {
@@ -408,6 +403,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 d.store(sm.d, tid);
                 x.store(sm.x, tid);
                 if (T::TWO) x2.store(sm.x2, tid);
+                v.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
             }
             __syncthreads();
             st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
@@ -431,17 +427,13 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     const floatx4 b = *reinterpret_cast<const floatx4*>(sm.bh + 16 * t + 4 * g);
                     floatx4 x = T::template ld_acc<DV>(sm.x, t, 16 * w, lane);
                     if (T::TWO) x += T::template ld_acc<DV>(sm.x2, t, 16 * w, lane);
+                    const floatx4 v = T::template ld_acc<DV>(sm.u, t, 16 * w, lane);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float vv = col < nv ? (float)v[4 * t + r] : 0.f;
                         // X.W for dbeta takes W itself (beta may be 0), U takes beta W
-                        x[r] *= vv - __builtin_amdgcn_exp2f(b[r]) * W[t][r];
-                        W[t][r] = be[r] * vv - bb[r] * W[t][r];
+                        x[r] = row16_sum(x[r] * (v[r] - __builtin_amdgcn_exp2f(b[r]) * W[t][r]));
+                        W[t][r] = be[r] * v[r] - bb[r] * W[t][r];
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int y = 1; y < 16; y *= 2) x[r] += __shfl_xor(x[r], y);
                     if (l16 == 0) {
                         floatx4* to = reinterpret_cast<floatx4*>(sm.xw[w] + 16 * t + 4 * g);
                         *to = v0 == 0 ? x : *to + x;
@@ -600,9 +592,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 brow += __shfl_xor(brow, 16);
                 brow += __shfl_xor(brow, 32);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int x = 1; x < 16; x *= 2) colsum[e] += __shfl_xor(colsum[e], x);
+                for (int e = 0; e < 4; ++e) colsum[e] = row16_sum(colsum[e]);
                 if (g == 0) {
                     sm.rows[j][r] = row;
                     sm.brow[j][r] = brow;
