@@ -276,7 +276,7 @@ struct GdrStage {
     __device__ __forceinline__ void load(const E* src, int64_t rs, int rows, int cols, int tid) {
         const int c = tid % TL::CPR * TL::EPC, step = 512 / TL::CPR * (int)rs * (int)sizeof(E);
         const int at = c < cols ? (tid / TL::CPR * (int)rs + c) * (int)sizeof(E) : GDR_NONE;
-        const auto buf = gdr_buffer(src, ((rows - 1) * rs + cols) * (int)sizeof(E));
+        const auto buf = gdr_buffer(src, rows > 0 ? ((rows - 1) * rs + cols) * (int)sizeof(E) : 0);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = gdr_load(buf, at == GDR_NONE ? at : at + i * step);
     }
@@ -307,7 +307,11 @@ struct GdrStage {
 template <class E, int DK, int DV>
 struct GdrGradLds {
     static constexpr bool TWO = GdrT<E>::TWO;
-    E k[64 * DK], q[64 * DK], s[DV * DK], x[64 * DV], x2[TWO ? 64 * DV : 8], u[64 * DV], u2[TWO ? 64 * DV : 8];
+    static constexpr int A = (TWO ? 2 : 1) * GDR_BLOCKS * 512;      // elements of A with its remainder
+    E k[64 * DK], q[64 * DK], s[DV * DK], x[64 * DV], x2[TWO ? 64 * DV : 8], u[64 * DV];
+    union {      // A is done with when U is made
+        E u2[TWO ? 64 * DV : 8], a[A];
+    };
     union {      // dO is done with when E and F are made
         E d[64 * DV];
         struct {
@@ -321,9 +325,11 @@ struct GdrGradLds {
     float ss[8];
 };
 
-// Gradients of one chunk's q, k, g and beta: eight waves per chunk and key
-// head, the value heads of the group one after the other, values in blocks of
-// DV.  bf16: X and U with their remainders, S0, dS, E and F rounded.
+// Gradients of a chunk's q, k, g and beta: eight waves per chunk and key head,
+// the value heads of the group one after the other, values in blocks of DV.
+// bf16: X and U with their remainders, S0, dS, E and F rounded.  As many
+// workgroups as compute units go over all chunks: what the next head or chunk
+// needs loads to registers beside the last stages of this one.
 template <class E, int DK, int DV>
 __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 {
@@ -336,27 +342,55 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     constexpr int NK = DK / 32, NV = DV / 32, CT = DK / 16, RT = CT / 2;      // column tiles of dq, row tiles of a wave
     __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
     const int tid = threadIdx.x, lane0 = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, G = a.Hv / a.Hk;
-    GdrChunk c;
-    if (!gdr_slot(a, slot, c)) return;
-    {
-        GdrStage<E, DK, 64> k, q;
-        k.load((const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2], a.ks[1], c.rows, a.dk, tid);
-        q.load((const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2], a.qs[1], c.rows, a.dk, tid);
-        k.store(sm.k, tid);
-        q.store(sm.q, tid);
-    }
+    const int G = a.Hv / a.Hk;
+    const int64_t items = (int64_t)a.slots * a.Hk;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     // this wave's tiles of dq^T and dk^T: column tile ct, row tiles r0 ..
     const int ct = w % CT, r0 = w / CT * RT;
     floatx4 dq[RT], dk[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) dq[t] = dk[t] = zero;
     // its tiles (i, j), j <= i, of the 64 x 64 matrices: number w and, for the first two waves, 8 + w
     auto tile_i = [](int n) { return n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3; };
     // (lane numbers made afresh in every phase: addresses that depend on them would otherwise be kept across all)
 #define KD_LANE const int lane = lane0 + opaque_zero(), l16 = lane & 15, g = lane >> 4
 
+    // the chunk after an item, if any
+    auto next = [&](int64_t item, GdrChunk& c) {
+        for (item += gridDim.x; item < items; item += gridDim.x)
+            if (gdr_slot(a, (int)(item / a.Hk), c)) return item;
+        return items;
+    };
+    GdrStage<E, DK, 64> lk, lq;
+    GdrStage<E, DK, DV> ls;
+    GdrStage<E, DV, 64> ld, lx, lx2, lv;
+    constexpr int AP = GdrGradLds<E, DK, DV>::A * (int)sizeof(E) / 16, NA = (AP + 511) / 512;      // 16-byte pieces
+    floatx4 la[NA];
+    // (without rows nothing is read, but the registers are written all the same,
+    // or their old values would have to be kept)
+    auto load = [&](int64_t item, GdrChunk c, int hg, int v0) {
+        if (item >= items) item = c.rows = c.first = c.base = 0;
+        const int hk = item % a.Hk, hv = hk * G + hg, nv = c.rows > 0 ? min(DV, a.dv - v0) : 0, kr = hg == 0 && v0 == 0 ? c.rows : 0;
+        const int64_t at = item / a.Hk * a.Hv + hv;
+        lk.load((const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2], a.ks[1], kr, a.dk, tid);
+        lq.load((const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2], a.qs[1], kr, a.dk, tid);
+        const auto rec = gdr_buffer((const char*)a.rec + at * gdr_rec_bytes<E>(true), c.rows > 0 ? AP * 16 : 0);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) la[i] = gdr_load(rec, (i * 512 + tid) * 16);
+        ls.load((const E*)a.hs + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
+        lv.load((const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0, a.vs[1], c.rows, nv, tid);
+        ld.load((const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0, (int64_t)a.Hv * a.dv, c.rows, nv, tid);
+        lx.load((const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+        if (T::TWO) lx2.load((const E*)a.x2 + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+    };
+    GdrChunk c, cn;
+    int64_t item = next((int64_t)blockIdx.x - gridDim.x, c), itemn;
+    load(item, c, 0, 0);
+
+#pragma unroll 1
+    for (; item < items; item = itemn, c = cn) {
+        itemn = next(item, cn);
+        const int hk = item % a.Hk, slot = item / a.Hk;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) dq[t] = dk[t] = zero;
 #pragma unroll 1
     for (int hg = 0; hg < G; ++hg) {
         const int hv = hk * G + hg;
@@ -372,23 +406,8 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         for (int v0 = 0; v0 < a.dv; v0 += DV) {
             const int nv = min(DV, a.dv - v0);
             GdrStage<E, DK, DV> st;
-            Frag A[6], A2[T::TWO ? 6 : 1];
             {
                 KD_LANE;
-                GdrStage<E, DV, 64> d, x, x2, v;
-                st.load((const E*)a.hs + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
-                d.load((const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0, (int64_t)a.Hv * a.dv, c.rows, nv, tid);
-                x.load((const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
-                if (T::TWO) x2.load((const E*)a.x2 + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
-                v.load((const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0, a.vs[1], c.rows, nv, tid);
-                if (w < DV / 16) {
-                    const E* rec = (const E*)record + lane * 8;
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) {
-                        A[i] = T::ld(rec + i * 512);
-                        if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
-                    }
-                }
                 __syncthreads();      // the head (or the values) before is done
                 if (v0 == 0) {
                     if (w == 0) {
@@ -398,22 +417,29 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                         sm.bl[lane] = (float)(b - (double)(float)b);
                     }
                     if (tid >= 64 && tid < 64 + 257) sm.vec[tid - 64] = vec[tid - 64];
+                    if (hg == 0) {
+                        lk.store(sm.k, tid);
+                        lq.store(sm.q, tid);
+                    }
                 }
-                st.store(sm.s, tid);
-                d.store(sm.d, tid);
-                x.store(sm.x, tid);
-                if (T::TWO) x2.store(sm.x2, tid);
-                v.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
+                ls.store(sm.s, tid);
+                ld.store(sm.d, tid);
+                lx.store(sm.x, tid);
+                if (T::TWO) lx2.store(sm.x2, tid);
+#pragma unroll
+                for (int i = 0; i < NA; ++i)
+                    if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
+                lv.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
             }
             __syncthreads();
             st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
             // W and U: 16 values a wave
+            floatx4 W[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) W[t] = zero;
             if (w < DV / 16) {
                 KD_LANE;
                 const int col = 16 * w + l16;
-                floatx4 W[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) W[t] = zero;
 #pragma unroll
                 for (int p = 0; p < NK; ++p) {
                     const Frag s = T::template ld_row<DK>(sm.s, col, p, g);
@@ -444,12 +470,24 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 for (int j = 0; j < 2; ++j) {
                     f[j] = T::pack(W[2 * j], W[2 * j + 1]);
                     f2[j] = T::rest(W[2 * j], W[2 * j + 1], f[j]);
+                    W[2 * j] = W[2 * j + 1] = zero;
                 }
+                const E* rec = sm.a + lane * 8;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) {
+                        const Frag A = T::ld(rec + gdr_block(t, j) * 512);
+                        W[t] = gdr_mma2<E>(f[j], f2[j], A, W[t]);
+                        if (T::TWO) W[t] = T::mma(f[j], T::ld(rec + gdr_part<E>() + gdr_block(t, j) * 512), W[t]);
+                    }
+            }
+            __syncthreads();
+            if (w < DV / 16) {
+                KD_LANE;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    floatx4 y = zero;
-#pragma unroll
-                    for (int j = 0; j <= t / 2; ++j) y = gdr_mma3<E>(f[j], f2[j], A[gdr_block(t, j)], A2[T::TWO ? gdr_block(t, j) : 0], y);
+                    const floatx4 y = W[t];
                     // lane: token, four values
                     const int to = TV::off(16 * t + l16, (16 * w + 4 * g) / TV::EPC) + 4 * g % TV::EPC;
                     const E4 hi = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
@@ -514,6 +552,10 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 }
             }
             __syncthreads();
+            {
+                const bool same = v0 + DV < a.dv || hg + 1 < G;
+                load(same ? item : itemn, same ? c : cn, v0 + DV < a.dv ? hg : same ? hg + 1 : 0, v0 + DV < a.dv ? v0 + DV : 0);
+            }
             // e^(bC - b) U dS
             {
                 KD_LANE;
@@ -676,6 +718,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         *reinterpret_cast<E4*>((E*)a.dq + to) = E4{(E)dq[t][0], (E)dq[t][1], (E)dq[t][2], (E)dq[t][3]};
         *reinterpret_cast<E4*>((E*)a.dk_ + to) = E4{(E)dk[t][0], (E)dk[t][1], (E)dk[t][2], (E)dk[t][3]};
     }
+    }
 }
 
 template <class E, int DK, int DV>
@@ -686,7 +729,8 @@ static hipError_t gdr_bwd(const GdrArgs& a, hipStream_t st)
     kd_gdr_back_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slots == 0) return e;
-    kd_gdr_grad_kernel<E, DK, DV><<<(unsigned)((int64_t)a.slots * a.Hk), 512, 0, st>>>(a);
+    const int64_t items = (int64_t)a.slots * a.Hk;
+    kd_gdr_grad_kernel<E, DK, DV><<<(unsigned)(items < 256 ? items : 256), 512, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -694,7 +738,10 @@ hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st)
 {
     const hipError_t e = launch_gdr_prep(bf16, true, a, st);
     if (e != hipSuccess) return e;
-    if (bf16) return a.dk <= 64 ? gdr_bwd<__bf16, 64, 128>(a, st) : gdr_bwd<__bf16, 128, 128>(a, st);
+    if (bf16) {
+        if (a.dk <= 64) return a.dv <= 64 ? gdr_bwd<__bf16, 64, 64>(a, st) : gdr_bwd<__bf16, 64, 128>(a, st);
+        return a.dv <= 64 ? gdr_bwd<__bf16, 128, 64>(a, st) : gdr_bwd<__bf16, 128, 128>(a, st);
+    }
     return a.dk <= 64 ? gdr_bwd<float, 64, 32>(a, st) : gdr_bwd<float, 128, 32>(a, st);
 }
 
