@@ -25,7 +25,8 @@ namespace kd {
 
 constexpr int GDR_C = 64;              // tokens of a chunk
 constexpr int GDR_BLOCKS = 6;          // 16 x 32 blocks of a lower triangular 64 x 64 matrix that hold anything
-constexpr int GDR_VEC = 5 * 64;        // floats of a chunk's gate factors
+constexpr int GDR_VEC = 7 * 64;        // floats of a chunk's gate factors: beta, beta e^b, e^(bC - b), scale e^b, {e^bC, whether a
+                                       // beta is next to 0}, b (base 2) and what its rounding left
 constexpr int GDR_MAX_STEP = 1 << 22;  // elements from one token to the next (64 of them in 32-bit offsets)
 
 typedef float floatx8 __attribute__((ext_vector_type(8)));

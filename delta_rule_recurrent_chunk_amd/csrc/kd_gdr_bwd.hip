@@ -318,10 +318,10 @@ struct GdrGradLds {
             E e[64 * 64], f[64 * 64];
         };
     };
-    float bh[64], bl[64], vec[GDR_VEC];
+    float vec[GDR_VEC];
     float rows[4][64], cols[4][64];      // of the two matrices that enter db
-    float brow[4][64];                   // of the one that enters dbeta
-    float xw[8][64], dot[8][64], send[8][64];
+    float xu[64], brow[4][64], xw[8][64];
+    float dot[4][64], send[4][64];
     float ss[8];
 };
 
@@ -339,64 +339,90 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     typedef SwaTile<E, DV> TV;
     typedef SwaTile<E, 64> TC;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = DK / 32, NV = DV / 32, CT = DK / 16, RT = CT / 2;      // column tiles of dq, row tiles of a wave
+    constexpr int NK = DK / 32, NV = DV / 32, CG = DK / 32, RT = CG / 2;      // pairs of column tiles of dq, row tiles of a wave
     __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
     const int tid = threadIdx.x, lane0 = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hv / a.Hk;
-    const int64_t items = (int64_t)a.slots * a.Hk;
+    const int items = a.slots * a.Hk;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    // this wave's tiles of dq^T and dk^T: column tile ct, row tiles r0 ..
-    const int ct = w % CT, r0 = w / CT * RT;
-    floatx4 dq[RT], dk[RT];
+    // this wave's tiles of dq^T and dk^T: two columns of tiles from key channel c0 on, row tiles r0 ..
+    const int cg = w % CG, c0 = 32 * cg, r0 = w / CG * RT;
+    floatx4 dq[2][RT], dk[2][RT];
     // its tiles (i, j), j <= i, of the 64 x 64 matrices: number w and, for the first two waves, 8 + w
     auto tile_i = [](int n) { return n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3; };
     // (lane numbers made afresh in every phase: addresses that depend on them would otherwise be kept across all)
 #define KD_LANE const int lane = lane0 + opaque_zero(), l16 = lane & 15, g = lane >> 4
 
     // the chunk after an item, if any
-    auto next = [&](int64_t item, GdrChunk& c) {
+    auto next = [&](int item, GdrChunk& c) {
         for (item += gridDim.x; item < items; item += gridDim.x)
-            if (gdr_slot(a, (int)(item / a.Hk), c)) return item;
+            if (gdr_slot(a, item / a.Hk, c)) return item;
         return items;
     };
     GdrStage<E, DK, 64> lk, lq;
     GdrStage<E, DK, DV> ls;
     GdrStage<E, DV, 64> ld, lx, lx2, lv;
     constexpr int AP = GdrGradLds<E, DK, DV>::A * (int)sizeof(E) / 16, NA = (AP + 511) / 512;      // 16-byte pieces
-    floatx4 la[NA];
-    // (without rows nothing is read, but the registers are written all the same,
-    // or their old values would have to be kept)
-    auto load = [&](int64_t item, GdrChunk c, int hg, int v0) {
+    floatx4 la[NA], lf;
+    // What the next head (or values, or chunk) needs, in three parts.  Without
+    // rows nothing is read, but the registers are written all the same, or their
+    // old values would have to be kept.
+    struct Next {
+        GdrChunk c;
+        int hk, hv, v0, nv, kr;
+        int64_t at;
+    };
+    auto which = [&](int item, GdrChunk c, int hg, int v0) {
+        Next n;
         if (item >= items) item = c.rows = c.first = c.base = 0;
-        const int hk = item % a.Hk, hv = hk * G + hg, nv = c.rows > 0 ? min(DV, a.dv - v0) : 0, kr = hg == 0 && v0 == 0 ? c.rows : 0;
-        const int64_t at = item / a.Hk * a.Hv + hv;
-        lk.load((const E*)a.k + c.base * a.ks[0] + (int64_t)c.first * a.ks[1] + hk * a.ks[2], a.ks[1], kr, a.dk, tid);
-        lq.load((const E*)a.q + c.base * a.qs[0] + (int64_t)c.first * a.qs[1] + hk * a.qs[2], a.qs[1], kr, a.dk, tid);
-        const auto rec = gdr_buffer((const char*)a.rec + at * gdr_rec_bytes<E>(true), c.rows > 0 ? AP * 16 : 0);
+        n.c = c;
+        n.hk = item % a.Hk;
+        n.hv = n.hk * G + hg;
+        n.v0 = v0;
+        n.nv = c.rows > 0 ? min(DV, a.dv - v0) : 0;
+        n.kr = hg == 0 && v0 == 0 ? c.rows : 0;
+        n.at = (int64_t)(item / a.Hk) * a.Hv + n.hv;
+        return n;
+    };
+    auto load1 = [&](const Next& n) {
+        ls.load((const E*)a.hs + (n.at * a.dv + n.v0) * a.dk, a.dk, n.nv, a.dk, tid);
+        lx.load((const E*)a.x + n.at * GDR_C * a.dv + n.v0, a.dv, n.c.rows, n.nv, tid);
+    };
+    auto load2 = [&](const Next& n) {
+        if (T::TWO) lx2.load((const E*)a.x2 + n.at * GDR_C * a.dv + n.v0, a.dv, n.c.rows, n.nv, tid);
+        ld.load((const E*)a.dO + ((n.c.base * a.T + n.c.first) * a.Hv + n.hv) * (int64_t)a.dv + n.v0, (int64_t)a.Hv * a.dv, n.c.rows, n.nv, tid);
+        lv.load((const E*)a.v + n.c.base * a.vs[0] + (int64_t)n.c.first * a.vs[1] + n.hv * a.vs[2] + n.v0, a.vs[1], n.c.rows, n.nv, tid);
+    };
+    auto load3 = [&](const Next& n) {
+        lk.load((const E*)a.k + n.c.base * a.ks[0] + (int64_t)n.c.first * a.ks[1] + n.hk * a.ks[2], a.ks[1], n.kr, a.dk, tid);
+        lq.load((const E*)a.q + n.c.base * a.qs[0] + (int64_t)n.c.first * a.qs[1] + n.hk * a.qs[2], a.qs[1], n.kr, a.dk, tid);
+        const char* record = (const char*)a.rec + n.at * gdr_rec_bytes<E>(true);
+        const auto rec = gdr_buffer(record, n.c.rows > 0 ? AP * 16 : 0);
 #pragma unroll
         for (int i = 0; i < NA; ++i) la[i] = gdr_load(rec, (i * 512 + tid) * 16);
-        ls.load((const E*)a.hs + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
-        lv.load((const E*)a.v + c.base * a.vs[0] + (int64_t)c.first * a.vs[1] + hv * a.vs[2] + v0, a.vs[1], c.rows, nv, tid);
-        ld.load((const E*)a.dO + ((c.base * a.T + c.first) * a.Hv + hv) * (int64_t)a.dv + v0, (int64_t)a.Hv * a.dv, c.rows, nv, tid);
-        lx.load((const E*)a.x + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
-        if (T::TWO) lx2.load((const E*)a.x2 + at * GDR_C * a.dv + v0, a.dv, c.rows, nv, tid);
+        lf = gdr_load(gdr_buffer(record + gdr_rec_bytes<E>(true) - GDR_VEC * 4, n.c.rows > 0 ? GDR_VEC * 4 : 0), tid * 16);
     };
     GdrChunk c, cn;
-    int64_t item = next((int64_t)blockIdx.x - gridDim.x, c), itemn;
-    load(item, c, 0, 0);
+    int item = next((int)blockIdx.x - (int)gridDim.x, c), itemn;
+    {
+        const Next n = which(item, c, 0, 0);
+        load1(n);
+        load2(n);
+        load3(n);
+    }
 
 #pragma unroll 1
     for (; item < items; item = itemn, c = cn) {
         itemn = next(item, cn);
         const int hk = item % a.Hk, slot = item / a.Hk;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) dq[t] = dk[t] = zero;
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) dq[y][t] = dk[y][t] = zero;
 #pragma unroll 1
     for (int hg = 0; hg < G; ++hg) {
         const int hv = hk * G + hg;
         const int64_t at = (int64_t)slot * a.Hv + hv;
-        const char* record = (const char*)a.rec + at * gdr_rec_bytes<E>(true);
-        const float* vec = (const float*)(record + gdr_rec_bytes<E>(true) - GDR_VEC * 4);
         floatx4 dP[2], dT[2];
         dP[0] = dP[1] = dT[0] = dT[1] = zero;
         float ss = 0.f, xs[RT], ys[RT];
@@ -404,35 +430,29 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         for (int t = 0; t < RT; ++t) xs[t] = ys[t] = 0.f;
 #pragma unroll 1
         for (int v0 = 0; v0 < a.dv; v0 += DV) {
-            const int nv = min(DV, a.dv - v0);
             GdrStage<E, DK, DV> st;
-            {
-                KD_LANE;
-                __syncthreads();      // the head (or the values) before is done
-                if (v0 == 0) {
-                    if (w == 0) {
-                        const int64_t gate = (c.base * a.T + c.first + min(lane, c.rows - 1)) * a.Hv + hv;
-                        const double b = gdr_cumsum(lane < c.rows ? gdr_gate(a.g, gate, a.gates32, (const E*)nullptr) : 0.f, lane);
-                        sm.bh[lane] = (float)b;
-                        sm.bl[lane] = (float)(b - (double)(float)b);
-                    }
-                    if (tid >= 64 && tid < 64 + 257) sm.vec[tid - 64] = vec[tid - 64];
-                    if (hg == 0) {
-                        lk.store(sm.k, tid);
-                        lq.store(sm.q, tid);
-                    }
+            __syncthreads();      // the head (or the values) before is done
+            if (v0 == 0) {
+                if (tid < GDR_VEC / 4) reinterpret_cast<floatx4*>(sm.vec)[tid] = lf;
+                if (hg == 0) {
+                    lk.store(sm.k, tid);
+                    lq.store(sm.q, tid);
                 }
-                ls.store(sm.s, tid);
-                ld.store(sm.d, tid);
-                lx.store(sm.x, tid);
-                if (T::TWO) lx2.store(sm.x2, tid);
-#pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
-                lv.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
             }
+            ls.store(sm.s, tid);
+            ld.store(sm.d, tid);
+            lx.store(sm.x, tid);
+            if (T::TWO) lx2.store(sm.x2, tid);
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+                if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
+            lv.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
             __syncthreads();
-            st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, nv, a.dk, tid);
+            st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, min(DV, a.dv - v0), a.dk, tid);
+            const bool same = v0 + DV < a.dv || hg + 1 < G;
+            const Next nx = which(same ? item : itemn, same ? c : cn, v0 + DV < a.dv ? hg : same ? hg + 1 : 0, v0 + DV < a.dv ? v0 + DV : 0);
+            // dbeta_r = X_r.U_r / beta_r; where a beta is 0 (or next to it), from W instead
+            const bool small = sm.vec[257] != 0.f;
             // W and U: 16 values a wave
             floatx4 W[4];
 #pragma unroll
@@ -450,20 +470,20 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 for (int t = 0; t < 4; ++t) {
                     const floatx4 be = *reinterpret_cast<const floatx4*>(sm.vec + 16 * t + 4 * g);
                     const floatx4 bb = *reinterpret_cast<const floatx4*>(sm.vec + 64 + 16 * t + 4 * g);
-                    const floatx4 b = *reinterpret_cast<const floatx4*>(sm.bh + 16 * t + 4 * g);
-                    floatx4 x = T::template ld_acc<DV>(sm.x, t, 16 * w, lane);
-                    if (T::TWO) x += T::template ld_acc<DV>(sm.x2, t, 16 * w, lane);
                     const floatx4 v = T::template ld_acc<DV>(sm.u, t, 16 * w, lane);
+                    if (small) {
+                        const floatx4 b = *reinterpret_cast<const floatx4*>(sm.vec + 320 + 16 * t + 4 * g);
+                        floatx4 x = T::template ld_acc<DV>(sm.x, t, 16 * w, lane);
+                        if (T::TWO) x += T::template ld_acc<DV>(sm.x2, t, 16 * w, lane);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        // X.W for dbeta takes W itself (beta may be 0), U takes beta W
-                        x[r] = row16_sum(x[r] * (v[r] - __builtin_amdgcn_exp2f(b[r]) * W[t][r]));
-                        W[t][r] = be[r] * v[r] - bb[r] * W[t][r];
+                        for (int r = 0; r < 4; ++r) x[r] = row16_sum(x[r] * (v[r] - __builtin_amdgcn_exp2f(b[r]) * W[t][r]));
+                        if (l16 == 0) {
+                            floatx4* to = reinterpret_cast<floatx4*>(sm.xw[w] + 16 * t + 4 * g);
+                            *to = v0 == 0 ? x : *to + x;
+                        }
                     }
-                    if (l16 == 0) {
-                        floatx4* to = reinterpret_cast<floatx4*>(sm.xw[w] + 16 * t + 4 * g);
-                        *to = v0 == 0 ? x : *to + x;
-                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) W[t][r] = be[r] * v[r] - bb[r] * W[t][r];
                 }
                 Frag f[2], f2[2];
 #pragma unroll
@@ -500,30 +520,44 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
             // scale e^b dO S0 and -beta e^b X S0, and their products with q and k
             {
                 KD_LANE;
-                floatx4 dqi[RT], dke[RT];
+                floatx4 dqi[2][RT], dke[2][RT];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) dqi[t] = dke[t] = zero;
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) dqi[y][t] = dke[y][t] = zero;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const Frag s = gdr_coln<DK>(sm.s, j, 16 * ct, lane);
+                    const Frag s[2] = {gdr_coln<DK>(sm.s, j, c0, lane), gdr_coln<DK>(sm.s, j, c0 + 16, lane)};
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        dqi[t] = T::mma(s, T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), dqi[t]);
-                        dke[t] = T::mma(s, T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g), dke[t]);
-                        if (T::TWO) dke[t] = T::mma(s, T::template ld_row<DV>(sm.x2, 16 * (r0 + t) + l16, j, g), dke[t]);
+                        const Frag d = T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), x = T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            dqi[y][t] = T::mma(s[y], d, dqi[y][t]);
+                            dke[y][t] = T::mma(s[y], x, dke[y][t]);
+                        }
+                        if (T::TWO) {
+                            const Frag x2 = T::template ld_row<DV>(sm.x2, 16 * (r0 + t) + l16, j, g);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) dke[y][t] = T::mma(s[y], x2, dke[y][t]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const int row = 16 * (r0 + t) + l16, to = TK::off(row, (16 * ct + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                    const int row = 16 * (r0 + t) + l16;
                     const float se = sm.vec[192 + row], bb = sm.vec[64 + row];
-                    const E4 q4 = *reinterpret_cast<const E4*>(sm.q + to), k4 = *reinterpret_cast<const E4*>(sm.k + to);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = se * dqi[t][e], y = -bb * dke[t][e];
-                        dq[t][e] += x;
-                        dk[t][e] += y;
-                        xs[t] = fmaf((float)q4[e], x, fmaf((float)k4[e], y, xs[t]));
+                    for (int y = 0; y < 2; ++y) {
+                        const int to = TK::off(row, (c0 + 16 * y + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                        const E4 q4 = *reinterpret_cast<const E4*>(sm.q + to), k4 = *reinterpret_cast<const E4*>(sm.k + to);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = se * dqi[y][t][e], z = -bb * dke[y][t][e];
+                            dq[y][t][e] += x;
+                            dk[y][t][e] += z;
+                            xs[t] = fmaf((float)q4[e], x, fmaf((float)k4[e], z, xs[t]));
+                        }
                     }
                 }
             }
@@ -552,39 +586,50 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 }
             }
             __syncthreads();
-            {
-                const bool same = v0 + DV < a.dv || hg + 1 < G;
-                load(same ? item : itemn, same ? c : cn, v0 + DV < a.dv ? hg : same ? hg + 1 : 0, v0 + DV < a.dv ? v0 + DV : 0);
-            }
+            load1(nx);
             // e^(bC - b) U dS
             {
                 KD_LANE;
-                floatx4 dks[RT];
+                floatx4 dks[2][RT];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) dks[t] = zero;
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) dks[y][t] = zero;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const Frag s = gdr_coln<DK>(sm.s, j, 16 * ct, lane);
+                    const Frag s[2] = {gdr_coln<DK>(sm.s, j, c0, lane), gdr_coln<DK>(sm.s, j, c0 + 16, lane)};
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        dks[t] = T::mma(s, T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g), dks[t]);
-                        if (T::TWO) dks[t] = T::mma(s, T::template ld_row<DV>(sm.u2, 16 * (r0 + t) + l16, j, g), dks[t]);
+                        const Frag u = T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) dks[y][t] = T::mma(s[y], u, dks[y][t]);
+                        if (T::TWO) {
+                            const Frag u2 = T::template ld_row<DV>(sm.u2, 16 * (r0 + t) + l16, j, g);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) dks[y][t] = T::mma(s[y], u2, dks[y][t]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const int row = 16 * (r0 + t) + l16, to = TK::off(row, (16 * ct + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                    const int row = 16 * (r0 + t) + l16;
                     const float ec = sm.vec[128 + row];
-                    const E4 k4 = *reinterpret_cast<const E4*>(sm.k + to);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = ec * dks[t][e];
-                        dk[t][e] += x;
-                        ys[t] = fmaf((float)k4[e], x, ys[t]);
+                    for (int y = 0; y < 2; ++y) {
+                        const E4 k4 = *reinterpret_cast<const E4*>(sm.k + TK::off(row, (c0 + 16 * y + 4 * g) / TK::EPC) + 4 * g % TK::EPC);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = ec * dks[y][t][e];
+                            dk[y][t][e] += x;
+                            ys[t] = fmaf((float)k4[e], x, ys[t]);
+                        }
                     }
                 }
             }
+            load2(nx);
+            if (v0 + DV < a.dv) load3(nx);
         }
+        const bool small = sm.vec[257] != 0.f;
         {
             KD_LANE;
             // E, F and their sums; lane: token r of block i, s = 16 j + 4 g + e
@@ -600,8 +645,9 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     qk = T::mma(s, T::template ld_row<DK>(sm.q, 16 * i + l16, p, g), qk);
                 }
                 const int r = 16 * i + l16;
-                const floatx4 sh = *reinterpret_cast<const floatx4*>(sm.bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(sm.bl + 16 * j + 4 * g);
-                const float rh = sm.bh[r], rl = sm.bl[r], br = sm.vec[r];
+                const float *bh = sm.vec + 320, *bl = sm.vec + 384;
+                const floatx4 sh = *reinterpret_cast<const floatx4*>(bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(bl + 16 * j + 4 * g);
+                const float rh = bh[r], rl = bl[r], br = sm.vec[r];
                 float row = 0.f, brow = 0.f;
                 floatx4 colsum;
                 E4 e4, f4;
@@ -616,6 +662,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     row += m;
                     brow = fmaf(y, kk[e], brow);
                     colsum[e] = m;
+                    if (s == r) sm.xu[r] = dT[o][e];
                     // F + F^T (the diagonal is 0)
                     if (s <= r) sm.f[TC::off(s, r / TC::EPC) + r % TC::EPC] = f4[e];
                 }
@@ -631,8 +678,10 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 }
                 row += __shfl_xor(row, 16);
                 row += __shfl_xor(row, 32);
-                brow += __shfl_xor(brow, 16);
-                brow += __shfl_xor(brow, 32);
+                if (small) {
+                    brow += __shfl_xor(brow, 16);
+                    brow += __shfl_xor(brow, 32);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) colsum[e] = row16_sum(colsum[e]);
                 if (g == 0) {
@@ -651,8 +700,8 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 y += __shfl_xor(y, 16);
                 y += __shfl_xor(y, 32);
                 if (g == 0) {
-                    sm.dot[ct][16 * (r0 + t) + l16] = x;
-                    sm.send[ct][16 * (r0 + t) + l16] = y;
+                    sm.dot[cg][16 * (r0 + t) + l16] = x;
+                    sm.send[cg][16 * (r0 + t) + l16] = y;
                 }
             }
         }
@@ -660,33 +709,54 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         {
             KD_LANE;
             // E K, E^T Q and (F + F^T) K
+            {
+                const bool same = hg + 1 < G;
+                load3(which(same ? item : itemn, same ? c : cn, same ? hg + 1 : 0, 0));
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const Frag k = gdr_coln<DK>(sm.k, j, 16 * ct, lane), q = gdr_coln<DK>(sm.q, j, 16 * ct, lane);
+                Frag k[2], q[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    k[y] = gdr_coln<DK>(sm.k, j, c0 + 16 * y, lane);
+                    q[y] = gdr_coln<DK>(sm.q, j, c0 + 16 * y, lane);
+                }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    dq[t] = T::mma(k, T::template ld_row<64>(sm.e, 16 * (r0 + t) + l16, j, g), dq[t]);
-                    dk[t] = T::mma(k, T::template ld_row<64>(sm.f, 16 * (r0 + t) + l16, j, g), dk[t]);
-                    dk[t] = T::mma(q, gdr_coln<64>(sm.e, j, 16 * (r0 + t), lane), dk[t]);
+                    const Frag e = T::template ld_row<64>(sm.e, 16 * (r0 + t) + l16, j, g), f = T::template ld_row<64>(sm.f, 16 * (r0 + t) + l16, j, g);
+                    const Frag ec = gdr_coln<64>(sm.e, j, 16 * (r0 + t), lane);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        dq[y][t] = T::mma(k[y], e, dq[y][t]);
+                        dk[y][t] = T::mma(k[y], f, dk[y][t]);
+                        dk[y][t] = T::mma(q[y], ec, dk[y][t]);
+                    }
                 }
             }
             if (w == 7) {
                 // lane: token
+                const int b = lane >> 4;
                 float db = 0.f, y = 0.f, dbeta = 0.f, send = 0.f;
-                for (int j = 0; j <= lane / 16; ++j) {
-                    db += sm.rows[j][lane];
-                    dbeta += sm.brow[j][lane];
-                }
-                for (int i = lane / 16; i < 4; ++i) db -= sm.cols[i][lane];
 #pragma unroll
-                for (int x = 0; x < CT; ++x) {
+                for (int x = 0; x < 4; ++x) {
+                    const float p = sm.rows[x][lane], m = sm.cols[x][lane];
+                    db += (x <= b ? p : 0.f) - (x >= b ? m : 0.f);
+                }
+#pragma unroll
+                for (int x = 0; x < CG; ++x) {
                     db += sm.dot[x][lane];
                     send += sm.send[x][lane];
                 }
 #pragma unroll
-                for (int x = 0; x < DV / 16; ++x) dbeta += sm.xw[x][lane];
-#pragma unroll
                 for (int x = 0; x < 8; ++x) y += sm.ss[x];
+                if (small) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) dbeta += x <= b ? sm.brow[x][lane] : 0.f;
+#pragma unroll
+                    for (int x = 0; x < DV / 16; ++x) dbeta += sm.xw[x][lane];
+                } else {
+                    dbeta = sm.xu[lane] / sm.vec[lane];
+                }
                 // from the chunk's end, with what e^bC multiplies
                 send = wave_sum(send);
 #pragma unroll
@@ -712,11 +782,15 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 #undef KD_LANE
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int row = 16 * (r0 + t) + l16, e0 = 16 * ct + 4 * g;
-        if (row >= c.rows || e0 >= a.dk) continue;
-        const int64_t to = ((c.base * a.T + c.first + row) * a.Hk + hk) * (int64_t)a.dk + e0;
-        *reinterpret_cast<E4*>((E*)a.dq + to) = E4{(E)dq[t][0], (E)dq[t][1], (E)dq[t][2], (E)dq[t][3]};
-        *reinterpret_cast<E4*>((E*)a.dk_ + to) = E4{(E)dk[t][0], (E)dk[t][1], (E)dk[t][2], (E)dk[t][3]};
+        const int row = 16 * (r0 + t) + l16;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int e0 = c0 + 16 * y + 4 * g;
+            if (row >= c.rows || e0 >= a.dk) continue;
+            const int64_t to = ((c.base * a.T + c.first + row) * a.Hk + hk) * (int64_t)a.dk + e0;
+            *reinterpret_cast<E4*>((E*)a.dq + to) = E4{(E)dq[y][t][0], (E)dq[y][t][1], (E)dq[y][t][2], (E)dq[y][t][3]};
+            *reinterpret_cast<E4*>((E*)a.dk_ + to) = E4{(E)dk[y][t][0], (E)dk[y][t][1], (E)dk[y][t][2], (E)dk[y][t][3]};
+        }
     }
     }
 }
@@ -729,7 +803,7 @@ static hipError_t gdr_bwd(const GdrArgs& a, hipStream_t st)
     kd_gdr_back_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slots == 0) return e;
-    const int64_t items = (int64_t)a.slots * a.Hk;
+    const int items = a.slots * a.Hk;
     kd_gdr_grad_kernel<E, DK, DV><<<(unsigned)(items < 256 ? items : 256), 512, 0, st>>>(a);
     return hipGetLastError();
 }

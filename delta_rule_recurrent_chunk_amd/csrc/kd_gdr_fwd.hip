@@ -56,7 +56,13 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
     vec[64 + lane] = beta * eb;
     vec[128 + lane] = __builtin_amdgcn_exp2f((float)(last - b));
     vec[192 + lane] = a.scale * eb;
-    if (lane == 0) vec[256] = __builtin_amdgcn_exp2f((float)last);
+    const bool small = __any(lane < c.rows && fabsf(beta) < 1e-20f);
+    if (lane == 0) {
+        vec[256] = __builtin_amdgcn_exp2f((float)last);
+        vec[257] = small ? 1.f : 0.f;
+    }
+    vec[320 + lane] = (float)b;
+    vec[384 + lane] = (float)(b - (double)(float)b);
     __syncthreads();
     E* rec = (E*)record + lane * 8;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
