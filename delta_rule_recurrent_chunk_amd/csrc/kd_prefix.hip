@@ -465,55 +465,67 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
     prefix_own<E, D>(a, sm.own[w % ITEMS].k, sm.own[w % ITEMS].v, K, b, h0, nh, k0, k1, part);
 }
 
-// Joins the parts: one wave a row.  A lane holds the maximum and sum of one
-// split, then D / 64 elements (32: half of the lanes) of the result.
-template <class E, int D>
+// Joins the parts: R rows a workgroup, 4 / R waves each with a share of the
+// splits.  A lane holds the maximum and sum of one split, then D / 64 elements
+// (32: half of the lanes) of the result.
+template <class E, int D, int R>
 __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
 {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, G = a.Hq / a.Hkv, S = a.sp + a.so;
-    const int64_t at = (int64_t)blockIdx.x * 4 + w;
-    if (at >= (int64_t)a.T * a.Hq) return;
-    const int t = at / a.Hq, h = at % a.Hq;
-    int b = t;
-    if (a.cu) {
-        b = paged_owner(a.cu, a.B, t, lane);
-        if (b >= a.B || a.cu[b] > t) return;      // no sequence holds the row
-    }
-    const bool dead = a.lens[b] < 0;
-    const int64_t rows = (int64_t)a.T * G, row = (int64_t)(h / G) * rows + (int64_t)t * G + h % G;
-    float2 x = make_float2(-INFINITY, 0.f);
-    if (lane < S && !dead) x = *reinterpret_cast<const float2*>(a.ml + 2 * (lane * (int64_t)a.Hkv * rows + row));
-    float M = x.x;
-#pragma unroll
-    for (int y = 32; y > 0; y /= 2) M = fmaxf(M, __shfl_xor(M, y));
-    const bool none = M == -INFINITY;
-    const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - M);
-    float L = f * x.y;
-#pragma unroll
-    for (int y = 32; y > 0; y /= 2) L += __shfl_xor(L, y);
-    constexpr int N = D >= 128 ? 2 : 1;
+    constexpr int N = D >= 128 ? 2 : 1, SHARE = 4 / R;
     typedef float F __attribute__((ext_vector_type(N)));
+    __shared__ F part[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, G = a.Hq / a.Hkv, S = a.sp + a.so;
+    const int64_t at = (int64_t)blockIdx.x * R + w / SHARE;
+    const int t = at / a.Hq, h = at % a.Hq;
+    bool held = at < (int64_t)a.T * a.Hq;
+    int b = t;
+    if (held && a.cu) {
+        b = paged_owner(a.cu, a.B, t, lane);
+        held = b < a.B && a.cu[min(b, a.B)] <= t;      // (otherwise no sequence holds the row)
+    }
     F sum;
 #pragma unroll
     for (int e = 0; e < N; ++e) sum[e] = 0.f;
-    const bool mine = lane * N < D;
-    const float* p = a.part + row * D + (mine ? lane * N : 0);
-    const int64_t step = (int64_t)a.Hkv * rows * D;
+    float M = -INFINITY, L = 0.f;
+    if (held) {
+        const int64_t rows = (int64_t)a.T * G, row = (int64_t)(h / G) * rows + (int64_t)t * G + h % G;
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (lane < S && a.lens[b] >= 0) x = *reinterpret_cast<const float2*>(a.ml + 2 * (lane * (int64_t)a.Hkv * rows + row));
+        M = x.x;
+#pragma unroll
+        for (int y = 32; y > 0; y /= 2) M = fmaxf(M, __shfl_xor(M, y));
+        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - M);
+        L = f * x.y;
+#pragma unroll
+        for (int y = 32; y > 0; y /= 2) L += __shfl_xor(L, y);
+        const float* p = a.part + row * D + (lane * N < D ? lane * N : 0);
+        const int64_t step = (int64_t)a.Hkv * rows * D;
 #pragma unroll 1
-    for (int s0 = 0; s0 < S; s0 += 8) {
-        F v[8];
+        for (int s0 = w % SHARE; s0 < S; s0 += 8 * SHARE) {
+            F v[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const F*>(p + min(s0 + s, S - 1) * step);
+            for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const F*>(p + min(s0 + s * SHARE, S - 1) * step);
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const float fs = s0 + s < S ? __shfl(f, s0 + s) : 0.f;
-            if (fs == 0.f) continue;      // (nothing was written where a split has no keys)
+            for (int s = 0; s < 8; ++s) {
+                const int i = s0 + s * SHARE;
+                const float fs = i < S ? __shfl(f, i & 63) : 0.f;
+                if (fs == 0.f) continue;      // (nothing was written where a split has no keys)
 #pragma unroll
-            for (int e = 0; e < N; ++e) sum[e] = fmaf(fs, v[s][e], sum[e]);
+                for (int e = 0; e < N; ++e) sum[e] = fmaf(fs, v[s][e], sum[e]);
+            }
         }
     }
+    if (SHARE > 1) {
+        part[w][lane] = sum;
+        __syncthreads();
+        if (w % SHARE != 0) return;
+#pragma unroll
+        for (int y = 1; y < SHARE; ++y) sum += part[w + y][lane];
+    }
+    if (!held) return;
+    const bool none = M == -INFINITY;
     const float inv = none ? 0.f : 1.f / L;
-    if (mine) {
+    if (lane * N < D) {
         E* o = (E*)a.o + at * D + lane * N;
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] = none ? (E)0.f : (E)(sum[e] * inv);
@@ -521,16 +533,17 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
     if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + t] = none ? -INFINITY : 0.6931471805599453f * (M + __log2f(L));
 }
 
-// Splits.  Two workgroups of 128 rows fit a compute unit (512 at once); the
-// prefix is cut so that rounds of 512 workgroups, each with its tiles and about
-// three tiles' worth of writing parts out, come out shortest.
+// Splits.  Two workgroups of 128 rows fit a compute unit, where a tile takes
+// each of them 1.6 times as long as one alone; writing a part out and joining
+// it takes as long as 8 tiles.
 static int prefix_splits(int64_t items, int P)
 {
     const int tiles = (P + 63) / 64;
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= PREFIX_MOST && s <= (tiles + 3) / 4; ++s) {
-        const double cost = (double)((items * s + 511) / 512) * ((tiles + s - 1) / s + 3);
+        const int64_t n = items * s;
+        const double cost = (n <= 256 ? 1.0 : 1.6 * (double)((n + 511) / 512)) * ((tiles + s - 1) / s + 8);
         if (cost < least) least = cost, best = s;
     }
     return P == 0 ? 0 : best;
@@ -570,7 +583,7 @@ bool prefix_fits(PrefixArgs a, bool packed)
     const int64_t G = a.Hq / a.Hkv;
     if ((int64_t)a.T * G > (1 << 30) || a.T * G / PREFIX_ROWS + a.B > (1 << 30)) return false;
     prefix_plan(a, packed);
-    return grid_fits(prefix_grid(a, packed, 2), 256) && grid_fits(((int64_t)a.T * a.Hq + 3) / 4, 256);
+    return grid_fits(prefix_grid(a, packed, 2), 256) && grid_fits((int64_t)a.T * a.Hq, 256);
 }
 
 template <class E, int D>
@@ -582,7 +595,10 @@ static hipError_t prefix(PrefixArgs a, hipStream_t st)
     kd_prefix_kernel<E, D><<<(unsigned)prefix_grid(a, a.cu != nullptr, PrefixLds<E, D>::ITEMS), 256, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    kd_prefix_join_kernel<E, D><<<(unsigned)(((int64_t)a.T * a.Hq + 3) / 4), 256, 0, st>>>(a);
+    // (a row's parts one after the other where rows are many, at once where they are few)
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    if (a.sp + a.so <= 8 || rows > 8192) kd_prefix_join_kernel<E, D, 4><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    else kd_prefix_join_kernel<E, D, 1><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import layers as _la
 from .layers import _call, _check, _code, _fits, _flat, _need_cuda, _ptr, _ready, _rows, _same_device, _workspace
@@ -29,6 +30,9 @@ class KdGdrDesc(ctypes.Structure):
                 ("gates32", _i32), ("scale", _f32), ("q_stride", _s3), ("k_stride", _s3), ("v_stride", _s3)]
 
 
+_DESC = struct.Struct("@8if9q").pack      # the same as bytes (a step's calls are short)
+
+
 def declare(L):
     """Argument types of this part of the library."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -40,7 +44,7 @@ def declare(L):
     L.kron_delta_gdr_bwd.restype = i32
     L.kron_delta_gdr_bwd.argtypes = [P(KdGdrDesc)] + [vp] * 15 + [vp, sz, vp]
     L.kron_delta_gdr_step.restype = i32
-    L.kron_delta_gdr_step.argtypes = [P(KdGdrDesc)] + [vp] * 8 + [vp]
+    L.kron_delta_gdr_step.argtypes = [vp] * 10
 
 
 def _gdr(q, k, v, g, beta, scale, cu):
@@ -77,6 +81,15 @@ def _gdr(q, k, v, g, beta, scale, cu):
     desc = KdGdrDesc(B, T, Hk, Hv, dk, dv, _code(q.dtype), int(g.dtype == torch.float32 and q.dtype != torch.float32),
                      1.0 / math.sqrt(dk) if scale is None else scale, *strides)
     return dev, desc, q, k, v, g, beta, cu
+
+
+def _heads(t):
+    """[n, H, d] as the kernels read it: contiguous last dimension, strides and
+    address in whole 16-byte pieces (a copy where it is not so)."""
+    s0, s1, s2 = t.stride()
+    if s2 == 1 and not ((s0 | s1) * t.element_size() | t.data_ptr()) & 15:
+        return t
+    return t.clone() if t.is_contiguous() else t.contiguous()
 
 
 def _slots(desc, cu):
@@ -144,13 +157,25 @@ def gdr_step(q, k, v, g, beta, S, *, scale=None, S_out=None):
     torch, L = _ready()
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or g.dim() != 2 or beta.dim() != 2:
         raise ValueError("q, k must be [B, Hk, dk], v [B, Hv, dv], g, beta [B, Hv]")
-    dev, desc, q, k, v, g, beta, _ = _gdr(q[:, None], k[:, None], v[:, None], g[:, None], beta[:, None], scale, None)
+    dev, dt, (B, Hk, dk), (_, Hv, dv), gt = _need_cuda(q, "q"), q.dtype, q.shape, v.shape, g.dtype
+    if gt != dt and gt != torch.float32:
+        raise TypeError("g and beta must both be %s or float32, got %s" % (dt, gt))
     out = S if S_out is None else S_out
-    for name, t in (("S", S), ("S_out", out)):
-        _check(name, t, (desc.B, desc.Hv, desc.dv, desc.dk), torch.float32)
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError("%s must be contiguous and on %s" % (name, dev))
-    o = torch.empty((desc.B, desc.Hv, desc.dv), dtype=q.dtype, device=dev)
-    _call("kron_delta_gdr_step", dev, L.kron_delta_gdr_step, ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    state, f32 = (B, Hv, dv, dk), torch.float32
+    for name, t, shape, ty in (("k", k, (B, Hk, dk), dt), ("v", v, (B, Hv, dv), dt), ("g", g, (B, Hv), gt),
+                               ("beta", beta, (B, Hv), gt), ("S", S, state, f32), ("S_out", out, state, f32)):
+        if t.shape != shape or t.dtype != ty or t.device != dev:
+            _check(name, t, shape, ty)
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+    if not S.is_contiguous() or not out.is_contiguous():
+        raise ValueError("S and S_out must be contiguous")
+    _fits("the state", state)
+    q, k, v = _heads(q), _heads(k), _heads(v)
+    g, beta = _flat(g), _flat(beta)
+    (q0, q1, _), (k0, k1, _), (v0, v1, _) = q.stride(), k.stride(), v.stride()
+    desc = _DESC(B, 1, Hk, Hv, dk, dv, _code(dt), gt != dt, 1.0 / math.sqrt(dk) if scale is None else scale, q0, 0, q1, k0,
+                 0, k1, v0, 0, v1)
+    o = torch.empty((B, Hv, dv), dtype=dt, device=dev)
+    _call("kron_delta_gdr_step", dev, L.kron_delta_gdr_step, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           g.data_ptr(), beta.data_ptr(), S.data_ptr(), o.data_ptr(), out.data_ptr())
     return o

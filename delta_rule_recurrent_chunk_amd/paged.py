@@ -9,9 +9,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import layers as _la
-from .layers import _call, _check, _code, _fits, _freqs, _int32, _layout, _need_cuda, _ptr, _ready, _same_device, _workspace
+from .gdr import _heads
+from .layers import _call, _check, _code, _fits, _freqs, _int32, _layout, _need_cuda, _ready
 
 EXPORTED = ("kron_delta_paged_append", "kron_delta_prefix_attn_workspace_bytes", "kron_delta_prefix_attn")
 
@@ -26,59 +28,64 @@ class KdPagedDesc(ctypes.Structure):
                 ("v_stride", _s3), ("table_stride", _i64)]
 
 
+# the descriptor and the rows' strides as bytes: a step's calls are short, and
+# ctypes takes a third of their host time to build the same structure
+_DESC = struct.Struct("@11ifqiif7q").pack
+_S2, _S6 = struct.Struct("@2q").pack, struct.Struct("@6q").pack
+
+
 def declare(L):
     """Argument types of this part of the library."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    P = ctypes.POINTER
     L.kron_delta_paged_append.restype = i32
-    L.kron_delta_paged_append.argtypes = [P(KdPagedDesc)] + [vp] * 3 + [P(_i64)] + [vp] * 7 + [vp]
+    L.kron_delta_paged_append.argtypes = [vp] * 13
     L.kron_delta_prefix_attn_workspace_bytes.restype = sz
-    L.kron_delta_prefix_attn_workspace_bytes.argtypes = [P(KdPagedDesc), i32]
+    L.kron_delta_prefix_attn_workspace_bytes.argtypes = [vp, i32]
     L.kron_delta_prefix_attn.restype = i32
-    L.kron_delta_prefix_attn.argtypes = [P(KdPagedDesc), vp, P(_i64)] + [vp] * 8 + [vp, sz, vp]
-
-
-def _packed_rows(t):
-    """[T, H, d] as the kernels read it: contiguous last dimension, strides and
-    address in whole 16-byte pieces (a copy where it is not so)."""
-    (n, h, d), (s0, s1, s2), es = t.shape, t.stride(), t.element_size()
-    if t.data_ptr() % 16 == 0 and (d == 1 or s2 == 1) and (n <= 1 or s0 * es % 16 == 0) and (h <= 1 or s1 * es % 16 == 0):
-        return t
-    return t.clone() if t.is_contiguous() else t.contiguous()
+    L.kron_delta_prefix_attn.argtypes = [vp] * 12 + [sz, vp]
 
 
 def _batch(dev, k_pages, v_pages, page_table, lens, cu_seqlens, T):
-    """Checks of the cache, the table and the batch; B and cu_seqlens."""
+    """Checks of the cache, the table and the batch.  Returns B, lens, cu_seqlens."""
     torch = _la._torch
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    shape, i32 = k_pages.shape, torch.int32
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages must be [pages, page, Hkv, d] of one dtype")
-    _fits("k_pages", k_pages.shape)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("%s must have a contiguous last dimension" % name)
-    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+    if page_table.dim() != 2 or page_table.dtype != i32:
         raise ValueError("page_table must be int32 [B, width]")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+    B, width = page_table.shape
+    _fits("the cache or its table", (*shape, B, width, T))
+    if shape[3] > 1 and (k_pages.stride(3) != 1 or v_pages.stride(3) != 1):
+        raise ValueError("k_pages and v_pages must have a contiguous last dimension")
+    if width > 1 and page_table.stride(1) != 1:
         raise ValueError("page_table must have contiguous rows")
-    _fits("page_table", page_table.shape)
-    B = page_table.shape[0]
-    _check("lens", lens, (B,), torch.int32)
-    if B > 1 and lens.stride(0) != 1:
-        lens = lens.contiguous()
     if cu_seqlens is not None:
-        _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
+        _check("cu_seqlens", cu_seqlens, (B + 1,), i32)
         cu_seqlens = cu_seqlens.contiguous()
+        if cu_seqlens.device != dev:
+            raise ValueError("cu_seqlens is on %s, not on %s" % (cu_seqlens.device, dev))
     elif T != B:
         raise ValueError("without cu_seqlens every sequence has one row: %d rows for %d sequences" % (T, B))
-    _same_device(dev, k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens, cu_seqlens=cu_seqlens)
-    return B, lens, cu_seqlens
+    if lens.shape != (B,) or lens.dtype != i32:
+        _check("lens", lens, (B,), i32)
+    if k_pages.device != dev or v_pages.device != dev or page_table.device != dev or lens.device != dev:
+        raise ValueError("the cache, its table and lens must be on %s" % dev)
+    return B, lens if lens.is_contiguous() else lens.contiguous(), cu_seqlens
 
 
-def _desc(k_pages, v_pages, page_table, B, T, Hq, **fields):
+def _row_check(name, t, shape, dt, dev):
+    if t.shape != shape or t.dtype != dt or t.device != dev:
+        _check(name, t, shape, dt)
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+
+
+def _desc(k_pages, v_pages, page_table, B, T, Hq, rot=0, layout=0, rope_scale=1.0, offset=0, prefix=0, prefix_width=0,
+          scale=1.0):
     pages, page, Hkv, d = k_pages.shape
-    return KdPagedDesc(B=B, T=T, Hq=Hq, Hkv=Hkv, d=d, dtype=_code(k_pages.dtype), page=page, pages=pages,
-                       width=page_table.shape[1], k_stride=k_pages.stride()[:3], v_stride=v_pages.stride()[:3],
-                       table_stride=page_table.stride(0) if B > 1 else 0, **fields)
+    a, b, c, _ = k_pages.stride()
+    e, f, g, _ = v_pages.stride()
+    return _DESC(B, T, Hq, Hkv, d, _code(k_pages.dtype), page, pages, page_table.shape[1], rot, layout, rope_scale, offset,
+                 prefix, prefix_width, scale, a, b, c, e, f, g, page_table.stride(0) if B > 1 else 0)
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, lens, *, q=None, cu_seqlens=None, freqs=None, layout="half",
@@ -95,29 +102,29 @@ def paged_append(k, v, k_pages, v_pages, page_table, lens, *, q=None, cu_seqlens
         raise ValueError("k and v must be [T, Hkv, d], q [T, Hq, d]")
     T = k.shape[0]
     B, lens, cu_seqlens = _batch(dev, k_pages, v_pages, page_table, lens, cu_seqlens, T)
-    Hkv, d = k_pages.shape[2:]
-    _fits("k", k.shape)
-    _check("k", k, (T, Hkv, d), k_pages.dtype)
-    _check("v", v, (T, Hkv, d), k_pages.dtype)
-    Hq = 0
-    if q is not None:
+    (_, _, Hkv, d), dt = k_pages.shape, k_pages.dtype
+    _row_check("k", k, (T, Hkv, d), dt, dev)
+    _row_check("v", v, (T, Hkv, d), dt, dev)
+    k, v = _heads(k), _heads(v)
+    if q is None:
+        Hq, out, qp, op, q0, q1 = 0, None, None, None, 0, 0
+    else:
         Hq = q.shape[1]
-        _fits("q", q.shape)
-        _check("q", q, (T, Hq, d), k_pages.dtype)
-        q = _packed_rows(q)
-    _same_device(dev, v=v, q=q)
-    k, v = _packed_rows(k), _packed_rows(v)
-    rot = 0
+        _fits("q", (T, Hq))
+        _row_check("q", q, (T, Hq, d), dt, dev)
+        q = _heads(q)
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        (q0, q1, _), qp, op = q.stride(), q.data_ptr(), out.data_ptr()
+    rot = fp = 0
     if freqs is not None:
         freqs = _freqs(freqs, dev)
-        rot = _int32(2 * freqs.numel())
-    desc = _desc(k_pages, v_pages, page_table, B, T, Hq, rot=rot, layout=_layout(layout), rope_scale=rope_scale,
-                 offset=min(max(int(offset), -(1 << 62)), 1 << 62))
-    out = None if q is None else torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
-    strides = _s6(*((0, 0) if q is None else q.stride()[:2]), *k.stride()[:2], *v.stride()[:2])
-    _call("kron_delta_paged_append", dev, L.kron_delta_paged_append, ctypes.byref(desc), _ptr(q), k.data_ptr(),
-          v.data_ptr(), strides, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
-          _ptr(cu_seqlens), _ptr(freqs), _ptr(out))
+        rot, fp = _int32(2 * freqs.numel()), freqs.data_ptr()
+    desc = _desc(k_pages, v_pages, page_table, B, T, Hq, rot, _layout(layout), rope_scale,
+                 min(max(int(offset), -(1 << 62)), 1 << 62))
+    (k0, k1, _), (v0, v1, _) = k.stride(), v.stride()
+    _call("kron_delta_paged_append", dev, L.kron_delta_paged_append, desc, qp, k.data_ptr(), v.data_ptr(),
+          _S6(q0, q1, k0, k1, v0, v1), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
+          None if cu_seqlens is None else cu_seqlens.data_ptr(), fp, op)
     return out
 
 
@@ -128,9 +135,10 @@ def prefix_attn_workspace(q, k_pages, prefix_len, page_table):
     need = 0
     for packed in (0, 1):
         if packed or q.shape[0] == page_table.shape[0]:
+            _fits("the batch", q.shape + k_pages.shape + page_table.shape)
             desc = _desc(k_pages, k_pages, page_table, page_table.shape[0], q.shape[0], q.shape[1], scale=1.0,
                          prefix=_int32(prefix_len), prefix_width=1 << 30)
-            need = max(need, int(L.kron_delta_prefix_attn_workspace_bytes(ctypes.byref(desc), packed)))
+            need = max(need, int(L.kron_delta_prefix_attn_workspace_bytes(desc, packed)))
     return torch.empty(max(need, 16), dtype=torch.uint8, device=k_pages.device)
 
 
@@ -149,20 +157,25 @@ def prefix_attn(q, k_pages, v_pages, prefix_table, prefix_len, page_table, lens,
         raise ValueError("q must be [T, Hq, d]")
     T, Hq, d = q.shape
     B, lens, cu_seqlens = _batch(dev, k_pages, v_pages, page_table, lens, cu_seqlens, T)
-    _fits("q", q.shape)
-    _check("q", q, (T, Hq, k_pages.shape[3]), k_pages.dtype)
-    if prefix_table.dim() != 1 or prefix_table.dtype != torch.int32:
-        raise ValueError("prefix_table must be an int32 vector")
-    _fits("prefix_table", prefix_table.shape)
-    _same_device(dev, prefix_table=prefix_table)
-    prefix_table, q = prefix_table.contiguous(), _packed_rows(q)
-    desc = _desc(k_pages, v_pages, page_table, B, T, Hq, scale=1.0 / math.sqrt(d) if scale is None else scale,
-                 prefix=_int32(prefix_len), prefix_width=prefix_table.numel())
-    need = int(L.kron_delta_prefix_attn_workspace_bytes(ctypes.byref(desc), int(cu_seqlens is not None)))
-    ws, wsb = _workspace(workspace, need, dev)
+    _fits("q", (T, Hq))
+    _row_check("q", q, (T, Hq, k_pages.shape[3]), k_pages.dtype, dev)
+    if prefix_table.dim() != 1 or prefix_table.dtype != torch.int32 or prefix_table.device != dev:
+        raise ValueError("prefix_table must be an int32 vector on %s" % dev)
+    width = prefix_table.numel()
+    _fits("prefix_table", (width, 0))
+    prefix_table, q = prefix_table.contiguous(), _heads(q)
+    desc = _desc(k_pages, v_pages, page_table, B, T, Hq, 0, 0, 1.0, 0, _int32(prefix_len), width,
+                 1.0 / math.sqrt(d) if scale is None else scale)
+    if workspace is None:
+        need = int(L.kron_delta_prefix_attn_workspace_bytes(desc, int(cu_seqlens is not None)))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous and on %s" % dev)
     o = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=dev) if return_lse else None
-    _call("kron_delta_prefix_attn", dev, L.kron_delta_prefix_attn, ctypes.byref(desc), q.data_ptr(), _s2(*q.stride()[:2]),
-          k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
-          _ptr(cu_seqlens), o.data_ptr(), _ptr(lse), _ptr(ws), wsb)
+    q0, q1, _ = q.stride()
+    _call("kron_delta_prefix_attn", dev, L.kron_delta_prefix_attn, desc, q.data_ptr(), _S2(q0, q1), k_pages.data_ptr(),
+          v_pages.data_ptr(), prefix_table.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
+          None if cu_seqlens is None else cu_seqlens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return (o, lse) if return_lse else o

@@ -82,6 +82,12 @@ def test_forward_and_backward_checks(L):
                dbeta=None, dS0=None, ws=None, wsb=0) == OK
 
 
+def test_descriptors_as_bytes_are_the_structure():
+    d = desc()
+    assert bytes(d) == gdr._DESC(*(x for n, _ in d._fields_ for x in (
+        lambda v: v if hasattr(v, "__len__") else (v,))(getattr(d, n))))
+
+
 def test_step_checks(L):
     def step(d, **o):
         p = dict(q=P(0), k=P(1), v=P(2), g=P(3), beta=P(4), Si=P(5), o=P(6), So=P(5))

@@ -35,9 +35,15 @@ BAD = [dict(B=0), dict(T=-1), dict(Hkv=0), dict(d=4), dict(page=0), dict(pages=0
        dict(k_stride=(2048, 128, -64)), dict(v_stride=(2048, 100, 64)), dict(T=4), dict(Hq=1 << 20), dict(B=(1 << 24) + 1)]
 
 
+def test_descriptors_as_bytes_are_the_structure():
+    d = desc(offset=-5, k_stride=(7, 6, 5), v_stride=(4, 3, 2))
+    assert bytes(d) == pg._DESC(*(x for n, _ in d._fields_ for x in (
+        lambda v: v if hasattr(v, "__len__") else (v,))(getattr(d, n)))).ljust(ctypes.sizeof(d), b"\0")
+
+
 def test_append_checks(L):
     def call(d, stride=(256, 64, 128, 64, 128, 64), **o):
-        p = dict(q=P(0), k=P(1), v=P(2), stride=pg._s6(*stride), kp=P(3), vp=P(4), table=P(5), lens=P(6), cu=None,
+        p = dict(q=P(0), k=P(1), v=P(2), stride=pg._S6(*stride), kp=P(3), vp=P(4), table=P(5), lens=P(6), cu=None,
                  freqs=P(8), out=P(9))
         p.update(o)
         return L.kron_delta_paged_append(ctypes.byref(d) if d else None, *p.values(), None)
@@ -66,7 +72,7 @@ def test_append_checks(L):
 
 def test_prefix_checks(L):
     def call(d, wsb=1 << 40, stride=(256, 64), **o):
-        p = dict(q=P(0), stride=pg._s2(*stride), kp=P(1), vp=P(2), pt=P(3), table=P(4), lens=P(5), cu=None, o=P(6),
+        p = dict(q=P(0), stride=pg._S2(*stride), kp=P(1), vp=P(2), pt=P(3), table=P(4), lens=P(5), cu=None, o=P(6),
                  lse=P(7), ws=P(8))
         p.update(o)
         return L.kron_delta_prefix_attn(ctypes.byref(d) if d else None, *p.values(), wsb, None)

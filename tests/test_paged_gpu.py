@@ -1,5 +1,4 @@
 """The paged cache and the attention over a shared prefix against plain references in 64 bits."""
-import ctypes
 import math
 
 import numpy as np
@@ -215,7 +214,7 @@ def test_rows_behind_the_last_sequence_are_left():
     cu, pt, tb, ln = c.dev(c.cu), c.dev(c.ptable), c.dev(c.table), c.dev(c.lens)
     desc = paged._desc(c.kp, c.vp, tb, c.B, c.T, 4, scale=0.125, prefix=c.P, prefix_width=len(c.ptable))
     st = kd.lib().kron_delta_prefix_attn(
-        ctypes.byref(desc), c.q.data_ptr(), paged._s2(*c.q.stride()[:2]), c.kp.data_ptr(), c.vp.data_ptr(),
+        desc, c.q.data_ptr(), paged._S2(*c.q.stride()[:2]), c.kp.data_ptr(), c.vp.data_ptr(),
         pt.data_ptr(), tb.data_ptr(), ln.data_ptr(), cu.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
         ws.numel(), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
