@@ -98,41 +98,42 @@ __device__ __forceinline__ bool prefix_finite(const floatx16* o, int nd) {
     return sum == 0.f;
 }
 
+// Tiles of BN keys, NBUF of them in LDS (all but the one in use on their way).
+constexpr int PREFIX_IDS = 512;      // keys whose page ids are in LDS at once (one of two such windows)
 template <class E, int D>
 struct PrefixLds {
-    static constexpr int BN = sizeof(E) == 2 ? 64 : 32;      // keys of a shared tile
+    static constexpr int KEYS = sizeof(E) == 2 ? 128 : 64;
     static constexpr int ITEMS = sizeof(E) * D > 256 ? 2 : 4; // waves with own tiles (32 keys)
     union {
         struct {
-            E k[2][BN * D], v[2][BN * D];
+            E k[KEYS * D], v[KEYS * D];
         } tile;
         struct {
             E k[32 * D], v[32 * D];
         } own[ITEMS];
     };
+    int ids[2][PREFIX_IDS + 1];
 };
 
 // 128 rows from r0 on (of nrows; row r is head r % G of row q0 + r / G) against
 // keys k0 .. k1 - 1.  CAUSAL: row r sees keys up to past + r / G.
-template <class E, int D, bool CAUSAL>
+template <class E, int D, bool CAUSAL, int BN>
 __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>& sm, const PrefixKeys<E>& K, int hk, int q0,
                                             int nrows, int r0, int64_t past, int k0, int k1, int64_t part)
 {
     typedef SwaT<E> T;
     typedef typename T::Frag Frag;
     typedef SwaTile<E, D> TL;
-    constexpr int BN = PrefixLds<E, D>::BN, NK = D / T::KC, NS = BN / 32, ND = D / 32, NP = 16 / T::PR;
-    constexpr int STEP = 256 / TL::CPR, NL = BN / STEP;      // rows per round of the workgroup, rounds
-    static_assert(BN % STEP == 0, "whole instructions");
+    constexpr int NBUF = PrefixLds<E, D>::KEYS / BN, NK = D / T::KC, NS = BN / 32, ND = D / 32, NP = 16 / T::PR;
+    constexpr int STEP = 256 / TL::CPR < BN ? 256 / TL::CPR : BN, NL = BN / STEP;      // rows per round of the workgroup, rounds
+    constexpr int BUSY = STEP * TL::CPR;                                               // threads that load
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5;
     const int G = a.Hq / a.Hkv, row = r0 + 32 * w + (lane & 31), rr = min(row, nrows - 1);
     const E* qrow = (const E*)a.q + (int64_t)(q0 + rr / G) * a.qs[0] + (hk * G + rr % G) * a.qs[1];
     Frag q[NK];
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) q[ks] = swa_ld_mem<E>(qrow, ks, g);
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
-    // the last key that the lane's row sees, and that the wave's first does
+    // the last key that the lane's row sees, and that the wave's first and last do
     const int lim = CAUSAL ? (int)min((int64_t)k1 - 1, past + rr / G) : k1 - 1;
     const int lim0 = CAUSAL ? (int)min((int64_t)k1 - 1, past + min(r0 + 32 * w, nrows - 1) / G) : k1 - 1;
     const int lim1 = CAUSAL ? (int)min((int64_t)k1 - 1, past + min(r0 + 32 * w + 31, nrows - 1) / G) : k1 - 1;
@@ -145,22 +146,31 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
     float m = -INFINITY, l = 0.f;
     const int nt = (k1 - k0 + BN - 1) / BN;
 
-    // each lane's NL rows of a tile: page number and slot go on by BN keys from
-    // tile to tile; page ids are loaded one tile ahead of the keys
-    const int fr = tid / TL::CPR, fc = tid % TL::CPR, bq = BN / K.page, br = BN % K.page;
-    int pn[NL], sl[NL], id[NL];
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const int key = min(k0 + fr + i * STEP, k1 - 1);
-        pn[i] = key / K.page;
-        sl[i] = key - pn[i] * K.page;
-    }
-    auto ids = [&]() {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) id[i] = K.id(pn[i]);
+    // Page ids pass through LDS, a window of PREFIX_IDS keys at a time: loads of
+    // ids between the keys' would make every use of one wait for all keys before it.
+    auto window = [&](int x) {
+        const int first = (k0 + x * PREFIX_IDS) / K.page, last = min(k0 + (x + 1) * PREFIX_IDS, k1) - 1;
+        const int n = last / K.page - first + 1;
+        for (int i = tid; i < n; i += 256) sm.ids[x & 1][i] = K.id(first + i);
+        __syncthreads();
     };
-    auto advance = [&](int t) {      // to tile t
-        if (k0 + (t + 1) * BN <= k1) {
+    // each lane's NL rows of a tile: page number (within the window) and slot go on
+    // by BN keys from tile to tile
+    const int fr = tid / TL::CPR, fc = tid % TL::CPR, bq = BN / K.page, br = BN % K.page;
+    int pn[NL], sl[NL];
+    auto fetch = [&](int t, E* kt, E* vt) {
+        constexpr int PER = PREFIX_IDS / BN;
+        const int x = t / PER;
+        if (t % PER == 0) window(x);
+        if (t % PER == 0 || k0 + (t + 1) * BN > k1) {
+            const int base = (k0 + x * PREFIX_IDS) / K.page;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int key = min(k0 + t * BN + fr + i * STEP, k1 - 1), p = key / K.page;
+                pn[i] = p - base;
+                sl[i] = key - p * K.page;
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
                 pn[i] += bq;
@@ -170,35 +180,25 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
                     ++pn[i];
                 }
             }
-        } else {
+        }
+        const uint32_t kd = lds_address(kt) + 1024 * w, vd = lds_address(vt) + 1024 * w;
+        if (BUSY == 256 || tid < BUSY) {
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                const int key = min(k0 + t * BN + fr + i * STEP, k1 - 1);
-                pn[i] = key / K.page;
-                sl[i] = key - pn[i] * K.page;
+                const int64_t id = sm.ids[x & 1][pn[i]];
+                const int ch = (fc ^ TL::swz(fr + i * STEP)) * TL::EPC;
+                load_lds16(kd + i * BUSY * 16, K.k + id * K.kp + sl[i] * K.ks + ch);
+                load_lds16(vd + i * BUSY * 16, K.v + id * K.vp + sl[i] * K.vs + ch);
             }
         }
     };
-    auto fetch = [&](E* kt, E* vt) {
-        const uint32_t kd = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)kt + 1024 * w;
-        const uint32_t vd = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)vt + 1024 * w;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int ch = (fc ^ TL::swz(fr + i * STEP)) * TL::EPC;
-            load_lds16(kd + i * 4096, K.k + id[i] * K.kp + sl[i] * K.ks + ch);
-            load_lds16(vd + i * 4096, K.v + id[i] * K.vp + sl[i] * K.vs + ch);
-        }
-    };
-    auto tile = [&](int i, const E* kl, const E* vl, E* kn, E* vn) {
+    auto tile = [&](int i, int buf) {
         // tile i is here; the buffer of tile i - 1 is free
-        swa_landed();
-        if (i + 1 < nt) {
-            fetch(kn, vn);
-            if (i + 2 < nt) {
-                advance(i + 2);
-                ids();
-            }
-        }
+        if (i + NBUF - 2 < nt) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * NL * (NBUF - 2)) : "memory");
+        else swa_landed();
+        if (i + NBUF - 1 < nt) fetch(i + NBUF - 1, sm.tile.k + (buf + NBUF - 1) % NBUF * BN * D, sm.tile.v + (buf + NBUF - 1) % NBUF * BN * D);
+        const E* kl = sm.tile.k + buf * BN * D;
+        const E* vl = sm.tile.v + buf * BN * D;
         const int key0 = k0 + i * BN;
         if (CAUSAL && key0 > lim1) return;      // nothing visible to the wave
         floatx16 sc[NS];
@@ -258,17 +258,18 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
             }
         __builtin_amdgcn_s_setprio(0);
     };
-    if (nt > 0) {
-        ids();
-        fetch(sm.tile.k[0], sm.tile.v[0]);
-        if (nt > 1) {
-            advance(1);
-            ids();
+#pragma unroll
+    for (int i = 0; i < NBUF - 1; ++i)
+        if (i < nt) fetch(i, sm.tile.k + i * BN * D, sm.tile.v + i * BN * D);
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
+    for (int i = 0; i < nt; i += NBUF) {
+        tile(i, 0);
+        if (i + 1 < nt) tile(i + 1, 1);
+        if (NBUF > 2) {
+            if (i + 2 < nt) tile(i + 2, 2 % NBUF);
+            if (i + 3 < nt) tile(i + 3, 3 % NBUF);
         }
-    }
-    for (int i = 0; i < nt; i += 2) {
-        tile(i, sm.tile.k[0], sm.tile.v[0], sm.tile.k[1], sm.tile.v[1]);
-        if (i + 1 < nt) tile(i + 1, sm.tile.k[1], sm.tile.v[1], sm.tile.k[0], sm.tile.v[0]);
     }
     l += swa_swap(l);
     // A masked key has weight 0, and 0 times an infinity or a NaN in its values
@@ -388,7 +389,8 @@ __device__ __forceinline__ void prefix_own(const PrefixArgs& a, E* kl, E* vl, co
     if (h < nh) prefix_part<E, D>(a, part + h, o, m, l, g);
 }
 
-template <class E, int D>
+// BN: tiles of 64 keys, or of 32 with more on their way.
+template <class E, int D, int BN>
 __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_kernel(PrefixArgs a)
 {
     __shared__ __align__(16) PrefixLds<E, D> sm;
@@ -410,7 +412,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
         K.k = (const E*)a.kc + hk * a.kcs[2];
         K.v = (const E*)a.vc + hk * a.vcs[2];
         K.pages = a.ptable;
-        prefix_rows<E, D, false>(a, sm, K, hk, 0, (int)rows, blk * PREFIX_ROWS, 0, k0, k1, ((int64_t)sp * a.Hkv + hk) * rows);
+        prefix_rows<E, D, false, BN>(a, sm, K, hk, 0, (int)rows, blk * PREFIX_ROWS, 0, k0, k1, ((int64_t)sp * a.Hkv + hk) * rows);
         return;
     }
     int64_t item = (int)blockIdx.x - a.nprefix;
@@ -437,7 +439,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
         K.k = (const E*)a.kc + hk * a.kcs[2];
         K.v = (const E*)a.vc + hk * a.vcs[2];
         K.pages = a.table + b * a.ts;
-        prefix_rows<E, D, true>(a, sm, K, hk, q0, nrows, r0, len, k0, k1,
+        prefix_rows<E, D, true, BN>(a, sm, K, hk, q0, nrows, r0, len, k0, k1,
                                 ((int64_t)(a.sp + so) * a.Hkv + hk) * rows + (int64_t)q0 * G);
         return;
     }
@@ -592,7 +594,10 @@ static hipError_t prefix(PrefixArgs a, hipStream_t st)
     prefix_plan(a, a.cu != nullptr);
     a.ml = a.part + (int64_t)(a.sp + a.so) * a.T * a.Hq * D;
     a.nprefix = (int)swa_grid((int64_t)a.blocks * a.Hkv * a.sp);
-    kd_prefix_kernel<E, D><<<(unsigned)prefix_grid(a, a.cu != nullptr, PrefixLds<E, D>::ITEMS), 256, 0, st>>>(a);
+    const unsigned grid = (unsigned)prefix_grid(a, a.cu != nullptr, PrefixLds<E, D>::ITEMS);
+    // few blocks of rows read the prefix from memory, many from a cache
+    if (sizeof(E) == 4 || a.blocks <= 4) kd_prefix_kernel<E, D, 32><<<grid, 256, 0, st>>>(a);
+    else kd_prefix_kernel<E, D, sizeof(E) == 4 ? 32 : 64><<<grid, 256, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // (a row's parts one after the other where rows are many, at once where they are few)
