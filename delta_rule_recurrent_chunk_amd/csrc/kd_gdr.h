@@ -9,6 +9,7 @@
 //     S_C = e^bC S0 + U^T (e^(bC - b) K).
 // A and P do not depend on the state: a first kernel makes them for all chunks
 // at once, a second one passes over the chunks with the state in registers.
+// The backward pass reads the same A and P, transposed.
 // The columns of S^T (values) do not mix, so every wave of the pass owns 16 of
 // them and needs nothing from another one.
 //
@@ -47,7 +48,7 @@ struct GdrArgs {
     float* dS0;
     void *ds, *x, *x2;                         // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv] (x2: its remainder)
     // workspace of both
-    void* rec;                                 // the chunks' records: matrices in blocks, then gate factors
+    void* rec;                                 // the chunks' records: P and A in blocks, then gate factors
     const int* cu;
     int B, T, Hk, Hv, dk, dv;                  // packed: B sequences in T rows
     int slots, gates32;
@@ -143,6 +144,14 @@ __device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c
     return c.rows > 0;
 }
 
+// Block (i, j) of a lower triangular matrix: rows 16 i .., columns 32 j ..;
+// blocks (0,0) (1,0) (2,0) (2,1) (3,0) (3,1).  In a block lane l holds row l %
+// 16 and columns 16 h + 4 (l / 16) + r at element 4 h + r: the order in which
+// two accumulator tiles of 16 rows each are packed.  Its transpose has the
+// blocks (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
+__device__ __forceinline__ constexpr int gdr_block(int i, int j) { return i < 2 ? i : 2 * i - 2 + j; }
+__device__ __forceinline__ constexpr int gdr_block_t(int i, int j) { return i < 2 ? 2 * i + j : 2 + i; }
+
 template <class E>
 struct GdrT;
 
@@ -206,6 +215,20 @@ struct GdrT<__bf16> {
                                                         (__attribute__((address_space(3))) v4s*)(tile + TL::off(r, c / 8) + c % 8)));
         return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
     }
+    // Block (i, j) of a transpose from the blocks of the matrix: lane's s = 16 i + l16, r = 32 j +
+    // 16 h + 4 g + e.  Row r's four columns 4 c .. of block (r / 16, i / 2) are
+    // the half i % 2 of its lane r % 16 + 16 c.
+    static __device__ __forceinline__ Frag ld_at(const __bf16* rec, int i, int j, int lane) {
+        typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+        const int l = lane & 15, at = (4 * (lane >> 4) + (l >> 2) + 16 * (l & 3)) * 8 + 4 * (i & 1);
+        s16x4 x = {0, 0, 0, 0}, y;
+        if (2 * j >= i)
+            x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                              (__attribute__((address_space(3))) v4s*)(rec + gdr_block(2 * j, i / 2) * 512 + at)));
+        y = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                          (__attribute__((address_space(3))) v4s*)(rec + gdr_block(2 * j + 1, i / 2) * 512 + at)));
+        return __builtin_bit_cast(Frag, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
     template <int D>
     static __device__ __forceinline__ Frag tr(const __bf16* tile, int r, int c) {
         typedef SwaTile<__bf16, D> TL;
@@ -263,6 +286,16 @@ struct GdrT<float> {
         for (int e = 0; e < 4; ++e) x[e] = tile[TL::off(r + e, c / 4) + c % 4];
         return x;
     }
+    static __device__ __forceinline__ Frag ld_at(const float* rec, int i, int j, int lane) {
+        const int l = lane & 15;
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = 2 * j + e / 4;      // r's tile
+            f[e] = t >= i ? rec[gdr_block(t, i / 2) * 512 + (4 * (lane >> 4) + e % 4 + 16 * (l >> 2)) * 8 + 4 * (i & 1) + (l & 3)] : 0.f;
+        }
+        return f;
+    }
     template <int D>
     static __device__ __forceinline__ Frag at(const float* tile, int j, int c, int lane) {
         typedef SwaTile<float, D> TL;
@@ -299,25 +332,16 @@ __device__ __forceinline__ floatx4 gdr_mma3(typename GdrT<E>::Frag a, typename G
     return c;
 }
 
-// Block (i, j) of a lower triangular matrix: rows 16 i .., columns 32 j ..;
-// blocks (0,0) (1,0) (2,0) (2,1) (3,0) (3,1).  In a block lane l holds row l %
-// 16 and columns 16 h + 4 (l / 16) + r at element 4 h + r: the order in which
-// two accumulator tiles of 16 rows each are packed.  Its transpose has the
-// blocks (0,0) (0,1) (1,0) (1,1) (2,1) (3,1).
-__device__ __forceinline__ constexpr int gdr_block(int i, int j) { return i < 2 ? i : 2 * i - 2 + j; }
-__device__ __forceinline__ constexpr int gdr_block_t(int i, int j) { return i < 2 ? 2 * i + j : 2 + i; }
-
 template <class E>
 __host__ __device__ constexpr int gdr_part() { return GDR_BLOCKS * 512; }      // elements of a part
-// Parts of a record (bf16: A, A^T and P^T each with a remainder), and its bytes.
-//   forward:  A [A2] P                backward: A [A2] A^T [A^T2] P^T [P^T2]
-// The last parts and the factors behind them are what a pass reads.
+// A record: P and A, then the gate factors.  In bf16 both have a remainder, P's
+// in front (only the backward pass reads it, and only its forward writes it).
+// Each pass reads from its first part on: the backward pass all, the forward
+// pass from P, the segments' maps from A.
 template <class E>
-__host__ __device__ constexpr int gdr_parts(bool bwd) { return sizeof(E) == 2 ? (bwd ? 6 : 3) : (bwd ? 3 : 2); }
+__host__ __device__ constexpr int gdr_parts() { return sizeof(E) == 2 ? 4 : 2; }
 template <class E>
-__host__ __device__ constexpr int64_t gdr_rec_bytes(bool bwd) {
-    return (int64_t)gdr_parts<E>(bwd) * gdr_part<E>() * (int)sizeof(E) + GDR_VEC * 4;
-}
+__host__ __device__ constexpr int64_t gdr_rec_bytes() { return (int64_t)gdr_parts<E>() * gdr_part<E>() * (int)sizeof(E) + GDR_VEC * 4; }
 
 // Stages 64 rows of K or Q in an LDS tile, from `row` on (past the sequence's
 // last they repeat it); columns past dk keep what the tile holds (zeros).  The
@@ -363,18 +387,20 @@ struct GdrFetch {
     }
 };
 
-// What a pass reads of a chunk beside K and Q: the end of its record (A or A^T,
-// P or P^T, and the gate factors) and 16 columns of V (or dO) a wave.  The
-// workgroup's threads load it to registers a chunk ahead and put it in LDS when
-// the chunk before is done.
-template <class E, bool BWD, int NW>
+// What a pass reads of a chunk beside K and Q: the last PARTS parts of its record,
+// the gate factors, and 16 columns of V (or dO) a wave.  The workgroup's threads
+// load it to registers a chunk ahead and put it in LDS when the chunk before is
+// done.
+template <class E, int PARTS, int NW>
 struct GdrSide {
-    static constexpr int REC = (GdrT<E>::TWO ? (BWD ? 4 : 3) : 2) * GDR_BLOCKS * 512;      // elements
+    static constexpr int REC = PARTS * gdr_part<E>();      // elements
     static constexpr int PIECES = (REC * (int)sizeof(E) + GDR_VEC * 4) / 16;
+    static constexpr int SKIP = (gdr_parts<E>() - PARTS) * gdr_part<E>() * (int)sizeof(E);      // bytes
     E rec[REC];
     float vec[GDR_VEC];
     E v[64 * 16 * NW];
 };
+
 // Rows of a matrix at a wave-uniform address as a buffer: what lies past its
 // bytes reads as zero and is not written, so the ends of a sequence and of a
 // head's columns need no branch.  GDR_NONE: an offset past any of them.
@@ -403,10 +429,10 @@ __device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floa
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{x[4], x[5], x[6], x[7]}), r, at + 16, 0, 0);
 }
 
-template <class E, bool BWD, int NW>
+template <class E, int PARTS, int NW>
 struct GdrSideAhead {
     typedef SwaTile<E, 16 * NW> TV;
-    typedef GdrSide<E, BWD, NW> Side;
+    typedef GdrSide<E, PARTS, NW> Side;
     static constexpr int NT = 64 * NW, N = (Side::PIECES + NT - 1) / NT, M = 64 * TV::CPR / NT, STEP = NT / TV::CPR;
     floatx4 x[N], v[M];
     const E* vb;
@@ -419,7 +445,7 @@ struct GdrSideAhead {
     }
     // a chunk's record from `rec` on
     __device__ __forceinline__ void load(const char* rec, int tid) {
-        const auto r = gdr_buffer(rec, Side::PIECES * 16);
+        const auto r = gdr_buffer(rec + Side::SKIP, Side::PIECES * 16);
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = gdr_load(r, (i * NT + tid) * 16);
     }

@@ -34,6 +34,7 @@ kd_status done(hipError_t e) { return e == hipSuccess ? KD_OK : KD_ERR_LAUNCH; }
 
 struct GdrSizes {
     size_t q, k, v, o, qg, kg, gate, state, slots;      // bytes (spanned by the inputs, contiguous others), chunk slots
+    size_t rec, saved;                                  // what the backward pass is given: records, then states
 };
 
 kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
@@ -60,6 +61,8 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     s->gate = (size_t)(rows * d->Hv * (d->gates32 ? 4 : es));
     s->state = (size_t)d->B * d->Hv * d->dv * d->dk * 4;
     s->slots = (size_t)slots;
+    s->rec = up256(s->slots * d->Hv * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>() : kd::gdr_rec_bytes<float>()));
+    s->saved = s->rec + up256(s->slots * d->Hv * d->dv * d->dk * es);
     int run;
     if (!grid_fits((int64_t)s->slots * d->Hv, 64) || !grid_fits((int64_t)s->slots * d->Hk, 512) ||
         !grid_fits(kd::gdr_pass_grid((int64_t)d->B * d->Hv * ((d->dv + 63) / 64), run), 256))
@@ -93,30 +96,37 @@ kd::GdrArgs gdr_args(const kd_gdr_desc* d, const GdrSizes& s, const void* q, con
     return a;
 }
 
-// Offsets of the workspace's parts: records; backward: dS, X and (bf16) its
-// remainder; forward in segments: their states and maps (si and m are equal
-// where a sequence is not cut).
+// Offsets of the workspace's parts.  Forward: records (not where they are
+// saved), the segments' states and maps (equal where a sequence is not cut).
+// Backward: dS, X and (bf16) its remainder.
 struct GdrSpace {
     size_t ds, x, x2, si, m, bytes;
 };
 GdrSpace gdr_space(const kd_gdr_desc* d, const GdrSizes& s, bool packed, bool bwd) {
     const size_t n = s.slots * d->Hv, es = es_of(d->dtype);
-    GdrSpace w;
-    w.ds = up256(n * (d->dtype == KD_BF16 ? kd::gdr_rec_bytes<__bf16>(bwd) : kd::gdr_rec_bytes<float>(bwd)));
-    w.x = w.ds + (bwd ? up256(n * d->dv * d->dk * es) : 0);
-    w.x2 = w.x + (bwd ? up256(n * kd::GDR_C * d->dv * es) : 0);
-    w.si = w.x2 + (bwd && es == 2 ? up256(n * kd::GDR_C * d->dv * es) : 0);
+    GdrSpace w = {};
+    if (bwd) {
+        w.x = up256(n * d->dv * d->dk * es);
+        w.x2 = w.x + up256(n * kd::GDR_C * d->dv * es);
+        w.bytes = w.x2 + (es == 2 ? up256(n * kd::GDR_C * d->dv * es) : 0);
+        return w;
+    }
     kd::GdrArgs a = gdr_args(d, s, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
     kd::gdr_plan(a, packed);
-    const bool cut = !bwd && a.nseg > 1;
-    w.m = w.si + (cut ? up256((size_t)a.segs * d->Hv * d->dv * d->dk * 4) : 0);
-    w.bytes = w.m + (cut ? up256((size_t)a.segs * d->Hv * d->dk * d->dk * 4) : 0);
+    w.si = s.rec;
+    w.m = w.si + (a.nseg > 1 ? up256((size_t)a.segs * d->Hv * d->dv * d->dk * 4) : 0);
+    w.bytes = w.m + (a.nseg > 1 ? up256((size_t)a.segs * d->Hv * d->dk * d->dk * 4) : 0);
     return w;
 }
 
 }  // namespace
 
 extern "C" {
+
+size_t kron_delta_gdr_saved_bytes(const kd_gdr_desc* d, int packed) {
+    GdrSizes s;
+    return check_gdr(d, packed != 0, &s) == KD_OK ? s.saved : 0;
+}
 
 size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc* d, int packed, int backward) {
     GdrSizes s;
@@ -125,22 +135,21 @@ size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc* d, int packed, int back
 }
 
 kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
-                             const void* g, const void* beta, const float* S0, void* o, float* ST, void* hs, void* ws,
+                             const void* g, const void* beta, const float* S0, void* o, float* ST, void* saved, void* ws,
                              size_t ws_bytes, void* stream) {
     GdrSizes s;
     const kd_status st = check_gdr(d, cu != nullptr, &s);
     if (st != KD_OK) return st;
     if (d->T > 0 && (!q || !k || !v || !g || !beta || !o)) return KD_ERR_NULL;
-    const void* ptrs[] = {q, k, v, g, beta, S0, o, ST, hs, ws};
+    const void* ptrs[] = {q, k, v, g, beta, S0, o, ST, saved, ws};
     for (const void* p : ptrs)
         if (misaligned(p)) return KD_ERR_ALIGN;
     if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
     const GdrSpace w = gdr_space(d, s, cu != nullptr, false);
-    const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
     const Range ins[] = {range_of(q, s.q),         range_of(k, s.k),       range_of(v, s.v),
                          range_of(g, s.gate),      range_of(beta, s.gate), range_of(S0, S0 ? s.state : 0),
                          range_of(cu, cu ? (size_t)(d->B + 1) * 4 : 0)};
-    const Range outs[] = {range_of(o, s.o), range_of(ST, ST ? s.state : 0), range_of(hs, hs ? hsb : 0), range_of(ws, ws ? w.bytes : 0)};
+    const Range outs[] = {range_of(o, s.o), range_of(ST, ST ? s.state : 0), range_of(saved, saved ? s.saved : 0), range_of(ws, ws ? w.bytes : 0)};
     if (any_overlap(outs, 4, ins, 7)) return KD_ERR_ALIAS;
     if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return KD_ERR_WORKSPACE;
     if (d->T == 0 && !ST) return KD_OK;
@@ -148,8 +157,8 @@ kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.S0 = S0;
     a.o = o;
     a.ST = ST;
-    a.hs = hs;
-    a.rec = ws;
+    a.rec = saved ? saved : ws;
+    a.hs = saved ? (char*)saved + s.rec : nullptr;
     kd::gdr_plan(a, cu != nullptr);
     if (w.m > w.si) {
         a.SI = (float*)((char*)ws + w.si);
@@ -159,21 +168,20 @@ kd_status kron_delta_gdr_fwd(const kd_gdr_desc* d, const int32_t* cu, const void
 }
 
 kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void* q, const void* k, const void* v,
-                             const void* g, const void* beta, const void* hs, const void* dO, const float* dST, void* dq,
+                             const void* g, const void* beta, const void* saved, const void* dO, const float* dST, void* dq,
                              void* dk, void* dv, void* dg, void* dbeta, float* dS0, void* ws, size_t ws_bytes,
                              void* stream) {
     GdrSizes s;
     const kd_status st = check_gdr(d, cu != nullptr, &s);
     if (st != KD_OK) return st;
-    if (d->T > 0 && (!q || !k || !v || !g || !beta || !hs || !dO || !dq || !dk || !dv || !dg || !dbeta)) return KD_ERR_NULL;
-    const void* ptrs[] = {q, k, v, g, beta, hs, dO, dST, dq, dk, dv, dg, dbeta, dS0, ws};
+    if (d->T > 0 && (!q || !k || !v || !g || !beta || !saved || !dO || !dq || !dk || !dv || !dg || !dbeta)) return KD_ERR_NULL;
+    const void* ptrs[] = {q, k, v, g, beta, saved, dO, dST, dq, dk, dv, dg, dbeta, dS0, ws};
     for (const void* p : ptrs)
         if (misaligned(p)) return KD_ERR_ALIGN;
     if (((uintptr_t)cu & 3u) != 0) return KD_ERR_ALIGN;
     const GdrSpace w = gdr_space(d, s, cu != nullptr, true);
-    const size_t hsb = s.slots * d->Hv * d->dv * d->dk * es_of(d->dtype);
     const Range ins[] = {range_of(q, s.q),    range_of(k, s.k),       range_of(v, s.v),
-                         range_of(g, s.gate), range_of(beta, s.gate), range_of(hs, hs ? hsb : 0),
+                         range_of(g, s.gate), range_of(beta, s.gate), range_of(saved, saved ? s.saved : 0),
                          range_of(dO, s.o),   range_of(dST, dST ? s.state : 0), range_of(cu, cu ? (size_t)(d->B + 1) * 4 : 0)};
     const Range outs[] = {range_of(dq, s.qg),   range_of(dk, s.kg),      range_of(dv, s.o),
                           range_of(dg, s.gate), range_of(dbeta, s.gate), range_of(dS0, dS0 ? s.state : 0),
@@ -182,7 +190,8 @@ kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void
     if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return KD_ERR_WORKSPACE;
     if (d->T == 0 && !dS0) return KD_OK;
     kd::GdrArgs a = gdr_args(d, s, q, k, v, g, beta, cu);
-    a.hs = const_cast<void*>(hs);
+    a.rec = const_cast<void*>(saved);
+    a.hs = (char*)const_cast<void*>(saved) + s.rec;
     a.dO = dO;
     a.dST = dST;
     a.dq = dq;
@@ -191,7 +200,6 @@ kd_status kron_delta_gdr_bwd(const kd_gdr_desc* d, const int32_t* cu, const void
     a.dg = dg;
     a.dbeta = dbeta;
     a.dS0 = dS0;
-    a.rec = ws;
     a.ds = (char*)ws + w.ds;
     a.x = (char*)ws + w.x;
     a.x2 = (char*)ws + w.x2;

@@ -20,7 +20,6 @@
 namespace kd {
 
 int64_t gdr_pass_grid(int64_t items, int& run);
-hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st);
 
 template <class E, int DK>
 __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
@@ -28,11 +27,10 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
-    constexpr int PPT = T::TWO ? 2 : 1;      // P^T's part of what is staged, behind A^T
+    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, PA = T::TWO ? 2 : 1;      // (P and its remainder in front of A)
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, true, 4> side[NBUF];
+        GdrSide<E, gdr_parts<E>(), 4> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -69,11 +67,10 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         kf(sm.k[buf], n * GDR_C, w);
         qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, true, 4> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
-    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(true) +
-                       (gdr_rec_bytes<E>(true) - GdrSide<E, true, 4>::PIECES * 16);
+    GdrSideAhead<E, gdr_parts<E>(), 4> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
     auto load = [&](int n) {
-        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(true), tid);
+        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(), tid);
         ahead.load_v(n * GDR_C);
     };
     auto chunk = [&](int n, int buf) {
@@ -87,19 +84,20 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
             if (NBUF == 2) fetch(n - 1, buf ^ 1);
             load(n - 1);
         }
+        const E* kt = sm.k[buf];
+        const E* qt = sm.q[buf];
+        const GdrSide<E, gdr_parts<E>(), 4>& sd = sm.side[buf];
         if (work) {
-            const E* kt = sm.k[buf];
-            const E* qt = sm.q[buf];
-            const GdrSide<E, true, 4>& sd = sm.side[buf];
-            const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
             Frag A[6], A2[T::TWO ? 6 : 1];
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
-                A[i] = T::ld(rec + i * 512);
-                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
-            }
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = t / 2; j < 2; ++j) {
+                    A[gdr_block_t(t, j)] = T::ld_at(sd.rec + PA * gdr_part<E>(), t, j, lane);
+                    if (T::TWO) A2[T::TWO ? gdr_block_t(t, j) : 0] = T::ld_at(sd.rec + (PA + 1) * gdr_part<E>(), t, j, lane);
+                }
             Frag sh[NK], sl[NK];
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
@@ -133,8 +131,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
             for (int j = 1; j >= 0; --j)
 #pragma unroll
                 for (int t = 0; t < 2 + 2 * j; ++t)
-                    for (int p = PPT; p < (T::TWO ? PPT + 2 : PPT + 1); ++p)
-                        U[t] = T::mma(T::ld(rec + p * gdr_part<E>() + gdr_block_t(t, j) * 512), d[j], U[t]);
+                    for (int p = 0; p < PA; ++p) U[t] = T::mma(T::ld_at(sd.rec + p * gdr_part<E>(), t, j, lane), d[j], U[t]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
@@ -396,11 +393,11 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     auto load3 = [&](const Next& n) {
         lk.load((const E*)a.k + n.c.base * a.ks[0] + (int64_t)n.c.first * a.ks[1] + n.hk * a.ks[2], a.ks[1], n.kr, a.dk, tid);
         lq.load((const E*)a.q + n.c.base * a.qs[0] + (int64_t)n.c.first * a.qs[1] + n.hk * a.qs[2], a.qs[1], n.kr, a.dk, tid);
-        const char* record = (const char*)a.rec + n.at * gdr_rec_bytes<E>(true);
-        const auto rec = gdr_buffer(record, n.c.rows > 0 ? AP * 16 : 0);
+        const char* record = (const char*)a.rec + n.at * gdr_rec_bytes<E>();
+        const auto rec = gdr_buffer(record + gdr_parts<E>() / 2 * gdr_part<E>() * (int)sizeof(E), n.c.rows > 0 ? AP * 16 : 0);      // (A)
 #pragma unroll
         for (int i = 0; i < NA; ++i) la[i] = gdr_load(rec, (i * 512 + tid) * 16);
-        lf = gdr_load(gdr_buffer(record + gdr_rec_bytes<E>(true) - GDR_VEC * 4, n.c.rows > 0 ? GDR_VEC * 4 : 0), tid * 16);
+        lf = gdr_load(gdr_buffer(record + gdr_rec_bytes<E>() - GDR_VEC * 4, n.c.rows > 0 ? GDR_VEC * 4 : 0), tid * 16);
     };
     GdrChunk c, cn;
     int item = next((int)blockIdx.x - (int)gridDim.x, c), itemn;
@@ -810,8 +807,6 @@ static hipError_t gdr_bwd(const GdrArgs& a, hipStream_t st)
 
 hipError_t launch_gdr_bwd(int bf16, const GdrArgs& a, hipStream_t st)
 {
-    const hipError_t e = launch_gdr_prep(bf16, true, a, st);
-    if (e != hipSuccess) return e;
     if (bf16) {
         if (a.dk <= 64) return a.dv <= 64 ? gdr_bwd<__bf16, 64, 64>(a, st) : gdr_bwd<__bf16, 64, 128>(a, st);
         return a.dv <= 64 ? gdr_bwd<__bf16, 128, 64>(a, st) : gdr_bwd<__bf16, 128, 128>(a, st);

@@ -10,16 +10,16 @@ namespace kd {
 // K K^T and Q K^T take 16-row fragments straight from memory.  A by blocks of
 // 16: the four diagonal blocks by substitution, one column a lane; then row by
 // row of blocks A_ij = -A_ii sum_k T_ik A_kj in fp32 products, in place of T.
-// BWD writes A, its transpose and P's transpose, otherwise A and P.
-template <class E, int DK, bool BWD>
+// SAVE (for a backward pass): P's remainder too.
+template <class E, int DK, bool SAVE>
 __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = DK / 32, LD = 68;
-    constexpr int PA2 = 1, PP = T::TWO ? 2 : 1, PAT = T::TWO ? 2 : 1, PAT2 = 3, PPT = T::TWO ? 4 : 2;
+    constexpr int PP2 = 0, PP = T::TWO ? 1 : 0, PA = PP + 1, PA2 = PA + 1;
     __shared__ __align__(16) float M[64 * LD];
-    __shared__ __align__(16) float bh[64], bl[64], be[64];
+    __shared__ __align__(16) float bh[64], bl[64];
     const int lane = threadIdx.x, l16 = lane & 15, g = lane >> 4;
     const int hv = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv, hk = hv / (a.Hv / a.Hk);
     GdrChunk c;
@@ -48,9 +48,8 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
     const double last = __shfl(b, 63);
     bh[lane] = (float)b;
     bl[lane] = (float)(b - (double)(float)b);
-    be[lane] = beta;
-    char* const record = (char*)a.rec + ((int64_t)slot * a.Hv + hv) * gdr_rec_bytes<E>(BWD);
-    float* vec = (float*)(record + gdr_parts<E>(BWD) * gdr_part<E>() * (int)sizeof(E));
+    char* const record = (char*)a.rec + ((int64_t)slot * a.Hv + hv) * gdr_rec_bytes<E>();
+    float* vec = (float*)(record + gdr_parts<E>() * gdr_part<E>() * (int)sizeof(E));
     const float eb = __builtin_amdgcn_exp2f((float)b);
     vec[lane] = beta;
     vec[64 + lane] = beta * eb;
@@ -71,7 +70,7 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 16 * i + l16;
-        const float rh = bh[r], rl = bl[r], br = be[r];
+        const float rh = bh[r], rl = bl[r], br = __shfl(beta, r);
         floatx4 p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -80,10 +79,8 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
             floatx4 x = zero;
 #pragma unroll
             for (int ks = 0; ks < NK; ++ks) x = T::mma(k[j][ks], k[i][ks], x);
-            if (!BWD) {
 #pragma unroll
-                for (int ks = 0; ks < NK; ++ks) p[j] = T::mma(k[j][ks], q[i][ks], p[j]);
-            }
+            for (int ks = 0; ks < NK; ++ks) p[j] = T::mma(k[j][ks], q[i][ks], p[j]);
             const floatx4 sh = *reinterpret_cast<const floatx4*>(bh + 16 * j + 4 * g), sl = *reinterpret_cast<const floatx4*>(bl + 16 * j + 4 * g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -94,37 +91,11 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
             }
             *reinterpret_cast<floatx4*>(M + r * LD + 16 * j + 4 * g) = x;
         }
-        if (!BWD) {
-            T::st(rec + PP * gdr_part<E>() + gdr_block(i, 0) * 512, T::pack(p[0], p[1]));
-            if (i >= 2) T::st(rec + PP * gdr_part<E>() + gdr_block(i, 1) * 512, T::pack(p[2], p[3]));
-        }
-    }
-    if (BWD) {
-        // P's transpose: lane: token s of block i, r = 16 j + 4 g + e
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = 16 * i + l16;
-            const float sh = bh[s], sl = bl[s];
-            floatx4 p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                p[j] = zero;
-                if (j < i) continue;
-#pragma unroll
-                for (int ks = 0; ks < NK; ++ks) p[j] = T::mma(q[j][ks], k[i][ks], p[j]);
-                const floatx4 rh = *reinterpret_cast<const floatx4*>(bh + 16 * j + 4 * g), rl = *reinterpret_cast<const floatx4*>(bl + 16 * j + 4 * g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 16 * j + 4 * g + e;
-                    p[j][e] = s <= r ? a.scale * __builtin_amdgcn_exp2f((rh[e] - sh) + (rl[e] - sl)) * p[j][e] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = i / 2; j < 2; ++j) {
-                const Frag f = T::pack(p[2 * j], p[2 * j + 1]);
-                T::st(rec + PPT * gdr_part<E>() + gdr_block_t(i, j) * 512, f);
-                if (T::TWO) T::st(rec + (PPT + 1) * gdr_part<E>() + gdr_block_t(i, j) * 512, T::rest(p[2 * j], p[2 * j + 1], f));
-            }
+        for (int j = 0; j <= i / 2; ++j) {
+            const Frag f = T::pack(p[2 * j], p[2 * j + 1]);
+            T::st(rec + PP * gdr_part<E>() + gdr_block(i, j) * 512, f);
+            if (T::TWO && SAVE) T::st(rec + PP2 * gdr_part<E>() + gdr_block(i, j) * 512, T::rest(p[2 * j], p[2 * j + 1], f));
         }
     }
     __syncthreads();
@@ -182,23 +153,8 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
             const floatx4 x = *reinterpret_cast<const floatx4*>(m);
             const floatx4 y = 2 * j + 1 <= i ? *reinterpret_cast<const floatx4*>(m + 16) : zero;
             const Frag f = T::pack(x, y);
-            T::st(rec + gdr_block(i, j) * 512, f);
+            T::st(rec + PA * gdr_part<E>() + gdr_block(i, j) * 512, f);
             if (T::TWO) T::st(rec + PA2 * gdr_part<E>() + gdr_block(i, j) * 512, T::rest(x, y, f));
-        }
-    if (!BWD) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = i / 2; j < 2; ++j) {
-            floatx4 x = zero, y = zero;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (2 * j >= i) x[e] = M[(32 * j + 4 * g + e) * LD + 16 * i + l16];
-                y[e] = M[(32 * j + 16 + 4 * g + e) * LD + 16 * i + l16];
-            }
-            const Frag f = T::pack(x, y);
-            T::st(rec + PAT * gdr_part<E>() + gdr_block_t(i, j) * 512, f);
-            if (T::TWO) T::st(rec + PAT2 * gdr_part<E>() + gdr_block_t(i, j) * 512, T::rest(x, y, f));
         }
 }
 
@@ -220,10 +176,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, NC0 = 16 * NW;      // (columns of a workgroup)
-    constexpr int PP = T::TWO ? 2 : 1;
+    constexpr int PA = MODE == GDR_MAPS ? 0 : 1, PARTS = PA + (T::TWO ? 2 : 1);         // (P in front of A)
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, false, NW> side[NBUF];
+        GdrSide<E, PARTS, NW> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int vslices = (a.dv + NC0 - 1) / NC0, slices = MODE == GDR_MAPS ? vslices + (a.dk + NC0 - 1) / NC0 : vslices;
@@ -282,10 +238,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
         kf(sm.k[buf], n * GDR_C, w);
         if (MODE != GDR_MAPS) qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, false, NW> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, tid);
-    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>(false);
+    GdrSideAhead<E, PARTS, NW> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, tid);
+    const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
     auto load = [&](int n) {
-        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(false), tid);
+        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(), tid);
         ahead.load_v(n * GDR_C);
     };
     // The order is for one wave a SIMD, which has nothing else to run while it
@@ -300,10 +256,10 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
         }
         swa_landed();
         const bool more = n + 1 < NC, early = NBUF == 2 && more;
+        const E* kt = sm.k[buf];
+        const E* qt = sm.q[buf];
+        const GdrSide<E, PARTS, NW>& sd = sm.side[buf];
         if (work) {
-            const E* kt = sm.k[buf];
-            const E* qt = sm.q[buf];
-            const GdrSide<E, false, NW>& sd = sm.side[buf];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             Frag sh[NK], sl[NK], x[4], A[6], A2[T::TWO ? 6 : 1], f[2], f2[2];
@@ -367,8 +323,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
             }
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
-                A[i] = T::ld(rec + i * 512);
-                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + gdr_part<E>() + i * 512);
+                A[i] = T::ld(rec + PA * gdr_part<E>() + i * 512);
+                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + (PA + 1) * gdr_part<E>() + i * 512);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -379,7 +335,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
             Frag P[6], kc[2 * NK];
             if (MODE != GDR_MAPS)
 #pragma unroll
-                for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + PP * gdr_part<E>() + i * 512);
+                for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + i * 512);
             if (NW == 4) {
 #pragma unroll
                 for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
@@ -398,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[T::TWO ? gdr_block(t, j) : 0], f[j], U[t]);
                 }
             }
-            if (more) ahead.load(rec0 + (n + 1) * a.Hv * gdr_rec_bytes<E>(false), tid);
+            if (more) ahead.load(rec0 + (n + 1) * a.Hv * gdr_rec_bytes<E>(), tid);
             const float eC = sd.vec[256];
 #pragma unroll
             for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
@@ -559,22 +515,14 @@ int64_t gdr_pass_grid(int64_t items, int& run)
     return (items + 8 * run - 1) / (8 * run) * 8 * run;
 }
 
-template <class E, int DK, bool BWD>
+template <class E, int DK>
 static hipError_t gdr_prep(const GdrArgs& a, hipStream_t st)
 {
-    kd_gdr_prep_kernel<E, DK, BWD><<<(unsigned)((int64_t)a.slots * a.Hv), 64, 0, st>>>(a);
+    const unsigned grid = (unsigned)((int64_t)a.slots * a.Hv);
+    if (grid == 0) return hipSuccess;
+    if (a.hs) kd_gdr_prep_kernel<E, DK, true><<<grid, 64, 0, st>>>(a);
+    else kd_gdr_prep_kernel<E, DK, false><<<grid, 64, 0, st>>>(a);
     return hipGetLastError();
-}
-
-hipError_t launch_gdr_prep(int bf16, bool bwd, const GdrArgs& a, hipStream_t st)
-{
-    if (a.slots == 0) return hipSuccess;
-    if (bf16) {
-        if (a.dk <= 64) return bwd ? gdr_prep<__bf16, 64, true>(a, st) : gdr_prep<__bf16, 64, false>(a, st);
-        return bwd ? gdr_prep<__bf16, 128, true>(a, st) : gdr_prep<__bf16, 128, false>(a, st);
-    }
-    if (a.dk <= 64) return bwd ? gdr_prep<float, 64, true>(a, st) : gdr_prep<float, 64, false>(a, st);
-    return bwd ? gdr_prep<float, 128, true>(a, st) : gdr_prep<float, 128, false>(a, st);
 }
 
 // Columns of a pass's workgroup: see the kernel.
@@ -603,6 +551,8 @@ static void gdr_pass(const GdrArgs& a, hipStream_t st)
 template <class E, int DK>
 static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
 {
+    const hipError_t e = gdr_prep<E, DK>(a, st);
+    if (e != hipSuccess) return e;
     if (a.SI) {
         gdr_pass<E, DK, GDR_MAPS>(a, st);
         kd_gdr_chain_kernel<DK><<<dim3((a.dv + 15) / 16, a.Hv, a.B), 256, 0, st>>>(a);
@@ -632,8 +582,6 @@ void gdr_plan(GdrArgs& a, bool packed)
 
 hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st)
 {
-    const hipError_t e = launch_gdr_prep(bf16, false, a, st);
-    if (e != hipSuccess) return e;
     if (bf16) return a.dk <= 64 ? gdr_passes<__bf16, 64>(a, st) : gdr_passes<__bf16, 128>(a, st);
     return a.dk <= 64 ? gdr_passes<float, 64>(a, st) : gdr_passes<float, 128>(a, st);
 }

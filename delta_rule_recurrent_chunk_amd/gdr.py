@@ -19,7 +19,7 @@ from .layers import _call, _check, _code, _fits, _flat, _need_cuda, _ptr, _ready
 GDR_MAX_DK, GDR_MAX_DV = 128, 256
 GDR_MAX_STEP = 1 << 22
 
-EXPORTED = ("kron_delta_gdr_workspace_bytes", "kron_delta_gdr_fwd", "kron_delta_gdr_bwd", "kron_delta_gdr_step")
+EXPORTED = ("kron_delta_gdr_workspace_bytes", "kron_delta_gdr_saved_bytes", "kron_delta_gdr_fwd", "kron_delta_gdr_bwd", "kron_delta_gdr_step")
 
 _i32, _i64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _s3 = _i64 * 3
@@ -39,6 +39,8 @@ def declare(L):
     P = ctypes.POINTER
     L.kron_delta_gdr_workspace_bytes.restype = sz
     L.kron_delta_gdr_workspace_bytes.argtypes = [P(KdGdrDesc), i32, i32]
+    L.kron_delta_gdr_saved_bytes.restype = sz
+    L.kron_delta_gdr_saved_bytes.argtypes = [P(KdGdrDesc), i32]
     L.kron_delta_gdr_fwd.restype = i32
     L.kron_delta_gdr_fwd.argtypes = [P(KdGdrDesc)] + [vp] * 10 + [vp, sz, vp]
     L.kron_delta_gdr_bwd.restype = i32
@@ -92,10 +94,6 @@ def _heads(t):
     return t.clone() if t.is_contiguous() else t.contiguous()
 
 
-def _slots(desc, cu):
-    return desc.T // 64 + desc.B if cu is not None else desc.B * ((desc.T + 63) // 64)
-
-
 def _state(name, S, desc, dev):
     if S is not None:
         _check(name, S, (desc.B, desc.Hv, desc.dv, desc.dk), _la._torch.float32)
@@ -119,7 +117,10 @@ def gdr_fwd(q, k, v, g, beta, S0=None, *, scale=None, cu_seqlens=None, return_st
     o = torch.empty(v.shape, dtype=q.dtype, device=dev)
     shape = (desc.B, desc.Hv, desc.dv, desc.dk)
     ST = torch.empty(shape, dtype=torch.float32, device=dev) if return_state else None
-    saved = torch.empty((_slots(desc, cu),) + shape[1:], dtype=q.dtype, device=dev) if save_states else None
+    saved = None
+    if save_states:
+        saved = torch.empty(int(L.kron_delta_gdr_saved_bytes(ctypes.byref(desc), int(cu is not None))), dtype=torch.uint8,
+                            device=dev)
     need = int(L.kron_delta_gdr_workspace_bytes(ctypes.byref(desc), int(cu is not None), 0))
     ws, wsb = _workspace(workspace, need, dev)
     _call("kron_delta_gdr_fwd", dev, L.kron_delta_gdr_fwd, ctypes.byref(desc), _ptr(cu), _ptr(q), _ptr(k), _ptr(v),
@@ -128,14 +129,14 @@ def gdr_fwd(q, k, v, g, beta, S0=None, *, scale=None, cu_seqlens=None, return_st
 
 
 def gdr_bwd(q, k, v, g, beta, saved, dO, dST=None, *, scale=None, cu_seqlens=None, return_dS0=True, workspace=None):
-    """Gradients of <dO, o> + <dST, ST> from gdr_fwd's inputs and its saved
-    states: a dict with dq, dk, dv, dg, dbeta (in their tensors' types) and dS0
+    """Gradients of <dO, o> + <dST, ST> from gdr_fwd's inputs and what it
+    saved: a dict with dq, dk, dv, dg, dbeta (in their tensors' types) and dS0
     [B, Hv, dv, dk] float32 (None if return_dS0=False).  Packed rows that no
     sequence holds are not written, as in gdr_fwd."""
     torch, L = _ready()
     dev, desc, q, k, v, g, beta, cu = _gdr(q, k, v, g, beta, scale, cu_seqlens)
     shape = (desc.B, desc.Hv, desc.dv, desc.dk)
-    _check("saved", saved, (_slots(desc, cu),) + shape[1:], q.dtype)
+    _check("saved", saved, (int(L.kron_delta_gdr_saved_bytes(ctypes.byref(desc), int(cu is not None))),), torch.uint8)
     _check("dO", dO, v.shape, q.dtype)
     _same_device(dev, saved=saved, dO=dO)
     saved, dO, dST = _flat(saved), _flat(dO), _state("dST", dST, desc, dev)

@@ -715,23 +715,24 @@ KD_API size_t kron_delta_gdr_workspace_bytes(const kd_gdr_desc *desc, int packed
 
 /*
  * Forward: o, and when not NULL the last state ST (S0 for an empty sequence)
- * and hs, the states entering every 64 tokens in desc->dtype, which the backward
- * pass starts from: [slots, Hv, dv, dk] with slots = B ceil(T / 64), or
- * T / 64 + B for packed sequences.
+ * and saved, kron_delta_gdr_saved_bytes(desc, cu_seqlens != NULL) bytes that the
+ * backward pass starts from (the states entering every 64 tokens in
+ * desc->dtype, and what the 64 tokens' keys and gates come to).
  */
+KD_API size_t kron_delta_gdr_saved_bytes(const kd_gdr_desc *desc, int packed);
 KD_API kd_status kron_delta_gdr_fwd(const kd_gdr_desc *desc, const int32_t *cu_seqlens,
                          const void *q, const void *k, const void *v, const void *g, const void *beta,
-                         const float *S0, void *o, float *ST, void *hs,
+                         const float *S0, void *o, float *ST, void *saved,
                          void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Backward: gradients of <dO, o> + <dST, ST> (dST NULL = 0) with respect to q,
- * k, v, g, beta and S0 (dS0 NULL: not returned), from the inputs and the hs of
- * the forward call.
+ * k, v, g, beta and S0 (dS0 NULL: not returned), from the inputs and what the
+ * forward call saved.
  */
 KD_API kd_status kron_delta_gdr_bwd(const kd_gdr_desc *desc, const int32_t *cu_seqlens,
                          const void *q, const void *k, const void *v, const void *g, const void *beta,
-                         const void *hs, const void *dO, const float *dST,
+                         const void *saved, const void *dO, const float *dST,
                          void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dS0,
                          void *ws, size_t ws_bytes, void *stream);
 

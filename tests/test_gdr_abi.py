@@ -43,12 +43,12 @@ def test_limits_match_the_header():
 
 def test_forward_and_backward_checks(L):
     def fwd(d, wsb=1 << 40, **o):
-        p = dict(cu=None, q=P(0), k=P(1), v=P(2), g=P(3), beta=P(4), S0=P(5), o=P(6), ST=P(7), hs=P(8), ws=P(9))
+        p = dict(cu=None, q=P(0), k=P(1), v=P(2), g=P(3), beta=P(4), S0=P(5), o=P(6), ST=P(7), saved=P(8), ws=P(9))
         p.update(o)
         return L.kron_delta_gdr_fwd(ctypes.byref(d) if d else None, *p.values(), wsb, None)
 
     def bwd(d, wsb=1 << 40, **o):
-        p = dict(cu=None, q=P(0), k=P(1), v=P(2), g=P(3), beta=P(4), hs=P(5), dO=P(6), dST=P(7), dq=P(8), dk=P(9), dv=P(10),
+        p = dict(cu=None, q=P(0), k=P(1), v=P(2), g=P(3), beta=P(4), saved=P(5), dO=P(6), dST=P(7), dq=P(8), dk=P(9), dv=P(10),
                  dg=P(11), dbeta=P(12), dS0=P(13), ws=P(14))
         p.update(o)
         return L.kron_delta_gdr_bwd(ctypes.byref(d) if d else None, *p.values(), wsb, None)
@@ -64,21 +64,21 @@ def test_forward_and_backward_checks(L):
         assert f(desc(), ws=None) == WORKSPACE
         assert f(desc(), ws=P(2, 256)) == ALIAS
         assert f(desc(B=1, T=1 << 29, Hv=65535, Hk=65535)) == SHAPE      # launches past 32 bits of threads
-    for name in ("S0", "o", "ST", "hs", "ws"):
+    for name in ("S0", "o", "ST", "saved", "ws"):
         assert fwd(desc(), **{name: P(20, 8)}) == ALIGN, name
-    for name in ("hs", "dO", "dST", "dq", "dk", "dv", "dg", "dbeta", "dS0", "ws"):
+    for name in ("saved", "dO", "dST", "dq", "dk", "dv", "dg", "dbeta", "dS0", "ws"):
         assert bwd(desc(), **{name: P(20, 8)}) == ALIGN, name
-    for name in ("hs", "dO", "dq", "dk", "dv", "dg", "dbeta"):
+    for name in ("saved", "dO", "dq", "dk", "dv", "dg", "dbeta"):
         assert bwd(desc(), **{name: None}) == NULL, name
     assert fwd(desc(), o=None) == NULL
-    assert fwd(desc(), o=P(2)) == ALIAS and fwd(desc(), ST=P(5)) == ALIAS and fwd(desc(), hs=P(6)) == ALIAS
+    assert fwd(desc(), o=P(2)) == ALIAS and fwd(desc(), ST=P(5)) == ALIAS and fwd(desc(), saved=P(6)) == ALIAS
     assert bwd(desc(), dv=P(6)) == ALIAS and bwd(desc(), dq=P(0)) == ALIAS and bwd(desc(), dg=P(12)) == ALIAS
     for back, f in ((0, fwd), (1, bwd)):
         size = need(ctypes.byref(desc()), 0, back)
         assert size > 0 and f(desc(), wsb=size - 1) == WORKSPACE
     assert need(ctypes.byref(desc()), 0, 1) > need(ctypes.byref(desc()), 0, 0)
     assert fwd(desc(T=0), q=None, k=None, v=None, g=None, beta=None, o=None, ST=None, ws=None, wsb=0) == OK
-    assert bwd(desc(T=0), q=None, k=None, v=None, g=None, beta=None, hs=None, dO=None, dq=None, dk=None, dv=None, dg=None,
+    assert bwd(desc(T=0), q=None, k=None, v=None, g=None, beta=None, saved=None, dO=None, dq=None, dk=None, dv=None, dg=None,
                dbeta=None, dS0=None, ws=None, wsb=0) == OK
 
 
