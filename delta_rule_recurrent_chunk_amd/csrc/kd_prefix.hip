@@ -535,17 +535,22 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
     if (a.lse && lane == 0) a.lse[(int64_t)h * a.T + t] = none ? -INFINITY : 0.6931471805599453f * (M + __log2f(L));
 }
 
-// Splits.  Two workgroups of 128 rows fit a compute unit, where a tile takes
-// each of them 1.6 times as long as one alone; writing a part out and joining
-// it takes as long as 8 tiles.
+// Splits.  While every workgroup has a compute unit to itself, the prefix takes
+// as long as one part's tiles of 64 keys (2 us each), and a part more costs the
+// joining of its rows, little (3 rows of 16 heads over 4 key heads, 2000 keys, us
+// at 8, 16 and 32 parts: 12.2, 9.1, 7.2).  Beyond that two workgroups share a
+// compute unit, where a tile takes each of them 1.6 times as long as one alone,
+// and a part costs its rows' traffic, as long as 8 tiles (4800 such rows, 8192
+// keys, us at 1, 2, 8 and 24 parts: 241, 174, 194, 257).
 static int prefix_splits(int64_t items, int P)
 {
     const int tiles = (P + 63) / 64;
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= PREFIX_MOST && s <= (tiles + 3) / 4; ++s) {
+    for (int s = 1; s <= PREFIX_MOST && s <= tiles; ++s) {
         const int64_t n = items * s;
-        const double cost = (n <= 256 ? 1.0 : 1.6 * (double)((n + 511) / 512)) * ((tiles + s - 1) / s + 8);
+        const int part = (tiles + s - 1) / s;
+        const double cost = n <= 256 ? part + 2 + s / 32.0 : 1.6 * (double)((n + 511) / 512) * (part + 8);
         if (cost < least) least = cost, best = s;
     }
     return P == 0 ? 0 : best;
