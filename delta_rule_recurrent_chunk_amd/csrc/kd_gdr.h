@@ -387,18 +387,21 @@ struct GdrFetch {
     }
 };
 
+// Groups of 16 value columns of a pass's workgroup (what LDS holds).
+template <class E>
+__host__ __device__ constexpr int gdr_groups() { return sizeof(E) == 2 ? 4 : 2; }
+
 // What a pass reads of a chunk beside K and Q: the last PARTS parts of its record,
-// the gate factors, and 16 columns of V (or dO) a wave.  The workgroup's threads
-// load it to registers a chunk ahead and put it in LDS when the chunk before is
-// done.
-template <class E, int PARTS, int NW>
+// the gate factors, and C columns of V (or dO).  The workgroup's NT threads load
+// it to registers a chunk ahead and put it in LDS when the chunk before is done.
+template <class E, int PARTS, int C>
 struct GdrSide {
     static constexpr int REC = PARTS * gdr_part<E>();      // elements
     static constexpr int PIECES = (REC * (int)sizeof(E) + GDR_VEC * 4) / 16;
     static constexpr int SKIP = (gdr_parts<E>() - PARTS) * gdr_part<E>() * (int)sizeof(E);      // bytes
     E rec[REC];
     float vec[GDR_VEC];
-    E v[64 * 16 * NW];
+    E v[64 * C];
 };
 
 // Rows of a matrix at a wave-uniform address as a buffer: what lies past its
@@ -429,16 +432,16 @@ __device__ __forceinline__ void gdr_store(__amdgpu_buffer_rsrc_t r, int at, floa
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{x[4], x[5], x[6], x[7]}), r, at + 16, 0, 0);
 }
 
-template <class E, int PARTS, int NW>
+template <class E, int PARTS, int C, int NT>
 struct GdrSideAhead {
-    typedef SwaTile<E, 16 * NW> TV;
-    typedef GdrSide<E, PARTS, NW> Side;
-    static constexpr int NT = 64 * NW, N = (Side::PIECES + NT - 1) / NT, M = 64 * TV::CPR / NT, STEP = NT / TV::CPR;
+    typedef SwaTile<E, C> TV;
+    typedef GdrSide<E, PARTS, C> Side;
+    static constexpr int N = (Side::PIECES + NT - 1) / NT, M = 64 * TV::CPR / NT, STEP = NT / TV::CPR;
     floatx4 x[N], v[M];
     const E* vb;
     int64_t vs;
     int T, cols, at;
-    // rows of v: 16 NW columns from vb on, of which `cols` are there
+    // rows of v: C columns from vb on, of which `cols` are there
     __device__ __forceinline__ GdrSideAhead(const E* vb_, int64_t vs_, int cols_, int T_, int tid) : vb(vb_), vs(vs_), T(T_), cols(cols_) {
         const int c = tid % TV::CPR * TV::EPC;
         at = c < cols ? (int)((tid / TV::CPR * vs + c) * (int)sizeof(E)) : GDR_NONE;
@@ -451,7 +454,7 @@ struct GdrSideAhead {
     }
     // rows `row` .. of v
     __device__ __forceinline__ void load_v(int row) {
-        const auto r = gdr_buffer(vb + row * vs, ((min(T - row, 64) - 1) * vs + min(cols, 16 * NW)) * (int)sizeof(E));
+        const auto r = gdr_buffer(vb + row * vs, ((min(T - row, 64) - 1) * vs + min(cols, C)) * (int)sizeof(E));
 #pragma unroll
         for (int i = 0; i < M; ++i) v[i] = gdr_load(r, at + (at == GDR_NONE ? 0 : (int)(i * STEP * vs * (int)sizeof(E))));
     }

@@ -65,7 +65,7 @@ kd_status check_gdr(const kd_gdr_desc* d, bool packed, GdrSizes* s) {
     s->saved = s->rec + up256(s->slots * d->Hv * d->dv * d->dk * es);
     int run;
     if (!grid_fits((int64_t)s->slots * d->Hv, 64) || !grid_fits((int64_t)s->slots * d->Hk, 512) ||
-        !grid_fits(kd::gdr_pass_grid((int64_t)d->B * d->Hv * ((d->dv + 63) / 64), run), 256))
+        !grid_fits(kd::gdr_pass_grid((int64_t)d->B * d->Hv * ((d->dv + 31) / 32), run), 512))
         return KD_ERR_SHAPE;
     return KD_OK;
 }

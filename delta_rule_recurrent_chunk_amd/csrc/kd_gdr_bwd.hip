@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, PA = T::TWO ? 2 : 1;      // (P and its remainder in front of A)
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, gdr_parts<E>(), 4> side[NBUF];
+        GdrSide<E, gdr_parts<E>(), 64> side[NBUF];
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
     const int slices = (a.dv + 63) / 64;
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         kf(sm.k[buf], n * GDR_C, w);
         qf(sm.q[buf], n * GDR_C, w);
     };
-    GdrSideAhead<E, gdr_parts<E>(), 4> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    GdrSideAhead<E, gdr_parts<E>(), 64, 256> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
     auto load = [&](int n) {
         ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(), tid);
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
         }
         const E* kt = sm.k[buf];
         const E* qt = sm.q[buf];
-        const GdrSide<E, gdr_parts<E>(), 4>& sd = sm.side[buf];
+        const GdrSide<E, gdr_parts<E>(), 64>& sd = sm.side[buf];
         if (work) {
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;

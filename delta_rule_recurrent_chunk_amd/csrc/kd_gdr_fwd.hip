@@ -158,11 +158,12 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
         }
 }
 
-// The pass: NW waves of 16 value columns each.  K and Q of a chunk come by
-// loads straight to LDS, two chunks' worth; what else it needs through
-// registers.  Four waves (one a SIMD) where there are workgroups of them for
-// every compute unit at most, eight otherwise (bf16): two waves of a SIMD fill
-// each other's waits.
+// The pass, two waves of a SIMD for every 16 value columns.  The first has the
+// state in registers and makes what the next chunk waits for: K S, U, the state
+// that leaves.  The second makes what nothing waits for, a chunk later, from the
+// packed states and U that it finds in LDS: the outputs, all loads and stores.
+// K and Q come by loads straight to LDS, two chunks' worth (fp32 with 128 key
+// channels: one), A, V and the factors through its registers.
 //
 // Few heads and long sequences (gdr_plan): a sequence is cut into segments, all
 // of which pass at once.  A segment maps the state that enters it to S M + N.
@@ -170,19 +171,22 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // state) and for M (dk columns, from the identity and without values); a small
 // kernel chains them; then the pass runs from the states it found.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
-template <class E, int DK, int MODE, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
+template <class E, int DK, int MODE>
+__global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, NC0 = 16 * NW;      // (columns of a workgroup)
-    constexpr int PA = MODE == GDR_MAPS ? 0 : 1, PARTS = PA + (T::TWO ? 2 : 1);         // (P in front of A)
+    constexpr int CG = gdr_groups<E>(), NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1;      // (columns of a workgroup)
+    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr bool OUT = MODE != GDR_MAPS;
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, PARTS, NW> side[NBUF];
+        GdrSide<E, W, NC0> side[2];
+        E s[OUT ? CG * NK * W * 512 : 8], u[OUT ? CG * 2 * W * 512 : 8];      // fragments for the second wave
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int vslices = (a.dv + NC0 - 1) / NC0, slices = MODE == GDR_MAPS ? vslices + (a.dk + NC0 - 1) / NC0 : vslices;
+    const int cg = w % CG;
+    const int vslices = (a.dv + NC0 - 1) / NC0, slices = OUT ? vslices : vslices + (a.dk + NC0 - 1) / NC0;
     const int64_t id = blockIdx.x;
     int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;      // neighbours, which share keys, on one XCD
     if (item >= (int64_t)a.segs * a.Hv * slices) return;
@@ -193,81 +197,62 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
     if (!gdr_segment(a, slot, sg)) return;
     const GdrSeq s = sg.s;
     const int64_t seq = sg.seq;
-    const bool map = MODE == GDR_MAPS && slice >= vslices;
-    if (MODE == GDR_MAPS && (sg.last || (map && sg.j == 0))) return;
+    const bool map = !OUT && slice >= vslices;
+    if (!OUT && (sg.last || (map && sg.j == 0))) return;
     if (map) slice -= vslices;
     const int width = map ? a.dk : a.dv;
-    const int dv0 = slice * NC0 + 16 * w, col = min(dv0 + l16, width - 1);
+    const int dv0 = slice * NC0 + 16 * cg, col = min(dv0 + l16, width - 1);
     const bool work = dv0 < width;
-    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
-    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
-    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * NC0;
-    const E* ob = (const E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
-    const int NC = gdr_chunks(s.T), os = a.Hv * a.dv;
-    // where the lane's four values of row 16 t + l16, and its eight of a kept state, go
-    int oat[4], hat[NK];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) oat[t] = dv0 + 4 * g < a.dv ? ((16 * t + l16) * os + dv0 + 4 * g) * (int)sizeof(E) : GDR_NONE;
-#pragma unroll
-    for (int p = 0; p < NK; ++p)
-        hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
-
-    // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
-    // two packed tiles are a fragment in natural order), column: the lane's value
-    floatx4 S[2 * NK];
-    const int64_t at = (int64_t)col * a.dk + 8 * g, size = (int64_t)a.dv * a.dk;
-    const float* from = sg.j == 0 ? (a.S0 ? a.S0 + (seq * a.Hv + hv) * size : nullptr)
-                                  : MODE == GDR_MAPS ? nullptr : a.SI + ((int64_t)slot * a.Hv + hv) * size;
-#pragma unroll
-    for (int x = 0; x < 2 * NK; ++x) {
-        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (map) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[x][r] = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r == dv0 + l16 ? 1.f : 0.f;
-        } else if (from && 32 * (x / 2) + 8 * g < a.dk) {
-            S[x] = *reinterpret_cast<const floatx4*>(from + at + 32 * (x / 2) + 4 * (x & 1));
-        }
-    }
+    const int NC = __builtin_amdgcn_readfirstlane(gdr_chunks(s.T));
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 64 * NW) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 2 * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
-    const GdrFetch<E, DK, 64 * NW> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
-    auto fetch = [&](int n, int buf) {
-        kf(sm.k[buf], n * GDR_C, w);
-        if (MODE != GDR_MAPS) qf(sm.q[buf], n * GDR_C, w);
-    };
-    GdrSideAhead<E, PARTS, NW> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, tid);
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
-    auto load = [&](int n) {
-        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(), tid);
-        ahead.load_v(n * GDR_C);
+    const int64_t recs = a.Hv * gdr_rec_bytes<E>();
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    E* const xs = sm.s + cg * NK * W * 512 + lane * 8;
+    E* const xu = sm.u + cg * 2 * W * 512 + lane * 8;
+
+    // Barriers of a step: one in the middle (the second wave has what it needs of
+    // the chunk before), one at its end.
+    auto end = [&]() __attribute__((always_inline)) {
+        lds_barrier();
+        if (NBUF == 1) swa_landed();
     };
-    // The order is for one wave a SIMD, which has nothing else to run while it
-    // waits: fragments are read a stage before their products, loads for the
-    // next chunk are spread over the stages.
-    auto chunk = [&](int n, int buf) {
-        // chunk n is here; the other buffers are free
-        if (NBUF == 1) {
-            __syncthreads();
-            ahead.store(sm.side[0], tid);
-            fetch(n, 0);
+    if (w < CG) {
+        // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
+        // two packed tiles are a fragment in natural order), column: the lane's value
+        floatx4 S[2 * NK];
+        const int64_t at = (int64_t)col * a.dk + 8 * g, size = (int64_t)a.dv * a.dk;
+        const float* from = sg.j == 0 ? (a.S0 ? a.S0 + (seq * a.Hv + hv) * size : nullptr)
+                                      : OUT ? a.SI + ((int64_t)slot * a.Hv + hv) * size : nullptr;
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x) {
+            S[x] = zero;
+            if (map) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[x][r] = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r == dv0 + l16 ? 1.f : 0.f;
+            } else if (from && 32 * (x / 2) + 8 * g < a.dk) {
+                S[x] = *reinterpret_cast<const floatx4*>(from + at + 32 * (x / 2) + 4 * (x & 1));
+            }
         }
-        swa_landed();
-        const bool more = n + 1 < NC, early = NBUF == 2 && more;
-        const E* kt = sm.k[buf];
-        const E* qt = sm.q[buf];
-        const GdrSide<E, PARTS, NW>& sd = sm.side[buf];
-        if (work) {
+        auto chunk = [&](int buf, int par) __attribute__((always_inline)) {
+            if (!work) {
+                if (OUT) lds_barrier();
+                return end();
+            }
+            const E* kt = sm.k[buf];
+            const GdrSide<E, W, NC0>& sd = sm.side[par];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
-            Frag sh[NK], sl[NK], x[4], A[6], A2[T::TWO ? 6 : 1], f[2], f2[2];
-            floatx4 U[4], O[4], be[4], bb[4], v[4];
+            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
+            floatx4 U[4], be[4], bb[4], v[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 x[t] = T::template ld_row<DK>(kt, 16 * t + l16, 0, g);
-                U[t] = O[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+                U[t] = zero;
             }
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
@@ -276,72 +261,55 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
             }
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
-                Frag y[4];      // the next ones: keys, then queries
+                Frag y[4];      // the next ones
+                if (p + 1 < NK) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    y[t] = p + 1 < NK ? T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g)
-                           : MODE == GDR_MAPS ? x[t] : T::template ld_row<DK>(qt, 16 * t + l16, 0, g);
+                    for (int t = 0; t < 4; ++t) y[t] = T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        v[t] = T::template ld_acc<NC0>(sd.v, t, 16 * cg, lane);
+                        be[t] = factor(0, t);
+                        bb[t] = factor(1, t);
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sh[p], U[t]);
                 if (T::TWO) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sl[p], U[t]);
                 }
+                if (p + 1 < NK) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) x[t] = y[t];
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                v[t] = T::template ld_acc<NC0>(sd.v, t, 16 * w, lane);
-                be[t] = factor(0, t);
-                bb[t] = factor(1, t);
-            }
-            if (early) kf(sm.k[buf ^ 1], (n + 1) * GDR_C, w);
-            // Q S beside what follows from K S
-#pragma unroll
-            for (int p = 0; p < NK; ++p) {
-                Frag y[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) y[t] = x[t];
-                if (p + 1 < NK && MODE != GDR_MAPS) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p + 1, g);
-                }
-                if (p == 1) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) U[t][r] = be[t][r] * v[t][r] - bb[t][r] * U[t][r];
-                }
-                if (MODE == GDR_MAPS) continue;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], y[t], O[t]);
-                if (T::TWO) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], y[t], O[t]);
+                    for (int t = 0; t < 4; ++t) x[t] = y[t];
                 }
             }
 #pragma unroll
             for (int i = 0; i < 6; ++i) {
-                A[i] = T::ld(rec + PA * gdr_part<E>() + i * 512);
-                if (T::TWO) A2[T::TWO ? i : 0] = T::ld(rec + (PA + 1) * gdr_part<E>() + i * 512);
+                A[i] = T::ld(rec + i * 512);
+                if (T::TWO) A2[i] = T::ld(rec + gdr_part<E>() + i * 512);
             }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[t][r] = be[t][r] * v[t][r] - bb[t][r] * U[t][r];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
-            if (early && MODE != GDR_MAPS) qf(sm.q[buf ^ 1], (n + 1) * GDR_C, w);
-            Frag P[6], kc[2 * NK];
-            if (MODE != GDR_MAPS)
+            if (OUT) {
+                lds_barrier();
 #pragma unroll
-                for (int i = 0; i < 6; ++i) P[i] = T::ld(rec + i * 512);
-            if (NW == 4) {
-#pragma unroll
-                for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
+                for (int p = 0; p < NK; ++p) {
+                    T::st(xs + p * W * 512, sh[p]);
+                    if (T::TWO) T::st(xs + (p * W + W - 1) * 512, sl[p]);
+                }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) U[t] = zero;
             // (every round over the four tiles: products that do not wait for each other)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -351,29 +319,18 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
 #pragma unroll
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A[gdr_block(t, j)], f2[j], U[t]);
 #pragma unroll
-                    for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[T::TWO ? gdr_block(t, j) : 0], f[j], U[t]);
+                    for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[gdr_block(t, j)], f[j], U[t]);
                 }
             }
-            if (more) ahead.load(rec0 + (n + 1) * a.Hv * gdr_rec_bytes<E>(), tid);
             const float eC = sd.vec[256];
 #pragma unroll
             for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
-            if (MODE != GDR_MAPS) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] *= sd.vec[192 + 16 * t + l16];
+            if (OUT) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     f[j] = T::pack(U[2 * j], U[2 * j + 1]);
-                    f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                    for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f[j], P[gdr_block(t, j)], O[t]);
-                    if (T::TWO) {
-#pragma unroll
-                        for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f2[j], P[gdr_block(t, j)], O[t]);
-                    }
+                    T::st(xu + j * W * 512, f[j]);
+                    if (T::TWO) T::st(xu + (j * W + W - 1) * 512, T::rest(U[2 * j], U[2 * j + 1], f[j]));
                 }
             }
 #pragma unroll
@@ -383,66 +340,157 @@ __global__ __launch_bounds__(64 * NW, 1) void kd_gdr_pass_kernel(GdrArgs a, int 
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
-            if (more) ahead.load_v((n + 1) * GDR_C);
-            const auto ob0 = gdr_buffer(ob + (int64_t)n * GDR_C * os, ((int64_t)(min(s.T - n * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (NW != 4) {
-#pragma unroll
-                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, j, 32 * (y / 2) + 4 * (y & 1), lane);
-                }
 #pragma unroll
                 for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f[j], S[y]);
                 if (T::TWO) {
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
                 }
-                if (j == 0) {
-                    if (NW == 4)
+                if (j == 0)
 #pragma unroll
-                        for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
-                    if (MODE != GDR_MAPS)
+                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
+            }
+            end();
+        };
+        if (NC > 0) swa_landed();
+        for (int n = 0; n < NC; n += 2) {
+            chunk(0, 0);
+            if (n + 1 < NC) chunk(NBUF - 1, 1);
+        }
+        if (OUT && NC > 0) lds_barrier();
+        float* to = OUT ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
+                    : map ? a.M + ((int64_t)slot * a.Hv + hv) * a.dk * a.dk
+                          : a.SI + ((int64_t)(slot + 1) * a.Hv + hv) * size;
+        if (map) {      // transposed, for the chain
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) gdr_store(ob0, oat[t], O[t], (const E*)nullptr);
+            for (int x = 0; x < 2 * NK; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r;
+                    if (work && dv0 + l16 < width && c < a.dk) to[(int64_t)c * a.dk + dv0 + l16] = S[x][r];
+                }
+        } else if (to && work && dv0 + l16 < width) {
+#pragma unroll
+            for (int x = 0; x < 2 * NK; ++x)
+                if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(to + at + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+        }
+        return;
+    }
+
+    const int ltid = tid - NT;
+    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
+    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * NC0;
+    const E* ob = (const E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
+    const int os = a.Hv * a.dv;
+    // where the lane's four values of row 16 t + l16, and its eight of a kept state, go
+    int oat[4], hat[NK];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) oat[t] = dv0 + 4 * g < a.dv ? ((16 * t + l16) * os + dv0 + 4 * g) * (int)sizeof(E) : GDR_NONE;
+#pragma unroll
+    for (int p = 0; p < NK; ++p)
+        hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
+    const GdrFetch<E, DK, NT> kf(kb, a.ks[1], s.T, a.dk, ltid), qf(qb, a.qs[1], s.T, a.dk, ltid);
+    GdrSideAhead<E, W, NC0, NT> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, ltid);
+    Frag P[6];
+    float se[4];
+    // a step: chunk n on its way (none past the last), outputs of chunk n - 1
+    auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
+        if (n + 1 < NC) kf(sm.k[buf ^ (NBUF - 1)], (n + 1) * GDR_C, cg);
+        if (OUT && n < NC) qf(sm.q[buf], n * GDR_C, cg);
+    };
+    auto step = [&](int n, int buf, int par) __attribute__((always_inline)) {
+        const bool out = OUT && work && n > 0;
+        Frag sh[NK], sl[NK], f[2], f2[2];
+        if (out) {
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                sh[p] = T::ld(xs + p * W * 512);
+                if (T::TWO) sl[p] = T::ld(xs + (p * W + W - 1) * 512);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[j] = T::ld(xu + j * W * 512);
+                if (T::TWO) f2[j] = T::ld(xu + (j * W + W - 1) * 512);
+            }
+        }
+        if (NBUF == 2) fetch(n, buf);
+        const char* rec = rec0 + min(n + 1, NC - 1) * recs;
+        ahead.load(rec, ltid);
+        ahead.load_v(min(n + 1, NC - 1) * GDR_C);
+        if (OUT) lds_barrier();
+        floatx4 O[4] = {zero, zero, zero, zero};
+        if (out) {
+            const E* qt = sm.q[buf ^ (NBUF - 1)];
+#pragma unroll
+            for (int p = 0; p < NK; ++p) {
+                Frag x[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p, g);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], x[t], O[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], x[t], O[t]);
                 }
             }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) O[t] *= se[t];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f[j], P[gdr_block(t, j)], O[t]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) O[t] = T::mma(f2[j], P[gdr_block(t, j)], O[t]);
+                }
+            }
+        }
+        // the next chunk is here; the stores that follow need not have been written when it begins
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        ahead.store(sm.side[par ^ 1], ltid);
+        if (out) {
+            const int c = n - 1;
+            const auto o = gdr_buffer(ob + (int64_t)c * GDR_C * os, ((int64_t)(min(s.T - c * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) gdr_store(o, oat[t], O[t], (const E*)nullptr);
             if (MODE == GDR_SAVE) {
-                const auto hs = gdr_buffer((const E*)a.hs + ((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
+                const auto hs = gdr_buffer((const E*)a.hs + ((int64_t)(s.slot0 + c) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
 #pragma unroll
                 for (int p = 0; p < NK; ++p) gdr_store(hs, hat[p], sh[p]);
             }
-        } else if (more) {
-            if (early) fetch(n + 1, buf ^ 1);
-            load(n + 1);
         }
-        if (early) ahead.store(sm.side[buf ^ 1], tid);
+        if (OUT && n < NC) {      // P and the factors of this chunk, for the next step
+            const char* r = rec0 + n * recs;
+            const E* ps = (const E*)r + (T::TWO ? gdr_part<E>() : 0) + lane * 8;
+            const float* vec = (const float*)(r + gdr_parts<E>() * gdr_part<E>() * (int)sizeof(E)) + 192 + l16;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) P[i] = T::ld(ps + i * 512);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) se[t] = vec[16 * t];
+        }
     };
     if (NC > 0) {
-        load(0);
-        if (NBUF == 2) {
-            fetch(0, 0);
-            ahead.store(sm.side[0], tid);
+        ahead.load(rec0, ltid);
+        ahead.load_v(0);
+        kf(sm.k[0], 0, cg);
+        ahead.store(sm.side[0], ltid);
+        swa_landed();
+    }
+    auto turn = [&](int n, int buf, int par) __attribute__((always_inline)) {
+        step(n, buf, par);
+        if (n == NC) return;
+        lds_barrier();
+        if (NBUF == 1) {
+            fetch(n, 0);
+            swa_landed();
         }
-    }
-    for (int n = 0; n < NC; n += 2) {
-        chunk(n, 0);
-        if (n + 1 < NC) chunk(n + 1, NBUF - 1);
-    }
-    float* to = MODE != GDR_MAPS ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
-                : map            ? a.M + ((int64_t)slot * a.Hv + hv) * a.dk * a.dk
-                                 : a.SI + ((int64_t)(slot + 1) * a.Hv + hv) * size;
-    if (map) {      // transposed, for the chain
-#pragma unroll
-        for (int x = 0; x < 2 * NK; ++x)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = 32 * (x / 2) + 8 * g + 4 * (x & 1) + r;
-                if (work && dv0 + l16 < width && c < a.dk) to[(int64_t)c * a.dk + dv0 + l16] = S[x][r];
-            }
-    } else if (to && work && dv0 + l16 < width) {
-#pragma unroll
-        for (int x = 0; x < 2 * NK; ++x)
-            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(to + at + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+    };
+    for (int n = 0; n < (OUT && NC > 0 ? NC + 1 : NC); n += 2) {
+        turn(n, 0, 0);
+        if (n + 1 < (OUT ? NC + 1 : NC)) turn(n + 1, NBUF - 1, 1);
     }
 }
 
@@ -525,28 +573,13 @@ static hipError_t gdr_prep(const GdrArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Columns of a pass's workgroup: see the kernel.
-template <class E>
-static int gdr_waves(int64_t heads, int columns) { return sizeof(E) == 2 && heads * ((columns + 63) / 64) > 256 && columns > 64 ? 8 : 4; }
-
-template <class E, int DK, int MODE, int NW>
-static void gdr_pass(const GdrArgs& a, hipStream_t st)
-{
-    constexpr int C = 16 * NW;
-    const int64_t heads = (int64_t)a.segs * a.Hv;
-    int run;
-    const int64_t grid = gdr_pass_grid(heads * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
-    kd_gdr_pass_kernel<E, DK, MODE, NW><<<(unsigned)grid, 64 * NW, 0, st>>>(a, run);
-}
 template <class E, int DK, int MODE>
 static void gdr_pass(const GdrArgs& a, hipStream_t st)
 {
-    const int64_t heads = (int64_t)a.segs * a.Hv;
-    if constexpr (sizeof(E) == 2) {
-        if (MODE == GDR_MAPS ? gdr_waves<E>(2 * heads, min(a.dv, a.dk)) == 8 : gdr_waves<E>(heads, a.dv) == 8)
-            return gdr_pass<E, DK, MODE, 8>(a, st);
-    }
-    gdr_pass<E, DK, MODE, 4>(a, st);
+    constexpr int CG = gdr_groups<E>(), C = 16 * CG;
+    int run;
+    const int64_t grid = gdr_pass_grid((int64_t)a.segs * a.Hv * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
+    kd_gdr_pass_kernel<E, DK, MODE><<<(unsigned)grid, 128 * CG, 0, st>>>(a, run);
 }
 template <class E, int DK>
 static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
