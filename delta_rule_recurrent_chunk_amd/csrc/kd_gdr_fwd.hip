@@ -181,7 +181,8 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     constexpr bool OUT = MODE != GDR_MAPS;
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, W, NC0> side[2];
+        GdrSide<E, W, NC0> side;
+        E p[2][OUT ? gdr_part<E>() : 8];
         E s[OUT ? CG * NK * W * 512 : 8], u[OUT ? CG * 2 * W * 512 : 8];      // fragments for the second wave
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
@@ -216,7 +217,8 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     E* const xu = sm.u + cg * 2 * W * 512 + lane * 8;
 
     // Barriers of a step: one in the middle (the second wave has what it needs of
-    // the chunk before), one at its end.
+    // the chunk before, the first what it needs of A, V and the factors), one at
+    // its end.
     auto end = [&]() __attribute__((always_inline)) {
         lds_barrier();
         if (NBUF == 1) swa_landed();
@@ -238,17 +240,17 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 S[x] = *reinterpret_cast<const floatx4*>(from + at + 32 * (x / 2) + 4 * (x & 1));
             }
         }
-        auto chunk = [&](int buf, int par) __attribute__((always_inline)) {
+        auto chunk = [&](int buf) __attribute__((always_inline)) {
             if (!work) {
-                if (OUT) lds_barrier();
+                lds_barrier();
                 return end();
             }
             const E* kt = sm.k[buf];
-            const GdrSide<E, W, NC0>& sd = sm.side[par];
+            const GdrSide<E, W, NC0>& sd = sm.side;
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
-            floatx4 U[4], be[4], bb[4], v[4];
+            floatx4 U[4], be[4], bb[4], bc[4], v[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 x[t] = T::template ld_row<DK>(kt, 16 * t + l16, 0, g);
@@ -271,6 +273,7 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                         v[t] = T::template ld_acc<NC0>(sd.v, t, 16 * cg, lane);
                         be[t] = factor(0, t);
                         bb[t] = factor(1, t);
+                        bc[t] = factor(2, t);
                     }
                 }
 #pragma unroll
@@ -298,8 +301,9 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
+            const float eC = sd.vec[256];
+            lds_barrier();
             if (OUT) {
-                lds_barrier();
 #pragma unroll
                 for (int p = 0; p < NK; ++p) {
                     T::st(xs + p * W * 512, sh[p]);
@@ -322,7 +326,6 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[gdr_block(t, j)], f[j], U[t]);
                 }
             }
-            const float eC = sd.vec[256];
 #pragma unroll
             for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
             if (OUT) {
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] *= factor(2, t);
+            for (int t = 0; t < 4; ++t) U[t] *= bc[t];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
@@ -356,8 +359,8 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
         };
         if (NC > 0) swa_landed();
         for (int n = 0; n < NC; n += 2) {
-            chunk(0, 0);
-            if (n + 1 < NC) chunk(NBUF - 1, 1);
+            chunk(0);
+            if (n + 1 < NC) chunk(NBUF - 1);
         }
         if (OUT && NC > 0) lds_barrier();
         float* to = OUT ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
@@ -394,7 +397,25 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
         hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
     const GdrFetch<E, DK, NT> kf(kb, a.ks[1], s.T, a.dk, ltid), qf(qb, a.qs[1], s.T, a.dk, ltid);
     GdrSideAhead<E, W, NC0, NT> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, ltid);
-    Frag P[6];
+    // P of the chunk whose outputs come next goes through LDS like A, its pieces are
+    constexpr int PP = gdr_part<E>() * (int)sizeof(E) / 16, NP = (PP + NT - 1) / NT;
+    floatx4 px[NP];
+    auto load = [&](int n) __attribute__((always_inline)) {
+        const char* r = rec0 + min(n, NC - 1) * recs;
+        ahead.load(r, ltid);
+        ahead.load_v(min(n, NC - 1) * GDR_C);
+        const auto ps = gdr_buffer(r + (T::TWO ? PP * 16 : 0), PP * 16);
+        if (OUT)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) px[i] = gdr_load(ps, (i * NT + ltid) * 16);
+    };
+    auto store = [&](int par) __attribute__((always_inline)) {
+        ahead.store(sm.side, ltid);
+        if (OUT)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p[par])[i * NT + ltid] = px[i];
+    };
     float se[4];
     // a step: chunk n on its way (none past the last), outputs of chunk n - 1
     auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
@@ -403,7 +424,10 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     };
     auto step = [&](int n, int buf, int par) __attribute__((always_inline)) {
         const bool out = OUT && work && n > 0;
-        Frag sh[NK], sl[NK], f[2], f2[2];
+        Frag sh[NK], sl[NK], f[2], f2[2], P[6];
+        float sn[4];      // the factors of this chunk, for the next step
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sn[t] = OUT ? sm.side.vec[192 + 16 * t + l16] : 0.f;
         if (out) {
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
@@ -417,25 +441,30 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
             }
         }
         if (NBUF == 2) fetch(n, buf);
-        const char* rec = rec0 + min(n + 1, NC - 1) * recs;
-        ahead.load(rec, ltid);
-        ahead.load_v(min(n + 1, NC - 1) * GDR_C);
-        if (OUT) lds_barrier();
+        load(n + 1);
         floatx4 O[4] = {zero, zero, zero, zero};
-        if (out) {
-            const E* qt = sm.q[buf ^ (NBUF - 1)];
+        const E* qt = sm.q[buf ^ (NBUF - 1)];
+        auto qs = [&](int p) __attribute__((always_inline)) {
+            Frag x[4];
 #pragma unroll
-            for (int p = 0; p < NK; ++p) {
-                Frag x[4];
+            for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p, g);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(qt, 16 * t + l16, p, g);
+            for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], x[t], O[t]);
+            if (T::TWO) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) O[t] = T::mma(sh[p], x[t], O[t]);
-                if (T::TWO) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], x[t], O[t]);
-                }
+                for (int t = 0; t < 4; ++t) O[t] = T::mma(sl[p], x[t], O[t]);
             }
+        };
+        if (out) {
+#pragma unroll
+            for (int p = 0; p < NK / 2; ++p) qs(p);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) P[i] = T::ld(sm.p[par ^ 1] + i * 512 + lane * 8);      // (its place is written again after the barrier)
+        }
+        lds_barrier();
+        if (out) {
+#pragma unroll
+            for (int p = NK / 2; p < NK; ++p) qs(p);
 #pragma unroll
             for (int t = 0; t < 4; ++t) O[t] *= se[t];
 #pragma unroll
@@ -450,7 +479,7 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
         }
         // the next chunk is here; the stores that follow need not have been written when it begins
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        ahead.store(sm.side[par ^ 1], ltid);
+        store(par ^ 1);
         if (out) {
             const int c = n - 1;
             const auto o = gdr_buffer(ob + (int64_t)c * GDR_C * os, ((int64_t)(min(s.T - c * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
@@ -462,21 +491,13 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 for (int p = 0; p < NK; ++p) gdr_store(hs, hat[p], sh[p]);
             }
         }
-        if (OUT && n < NC) {      // P and the factors of this chunk, for the next step
-            const char* r = rec0 + n * recs;
-            const E* ps = (const E*)r + (T::TWO ? gdr_part<E>() : 0) + lane * 8;
-            const float* vec = (const float*)(r + gdr_parts<E>() * gdr_part<E>() * (int)sizeof(E)) + 192 + l16;
 #pragma unroll
-            for (int i = 0; i < 6; ++i) P[i] = T::ld(ps + i * 512);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) se[t] = vec[16 * t];
-        }
+        for (int t = 0; t < 4; ++t) se[t] = sn[t];
     };
     if (NC > 0) {
-        ahead.load(rec0, ltid);
-        ahead.load_v(0);
+        load(0);
         kf(sm.k[0], 0, cg);
-        ahead.store(sm.side[0], ltid);
+        store(0);
         swa_landed();
     }
     auto turn = [&](int n, int buf, int par) __attribute__((always_inline)) {
