@@ -169,10 +169,12 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // of which pass at once.  A segment maps the state that enters it to S M + N.
 // GDR_MAPS passes over segments without their outputs, for N (from a zero
 // state) and for M (dk columns, from the identity and without values); a small
-// kernel chains them; then the pass runs from the states it found.
+// kernel chains them; then the pass runs from the states it found.  Without
+// outputs there are first waves alone, which load for themselves, in two
+// workgroups a compute unit.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
 template <class E, int DK, int MODE>
-__global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
+__global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * gdr_groups<E>(), sizeof(E) == 2 ? 2 : 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
@@ -180,8 +182,8 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
     constexpr bool OUT = MODE != GDR_MAPS;
     __shared__ __align__(16) struct {
-        E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, W, NC0> side;
+        E k[NBUF][64 * DK], q[OUT ? NBUF : 1][OUT ? 64 * DK : 8];
+        GdrSide<E, W, NC0> side[OUT ? 1 : 2];
         E p[2][OUT ? gdr_part<E>() : 8];
         E s[OUT ? CG * NK * W * 512 : 8], u[OUT ? CG * 2 * W * 512 : 8];      // fragments for the second wave
     } sm;
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     const int NC = __builtin_amdgcn_readfirstlane(gdr_chunks(s.T));
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 2 * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)(NBUF * (OUT ? 2 : 1) * 64 * DK * sizeof(E) / 16); i += (OUT ? 2 : 1) * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
@@ -216,14 +218,27 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
     E* const xs = sm.s + cg * NK * W * 512 + lane * 8;
     E* const xu = sm.u + cg * 2 * W * 512 + lane * 8;
 
+    const int ltid = tid % NT;
+    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
+    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * NC0;
+    const GdrFetch<E, DK, NT> kf(kb, a.ks[1], s.T, a.dk, ltid);
+    GdrSideAhead<E, W, NC0, NT> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, ltid);
+
     // Barriers of a step: one in the middle (the second wave has what it needs of
     // the chunk before, the first what it needs of A, V and the factors), one at
     // its end.
-    auto end = [&]() __attribute__((always_inline)) {
+    auto end = [&](int n) __attribute__((always_inline)) {
         lds_barrier();
-        if (NBUF == 1) swa_landed();
+        if (NBUF == 1) {
+            if (!OUT && n + 1 < NC) kf(sm.k[0], (n + 1) * GDR_C, cg);
+            swa_landed();
+        }
     };
-    if (w < CG) {
+    auto load_side = [&](int n) __attribute__((always_inline)) {
+        ahead.load(rec0 + min(n, NC - 1) * recs, ltid);
+        ahead.load_v(min(n, NC - 1) * GDR_C);
+    };
+    if (!OUT || w < CG) {
         // S^T: tile 2 p + h, register r: key channel 32 p + 8 g + 4 h + r (so that
         // two packed tiles are a fragment in natural order), column: the lane's value
         floatx4 S[2 * NK];
@@ -240,13 +255,22 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 S[x] = *reinterpret_cast<const floatx4*>(from + at + 32 * (x / 2) + 4 * (x & 1));
             }
         }
-        auto chunk = [&](int buf) __attribute__((always_inline)) {
+        auto chunk = [&](int n, int buf, int par) __attribute__((always_inline)) {
+            if (!OUT) {
+                if (NBUF == 2 && n + 1 < NC) kf(sm.k[buf ^ 1], (n + 1) * GDR_C, cg);
+                load_side(n + 1);
+            }
             if (!work) {
-                lds_barrier();
-                return end();
+                if (OUT) {
+                    lds_barrier();
+                } else {
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    ahead.store(sm.side[par ^ 1], ltid);
+                }
+                return end(n);
             }
             const E* kt = sm.k[buf];
-            const GdrSide<E, W, NC0>& sd = sm.side;
+            const GdrSide<E, W, NC0>& sd = sm.side[OUT ? 0 : par];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
             Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
@@ -302,8 +326,8 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
             const float eC = sd.vec[256];
-            lds_barrier();
             if (OUT) {
+                lds_barrier();
 #pragma unroll
                 for (int p = 0; p < NK; ++p) {
                     T::st(xs + p * W * 512, sh[p]);
@@ -355,12 +379,23 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
             }
-            end();
+            if (!OUT) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                ahead.store(sm.side[par ^ 1], ltid);
+            }
+            end(n);
         };
-        if (NC > 0) swa_landed();
+        if (NC > 0) {
+            if (!OUT) {
+                load_side(0);
+                kf(sm.k[0], 0, cg);
+                ahead.store(sm.side[0], ltid);
+            }
+            swa_landed();
+        }
         for (int n = 0; n < NC; n += 2) {
-            chunk(0);
-            if (n + 1 < NC) chunk(NBUF - 1);
+            chunk(n, 0, 0);
+            if (n + 1 < NC) chunk(n + 1, NBUF - 1, 1);
         }
         if (OUT && NC > 0) lds_barrier();
         float* to = OUT ? (a.ST && sg.last ? a.ST + (seq * a.Hv + hv) * size : nullptr)
@@ -382,10 +417,7 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
         return;
     }
 
-    const int ltid = tid - NT;
-    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
     const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
-    const E* vb = (const E*)a.v + s.b * a.vs[0] + (int64_t)s.row0 * a.vs[1] + hv * a.vs[2] + slice * NC0;
     const E* ob = (const E*)a.o + ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
     const int os = a.Hv * a.dv;
     // where the lane's four values of row 16 t + l16, and its eight of a kept state, go
@@ -395,39 +427,35 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
 #pragma unroll
     for (int p = 0; p < NK; ++p)
         hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
-    const GdrFetch<E, DK, NT> kf(kb, a.ks[1], s.T, a.dk, ltid), qf(qb, a.qs[1], s.T, a.dk, ltid);
-    GdrSideAhead<E, W, NC0, NT> ahead(vb, a.vs[1], map ? 0 : a.dv - slice * NC0, s.T, ltid);
+    const GdrFetch<E, DK, NT> qf(qb, a.qs[1], s.T, a.dk, ltid);
     // P of the chunk whose outputs come next goes through LDS like A, its pieces are
     constexpr int PP = gdr_part<E>() * (int)sizeof(E) / 16, NP = (PP + NT - 1) / NT;
     floatx4 px[NP];
     auto load = [&](int n) __attribute__((always_inline)) {
         const char* r = rec0 + min(n, NC - 1) * recs;
-        ahead.load(r, ltid);
-        ahead.load_v(min(n, NC - 1) * GDR_C);
+        load_side(n);
         const auto ps = gdr_buffer(r + (T::TWO ? PP * 16 : 0), PP * 16);
-        if (OUT)
 #pragma unroll
-            for (int i = 0; i < NP; ++i) px[i] = gdr_load(ps, (i * NT + ltid) * 16);
+        for (int i = 0; i < NP; ++i) px[i] = gdr_load(ps, (i * NT + ltid) * 16);
     };
     auto store = [&](int par) __attribute__((always_inline)) {
-        ahead.store(sm.side, ltid);
-        if (OUT)
+        ahead.store(sm.side[0], ltid);
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p[par])[i * NT + ltid] = px[i];
+        for (int i = 0; i < NP; ++i)
+            if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p[OUT ? par : 0])[OUT ? i * NT + ltid : 0] = px[i];
     };
     float se[4];
     // a step: chunk n on its way (none past the last), outputs of chunk n - 1
     auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
         if (n + 1 < NC) kf(sm.k[buf ^ (NBUF - 1)], (n + 1) * GDR_C, cg);
-        if (OUT && n < NC) qf(sm.q[buf], n * GDR_C, cg);
+        if (n < NC) qf(sm.q[buf], n * GDR_C, cg);
     };
     auto step = [&](int n, int buf, int par) __attribute__((always_inline)) {
-        const bool out = OUT && work && n > 0;
+        const bool out = work && n > 0;
         Frag sh[NK], sl[NK], f[2], f2[2], P[6];
         float sn[4];      // the factors of this chunk, for the next step
 #pragma unroll
-        for (int t = 0; t < 4; ++t) sn[t] = OUT ? sm.side.vec[192 + 16 * t + l16] : 0.f;
+        for (int t = 0; t < 4; ++t) sn[t] = sm.side[0].vec[192 + 16 * t + l16];
         if (out) {
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
@@ -509,9 +537,9 @@ __global__ __launch_bounds__(128 * gdr_groups<E>(), 1) void kd_gdr_pass_kernel(G
             swa_landed();
         }
     };
-    for (int n = 0; n < (OUT && NC > 0 ? NC + 1 : NC); n += 2) {
+    for (int n = 0; n < (NC > 0 ? NC + 1 : 0); n += 2) {
         turn(n, 0, 0);
-        if (n + 1 < (OUT ? NC + 1 : NC)) turn(n + 1, NBUF - 1, 1);
+        if (n < NC) turn(n + 1, NBUF - 1, 1);
     }
 }
 
@@ -538,40 +566,44 @@ __global__ __launch_bounds__(256, 1) void kd_gdr_chain_kernel(GdrArgs a)
     auto state = [&](int j, int x) {
         return a.SI + ((int64_t)(slot + j) * a.Hv + hv) * size + (int64_t)v * a.dk + channel(x, g);
     };
-    floatx4 S[NT], N[NY], m[NY][NT];
-    auto load = [&](int j) {
+    floatx4 S[NT], N[2][NY], m[2][NY][NT];
+    auto load = [&](int j, int b) __attribute__((always_inline)) {
         const float* M = a.M + ((int64_t)(slot + j) * a.Hv + hv) * a.dk * a.dk;
 #pragma unroll
         for (int y = 0; y < NY; ++y) {
             const int own = NY * w + y, c = channel(own, l16 >> 2) + (l16 & 3);      // the operand's row, as the state's are laid out
-            N[y] = channel(own, g) < a.dk ? *reinterpret_cast<const floatx4*>(state(j + 1, own)) : zero;
+            N[b][y] = channel(own, g) < a.dk ? *reinterpret_cast<const floatx4*>(state(j + 1, own)) : zero;
 #pragma unroll
             for (int x = 0; x < NT; ++x)
-                m[y][x] = c < a.dk && channel(x, g) < a.dk ? *reinterpret_cast<const floatx4*>(M + (int64_t)c * a.dk + channel(x, g)) : zero;
+                m[b][y][x] = c < a.dk && channel(x, g) < a.dk ? *reinterpret_cast<const floatx4*>(M + (int64_t)c * a.dk + channel(x, g)) : zero;
         }
     };
 #pragma unroll
     for (int x = 0; x < NT; ++x) S[x] = channel(x, g) < a.dk ? *reinterpret_cast<const floatx4*>(state(1, x)) : zero;
-    load(1);
-    for (int j = 1; j + 1 < n; ++j) {
+    load(1, 0);
+    auto turn = [&](int j, int b) __attribute__((always_inline)) {
+        if (j + 2 < n) load(j + 1, b ^ 1);
         floatx4 R[NY];
 #pragma unroll
-        for (int y = 0; y < NY; ++y) R[y] = N[y];
+        for (int y = 0; y < NY; ++y) R[y] = N[b][y];
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int y = 0; y < NY; ++y) R[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[y][x][r], S[x][r], R[y], 0, 0, 0);
-        if (j + 2 < n) load(j + 1);
+                for (int y = 0; y < NY; ++y) R[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[b][y][x][r], S[x][r], R[y], 0, 0, 0);
 #pragma unroll
         for (int y = 0; y < NY; ++y) {
-            tile[j & 1][NY * w + y][lane] = R[y];
+            tile[b][NY * w + y][lane] = R[y];
             if (channel(NY * w + y, g) < a.dk && blockIdx.x * 16 + l16 < a.dv) *reinterpret_cast<floatx4*>(state(j + 1, NY * w + y)) = R[y];
         }
         lds_barrier();
 #pragma unroll
-        for (int x = 0; x < NT; ++x) S[x] = tile[j & 1][x][lane];
+        for (int x = 0; x < NT; ++x) S[x] = tile[b][x][lane];
+    };
+    for (int j = 1; j + 1 < n; j += 2) {
+        turn(j, 0);
+        if (j + 2 < n) turn(j + 1, 1);
     }
 }
 
@@ -600,7 +632,7 @@ static void gdr_pass(const GdrArgs& a, hipStream_t st)
     constexpr int CG = gdr_groups<E>(), C = 16 * CG;
     int run;
     const int64_t grid = gdr_pass_grid((int64_t)a.segs * a.Hv * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
-    kd_gdr_pass_kernel<E, DK, MODE><<<(unsigned)grid, 128 * CG, 0, st>>>(a, run);
+    kd_gdr_pass_kernel<E, DK, MODE><<<(unsigned)grid, (MODE == GDR_MAPS ? 64 : 128) * CG, 0, st>>>(a, run);
 }
 template <class E, int DK>
 static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
