@@ -387,9 +387,10 @@ struct GdrFetch {
     }
 };
 
-// Groups of 16 value columns of a pass's workgroup (what LDS holds).
-template <class E>
-__host__ __device__ constexpr int gdr_groups() { return sizeof(E) == 2 ? 4 : 2; }
+// Two groups of 16 value columns a workgroup instead of four, while that leaves
+// no more workgroups than compute units: both waves of a group have a SIMD for
+// themselves then (64 heads' sequences of 2048 tokens, 128 x 128: 77 us for 98).
+__host__ __forceinline__ bool gdr_narrow(const GdrArgs& a, int segs) { return (int64_t)segs * a.Hv * ((a.dv + 63) / 64) <= 128; }
 
 // What a pass reads of a chunk beside K and Q: the last PARTS parts of its record,
 // the gate factors, and C columns of V (or dO).  The workgroup's NT threads load

@@ -158,12 +158,14 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
         }
 }
 
-// The pass, two waves of a SIMD for every 16 value columns.  The first has the
+// The pass, two waves for every 16 value columns.  The first has the
 // state in registers and makes what the next chunk waits for: K S, U, the state
 // that leaves.  The second makes what nothing waits for, a chunk later, from the
 // packed states and U that it finds in LDS: the outputs, all loads and stores.
 // K and Q come by loads straight to LDS, two chunks' worth (fp32 with 128 key
 // channels: one), A, V and the factors through its registers.
+// A workgroup has CG groups of 16 columns: four, two waves to a SIMD, or two with
+// a SIMD for each wave (gdr_narrow; fp32, which needs the LDS).
 //
 // Few heads and long sequences (gdr_plan): a sequence is cut into segments, all
 // of which pass at once.  A segment maps the state that enters it to S M + N.
@@ -173,12 +175,12 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // outputs there are first waves alone, which load for themselves, in two
 // workgroups a compute unit.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
-template <class E, int DK, int MODE>
-__global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * gdr_groups<E>(), sizeof(E) == 2 ? 2 : 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
+template <class E, int DK, int MODE, int CG>
+__global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
-    constexpr int CG = gdr_groups<E>(), NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1;      // (columns of a workgroup)
+    constexpr int NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1;      // (columns of a workgroup)
     constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
     constexpr bool OUT = MODE != GDR_MAPS;
     __shared__ __align__(16) struct {
@@ -626,13 +628,25 @@ static hipError_t gdr_prep(const GdrArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
+template <class E, int DK, int MODE, int CG>
+static void gdr_pass(const GdrArgs& a, hipStream_t st)
+{
+    constexpr int C = 16 * CG;
+    int run;
+    const int64_t grid = gdr_pass_grid((int64_t)a.segs * a.Hv * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
+    kd_gdr_pass_kernel<E, DK, MODE, CG><<<(unsigned)grid, (MODE == GDR_MAPS ? 64 : 128) * CG, 0, st>>>(a, run);
+}
 template <class E, int DK, int MODE>
 static void gdr_pass(const GdrArgs& a, hipStream_t st)
 {
-    constexpr int CG = gdr_groups<E>(), C = 16 * CG;
-    int run;
-    const int64_t grid = gdr_pass_grid((int64_t)a.segs * a.Hv * ((a.dv + C - 1) / C + (MODE == GDR_MAPS ? (a.dk + C - 1) / C : 0)), run);
-    kd_gdr_pass_kernel<E, DK, MODE><<<(unsigned)grid, (MODE == GDR_MAPS ? 64 : 128) * CG, 0, st>>>(a, run);
+    if constexpr (sizeof(E) == 4) {
+        gdr_pass<E, DK, MODE, 2>(a, st);
+    } else if constexpr (MODE == GDR_MAPS) {
+        gdr_pass<E, DK, MODE, 4>(a, st);
+    } else {
+        if (gdr_narrow(a, a.segs)) gdr_pass<E, DK, MODE, 2>(a, st);
+        else gdr_pass<E, DK, MODE, 4>(a, st);
+    }
 }
 template <class E, int DK>
 static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
@@ -652,13 +666,13 @@ static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
 // chunk, however few workgroups there are; the maps cost about as much work
 // again as the pass itself.  So sequences are cut where they leave three
 // quarters of the 256 compute units idle, into segments of at least 8 chunks,
-// as many as make 512 workgroups of four waves.  Packed sequences are cut by
+// as many as make 256 workgroups (32768 tokens of 16 heads: 553 us; 512: 578).  Packed sequences are cut by
 // what their average length would be.
 void gdr_plan(GdrArgs& a, bool packed)
 {
     const int64_t wgs = (int64_t)a.B * a.Hv * ((a.dv + 63) / 64);
     const int NC = packed ? (a.T / a.B + GDR_C - 1) / GDR_C : (a.T + GDR_C - 1) / GDR_C;
-    int n = wgs * 4 <= 256 ? (int)(512 / wgs) : 1;
+    int n = wgs * 4 <= 256 ? (int)(256 / wgs) : 1;
     n = n < NC / 8 ? n : NC / 8;
     if (n < 3) n = 1;
     a.seg = n > 1 ? (NC + n - 1) / n : 1 << 24;
