@@ -215,6 +215,15 @@ struct GdrT<__bf16> {
                                                         (__attribute__((address_space(3))) v4s*)(tile + TL::off(r, c / 8) + c % 8)));
         return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
     }
+    // columns 16 t + l16 of rows 4 g .. + 3 of a tile with rows of S elements
+    template <int S>
+    static __device__ __forceinline__ floatx4 ld_t4(const __bf16* tile, int t, int lane) {
+        typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
+        const int l = lane & 15;
+        const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                        (__attribute__((address_space(3))) v4s*)(tile + (4 * (lane >> 4) + (l >> 2)) * S + 16 * t + 4 * (l & 3))));
+        return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+    }
     // Block (i, j) of a transpose from the blocks of the matrix: lane's s = 16 i + l16, r = 32 j +
     // 16 h + 4 g + e.  Row r's four columns 4 c .. of block (r / 16, i / 2) are
     // the half i % 2 of its lane r % 16 + 16 c.
@@ -284,6 +293,13 @@ struct GdrT<float> {
         floatx4 x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = tile[TL::off(r + e, c / 4) + c % 4];
+        return x;
+    }
+    template <int S>
+    static __device__ __forceinline__ floatx4 ld_t4(const float* tile, int t, int lane) {
+        floatx4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = tile[(4 * (lane >> 4) + e) * S + 16 * t + (lane & 15)];
         return x;
     }
     static __device__ __forceinline__ Frag ld_at(const float* rec, int i, int j, int lane) {

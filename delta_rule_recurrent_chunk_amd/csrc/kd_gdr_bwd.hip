@@ -4,8 +4,7 @@
 // gradient of the one leaving it and the notation of kd_gdr.h:
 //     dU  = P^T dO + e^(bC - b) K dS_C^T,   X = A^T dU,   dV = beta X
 //     dS0 = e^bC dS_C + (scale e^b dO)^T Q - (beta e^b X)^T K
-// is the pass over the chunks, backwards, as the forward's (16 value columns a
-// wave, the gradient of the state in registers); and per chunk
+// is the pass over the chunks, backwards, as the forward's; and per chunk
 //     W = V - e^b K S0^T,  U = A beta W
 //     E = Gam (scale dO U^T) (s <= r),   F = -beta Gam (X U^T) (s < r)
 //     dQ = E K + scale e^b dO S0
@@ -21,221 +20,334 @@ namespace kd {
 
 int64_t gdr_pass_grid(int64_t items, int& run);
 
-template <class E, int DK>
-__global__ __launch_bounds__(256, 1) void kd_gdr_back_kernel(GdrArgs a, int run)
+// The pass backwards, two waves for every 16 value columns as in the forward
+// pass.  The first has the gradient of the state in registers and makes what the
+// next chunk waits for.  The second makes what does not depend on it a chunk
+// ahead, P^T dO and (scale e^b dO)^T Q, which the first adds in fp32 from LDS, and
+// a chunk behind writes X (and dV from it), which it finds in LDS; it makes all
+// other loads.
+template <class E, int DK, int CG>
+__global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(GdrArgs a, int run)
 {
     typedef GdrT<E> T;
     typedef typename T::Frag Frag;
     typedef E E4 __attribute__((ext_vector_type(4)));
-    constexpr int NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2, PA = T::TWO ? 2 : 1;      // (P and its remainder in front of A)
+    constexpr int NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1, NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr int XS = 72, XG = 16 * XS;      // X: a row of tokens per value, elements of a group
     __shared__ __align__(16) struct {
-        E k[NBUF][64 * DK], q[NBUF][64 * DK];
-        GdrSide<E, gdr_parts<E>(), 64> side[NBUF];
+        E k[NBUF][64 * DK], q[64 * DK];
+        GdrSide<E, W, NC0> side;      // A and the factors of the chunk, dO of the next
+        E p[W * gdr_part<E>()];       // P of the next, with its remainder in front
+        float se[64];
+        float pq[CG * (4 + 2 * NK) * 256];      // P^T dO and Q^T dO of the next
+        E x[CG * W * XG];                       // X of the chunk before
     } sm;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g = lane >> 4;
-    const int slices = (a.dv + 63) / 64;
+    const int cg = w % CG;
+    const int slices = (a.dv + NC0 - 1) / NC0;
     const int64_t id = blockIdx.x;
     int64_t item = (id >> 3) / run * 8 * run + (id & 7) * run + (id >> 3) % run;
     if (item >= (int64_t)a.B * a.Hv * slices) return;
     const int slice = item % slices;
     item /= slices;
     const int hv = item % a.Hv, hk = hv / (a.Hv / a.Hk);
-    const GdrSeq s = gdr_seq(a, item / a.Hv);
     const int64_t seq = item / a.Hv;
-    const int dv0 = slice * 64 + 16 * w, col = min(dv0 + l16, a.dv - 1);
+    const GdrSeq s = gdr_seq(a, seq);
+    const int dv0 = slice * NC0 + 16 * cg, col = min(dv0 + l16, a.dv - 1);
     const bool work = dv0 < a.dv;
-    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
-    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
-    const int64_t out = ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
-    E* vb = (E*)a.dv_ + out + dv0 + 4 * g;
-    const int NC = gdr_chunks(s.T);
-
-    floatx4 S[2 * NK];      // dS^T, laid out as the forward's state
-    const int64_t state = ((seq * a.Hv + hv) * (int64_t)a.dv + col) * a.dk + 8 * g;
-#pragma unroll
-    for (int x = 0; x < 2 * NK; ++x) {
-        S[x] = floatx4{0.f, 0.f, 0.f, 0.f};
-        if (a.dST && 32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(a.dST + state + 32 * (x / 2) + 4 * (x & 1));
-    }
+    const int NC = __builtin_amdgcn_readfirstlane(gdr_chunks(s.T));
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)(NBUF * 2 * 64 * DK * sizeof(E) / 16); i += 256) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)((NBUF + 1) * 64 * DK * sizeof(E) / 16); i += 2 * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
-    const GdrFetch<E, DK, 256> kf(kb, a.ks[1], s.T, a.dk, tid), qf(qb, a.qs[1], s.T, a.dk, tid);
-    auto fetch = [&](int n, int buf) {
-        kf(sm.k[buf], n * GDR_C, w);
-        qf(sm.q[buf], n * GDR_C, w);
-    };
-    GdrSideAhead<E, gdr_parts<E>(), 64, 256> ahead((const E*)a.dO + out + slice * 64, (int64_t)a.Hv * a.dv, a.dv - slice * 64, s.T, tid);
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     const char* rec0 = (const char*)a.rec + ((int64_t)s.slot0 * a.Hv + hv) * gdr_rec_bytes<E>();
-    auto load = [&](int n) {
-        ahead.load(rec0 + n * a.Hv * gdr_rec_bytes<E>(), tid);
-        ahead.load_v(n * GDR_C);
-    };
-    auto chunk = [&](int n, int buf) {
+    const int64_t recs = a.Hv * gdr_rec_bytes<E>();
+    const int ltid = tid % NT;
+    const E* kb = (const E*)a.k + s.b * a.ks[0] + (int64_t)s.row0 * a.ks[1] + hk * a.ks[2];
+    const E* qb = (const E*)a.q + s.b * a.qs[0] + (int64_t)s.row0 * a.qs[1] + hk * a.qs[2];
+    const GdrFetch<E, DK, NT> kf(kb, a.ks[1], s.T, a.dk, ltid), qf(qb, a.qs[1], s.T, a.dk, ltid);
+    float* const pq = sm.pq + cg * (4 + 2 * NK) * 256 + lane * 4;
+    E* const xw = sm.x + cg * W * XG;
+    // Steps: in step i the first wave has chunk n = NC - i (none in the first and
+    // the last one), the second chunks n - 1 and n + 1.  Barriers as in the forward
+    // pass: in the middle both have read what the other is about to write.
+    auto end = [&](int n) __attribute__((always_inline)) {
+        lds_barrier();
         if (NBUF == 1) {
-            __syncthreads();
-            ahead.store(sm.side[0], tid);
-            fetch(n, 0);
+            if (w >= CG && n >= 1) kf(sm.k[0], (n - 1) * GDR_C, cg);
+            swa_landed();
         }
-        swa_landed();
-        if (n > 0) {
-            if (NBUF == 2) fetch(n - 1, buf ^ 1);
-            load(n - 1);
+    };
+    if (w < CG) {
+        floatx4 S[2 * NK];      // dS^T, laid out as the forward's state
+        const int64_t state = ((seq * a.Hv + hv) * (int64_t)a.dv + col) * a.dk + 8 * g;
+        int hat[NK];
+#pragma unroll
+        for (int p = 0; p < NK; ++p)
+            hat[p] = dv0 + l16 < a.dv && 32 * p + 8 * g < a.dk ? (col * a.dk + 32 * p + 8 * g) * (int)sizeof(E) : GDR_NONE;
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x) {
+            S[x] = zero;
+            if (a.dST && 32 * (x / 2) + 8 * g < a.dk) S[x] = *reinterpret_cast<const floatx4*>(a.dST + state + 32 * (x / 2) + 4 * (x & 1));
         }
-        const E* kt = sm.k[buf];
-        const E* qt = sm.q[buf];
-        const GdrSide<E, gdr_parts<E>(), 64>& sd = sm.side[buf];
-        if (work) {
-            auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
-            const int64_t at = (int64_t)(s.slot0 + n) * a.Hv + hv;
-            Frag A[6], A2[T::TWO ? 6 : 1];
+        auto chunk = [&](int i, int buf) __attribute__((always_inline)) {
+            const int n = NC - i;
+            if (!work || i == 0 || n < 0) {
+                lds_barrier();
+                return end(n);
+            }
+            const E* kt = sm.k[buf];
+            const GdrSide<E, W, NC0>& sd = sm.side;
+            auto factor = [&](int f, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * f + 16 * t + 4 * g); };
+            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
+            floatx4 U[4], X[4], bb[4], bc[4], po[4], qo[2 * NK];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = t / 2; j < 2; ++j) {
-                    A[gdr_block_t(t, j)] = T::ld_at(sd.rec + PA * gdr_part<E>(), t, j, lane);
-                    if (T::TWO) A2[T::TWO ? gdr_block_t(t, j) : 0] = T::ld_at(sd.rec + (PA + 1) * gdr_part<E>(), t, j, lane);
-                }
-            Frag sh[NK], sl[NK];
+            for (int t = 0; t < 4; ++t) {
+                x[t] = T::template ld_row<DK>(kt, 16 * t + l16, 0, g);
+                U[t] = X[t] = zero;
+            }
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
                 sh[p] = T::pack(S[2 * p], S[2 * p + 1]);
                 sl[p] = T::rest(S[2 * p], S[2 * p + 1], sh[p]);
             }
-            floatx4 dO[4], U[4], X[4], Y[4];
-            Frag d[2], f[2], f2[2];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                dO[t] = T::template ld_acc<64>(sd.v, t, 16 * w, lane);
-                U[t] = X[t] = Y[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
 #pragma unroll
             for (int p = 0; p < NK; ++p) {
-                Frag x[4];
+                Frag y[4];      // the next ones
+                if (p + 1 < NK) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) x[t] = T::template ld_row<DK>(kt, 16 * t + l16, p, g);
+                    for (int t = 0; t < 4; ++t) y[t] = T::template ld_row<DK>(kt, 16 * t + l16, p + 1, g);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        bb[t] = factor(1, t);
+                        bc[t] = factor(2, t);
+                        po[t] = *reinterpret_cast<const floatx4*>(pq + t * 256);
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sh[p], U[t]);
                 if (T::TWO) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) U[t] = T::mma(x[t], sl[p], U[t]);
                 }
+                if (p + 1 < NK) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) x[t] = y[t];
+                }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) U[t] *= factor(2, t);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 1; j >= 0; --j)
+                for (int j = t / 2; j < 2; ++j) {
+                    A[gdr_block_t(t, j)] = T::ld_at(sd.rec, t, j, lane);
+                    if (T::TWO) A2[gdr_block_t(t, j)] = T::ld_at(sd.rec + (W - 1) * gdr_part<E>(), t, j, lane);
+                }
 #pragma unroll
-                for (int t = 0; t < 2 + 2 * j; ++t)
-                    for (int p = 0; p < PA; ++p) U[t] = T::mma(T::ld_at(sd.rec + p * gdr_part<E>(), t, j, lane), d[j], U[t]);
+            for (int y = 0; y < 2 * NK; ++y) qo[y] = *reinterpret_cast<const floatx4*>(pq + (4 + y) * 256);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) U[t][r] = fmaf(U[t][r], bc[t][r], po[t][r]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
             }
-            // X once with rows = tokens (what the state takes) and once with rows =
-            // values (what is stored)
+            const float eC = sd.vec[256];
+            lds_barrier();
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
 #pragma unroll
             for (int j = 1; j >= 0; --j) {
 #pragma unroll
-                for (int t = 0; t < 2 + 2 * j; ++t) {
-                    X[t] = T::mma(A[gdr_block_t(t, j)], f[j], X[t]);
-                    Y[t] = T::mma(f[j], A[gdr_block_t(t, j)], Y[t]);
-                }
+                for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A[gdr_block_t(t, j)], f[j], X[t]);
                 if (T::TWO) {
 #pragma unroll
-                    for (int t = 0; t < 2 + 2 * j; ++t) {
-                        X[t] = T::mma(A[gdr_block_t(t, j)], f2[j], X[t]);
-                        Y[t] = T::mma(f2[j], A[gdr_block_t(t, j)], Y[t]);
-                    }
+                    for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A[gdr_block_t(t, j)], f2[j], X[t]);
 #pragma unroll
-                    for (int t = 0; t < 2 + 2 * j; ++t) {
-                        X[t] = T::mma(A2[T::TWO ? gdr_block_t(t, j) : 0], f[j], X[t]);
-                        Y[t] = T::mma(f[j], A2[T::TWO ? gdr_block_t(t, j) : 0], Y[t]);
-                    }
+                    for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A2[gdr_block_t(t, j)], f[j], X[t]);
+                }
+            }
+            const auto ds = gdr_buffer((const E*)a.ds + ((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
+#pragma unroll
+            for (int p = 0; p < NK; ++p) gdr_store(ds, hat[p], sh[p]);
+#pragma unroll
+            for (int y = 0; y < 2 * NK; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[y][r] = fmaf(eC, S[y][r], qo[y][r]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const Frag h = T::pack(X[2 * j], X[2 * j + 1]);
+                E* to = xw + l16 * XS + 32 * j + 4 * g;
+                *reinterpret_cast<E4*>(to) = __builtin_shufflevector(h, h, 0, 1, 2, 3);
+                *reinterpret_cast<E4*>(to + 16) = __builtin_shufflevector(h, h, 4, 5, 6, 7);
+                if (T::TWO) {
+                    const Frag r = T::rest(X[2 * j], X[2 * j + 1], h);
+                    *reinterpret_cast<E4*>(to + (W - 1) * XG) = __builtin_shufflevector(r, r, 0, 1, 2, 3);
+                    *reinterpret_cast<E4*>(to + (W - 1) * XG + 16) = __builtin_shufflevector(r, r, 4, 5, 6, 7);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                X[t] *= -factor(1, t);
-                dO[t] *= factor(3, t);
-            }
-            Frag d2[2];
+            for (int t = 0; t < 4; ++t) X[t] *= -bb[t];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(X[2 * j], X[2 * j + 1]);
                 f2[j] = T::rest(X[2 * j], X[2 * j + 1], f[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f[j], S[y]);
+                if (T::TWO) {
+#pragma unroll
+                    for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
+                }
+                if (j == 0)
+#pragma unroll
+                    for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
+            }
+            end(n);
+        };
+        if (NC > 0) {
+            swa_landed();
+            for (int i = 0; i < NC + 2; i += 2) {
+                chunk(i, 0);
+                if (i + 1 < NC + 2) chunk(i + 1, NBUF - 1);
+            }
+        }
+        if (a.dS0 && work && dv0 + l16 < a.dv) {
+#pragma unroll
+            for (int x = 0; x < 2 * NK; ++x)
+                if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(a.dS0 + state + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+        }
+        return;
+    }
+
+    if (NC == 0) return;
+    const int64_t out = ((s.b * a.T + s.row0) * a.Hv + hv) * (int64_t)a.dv;
+    const int os = a.Hv * a.dv;
+    // where the lane's four values of row 16 t + l16 go in X and in dV
+    int xat[4], oat[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        xat[t] = dv0 + 4 * g < a.dv ? ((16 * t + l16) * a.dv + dv0 + 4 * g) * (int)sizeof(E) : GDR_NONE;
+        oat[t] = dv0 + 4 * g < a.dv ? ((16 * t + l16) * os + dv0 + 4 * g) * (int)sizeof(E) : GDR_NONE;
+    }
+    GdrSideAhead<E, W, NC0, NT> ahead((const E*)a.dO + out + slice * NC0, os, a.dv - slice * NC0, s.T, ltid);
+    constexpr int PP = W * gdr_part<E>() * (int)sizeof(E) / 16, NP = (PP + NT - 1) / NT;
+    floatx4 px[NP], sx;
+    auto load = [&](int n) __attribute__((always_inline)) {
+        const int n1 = max(min(n - 1, NC - 1), 0), n2 = max(min(n - 2, NC - 1), 0);
+        ahead.load(rec0 + n1 * recs, ltid);
+        ahead.load_v(n2 * GDR_C);
+        const char* r = rec0 + n2 * recs;
+        const auto ps = gdr_buffer(r, PP * 16);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) px[i] = gdr_load(ps, (i * NT + ltid) * 16);
+        sx = gdr_load(gdr_buffer(r + gdr_rec_bytes<E>() - GDR_VEC * 4 + 192 * 4, 256), ltid * 16);
+    };
+    auto store = [&]() __attribute__((always_inline)) {
+        ahead.store(sm.side, ltid);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p)[i * NT + ltid] = px[i];
+        if (ltid < 16) reinterpret_cast<floatx4*>(sm.se)[ltid] = sx;
+    };
+    float be[4] = {0.f, 0.f, 0.f, 0.f};
+    auto step = [&](int i, int buf) __attribute__((always_inline)) {
+        const int n = NC - i;
+        const bool before = work && n >= 1, after = work && n <= NC - 2;
+        if (NBUF == 2 && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
+        load(n);
+        floatx4 X[4], X2[4], PO[4] = {zero, zero, zero, zero}, QO[2 * NK];
+        float bn[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) bn[t] = sm.side.vec[16 * t + l16];
+#pragma unroll
+        for (int y = 0; y < 2 * NK; ++y) QO[y] = zero;
+        if (after) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                X[t] = T::template ld_t4<XS>(xw, t, lane);
+                if (T::TWO) X2[t] = T::template ld_t4<XS>(xw + (W - 1) * XG, t, lane);
+            }
+        }
+        if (before) {
+            floatx4 dO[4];
+            Frag d[2], d2[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dO[t] = T::template ld_acc<NC0>(sm.side.v, t, 16 * cg, lane);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
+#pragma unroll
+            for (int j = 1; j >= 0; --j)
+#pragma unroll
+                for (int p = 0; p < W; ++p)
+#pragma unroll
+                    for (int t = 0; t < 2 + 2 * j; ++t) PO[t] = T::mma(T::ld_at(sm.p + p * gdr_part<E>(), t, j, lane), d[j], PO[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dO[t] *= *reinterpret_cast<const floatx4*>(sm.se + 16 * t + 4 * g);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
                 d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
                 d2[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j]);
             }
-            const float eC = sd.vec[256];
-#pragma unroll
-            for (int y = 0; y < 2 * NK; ++y) S[y] *= eC;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int y0 = 0; y0 < 2 * NK; y0 += 4) {
-                    Frag x[4], z[4];
+                    Frag z[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        z[i] = T::template ld_col8<DK>(qt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
-                        x[i] = T::template ld_col8<DK>(kt, j, 32 * ((y0 + i) / 2) + 4 * (i & 1), lane);
-                    }
+                    for (int y = 0; y < 4; ++y) z[y] = T::template ld_col8<DK>(sm.q, j, 32 * ((y0 + y) / 2) + 4 * (y & 1), lane);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(z[i], d[j], S[y0 + i]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f[j], S[y0 + i]);
+                    for (int y = 0; y < 4; ++y) QO[y0 + y] = T::mma(z[y], d[j], QO[y0 + y]);
                     if (T::TWO) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(z[i], d2[j], S[y0 + i]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) S[y0 + i] = T::mma(x[i], f2[j], S[y0 + i]);
+                        for (int y = 0; y < 4; ++y) QO[y0 + y] = T::mma(z[y], d2[j], QO[y0 + y]);
                     }
                 }
-            if (dv0 + l16 < a.dv) {
-                E* ds = (E*)a.ds + (at * a.dv + col) * a.dk + 8 * g;
+        }
+        lds_barrier();
+        if (n >= 2) qf(sm.q, (n - 2) * GDR_C, cg);
+        if (before) {
 #pragma unroll
-                for (int p = 0; p < NK; ++p)
-                    if (32 * p + 8 * g < a.dk) T::st(ds + 32 * p, sh[p]);
-            }
-            if (dv0 + 4 * g < a.dv) {
+            for (int t = 0; t < 4; ++t) *reinterpret_cast<floatx4*>(pq + t * 256) = PO[t];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int row = 16 * t + l16;
-                    floatx4 y = Y[t];
-                    const E4 hi = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
-                    const int64_t to = (at * GDR_C + row) * a.dv + dv0 + 4 * g;
-                    *reinterpret_cast<E4*>((E*)a.x + to) = hi;
-                    if (T::TWO)
-                        *reinterpret_cast<E4*>((E*)a.x2 + to) = E4{(E)(y[0] - (float)hi[0]), (E)(y[1] - (float)hi[1]),
-                                                                   (E)(y[2] - (float)hi[2]), (E)(y[3] - (float)hi[3])};
-                    y *= sd.vec[row];
-                    if (n * GDR_C + row < s.T)
-                        *reinterpret_cast<E4*>(vb + (int64_t)(n * GDR_C + row) * a.Hv * a.dv) = E4{(E)y[0], (E)y[1], (E)y[2], (E)y[3]};
+            for (int y = 0; y < 2 * NK; ++y) *reinterpret_cast<floatx4*>(pq + (4 + y) * 256) = QO[y];
+        }
+        // the next chunks are here; the stores that follow need not have been written when they begin
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        store();
+        if (after) {
+            const int c = n + 1;
+            const int64_t x0 = ((int64_t)(s.slot0 + c) * a.Hv + hv) * GDR_C * a.dv;
+            const auto xb = gdr_buffer((const E*)a.x + x0, (int64_t)GDR_C * a.dv * (int)sizeof(E));
+            const auto x2b = gdr_buffer(T::TWO ? (const E*)a.x2 + x0 : nullptr, T::TWO ? (int64_t)GDR_C * a.dv * (int)sizeof(E) : 0);
+            const auto vb = gdr_buffer((const E*)a.dv_ + out + (int64_t)c * GDR_C * os, ((int64_t)(min(s.T - c * GDR_C, GDR_C) - 1) * os + a.dv) * (int)sizeof(E));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                gdr_store(xb, xat[t], X[t], (const E*)nullptr);
+                if (T::TWO) {
+                    gdr_store(x2b, xat[t], X2[t], (const E*)nullptr);
+                    X[t] += X2[t];
                 }
+                gdr_store(vb, oat[t], X[t] * be[t], (const E*)nullptr);
             }
         }
-        if (NBUF == 2 && n > 0) ahead.store(sm.side[buf ^ 1], tid);
-    };
-    if (NC > 0) {
-        load(NC - 1);
-        if (NBUF == 2) {
-            fetch(NC - 1, 0);
-            ahead.store(sm.side[0], tid);
-        }
-    }
-    for (int n = NC - 1; n >= 0; n -= 2) {
-        chunk(n, 0);
-        if (n > 0) chunk(n - 1, NBUF - 1);
-    }
-    if (a.dS0 && work && dv0 + l16 < a.dv) {
 #pragma unroll
-        for (int x = 0; x < 2 * NK; ++x)
-            if (32 * (x / 2) + 8 * g < a.dk) *reinterpret_cast<floatx4*>(a.dS0 + state + 32 * (x / 2) + 4 * (x & 1)) = S[x];
+        for (int t = 0; t < 4; ++t) be[t] = bn[t];
+        end(n);
+    };
+    load(NC + 1);
+    qf(sm.q, (NC - 1) * GDR_C, cg);
+    store();
+    swa_landed();
+    for (int i = 0; i < NC + 2; i += 2) {
+        step(i, 0);
+        if (i + 1 < NC + 2) step(i + 1, NBUF - 1);
     }
 }
 
@@ -792,12 +904,23 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     }
 }
 
+template <class E, int DK, int CG>
+static void gdr_back(const GdrArgs& a, hipStream_t st)
+{
+    int run;
+    const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 16 * CG - 1) / (16 * CG)), run);
+    kd_gdr_back_kernel<E, DK, CG><<<(unsigned)grid, 128 * CG, 0, st>>>(a, run);
+}
+
 template <class E, int DK, int DV>
 static hipError_t gdr_bwd(const GdrArgs& a, hipStream_t st)
 {
-    int run;
-    const int64_t grid = gdr_pass_grid((int64_t)a.B * a.Hv * ((a.dv + 63) / 64), run);
-    kd_gdr_back_kernel<E, DK><<<(unsigned)grid, 256, 0, st>>>(a, run);
+    if constexpr (sizeof(E) == 2) {
+        if (gdr_narrow(a, a.B)) gdr_back<E, DK, 2>(a, st);
+        else gdr_back<E, DK, 4>(a, st);
+    } else {
+        gdr_back<E, DK, 2>(a, st);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.slots == 0) return e;
     const int items = a.slots * a.Hk;
