@@ -25,7 +25,8 @@ int64_t gdr_pass_grid(int64_t items, int& run);
 // next chunk waits for.  The second makes what does not depend on it a chunk
 // ahead, P^T dO and (scale e^b dO)^T Q, which the first adds in fp32 from LDS, and
 // a chunk behind writes X (and dV from it), which it finds in LDS; it makes all
-// other loads.
+// other loads.  Where LDS holds two chunks' worth of what the second wave reads
+// (FAR), the barrier in the middle comes before its products, not behind.
 template <class E, int DK, int CG>
 __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(GdrArgs a, int run)
 {
@@ -33,12 +34,13 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
     typedef typename T::Frag Frag;
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1, NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
+    constexpr bool FAR = sizeof(E) == 2 && (DK == 64 || CG == 2);
     constexpr int XS = 72, XG = 16 * XS;      // X: a row of tokens per value, elements of a group
     __shared__ __align__(16) struct {
-        E k[NBUF][64 * DK], q[64 * DK];
-        GdrSide<E, W, NC0> side;      // A and the factors of the chunk, dO of the next
-        E p[W * gdr_part<E>()];       // P of the next, with its remainder in front
-        float se[64];
+        E k[NBUF][64 * DK], q[FAR ? 2 : 1][64 * DK];
+        GdrSide<E, W, NC0> side[FAR ? 2 : 1];      // A and the factors of the chunk, dO of the next
+        E p[FAR ? 2 : 1][W * gdr_part<E>()];       // P of the next, with its remainder in front
+        float se[FAR ? 2 : 1][64];
         float pq[CG * (4 + 2 * NK) * 256];      // P^T dO and Q^T dO of the next
         E x[CG * W * XG];                       // X of the chunk before
     } sm;
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
     const int NC = __builtin_amdgcn_readfirstlane(gdr_chunks(s.T));
     if (a.dk < DK) {
         floatx4* z = reinterpret_cast<floatx4*>(&sm);
-        for (int i = tid; i < (int)((NBUF + 1) * 64 * DK * sizeof(E) / 16); i += 2 * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = tid; i < (int)((NBUF + (FAR ? 2 : 1)) * 64 * DK * sizeof(E) / 16); i += 2 * NT) z[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();
     }
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                 return end(n);
             }
             const E* kt = sm.k[buf];
-            const GdrSide<E, W, NC0>& sd = sm.side;
+            const GdrSide<E, W, NC0>& sd = sm.side[FAR ? buf : 0];
             auto factor = [&](int f, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * f + 16 * t + 4 * g); };
             Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
             floatx4 U[4], X[4], bb[4], bc[4], po[4], qo[2 * NK];
@@ -249,23 +251,25 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
         for (int i = 0; i < NP; ++i) px[i] = gdr_load(ps, (i * NT + ltid) * 16);
         sx = gdr_load(gdr_buffer(r + gdr_rec_bytes<E>() - GDR_VEC * 4 + 192 * 4, 256), ltid * 16);
     };
-    auto store = [&]() __attribute__((always_inline)) {
-        ahead.store(sm.side, ltid);
+    auto store = [&](int b) __attribute__((always_inline)) {
+        ahead.store(sm.side[b], ltid);
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p)[i * NT + ltid] = px[i];
-        if (ltid < 16) reinterpret_cast<floatx4*>(sm.se)[ltid] = sx;
+            if (i < NP - 1 || (NP - 1) * NT + ltid < PP) reinterpret_cast<floatx4*>(sm.p[b])[i * NT + ltid] = px[i];
+        if (ltid < 16) reinterpret_cast<floatx4*>(sm.se[b])[ltid] = sx;
     };
     float be[4] = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](int i, int buf) __attribute__((always_inline)) {
         const int n = NC - i;
         const bool before = work && n >= 1, after = work && n <= NC - 2;
         if (NBUF == 2 && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
+        const int fb = FAR ? buf : 0;
+        if (FAR && n >= 2) qf(sm.q[FAR ? buf ^ 1 : 0], (n - 2) * GDR_C, cg);
         load(n);
         floatx4 X[4], X2[4], PO[4] = {zero, zero, zero, zero}, QO[2 * NK];
         float bn[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) bn[t] = sm.side.vec[16 * t + l16];
+        for (int t = 0; t < 4; ++t) bn[t] = sm.side[fb].vec[16 * t + l16];
 #pragma unroll
         for (int y = 0; y < 2 * NK; ++y) QO[y] = zero;
         if (after) {
@@ -275,11 +279,12 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                 if (T::TWO) X2[t] = T::template ld_t4<XS>(xw + (W - 1) * XG, t, lane);
             }
         }
+        if (FAR) lds_barrier();
         if (before) {
             floatx4 dO[4];
             Frag d[2], d2[2];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dO[t] = T::template ld_acc<NC0>(sm.side.v, t, 16 * cg, lane);
+            for (int t = 0; t < 4; ++t) dO[t] = T::template ld_acc<NC0>(sm.side[fb].v, t, 16 * cg, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j) d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
 #pragma unroll
@@ -287,9 +292,9 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
 #pragma unroll
                 for (int p = 0; p < W; ++p)
 #pragma unroll
-                    for (int t = 0; t < 2 + 2 * j; ++t) PO[t] = T::mma(T::ld_at(sm.p + p * gdr_part<E>(), t, j, lane), d[j], PO[t]);
+                    for (int t = 0; t < 2 + 2 * j; ++t) PO[t] = T::mma(T::ld_at(sm.p[fb] + p * gdr_part<E>(), t, j, lane), d[j], PO[t]);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dO[t] *= *reinterpret_cast<const floatx4*>(sm.se + 16 * t + 4 * g);
+            for (int t = 0; t < 4; ++t) dO[t] *= *reinterpret_cast<const floatx4*>(sm.se[fb] + 16 * t + 4 * g);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
@@ -301,7 +306,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                 for (int y0 = 0; y0 < 2 * NK; y0 += 4) {
                     Frag z[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) z[y] = T::template ld_col8<DK>(sm.q, j, 32 * ((y0 + y) / 2) + 4 * (y & 1), lane);
+                    for (int y = 0; y < 4; ++y) z[y] = T::template ld_col8<DK>(sm.q[fb], j, 32 * ((y0 + y) / 2) + 4 * (y & 1), lane);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) QO[y0 + y] = T::mma(z[y], d[j], QO[y0 + y]);
                     if (T::TWO) {
@@ -310,8 +315,10 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                     }
                 }
         }
-        lds_barrier();
-        if (n >= 2) qf(sm.q, (n - 2) * GDR_C, cg);
+        if (!FAR) {
+            lds_barrier();
+            if (n >= 2) qf(sm.q[0], (n - 2) * GDR_C, cg);
+        }
         if (before) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) *reinterpret_cast<floatx4*>(pq + t * 256) = PO[t];
@@ -320,7 +327,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
         }
         // the next chunks are here; the stores that follow need not have been written when they begin
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        store();
+        store(FAR ? buf ^ 1 : 0);
         if (after) {
             const int c = n + 1;
             const int64_t x0 = ((int64_t)(s.slot0 + c) * a.Hv + hv) * GDR_C * a.dv;
@@ -342,8 +349,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
         end(n);
     };
     load(NC + 1);
-    qf(sm.q, (NC - 1) * GDR_C, cg);
-    store();
+    qf(sm.q[0], (NC - 1) * GDR_C, cg);
+    store(0);
     swa_landed();
     for (int i = 0; i < NC + 2; i += 2) {
         step(i, 0);
