@@ -24,8 +24,8 @@ int64_t gdr_pass_grid(int64_t items, int& run);
 // pass.  The first has the gradient of the state in registers and makes what the
 // next chunk waits for.  The second makes what does not depend on it a chunk
 // ahead, P^T dO and (scale e^b dO)^T Q, which the first adds in fp32 from LDS, and
-// a chunk behind writes X (and dV from it), which it finds in LDS; it makes all
-// other loads.  Where LDS holds two chunks' worth of what the second wave reads
+// a chunk behind writes X (and dV from it), which it finds in LDS; it makes the
+// loads.  Where LDS holds two chunks' worth of what the second wave reads
 // (FAR), the barrier in the middle comes before its products, not behind.
 template <class E, int DK, int CG>
 __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(GdrArgs a, int run)
@@ -35,6 +35,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NT = 64 * CG, NC0 = 16 * CG, W = T::TWO ? 2 : 1, NK = DK / 32, NBUF = sizeof(E) * DK > 256 ? 1 : 2;
     constexpr bool FAR = sizeof(E) == 2 && (DK == 64 || CG == 2);
+    constexpr bool KFIRST = sizeof(E) == 2 && CG == 2;      // the first wave loads K (which waits less where it has a SIMD for itself)
     constexpr int XS = 72, XG = 16 * XS;      // X: a row of tokens per value, elements of a group
     __shared__ __align__(16) struct {
         E k[NBUF][64 * DK], q[FAR ? 2 : 1][64 * DK];
@@ -98,6 +99,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             const int n = NC - i;
             if (!work || i == 0 || n < 0) {
                 lds_barrier();
+                if (KFIRST && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
+                if (KFIRST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                 return end(n);
             }
             const E* kt = sm.k[buf];
@@ -160,6 +163,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             }
             const float eC = sd.vec[256];
             lds_barrier();
+            if (KFIRST && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
 #pragma unroll
             for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 0, 32 * (y / 2) + 4 * (y & 1), lane);
 #pragma unroll
@@ -211,6 +215,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) kc[y] = T::template ld_col8<DK>(kt, 1, 32 * (y / 2) + 4 * (y & 1), lane);
             }
+            if (KFIRST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             end(n);
         };
         if (NC > 0) {
@@ -262,8 +267,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
     auto step = [&](int i, int buf) __attribute__((always_inline)) {
         const int n = NC - i;
         const bool before = work && n >= 1, after = work && n <= NC - 2;
-        if (NBUF == 2 && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
         const int fb = FAR ? buf : 0;
+        if (NBUF == 2 && !KFIRST && n >= 1) kf(sm.k[buf ^ (NBUF - 1)], (n - 1) * GDR_C, cg);
         if (FAR && n >= 2) qf(sm.q[FAR ? buf ^ 1 : 0], (n - 2) * GDR_C, cg);
         load(n);
         floatx4 X[4], X2[4], PO[4] = {zero, zero, zero, zero}, QO[2 * NK];
