@@ -552,7 +552,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 #pragma unroll 1
         for (int v0 = 0; v0 < a.dv; v0 += DV) {
             GdrStage<E, DK, DV> st;
-            __syncthreads();      // the head (or the values) before is done
+            lds_barrier();      // the head (or the values) before is done
             if (v0 == 0) {
                 if (tid < GDR_VEC / 4) reinterpret_cast<floatx4*>(sm.vec)[tid] = lf;
                 if (hg == 0) {
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
             for (int i = 0; i < NA; ++i)
                 if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
             lv.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
-            __syncthreads();
+            lds_barrier();
             st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, min(DV, a.dv - v0), a.dk, tid);
             const bool same = v0 + DV < a.dv || hg + 1 < G;
             const Next nx = which(same ? item : itemn, same ? c : cn, v0 + DV < a.dv ? hg : same ? hg + 1 : 0, v0 + DV < a.dv ? v0 + DV : 0);
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                         if (T::TWO) W[t] = T::mma(f[j], T::ld(rec + gdr_part<E>() + gdr_block(t, j) * 512), W[t]);
                     }
             }
-            __syncthreads();
+            lds_barrier();
             if (w < DV / 16) {
                 KD_LANE;
 #pragma unroll
@@ -682,7 +682,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     }
                 }
             }
-            __syncthreads();
+            lds_barrier();
             ss += st.replace(sm.s, tid);      // dS in place of S0
             // dO U^T and X U^T
             {
@@ -706,7 +706,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     }
                 }
             }
-            __syncthreads();
+            lds_barrier();
             load1(nx);
             // e^(bC - b) U dS
             {
@@ -826,7 +826,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
         {
             KD_LANE;
             // E K, E^T Q and (F + F^T) K
