@@ -429,10 +429,11 @@ template <class E, int DK, int DV>
 struct GdrGradLds {
     static constexpr bool TWO = GdrT<E>::TWO;
     static constexpr int A = (TWO ? 2 : 1) * GDR_BLOCKS * 512;      // elements of A with its remainder
-    E k[64 * DK], q[64 * DK], s[DV * DK], x[64 * DV], x2[TWO ? 64 * DV : 8], u[64 * DV];
     union {      // A is done with when U is made
         E u2[TWO ? 64 * DV : 8], a[A];
     };
+    E u[64 * DV], s[DV * DK];      // (loads straight to LDS reach this far)
+    E k[64 * DK], q[64 * DK], x[64 * DV], x2[TWO ? 64 * DV : 8];
     union {      // dO is done with when E and F are made
         E d[64 * DV];
         struct {
@@ -450,7 +451,8 @@ struct GdrGradLds {
 // the value heads of the group one after the other, values in blocks of DV.
 // bf16: X and U with their remainders, S0, dS, E and F rounded.  As many
 // workgroups as compute units go over all chunks: what the next head or chunk
-// needs loads to registers beside the last stages of this one.
+// needs loads beside the last stages of this one, to registers or (bf16: A, V
+// and S0) straight to LDS, where their places are free by then.
 template <class E, int DK, int DV>
 __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 {
@@ -461,6 +463,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
     typedef SwaTile<E, 64> TC;
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = DK / 32, NV = DV / 32, CG = DK / 32, RT = CG / 2;      // pairs of column tiles of dq, row tiles of a wave
+    constexpr bool DIRECT = T::TWO;
     __shared__ __align__(16) GdrGradLds<E, DK, DV> sm;
     const int tid = threadIdx.x, lane0 = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.Hv / a.Hk;
@@ -505,28 +508,56 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
         n.at = (int64_t)(item / a.Hk) * a.Hv + n.hv;
         return n;
     };
+    // A, V and S0 straight to LDS; what they do not fill is cleared
+    auto direct = [&](const Next& n) __attribute__((always_inline)) {
+        if (!DIRECT || n.c.rows == 0) return;
+        KD_LANE;
+        const int t = 64 * w + lane;
+        const char* rec = (const char*)a.rec + n.at * gdr_rec_bytes<E>() + gdr_parts<E>() / 2 * gdr_part<E>() * (int)sizeof(E);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(1024 * w);
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (i < NA - 1 || i * 512 + t < AP) load_lds16(lds_address(sm.a) + to + i * 8192, rec + (i * 512 + t) * 16);
+        const E* v = (const E*)a.v + n.c.base * a.vs[0] + (int64_t)n.c.first * a.vs[1] + n.hv * a.vs[2] + n.v0;
+        const E* s = (const E*)a.hs + (n.at * a.dv + n.v0) * a.dk;
+        const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 64 * TV::CPR / 512; ++i) {
+            const int r = (i * 512 + t) / TV::CPR, c = ((i * 512 + t) % TV::CPR ^ TV::swz(r)) * TV::EPC;
+            if (r < n.c.rows && c < n.nv) load_lds16(lds_address(sm.u) + to + i * 8192, v + r * a.vs[1] + c);
+            else reinterpret_cast<floatx4*>(sm.u)[i * 512 + t] = z;
+        }
+#pragma unroll
+        for (int i = 0; i < DV * TK::CPR / 512; ++i) {
+            const int r = (i * 512 + t) / TK::CPR, c = ((i * 512 + t) % TK::CPR ^ TK::swz(r)) * TK::EPC;
+            if (r < n.nv && c < a.dk) load_lds16(lds_address(sm.s) + to + i * 8192, s + r * a.dk + c);
+            else reinterpret_cast<floatx4*>(sm.s)[i * 512 + t] = z;
+        }
+    };
     auto load1 = [&](const Next& n) {
-        ls.load((const E*)a.hs + (n.at * a.dv + n.v0) * a.dk, a.dk, n.nv, a.dk, tid);
+        if (!DIRECT) ls.load((const E*)a.hs + (n.at * a.dv + n.v0) * a.dk, a.dk, n.nv, a.dk, tid);
         lx.load((const E*)a.x + n.at * GDR_C * a.dv + n.v0, a.dv, n.c.rows, n.nv, tid);
     };
     auto load2 = [&](const Next& n) {
         if (T::TWO) lx2.load((const E*)a.x2 + n.at * GDR_C * a.dv + n.v0, a.dv, n.c.rows, n.nv, tid);
         ld.load((const E*)a.dO + ((n.c.base * a.T + n.c.first) * a.Hv + n.hv) * (int64_t)a.dv + n.v0, (int64_t)a.Hv * a.dv, n.c.rows, n.nv, tid);
-        lv.load((const E*)a.v + n.c.base * a.vs[0] + (int64_t)n.c.first * a.vs[1] + n.hv * a.vs[2] + n.v0, a.vs[1], n.c.rows, n.nv, tid);
+        if (!DIRECT) lv.load((const E*)a.v + n.c.base * a.vs[0] + (int64_t)n.c.first * a.vs[1] + n.hv * a.vs[2] + n.v0, a.vs[1], n.c.rows, n.nv, tid);
     };
     auto load3 = [&](const Next& n) {
         lk.load((const E*)a.k + n.c.base * a.ks[0] + (int64_t)n.c.first * a.ks[1] + n.hk * a.ks[2], a.ks[1], n.kr, a.dk, tid);
         lq.load((const E*)a.q + n.c.base * a.qs[0] + (int64_t)n.c.first * a.qs[1] + n.hk * a.qs[2], a.qs[1], n.kr, a.dk, tid);
         const char* record = (const char*)a.rec + n.at * gdr_rec_bytes<E>();
         const auto rec = gdr_buffer(record + gdr_parts<E>() / 2 * gdr_part<E>() * (int)sizeof(E), n.c.rows > 0 ? AP * 16 : 0);      // (A)
+        if (!DIRECT)
 #pragma unroll
-        for (int i = 0; i < NA; ++i) la[i] = gdr_load(rec, (i * 512 + tid) * 16);
+            for (int i = 0; i < NA; ++i) la[i] = gdr_load(rec, (i * 512 + tid) * 16);
         lf = gdr_load(gdr_buffer(record + gdr_rec_bytes<E>() - GDR_VEC * 4, n.c.rows > 0 ? GDR_VEC * 4 : 0), tid * 16);
     };
     GdrChunk c, cn;
     int item = next((int)blockIdx.x - (int)gridDim.x, c), itemn;
     {
         const Next n = which(item, c, 0, 0);
+        direct(n);
         load1(n);
         load2(n);
         load3(n);
@@ -560,14 +591,17 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     lq.store(sm.q, tid);
                 }
             }
-            ls.store(sm.s, tid);
             ld.store(sm.d, tid);
             lx.store(sm.x, tid);
             if (T::TWO) lx2.store(sm.x2, tid);
+            if (!DIRECT) {
+                ls.store(sm.s, tid);
 #pragma unroll
-            for (int i = 0; i < NA; ++i)
-                if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
-            lv.store(sm.u, tid);      // where U will be: a wave reads and writes the same columns
+                for (int i = 0; i < NA; ++i)
+                    if (i < NA - 1 || (NA - 1) * 512 + tid < AP) reinterpret_cast<floatx4*>(sm.a)[i * 512 + tid] = la[i];
+                lv.store(sm.u, tid);      // (V where U will be: a wave reads and writes the same columns)
+            }
+            if (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             lds_barrier();
             st.load((const E*)a.ds + (at * a.dv + v0) * a.dk, a.dk, min(DV, a.dv - v0), a.dk, tid);
             const bool same = v0 + DV < a.dv || hg + 1 < G;
@@ -748,7 +782,11 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 }
             }
             load2(nx);
-            if (v0 + DV < a.dv) load3(nx);
+            if (v0 + DV < a.dv) {
+                if (DIRECT) lds_barrier();      // U and dS are done with
+                direct(nx);
+                load3(nx);
+            }
         }
         const bool small = sm.vec[257] != 0.f;
         {
@@ -832,7 +870,9 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
             // E K, E^T Q and (F + F^T) K
             {
                 const bool same = hg + 1 < G;
-                load3(which(same ? item : itemn, same ? c : cn, same ? hg + 1 : 0, 0));
+                const Next nx = which(same ? item : itemn, same ? c : cn, same ? hg + 1 : 0, 0);
+                direct(nx);
+                load3(nx);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
