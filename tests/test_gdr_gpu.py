@@ -167,7 +167,7 @@ def test_long_sequences_of_few_heads(lens, Hk, Hv, dk, dv, state, dtype):
 
 @pytest.mark.parametrize("B,T,H,d", [(3, 70, 48, 128), (1, 1600, 32, 128), (9, 65, 16, 72)])
 def test_forward_of_many_heads(B, T, H, d):
-    """Eight waves a workgroup, in the maps of segments too."""
+    """Four groups of value columns a workgroup, in the maps of segments too."""
     import delta_rule_recurrent_chunk_amd as kd
     t = inputs((B, T), H // 4, H, d, d, "bf16", T)
     o, ST = kd.gdr_fwd(*(t[n] for n in NAMES), t["S0"])
@@ -320,3 +320,55 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(ref[n], out[n]) for n in ref) and torch.equal(o, step)
         assert all(torch.equal(ref[n], x) for n, x in run(t, 0.2).items())
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,dk,dv", [(9, 70, 8, 16, 128, 64), (17, 65, 2, 8, 64, 72), (5, 130, 4, 16, 128, 136)])
+def test_backward_of_many_heads(B, T, Hk, Hv, dk, dv):
+    """Four groups of value columns a workgroup."""
+    t = inputs((B, T), Hk, Hv, dk, dv, "bf16", T + dv)
+    compare(t, run(t, 0.2), 0.2, "bf16")
+
+
+def test_backward_of_many_packed_sequences():
+    torch = _torch()
+    lens = [(37 * i) % 71 for i in range(70)]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    t = inputs((int(cu[-1]),), 1, 2, 64, 64, "bf16", 31, n=len(lens))
+    got = run(t, 0.2, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    compare(t, got, 0.2, "bf16", [(0, int(a), int(b)) for a, b in zip(cu[:-1], cu[1:])])
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 72), ("bf16", 128, 200), ("fp32", 40, 40)])
+def test_what_is_not_finite_stays_in_its_head(dtype, dk, dv):
+    """More chunks than workgroups: what one leaves in LDS does not reach the next."""
+    torch = _torch()
+    t = inputs((3, 1600), 4, 4, dk, dv, dtype, 21)
+    ref = run(t, 0.2)
+    bad = {n: None if x is None else x.clone() for n, x in t.items()}
+    bad["v"][0, 3, 0] = float("inf")
+    bad["dO"][1, 1500, 2] = float("nan")
+    got = run(bad, 0.2)
+    for n, x in ref.items():
+        for b in range(3):
+            for h in range(4):
+                if (b, h) in ((0, 0), (1, 2)):
+                    continue
+                at = (b, h) if n in ("ST", "dS0") else (b, slice(None), h)
+                assert torch.equal(got[n][at], x[at]), (n, b, h)
+    assert not torch.isfinite(got["o"][0, 3:, 0]).any() and torch.equal(got["o"][1], ref["o"][1])
+
+
+def test_calls_that_run_at_once():
+    torch = _torch()
+    ts = [inputs((2, 700), 2, 4, 64, 64, "bf16", 40 + i) for i in range(2)]
+    refs = [run(t, 0.2) for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(run(ts[i], 0.2))
+    torch.cuda.synchronize()
+    for ref, rs in zip(refs, outs):
+        assert all(torch.equal(ref[n], r[n]) for r in rs for n in ref)
