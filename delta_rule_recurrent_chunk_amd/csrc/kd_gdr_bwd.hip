@@ -364,22 +364,23 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
 }
 
 // Natural-order fragments of a row-major LDS tile read by columns: K = rows 32
-// j + 8 g + e, row (or column) of the operand = column c0 + l16.
-template <int D>
+// j + 8 g + e, row (or column) m of the operand = column c0 + P (m / 4) + m % 4.
+// (P = 8: two of them, 4 columns apart, leave a lane eight columns in a row.)
+template <int D, int P = 4>
 __device__ __forceinline__ bf16x8 gdr_coln(const __bf16* tile, int j, int c0, int lane) {
     typedef SwaTile<__bf16, D> TL;
     typedef __attribute__((__vector_size__(4 * sizeof(short)))) short v4s;
-    const int l = lane & 15, r = 32 * j + 8 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
+    const int l = lane & 15, r = 32 * j + 8 * (lane >> 4) + (l >> 2), c = c0 + P * (l & 3);
     const __bf16* lo = tile + TL::off(r, c / 8) + c % 8;
     const __bf16* hi = tile + TL::off(r + 4, c / 8) + c % 8;
     const s16x4 x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(lo)));
     const s16x4 y = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(hi)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-template <int D>
+template <int D, int P = 4>
 __device__ __forceinline__ floatx8 gdr_coln(const float* tile, int j, int c0, int lane) {
     typedef SwaTile<float, D> TL;
-    const int c = c0 + (lane & 15), r = 32 * j + 8 * (lane >> 4);
+    const int l = lane & 15, c = c0 + P * (l >> 2) + (l & 3), r = 32 * j + 8 * (lane >> 4);
     floatx8 f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = tile[TL::off(r + e, c / 4) + c % 4];
@@ -682,7 +683,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     for (int t = 0; t < RT; ++t) dqi[y][t] = dke[y][t] = zero;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const Frag s[2] = {gdr_coln<DK>(sm.s, j, c0, lane), gdr_coln<DK>(sm.s, j, c0 + 16, lane)};
+                    const Frag s[2] = {gdr_coln<DK, 8>(sm.s, j, c0, lane), gdr_coln<DK, 8>(sm.s, j, c0 + 4, lane)};
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         const Frag d = T::template ld_row<DV>(sm.d, 16 * (r0 + t) + l16, j, g), x = T::template ld_row<DV>(sm.x, 16 * (r0 + t) + l16, j, g);
@@ -704,7 +705,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     const float se = sm.vec[192 + row], bb = sm.vec[64 + row];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int to = TK::off(row, (c0 + 16 * y + 4 * g) / TK::EPC) + 4 * g % TK::EPC;
+                        const int to = TK::off(row, (c0 + 8 * g + 4 * y) / TK::EPC) + 4 * y % TK::EPC;
                         const E4 q4 = *reinterpret_cast<const E4*>(sm.q + to), k4 = *reinterpret_cast<const E4*>(sm.k + to);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -752,7 +753,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     for (int t = 0; t < RT; ++t) dks[y][t] = zero;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const Frag s[2] = {gdr_coln<DK>(sm.s, j, c0, lane), gdr_coln<DK>(sm.s, j, c0 + 16, lane)};
+                    const Frag s[2] = {gdr_coln<DK, 8>(sm.s, j, c0, lane), gdr_coln<DK, 8>(sm.s, j, c0 + 4, lane)};
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         const Frag u = T::template ld_row<DV>(sm.u, 16 * (r0 + t) + l16, j, g);
@@ -771,7 +772,7 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                     const float ec = sm.vec[128 + row];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const E4 k4 = *reinterpret_cast<const E4*>(sm.k + TK::off(row, (c0 + 16 * y + 4 * g) / TK::EPC) + 4 * g % TK::EPC);
+                        const E4 k4 = *reinterpret_cast<const E4*>(sm.k + TK::off(row, (c0 + 8 * g + 4 * y) / TK::EPC) + 4 * y % TK::EPC);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float x = ec * dks[y][t][e];
@@ -879,8 +880,8 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
                 Frag k[2], q[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    k[y] = gdr_coln<DK>(sm.k, j, c0 + 16 * y, lane);
-                    q[y] = gdr_coln<DK>(sm.q, j, c0 + 16 * y, lane);
+                    k[y] = gdr_coln<DK, 8>(sm.k, j, c0 + 4 * y, lane);
+                    q[y] = gdr_coln<DK, 8>(sm.q, j, c0 + 4 * y, lane);
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
@@ -944,14 +945,10 @@ __global__ __launch_bounds__(512, 1) void kd_gdr_grad_kernel(GdrArgs a)
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int row = 16 * (r0 + t) + l16;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int e0 = c0 + 16 * y + 4 * g;
-            if (row >= c.rows || e0 >= a.dk) continue;
-            const int64_t to = ((c.base * a.T + c.first + row) * a.Hk + hk) * (int64_t)a.dk + e0;
-            *reinterpret_cast<E4*>((E*)a.dq + to) = E4{(E)dq[y][t][0], (E)dq[y][t][1], (E)dq[y][t][2], (E)dq[y][t][3]};
-            *reinterpret_cast<E4*>((E*)a.dk_ + to) = E4{(E)dk[y][t][0], (E)dk[y][t][1], (E)dk[y][t][2], (E)dk[y][t][3]};
-        }
+        if (row >= c.rows || c0 + 8 * g >= a.dk) continue;
+        const int64_t to = ((c.base * a.T + c.first + row) * a.Hk + hk) * (int64_t)a.dk + c0 + 8 * g;
+        T::st((E*)a.dq + to, T::pack(dq[0][t], dq[1][t]));
+        T::st((E*)a.dk_ + to, T::pack(dk[0][t], dk[1][t]));
     }
     }
 }
