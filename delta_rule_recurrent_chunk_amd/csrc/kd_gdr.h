@@ -10,8 +10,8 @@
 // A and P do not depend on the state: a first kernel makes them for all chunks
 // at once, a second one passes over the chunks with the state in registers.
 // The backward pass reads the same A and P, transposed.
-// The columns of S^T (values) do not mix, so every wave of the pass owns 16 of
-// them and needs nothing from another one.
+// The columns of S^T (values) do not mix: 16 of them are one wave's, and nothing
+// goes from group to group.
 //
 // 16x16x32 products (kd_device.h).  bf16: what is not a rounded input (S, U and
 // A) goes through as a rounded part and its remainder, 16 bits in all, so the
@@ -47,7 +47,7 @@ struct GdrArgs {
     void *dq, *dk_, *dv_, *dg, *dbeta;
     float* dS0;
     void *ds, *x, *x2;                         // dS leaving every chunk [slots, Hv, dv, dk], X [slots, Hv, 64, dv] (x2: its remainder)
-    // workspace of both
+    // workspace (kept from the forward for the backward)
     void* rec;                                 // the chunks' records: P and A in blocks, then gate factors
     const int* cu;
     int B, T, Hk, Hv, dk, dv;                  // packed: B sequences in T rows
@@ -405,8 +405,14 @@ struct GdrFetch {
 
 // Two groups of 16 value columns a workgroup instead of four, while that leaves
 // no more workgroups than compute units: both waves of a group have a SIMD for
-// themselves then (64 heads' sequences of 2048 tokens, 128 x 128: 77 us for 98).
-__host__ __forceinline__ bool gdr_narrow(const GdrArgs& a, int segs) { return (int64_t)segs * a.Hv * ((a.dv + 63) / 64) <= 128; }
+// themselves then (64 heads' sequences of 2048 tokens, 128 x 128: the forward
+// pass 77 us for 98).  From there on four (192 heads, 64 x 64: 98 us for 121;
+// backwards 137 for 174), but for packed sequences a little later: the short
+// ones' compute units come free (13 ragged ones of 12 heads, 64 x 64: 54 us for
+// 68, backwards 75 for 111).
+__host__ __forceinline__ bool gdr_narrow(const GdrArgs& a, int segs) {
+    return (int64_t)segs * a.Hv * ((a.dv + 63) / 64) <= (a.cu ? 192 : 128);
+}
 
 // What a pass reads of a chunk beside K and Q: the last PARTS parts of its record,
 // the gate factors, and C columns of V (or dO).  The workgroup's NT threads load

@@ -10,7 +10,9 @@ namespace kd {
 // K K^T and Q K^T take 16-row fragments straight from memory.  A by blocks of
 // 16: the four diagonal blocks by substitution, one column a lane; then row by
 // row of blocks A_ij = -A_ii sum_k T_ik A_kj in fp32 products, in place of T.
-// SAVE (for a backward pass): P's remainder too.
+// SAVE (for a backward pass): P's remainder too.  Bound by memory: 8 sequences
+// of 2048 tokens, 16 heads of 128, bf16: 54 us for 134 MB of keys and queries
+// and 89 MB of records (4.1 TB/s; a large copy reaches 4.9).
 template <class E, int DK, bool SAVE>
 __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 {
@@ -167,13 +169,22 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // A workgroup has CG groups of 16 columns: four, two waves to a SIMD, or two with
 // a SIMD for each wave (gdr_narrow; fp32, which needs the LDS).
 //
+// Bound by what a chunk waits for: K S, U, A U and the state's update follow each
+// other (four products, a packing of each result, two barriers), 3.0 us a chunk
+// where all compute units have a workgroup of four groups: 98 us for the 32
+// chunks of the sequences above (3.6 TB/s, matrix units busy in a third of the
+// cycles).  One wave for 16 columns, which made the outputs as well: 133 us; two
+// waves that share every product and hand each other halves through LDS: 122 us
+// (LDS has twice as much to move).
+//
 // Few heads and long sequences (gdr_plan): a sequence is cut into segments, all
 // of which pass at once.  A segment maps the state that enters it to S M + N.
 // GDR_MAPS passes over segments without their outputs, for N (from a zero
 // state) and for M (dk columns, from the identity and without values); a small
 // kernel chains them; then the pass runs from the states it found.  Without
 // outputs there are first waves alone, which load for themselves, in two
-// workgroups a compute unit.
+// workgroups a compute unit (32768 tokens of 16 heads in 8 segments: 213 us;
+// eight waves a workgroup that share K: 268 us), and the pass behind them 201 us.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
 template <class E, int DK, int MODE, int CG>
 __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
@@ -550,7 +561,7 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
 // A workgroup per 16 values of a head, in fp32 products: the state's
 // accumulators are the next product's B operand.  Its four waves make NT / 4
 // tiles of rows each and hand them to each other through LDS; maps load a
-// segment ahead.
+// segment ahead (3.3 us a segment; without, 3.7 us).
 template <int DK>
 __global__ __launch_bounds__(256, 1) void kd_gdr_chain_kernel(GdrArgs a)
 {
@@ -666,8 +677,9 @@ static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
 // chunk, however few workgroups there are; the maps cost about as much work
 // again as the pass itself.  So sequences are cut where they leave three
 // quarters of the 256 compute units idle, into segments of at least 8 chunks,
-// as many as make 256 workgroups (32768 tokens of 16 heads: 553 us; 512: 578).  Packed sequences are cut by
-// what their average length would be.
+// as many as make 256 workgroups (32768 tokens of 16 heads: 530 us; as many as
+// make 512: 578; in one piece: 1.7 ms).  Packed sequences are cut by what their
+// average length would be.
 void gdr_plan(GdrArgs& a, bool packed)
 {
     const int64_t wgs = (int64_t)a.B * a.Hv * ((a.dv + 63) / 64);
@@ -690,7 +702,7 @@ hipError_t launch_gdr_fwd(int bf16, const GdrArgs& a, hipStream_t st)
 // old state in one pass: with r = S k, s = S q,
 //     u = beta (v - e^g r),  S' = e^g S + u k^T,  o = scale (e^g s + u (k.q)).
 // A workgroup takes `rows` rows of one head's state.  Bound by reading and
-// writing the states.
+// writing the states: 32 requests, 16 heads of 128 x 128: 67 MB in 14.8 us.
 template <class E, int L>
 __global__ __launch_bounds__(256) void kd_gdr_step_kernel(const E* q, const E* k, const E* v, const void* gp, const void* bp,
                                                           const float* Si, float* So, E* o, int64_t qb, int64_t kb, int64_t vb,

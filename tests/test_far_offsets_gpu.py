@@ -1,0 +1,89 @@
+"""Offsets past 32 bits: caches, prompts and states of more than 2^31 elements."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _room(gib):
+    torch = _torch()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip("needs %d GiB of device memory" % gib)
+
+
+def test_pages_past_32_bits():
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    _room(16)
+    G = torch.Generator(device="cuda").manual_seed(1)
+    page, Hkv, d, few = 64, 4, 128, 40
+    pages = (1 << 31) // (page * Hkv * d) + few + 5
+    big = [torch.empty(pages, page, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    small = [torch.randn(few, page, Hkv, d, generator=G, device="cuda").bfloat16() for _ in range(2)]
+    far = pages - few
+    for b, s in zip(big, small):
+        b[far:].copy_(s)
+    B = 5
+    ids = torch.randperm(few, generator=G, device="cuda").int()
+    prefix, table = ids[:16], ids[16:36].view(B, 4).contiguous()
+    lens = torch.tensor([0, 70, 200, 63, 64], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, 16, d, generator=G, device="cuda").bfloat16()
+    k, v = (torch.randn(B, Hkv, d, generator=G, device="cuda").bfloat16() for _ in range(2))
+    freqs = torch.rand(d // 2, generator=G, device="cuda", dtype=torch.float64)
+    out = []
+    for (kp, vp), at in ((small, 0), (big, far)):
+        turned = kd.paged_append(k, v, kp, vp, table + at, lens, q=q, freqs=freqs, offset=1000)
+        out.append((turned, *kd.prefix_attn(turned, kp, vp, prefix + at, 1000, table + at, lens, return_lse=True)))
+    assert all(torch.equal(x, y) for x, y in zip(*out))
+    assert all(torch.equal(s, b[far:]) for s, b in zip(small, big))
+
+
+def test_packed_prompts_and_results_past_32_bits():
+    """More than 2^31 elements of q and o, one sequence behind another."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    _room(40)
+    G = torch.Generator(device="cuda").manual_seed(2)
+    Hq, Hkv, d, page = 32, 1, 128, 64
+    n = (1 << 31) // (Hq * d) + 100
+    q = torch.empty(n, Hq, d, dtype=torch.bfloat16, device="cuda")
+    q[-100:].normal_(generator=G)
+    k, v = (torch.randn(n, Hkv, d, generator=G, device="cuda").bfloat16() for _ in range(2))
+    kp, vp = (torch.zeros(4, page, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    freqs = torch.rand(d // 2, generator=G, device="cuda", dtype=torch.float64)
+    lens = torch.tensor([-1, 3], dtype=torch.int32, device="cuda")      # the first sequence is not in use
+    table = torch.tensor([[0, 1], [2, 1]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n - 100, n], dtype=torch.int32, device="cuda")
+    got = kd.paged_append(k, v, kp, vp, table, lens, q=q, cu_seqlens=cu, freqs=freqs)[-100:].clone()
+    kp2, vp2 = torch.zeros_like(kp), torch.zeros_like(vp)
+    want = kd.paged_append(k[-100:].clone(), v[-100:].clone(), kp2, vp2, table[1:], lens[1:], q=q[-100:].clone(),
+                           cu_seqlens=torch.tensor([0, 100], dtype=torch.int32, device="cuda"), freqs=freqs)
+    assert torch.equal(got, want) and torch.equal(kp, kp2) and torch.equal(vp, vp2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_delta_rule_with_far_batches(dtype):
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    _room(48)
+    G = torch.Generator(device="cuda").manual_seed(3)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    T, Hk, Hv, dk, dv = 130, 1, 2, 64, 72
+    buf = torch.empty((1 << 31) + (T + 4) * 4096, dtype=dt, device="cuda")
+    near = [torch.randn(2, T, h, d, generator=G, device="cuda").mul_(0.3).to(dt) for h, d in ((Hk, dk), (Hk, dk), (Hv, dv))]
+    # tokens 4096 elements apart, the second batch 2^31 behind the first
+    far = [buf.as_strided((2, T, *x.shape[2:]), (1 << 31, 4096, x.shape[3], 1), 512 * i) for i, x in enumerate(near)]
+    for f, x in zip(far, near):
+        f.copy_(x)
+    g = torch.nn.functional.logsigmoid(torch.randn(2, T, Hv, generator=G, device="cuda")).to(dt)
+    beta = torch.rand(2, T, Hv, generator=G, device="cuda").to(dt)
+    dO = torch.randn(2, T, Hv, dv, generator=G, device="cuda").to(dt)
+    out = []
+    for q, k, v in (near, far):
+        o, ST, saved = kd.gdr_fwd(q, k, v, g, beta, save_states=True)
+        out.append(dict(o=o, ST=ST, **kd.gdr_bwd(q, k, v, g, beta, saved, dO)))
+    assert all(torch.equal(out[0][n], out[1][n]) for n in out[0])

@@ -331,7 +331,7 @@ def test_backward_of_many_heads(B, T, Hk, Hv, dk, dv):
 
 def test_backward_of_many_packed_sequences():
     torch = _torch()
-    lens = [(37 * i) % 71 for i in range(70)]
+    lens = [(37 * i) % 71 for i in range(110)]
     cu = np.concatenate([[0], np.cumsum(lens)])
     t = inputs((int(cu[-1]),), 1, 2, 64, 64, "bf16", 31, n=len(lens))
     got = run(t, 0.2, torch.tensor(cu, dtype=torch.int32, device="cuda"))

@@ -282,7 +282,8 @@ def append_ref(c, k, v, q, rot, layout, offset, scale=1.0):
     ([0], [1], 16, 1, 1, 64, 64), ([0, 5, -1, 40], [1] * 4, 16, 4, 2, 128, 128), ([3, 0, 17], [1] * 3, 1, 0, 4, 32, 0),
     ([0, 0, 7, -3, 20], [50, 0, 1, 4, 33], 24, 6, 2, 64, 36), ([0, 2], [130, 9], 64, 16, 4, 128, 64),
     ([9, 1], [3, 2], 5, 3, 3, 96, 34), ([0], [300], 7, 2, 1, 256, 256), ([4, 0], [2, 5], 16, 5, 1, 8, 2),
-    ([0, 1], [6, 7], 16, 40, 8, 128, 128)])
+    ([0, 1], [6, 7], 16, 40, 8, 128, 128), ([0, 0, 9], [3100, 1, 2050], 64, 2, 1, 64, 64), ([5], [8500], 128, 1, 1, 8, 8),
+    ([0, 3], [2030, 1100], 48, 20, 4, 128, 64)])
 def test_append(lens, new, page, Hq, Hkv, d, rot, layout, dtype):
     import delta_rule_recurrent_chunk_amd as kd
     torch = _torch()
