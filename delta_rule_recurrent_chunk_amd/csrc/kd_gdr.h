@@ -184,6 +184,18 @@ struct GdrT<__bf16> {
         }
         return __builtin_bit_cast(Frag, r);
     }
+    // and what that has left (p and q were rounded from it)
+    static __device__ __forceinline__ Frag rest(floatx4 x, floatx4 y, Frag p, Frag q) {
+        const uintx4 u = __builtin_bit_cast(uintx4, p), v = __builtin_bit_cast(uintx4, q);
+        uintx4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = i < 2 ? x[2 * i] : y[2 * i - 4], b = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+            r[i] = two((a - __uint_as_float(u[i] << 16)) - __uint_as_float(v[i] << 16),
+                       (b - __uint_as_float(u[i] & 0xffff0000u)) - __uint_as_float(v[i] & 0xffff0000u));
+        }
+        return __builtin_bit_cast(Frag, r);
+    }
     static __device__ __forceinline__ Frag ld(const __bf16* p) { return *reinterpret_cast<const Frag*>(p); }
     static __device__ __forceinline__ void st(__bf16* p, Frag f) { *reinterpret_cast<Frag*>(p) = f; }
     // natural fragment of a tile's row r: columns 32 ks + 8 g ..
@@ -263,6 +275,7 @@ struct GdrT<float> {
         return Frag{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     }
     static __device__ __forceinline__ Frag rest(floatx4, floatx4, Frag p) { return p; }
+    static __device__ __forceinline__ Frag rest(floatx4, floatx4, Frag p, Frag) { return p; }
     static __device__ __forceinline__ Frag ld(const float* p) {
         const floatx4 x = *reinterpret_cast<const floatx4*>(p), y = *reinterpret_cast<const floatx4*>(p + 4);
         return pack(x, y);

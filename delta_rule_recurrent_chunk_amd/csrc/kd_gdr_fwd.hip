@@ -286,7 +286,7 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
             const GdrSide<E, W, NC0>& sd = sm.side[OUT ? 0 : par];
             const E* rec = sd.rec + lane * 8;
             auto factor = [&](int i, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * i + 16 * t + 4 * g); };
-            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
+            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], f3[2], kc[2 * NK];
             floatx4 U[4], be[4], bb[4], bc[4], v[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -337,6 +337,7 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+                f3[j] = T::rest(U[2 * j], U[2 * j + 1], f[j], f2[j]);
             }
             const float eC = sd.vec[256];
             if (OUT) {
@@ -361,6 +362,8 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A[gdr_block(t, j)], f2[j], U[t]);
 #pragma unroll
                     for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A2[gdr_block(t, j)], f[j], U[t]);
+#pragma unroll
+                    for (int t = 2 * j; t < 4; ++t) U[t] = T::mma(A[gdr_block(t, j)], f3[j], U[t]);
                 }
             }
 #pragma unroll
@@ -379,6 +382,7 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+                f3[j] = T::rest(U[2 * j], U[2 * j + 1], f[j], f2[j]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -387,6 +391,8 @@ __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1
                 if (T::TWO) {
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
+#pragma unroll
+                    for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f3[j], S[y]);
                 }
                 if (j == 0)
 #pragma unroll

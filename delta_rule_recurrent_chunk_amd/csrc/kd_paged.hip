@@ -6,8 +6,8 @@
 // p = lens[b] + r.  Its key (and its queries, when they are given) turn to
 // position offset + p as in kd_rope.hip, its value is copied.
 //
-// Bound by memory: every element is read and written once (13200 rows of 16
-// queries, 4 keys and 4 values of 128, bf16: 162 MB in 34 us, 4.7 TB/s; a large
+// Bound by memory: every element is read and written once (13050 rows of 16
+// queries, 4 keys and 4 values of 128, bf16: 160 MB in 34 us, 4.7 TB/s; a large
 // copy reaches 4.9).  A workgroup takes up to eight rows; sines and cosines are
 // made once for a row's heads; the first pieces load while its waves look the
 // rows' sequences and pages up.
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void kd_append_kernel(AppendArgs a)
 
 // A workgroup takes as many rows as leave 1024 workgroups, eight at most: the
 // angles' parts are read once for them, and small calls spread over the chip
-// (13200 rows of 20 + 4 heads of 128: 34 us with eight, 38 with five, 40 with
+// (13050 rows of 20 + 4 heads of 128: 34 us with eight, 38 with five, 40 with
 // one; 32 rows: 5.9 us with one, 9.2 with three).  Returns the workgroups.
 static int64_t append_plan(AppendArgs& a, int es, int& mode)
 {

@@ -17,11 +17,11 @@
 //  * own keys of single rows: 4 independent waves a workgroup, each with the
 //    heads of one group as columns and its own tiles (a step's own keys: bound
 //    by reading them).
-// 64 rows of 16 heads over 4 key heads, 32768 shared keys, up to 1000 own ones: 45
-// us for 130 MB of keys and values (2.9 TB/s; of it 2 us a tile of 64 keys,
-// whose scores, exponentials and sums follow each other), 7 us the join.  2400 such
-// rows, 8192 shared keys: 174 us (925 TFLOP/s; a large product reaches 1195),
-// 20 us the join.
+// 64 rows of 16 heads over 4 key heads, 32768 shared keys, up to 1000 own ones: 51
+// us, 7 of them the join, for 130 MB of keys and values (2.6 TB/s; a tile of 64
+// keys takes 2 us: its scores, exponentials and sums follow each other).  2015
+// such rows, 8192 shared keys: 174 us, 18 of them the join (780 TFLOP/s; a large
+// product reaches 1195).
 // Products, K order and tiles are those of kd_swa.h.
 #include "kd_check.h"
 #include "kd_paged.h"
@@ -545,7 +545,7 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
 // joining of its rows, little (3 rows of 16 heads over 4 key heads, 2000 keys, us
 // at 8, 16 and 32 parts: 12.2, 9.1, 7.2).  Beyond that two workgroups share a
 // compute unit, where a tile takes each of them 1.6 times as long as one alone,
-// and a part costs its rows' traffic, as long as 8 tiles (4800 such rows, 8192
+// and a part costs its rows' traffic, as long as 8 tiles (2015 such rows, 8192
 // keys, us at 1, 2, 8 and 24 parts: 241, 174, 194, 257).
 static int prefix_splits(int64_t items, int P)
 {
@@ -609,7 +609,7 @@ static hipError_t prefix(PrefixArgs a, hipStream_t st)
     a.nprefix = (int)swa_grid((int64_t)a.blocks * a.Hkv * a.sp);
     const unsigned grid = (unsigned)prefix_grid(a, a.cu != nullptr, PrefixLds<E, D>::ITEMS);
     // few blocks of rows read the prefix from memory, many from a cache (2 blocks,
-    // 32768 keys: 45.4 us with tiles of 32 keys, 46.6 with 64; 75 blocks, 8192
+    // 32768 keys: 45.4 us with tiles of 32 keys, 46.6 with 64; 63 blocks, 8192
     // keys: 191 and 178)
     if (sizeof(E) == 4 || a.blocks <= 4) kd_prefix_kernel<E, D, 32><<<grid, 256, 0, st>>>(a);
     else kd_prefix_kernel<E, D, sizeof(E) == 4 ? 32 : 64><<<grid, 256, 0, st>>>(a);
@@ -617,7 +617,7 @@ static hipError_t prefix(PrefixArgs a, hipStream_t st)
     if (e != hipSuccess) return e;
     // A row's parts one after the other where rows are many, shared out to four
     // waves where they are few (1024 rows, 40 parts: 7.8 and 7.4 us; 48 rows, 34
-    // parts: 6.1 and 4.8; 38400 rows, 3 parts: 20 and 69).
+    // parts: 6.1 and 4.8; 32240 rows, 3 parts: 20 and 69).
     const int64_t rows = (int64_t)a.T * a.Hq;
     if (a.sp + a.so <= 8 || rows > 8192) kd_prefix_join_kernel<E, D, 4><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
     else kd_prefix_join_kernel<E, D, 1><<<(unsigned)rows, 256, 0, st>>>(a);
