@@ -111,7 +111,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             const E* kt = sm.k[buf];
             const GdrSide<E, W, NC0>& sd = sm.side[FAR ? buf : 0];
             auto factor = [&](int f, int t) { return *reinterpret_cast<const floatx4*>(sd.vec + 64 * f + 16 * t + 4 * g); };
-            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], kc[2 * NK];
+            Frag sh[NK], sl[NK], x[4], A[6], A2[6], f[2], f2[2], f3[2], kc[2 * NK];
             floatx4 U[4], X[4], bb[4], bc[4], po[4], qo[2 * NK];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -165,6 +165,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(U[2 * j], U[2 * j + 1]);
                 f2[j] = T::rest(U[2 * j], U[2 * j + 1], f[j]);
+                f3[j] = T::rest(U[2 * j], U[2 * j + 1], f[j], f2[j]);
             }
             const float eC = sd.vec[256];
             lds_barrier();
@@ -180,6 +181,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                     for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A[gdr_block_t(t, j)], f2[j], X[t]);
 #pragma unroll
                     for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A2[gdr_block_t(t, j)], f[j], X[t]);
+#pragma unroll
+                    for (int t = 0; t < 2 + 2 * j; ++t) X[t] = T::mma(A[gdr_block_t(t, j)], f3[j], X[t]);
                 }
             }
             const auto ds = gdr_buffer((const E*)a.ds + ((int64_t)(s.slot0 + n) * a.Hv + hv) * a.dv * a.dk, (int64_t)a.dv * a.dk * (int)sizeof(E));
@@ -207,6 +210,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             for (int j = 0; j < 2; ++j) {
                 f[j] = T::pack(X[2 * j], X[2 * j + 1]);
                 f2[j] = T::rest(X[2 * j], X[2 * j + 1], f[j]);
+                f3[j] = T::rest(X[2 * j], X[2 * j + 1], f[j], f2[j]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -215,6 +219,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                 if (T::TWO) {
 #pragma unroll
                     for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f2[j], S[y]);
+#pragma unroll
+                    for (int y = 0; y < 2 * NK; ++y) S[y] = T::mma(kc[y], f3[j], S[y]);
                 }
                 if (j == 0)
 #pragma unroll
@@ -292,7 +298,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
         if (FAR) lds_barrier();
         if (before) {
             floatx4 dO[4];
-            Frag d[2], d2[2];
+            Frag d[2], d2[2], d3[2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) dO[t] = T::template ld_acc<NC0>(sm.side[fb].v, t, 16 * cg, lane);
 #pragma unroll
@@ -309,6 +315,7 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
             for (int j = 0; j < 2; ++j) {
                 d[j] = T::pack(dO[2 * j], dO[2 * j + 1]);
                 d2[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j]);
+                d3[j] = T::rest(dO[2 * j], dO[2 * j + 1], d[j], d2[j]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -322,6 +329,8 @@ __global__ __launch_bounds__(128 * CG, CG == 4 ? 2 : 1) void kd_gdr_back_kernel(
                     if (T::TWO) {
 #pragma unroll
                         for (int y = 0; y < 4; ++y) QO[y0 + y] = T::mma(z[y], d2[j], QO[y0 + y]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) QO[y0 + y] = T::mma(z[y], d3[j], QO[y0 + y]);
                     }
                 }
         }
