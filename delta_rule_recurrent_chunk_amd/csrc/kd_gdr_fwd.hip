@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // Bound by what a chunk waits for: K S, U, A U and the state's update follow each
 // other (four products, a packing of each result, two barriers), 3.0 us a chunk
 // where all compute units have a workgroup of four groups: 98 us for the 32
-// chunks of the sequences above (3.6 TB/s, matrix units busy in a third of the
+// chunks of the sequences above (3.6 TB/s, matrix units busy in 37% of the
 // cycles).  One wave for 16 columns, which made the outputs as well: 133 us; two
 // waves that share every product and hand each other halves through LDS: 122 us
 // (LDS has twice as much to move).
@@ -183,8 +183,9 @@ __global__ __launch_bounds__(64, 1) void kd_gdr_prep_kernel(GdrArgs a)
 // state) and for M (dk columns, from the identity and without values); a small
 // kernel chains them; then the pass runs from the states it found.  Without
 // outputs there are first waves alone, which load for themselves, in two
-// workgroups a compute unit (32768 tokens of 16 heads in 8 segments: 213 us;
-// eight waves a workgroup that share K: 268 us), and the pass behind them 201 us.
+// workgroups a compute unit (32768 tokens of 16 heads in 8 segments: 230 us;
+// eight waves a workgroup that share K take a quarter longer), and the pass behind
+// them 200 us.
 enum { GDR_OUT, GDR_SAVE, GDR_MAPS };
 template <class E, int DK, int MODE, int CG>
 __global__ __launch_bounds__((MODE == GDR_MAPS ? 64 : 128) * CG, CG == 4 ? 2 : 1) void kd_gdr_pass_kernel(GdrArgs a, int run)
@@ -683,9 +684,9 @@ static hipError_t gdr_passes(const GdrArgs& a, hipStream_t st)
 // chunk, however few workgroups there are; the maps cost about as much work
 // again as the pass itself.  So sequences are cut where they leave three
 // quarters of the 256 compute units idle, into segments of at least 8 chunks,
-// as many as make 256 workgroups (32768 tokens of 16 heads: 530 us; as many as
-// make 512: 578; in one piece: 1.7 ms).  Packed sequences are cut by what their
-// average length would be.
+// as many as make 256 workgroups (32768 tokens of 16 heads: 25 us less than with
+// 512, most of it in the chain; in one piece 1.7 ms for 0.5).  Packed sequences
+// are cut by what their average length would be.
 void gdr_plan(GdrArgs& a, bool packed)
 {
     const int64_t wgs = (int64_t)a.B * a.Hv * ((a.dv + 63) / 64);
