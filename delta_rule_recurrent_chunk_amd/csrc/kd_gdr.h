@@ -215,12 +215,6 @@ struct GdrT<__bf16> {
         const int l = lane & 15, r = 32 * j + 4 * (lane >> 4) + (l >> 2), c = c0 + 8 * (l & 3);
         return tr<D>(tile, r, c);
     }
-    // the same with row m = column c0 + m
-    template <int D>
-    static __device__ __forceinline__ Frag ld_col(const __bf16* tile, int j, int c0, int lane) {
-        const int l = lane & 15, r = 32 * j + 4 * (lane >> 4) + (l >> 2), c = c0 + 4 * (l & 3);
-        return tr<D>(tile, r, c);
-    }
     // rows 16 t + 4 g .. + 3 of column c0 + l16, as an accumulator holds them
     template <int D>
     static __device__ __forceinline__ floatx4 ld_acc(const __bf16* tile, int t, int c0, int lane) {
@@ -300,10 +294,6 @@ struct GdrT<float> {
         return at<D>(tile, j, c0 + 8 * (m >> 2) + (m & 3), lane);
     }
     template <int D>
-    static __device__ __forceinline__ Frag ld_col(const float* tile, int j, int c0, int lane) {
-        return at<D>(tile, j, c0 + (lane & 15), lane);
-    }
-    template <int D>
     static __device__ __forceinline__ floatx4 ld_acc(const float* tile, int t, int c0, int lane) {
         typedef SwaTile<float, D> TL;
         const int c = c0 + (lane & 15), r = 16 * t + 4 * (lane >> 4);
@@ -347,24 +337,6 @@ __device__ __forceinline__ floatx4 gdr_mma2(typename GdrT<E>::Frag a, typename G
     if (GdrT<E>::TWO) c = GdrT<E>::mma(a2, b, c);
     return c;
 }
-template <class E>
-__device__ __forceinline__ floatx4 gdr_mma2b(typename GdrT<E>::Frag a, typename GdrT<E>::Frag b, typename GdrT<E>::Frag b2, floatx4 c) {
-    c = GdrT<E>::mma(a, b, c);
-    if (GdrT<E>::TWO) c = GdrT<E>::mma(a, b2, c);
-    return c;
-}
-// both with remainders (their product is left out: 2^-18)
-template <class E>
-__device__ __forceinline__ floatx4 gdr_mma3(typename GdrT<E>::Frag a, typename GdrT<E>::Frag a2, typename GdrT<E>::Frag b,
-                                            typename GdrT<E>::Frag b2, floatx4 c) {
-    c = GdrT<E>::mma(a, b, c);
-    if (GdrT<E>::TWO) {
-        c = GdrT<E>::mma(a2, b, c);
-        c = GdrT<E>::mma(a, b2, c);
-    }
-    return c;
-}
-
 template <class E>
 __host__ __device__ constexpr int gdr_part() { return GDR_BLOCKS * 512; }      // elements of a part
 // A record: P and A, then the gate factors.  In bf16 both have a remainder, P's
