@@ -18,7 +18,8 @@
 // to a state as two remainders (U before A and after it; backwards dU, X and
 // dO with its factor): with 16 bits of those the last state is off by 3.5e-6 of
 // it and the first one's gradient by 2.7e-6, with 24 by 0.7e-6 and 0.6e-6 (what
-// 16 bits of S and A leave), for a tenth more products, of the passes' time 3%.
+// 16 bits of S and A leave), for a quarter more products (3% of the passes' time
+// with two groups of columns a workgroup, up to a fifth backwards with four).
 // P, which only reaches o, is rounded.  fp32: the same fragments through eight
 // fp32 products.
 #pragma once
