@@ -94,7 +94,8 @@ __device__ __forceinline__ GdrSeq gdr_seq(const GdrArgs& a, int s) {
 }
 // Segment `slot` as a sequence of its own, with its number and whether it is the
 // last of its sequence.  Packed: sequence s owns the slots cu[s] / 64 / seg + s
-// onwards.  False when the slot holds none.  The whole wave calls it.
+// onwards.  False when the slot holds none (with offsets that are out of order
+// also when it comes before its sequence's first).  The whole wave calls it.
 struct GdrSegment {
     GdrSeq s;
     int seq, j;
@@ -118,14 +119,14 @@ __device__ __forceinline__ bool gdr_segment(const GdrArgs& a, int slot, GdrSegme
     const int NC = gdr_chunks(r.s.T);
     if (a.cu) r.j = slot - (r.s.row0 / GDR_C / a.seg + r.seq);
     const int c0 = r.j * a.seg;
-    if (c0 > 0 && c0 >= NC) return false;
+    if (r.j < 0 || (c0 > 0 && c0 >= NC)) return false;
     r.last = NC - c0 <= a.seg;
     r.s.row0 += c0 * GDR_C;
     r.s.T = r.last ? r.s.T - c0 * GDR_C : a.seg * GDR_C;
     r.s.slot0 += c0;
     return true;
 }
-// The chunk in a slot, false when it holds none.  The whole wave calls it.
+// The chunk in a slot, false when it holds none (as above).  The whole wave calls it.
 __device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c) {
     if (!a.cu) {
         const int nc = gdr_chunks(a.T);
@@ -146,7 +147,7 @@ __device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c
     c.first = s.row0 + c.n * GDR_C;
     c.rows = min(s.T - c.n * GDR_C, GDR_C);
     c.base = s.b;
-    return c.rows > 0;
+    return c.n >= 0 && c.rows > 0;
 }
 
 // Block (i, j) of a lower triangular matrix: rows 16 i .., columns 32 j ..;

@@ -434,9 +434,11 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
         }
         if (n == 0) return;
         const int b = n - 1, q0 = min(max(a.cu[b], 0), a.T), q1 = min(max(a.cu[b + 1], q0), a.T);
-        const int nrows = (q1 - q0) * G, r0 = (slot - (int)((int64_t)q0 * G / PREFIX_ROWS + b)) * PREFIX_ROWS;
+        const int nrows = (q1 - q0) * G, blk = slot - (int)((int64_t)q0 * G / PREFIX_ROWS + b);
         const int len = a.lens[b];
-        if (r0 >= nrows || len < 0) return;
+        // (blk is negative where offsets are out of order)
+        if (blk < 0 || (int64_t)blk * PREFIX_ROWS >= nrows || len < 0) return;
+        const int r0 = blk * PREFIX_ROWS;
         // keys that the block's last row sees, as far as the table goes
         const int64_t all = min((int64_t)len + min(r0 + PREFIX_ROWS - 1, nrows - 1) / G + 1, (int64_t)a.width * a.page);
         const int nk = (int)min(all, (int64_t)INT32_MAX - 64), tiles = (nk + 63) / 64, per = (tiles + a.so - 1) / a.so;

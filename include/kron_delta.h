@@ -602,10 +602,11 @@ KD_API kd_status kron_delta_swa_cache_store(const kd_swa_cache_desc *desc, int32
  * i % page of page table[b * table_stride + i / page], i / page < width.
  * Sequences have either one row each in a call (T = B, cu_seqlens NULL), or
  * cu_seqlens[b + 1] - cu_seqlens[b] packed rows (offsets int32 [B + 1] on the
- * device, non-decreasing, at most T).  lens[b] (int32, on the device, not
- * changed) is the number of own tokens before the call's: row r of sequence b
- * is own token lens[b] + r.  A negative lens[b] marks an unused sequence.
- * Rows that no sequence holds are left unwritten.
+ * device, non-decreasing, at most T; out of order they give rows without
+ * meaning, none outside the tensors).  lens[b] (int32, on the device, not changed) is the
+ * number of own tokens before the call's: row r of sequence b is own token
+ * lens[b] + r.  A negative lens[b] marks an unused sequence.  Rows that no
+ * sequence holds are left unwritten.
  */
 typedef struct {
     int32_t B, T, Hq, Hkv, d;
@@ -690,7 +691,8 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *    are computed as they are.
  *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of T
  *    rows, offsets int32 [B + 1] on the device, non-decreasing from 0 to T
- *    (clamped into that range where they are read); the batch strides are
+ *    (clamped into that range where they are read; out of order they give rows
+ *    without meaning, none outside the tensors); the batch strides are
  *    ignored, the states are [B, Hv, dv, dk].  Rows that no sequence covers are
  *    left unwritten.
  *  * Tokens are taken 64 at a time: a token with an infinity or a NaN in it
