@@ -532,7 +532,9 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
         for (int y = 1; y < SHARE; ++y) sum += part[w + y][lane];
     }
     if (!held) return;
-    const bool none = M == -INFINITY;
+    // What a row sees is a matter of its keys' number: scores that are all NaN leave
+    // M at -infinity too (with L a NaN), and so do scores of -infinity (0 / 0).
+    const bool none = a.lens[b] < 0 || (a.P == 0 && a.width == 0);
     const float inv = none ? 0.f : 1.f / L;
     if (lane * N < D) {
         E* o = (E*)a.o + at * D + lane * N;

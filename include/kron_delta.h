@@ -655,8 +655,9 @@ KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *
  *    nothing, get o = 0 and lse = -infinity.  Page ids outside [0, pages) are
  *    clamped into that range where they are read.
  *  * What a row does not see (later rows' keys, slots behind the last key) may
- *    hold infinities and NaNs; those that are seen show as IEEE arithmetic has
- *    them.
+ *    hold infinities and NaNs; those that are seen, and those of the row's own
+ *    query, show as IEEE arithmetic has them (keys that all have a score of
+ *    -infinity: o is a NaN, lse -infinity).
  *  * ws: kron_delta_prefix_attn_workspace_bytes(desc, cu_seqlens != NULL)
  *    bytes, contents on entry ignored.  Calls that overlap on the device must
  *    not share it.

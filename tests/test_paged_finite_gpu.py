@@ -1,0 +1,79 @@
+"""Attention over a shared prefix where queries, keys and values are not finite, and where rows are nobody's."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_ref as R
+from test_paged_gpu import Case, _torch, check, f64
+
+pytestmark = pytest.mark.gpu
+
+# packed or one row per sequence; rows see the prefix and own keys, own keys alone, one own key alone
+BATCHES = [(False, [3, 0, 200, 70], [1] * 4, 100), (False, [3, 0, 200, 70], [1] * 4, 0), (False, [0, 0], [1, 1], 0),
+           (True, [3, 0, 9], [20, 40, 2], 300), (True, [3, 0, 9], [20, 40, 2], 0), (True, [0, 0], [1, 1], 0)]
+
+
+def compare(c, o, lse, scale=None, atol=0.0):
+    """Against plain arithmetic in 64 bits: scores that are NaN or +infinity make NaNs; keys of score -infinity weigh
+    nothing, and a row that sees no other has no weights (0 / 0) and the logarithm of 0."""
+    scale = 1.0 / math.sqrt(c.d) if scale is None else scale
+    q, k, v = f64(c.q), f64(c.kp), f64(c.vp)
+    u = 2.0 ** -8 if c.dt == _torch().bfloat16 else R.W
+    for r, owner in enumerate(R.rows_of(c.lens, c.cu, c.T)):
+        if owner is None or owner[1] is None:
+            continue
+        at = R.keys_of(owner, c.lens, c.cu, c.ptable, c.P, c.table, c.page, c.pages)
+        pg, sl = (np.array([x[i] for x in at], int) for i in (0, 1))
+        for h in range(c.Hq):
+            hk = h // (c.Hq // c.Hkv)
+            with np.errstate(invalid="ignore"):
+                s = (k[pg, sl, hk] @ q[r, h]) * scale
+                ro, eo, rl, el = R.attend(q[r, h], k[pg, sl, hk], v[pg, sl, hk], scale, u)
+            if np.isneginf(s).all():
+                ro, rl = np.full(c.d, np.nan), -np.inf
+            elif np.isneginf(s).any() and np.isfinite(s).any() and not np.isnan(s).any():
+                live = np.isfinite(s)      # (the bounds come from the keys that weigh something)
+                ro, eo, rl, el = R.attend(q[r, h], k[pg, sl, hk][live], v[pg, sl, hk][live], scale, u)
+            check("o of row %d, head %d" % (r, h), o[r, h], ro, eo)
+            check("lse of row %d, head %d" % (r, h), np.float64(lse[h, r].item()), np.float64(rl), el)
+
+
+def case(i, dtype, seed):
+    packed, lens, new, P = BATCHES[i]
+    print("batch", BATCHES[i], dtype, flush=True)
+    return Case(lens, new, P, 16, 4, 2, 64, dtype, seed=seed, packed=packed)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("i", range(len(BATCHES)))
+def test_a_query_that_is_not_finite_shows(i, value, dtype):
+    c = case(i, dtype, 40 + i)
+    c.q[1, 2, 5] = float(value)
+    o, lse = c.run(return_lse=True)
+    compare(c, o, lse)
+    assert np.isnan(f64(o)[1, 2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("i", range(len(BATCHES)))
+def test_keys_that_are_not_finite_show(i, value, dtype):
+    """All keys of one head in pages that the second sequence alone sees."""
+    c = case(i, dtype, 50 + i)
+    own = [int(p) for p in c.table[1] if p >= 0]
+    c.kp[own, :, 1, 3] = float(value)
+    o, lse = c.run(return_lse=True)
+    compare(c, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_rows_whose_scores_are_all_minus_infinity(packed, dtype):
+    c = Case([3, 40], [1, 1], 70, 16, 4, 2, 64, dtype, seed=60, packed=packed)
+    c.kp[..., 7] = c.kp[..., 7].abs() + 0.5
+    c.q[0, 1, 7] = float("-inf")
+    o, lse = c.run(return_lse=True)
+    compare(c, o, lse)
+    assert np.isnan(f64(o)[0, 1]).all() and np.isneginf(lse[1, 0].item())
