@@ -32,6 +32,7 @@ namespace kd {
 constexpr int PREFIX_ROWS = 128;          // rows of a workgroup
 constexpr int PREFIX_MOST = 48;           // splits of the prefix
 constexpr int PREFIX_OWN_MOST = 16;       // and of the own keys
+constexpr float PREFIX_EMPTY = -1.f;      // sum of a part that has not been written
 
 // Where keys are: a list of pages of one head.  Ids outside the cache are
 // clamped into it, numbers past the last key to that key (they are masked).
@@ -464,8 +465,8 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
     const int64_t all = len < 0 ? 0 : min((int64_t)len + 1, (int64_t)a.width * a.page);
     const int nk = (int)min(all, (int64_t)INT32_MAX - 64), tiles = (nk + 31) / 32, per = (tiles + a.so - 1) / a.so;
     const int k0 = (int)min((int64_t)so * per * 32, (int64_t)nk), k1 = (int)min((int64_t)k0 + (int64_t)per * 32, (int64_t)nk);
-    if (k0 >= k1) {      // (a split without keys weighs nothing; its o is not read)
-        if (lane < nh) *reinterpret_cast<float2*>(a.ml + 2 * (part + lane)) = make_float2(-INFINITY, 0.f);
+    if (k0 >= k1) {      // (a split without keys: its o, which is not written, is not read)
+        if (lane < nh) *reinterpret_cast<float2*>(a.ml + 2 * (part + lane)) = make_float2(-INFINITY, PREFIX_EMPTY);
         return;
     }
     K.k = (const E*)a.kc + hk * a.kcs[2];
@@ -498,13 +499,15 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
     float M = -INFINITY, L = 0.f;
     if (held) {
         const int64_t rows = (int64_t)a.T * G, row = (int64_t)(h / G) * rows + (int64_t)t * G + h % G;
-        float2 x = make_float2(-INFINITY, 0.f);
+        float2 x = make_float2(-INFINITY, PREFIX_EMPTY);
         if (lane < S && a.lens[b] >= 0) x = *reinterpret_cast<const float2*>(a.ml + 2 * (lane * (int64_t)a.Hkv * rows + row));
         M = x.x;
 #pragma unroll
         for (int y = 32; y > 0; y /= 2) M = fmaxf(M, __shfl_xor(M, y));
-        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - M);
-        L = f * x.y;
+        // (a part of no weight counts all the same: 0 times an infinity that is seen)
+        const bool empty = x.y == PREFIX_EMPTY;
+        const float f = empty ? PREFIX_EMPTY : x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - M);
+        L = empty ? 0.f : f * x.y;
 #pragma unroll
         for (int y = 32; y > 0; y /= 2) L += __shfl_xor(L, y);
         const float* p = a.part + row * D + (lane * N < D ? lane * N : 0);
@@ -517,8 +520,8 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const int i = s0 + s * SHARE;
-                const float fs = i < S ? __shfl(f, i & 63) : 0.f;
-                if (fs == 0.f) continue;      // (nothing was written where a split has no keys)
+                const float fs = i < S ? __shfl(f, i & 63) : PREFIX_EMPTY;
+                if (fs == PREFIX_EMPTY) continue;
 #pragma unroll
                 for (int e = 0; e < N; ++e) sum[e] = fmaf(fs, v[s][e], sum[e]);
             }

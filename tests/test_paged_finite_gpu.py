@@ -77,3 +77,20 @@ def test_rows_whose_scores_are_all_minus_infinity(packed, dtype):
     o, lse = c.run(return_lse=True)
     compare(c, o, lse)
     assert np.isnan(f64(o)[0, 1]).all() and np.isneginf(lse[1, 0].item())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("where", ["own", "prefix"])
+def test_an_infinite_value_of_no_weight_shows(where, packed, dtype):
+    """Weights below fp32's range: e^-400 of infinity is not 0."""
+    c = Case([5, 2], [1, 1], 40, 16, 2, 1, 64, dtype, seed=61, packed=packed)
+    big = [int(p) for p in c.ptable] if where == "own" else [int(p) for p in c.table[0] if p >= 0]
+    c.q[0] = 0
+    c.q[0, :, 0] = 20
+    c.kp[:, :, :, 0] = 0
+    c.kp[big, :, :, 0] = 160        # scores of 400 there, of 0 elsewhere
+    pg, sl = (int(c.table[0, 0]), 1) if where == "own" else (int(c.ptable[1]), 2)
+    c.vp[pg, sl, 0, 9] = float("inf")
+    o = f64(c.run())
+    assert not np.isfinite(o[0, :, 9]).any() and np.isfinite(np.delete(o[0], 9, -1)).all()
