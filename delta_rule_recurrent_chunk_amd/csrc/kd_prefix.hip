@@ -46,20 +46,22 @@ struct PrefixKeys {
     __device__ __forceinline__ int id(int at) const { return min(max(pages[at], 0), most); }
 };
 
-// o of a wave's rows again (rare, see its call), from the maxima it has: key
-// by key, each for the rows that see it (key <= lim).
+// o of those of a wave's rows that ask for it (`again`; rare, see its calls),
+// from the maxima they have: key by key, each for the rows that see it (key <=
+// lim).
 template <class E, int D>
 __device__ __forceinline__ void prefix_single(floatx16* o, const typename SwaT<E>::Frag* q, const PrefixKeys<E>& K, int first,
-                                              int last, int lim, float c, float mu, int lane)
+                                              int last, int lim, float c, float mu, bool again, int lane)
 {
     typedef SwaT<E> T;
     typedef E E4 __attribute__((ext_vector_type(4)));
     constexpr int NK = D / T::KC, ND = D / 32;
     const int g = lane >> 5;
+    if (again)
 #pragma unroll
-    for (int i = 0; i < ND; ++i)
+        for (int i = 0; i < ND; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+            for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
 #pragma unroll 1
     for (int key = first; key <= last; ++key) {
         const int64_t pg = K.id(key / K.page), slot = key % K.page;
@@ -71,14 +73,15 @@ __device__ __forceinline__ void prefix_single(floatx16* o, const typename SwaT<E
         s += swa_swap(s);
         const bool sees = key <= lim;
         const float p = sees ? __builtin_amdgcn_exp2f(fmaf(s, c, -mu)) : 0.f;
+        if (again)
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
+            for (int i = 0; i < ND; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const E4 x = *reinterpret_cast<const E4*>(vr + 32 * i + 8 * j + 4 * g);
+                for (int j = 0; j < 4; ++j) {
+                    const E4 x = *reinterpret_cast<const E4*>(vr + 32 * i + 8 * j + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][4 * j + e] = fmaf(p, sees ? (float)x[e] : 0.f, o[i][4 * j + e]);
-            }
+                    for (int e = 0; e < 4; ++e) o[i][4 * j + e] = fmaf(p, sees ? (float)x[e] : 0.f, o[i][4 * j + e]);
+                }
     }
 }
 
@@ -95,14 +98,47 @@ __device__ __forceinline__ void prefix_part(const PrefixArgs& a, int64_t at, con
     if (g == 0) *reinterpret_cast<float2*>(a.ml + 2 * at) = make_float2(m, l);
 }
 
-template <class E>
-__device__ __forceinline__ bool prefix_finite(const floatx16* o, int nd) {
+// Whether a row's o has to be made again: where it is not finite, but not where
+// the row's sum is a NaN, which makes NaNs of whatever is made.
+template <int ND>
+__device__ __forceinline__ bool prefix_again(const floatx16* o, float l) {
     float sum = 0.f;      // (0 times what is not finite is a NaN)
-    for (int i = 0; i < nd; ++i)
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) sum = fmaf(o[i][r], 0.f, sum);
-    return sum == 0.f;
+    sum += swa_swap(sum);
+    return !(sum == 0.f) && l == l;
 }
+
+// Whether a sequence in use holds row t of the call (every lane asks for its
+// own).  Its loads start with the object, and answers take no others while there
+// are no more sequences than lanes: one's end and length a lane.
+struct PrefixHeld {
+    const PrefixArgs& a;
+    int end, len, begin;
+    bool few;
+    __device__ __forceinline__ PrefixHeld(const PrefixArgs& a_, int t, int lane) : a(a_), end(0), begin(0), few(a_.B <= 64) {
+        const int at = min(lane, a.B - 1);
+        len = a.lens[a.cu ? at : t];
+        if (a.cu) {
+            end = a.cu[at + 1];
+            begin = a.cu[0];
+        }
+    }
+    __device__ __forceinline__ bool operator()(int t) const {
+        if (!a.cu) return len >= 0;
+        int lo = 0, hi = a.B;      // as many sequences as lo end at or before t
+        while (__any(lo < hi)) {
+            const int mid = min((lo + hi) / 2, a.B - 1), e = few ? __shfl(end, mid) : a.cu[mid + 1];
+            const bool up = lo < hi && e <= t;
+            hi = lo < hi && !up ? mid : hi;
+            lo = up ? mid + 1 : lo;
+        }
+        const int b = min(lo, a.B - 1), n = few ? __shfl(len, b) : a.lens[b];
+        return begin <= t && lo < a.B && n >= 0;
+    }
+};
 
 // Tiles of BN keys, NBUF of them in LDS (all but the one in use on their way).
 constexpr int PREFIX_IDS = 512;      // keys whose page ids are in LDS at once (one of two such windows)
@@ -139,6 +175,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
     Frag q[NK];
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) q[ks] = swa_ld_mem<E>(qrow, ks, g);
+    const PrefixHeld held(a, rr / G, lane);
     // the last key that the lane's row sees, and that the wave's first and last do
     const int lim = CAUSAL ? (int)min((int64_t)k1 - 1, past + rr / G) : k1 - 1;
     const int lim0 = CAUSAL ? (int)min((int64_t)k1 - 1, past + min(r0 + 32 * w, nrows - 1) / G) : k1 - 1;
@@ -269,6 +306,11 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
         if (i < nt) fetch(i, sm.tile.k + i * BN * D, sm.tile.v + i * BN * D);
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) swa_arrive(q[ks]);
+    // A row that is nobody's stands among the others as zeros: what it holds would
+    // reach their bits, by the rescaling that a wave's rows do together.
+    if (!CAUSAL && !held(rr / G))
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) q[ks] = swa_zero<E>();
     for (int i = 0; i < nt; i += NBUF) {
         tile(i, 0);
         if (i + 1 < nt) tile(i + 1, 1);
@@ -279,10 +321,10 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
     }
     l += swa_swap(l);
     // A masked key has weight 0, and 0 times an infinity or a NaN in its values
-    // would still reach the rows of its tile: a wave with an output that is not
-    // finite makes its outputs again, each from the keys that its row sees.
-    if (__any(!prefix_finite<E>(o, ND)))
-        prefix_single<E, D>(o, q, K, k0, lim1, lim, a.c, m == -INFINITY ? 0.f : m, lane);
+    // would still reach the rows of its tile: rows whose outputs are not finite
+    // have them made again, each from the keys that it sees.
+    const bool again = prefix_again<ND>(o, l);
+    if (__any(again)) prefix_single<E, D>(o, q, K, k0, lim1, lim, a.c, m == -INFINITY ? 0.f : m, again, lane);
     if (row < nrows) prefix_part<E, D>(a, part + row, o, m, l, g);
 }
 
@@ -391,7 +433,8 @@ __device__ __forceinline__ void prefix_own(const PrefixArgs& a, E* kl, E* vl, co
     l += swa_swap(l);
     // (a row that fills up the last tile, and the remainders, make NaNs of an
     // infinity that is seen)
-    if (__any(!prefix_finite<E>(o, ND))) prefix_single<E, D>(o, q, K, k0, k1 - 1, k1 - 1, a.c, m == -INFINITY ? 0.f : m, lane);
+    const bool again = prefix_again<ND>(o, l);
+    if (__any(again)) prefix_single<E, D>(o, q, K, k0, k1 - 1, k1 - 1, a.c, m == -INFINITY ? 0.f : m, again, lane);
     if (h < nh) prefix_part<E, D>(a, part + h, o, m, l, g);
 }
 

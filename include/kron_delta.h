@@ -658,6 +658,10 @@ KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *
  *    hold infinities and NaNs; those that are seen, and those of the row's own
  *    query, show as IEEE arithmetic has them (keys that all have a score of
  *    -infinity: o is a NaN, lse -infinity).
+ *    Rows that such values of what they share a tile with have reached are made
+ *    again with care, key by key (64 rows behind 32768 keys: milliseconds).
+ *    Rows that are nobody's (of unused sequences, behind the last one) reach no
+ *    others, whatever q holds there.
  *  * ws: kron_delta_prefix_attn_workspace_bytes(desc, cu_seqlens != NULL)
  *    bytes, contents on entry ignored.  Calls that overlap on the device must
  *    not share it.

@@ -94,3 +94,59 @@ def test_an_infinite_value_of_no_weight_shows(where, packed, dtype):
     c.vp[pg, sl, 0, 9] = float("inf")
     o = f64(c.run())
     assert not np.isfinite(o[0, :, 9]).any() and np.isfinite(np.delete(o[0], 9, -1)).all()
+
+
+FILLS = ["nan", "inf", "-inf", 1e30, -3.0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_rows_that_are_nobodys_change_nothing(packed, dtype):
+    """Rows of unused sequences and rows that no sequence holds: other rows have the same bits whatever is there."""
+    torch = _torch()
+    if packed:
+        c = Case([3, -1, 0, 50, -2], [20, 5, 3, 1, 1], 700, 16, 4, 2, 64, dtype, seed=62, packed=True, gap=9)
+    else:
+        c = Case([3, -1, 0, 50, -2], [1] * 5, 700, 16, 4, 2, 64, dtype, seed=62)
+    held = torch.tensor([o is not None and o[1] is not None for o in R.rows_of(c.lens, c.cu, c.T)], device="cuda")
+    c.q *= 4
+    c.q[~held] = 0
+    ref, rl = c.run(return_lse=True)
+    c.check(ref, rl, rows=[0, 1])
+    for fill in FILLS:
+        c.q[~held] = float(fill)
+        o, lse = c.run(return_lse=True)
+        assert torch.equal(o[held], ref[held]) and torch.equal(lse[:, held], rl[:, held]), fill
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_another_rows_nan_changes_nothing(packed, dtype):
+    """A request whose queries are NaN beside others: theirs have the same bits as with queries of 0 there."""
+    torch = _torch()
+    lens, new = ([3, 6, 0, 50], [20, 5, 3, 1]) if packed else ([3, 6, 0, 50], [1] * 4)
+    c = Case(lens, new, 700, 16, 4, 2, 64, dtype, seed=63, packed=packed)
+    mine = torch.tensor([o[0] == 1 for o in R.rows_of(c.lens, c.cu, c.T)], device="cuda")
+    c.q[mine] = 0
+    ref, rl = c.run(return_lse=True)
+    c.q[mine] = float("nan")
+    o, lse = c.run(return_lse=True)
+    assert torch.equal(o[~mine], ref[~mine]) and torch.equal(lse[:, ~mine], rl[:, ~mine])
+    assert torch.isnan(o[mine]).all() and torch.isnan(lse[:, mine]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_sequences_with_unused_ones_between(dtype):
+    """More sequences than lanes, some empty, some unused."""
+    torch = _torch()
+    rng = np.random.default_rng(64)
+    lens = [int(x) if x > 4 else -1 for x in rng.integers(0, 30, 150)]
+    new = [int(x) for x in rng.integers(0, 5, 150)]
+    c = Case(lens, new, 130, 16, 2, 1, 32, dtype, seed=64, packed=True, gap=4)
+    held = torch.tensor([o is not None and o[1] is not None for o in R.rows_of(c.lens, c.cu, c.T)], device="cuda")
+    c.q[~held] = 0
+    ref, rl = c.run(return_lse=True)
+    c.check(ref, rl, rows=range(0, c.T - 4, 7))
+    c.q[~held] = float("nan")
+    o, lse = c.run(return_lse=True)
+    assert torch.equal(o[held], ref[held]) and torch.equal(lse[:, held], rl[:, held])
