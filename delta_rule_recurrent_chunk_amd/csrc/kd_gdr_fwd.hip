@@ -727,7 +727,10 @@ __global__ __launch_bounds__(256) void kd_gdr_step_kernel(const E* q, const E* k
     floatx4 S[U];
     auto load = [&](int r0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) S[u] = *reinterpret_cast<const floatx4*>(Sr + (int64_t)min(r0 + u * PER + tid / L, dv - 1) * dk);
+        for (int u = 0; u < U; ++u) {
+            S[u] = *reinterpret_cast<const floatx4*>(Sr + (int64_t)min(r0 + u * PER + tid / L, dv - 1) * dk);
+            if (!in) S[u] = floatx4{0.f, 0.f, 0.f, 0.f};      // (0 times an infinity of the first channels)
+        }
     };
     load(part * rows);
     floatx4 kx = {0.f, 0.f, 0.f, 0.f}, qx = {0.f, 0.f, 0.f, 0.f};
