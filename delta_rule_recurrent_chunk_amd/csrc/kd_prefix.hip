@@ -192,7 +192,8 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
     // Page ids pass through LDS, a window of PREFIX_IDS keys at a time: loads of
     // ids between the keys' would make every use of one wait for all keys before it.
     auto window = [&](int x) {
-        const int first = (k0 + x * PREFIX_IDS) / K.page, last = min(k0 + (x + 1) * PREFIX_IDS, k1) - 1;
+        const int key = k0 + x * PREFIX_IDS, first = key / K.page;
+        const int last = key + min(PREFIX_IDS, k1 - key) - 1;      // (the window's end may lie past 31 bits)
         const int n = last / K.page - first + 1;
         for (int i = tid; i < n; i += 256) sm.ids[x & 1][i] = K.id(first + i);
         __syncthreads();

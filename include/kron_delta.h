@@ -651,7 +651,7 @@ KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *
  *    reads key head h / (Hq / Hkv).  d in {32, 64, 128}; bf16, or fp32 (a
  *    diagnostic precision).  prefix <= 2^30 and prefix_width * page.
  *  * A sequence with prefix 0 has its own keys alone.  Own keys past the
- *    table's width are not seen.  Rows of unused sequences, and rows that see
+ *    table's width, or from the 2^31 - 64th on, are not seen.  Rows of unused sequences, and rows that see
  *    nothing, get o = 0 and lse = -infinity.  Page ids outside [0, pages) are
  *    clamped into that range where they are read.
  *  * What a row does not see (later rows' keys, slots behind the last key) may

@@ -87,3 +87,19 @@ def test_delta_rule_with_far_batches(dtype):
         o, ST, saved = kd.gdr_fwd(q, k, v, g, beta, save_states=True)
         out.append(dict(o=o, ST=ST, **kd.gdr_bwd(q, k, v, g, beta, saved, dO)))
     assert all(torch.equal(out[0][n], out[1][n]) for n in out[0])
+
+
+def test_own_keys_up_to_31_bits():
+    """The last of 2^31 - 65 own keys, in a page of its own, takes nearly all the weight."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    page, d, n = 256, 32, 2 ** 31 - 65
+    kp, vp = (torch.zeros(2, page, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kp[1], vp[1] = 4.0, 1.0                       # scores of 128 there, of 0 elsewhere
+    table = torch.zeros(1, 1 << 23, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    q = torch.ones(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    o, lse = kd.prefix_attn(q, kp, vp, i32([]), 0, table, i32([n - 1]), scale=1.0, cu_seqlens=i32([0, 1]), return_lse=True)
+    # 191 keys of weight 1 in the last page; e^-128 of 2^31 others adds nothing
+    assert torch.equal(o, torch.ones_like(o)) and abs(lse.item() - 128 - torch.tensor(191.0).log().item()) < 1e-4
