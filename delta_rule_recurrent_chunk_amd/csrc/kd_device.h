@@ -54,6 +54,23 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
+// How many of the items 0 .. n - 1 hold, of which those that do come first.  The
+// whole wave looks at 64 places at a time: one round up to 64 items, four up to
+// 2^24 (packed sequences, which every workgroup looks for its own among).
+template <class F>
+__device__ __forceinline__ int wave_count(int n, F holds) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = n;
+    while (hi - lo > 64) {
+        const int step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step - 1;      // the last item of each step
+        const int c = __popcll(__ballot(at < hi && holds(min(at, n - 1))));
+        lo += c * step;
+        hi = min(hi, lo + step - 1);
+    }
+    const int at = lo + lane;
+    return lo + __popcll(__ballot(at < hi && holds(min(at, n - 1))));
+}
+
 // A zero the compiler cannot see through: adding it to a per-lane index inside
 // a loop keeps the addresses derived from that index from being hoisted out of
 // the loop (where they would hold registers across the whole loop).

@@ -106,12 +106,7 @@ __device__ __forceinline__ bool gdr_segment(const GdrArgs& a, int slot, GdrSegme
         r.seq = slot / a.nseg;
         r.j = slot - r.seq * a.nseg;
     } else {
-        const int lane = threadIdx.x & 63;
-        int n = 0;
-        for (int i = 0; i < a.B; i += 64) {
-            const int at = i + lane;
-            n += __popcll(__ballot(at < a.B && min(max(a.cu[min(at, a.B)], 0), a.T) / GDR_C / a.seg + at <= slot));
-        }
+        const int n = wave_count(a.B, [&](int at) { return min(max(a.cu[at], 0), a.T) / GDR_C / a.seg + at <= slot; });
         if (n == 0) return false;
         r.seq = n - 1;
     }
@@ -133,12 +128,7 @@ __device__ __forceinline__ bool gdr_slot(const GdrArgs& a, int slot, GdrChunk& c
         c.seq = slot / nc;
         c.n = slot - c.seq * nc;
     } else {
-        const int lane = threadIdx.x & 63;
-        int n = 0;
-        for (int i = 0; i < a.B; i += 64) {
-            const int at = i + lane;
-            n += __popcll(__ballot(at < a.B && min(max(a.cu[min(at, a.B)], 0), a.T) / GDR_C + at <= slot));
-        }
+        const int n = wave_count(a.B, [&](int at) { return min(max(a.cu[at], 0), a.T) / GDR_C + at <= slot; });
         if (n == 0) return false;
         c.seq = n - 1;
     }

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kd_device.h"
+
 namespace kd {
 
 constexpr int APPEND_TOKENS = 8;      // most tokens of a workgroup
@@ -45,13 +47,8 @@ struct PrefixArgs {
 
 // Sequence of packed row `row` as the whole wave finds it: how many of the
 // offsets cu[1 ..] are at most it.  B or more: behind the last sequence.
-__device__ __forceinline__ int paged_owner(const int* cu, int B, int row, int lane) {
-    int n = 0;
-    for (int i = 0; i < B; i += 64) {
-        const int at = i + lane;
-        n += __popcll(__ballot(at < B && cu[min(at, B - 1) + 1] <= row));
-    }
-    return n;
+__device__ __forceinline__ int paged_owner(const int* cu, int B, int row) {
+    return wave_count(B, [&](int at) { return cu[at + 1] <= row; });
 }
 
 }  // namespace kd

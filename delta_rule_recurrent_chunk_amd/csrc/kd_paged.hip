@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256) void kd_append_kernel(AppendArgs a)
         int b = r, first = r;
         bool in = true;
         if (a.cu) {
-            b = paged_owner(a.cu, a.B, r, lane);
+            b = paged_owner(a.cu, a.B, r);
             in = b < a.B;
             if (in) first = a.cu[b];
             in = in && first <= r;

@@ -471,12 +471,7 @@ __global__ __launch_bounds__(256, sizeof(E) * D > 256 ? 1 : 2) void kd_prefix_ke
         const int hk = item % a.Hkv;
         item /= a.Hkv;
         const int slot = item % a.nslots, so = item / a.nslots;
-        int n = 0;
-        for (int i = 0; i < a.B; i += 64) {
-            const int at = i + lane;
-            const int64_t first = (int64_t)min(max(a.cu[min(at, a.B)], 0), a.T) * G / PREFIX_ROWS + at;
-            n += __popcll(__ballot(at < a.B && first <= slot));
-        }
+        const int n = wave_count(a.B, [&](int at) { return (int64_t)min(max(a.cu[at], 0), a.T) * G / PREFIX_ROWS + at <= slot; });
         if (n == 0) return;
         const int b = n - 1, q0 = min(max(a.cu[b], 0), a.T), q1 = min(max(a.cu[b + 1], q0), a.T);
         const int nrows = (q1 - q0) * G, blk = slot - (int)((int64_t)q0 * G / PREFIX_ROWS + b);
@@ -534,7 +529,7 @@ __global__ __launch_bounds__(256) void kd_prefix_join_kernel(PrefixArgs a)
     bool held = at < (int64_t)a.T * a.Hq;
     int b = t;
     if (held && a.cu) {
-        b = paged_owner(a.cu, a.B, t, lane);
+        b = paged_owner(a.cu, a.B, t);
         held = b < a.B && a.cu[min(b, a.B)] <= t;      // (otherwise no sequence holds the row)
     }
     F sum;
