@@ -103,3 +103,43 @@ def test_own_keys_up_to_31_bits():
     o, lse = kd.prefix_attn(q, kp, vp, i32([]), 0, table, i32([n - 1]), scale=1.0, cu_seqlens=i32([0, 1]), return_lse=True)
     # 191 keys of weight 1 in the last page; e^-128 of 2^31 others adds nothing
     assert torch.equal(o, torch.ones_like(o)) and abs(lse.item() - 128 - torch.tensor(191.0).log().item()) < 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_delta_rule_with_far_states(dtype):
+    """More than 2^31 elements of states, of those that are kept per chunk and of their gradients: the last sequences
+    against a call for themselves."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    _room(100)
+    G = torch.Generator(device="cuda").manual_seed(4)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    Hk, Hv, dk, dv, few = 2, 16, 128, 256, 6
+    N = (1 << 31) // (Hv * dv * dk) + few
+    lens = torch.ones(N, dtype=torch.int64)
+    lens[-few:] = torch.tensor([1, 70, 0, 3, 130, 2])
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    T, first = int(cu[-1]), int(cu[-few - 1])
+    mk = lambda *s: torch.randn(*s, generator=G, device="cuda")  # noqa: E731
+    q, k, v, dO = (mk(T, h, d).mul_(0.1).to(dt) for h, d in ((Hk, dk), (Hk, dk), (Hv, dv), (Hv, dv)))
+    g, beta = -torch.rand(T, Hv, generator=G, device="cuda"), torch.rand(T, Hv, generator=G, device="cuda")
+    S0 = torch.zeros(N, Hv, dv, dk, device="cuda")
+    S0[-few:].normal_(generator=G)
+    dST = torch.zeros(few, Hv, dv, dk, device="cuda").normal_(generator=G)
+    small = {}
+    for part in (slice(first, T), slice(0, T)):
+        alone = part.start > 0
+        c = (cu[-few - 1:] - first if alone else cu).to("cuda", torch.int32)
+        x = [t[part] for t in (q, k, v, g, beta)]
+        o, ST, saved = kd.gdr_fwd(*x, S0[-few:] if alone else S0, cu_seqlens=c, save_states=True)
+        if not alone:
+            S0.zero_()
+            S0[-few:] = dST           # (the states' place for their gradients)
+        r = kd.gdr_bwd(*x, saved, dO[part], dST if alone else S0, cu_seqlens=c)
+        n = T - first
+        out = dict(o=o[-n:], ST=ST[-few:], dS0=r.pop("dS0")[-few:], **{m: t[-n:] for m, t in r.items()})
+        if alone:
+            small = {m: t.clone() for m, t in out.items()}
+        else:
+            assert saved.numel() > (1 << 31) * q.element_size()
+            assert all(torch.equal(small[m], out[m]) for m in out)
