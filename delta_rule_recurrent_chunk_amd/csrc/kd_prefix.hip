@@ -639,12 +639,17 @@ static int64_t prefix_grid(const PrefixArgs& a, bool packed, int items)
     return swa_grid((int64_t)a.blocks * a.Hkv * a.sp) + own;
 }
 
+// Rows of o that a workgroup of the join takes: one after the other where rows
+// are many, shared out to four waves where they are few (1024 rows, 40 parts: 7.8
+// and 7.4 us; 48 rows, 34 parts: 6.1 and 4.8; 32240 rows, 3 parts: 20 and 69).
+static int prefix_join_rows(const PrefixArgs& a) { return a.sp + a.so <= 8 || (int64_t)a.T * a.Hq > 8192 ? 4 : 1; }
+
 bool prefix_fits(PrefixArgs a, bool packed)
 {
     const int64_t G = a.Hq / a.Hkv;
     if ((int64_t)a.T * G > (1 << 30) || a.T * G / PREFIX_ROWS + a.B > (1 << 30)) return false;
     prefix_plan(a, packed);
-    return grid_fits(prefix_grid(a, packed, 2), 256) && grid_fits((int64_t)a.T * a.Hq, 256);
+    return grid_fits(prefix_grid(a, packed, 2), 256) && grid_fits(((int64_t)a.T * a.Hq + 3) / prefix_join_rows(a), 256);
 }
 
 template <class E, int D>
@@ -661,11 +666,8 @@ static hipError_t prefix(PrefixArgs a, hipStream_t st)
     else kd_prefix_kernel<E, D, sizeof(E) == 4 ? 32 : 64><<<grid, 256, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // A row's parts one after the other where rows are many, shared out to four
-    // waves where they are few (1024 rows, 40 parts: 7.8 and 7.4 us; 48 rows, 34
-    // parts: 6.1 and 4.8; 32240 rows, 3 parts: 20 and 69).
     const int64_t rows = (int64_t)a.T * a.Hq;
-    if (a.sp + a.so <= 8 || rows > 8192) kd_prefix_join_kernel<E, D, 4><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    if (prefix_join_rows(a) == 4) kd_prefix_join_kernel<E, D, 4><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
     else kd_prefix_join_kernel<E, D, 1><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }

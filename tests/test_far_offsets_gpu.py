@@ -143,3 +143,21 @@ def test_delta_rule_with_far_states(dtype):
         else:
             assert saved.numel() > (1 << 31) * q.element_size()
             assert all(torch.equal(small[m], out[m]) for m in out)
+
+
+def test_results_behind_a_prefix_past_32_bits():
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    _room(60)
+    G = torch.Generator(device="cuda").manual_seed(5)
+    Hq, Hkv, d, page, few = 32, 1, 128, 64, 100
+    n = (1 << 31) // (Hq * d) + few
+    q = torch.zeros(n, Hq, d, dtype=torch.bfloat16, device="cuda")
+    q[-few:].normal_(generator=G)
+    kp, vp = (torch.randn(4, page, Hkv, d, generator=G, device="cuda").bfloat16() for _ in range(2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, table, prefix = i32([-1, 3]), i32([[0, 1], [2, 1]]), i32([3])
+    o, lse = kd.prefix_attn(q, kp, vp, prefix, 60, table, lens, cu_seqlens=i32([0, n - few, n]), return_lse=True)
+    want, wl = kd.prefix_attn(q[-few:].clone(), kp, vp, prefix, 60, table[1:], lens[1:], cu_seqlens=i32([0, few]),
+                              return_lse=True)
+    assert torch.equal(o[-few:], want) and torch.equal(lse[:, -few:], wl) and not o[:n - few].any()
