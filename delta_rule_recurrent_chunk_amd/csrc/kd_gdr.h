@@ -386,11 +386,19 @@ struct GdrFetch {
 
 // Two groups of 16 value columns a workgroup instead of four, while that leaves
 // no more workgroups than compute units: both waves of a group have a SIMD for
-// themselves then (64 heads' sequences of 2048 tokens, 128 x 128: the forward
-// pass 77 us for 98).  From there on four (192 heads, 64 x 64: 98 us for 121;
-// backwards 137 for 174), but for packed sequences a little later: the short
-// ones' compute units come free (13 ragged ones of 12 heads, 64 x 64: 54 us for
-// 68, backwards 75 for 111).
+// themselves then (with 128 workgroups of four, sequences of 2048 tokens: heads of
+// 128 x 128 87 us for 97, backwards 113 for 150; of 64 x 64 63 for 68 and 95 for
+// 119).  From there on four (heads of 64 x 64, 144 of four: 71 us for 87, backwards
+// 124 for 163; 192: 87 for 105 and 130 for 174; 128 x 128, 192: 101 for 139 and 162
+// for 196).  For packed sequences a little later: the short ones' compute units
+// come free.  Lengths are known on the device alone, so a packed call is taken to
+// be ragged (8191 tokens in 13 sequences of 12 heads, 64 x 64, the longest 3.4
+// times the average, 156 of four: 57 us for 67, backwards 73 for 118; eight others
+// with 144 to 192, the longest 2.3 to 3.9 times the average: 8 to 19% less,
+// backwards 24 to 37%).  Packed sequences of equal length lose by it what batched
+// ones would (192, 64 x 64: 103 us for 88, backwards 173 for 131), nearly equal
+// ones less (the longest 1.6 times the average, 128 x 128: 56 for 44 and 70 for
+// 64).
 __host__ __forceinline__ bool gdr_narrow(const GdrArgs& a, int segs) {
     return (int64_t)segs * a.Hv * ((a.dv + 63) / 64) <= (a.cu ? 192 : 128);
 }

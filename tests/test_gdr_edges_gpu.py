@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import gdr_ref as R
-from test_gdr_gpu import NAMES, _torch, check, f64, inputs
+from test_gdr_gpu import NAMES, _torch, check, compare, f64, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,26 @@ def test_steps_with_resets_and_strong_decays(g, dtype):
             check("S", S[b, h], st[2], 2 * (dk + 8) * R.W * mag + 1e-37)
             check("o", o[b, :, h], ro, 1.01 * u * np.abs(ro) +
                   2 * (dk + 8) * R.W * (mag[:, 0] * np.abs(a["q"][b]).max() * dk ** 0.5) + 1e-37)
+
+
+# ------------------------------------- packed calls around the widths' borders
+@pytest.mark.parametrize("lens,H,d", [([70] * 9, 16, 64), ([1, 200, 0, 64, 129, 3, 90, 65, 2, 150], 16, 64), ([65] * 12, 16, 64),
+                                      ([66] * 13, 16, 64), ([100, 1, 63, 130, 5, 64], 16, 128), ([70] * 7, 16, 128)])
+def test_packed_calls_of_many_heads(lens, H, d):
+    """128 to 224 workgroups of four groups of value columns: each sequence has the bits of a call for itself, and some
+    heads of it the results."""
+    import delta_rule_recurrent_chunk_amd as kd
+    torch = _torch()
+    print("case", lens, H, d, flush=True)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    t = inputs((int(cu[-1]),), H // 4, H, d, d, "bf16", sum(lens), n=len(lens))
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    got = run(t, 0.2, c)
+    for i, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        one = {n: x[i:i + 1] if n in ("S0", "dST") else x[None, a:b] for n, x in t.items()}
+        alone = run(one, 0.2)
+        assert all(torch.equal(alone[n][0], got[n][i] if n in ("ST", "dS0") else got[n][a:b]) for n in got), i
+    i = int(np.argmax(lens))
+    few = {n: (x[i:i + 1, :4] if n in ("S0", "dST") else x[None, cu[i]:cu[i + 1], :1 if n in ("q", "k") else 4]) for n, x in t.items()}
+    part = {n: (x[i:i + 1, :4] if n in ("ST", "dS0") else x[None, cu[i]:cu[i + 1], :1 if n in ("dq", "dk") else 4]) for n, x in got.items()}
+    compare(few, part, 0.2, "bf16")
