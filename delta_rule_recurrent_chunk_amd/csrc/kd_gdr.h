@@ -20,7 +20,7 @@
 // it and the first one's gradient by 2.7e-6, with 24 by 0.7e-6 and 0.6e-6 (what
 // 16 bits of S and A leave), for a quarter more products (3% of the passes' time
 // with two groups of columns a workgroup, up to a fifth backwards with four).
-// P, which only reaches o, is rounded.  fp32: the same fragments through eight
+// P is rounded in o, and keeps its remainder in dU.  fp32: the same fragments through eight
 // fp32 products.
 #pragma once
 

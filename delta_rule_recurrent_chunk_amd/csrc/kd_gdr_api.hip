@@ -96,9 +96,9 @@ kd::GdrArgs gdr_args(const kd_gdr_desc* d, const GdrSizes& s, const void* q, con
     return a;
 }
 
-// Offsets of the workspace's parts.  Forward: records (not where they are
-// saved), the segments' states and maps (equal where a sequence is not cut).
-// Backward: dS, X and (bf16) its remainder.
+// Offsets of the workspace's parts.  Forward: records (their room is asked for
+// also where they are saved, and not used then), the segments' states and maps
+// (equal where a sequence is not cut).  Backward: dS, X and (bf16) its remainder.
 struct GdrSpace {
     size_t ds, x, x2, si, m, bytes;
 };

@@ -633,7 +633,8 @@ typedef struct {
  *  * Tokens without a page (a table entry outside [0, pages), or past the
  *    table's width) are not stored; their queries are turned.  Nothing of an
  *    unused sequence is stored; its rows of q_out are 0.
- *  * Two tokens of one call that the table sends to one slot: either may stay.
+ *  * Two tokens of one call that the table sends to one slot: 16 bytes of either
+ *    stay, a mix of both as a rule.
  */
 KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *q, const void *k, const void *v,
                          const int64_t in_stride[6], void *k_pages, void *v_pages, const int32_t *table,
@@ -659,12 +660,16 @@ KD_API kd_status kron_delta_paged_append(const kd_paged_desc *desc, const void *
  *    query, show as IEEE arithmetic has them (keys that all have a score of
  *    -infinity: o is a NaN, lse -infinity).
  *    Rows that such values of what they share a tile with have reached are made
- *    again with care, key by key (64 rows behind 32768 keys: milliseconds).
+ *    again with care, key by key (64 rows behind 32768 keys: 1.4 ms for 0.05).
  *    Rows that are nobody's (of unused sequences, behind the last one) reach no
  *    others, whatever q holds there.
  *  * ws: kron_delta_prefix_attn_workspace_bytes(desc, cu_seqlens != NULL)
  *    bytes, contents on entry ignored.  Calls that overlap on the device must
  *    not share it.
+ *  * bf16: the weights of the prefix's keys, and of packed rows' own ones, are
+ *    rounded to bf16 where they meet the values (o is off by 2.2e-3 of 64 bits,
+ *    where its own rounding is 1.7e-3); those of single rows' own keys keep a
+ *    remainder.
  * Results do not depend on how the work is scheduled: repeated calls agree bit
  * for bit.
  */
@@ -701,9 +706,17 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *    ignored, the states are [B, Hv, dv, dk].  Rows that no sequence covers are
  *    left unwritten.
  *  * Tokens are taken 64 at a time: a token with an infinity or a NaN in it
- *    shows in all rows of its 64.
+ *    shows in all rows of its 64, those before it too.
+ *  * Roundings to bf16 (desc->dtype KD_BF16) beside those of inputs and results:
+ *    forward, of the decayed scale q . k in o alone; backward, of the kept states
+ *    and their gradients, one of each per 64 tokens, and of the matrices that
+ *    weigh k and q in dq and dk.  States pass from token to token in 32 bits,
+ *    and what meets them in products has 16 bits or 24.  Relative to 64 bits
+ *    (root of the sum of squares): o, dq, dk 2.2e-3 to 2.5e-3, dv 1.7e-3 (a
+ *    rounding of the result alone is 1.7e-3), ST and dS0 below 1e-6; dg
+ *    cancels, and is off by 1e-3 to 1e-2 as the gates forget much or little.
  *  * ws: kron_delta_gdr_workspace_bytes(desc, cu_seqlens != NULL, backward)
- *    bytes, contents on entry ignored.  Calls that overlap on the device must
+ *    bytes (forward: as many with saved as without), contents on entry ignored.  Calls that overlap on the device must
  *    not share it.
  * Results do not depend on how the work is scheduled: repeated calls agree bit
  * for bit.
