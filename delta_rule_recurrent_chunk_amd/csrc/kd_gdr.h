@@ -20,8 +20,13 @@
 // it and the first one's gradient by 2.7e-6, with 24 by 0.7e-6 and 0.6e-6 (what
 // 16 bits of S and A leave), for a quarter more products (3% of the passes' time
 // with two groups of columns a workgroup, up to a fifth backwards with four).
-// P is rounded in o, and keeps its remainder in dU.  fp32: the same fragments through eight
-// fp32 products.
+// P is rounded in o, and keeps its remainder in dU: o is off by 2.2e-3 of 64
+// bits, where its own rounding is 1.7e-3, for one product a block less in a wave
+// that the next chunk does not wait for but shares a SIMD with one it does.  The
+// states and their gradients that the chunks' gradients start from are kept in
+// the inputs' type (half the memory and traffic; dq and dk are off by 2.3e-3 to
+// 2.5e-3, dg by what is left when it cancels).  fp32: the same fragments through
+// eight fp32 products.
 #pragma once
 
 #include "kd_device.h"

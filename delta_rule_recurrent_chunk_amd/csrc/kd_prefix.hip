@@ -290,6 +290,9 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs& a, PrefixLds<E, D>
                 ls += sc[n][r];
             }
         l += ls;
+        // (bf16: weights are rounded here, and not in their sum: o is off by 2.2e-3,
+        // where its own rounding is 1.7e-3.  Their remainder would be half as many
+        // products again, which bound prompts.)
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int n = 0; n < NS; ++n)

@@ -606,7 +606,8 @@ KD_API kd_status kron_delta_swa_cache_store(const kd_swa_cache_desc *desc, int32
  * meaning, none outside the tensors).  lens[b] (int32, on the device, not changed) is the
  * number of own tokens before the call's: row r of sequence b is own token
  * lens[b] + r.  A negative lens[b] marks an unused sequence.  Rows that no
- * sequence holds are left unwritten.
+ * sequence holds are left unwritten.  B <= 2^24, T <= 2^29, and T Hq / Hkv <=
+ * 2^30 in attention.
  */
 typedef struct {
     int32_t B, T, Hq, Hkv, d;
@@ -696,7 +697,8 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *  * S0, ST, dST, dS0: [B, Hv, dv, dk] fp32.
  *  * dk and dv multiples of 8, dk <= KRON_DELTA_GDR_MAX_DK, dv <=
  *    KRON_DELTA_GDR_MAX_DV; Hv dv and the token strides at most 2^22 elements;
- *    bf16, or fp32 (a diagnostic precision).  Keys of
+ *    B <= 65535 (packed: 2^24), T <= 2^29, and launches of less than 2^32
+ *    threads (per 64 tokens and head 64, per sequence and 16 values 128); bf16, or fp32 (a diagnostic precision).  Keys of
  *    length at most 1 (and beta in [0, 1]) keep the rule stable; longer ones
  *    are computed as they are.
  *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of T
@@ -712,9 +714,10 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *    and their gradients, one of each per 64 tokens, and of the matrices that
  *    weigh k and q in dq and dk.  States pass from token to token in 32 bits,
  *    and what meets them in products has 16 bits or 24.  Relative to 64 bits
- *    (root of the sum of squares): o, dq, dk 2.2e-3 to 2.5e-3, dv 1.7e-3 (a
- *    rounding of the result alone is 1.7e-3), ST and dS0 below 1e-6; dg
- *    cancels, and is off by 1e-3 to 1e-2 as the gates forget much or little.
+ *    (root of the sum of squares): o, dq, dk 2.2e-3 to 2.5e-3 (up to 3.2e-3 of
+ *    one or two tokens), dv 1.7e-3 (a rounding of the result alone is 1.7e-3),
+ *    ST and dS0 1e-6 (with 8 key channels 2e-6); dg cancels, and is off by 1e-3
+ *    to 1e-2 as the gates forget much or little.
  *  * ws: kron_delta_gdr_workspace_bytes(desc, cu_seqlens != NULL, backward)
  *    bytes (forward: as many with saved as without), contents on entry ignored.  Calls that overlap on the device must
  *    not share it.
