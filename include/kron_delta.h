@@ -698,7 +698,8 @@ KD_API kd_status kron_delta_prefix_attn(const kd_paged_desc *desc, const void *q
  *  * dk and dv multiples of 8, dk <= KRON_DELTA_GDR_MAX_DK, dv <=
  *    KRON_DELTA_GDR_MAX_DV; Hv dv and the token strides at most 2^22 elements;
  *    B <= 65535 (packed: 2^24), T <= 2^29, and launches of less than 2^32
- *    threads (per 64 tokens and head 64, per sequence and 16 values 128); bf16, or fp32 (a diagnostic precision).  Keys of
+ *    threads (512 per 64 tokens and key head; per sequence, value head and 32
+ *    values as well); bf16, or fp32 (a diagnostic precision).  Keys of
  *    length at most 1 (and beta in [0, 1]) keep the rule stable; longer ones
  *    are computed as they are.
  *  * cu_seqlens (NULL: batched): B packed sequences in one batch element of T
